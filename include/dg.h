@@ -26,7 +26,8 @@
  *     DG_NO_DEVICE_SUPPORT.
  *   - Device-side waits are bounded; a kernel that gives up records DG_DEVICE_TIMEOUT, which
  *     dg_device_status() reports. Tuning overrides and a test hook for this path: dg_tuning.h.
- *   - Distinct streams may call concurrently (no mutable host state after first use per device).
+ *   - Distinct streams may call concurrently (no mutable host state after first use per device). Calls
+ *     that take a workspace need one each: a workspace serves one call at a time.
  */
 #ifndef DG_H
 #define DG_H
@@ -150,6 +151,100 @@ dg_status dg_k_grouped_wgrad(const uint8_t* A, const float* sfa, const uint8_t* 
  */
 dg_status dg_wgrad_fp8_nt(const uint8_t* A, const float* sfa, const uint8_t* B, const float* sfb,
                           float* D, int M, int N, int K, int accumulate, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------- around the products */
+
+/* Activations of dg_gemm_fp8_nt_epilogue, dg_epilogue_backward and dg_moe_layer. GELU is z Phi(z) (with erf),
+ * GELU_TANH its tanh form, SILU z / (1 + exp(-z)). */
+enum { DG_ACT_NONE = 0, DG_ACT_RELU = 1, DG_ACT_GELU = 2, DG_ACT_GELU_TANH = 3, DG_ACT_SILU = 4 };
+
+/* Element types of the router's logits. */
+enum { DG_TYPE_BF16 = 0, DG_TYPE_F32 = 1 };
+
+/* Router scores. */
+enum { DG_SCORE_SOFTMAX = 0, DG_SCORE_SIGMOID = 1 };
+
+/*
+ * The normal GEMM with bias, activation and residual in its epilogue:
+ *   Z = A . B^T + bias,   D = act(Z) + residual
+ *   A, sfa, B, sfb, D     as dg_gemm_fp8_nt
+ *   bias     [N] fp32, or null
+ *   residual [M, N] bf16, or null; may be D itself (added in place), must not overlap it otherwise
+ *   Z        [M, N] bf16, or null: the pre-activation kept for dg_epilogue_backward
+ * Everything up to the two BF16 outputs stays in FP32. bias 4-byte, residual and Z 16-byte aligned. K = 0
+ * is DG_UNSUPPORTED_SHAPE.
+ */
+dg_status dg_gemm_fp8_nt_epilogue(const uint8_t* A, const float* sfa, const uint8_t* B, const float* sfb, void* D,
+                                  const float* bias, int act, const void* residual, void* Z, int M, int N, int K,
+                                  cudaStream_t stream);
+
+/*
+ * Its backward pass up to the two products: dZ = dD * act'(Z), quantised in both directions, and the bias
+ * gradient. (The residual's gradient is dD itself.)
+ *   dD    [M, N] bf16        Z [M, N] bf16 (not read, and may be null, for DG_ACT_NONE)
+ *   q     [M, N] e4m3        sf  [M, N/128]       dZ, 1x128 scales along N: A of dX = dZ . B, which is
+ *                                                 dg_gemm_fp8 with b_mn_major and sfb transposed
+ *   qt    [N, Mp] e4m3       sft [N, Mp/128]      dZ^T, 1x128 scales along M, Mp = M rounded up to 128, zeros
+ *                                                 past M: an operand of dg_wgrad_fp8_nt / dg_k_grouped_wgrad
+ *   dbias [N] fp32                                sum of dZ's rows (before quantisation), in a fixed order
+ * q with sf, qt with sft, and dbias may each be null. Quantisation: s = max(amax, 1e-4) / 448 per block,
+ * code = e4m3(v / s), both quotients rounded to FP32. With DG_ACT_NONE this quantises a BF16 matrix in one
+ * or both directions. N must be a multiple of 128; M is free. dD, Z, q, qt 16-byte aligned.
+ * workspace: device memory of dg_epilogue_backward_workspace(M, N) bytes, 16-byte aligned, needed for dbias
+ * (else it may be null), zeroed before its first use; every call leaves it ready for the next one.
+ */
+dg_status dg_epilogue_backward(const void* dD, const void* Z, int act, uint8_t* q, float* sf, uint8_t* qt, float* sft,
+                               float* dbias, void* workspace, int64_t workspace_bytes, int M, int N,
+                               cudaStream_t stream);
+int64_t dg_epilogue_backward_workspace(int M, int N);
+
+/*
+ * The router: the k experts of each row with the largest selection values, largest first, ties to the lower
+ * expert, and their weights.
+ *   logits  [T, E] bf16 or fp32 (logits_type)
+ *   bias    [E] fp32, or null; only with DG_SCORE_SIGMOID
+ *   ids     [T, k] int32      weights [T, k] fp32
+ * Selection value: the logit, or with a bias sigmoid(logit) + bias. Weight: scale times the score, softmax
+ * over the row or sigmoid(logit) (never the bias), divided by the sum of the k scores with renormalize.
+ * Logits of -inf and NaN cannot be selected and are no part of a softmax; +inf counts as the largest
+ * finite value. Where fewer than k experts can be selected the slots left over get id -1 and weight 0; a
+ * sum of scores that is 0 gives weights 0. E <= 1024, k <= 32, k <= E.
+ */
+dg_status dg_moe_route(const void* logits, int logits_type, const float* bias, int32_t* ids, float* weights, int T, int E,
+                       int k, int scoring, int renormalize, float scale, cudaStream_t stream);
+
+/*
+ * The gradient of dg_moe_route's weights with respect to the logits: dlogits [T, E], of the logits' type,
+ * from dweights [T, k] fp32 and the ids of the forward pass (ids outside [0, E) are empty slots). Every
+ * logit is written, 0 where the weights do not depend on it. dlogits must not overlap logits.
+ */
+dg_status dg_moe_route_backward(const void* logits, int logits_type, const int32_t* ids, const float* dweights,
+                                void* dlogits, int T, int E, int k, int scoring, int renormalize, float scale,
+                                cudaStream_t stream);
+
+/*
+ * A whole mixture-of-experts layer for a few tokens (decode), in one launch:
+ *   out[t] = residual[t] + sum_j weights[t,j] * W2[e] . Q(act(g) * u),   (g; u) = W13[e] . Q(x[t]),   e = ids[t,j]
+ *   x        [T, H] bf16
+ *   ids      [T, k] int32 (device)      weights [T, k] fp32      as dg_moe_route gives them; an id outside
+ *                                                                 [0, E) is an empty slot
+ *   W13      [E, 2I, H] e4m3            s13 [E, 2I/128, H/128]   gate rows [0, I), up rows [I, 2I)
+ *   W2       [E, H, I] e4m3             s2  [E, H/128, I/128]
+ *   residual [T, H] bf16, or null; may be out or x
+ *   out      [T, H] bf16, overwritten; may be x
+ * Q is the 1x128 quantisation of dg_epilogue_backward; the products, the activation and the sum over a token's
+ * experts are FP32, rounded to BF16 once. The weights are the operands of the grouped GEMMs unchanged, and
+ * only those of experts that a token meets are read.
+ * 1 <= T <= 64 (0: no-op), T * k <= 1024, E <= 1024, H and I multiples of 128.
+ * workspace: device memory of dg_moe_layer_workspace(T, k, E, H, I) bytes (-1 for sizes outside these), 256-byte
+ * aligned, zeroed before its first use; every call leaves it ready for the next one, of any sizes it is large
+ * enough for. After DG_DEVICE_TIMEOUT zero it again. The launch is cooperative: its CTAs, one per SM, run at
+ * the same time.
+ */
+dg_status dg_moe_layer(const void* x, const int32_t* ids, const float* weights, const uint8_t* W13, const float* s13,
+                       const uint8_t* W2, const float* s2, const void* residual, void* out, void* workspace,
+                       int64_t workspace_bytes, int T, int k, int E, int H, int I, int act, cudaStream_t stream);
+int64_t dg_moe_layer_workspace(int T, int k, int E, int H, int I);
 
 /* Human-readable name of a status code (static storage). */
 const char* dg_status_string(dg_status status);

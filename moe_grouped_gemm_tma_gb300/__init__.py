@@ -20,7 +20,9 @@ import threading
 __all__ = [
     "DGError", "load", "dg_gemm_fp8_nt", "dg_gemm_fp8", "dg_gemm_fp8_nt_ue8m0", "dg_gemm_fp8_nt_ue8m0_packed",
     "dg_m_grouped_contiguous", "dg_m_grouped_masked",
-    "dg_k_grouped_wgrad", "dg_wgrad_fp8_nt", "dg_device_status", "dg_status_string", "scale_shapes", "library_path",
+    "dg_k_grouped_wgrad", "dg_wgrad_fp8_nt", "dg_gemm_fp8_nt_epilogue", "dg_epilogue_backward",
+    "dg_moe_route", "dg_moe_route_backward", "dg_moe_layer",
+    "epilogue_backward_workspace", "moe_layer_workspace", "ACTIVATIONS", "SCORES", "dg_device_status", "dg_status_string", "scale_shapes", "library_path",
     "TUNE_KNOBS", "dg_tuning_set", "dg_tuning_get", "dg_tuning_reset", "tuning", "dg_testing_arm_wait_timeout",
 ]
 
@@ -53,7 +55,7 @@ def load(build_if_missing: bool = True):
             if not os.path.exists(path):
                 raise RuntimeError(f"libdg.so not found at {path}; run moe_grouped_gemm_tma_gb300/build.py")
             L = ctypes.CDLL(path)
-            P, I = ctypes.c_void_p, ctypes.c_int
+            P, I, F, S = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_int64
             L.dg_gemm_fp8_nt.argtypes = [P, P, P, P, P, I, I, I, P]
             L.dg_gemm_fp8.argtypes = [P, P, P, P, P, I, I, I, I, I, P]
             L.dg_gemm_fp8_nt_ue8m0.argtypes = [P, P, P, P, P, I, I, I, P]
@@ -62,6 +64,14 @@ def load(build_if_missing: bool = True):
             L.dg_m_grouped_masked.argtypes = [P, P, P, P, P, P, I, I, I, I, I, P]
             L.dg_k_grouped_wgrad.argtypes = [P, P, P, P, P, P, I, I, I, P]
             L.dg_wgrad_fp8_nt.argtypes = [P, P, P, P, P, I, I, I, I, P]
+            L.dg_gemm_fp8_nt_epilogue.argtypes = [P, P, P, P, P, P, I, P, P, I, I, I, P]
+            L.dg_epilogue_backward.argtypes = [P, P, I, P, P, P, P, P, P, S, I, I, P]
+            L.dg_moe_route.argtypes = [P, I, P, P, P, I, I, I, I, I, F, P]
+            L.dg_moe_route_backward.argtypes = [P, I, P, P, P, I, I, I, I, I, F, P]
+            L.dg_moe_layer.argtypes = [P, P, P, P, P, P, P, P, P, P, S, I, I, I, I, I, I, P]
+            L.dg_epilogue_backward_workspace.argtypes = [I, I]
+            L.dg_moe_layer_workspace.argtypes = [I, I, I, I, I]
+            L.dg_epilogue_backward_workspace.restype = L.dg_moe_layer_workspace.restype = S
             L.dg_device_status.argtypes = [P]
             L.dg_tuning_set.argtypes = [I, I]
             L.dg_tuning_set.restype = I
@@ -75,7 +85,8 @@ def load(build_if_missing: bool = True):
             L.dg_status_string.restype = ctypes.c_char_p
             for f in ("dg_gemm_fp8_nt", "dg_gemm_fp8", "dg_gemm_fp8_nt_ue8m0", "dg_gemm_fp8_nt_ue8m0_packed",
                       "dg_m_grouped_contiguous", "dg_m_grouped_masked",
-                      "dg_k_grouped_wgrad", "dg_wgrad_fp8_nt", "dg_device_status"):
+                      "dg_k_grouped_wgrad", "dg_wgrad_fp8_nt", "dg_gemm_fp8_nt_epilogue", "dg_epilogue_backward",
+                      "dg_moe_route", "dg_moe_route_backward", "dg_moe_layer", "dg_device_status"):
                 getattr(L, f).restype = I
             _lib = L
     return _lib
@@ -288,6 +299,168 @@ def dg_wgrad_fp8_nt(A, sfa, B, sfb, D, accumulate=True, stream=None):
                                 1 if accumulate else 0, _stream(stream))
     _check(st, "dg_wgrad_fp8_nt")
     return D
+
+
+# Activations and router scores by name (include/dg.h).
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _choice(table, name, what):
+    if name not in table:
+        raise ValueError(f"{what} must be one of {', '.join(table)}, got {name!r}")
+    return table[name]
+
+
+def _typed(t, name, dtype, shape):
+    """A contiguous CUDA tensor of this type and shape; None stays None."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return _dense(t, name)
+
+
+def _bytes(t, name):
+    """A workspace's address and size."""
+    torch = _torch()
+    if t is None:
+        return None, 0
+    if t.dtype != torch.uint8:
+        raise TypeError(f"{name} must be uint8, got {t.dtype}")
+    return _ptr(_dense(t, name)), t.numel()
+
+
+def dg_gemm_fp8_nt_epilogue(A, sfa, B, sfb, D, bias=None, act="none", residual=None, Z=None, stream=None):
+    """D = act(A . B^T + bias) + residual (bf16); A, sfa, B, sfb as dg_gemm_fp8_nt, bias fp32 [N], residual bf16
+    [M,N] (may be D), Z bf16 [M,N] receives the pre-activation."""
+    torch = _torch()
+    A, B = _codes(A, "A"), _codes(B, "B")
+    sfa, sfb = _f32(sfa, "sfa"), _f32(sfb, "sfb")
+    M, K = A.shape
+    N = B.shape[0]
+    D = _typed(D, "D", torch.bfloat16, (M, N))
+    if B.shape[1] != K:
+        raise ValueError(f"shape mismatch: A {tuple(A.shape)} B {tuple(B.shape)}")
+    if (tuple(sfa.shape), tuple(sfb.shape)) != scale_shapes(M, N, K):
+        raise ValueError(f"scale shapes {tuple(sfa.shape)}, {tuple(sfb.shape)} != {scale_shapes(M, N, K)}")
+    bias = _typed(bias, "bias", torch.float32, (N,))
+    residual = _typed(residual, "residual", torch.bfloat16, (M, N))
+    Z = _typed(Z, "Z", torch.bfloat16, (M, N))
+    st = load().dg_gemm_fp8_nt_epilogue(_ptr(A), _ptr(sfa), _ptr(B), _ptr(sfb), _ptr(D), _ptr(bias),
+                                        _choice(ACTIVATIONS, act, "act"), _ptr(residual), _ptr(Z), M, N, K, _stream(stream))
+    _check(st, "dg_gemm_fp8_nt_epilogue")
+    return D
+
+
+def epilogue_backward_workspace(M: int, N: int, device=None):
+    """A workspace for dg_epilogue_backward with dbias at up to this size, ready for its first call."""
+    torch = _torch()
+    return torch.zeros(load().dg_epilogue_backward_workspace(M, N), dtype=torch.uint8, device=device or "cuda")
+
+
+def dg_epilogue_backward(dD, Z, q, sf, qt, sft, dbias, workspace=None, act="none", stream=None):
+    """dZ = dD * act'(Z), bf16 [M,N] in, out as e4m3 codes q [M,N] with scales sf [M,N/128], codes of the
+    transpose qt [N,Mp] with scales sft [N,Mp/128] (Mp = M rounded up to 128), and dbias fp32 [N], the sum of
+    its rows. q with sf, qt with sft, and dbias may be None; dbias needs a workspace
+    (epilogue_backward_workspace). Z is not read for act "none"."""
+    torch = _torch()
+    M, N = dD.shape
+    Mp = (M + 127) // 128 * 128
+    dD = _typed(dD, "dD", torch.bfloat16, (M, N))
+    Z = _typed(Z, "Z", torch.bfloat16, (M, N))
+    if q is not None:
+        q = _typed(_codes(q, "q"), "q", torch.uint8, (M, N))
+    if qt is not None:
+        qt = _typed(_codes(qt, "qt"), "qt", torch.uint8, (N, Mp))
+    sf = _typed(sf, "sf", torch.float32, (M, N // 128))
+    sft = _typed(sft, "sft", torch.float32, (N, Mp // 128))
+    dbias = _typed(dbias, "dbias", torch.float32, (N,))
+    ws, size = _bytes(workspace, "workspace")
+    st = load().dg_epilogue_backward(_ptr(dD), _ptr(Z), _choice(ACTIVATIONS, act, "act"), _ptr(q), _ptr(sf), _ptr(qt),
+                                     _ptr(sft), _ptr(dbias), ws, size, M, N, _stream(stream))
+    _check(st, "dg_epilogue_backward")
+
+
+def _logits_type(logits):
+    torch = _torch()
+    if logits.dtype == torch.bfloat16:
+        return 0
+    if logits.dtype == torch.float32:
+        return 1
+    raise TypeError(f"logits must be bfloat16 or float32, got {logits.dtype}")
+
+
+def dg_moe_route(logits, ids, weights, bias=None, scoring="softmax", renormalize=True, scale=1.0, stream=None):
+    """The router: ids int32 [T,k] and weights fp32 [T,k] of the k largest selection values of each row of
+    logits [T,E] (bf16 or fp32; with a bias fp32 [E], sigmoid scoring only, sigmoid(logit) + bias)."""
+    torch = _torch()
+    T, E = logits.shape
+    k = ids.shape[1]
+    kind = _logits_type(logits)
+    logits = _dense(logits, "logits")
+    ids = _typed(ids, "ids", torch.int32, (T, k))
+    weights = _typed(weights, "weights", torch.float32, (T, k))
+    bias = _typed(bias, "bias", torch.float32, (E,))
+    st = load().dg_moe_route(_ptr(logits), kind, _ptr(bias), _ptr(ids), _ptr(weights), T, E, k,
+                             _choice(SCORES, scoring, "scoring"), 1 if renormalize else 0, float(scale), _stream(stream))
+    _check(st, "dg_moe_route")
+    return ids, weights
+
+
+def dg_moe_route_backward(logits, ids, dweights, dlogits, scoring="softmax", renormalize=True, scale=1.0, stream=None):
+    """dlogits [T,E] (the logits' type) from dweights fp32 [T,k], for the ids that dg_moe_route gave."""
+    torch = _torch()
+    T, E = logits.shape
+    k = ids.shape[1]
+    kind = _logits_type(logits)
+    logits = _dense(logits, "logits")
+    ids = _typed(ids, "ids", torch.int32, (T, k))
+    dweights = _typed(dweights, "dweights", torch.float32, (T, k))
+    dlogits = _typed(dlogits, "dlogits", logits.dtype, (T, E))
+    st = load().dg_moe_route_backward(_ptr(logits), kind, _ptr(ids), _ptr(dweights), _ptr(dlogits), T, E, k,
+                                      _choice(SCORES, scoring, "scoring"), 1 if renormalize else 0, float(scale),
+                                      _stream(stream))
+    _check(st, "dg_moe_route_backward")
+    return dlogits
+
+
+def moe_layer_workspace(T: int, k: int, E: int, H: int, I: int, device=None):
+    """A workspace for dg_moe_layer at these sizes, ready for its first call."""
+    torch = _torch()
+    size = load().dg_moe_layer_workspace(T, k, E, H, I)
+    if size < 0:
+        raise DGError(2, "dg_moe_layer_workspace")
+    return torch.zeros(size, dtype=torch.uint8, device=device or "cuda")
+
+
+def dg_moe_layer(x, ids, weights, W13, s13, W2, s2, out, workspace, act="silu", residual=None, stream=None):
+    """A whole mixture-of-experts layer for up to 64 tokens:
+    out[t] = residual[t] + sum_j weights[t,j] W2[e] . Q(act(g) * u), (g; u) = W13[e] . Q(x[t]), e = ids[t,j];
+    x, out, residual bf16 [T,H], ids int32 [T,k] (outside [0,E): no expert), weights fp32 [T,k], W13 e4m3
+    [E,2I,H] (gate rows, then up rows), W2 e4m3 [E,H,I], each with fp32 scales per 128x128 block."""
+    torch = _torch()
+    T, H = x.shape
+    k = ids.shape[1]
+    W13, W2 = _codes(W13, "W13"), _codes(W2, "W2")
+    E, I2, _ = W13.shape
+    I = I2 // 2
+    x = _typed(x, "x", torch.bfloat16, (T, H))
+    ids = _typed(ids, "ids", torch.int32, (T, k))
+    weights = _typed(weights, "weights", torch.float32, (T, k))
+    if W13.shape != (E, 2 * I, H) or W2.shape != (E, H, I):
+        raise ValueError(f"shape mismatch: x {tuple(x.shape)} W13 {tuple(W13.shape)} W2 {tuple(W2.shape)}")
+    s13 = _typed(s13, "s13", torch.float32, (E, 2 * I // 128, H // 128))
+    s2 = _typed(s2, "s2", torch.float32, (E, H // 128, I // 128))
+    out = _typed(out, "out", torch.bfloat16, (T, H))
+    residual = _typed(residual, "residual", torch.bfloat16, (T, H))
+    ws, size = _bytes(workspace, "workspace")
+    st = load().dg_moe_layer(_ptr(x), _ptr(ids), _ptr(weights), _ptr(W13), _ptr(s13), _ptr(W2), _ptr(s2), _ptr(residual),
+                             _ptr(out), ws, size, T, k, E, H, I, _choice(ACTIVATIONS, act, "act"), _stream(stream))
+    _check(st, "dg_moe_layer")
+    return out
 
 
 def dg_device_status(stream=None) -> int:

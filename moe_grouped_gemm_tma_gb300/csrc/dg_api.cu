@@ -15,6 +15,7 @@
 #include <mutex>
 
 #include "dg.h"
+#include "dg_host.cuh"
 #include "dg_launch.cuh"
 #include "dg_tuning.h"
 
@@ -56,16 +57,10 @@ namespace {
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::once_flag g_encode_once;
 
-constexpr int kMaxDevices = 64;
-struct DeviceInfo {
-    bool ready = false;
-    bool supported = false;
-    int sms = 0;
-    int l2_bytes = 0;
-    int* status = nullptr;
-};
 DeviceInfo g_devices[kMaxDevices];
 std::mutex g_devices_mutex;
+
+}  // namespace
 
 dg_status device_info(DeviceInfo* out) {
     int dev = 0;
@@ -93,6 +88,8 @@ dg_status device_info(DeviceInfo* out) {
     return d.supported ? DG_OK : DG_NO_DEVICE_SUPPORT;
 }
 
+namespace {
+
 dg_status encoder() {
     std::call_once(g_encode_once, [] {
         void* fn = nullptr;
@@ -105,8 +102,14 @@ dg_status encoder() {
     return g_encode ? DG_OK : DG_CUDA_ERROR;
 }
 
-// Row-major e4m3 matrix [rows, k] (k contiguous) read in boxes of box_rows x 128 with the 128-byte
-// swizzle the MMA descriptors expect.
+}  // namespace
+
+dg_status common_prologue(DeviceInfo* dev) {
+    dg_status st = device_info(dev);
+    if (st != DG_OK) return st;
+    return encoder();
+}
+
 dg_status make_operand_map(CUtensorMap* m, const void* base, int64_t rows, int64_t k, int box_rows) {
     cuuint64_t dims[2] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(rows)};
     cuuint64_t strides[1] = {static_cast<cuuint64_t>(k)};
@@ -117,6 +120,8 @@ dg_status make_operand_map(CUtensorMap* m, const void* base, int64_t rows, int64
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? DG_OK : DG_CUDA_ERROR;
 }
+
+namespace {
 
 // MN-major e4m3 operand stored [k, cols] (cols contiguous: A as [K, M] or B as [K, N]) read in boxes of
 // 128 columns x 128 k rows with the 128-byte swizzle, the layout of the MN-major MMA descriptors.
@@ -157,15 +162,13 @@ dg_status make_tile_output_map(CUtensorMap* m, void* base, int64_t rows, int64_t
     return r == CUDA_SUCCESS ? DG_OK : DG_CUDA_ERROR;
 }
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-int cdiv(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
-
 // Specialisations per layout: (BN, PAIR); each must be instantiated in the matching dg_inst_*.cu.
 struct Spec {
     int bn, pair;
 };
 constexpr Spec kNormalSpecs1[] = {{64, 1}, {96, 1}, {128, 1}, {160, 1}, {192, 1}, {224, 1}, {256, 1}};
+// with an epilogue: the widths whose whole tile is staged in shared memory (the residual arrives there)
+constexpr Spec kEpilogueSpecs1[] = {{64, 1}, {128, 1}, {192, 1}};
 constexpr Spec kNormalSpecs2[] = {{128, 2}, {160, 2}, {192, 2}, {224, 2}, {256, 2}};
 // block-scaled (UE8M0) normal GEMM
 constexpr Spec kBlockScaledSpecs[] = {{128, 1}, {192, 1}, {224, 1}, {256, 1}};
@@ -276,6 +279,12 @@ cudaError_t launch_spec<kNormal>(Spec sp, const Launch& L) {
 }
 
 template <>
+cudaError_t launch_spec<kEpilogue>(Spec sp, const Launch& L) {
+    DG_CASE(kEpilogue, 64, 1) DG_CASE(kEpilogue, 128, 1) DG_CASE(kEpilogue, 192, 1) DG_CASE(kEpilogue, 256, 2)
+    return cudaErrorInvalidValue;
+}
+
+template <>
 cudaError_t launch_spec<kContiguous>(Spec sp, const Launch& L) {
     DG_CASE(kContiguous, 128, 1) DG_CASE(kContiguous, 160, 1) DG_CASE(kContiguous, 192, 1)
     DG_CASE(kContiguous, 224, 1) DG_CASE(kContiguous, 256, 1)
@@ -313,8 +322,10 @@ int decode_capacity(int bmt, int split, int sms) {
     switch (bmt) {
         case 32: return decode_cluster_capacity<MODE, 32>(split, sms);
         case 64: return decode_cluster_capacity<MODE, 64>(split, sms);
-        default: return decode_cluster_capacity<MODE, 128>(split, sms);
+        default:
+            if constexpr (MODE != kEpilogue) return decode_cluster_capacity<MODE, 128>(split, sms);
     }
+    return 1;
 }
 
 template <int MODE>
@@ -346,15 +357,10 @@ cudaError_t launch_decode_bmt(int bmt, const Launch& L) {
     switch (bmt) {
         case 32: return launch_decode<MODE, 32>(L);
         case 64: return launch_decode<MODE, 64>(L);
-        case 128: return launch_decode<MODE, 128>(L);
+        case 128:
+            if constexpr (MODE != kEpilogue) return launch_decode<MODE, 128>(L);
     }
     return cudaErrorInvalidValue;
-}
-
-dg_status common_prologue(DeviceInfo* dev) {
-    dg_status st = device_info(dev);
-    if (st != DG_OK) return st;
-    return encoder();
 }
 
 }  // namespace
@@ -425,9 +431,27 @@ static dg_status wgrad_impl(const uint8_t* A, const float* sfa, const uint8_t* B
 
 // The normal GEMM for every operand layout: A stored [M, K] or (a_mn) [K, M], B stored [N, K] or
 // (b_mn) [K, N]. MN-major operands need their contiguous extent to be a multiple of 16 (TMA row
-// strides); MN-major B is tiled in whole 128-column boxes; CTA pairs serve the K-major layout only.
+// strides); MN-major B is tiled in whole 128-column boxes; CTA pairs serve the K-major layout only. With
+// `ep` (K-major operands) the epilogue mode's kernels run: same tiles and splits, of the widths that mode has.
+namespace {
+struct Epilogue {
+    const float* bias;
+    int act;
+    const void* residual;
+    void* z;
+};
+}  // namespace
+
+static void set_epilogue(EpilogueParams& p, const Epilogue& ep) {
+    p.bias = ep.bias;
+    p.residual = static_cast<const __nv_bfloat16*>(ep.residual);
+    p.z = static_cast<__nv_bfloat16*>(ep.z);
+    p.act = ep.act;
+}
+
 static dg_status gemm_impl(const uint8_t* A, const float* sfa, const uint8_t* B, const float* sfb, void* D,
-                           int M, int N, int K, bool a_mn, bool b_mn, cudaStream_t stream) {
+                           int M, int N, int K, bool a_mn, bool b_mn, cudaStream_t stream,
+                           const Epilogue* ep = nullptr) {
     if (M < 0 || N < 0 || K < 0) return DG_INVALID_ARG;
     if (M == 0 || N == 0) return DG_OK;
     if (!D) return DG_INVALID_ARG;
@@ -456,6 +480,13 @@ static dg_status gemm_impl(const uint8_t* A, const float* sfa, const uint8_t* B,
         split = choose_split(kNormalSpecsBMN, &sp, cdiv(M, BM), N, K / 128, dev.sms);
     } else if (short_k_pair) {
         sp = Spec{256, 2};
+    } else if (ep) {
+        if (pair) {
+            sp = Spec{256, 2};
+        } else {
+            sp = spec_override(kEpilogueSpecs1, choose_spec(kEpilogueSpecs1, cdiv(M, BM), N, dev.sms));
+            split = choose_split(kEpilogueSpecs1, &sp, cdiv(M, BM), N, K / 128, dev.sms);
+        }
     } else if (pair) {
         sp = spec_override(kNormalSpecs2, choose_spec(kNormalSpecs2, cdiv(M, 2 * BM), N, dev.sms));
     } else {
@@ -478,8 +509,8 @@ static dg_status gemm_impl(const uint8_t* A, const float* sfa, const uint8_t* B,
     if (!a_mn && !b_mn && !pair && M <= 128 && tune(DG_TUNE_BN) < 0) {
         const int col_tiles = cdiv(N, 128);
         decode = M <= 64 && K >= 7168 && col_tiles >= 32 && col_tiles <= 64;
-        if (const int v = tune(DG_TUNE_SWAP); v >= 0) decode = (v == 1);
-        if (decode) pl = plan_decode<kNormal>(1, M, M, N, kbs, dev.sms);
+        if (const int v = tune(DG_TUNE_SWAP); v >= 0) decode = (v == 1) && (!ep || M <= 64);
+        if (decode) pl = ep ? plan_decode<kEpilogue>(1, M, M, N, kbs, dev.sms) : plan_decode<kNormal>(1, M, M, N, kbs, dev.sms);
     }
     if (decode) {
         if (make_operand_map(&L.tmap_a, A, M, K, pl.bmt) != DG_OK) return DG_CUDA_ERROR;
@@ -501,6 +532,10 @@ static dg_status gemm_impl(const uint8_t* A, const float* sfa, const uint8_t* B,
         L.units = pl.units;
         L.sms = dev.sms;
         L.stream = stream;
+        if (ep) {
+            set_epilogue(L.params, *ep);
+            return launch_decode_bmt<kEpilogue>(pl.bmt, L) == cudaSuccess ? DG_OK : DG_CUDA_ERROR;
+        }
         return launch_decode_bmt<kNormal>(pl.bmt, L) == cudaSuccess ? DG_OK : DG_CUDA_ERROR;
     }
     if ((a_mn ? make_mn_operand_map(&L.tmap_a, A, K, M) : make_operand_map(&L.tmap_a, A, M, K, BM)) != DG_OK)
@@ -535,6 +570,12 @@ static dg_status gemm_impl(const uint8_t* A, const float* sfa, const uint8_t* B,
     L.units = p.tiles;
     L.sms = dev.sms;
     L.stream = stream;
+    if (ep) {
+        set_epilogue(L.params, *ep);
+        if (ep->residual && make_tile_output_map(&L.params.tmap_r, const_cast<void*>(ep->residual), M, N) != DG_OK)
+            return DG_CUDA_ERROR;
+        return launch_spec<kEpilogue>(sp, L) == cudaSuccess ? DG_OK : DG_CUDA_ERROR;
+    }
     return launch_spec<kNormal>(sp, L) == cudaSuccess ? DG_OK : DG_CUDA_ERROR;
 }
 
@@ -595,6 +636,18 @@ dg_status dg_gemm_fp8_nt(const uint8_t* A, const float* sfa, const uint8_t* B, c
 dg_status dg_gemm_fp8(const uint8_t* A, const float* sfa, const uint8_t* B, const float* sfb, void* D, int M,
                       int N, int K, int a_mn_major, int b_mn_major, cudaStream_t stream) {
     return gemm_impl(A, sfa, B, sfb, D, M, N, K, a_mn_major != 0, b_mn_major != 0, stream);
+}
+
+dg_status dg_gemm_fp8_nt_epilogue(const uint8_t* A, const float* sfa, const uint8_t* B, const float* sfb, void* D,
+                                  const float* bias, int act, const void* residual, void* Z, int M, int N, int K,
+                                  cudaStream_t stream) {
+    if (act < DG_ACT_NONE || act > DG_ACT_SILU) return DG_INVALID_ARG;
+    if (M < 0 || N < 0 || K < 0) return DG_INVALID_ARG;
+    if (M == 0 || N == 0) return DG_OK;
+    if (K == 0) return DG_UNSUPPORTED_SHAPE;
+    if (!aligned(bias, 4) || !aligned(residual, 16) || !aligned(Z, 16)) return DG_MISALIGNED;
+    const Epilogue ep{bias, act, residual, Z};
+    return gemm_impl(A, sfa, B, sfb, D, M, N, K, false, false, stream, &ep);
 }
 
 // The block-scaled GEMM behind both UE8M0 entry points: FP32 power-of-two scales (converted and checked

@@ -95,7 +95,8 @@ cudaError_t launch_decode(const Launch& L) {
         cfg.numAttrs += 1;
     }
     cfg.attrs = cfg.numAttrs ? attr : nullptr;
-    return cudaLaunchKernelEx(&cfg, dg_decode_kernel<MODE, BMT>, L.tmap_a, L.tmap_b, L.params);
+    const typename ParamsOf<MODE>::type prm = L.params;
+    return cudaLaunchKernelEx(&cfg, dg_decode_kernel<MODE, BMT>, L.tmap_a, L.tmap_b, prm);
 }
 
 template int decode_cluster_capacity<kNormal, 32>(int, int);
@@ -104,11 +105,15 @@ template int decode_cluster_capacity<kNormal, 128>(int, int);
 template int decode_cluster_capacity<kMasked, 32>(int, int);
 template int decode_cluster_capacity<kMasked, 64>(int, int);
 template int decode_cluster_capacity<kMasked, 128>(int, int);
+template int decode_cluster_capacity<kEpilogue, 32>(int, int);
+template int decode_cluster_capacity<kEpilogue, 64>(int, int);
 template cudaError_t launch_decode<kNormal, 32>(const Launch&);
 template cudaError_t launch_decode<kNormal, 64>(const Launch&);
 template cudaError_t launch_decode<kNormal, 128>(const Launch&);
 template cudaError_t launch_decode<kMasked, 32>(const Launch&);
 template cudaError_t launch_decode<kMasked, 64>(const Launch&);
 template cudaError_t launch_decode<kMasked, 128>(const Launch&);
+template cudaError_t launch_decode<kEpilogue, 32>(const Launch&);
+template cudaError_t launch_decode<kEpilogue, 64>(const Launch&);
 
 }  // namespace dg

@@ -55,6 +55,7 @@
 #include <cstdint>
 
 #include "dg_ptx.cuh"
+#include "dg_quant.cuh"
 
 namespace dg {
 
@@ -78,7 +79,11 @@ constexpr uint64_t WAIT_LIMIT_NS = 1000000000ull;
 constexpr uint64_t DRAIN_LIMIT_NS = 50000000ull;
 constexpr int STATUS_TIMEOUT = 6;       // DG_DEVICE_TIMEOUT
 
-enum Mode : int { kNormal = 0, kContiguous = 1, kMasked = 2, kKGrouped = 3 };
+enum Mode : int { kNormal = 0, kContiguous = 1, kMasked = 2, kKGrouped = 3, kEpilogue = 4 };
+
+// kEpilogue is the normal layout with bias, activation and residual applied to the tile before it is
+// rounded; everything before that point is the normal layout's.
+__host__ __device__ constexpr bool normal_layout(int mode) { return mode == kNormal || mode == kEpilogue; }
 
 struct Params {
     const float* sfa;          // scales of A rows, row stride kbs
@@ -107,6 +112,20 @@ struct Params {
                                 // stage unfilled, so the MMA issuer's wait on it runs out
     int kb_off[MAX_KGROUPS + 1];  // k-grouped: first K block of each expert, kb_off[G] = sumK/128
 };
+
+// What the epilogue mode takes beside that. Only its kernels have these parameters.
+struct EpilogueParams : Params {
+    CUtensorMap tmap_r;            // the residual in the output's boxes (valid when residual is set)
+    const float* bias;             // [n], or null
+    const __nv_bfloat16* residual; // [rows][n], or null
+    __nv_bfloat16* z;              // [rows][n] pre-activation out, or null
+    int act;                       // DG_ACT_*
+};
+
+template <int MODE>
+struct ParamsOf { using type = Params; };
+template <>
+struct ParamsOf<kEpilogue> { using type = EpilogueParams; };
 
 // Deepest operand ring (at most 8 stages) whose dynamic layout -- alignment slack, ring and scale slots
 // rounded up to 1 KB, output staging -- fits next to the static shared memory.
@@ -206,10 +225,11 @@ struct Cfg {
     // operand ring, which is idle once the tile's last MMA has completed
     static constexpr int PSTRIDE = BN + 4;
     static constexpr int PARTIAL_BYTES = BM * PSTRIDE * 4;
-    static_assert(!((MODE == kNormal || MODE == kMasked) && PAIR == 1) || PARTIAL_BYTES <= STAGES * STAGE_BYTES,
+    static_assert(!((normal_layout(MODE) || MODE == kMasked) && PAIR == 1) || PARTIAL_BYTES <= STAGES * STAGE_BYTES,
                   "split-K partials must fit in the operand ring");
     static_assert(STAGES >= 2, "not enough shared memory for two stages");
     static_assert(B_BYTES % 1024 == 0, "B stage must keep 1024-byte swizzle-atom alignment");
+    static_assert(MODE != kEpilogue || FULL_STAGE, "the epilogue mode takes its residual through the whole-tile staging");
 };
 
 struct TileInfo {
@@ -230,7 +250,7 @@ __device__ __forceinline__ TileInfo decode_tile(const Params& p, int t, const in
     ti.g = 0;
     ti.kb0 = 0;
     ti.nkb = p.kbs;
-    if (MODE == kNormal || MODE == kContiguous) {
+    if (normal_layout(MODE) || MODE == kContiguous) {
         // bands of group_m row blocks; within a band the row block varies fastest. Odd bands take the
         // column blocks in reverse (serpentine), so a band starts on the B column blocks the previous
         // band read last, which may still be in L2 (DRAM reads of 4096 x 7168 x 16384: 324.8 -> 318.2
@@ -247,7 +267,7 @@ __device__ __forceinline__ TileInfo decode_tile(const Params& p, int t, const in
         ti.d_row = ti.m0;
         ti.rows_valid = min(BM, p.rows - ti.m0);
         ti.b_row = ti.n0 + rank * B_ROWS;
-        if (MODE == kNormal && p.split > 1) {   // this CTA's share of the tile's K blocks
+        if (normal_layout(MODE) && p.split > 1) {   // this CTA's share of the tile's K blocks
             ti.kb0 = (srank * p.kbs) / p.split;
             ti.nkb = ((srank + 1) * p.kbs) / p.split - ti.kb0;
         }
@@ -381,11 +401,94 @@ __device__ __forceinline__ void promote_kg_chunk(float (&accum)[COLS], const uin
     }
 }
 
+// The epilogue of one thread's row of a tile: v (the product, COLS columns from column `col`) becomes
+// act(v + bias) + residual in FP32, and the BF16 pre-activation is written on the way. `boxes` is the warp's
+// staging with the residual in 32-column boxes (64 bytes a row, chunk ^ ((row >> 1) & 3)), or null. Lanes of
+// a warp read the same bias words. A lane writes 32 contiguous bytes of Z a store, a whole sector, where the
+// rows are 32-byte aligned (N % 16 == 0), 16 bytes otherwise.
+template <int COLS>
+__device__ __forceinline__ void epilogue_tile(float (&v)[COLS], const EpilogueParams& p, int row, int col, bool row_valid,
+                                              const uint8_t* boxes, int lane) {
+    const bool wide = (p.n & 15) == 0 && (reinterpret_cast<uintptr_t>(p.z) & 31) == 0;
+#pragma unroll
+    for (int r = 0; r < COLS / 32; ++r) {
+        float w[32];
+        if (p.bias != nullptr) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+                const int c = col + r * 32 + j;
+                // (p.n is a multiple of 8 and the bias only 4-byte aligned)
+                if (c < p.n) {
+                    w[j] = v[r * 32 + j] + __ldg(p.bias + c);
+                    w[j + 1] = v[r * 32 + j + 1] + __ldg(p.bias + c + 1);
+                    w[j + 2] = v[r * 32 + j + 2] + __ldg(p.bias + c + 2);
+                    w[j + 3] = v[r * 32 + j + 3] + __ldg(p.bias + c + 3);
+                } else {
+                    w[j] = w[j + 1] = w[j + 2] = w[j + 3] = 0.f;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) w[j] = v[r * 32 + j];
+        }
+        if (p.z != nullptr && row_valid) {
+            __nv_bfloat16* zrow = p.z + static_cast<size_t>(row) * p.n + col + r * 32;
+#pragma unroll
+            for (int j = 0; j < 32; j += 16) {
+                uint32_t u[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) u[i] = pack_bf16x2(w[j + 2 * i], w[j + 2 * i + 1]);
+                if (wide) {
+                    if (col + r * 32 + j < p.n) st_global_v8(zrow + j, u);
+                } else {
+                    if (col + r * 32 + j < p.n) st_global_v4(zrow + j, u[0], u[1], u[2], u[3]);
+                    if (col + r * 32 + j + 8 < p.n) st_global_v4(zrow + j + 8, u[4], u[5], u[6], u[7]);
+                }
+            }
+        }
+        act_values<32>(p.act, w);
+        if (boxes != nullptr) {
+            // (boxes that lie past the last column were not copied: whatever is there is not stored either)
+            const uint4* mine = reinterpret_cast<const uint4*>(boxes + r * 2048 + lane * 64);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const uint4 u = mine[c ^ ((lane >> 1) & 3)];
+                const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    w[c * 8 + 2 * i] += bf16_lo(x[i]);
+                    w[c * 8 + 2 * i + 1] += bf16_hi(x[i]);
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[r * 32 + j] = w[j];
+    }
+}
+
+// The same for four columns of a row held by one thread (`at`: their offset in the [rows][n] matrices).
+__device__ __forceinline__ void epilogue_four(float (&v)[4], const EpilogueParams& p, int col, size_t at) {
+    if (p.bias != nullptr) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] += __ldg(p.bias + col + i);
+    }
+    if (p.z != nullptr) st_global_v2(p.z + at, pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    act_values<4>(p.act, v);
+    if (p.residual != nullptr) {
+        const uint2 u = *reinterpret_cast<const uint2*>(p.residual + at);
+        v[0] += bf16_lo(u.x);
+        v[1] += bf16_hi(u.x);
+        v[2] += bf16_lo(u.y);
+        v[3] += bf16_hi(u.y);
+    }
+}
+
 template <int MODE, int BN, int PAIR>
 __global__ void __launch_bounds__(Cfg<MODE, BN, PAIR>::THREADS_C, 1)
 dg_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
-               const __grid_constant__ CUtensorMap tmap_d, const __grid_constant__ Params p) {
+               const __grid_constant__ CUtensorMap tmap_d, const __grid_constant__ typename ParamsOf<MODE>::type p) {
     using C = Cfg<MODE, BN, PAIR>;
+    constexpr bool NORMAL = normal_layout(MODE);
     constexpr int STAGES = C::STAGES;
     constexpr int NACC = C::NACC;
     constexpr int COLS = C::COLS;
@@ -397,6 +500,7 @@ dg_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant
     __shared__ uint64_t tmem_full_bar[NACC], tmem_empty_bar[NACC];
     __shared__ uint64_t scale_full_bar[C::SCALE_SLOTS], scale_empty_bar[C::SCALE_SLOTS];
     __shared__ uint64_t xchg_full_bar, xchg_free_bar;   // narrow-tile partial-sum exchange
+    __shared__ uint64_t residual_bar[MODE == kEpilogue ? C::EPI_WARPS_C : 1];
     __shared__ uint32_t s_tmem_base;
     __shared__ int s_abort;
     __shared__ int s_prefix[MODE == kMasked ? MAX_MASKED_G + 1 : 1];
@@ -404,7 +508,7 @@ dg_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     // split-K: a cluster of p.split CTAs shares one tile (one tile per cluster), each CTA a K range
-    const bool split_k = ((MODE == kNormal || MODE == kMasked) && PAIR == 1 && p.split > 1);
+    const bool split_k = ((NORMAL || MODE == kMasked) && PAIR == 1 && p.split > 1);
     const int crank = (PAIR == 2 || split_k) ? static_cast<int>(cluster_ctarank()) : 0;
     const int rank = (PAIR == 2) ? crank : 0;      // row half of a CTA-pair tile
     const int srank = split_k ? crank : 0;         // K share of a split-K tile
@@ -445,6 +549,8 @@ dg_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant
             mbar_init(&xchg_full_bar, C::EPI_WARPS_C);
             mbar_init(&xchg_free_bar, C::EPI_WARPS_C);
         }
+        if constexpr (MODE == kEpilogue)
+            for (int w = 0; w < C::EPI_WARPS_C; ++w) mbar_init(&residual_bar[w], 1);
         s_abort = 0;
         fence_mbar_init();
     }
@@ -507,7 +613,7 @@ dg_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant
             // L2 policies for the long-K normal layout: a band's A row blocks are read again by the next
             // round of tiles, B's column blocks only by tiles in flight at the same time
             const uint64_t pol_a = policy_evict_last(), pol_b = policy_evict_first();
-            const bool hint = (MODE == kNormal && PAIR == 1 && p.l2_hint != 0);
+            const bool hint = (NORMAL && PAIR == 1 && p.l2_hint != 0);
             for (int t = unit; t < num_tiles && ok; t += num_units) {
                 const TileInfo ti = decode_tile<MODE, BN, PAIR>(p, t, s_prefix, rank, srank);
                 if (!ti.valid) continue;
@@ -541,10 +647,10 @@ dg_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant
                                 mbar_arrive_expect_tx(&full_bar[stage], PAIR * C::STAGE_BYTES);
                                 // MN-major operands: boxes of 128 M (N) bytes x 128 k rows; B takes one
                                 // box per 128 columns of the tile (the host allows it for BN % 128 == 0)
-                                if ((MODE == kNormal && p.a_mn)) tma_load_2d(&tmap_a, &full_bar[stage], a_dst, ti.a_row, x);
+                                if ((NORMAL && p.a_mn)) tma_load_2d(&tmap_a, &full_bar[stage], a_dst, ti.a_row, x);
                                 else if (hint) tma_load_2d_hint(&tmap_a, &full_bar[stage], a_dst, x, ti.a_row, pol_a);
                                 else tma_load_2d(&tmap_a, &full_bar[stage], a_dst, x, ti.a_row);
-                                if ((MODE == kNormal && p.b_mn)) {
+                                if ((NORMAL && p.b_mn)) {
                                     for (int j = 0; j < C::B_ROWS / 128; ++j)
                                         tma_load_2d(&tmap_b, &full_bar[stage], b_dst + j * (128 * BK), ti.b_row + 128 * j, x);
                                 } else if (hint) {
@@ -628,13 +734,13 @@ dg_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant
                     for (int j = 0; j < take; ++j) {
                         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
                         const uint32_t a_addr = a_base + stage * C::A_BYTES, b_addr = b_base + stage * C::B_BYTES;
-                        const uint64_t a_desc = (MODE == kNormal && p.a_mn) ? sw128_mnmajor_desc(a_addr, 128 * BK) : sw128_kmajor_desc(a_addr);
-                        const uint64_t b_desc = (MODE == kNormal && p.b_mn) ? sw128_mnmajor_desc(b_addr, 128 * BK) : sw128_kmajor_desc(b_addr);
+                        const uint64_t a_desc = (NORMAL && p.a_mn) ? sw128_mnmajor_desc(a_addr, 128 * BK) : sw128_kmajor_desc(a_addr);
+                        const uint64_t b_desc = (NORMAL && p.b_mn) ? sw128_mnmajor_desc(b_addr, 128 * BK) : sw128_kmajor_desc(b_addr);
                         // K-major: K = 32 is 32 bytes along the swizzled row (>> 4 = 2); MN-major: 32 rows
                         // of k, four whole 1024-byte atoms (>> 4 = 256)
-                        const uint32_t a_kstep = (MODE == kNormal && p.a_mn) ? (32 * 128) >> 4 : UMMA_K >> 4;
-                        const uint32_t b_kstep = (MODE == kNormal && p.b_mn) ? (32 * 128) >> 4 : UMMA_K >> 4;
-                        const uint32_t idesc = IDESC | ((MODE == kNormal && p.a_mn) ? IDESC_A_MN : 0u) | ((MODE == kNormal && p.b_mn) ? IDESC_B_MN : 0u);
+                        const uint32_t a_kstep = (NORMAL && p.a_mn) ? (32 * 128) >> 4 : UMMA_K >> 4;
+                        const uint32_t b_kstep = (NORMAL && p.b_mn) ? (32 * 128) >> 4 : UMMA_K >> 4;
+                        const uint32_t idesc = IDESC | ((NORMAL && p.a_mn) ? IDESC_A_MN : 0u) | ((NORMAL && p.b_mn) ? IDESC_B_MN : 0u);
                         if (issuer) {
 #pragma unroll
                             for (int k = 0; k < BK / UMMA_K; ++k) {
@@ -777,6 +883,8 @@ dg_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant
         const int row_in_tile = q * 32 + lane;
         const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + h * COLS;
         uint32_t xphase = 0;                   // narrow-tile exchange rounds so far (parity)
+        uint32_t rphase = 0;                   // epilogue mode: residual tiles so far (parity)
+        bool rpending = false;                 // ... and whether a residual copy has not been waited for
         int acc = 0, slot = 0;
         uint32_t acc_phase = 0, sphase = 0;
         bool ok = true;
@@ -786,6 +894,22 @@ dg_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant
             if (!ti.valid) continue;
             const int cstart = ti.n0 + h * COLS;   // first output column of this thread
             const int split = (128 * (cstart / 128 + 1) - cstart) / 16;   // chunks before the next block
+
+            // Epilogue mode: the residual's boxes of this warp's part of the tile are copied into the
+            // warp's output staging while the products run, once the previous tile's stores have read it.
+            bool residual_on = false;
+            if constexpr (MODE == kEpilogue) {
+                const int y = ti.d_row + q * 32;
+                residual_on = p.residual != nullptr && !split_k && y < p.rows && cstart < p.n;
+                rpending = residual_on;
+                if (residual_on && lane == 0) {
+                    bulk_wait_read_n<0>();
+                    const int boxes = min(COLS / 32, (p.n - cstart + 31) / 32);
+                    mbar_arrive_expect_tx(&residual_bar[ew], static_cast<uint32_t>(boxes) * 2048u);
+                    for (int r = 0; r < boxes; ++r)
+                        tma_load_2d(&p.tmap_r, &residual_bar[ew], s_store + ew * C::STORE_WARP_BYTES + r * 2048, cstart + r * 32, y);
+                }
+            }
 
             // the k-grouped output is added into D at the tile's end, so every layout starts the tile's
             // sum at zero
@@ -1035,6 +1159,20 @@ dg_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant
                     *reinterpret_cast<float4*>(prow + j) = make_float4(accum[j], accum[j + 1], accum[j + 2], accum[j + 3]);
                 continue;
             }
+            if constexpr (MODE == kEpilogue) {
+                bool got = true;
+                if (residual_on) {
+                    got = wait_bounded(&residual_bar[ew], rphase, abort_flag, p.status, p.wait_limit_ns);
+                    rphase ^= 1u;
+                    rpending = false;
+                }
+                if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+                // the staging holds the residual as the output's boxes will: this lane's row is its own
+                // 64 bytes of each box
+                const uint8_t* rbuf = s_store + ew * C::STORE_WARP_BYTES;
+                epilogue_tile<COLS>(accum, p, ti.d_row + row_in_tile, cstart, row_in_tile < ti.rows_valid,
+                                    residual_on ? rbuf : nullptr, lane);
+            }
             // ---- store this CTA's rows of the tile
             if constexpr (MODE == kKGrouped) {
                 // D[g] += tile (or D[g] = tile in the overwriting form). Per 16-column chunk and row i, the
@@ -1174,6 +1312,8 @@ dg_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant
                 }
             }
         }
+        // (aborting) a residual copy still in flight lands before the shared memory is given up
+        if (MODE == kEpilogue && rpending && lane == 0) drain_wait(&residual_bar[MODE == kEpilogue ? ew : 0], rphase);
         // every TMA store of this warp has completed (and released its staging buffer) before exit
         if (lane == 0) bulk_wait_all();
         __syncwarp();
@@ -1198,9 +1338,11 @@ dg_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant
                 const uint32_t off = static_cast<uint32_t>((row * C::PSTRIDE + c4) * 4);
                 const float4 sum = cluster_sum_v4(part_local + off, p.split);
                 if (row < ti.rows_valid && ti.n0 + c4 < p.n) {
-                    __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.d) +
-                                         static_cast<size_t>(ti.d_row + row) * p.n + ti.n0 + c4;
-                    st_global_v2(dst, pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
+                    const size_t at = static_cast<size_t>(ti.d_row + row) * p.n + ti.n0 + c4;
+                    __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.d) + at;
+                    float v[4] = {sum.x, sum.y, sum.z, sum.w};
+                    if constexpr (MODE == kEpilogue) epilogue_four(v, p, ti.n0 + c4, at);
+                    st_global_v2(dst, pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
                 }
             }
         }

@@ -102,10 +102,20 @@ __device__ __forceinline__ DecTile decode_dec(const Params& p, int t, const int*
     return ti;
 }
 
+// Epilogue mode: one element of D (the unsplit tiles hold a column of it per thread).
+__device__ __forceinline__ void epilogue_one(float& x, const EpilogueParams& p, int col, size_t at) {
+    float v[1] = {x};
+    if (p.bias != nullptr) v[0] += __ldg(p.bias + col);
+    if (p.z != nullptr) p.z[at] = __float2bfloat16_rn(v[0]);
+    act_values<1>(p.act, v);
+    if (p.residual != nullptr) v[0] += __bfloat162float(p.residual[at]);
+    x = v[0];
+}
+
 template <int MODE, int BMT>
 __global__ void __launch_bounds__(THREADS, 1)
 dg_decode_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
-                 const __grid_constant__ Params p) {
+                 const __grid_constant__ typename ParamsOf<MODE>::type p) {
     using C = CfgDec<BMT>;
     constexpr int STAGES = C::STAGES;
     constexpr int KG = C::KG;
@@ -411,7 +421,10 @@ dg_decode_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_consta
 #pragma unroll
                         for (int m = 0; m < HALF; ++m) {
                             const int rr = h * HALF + m;
-                            if (rr < ti.rows_valid) dcol[(d_row + rr) * p.n] = __float2bfloat16_rn(acc[m]);
+                            if (rr < ti.rows_valid) {
+                                if constexpr (MODE == kEpilogue) epilogue_one(acc[m], p, n, (d_row + rr) * p.n + n);
+                                dcol[(d_row + rr) * p.n] = __float2bfloat16_rn(acc[m]);
+                            }
                         }
                     }
                 }
@@ -434,9 +447,10 @@ dg_decode_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_consta
                         const int n4 = (f % (C::BNT / 4)) * 4;
                         const float4 sum = cluster_sum_v4(part_local + static_cast<uint32_t>((m * C::BNT + n4) * 4), p.split);
                         if (m < ti.rows_valid && ti.n0 + n4 < p.n) {
-                            __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.d) +
-                                                 static_cast<size_t>(ti.a_row + m) * p.n + ti.n0 + n4;
-                            st_global_v2(dst, pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
+                            const size_t at = static_cast<size_t>(ti.a_row + m) * p.n + ti.n0 + n4;
+                            float v[4] = {sum.x, sum.y, sum.z, sum.w};
+                            if constexpr (MODE == kEpilogue) epilogue_four(v, p, ti.n0 + n4, at);
+                            st_global_v2(reinterpret_cast<__nv_bfloat16*>(p.d) + at, pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
                         }
                     }
                 }

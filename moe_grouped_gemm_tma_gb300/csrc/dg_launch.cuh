@@ -15,7 +15,7 @@ struct Launch {
     CUtensorMap tmap_a;
     CUtensorMap tmap_b;
     CUtensorMap tmap_d;     // the BF16 output for TMA stores (unused by the k-grouped gradient)
-    Params params;
+    EpilogueParams params;   // the other modes' kernels take its Params part
     int units;          // work units wanted: tiles (single CTA) or tile pairs (CTA pairs)
     int sms;
     cudaStream_t stream;
@@ -98,7 +98,7 @@ cudaError_t launch(const Launch& L) {
     cfg.blockDim = dim3(C::THREADS_C, 1, 1);
     cfg.dynamicSmemBytes = C::DYN_SMEM;
     cfg.stream = L.stream;
-    if ((MODE == kNormal || MODE == kMasked) && PAIR == 1 && L.params.split > 1) {
+    if ((normal_layout(MODE) || MODE == kMasked) && PAIR == 1 && L.params.split > 1) {
         // split-K: one cluster of `split` CTAs per tile (masked: per possible tile), not persistent
         attr[0].id = cudaLaunchAttributeClusterDimension;
         attr[0].val.clusterDim.x = static_cast<unsigned>(L.params.split);
@@ -133,7 +133,7 @@ cudaError_t launch(const Launch& L) {
         cfg.attrs = attr;
         cfg.numAttrs += 1;
     }
-    Params prm = L.params;
+    typename ParamsOf<MODE>::type prm = L.params;
     if (const unsigned long long ns = take_armed_wait_fault()) {
         prm.wait_limit_ns = ns;
         prm.fault_skip_first_fill = 1;
