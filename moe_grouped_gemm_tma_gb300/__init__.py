@@ -48,6 +48,8 @@ def library_path() -> str:
 def load(build_if_missing: bool = True):
     """Load ``libdg.so`` (building it with nvcc first when absent or stale)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             from . import build as _build
@@ -92,27 +94,34 @@ def load(build_if_missing: bool = True):
     return _lib
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
+# The calls of a decode step are a few microseconds of GPU work each, so what the binding does per call is kept
+# small: addresses go to ctypes as plain numbers, and the current stream is asked for as one (building a
+# torch Stream object for it takes 3 us).
 def _ptr(t):
-    return ctypes.c_void_p(t.data_ptr()) if t is not None else None
+    return t.data_ptr() if t is not None else None
 
 
 def _stream(stream):
-    torch = _torch()
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+        c = _torch()._C
+        return c._cuda_getCurrentRawStream(c._cuda_getDevice())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _codes(t, name):
     torch = _torch()
-    if t.dtype == torch.float8_e4m3fn:
-        t = t.view(torch.uint8)
-    if t.dtype != torch.uint8:
+    if t.dtype != torch.float8_e4m3fn and t.dtype != torch.uint8:
         raise TypeError(f"{name} must hold e4m3 codes (torch.float8_e4m3fn or uint8), got {t.dtype}")
     return _dense(t, name)
 
@@ -344,7 +353,7 @@ def dg_gemm_fp8_nt_epilogue(A, sfa, B, sfb, D, bias=None, act="none", residual=N
     D = _typed(D, "D", torch.bfloat16, (M, N))
     if B.shape[1] != K:
         raise ValueError(f"shape mismatch: A {tuple(A.shape)} B {tuple(B.shape)}")
-    if (tuple(sfa.shape), tuple(sfb.shape)) != scale_shapes(M, N, K):
+    if (sfa.shape, sfb.shape) != scale_shapes(M, N, K):
         raise ValueError(f"scale shapes {tuple(sfa.shape)}, {tuple(sfb.shape)} != {scale_shapes(M, N, K)}")
     bias = _typed(bias, "bias", torch.float32, (N,))
     residual = _typed(residual, "residual", torch.bfloat16, (M, N))
@@ -371,10 +380,9 @@ def dg_epilogue_backward(dD, Z, q, sf, qt, sft, dbias, workspace=None, act="none
     Mp = (M + 127) // 128 * 128
     dD = _typed(dD, "dD", torch.bfloat16, (M, N))
     Z = _typed(Z, "Z", torch.bfloat16, (M, N))
-    if q is not None:
-        q = _typed(_codes(q, "q"), "q", torch.uint8, (M, N))
-    if qt is not None:
-        qt = _typed(_codes(qt, "qt"), "qt", torch.uint8, (N, Mp))
+    for name, t, shape in (("q", q, (M, N)), ("qt", qt, (N, Mp))):
+        if t is not None and _codes(t, name).shape != shape:
+            raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
     sf = _typed(sf, "sf", torch.float32, (M, N // 128))
     sft = _typed(sft, "sft", torch.float32, (N, Mp // 128))
     dbias = _typed(dbias, "dbias", torch.float32, (N,))

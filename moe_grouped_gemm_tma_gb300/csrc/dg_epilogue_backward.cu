@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(EB_THREADS, 2) epilogue_backward_kernel(const 
     __shared__ __align__(16) uint8_t s_codes[EB_TILE * EB_TILE];
     __shared__ __align__(16) uint32_t s_amax[16][EB_TILE];
     __shared__ __align__(16) float s_sum[8][EB_TILE];
-    __shared__ float s_scale[EB_TILE];
+    __shared__ float2 s_scale[EB_TILE];
     __shared__ int s_last;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -123,12 +123,12 @@ __global__ void __launch_bounds__(EB_THREADS, 2) epilogue_backward_kernel(const 
             for (int j = 0; j < 8; ++j) a = max(a, abs_bits(dz[i][j]));
 #pragma unroll
             for (int o = 8; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
-            const float s = block_scale(a), r = __frcp_rn(s);
+            const BlockScale k = block_scale(a);
             if (i < valid) {
-                const uint32_t w0 = quantise4(dz[i][0], dz[i][1], dz[i][2], dz[i][3], s, r);
-                const uint32_t w1 = quantise4(dz[i][4], dz[i][5], dz[i][6], dz[i][7], s, r);
+                const uint32_t w0 = quantise4(dz[i][0], dz[i][1], dz[i][2], dz[i][3], k);
+                const uint32_t w1 = quantise4(dz[i][4], dz[i][5], dz[i][6], dz[i][7], k);
                 *reinterpret_cast<uint2*>(p.q + base + static_cast<size_t>(i) * p.n) = make_uint2(w0, w1);
-                if (l16 == 0) p.sf[static_cast<size_t>(m0 + r0 + i) * (p.n / 128) + blockIdx.y] = s;
+                if (l16 == 0) p.sf[static_cast<size_t>(m0 + r0 + i) * (p.n / 128) + blockIdx.y] = k.s;
             }
         }
     }
@@ -142,9 +142,9 @@ __global__ void __launch_bounds__(EB_THREADS, 2) epilogue_backward_kernel(const 
             uint32_t a = 0;
 #pragma unroll
             for (int g = 0; g < 16; ++g) a = max(a, s_amax[g][c]);
-            const float s = block_scale(a);
-            s_scale[c] = s;
-            p.sft[static_cast<size_t>(n0 + c) * mt + blockIdx.x] = s;
+            const BlockScale k = block_scale(a);
+            s_scale[c] = make_float2(k.d, k.r);
+            p.sft[static_cast<size_t>(n0 + c) * mt + blockIdx.x] = k.s;
         }
     } else if (p.dbias != nullptr) {
         const int c = threadIdx.x - EB_TILE;
@@ -164,9 +164,9 @@ __global__ void __launch_bounds__(EB_THREADS, 2) epilogue_backward_kernel(const 
     if (p.qt != nullptr) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const float s = s_scale[c0 + j], r = __frcp_rn(s);
-            const uint32_t w0 = quantise4(dz[0][j], dz[1][j], dz[2][j], dz[3][j], s, r);
-            const uint32_t w1 = quantise4(dz[4][j], dz[5][j], dz[6][j], dz[7][j], s, r);
+            const BlockScale k{0.f, s_scale[c0 + j].x, s_scale[c0 + j].y};
+            const uint32_t w0 = quantise4(dz[0][j], dz[1][j], dz[2][j], dz[3][j], k);
+            const uint32_t w1 = quantise4(dz[4][j], dz[5][j], dz[6][j], dz[7][j], k);
             const int slot = (warp * 2 + half) ^ l16;
             *reinterpret_cast<uint2*>(s_codes + (c0 + j) * EB_TILE + slot * 8) = make_uint2(w0, w1);
         }

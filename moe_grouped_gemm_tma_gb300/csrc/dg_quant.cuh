@@ -17,25 +17,42 @@ namespace dg {
 constexpr float E4M3_TOP = 448.f;
 constexpr float AMAX_FLOOR = 1e-4f;
 
-// The scale of a block from its largest magnitude, given as the bits of |v|: as unsigned integers these
-// order like the magnitudes, with the infinity above every finite value and NaN above that, so integer
-// maxima carry NaN through (fmaxf would drop it).
-__device__ __forceinline__ float block_scale(uint32_t amax_bits) {
-    const float a = __uint_as_float(amax_bits);
-    return __fdiv_rn(a < AMAX_FLOOR ? AMAX_FLOOR : a, E4M3_TOP);
-}
-
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
-// v / s correctly rounded, for many v of one block: with r = 1 / s to nearest, q = v r is within an ulp of
-// the quotient and q + (v - q s) r, each step fused, rounds to it (Markstein's division). The residual is
-// not finite for an infinite scale, where the caller divides instead (`finite_scale`).
-__device__ __forceinline__ float block_quotient(float v, float s, float r) {
+// 1 / s to nearest: the hardware's approximation and one Newton step.
+__device__ __forceinline__ float reciprocal(float s) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    return fmaf(fmaf(-s, r, 1.f), r, r);
+}
+
+// v / s correctly rounded, with r = 1 / s to nearest: q = v r is within an ulp of the quotient and
+// q + (v - q s) r, each step fused, rounds to it (Markstein's division). Three instructions where the general
+// division takes a dozen and a call, which counts here: the quantisation is bound by instruction issue.
+__device__ __forceinline__ float quotient(float v, float s, float r) {
     const float q = v * r;
     return fmaf(fmaf(-q, s, v), r, q);
 }
 
-__device__ __forceinline__ bool finite_scale(float s) { return abs_bits(s) < 0x7f800000u; }
+// The scale of a block, and what its values are divided by. The largest magnitude comes as the bits of |v|:
+// as unsigned integers these order like the magnitudes, with the infinity above every finite value and NaN
+// above that, so integer maxima carry NaN through (fmaxf would drop it). For a scale that is not finite the
+// divisor's pair is (0, 0) or (0, NaN), for which quotient() gives what the division would: 0 for finite
+// values over an infinite scale, NaN for infinite ones and wherever the scale is NaN.
+struct BlockScale {
+    float s;               // the scale
+    float d, r;            // divisor and its reciprocal for quotient()
+};
+
+__device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits) {
+    const float a = __uint_as_float(amax_bits);
+    const bool finite = amax_bits < 0x7f800000u;
+    BlockScale b;
+    b.s = finite ? quotient(a < AMAX_FLOOR ? AMAX_FLOOR : a, E4M3_TOP, 1.f / E4M3_TOP) : a;
+    b.d = finite ? b.s : 0.f;
+    b.r = finite ? reciprocal(b.s) : (amax_bits == 0x7f800000u ? 0.f : a);
+    return b;
+}
 
 // Two values to e4m3 codes, `lo` in the low byte (to nearest even, saturating, NaN kept).
 __device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
@@ -45,19 +62,9 @@ __device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
 }
 
 // Four values of a block to codes, in order from the lowest byte.
-__device__ __forceinline__ uint32_t quantise4(float a, float b, float c, float d, float s, float r) {
-    if (finite_scale(s)) {
-        a = block_quotient(a, s, r);
-        b = block_quotient(b, s, r);
-        c = block_quotient(c, s, r);
-        d = block_quotient(d, s, r);
-    } else {
-        a = __fdiv_rn(a, s);
-        b = __fdiv_rn(b, s);
-        c = __fdiv_rn(c, s);
-        d = __fdiv_rn(d, s);
-    }
-    return pack_e4m3x2(a, b) | (pack_e4m3x2(c, d) << 16);
+__device__ __forceinline__ uint32_t quantise4(float a, float b, float c, float d, const BlockScale& k) {
+    return pack_e4m3x2(quotient(a, k.d, k.r), quotient(b, k.d, k.r)) |
+           (pack_e4m3x2(quotient(c, k.d, k.r), quotient(d, k.d, k.r)) << 16);
 }
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
