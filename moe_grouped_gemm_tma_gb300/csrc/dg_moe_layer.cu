@@ -20,11 +20,14 @@
 //     on the way into shared memory, in every CTA, saves that barrier but not time: four warps take 1.2 us a
 //     stage for one token and 2.5 us for 32, where the weights take 0.74.)
 //   * A phase-1 unit is 128 gate rows with their 128 up rows; whoever completes it applies the activation and
-//     quantises 128 hidden values per token. A phase-2 unit is 256 output rows of one expert, written as FP32
+//     quantises 128 hidden values per token. Four warps of their own do that, from the sums that the promoting
+//     warps leave in L2: a round trip through L2 takes 2 us beside the weight stream, and a divided unit takes
+//     four of them. A phase-2 unit is 256 output rows of one expert, written as FP32
 //     per gathered row; after the last grid barrier all CTAs sum each token's experts, weighted, in order.
 //
 // Warp roles: warp 0 streams weights, warp 2 tokens and their scales, warp 1 issues MMAs, warp 3 crosses the grid
-// barriers, warps 4..11 quantise the tokens, promote and finish units. Every wait is bounded as in dg_gemm_kernel; a CTA that gives up still arrives at the grid
+// barriers, warps 4..7 finish phase-1 units, warps 8..15 promote; those twelve quantise the tokens at the start and
+// sum the output at the end. Every wait is bounded as in dg_gemm_kernel; a CTA that gives up still arrives at the grid
 // barriers.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -45,12 +48,18 @@ namespace {
 constexpr int ML_MAX_T = 64;
 constexpr int ML_MAX_A = 1024;                 // assignments, T * k
 constexpr int ML_MAX_E = 1024;
-constexpr int ML_MAX_CTAS = 192;               // CTAs (workspace slots) at most; one per SM
+constexpr int ML_MAX_CTAS = 160;               // CTAs (workspace slots) at most; one per SM
 constexpr int ML_MAX_ROWS = ML_MAX_A + 3 * ML_MAX_A;   // gathered rows: every expert's start on a multiple of 4
 constexpr int ML_W_BYTES = 2 * 128 * BK;       // weights of a stage
 constexpr int ML_FIXED = 4096;                 // workspace: barrier word and counters
+constexpr int ML_THREADS = 512;
+constexpr int ML_FIN_WARP0 = 4, ML_EPI_WARP0 = 8, ML_WORKERS = 12;
+constexpr int ML_CTRL_REGS = 56, ML_FIN_REGS = 104, ML_EPI_REGS = 176;  // 128 * (56 + 104) + 256 * 176 = 512 * 128
+constexpr int ML_PARTS = 4;                    // segments between the promoting and the finishing warps
+constexpr int ML_SLOTS = 4 + ML_PARTS;         // sums in L2 per CTA: first and last unit of either line, whole units
 constexpr int ML_BARRIERS = 4;                 // grid barriers: tokens, hidden of either half, products
 constexpr unsigned FULL_MASK = 0xffffffffu;
+constexpr uint32_t NO_ROW = 0xffffffffu;
 
 struct MoeParams {
     const __nv_bfloat16* x;
@@ -64,7 +73,7 @@ struct MoeParams {
     float* sx;             // [H / 128][rows_cap]
     uint8_t* hg;           // [rows_cap][I] codes of the hidden activations, by gathered row
     float* sh;             // [I / 128][rows_cap]
-    float* parts;          // [CTA][phase-1 line][2][NT][256]: parts of divided phase-1 units
+    float* parts;          // [CTA][ML_SLOTS][NT][256]: sums of phase-1 units and of parts of them
     float* y;              // [gathered row][part][pairs * 256] weighted by nothing yet
     unsigned* barrier;     // grid barrier word
     unsigned* count;       // [phase-1 line][CTA]: parts written of the unit that the CTA's share ends in
@@ -82,11 +91,12 @@ struct MlCfg {
     // The token scales of a stage live until it is promoted: the ring and the accumulators can hold that
     // many stages between the two, so with two more no slot is rewritten before it has been read.
     static constexpr int SLOTS = 6 + NACC + 2;
-    static constexpr int TABLES = 4 * ML_MAX_A + 2 * ML_MAX_A + ML_MAX_ROWS + 4 * 4 * (ML_MAX_CTAS + 1);
-    static constexpr int STATIC_RESERVE = TABLES + SLOTS * NT * 4 + 2 * 32 * 4 * 6 + 640;
+    static constexpr int TABLES = 4 * ML_MAX_A + 4 * ML_MAX_A + ML_MAX_ROWS + 4 * 4 * (ML_MAX_CTAS + 1);
+    static constexpr int STATIC_RESERVE = TABLES + SLOTS * NT * 4 + 768;
     static constexpr int STAGES_FIT = ring_stages(STAGE_BYTES, 0, 0, STATIC_RESERVE);
     static constexpr int STAGES = STAGES_FIT > 6 ? 6 : STAGES_FIT;
     static constexpr int DYN_SMEM = 1024 + STAGES * STAGE_BYTES;
+    static constexpr int FLIGHT = 3;            // weight stages in flight at once
     static constexpr int NG = NT / 16;          // 8-column groups per epilogue warpgroup
     static_assert(DYN_SMEM + STATIC_RESERVE <= SMEM_LIMIT && STAGES >= 4, "ring");
 };
@@ -119,19 +129,22 @@ __device__ __forceinline__ unsigned atom_add_acq_rel(unsigned* p, unsigned v) {
     return old;
 }
 
-__device__ __forceinline__ void epi_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ void finishers_barrier() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+__device__ __forceinline__ void add4(float4& a, const float4& b) { a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w; }
 
 // One thread's arrival at the barrier of all CTAs, and its wait. CTA 0 adds what carries the others' ones
 // into the top bit, so the bit flips when the last one arrives and the low bits are back at zero: the word
-// needs no reset between barriers or launches. The CTAs are co-resident (cooperative launch); the wait ends
-// by itself all the same.
-__device__ __forceinline__ bool grid_barrier(unsigned* word, volatile int* abort_flag, int* status, uint64_t limit_ns) {
+// needs no reset between barriers or launches. `top` is the top bit before this barrier (it cannot flip before
+// this CTA has arrived), so the arrival itself has nothing to wait for. The CTAs are co-resident (cooperative
+// launch); the wait ends by itself all the same.
+__device__ __forceinline__ bool grid_barrier(unsigned* word, unsigned top, volatile int* abort_flag, int* status, uint64_t limit_ns) {
     const unsigned add = blockIdx.x == 0 ? 0x80000000u - (gridDim.x - 1) : 1u;
-    const unsigned old = atom_add_acq_rel(word, add);
+    asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(word), "r"(add) : "memory");
     const uint64_t t0 = global_timer_ns();
     const uint64_t limit = limit_ns ? limit_ns : WAIT_LIMIT_NS;
     for (int i = 0; i < (1 << 26); ++i) {
-        if ((ld_acquire(word) ^ old) & 0x80000000u) return true;
+        if ((ld_acquire(word) ^ top) & 0x80000000u) return true;
         if ((i & 63) == 63 && global_timer_ns() - t0 > limit) break;
     }
     *abort_flag = 1;
@@ -146,17 +159,16 @@ __device__ __forceinline__ uint32_t pack_chunk(int e, int off, int n) {
 
 template <int NT>
 struct Shared {
-    uint64_t full[MlCfg<NT>::STAGES], empty[MlCfg<NT>::STAGES];
+    uint64_t full_w[MlCfg<NT>::STAGES], full_t[MlCfg<NT>::STAGES], empty[MlCfg<NT>::STAGES];   // weights, tokens
     uint64_t acc_full[MlCfg<NT>::NACC], acc_empty[MlCfg<NT>::NACC];
     uint64_t scale_full[MlCfg<NT>::SLOTS];
+    uint64_t part_full[ML_PARTS], part_empty[ML_PARTS];
     uint64_t done[ML_BARRIERS], go[ML_BARRIERS];                   // this CTA's work before a grid barrier is done; it is crossed
     uint32_t tmem;
     int abort, chunks, rows, last;
     __align__(16) float scales[MlCfg<NT>::SLOTS][NT];
-    uint32_t amax[2][4][32];                    // [warpgroup][warp][column] of a unit being finished
-    float unit_scale[2][2][32];                 // [warpgroup]: each column's divisor and its reciprocal
     uint32_t chunk[ML_MAX_A];
-    uint16_t row_of[ML_MAX_A];                  // gathered row of an assignment (t * k + j); 0xffff: no expert
+    uint32_t row_of[ML_MAX_A];                  // gathered row of an assignment (t * k + j) | chunk << 16, or NO_ROW
     uint8_t token[ML_MAX_ROWS];                 // token of a gathered row
     uint32_t share[4][ML_MAX_CTAS + 1];         // first stage of each CTA's share of each line
 };
@@ -168,9 +180,18 @@ struct Line {
     int total;             // stages
 };
 
+// Chunks of the first "half", five eighths: the second's phase 1 has to hide the finishing of the first's units,
+// and the first's phase 2, which is half as long per chunk, that of the second's. Where half of phase 1 streams for less than the 8 us that its units take to be
+// finished and seen by all (11 stages a CTA), one half is all: a second one only adds a barrier (5 tokens, 8
+// experts of 1024 x 384: 25 us with halves, 21 without; 1 token, 8 experts of 7168 x 2048: 70 and 76).
+__device__ __forceinline__ int first_half(const MoeParams& p, int chunks) {
+    const int stages = chunks * (p.I / 128) * (p.H / 128);
+    return stages >= 22 * static_cast<int>(gridDim.x) ? (chunks * 5 + 7) / 8 : chunks;
+}
+
 __device__ __forceinline__ Line line_of(const MoeParams& p, int chunks, int l) {
     Line n;
-    const int half = (chunks + 1) / 2;
+    const int half = first_half(p, chunks);
     n.c0 = (l & 1) ? half : 0;
     n.nc = (l & 1) ? chunks - half : half;
     n.kbs = (l < 2 ? p.H : p.I) / 128;
@@ -271,31 +292,48 @@ __device__ __forceinline__ bool for_segments(const MoeParams& p, const Shared<NT
 }
 
 // ---- routing: chunks of at most NT tokens of one expert, their rows, and each assignment's row (its rank among
-// the assignments of its expert, in order). Every CTA makes the same tables from the same ids. `scratch`: 8 KB.
+// the assignments of its expert, in order). Every CTA makes the same tables from the same ids: every warp ranks
+// 32 assignments among themselves and counts their experts, the counts are summed over the warps' turns per
+// expert, then over the experts. `scratch`: 72 KB.
 template <int NT>
-__device__ void make_tables(const MoeParams& p, Shared<NT>& s, uint32_t* scratch) {
-    uint32_t* offset = scratch;                                          // rows of an expert, then its first row
-    int32_t* ids = reinterpret_cast<int32_t*>(scratch + ML_MAX_E);
+__device__ void make_tables(const MoeParams& p, Shared<NT>& s, uint8_t* scratch) {
+    uint32_t* offset = reinterpret_cast<uint32_t*>(scratch);            // rows of an expert, then its first row
+    uint32_t* first_chunk = offset + ML_MAX_E;
+    uint16_t* counts = reinterpret_cast<uint16_t*>(first_chunk + ML_MAX_E);   // [group of 32 assignments][expert]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int A = p.T * p.k;
-    for (int a = tid; a < A; a += THREADS) {
-        const int e = __ldg(p.ids + a);
-        ids[a] = e >= 0 && e < p.E ? e : -1;
+    const int A = p.T * p.k, groups = (A + 31) / 32;
+    const int pitch = (p.E + 7) & ~7;
+    constexpr int TURNS = ML_MAX_A / ML_THREADS;
+    int expert[TURNS], rank[TURNS];
+#pragma unroll
+    for (int i = 0; i < TURNS; ++i) {
+        const int a = i * ML_THREADS + tid;
+        expert[i] = a < A ? __ldg(p.ids + a) : -1;
+        if (expert[i] >= p.E) expert[i] = -1;
     }
-    for (int e = tid; e < p.E; e += THREADS) offset[e] = 0;
+    for (int i = tid; i < groups * pitch / 8; i += ML_THREADS) reinterpret_cast<uint4*>(counts)[i] = make_uint4(0u, 0u, 0u, 0u);
     __syncthreads();
-    if (warp == EPI_WARP0) {
-        for (int base = 0; base < A; base += 32) {
-            const int a = base + lane;
-            const int e = a < A ? ids[a] : -1;
-            const unsigned same = __match_any_sync(FULL_MASK, e);
-            const int rank = __popc(same & ((1u << lane) - 1u));
-            const uint32_t before = e >= 0 ? offset[e] : 0u;
-            __syncwarp();
-            if (a < A) s.row_of[a] = e >= 0 ? static_cast<uint16_t>(before + rank) : 0xffffu;
-            if (e >= 0 && rank == 0) offset[e] = before + __popc(same);
-            __syncwarp();
+#pragma unroll
+    for (int i = 0; i < TURNS; ++i) {
+        const int g = i * (ML_THREADS / 32) + warp;
+        if (g >= groups) continue;
+        const int e = expert[i] < 0 ? -1 : expert[i];
+        const unsigned same = __match_any_sync(FULL_MASK, e);
+        rank[i] = __popc(same & ((1u << lane) - 1u));
+        if (e >= 0 && rank[i] == 0) counts[g * pitch + e] = static_cast<uint16_t>(__popc(same));
+    }
+    __syncthreads();
+    for (int e = tid; e < p.E; e += ML_THREADS) {
+        uint32_t sum = 0;
+        for (int g = 0; g < groups; ++g) {
+            const uint32_t n = counts[g * pitch + e];
+            counts[g * pitch + e] = static_cast<uint16_t>(sum);
+            sum += n;
         }
+        offset[e] = sum;
+    }
+    __syncthreads();
+    if (warp == ML_FIN_WARP0) {
         // exclusive sums over the experts: rows rounded up to 4, and chunks
         int rows = 0, chunks = 0;
         for (int base = 0; base < p.E; base += 32) {
@@ -309,7 +347,10 @@ __device__ void make_tables(const MoeParams& p, Shared<NT>& s, uint32_t* scratch
                 if (lane >= o) { r += ur; c += uc; }
             }
             const int r0 = rows + r - r_own, c0 = chunks + c - c_own;
-            if (e < p.E) offset[e] = static_cast<uint32_t>(r0);
+            if (e < p.E) {
+                offset[e] = static_cast<uint32_t>(r0);
+                first_chunk[e] = static_cast<uint32_t>(c0);
+            }
             for (int i = 0; i < c_own; ++i) s.chunk[c0 + i] = pack_chunk(e, r0 + i * NT, min(NT, n - i * NT));
             rows += __shfl_sync(FULL_MASK, r, 31);
             chunks += __shfl_sync(FULL_MASK, c, 31);
@@ -320,27 +361,127 @@ __device__ void make_tables(const MoeParams& p, Shared<NT>& s, uint32_t* scratch
         }
     }
     __syncthreads();
-    for (int a = tid; a < A; a += THREADS) {
-        if (s.row_of[a] != 0xffffu) {
-            const uint32_t r = offset[ids[a]] + s.row_of[a];
-            s.row_of[a] = static_cast<uint16_t>(r);
+#pragma unroll
+    for (int i = 0; i < TURNS; ++i) {
+        const int a = i * ML_THREADS + tid;
+        if (a >= A) continue;
+        const int e = expert[i];
+        uint32_t where = NO_ROW;
+        if (e >= 0) {
+            const uint32_t n = counts[(a >> 5) * pitch + e] + static_cast<uint32_t>(rank[i]);   // of the expert's rows
+            const uint32_t r = offset[e] + n;
+            where = r | ((first_chunk[e] + n / NT) << 16);
             s.token[r] = static_cast<uint8_t>(a / p.k);
         }
+        s.row_of[a] = where;
     }
-    for (int i = tid; i < 4 * static_cast<int>(gridDim.x + 1); i += THREADS) {
+    for (int i = tid; i < 4 * static_cast<int>(gridDim.x + 1); i += ML_THREADS) {
         const int l = i / static_cast<int>(gridDim.x + 1), c = i - l * static_cast<int>(gridDim.x + 1);
         const Line n = line_of(p, s.chunks, l);
         s.share[l][c] = n.total ? share_start(n.total, static_cast<unsigned>(c)) : 0u;
     }
 }
 
+// ---- output: a warp takes 128 columns of a token and adds up the parts of its experts' sums, weighted, from task
+// `first` on. Eight lanes hold the columns, 16 each; the warp's four groups of eight take every fourth part, three
+// at a time, and their sums are added at the end: a fixed order. The loop is short on purpose: this code is
+// new to the SM when the last grid barrier opens, and unrolled over the parts it waited for its instructions
+// longer than for its loads (6 us for one token). The sources are worked out before that barrier.
 template <int NT>
-__global__ void __launch_bounds__(THREADS, 1)
+__device__ __forceinline__ void sum_output(const MoeParams& p, const Shared<NT>& s, int first, bool ok, volatile int* abort_flag, int lane) {
+    const Line la = line_of(p, s.chunks, 2), lb = line_of(p, s.chunks, 3);
+    const int pa = most_parts(la), pb = most_parts(lb);
+    const int base_b = lb.nc ? static_cast<int>((s.chunk[la.nc] >> 10) & 0xfffu) : s.rows;
+    const size_t width = static_cast<size_t>(la.blocks) * 256;
+    const int blocks = p.H / 128, tasks = p.T * blocks, stride = static_cast<int>(gridDim.x) * ML_WORKERS;
+    const int group = lane >> 3, l8 = lane & 7;
+    bool crossed = false;
+    for (int w = first; w < tasks && ok; w += stride) {
+        const int t = w / blocks, blk = w - t * blocks;
+        float sum[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sum[i] = 0.f;
+#pragma unroll 1
+        for (int j0 = 0; j0 < p.k; j0 += 32) {
+            // lane j: where assignment j's sums of this block lie (in rows of `width`), of how many parts they
+            // are (0: no expert), and its weight
+            int at = 0, parts = 0;
+            float weight = 0.f;
+            const int here = min(32, p.k - j0);
+            const uint32_t where = lane < here ? s.row_of[t * p.k + j0 + lane] : NO_ROW;
+            if (where != NO_ROW) {
+                weight = __ldg(p.weights + t * p.k + j0 + lane);
+                const int row = static_cast<int>(where & 0xffffu), chunk = static_cast<int>(where >> 16);
+                const bool b = chunk >= la.nc;
+                const int nc = b ? lb.nc : la.nc, total = b ? lb.total : la.total;
+                const unsigned u0 = static_cast<unsigned>((blk >> 1) * nc + chunk - (b ? la.nc : 0)) * la.kbs;
+                parts = cta_of(u0 + la.kbs - 1, total) - cta_of(u0, total) + 1;
+                at = b ? base_b * pa + (row - base_b) * pb : row * pa;
+            }
+            const int most = static_cast<int>(__reduce_max_sync(FULL_MASK, static_cast<unsigned>(parts))) * here;
+            if (!crossed) {
+                const bool got = wait_bounded(const_cast<uint64_t*>(&s.go[3]), 0, abort_flag, p.status, p.wait_limit_ns);
+                ok = __all_sync(FULL_MASK, got) != 0;
+                crossed = true;
+            }
+#pragma unroll 1
+            for (int n0 = 0; n0 < most; n0 += 12) {
+                float4 v[3][4];
+                float u[3];
+#pragma unroll
+                for (int i = 0; i < 3; ++i) {
+                    const int n = n0 + 4 * i + group, c = n / here, j = n - c * here;
+                    const int f = __shfl_sync(FULL_MASK, at, j);
+                    const bool there = c < __shfl_sync(FULL_MASK, parts, j);
+                    u[i] = __shfl_sync(FULL_MASK, weight, j);
+                    u[i] = there ? u[i] : 0.f;
+                    const float4* src = reinterpret_cast<const float4*>(p.y + static_cast<size_t>(f + c) * width + blk * 128 + l8 * 16);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        v[i][x] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (there) v[i][x] = __ldcg(src + x);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 3; ++i)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        sum[4 * x + 0] = fmaf(u[i], v[i][x].x, sum[4 * x + 0]);
+                        sum[4 * x + 1] = fmaf(u[i], v[i][x].y, sum[4 * x + 1]);
+                        sum[4 * x + 2] = fmaf(u[i], v[i][x].z, sum[4 * x + 2]);
+                        sum[4 * x + 3] = fmaf(u[i], v[i][x].w, sum[4 * x + 3]);
+                    }
+            }
+        }
+        // the groups' sums: groups g and g ^ 2 exchange halves of the columns, then g and g ^ 1 quarters, so that
+        // a lane ends with four columns, 4 * group' of its 16
+        float half[8], four[4];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float give = group & 2 ? sum[i] : sum[8 + i], keep = group & 2 ? sum[8 + i] : sum[i];
+            half[i] = keep + __shfl_xor_sync(FULL_MASK, give, 16);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float give = group & 1 ? half[i] : half[4 + i], keep = group & 1 ? half[4 + i] : half[i];
+            four[i] = keep + __shfl_xor_sync(FULL_MASK, give, 8);
+        }
+        const size_t at = static_cast<size_t>(t) * p.H + blk * 128 + l8 * 16 + group * 4;
+        if (p.residual != nullptr) {
+            const uint2 res = *reinterpret_cast<const uint2*>(p.residual + at);
+            four[0] += bf16_lo(res.x); four[1] += bf16_hi(res.x); four[2] += bf16_lo(res.y); four[3] += bf16_hi(res.y);
+        }
+        if (ok) st_global_v2(p.out + at, pack_bf16x2(four[0], four[1]), pack_bf16x2(four[2], four[3]));
+    }
+}
+
+template <int NT>
+__global__ void __launch_bounds__(ML_THREADS, 1)
 moe_layer_kernel(const __grid_constant__ CUtensorMap map_w13, const __grid_constant__ CUtensorMap map_w2,
                  const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_h,
                  const __grid_constant__ MoeParams p) {
     using C = MlCfg<NT>;
-    constexpr int STAGES = C::STAGES, NACC = C::NACC, NG = C::NG, SLOTS = C::SLOTS;
+    constexpr int STAGES = C::STAGES, NACC = C::NACC, NG = C::NG, SLOTS = C::SLOTS, FLIGHT = C::FLIGHT;
     static_assert(sizeof(Shared<NT>) <= C::STATIC_RESERVE, "static shared memory");
     static_assert(SLOTS >= STAGES + NACC + 2, "a scale slot is rewritten only after it has been read");
 
@@ -359,7 +500,8 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap map_w13, const __grid_const
         prefetch_tmap(&map_x);
         prefetch_tmap(&map_h);
         for (int i = 0; i < STAGES; ++i) {
-            mbar_init(&s.full[i], 2);           // the weight and the token producer
+            mbar_init(&s.full_w[i], 1);
+            mbar_init(&s.full_t[i], 1);
             mbar_init(&s.empty[i], 1);
         }
         for (int i = 0; i < NACC; ++i) {
@@ -367,8 +509,12 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap map_w13, const __grid_const
             mbar_init(&s.acc_empty[i], EPI_WARPS);
         }
         for (int i = 0; i < SLOTS; ++i) mbar_init(&s.scale_full[i], 1);
+        for (int i = 0; i < ML_PARTS; ++i) {
+            mbar_init(&s.part_full[i], EPI_WARPS);
+            mbar_init(&s.part_empty[i], 4);
+        }
         for (int i = 0; i < ML_BARRIERS; ++i) {
-            mbar_init(&s.done[i], EPI_WARPS);
+            mbar_init(&s.done[i], i == 0 ? ML_WORKERS : (i < 3 ? 4 : EPI_WARPS));
             mbar_init(&s.go[i], 1);
         }
         s.abort = 0;
@@ -380,18 +526,18 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap map_w13, const __grid_const
     }
     // the tokens' values that this warp quantises (blocks w, w + stride, ...; the first ones are loaded while
     // the tables are made)
-    constexpr int AHEAD = 3;
-    const int kbs_x = p.H / 128, blocks_x = p.T * kbs_x, stride_x = static_cast<int>(gridDim.x) * EPI_WARPS;
-    const int first_x = cta + (warp - EPI_WARP0) * static_cast<int>(gridDim.x);
+    constexpr int AHEAD = 2;
+    const int kbs_x = p.H / 128, blocks_x = p.T * kbs_x, stride_x = static_cast<int>(gridDim.x) * ML_WORKERS;
+    const int first_x = cta + (warp - ML_FIN_WARP0) * static_cast<int>(gridDim.x);
     uint2 ahead[AHEAD];
-    if (warp >= EPI_WARP0) {
+    if (warp >= ML_FIN_WARP0) {
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
             const int w = first_x + i * stride_x;
             if (w < blocks_x) ahead[i] = *reinterpret_cast<const uint2*>(p.x + static_cast<size_t>(w) * 128 + lane * 4);
         }
     }
-    make_tables<NT>(p, s, reinterpret_cast<uint32_t*>(smem));   // before the ring is in use
+    make_tables<NT>(p, s, smem);   // before the ring is in use
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
@@ -400,23 +546,37 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap map_w13, const __grid_const
     volatile int* abort_flag = &s.abort;
     const auto nothing = [](int) { return true; };
 
-    if (warp < EPI_WARP0) {
-        regs_dec<CTRL_REGS>();
+    if (warp < ML_FIN_WARP0) {
+        regs_dec<ML_CTRL_REGS>();
         const bool issuer = elect_one();
         if (warp == 0) {
             // ---------------------------------------------------------------- weights
-            Ring ring;
+            // At most FLIGHT stages are on their way at once: what the whole GPU has asked of HBM is the latency
+            // of every other access (all the rings' 29 MB are 4.4 us of HBM), and half of that already keeps
+            // HBM busy. The rest of the ring fills up while the consumers wait for something. One at a time until
+            // the tokens are there, whose stores and barrier nothing can hide.
+            const uint64_t once = policy_evict_first();   // L2 is for the sums and activations
+            Ring ring, landed;
+            int flying = 0, limit = 1;
             uint32_t issued = 0, issued_parity = 0;
             bool ok = for_segments<NT>(p, s, nothing, [&](auto tag, int, const Line&, const Seg& g) {
                 const CUtensorMap* map = decltype(tag)::value == 1 ? &map_w13 : &map_w2;
                 for (int kb = g.kb0; kb < g.kb0 + g.nkb; ++kb) {
-                    const bool got = wait_bounded(&s.empty[ring.stage], ring.phase ^ 1u, abort_flag, p.status, p.wait_limit_ns);
+                    bool got = wait_bounded(&s.empty[ring.stage], ring.phase ^ 1u, abort_flag, p.status, p.wait_limit_ns);
+                    if (limit == 1 && mbar_test_wait(&s.go[0], 0)) limit = FLIGHT;
+                    limit = __shfl_sync(FULL_MASK, limit, 0);
+                    if (flying == limit) {
+                        got = got && wait_bounded(&s.full_w[landed.stage], landed.phase, abort_flag, p.status, p.wait_limit_ns);
+                        landed.next(STAGES);
+                    } else {
+                        ++flying;
+                    }
                     if (!__all_sync(FULL_MASK, got)) return false;
                     if (issuer) {
                         uint8_t* dst = smem + ring.stage * ML_W_BYTES;
-                        mbar_arrive_expect_tx(&s.full[ring.stage], g.two ? ML_W_BYTES : ML_W_BYTES / 2);
-                        tma_load_2d(map, &s.full[ring.stage], dst, kb * BK, g.row0);
-                        if (g.two) tma_load_2d(map, &s.full[ring.stage], dst + 128 * BK, kb * BK, g.row1);
+                        mbar_arrive_expect_tx(&s.full_w[ring.stage], g.two ? ML_W_BYTES : ML_W_BYTES / 2);
+                        tma_load_2d_hint(map, &s.full_w[ring.stage], dst, kb * BK, g.row0, once);
+                        if (g.two) tma_load_2d_hint(map, &s.full_w[ring.stage], dst + 128 * BK, kb * BK, g.row1, once);
                     }
                     issued |= 1u << ring.stage;
                     issued_parity = (issued_parity & ~(1u << ring.stage)) | (ring.phase << ring.stage);
@@ -433,7 +593,7 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap map_w13, const __grid_const
             }
             if (!ok && issuer) {
                 for (int i = 0; i < STAGES; ++i)
-                    if (issued & (1u << i)) drain_wait(&s.full[i], (issued_parity >> i) & 1u);
+                    if (issued & (1u << i)) drain_wait(&s.full_w[i], (issued_parity >> i) & 1u);
             }
         } else if (warp == 1) {
             // ---------------------------------------------------------------- MMA issue
@@ -445,7 +605,8 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap map_w13, const __grid_const
                 const uint32_t idesc = idesc_e4m3_f32(128, (g.n + 15) & ~15);
                 for (int kb = 0; kb < g.nkb; ++kb) {
                     const bool got = wait_bounded(&s.acc_empty[acc.stage], acc.phase ^ 1u, abort_flag, p.status, p.wait_limit_ns) &&
-                                     wait_bounded(&s.full[ring.stage], ring.phase, abort_flag, p.status, p.wait_limit_ns);
+                                     wait_bounded(&s.full_w[ring.stage], ring.phase, abort_flag, p.status, p.wait_limit_ns) &&
+                                     wait_bounded(&s.full_t[ring.stage], ring.phase, abort_flag, p.status, p.wait_limit_ns);
                     if (!__all_sync(FULL_MASK, got)) return false;
                     tc_fence_after();
                     if (issuer) {
@@ -476,8 +637,10 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap map_w13, const __grid_const
         } else if (warp == 2) {
             // ---------------------------------------------------------------- tokens
             Ring ring, slot;
-            for_segments<NT>(p, s, [&](int l) {
+            uint32_t issued = 0, issued_parity = 0;
+            const bool ok = for_segments<NT>(p, s, [&](int l) {
                 if (l == 1) return true;
+                if (l == 3 && first_half(p, s.chunks) == s.chunks) return true;
                 const bool got = wait_bounded(&s.go[l == 0 ? 0 : l - 1], 0, abort_flag, p.status, p.wait_limit_ns);
                 fence_proxy_async_all();        // what other CTAs wrote before the barrier is read by TMA
                 return __all_sync(FULL_MASK, got) != 0;
@@ -492,25 +655,36 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap map_w13, const __grid_const
                     if (!__all_sync(FULL_MASK, got)) return false;
                     if (issuer) {
                         uint8_t* dst = smem_t + ring.stage * C::T_BYTES;
-                        mbar_arrive_expect_tx(&s.full[ring.stage], static_cast<uint32_t>(boxes * 16 * BK));
+                        mbar_arrive_expect_tx(&s.full_t[ring.stage], static_cast<uint32_t>(boxes * 16 * BK));
                         for (int b = 0; b < boxes; ++b)
-                            tma_load_2d(map, &s.full[ring.stage], dst + b * 16 * BK, kb * BK, g.off + b * 16);
+                            tma_load_2d(map, &s.full_t[ring.stage], dst + b * 16 * BK, kb * BK, g.off + b * 16);
                         mbar_arrive_expect_tx(&s.scale_full[slot.stage], scale_bytes);
                         bulk_load(s.scales[slot.stage], scales + static_cast<size_t>(kb) * p.rows_cap, scale_bytes, &s.scale_full[slot.stage]);
                     }
+                    issued |= 1u << ring.stage;
+                    issued_parity = (issued_parity & ~(1u << ring.stage)) | (ring.phase << ring.stage);
                     ring.next(STAGES);
                     slot.next(SLOTS);
                     __syncwarp();
                 }
                 return true;
             });
+            // (aborting) copies still in flight land before the shared memory is given up; the scales' are older
+            // or as old as a codes' copy waited for here, and as quick
+            if (!ok && issuer) {
+                for (int i = 0; i < STAGES; ++i)
+                    if (issued & (1u << i)) drain_wait(&s.full_t[i], (issued_parity >> i) & 1u);
+            }
         } else if (warp == 3) {
             // ---------------------------------------------------------------- grid barriers
             if (lane == 0) {
+                unsigned top = ld_acquire(p.barrier) & 0x80000000u;
 #pragma unroll 1
                 for (int b = 0; b < ML_BARRIERS; ++b) {
+                    if (b == 2 && first_half(p, s.chunks) == s.chunks) continue;   // no second half
                     wait_bounded(&s.done[b], 0, abort_flag, p.status, p.wait_limit_ns);
-                    const bool got = grid_barrier(p.barrier, abort_flag, p.status, p.wait_limit_ns);
+                    const bool got = grid_barrier(p.barrier, top, abort_flag, p.status, p.wait_limit_ns);
+                    top ^= 0x80000000u;
                     fence_proxy_async_all();
                     if (got) mbar_arrive(&s.go[b]);
                 }
@@ -518,20 +692,32 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap map_w13, const __grid_const
         }
         __syncwarp();
     } else {
-        // -------------------------------------------------------------------- promotion, units, output
-        regs_inc<EPI_REGS>();
+        // Where a segment's sums lie: the first and the last unit of the CTA's share of a line may be divided
+        // (the unit is the first of every CTA but the one in whose share it starts); whole units take turns.
+        auto slot_at = [&](int c, int which) { return p.parts + static_cast<size_t>(c * ML_SLOTS + which) * (NT * 256); };
+        auto divided_slot = [&](int c, int l, unsigned u0) { return slot_at(c, l * 2 + (u0 < s.share[l][c] ? 0 : 1)); };
+        auto line_done = [&](int b) {
+            // (codes and scales are read by TMA; the grid barrier's arrival releases the CTA's writes)
+            fence_proxy_async_all();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.done[b]);
+        };
         // ---- the tokens' codes and scales, to every row that they are gathered to
         auto quantise = [&](int w, uint2 u) {
             const int t = w / kbs_x, kb = w - t * kbs_x;
             const float a = bf16_lo(u.x), b = bf16_hi(u.x), c = bf16_lo(u.y), d = bf16_hi(u.y);
             const BlockScale sc = block_scale(__reduce_max_sync(FULL_MASK, max(max(abs_bits(a), abs_bits(b)), max(abs_bits(c), abs_bits(d)))));
             const uint32_t code = quantise4(a, b, c, d, sc);
+            uint8_t* dst = p.xg + kb * 128 + lane * 4;
+            for (int j0 = 0; j0 < p.k; j0 += 32) {
+                const uint32_t row = j0 + lane < p.k ? s.row_of[t * p.k + j0 + lane] : NO_ROW;
+                if (row != NO_ROW) p.sx[static_cast<size_t>(kb) * p.rows_cap + (row & 0xffffu)] = sc.s;
+                const int here = min(32, p.k - j0);
 #pragma unroll 4
-            for (int j = 0; j < p.k; ++j) {
-                const uint32_t row = s.row_of[t * p.k + j];
-                if (row == 0xffffu) continue;
-                *reinterpret_cast<uint32_t*>(p.xg + static_cast<size_t>(row) * p.H + kb * 128 + lane * 4) = code;
-                if (lane == 0) p.sx[static_cast<size_t>(kb) * p.rows_cap + row] = sc.s;
+                for (int j = 0; j < here; ++j) {
+                    const uint32_t to = __shfl_sync(FULL_MASK, row, j);
+                    if (to != NO_ROW) *reinterpret_cast<uint32_t*>(dst + static_cast<size_t>(to & 0xffffu) * p.H) = code;
+                }
             }
         };
 #pragma unroll
@@ -539,256 +725,228 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap map_w13, const __grid_const
             if (first_x + i * stride_x < blocks_x) quantise(first_x + i * stride_x, ahead[i]);
         for (int w = first_x + AHEAD * stride_x; w < blocks_x; w += stride_x)
             quantise(w, *reinterpret_cast<const uint2*>(p.x + static_cast<size_t>(w) * 128 + lane * 4));
-        const int tid = static_cast<int>(threadIdx.x) - EPI_WARP0 * 32;   // 0 .. 255
-        const int ew = warp - EPI_WARP0;
-        const int q = warp & 3;                 // TMEM lane quarter
-        const int h = ew >> 2;                  // warpgroup: 8-column groups h, h + 2, ...
-        const int r = q * 32 + lane;            // row of each 128-row tile
-        const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(8 * h);
-        bool ok = true;
-        Ring acc, slot;
-
-        float a0[NG][8], a1[NG][8];
-        auto clear = [&] {
-#pragma unroll
-            for (int i = 0; i < NG; ++i)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) a0[i][j] = a1[i][j] = 0.f;
-        };
-        // Promotion over a segment: sb0 / sb1 the two tiles' weight scales (by K block), 32 of them a load.
-        auto promote = [&](const Seg& g, const float* sb0, const float* sb1) {
-            float b0n = 0.f, b1n = 0.f;
-            for (int kb = g.kb0; kb < g.kb0 + g.nkb; ++kb) {
-                const int k32 = (kb - g.kb0) & 31;
-                if (k32 == 0 && kb + lane < g.kb0 + g.nkb) {
-                    b0n = __ldg(sb0 + kb + lane);
-                    b1n = __ldg(sb1 + kb + lane);
-                }
-                bool got = (static_cast<unsigned>(mbar_try_wait(&s.acc_full[acc.stage], acc.phase)) &
-                            static_cast<unsigned>(mbar_try_wait(&s.scale_full[slot.stage], slot.phase))) != 0u;
-                if (!got)
-                    got = wait_bounded(&s.acc_full[acc.stage], acc.phase, abort_flag, p.status, p.wait_limit_ns) &&
-                          wait_bounded(&s.scale_full[slot.stage], slot.phase, abort_flag, p.status, p.wait_limit_ns);
-                if (!__all_sync(FULL_MASK, got)) { ok = false; break; }
-                tc_fence_after();
-                const uint32_t taddr = lane_addr + static_cast<uint32_t>(acc.stage * 2 * NT);
-                uint32_t p0[NG][8], p1[NG][8];
-#pragma unroll
-                for (int i = 0; i < NG; ++i) {
-                    if ((2 * i + h) * 8 < g.n) {
-                        tmem_ld_x8(taddr + 16 * i, p0[i]);
-                        tmem_ld_x8(taddr + NT + 16 * i, p1[i]);
-                    }
-                }
-                tmem_ld_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&s.acc_empty[acc.stage]);
-                acc.next(NACC);
-                const float b0 = __shfl_sync(FULL_MASK, b0n, k32), b1 = __shfl_sync(FULL_MASK, b1n, k32);
-                const float* sx = s.scales[slot.stage];
-                slot.next(SLOTS);
-#pragma unroll
-                for (int i = 0; i < NG; ++i) {
-                    if ((2 * i + h) * 8 < g.n) {
-                        const float4 u = *reinterpret_cast<const float4*>(sx + (2 * i + h) * 8);
-                        const float4 w = *reinterpret_cast<const float4*>(sx + (2 * i + h) * 8 + 4);
-                        const float v[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            a0[i][j] = fmaf(__uint_as_float(p0[i][j]), v[j] * b0, a0[i][j]);
-                            a1[i][j] = fmaf(__uint_as_float(p1[i][j]), v[j] * b1, a1[i][j]);
-                        }
-                    }
-                }
-            }
-        };
-        // f(column of the chunk, accumulators) for this thread's valid columns
-        auto columns = [&](int n, auto&& f) {
-#pragma unroll
-            for (int i = 0; i < NG; ++i)
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if ((2 * i + h) * 8 + j < n) f((2 * i + h) * 8 + j, a0[i][j], a1[i][j]);
-        };
-        auto part_of = [&](int c, int l, int which) { return p.parts + static_cast<size_t>((c * 2 + l) * 2 + which) * (NT * 256); };
-        auto line_done = [&](int b) {
-            // (codes and scales are read by TMA; the grid barrier's arrival releases the CTA's writes)
-            fence_proxy_async_all();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s.done[b]);
-        };
-        // The sum of a divided unit's parts in the order of its CTAs, if this CTA's came last: every thread's
-        // writes of the part are visible to whoever sees the full count.
-        auto whole = [&](int l, const Line& ln, const Seg& g) {
-            const unsigned u0 = static_cast<unsigned>(g.unit) * ln.kbs;
-            const int c_lo = cta_of(u0, ln.total), c_hi = cta_of(u0 + ln.kbs - 1, ln.total);
-            // the unit is the first of every CTA but the one in whose share it starts
-            float* mine = part_of(cta, l, u0 < s.share[l][cta] ? 0 : 1);
-            columns(g.n, [&](int col, float& x0, float& x1) {
-                __stcg(mine + col * 256 + r, x0);
-                __stcg(mine + col * 256 + 128 + r, x1);
-            });
-            epi_barrier();
-            if (tid == 0) {
-                // (releases what the barrier has gathered from the CTA's threads, acquires the others' parts)
-                unsigned* count = p.count + l * ML_MAX_CTAS + c_lo;
-                const bool last = atom_add_acq_rel(count, 1u) == static_cast<unsigned>(c_hi - c_lo);
-                if (last) *count = 0;           // as the next launch expects it
-                s.last = last ? 1 : 0;
-            }
-            epi_barrier();
-            if (s.last == 0) return false;
-            clear();
-            for (int c = c_lo; c <= c_hi; ++c) {
-                const float* part = part_of(c, l, u0 < s.share[l][c] ? 0 : 1);
-                columns(g.n, [&](int col, float& x0, float& x1) {
-                    x0 += __ldcg(part + col * 256 + r);
-                    x1 += __ldcg(part + col * 256 + 128 + r);
-                });
-            }
-            return true;
-        };
-
         line_done(0);
-        for_segments<NT>(p, s, [&](int l) {
-            if (l == 1 || l == 2) line_done(l);
-            return true;
-        }, [&](auto tag, int l, const Line& ln, const Seg& g) {
-            clear();
-            if constexpr (decltype(tag)::value == 1) {
-                const int blocks = ln.blocks;
-                const float* sb = p.s13 + (static_cast<size_t>(g.e) * 2 * blocks + g.blk) * ln.kbs;
-                if (ok) promote(g, sb, sb + static_cast<size_t>(blocks) * ln.kbs);
-                if (g.nkb < ln.kbs && !whole(l, ln, g)) return true;
-                // hidden activations of 128 rows of I: act(gate) * up, then codes by the largest of the 128
-#pragma unroll
-                for (int i = 0; i < NG; ++i) {
-                    if ((2 * i + h) * 8 < g.n) {
-                        act_values<8>(p.act, a0[i]);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            a0[i][j] *= a1[i][j];
-                            const uint32_t top = __reduce_max_sync(FULL_MASK, abs_bits(a0[i][j]));
-                            if (lane == 0) s.amax[h][q][i * 8 + j] = top;
-                        }
-                    }
+        bool ok = true;
+        if (warp < ML_EPI_WARP0) {
+            // ---------------------------------------------------------------- finishing phase-1 units
+            regs_dec<ML_FIN_REGS>();
+            const int q = warp & 3;
+            Ring part;
+            for_segments<NT>(p, s, [&](int l) {
+                if (l > 0) line_done(l);
+                return l < 2;
+            }, [&](auto, int l, const Line& ln, const Seg& g) {
+                if (ok) {
+                    const bool got = wait_bounded(&s.part_full[part.stage], part.phase, abort_flag, p.status, p.wait_limit_ns);
+                    ok = __all_sync(FULL_MASK, got) != 0;
                 }
-                asm volatile("bar.sync %0, 128;" ::"r"(2 + h) : "memory");
-                if (q == 0) {                   // one lane a column (NT / 2 of them)
-                    const int col = (2 * (lane >> 3) + h) * 8 + (lane & 7);
-                    if (lane < 8 * NG && col < g.n) {
-                        const BlockScale k = block_scale(max(max(s.amax[h][0][lane], s.amax[h][1][lane]), max(s.amax[h][2][lane], s.amax[h][3][lane])));
-                        s.unit_scale[h][0][lane] = k.d;
-                        s.unit_scale[h][1][lane] = k.r;
-                        p.sh[static_cast<size_t>(g.blk) * p.rows_cap + g.off + col] = k.s;
+                const unsigned u0 = static_cast<unsigned>(g.unit) * ln.kbs;
+                const bool divided = g.nkb < ln.kbs;
+                const int c_lo = divided ? cta_of(u0, ln.total) : cta, c_hi = divided ? cta_of(u0 + ln.kbs - 1, ln.total) : cta;
+                bool mine = true;
+                if (divided) {
+                    // the unit is finished by the CTA whose part comes last, adding the parts in order
+                    finishers_barrier();
+                    if (q == 0 && lane == 0) {
+                        // (releases what part_full has gathered from this CTA, acquires the others' parts)
+                        unsigned* count = p.count + l * ML_MAX_CTAS + c_lo;
+                        const bool last = atom_add_acq_rel(count, 1u) == static_cast<unsigned>(c_hi - c_lo);
+                        if (last) *count = 0;   // as the next launch expects it
+                        s.last = last ? 1 : 0;
                     }
+                    finishers_barrier();
+                    mine = s.last != 0;
                 }
-                asm volatile("bar.sync %0, 128;" ::"r"(2 + h) : "memory");
-#pragma unroll
-                for (int i = 0; i < NG; ++i) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int col = (2 * i + h) * 8 + j;
+                if (mine) {
+                    // A warp takes whole columns (tokens), four rows a lane. Eight pairs of loads are in flight: up
+                    // to two parts of four columns, or the first eight parts of one.
+                    const int parts = c_hi - c_lo + 1;
+                    const float* mine_at = p.parts + lane * 4;
+                    auto part_at = [&](int pt) {    // in floats from there
+                        return static_cast<size_t>((divided ? divided_slot(c_lo + pt, l, u0) : slot_at(cta, 4 + part.stage)) - p.parts);
+                    };
+                    auto finish = [&](const float4& gate, const float4& upv, int col) {
+                        float v[4] = {gate.x, gate.y, gate.z, gate.w};
+                        act_values<4>(p.act, v);
+                        v[0] *= upv.x; v[1] *= upv.y; v[2] *= upv.z; v[3] *= upv.w;
+                        const BlockScale k = block_scale(__reduce_max_sync(FULL_MASK, max(max(abs_bits(v[0]), abs_bits(v[1])), max(abs_bits(v[2]), abs_bits(v[3])))));
+                        const uint32_t code = quantise4(v[0], v[1], v[2], v[3], k);
+                        const int row = g.off + col;
                         if (col < g.n) {
-                            const float v = quotient(a0[i][j], s.unit_scale[h][0][i * 8 + j], s.unit_scale[h][1][i * 8 + j]);
-                            p.hg[static_cast<size_t>(g.off + col) * p.I + g.blk * 128 + r] = static_cast<uint8_t>(pack_e4m3x2(v, 0.f) & 0xffu);
+                            *reinterpret_cast<uint32_t*>(p.hg + static_cast<size_t>(row) * p.I + g.blk * 128 + lane * 4) = code;
+                            if (lane == 0) p.sh[static_cast<size_t>(g.blk) * p.rows_cap + row] = k.s;
+                        }
+                    };
+                    // (adding the zeros of parts that do not exist changes no sum)
+                    if (parts <= 2) {
+                        const float* at0 = mine_at + part_at(0);
+                        const float* at1 = parts == 2 ? mine_at + part_at(1) : at0;
+#pragma unroll 1
+                        for (int c0 = q * 4; c0 < g.n; c0 += 16) {
+                            float4 gate[4], upv[4], gate1[4], upv1[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                gate[j] = upv[j] = gate1[j] = upv1[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                                if (c0 + j < g.n) {
+                                    gate[j] = __ldcg(reinterpret_cast<const float4*>(at0 + (c0 + j) * 256));
+                                    upv[j] = __ldcg(reinterpret_cast<const float4*>(at0 + (c0 + j) * 256 + 128));
+                                    if (parts == 2) {
+                                        gate1[j] = __ldcg(reinterpret_cast<const float4*>(at1 + (c0 + j) * 256));
+                                        upv1[j] = __ldcg(reinterpret_cast<const float4*>(at1 + (c0 + j) * 256 + 128));
+                                    }
+                                }
+                            }
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                add4(gate[j], gate1[j]);
+                                add4(upv[j], upv1[j]);
+                                finish(gate[j], upv[j], c0 + j);
+                            }
+                        }
+                    } else {
+#pragma unroll 1
+                        for (int c0 = q; c0 < g.n; c0 += 4) {
+                            float4 gate = make_float4(0.f, 0.f, 0.f, 0.f), upv = gate;
+#pragma unroll 1
+                            for (int p0 = 0; p0 < parts; p0 += 8) {
+                                float4 vg[8], vu[8];
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    vg[i] = vu[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                                    if (p0 + i < parts) {
+                                        const float* src = mine_at + part_at(p0 + i) + c0 * 256;
+                                        vg[i] = __ldcg(reinterpret_cast<const float4*>(src));
+                                        vu[i] = __ldcg(reinterpret_cast<const float4*>(src + 128));
+                                    }
+                                }
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    add4(gate, vg[i]);
+                                    add4(upv, vu[i]);
+                                }
+                            }
+                            finish(gate, upv, c0);
                         }
                     }
                 }
-                // (the next unit's first barrier keeps its scales from these reads)
-            } else {
-                const float* sb = p.s2 + (static_cast<size_t>(g.e) * (p.H / 128) + 2 * g.blk) * ln.kbs;
-                if (ok) promote(g, sb, g.two ? sb + ln.kbs : sb);
-                // the unit's (part of the) products, by gathered row
-                const int parts = most_parts(ln);
-                const int part = g.kb0 == 0 ? 0 : cta - cta_of(static_cast<unsigned>(g.unit) * ln.kbs, ln.total);
-                const Line first = line_of(p, s.chunks, 2);
-                const int base = l == 2 ? 0 : static_cast<int>((s.chunk[first.nc] >> 10) & 0xfffu);
-                const int before = l == 2 ? 0 : base * most_parts(first);
-                const size_t width = static_cast<size_t>(ln.blocks) * 256;
-                float* y = p.y + (static_cast<size_t>(before) + (g.off - base) * parts + part) * width + g.blk * 256 + r;
-                columns(g.n, [&](int col, float& x0, float& x1) {
-                    __stcg(y + static_cast<size_t>(col) * parts * width, x0);
-                    if (g.two) __stcg(y + static_cast<size_t>(col) * parts * width + 128, x1);
-                });
-            }
-            return true;
-        });
-        line_done(3);
-        {
-            const bool got = wait_bounded(&s.go[3], 0, abort_flag, p.status, p.wait_limit_ns);
-            ok = __all_sync(FULL_MASK, got) != 0;
-        }
-        // ---- output: a warp takes 128 columns of a token and adds up its experts in the order of its slots
-        if (ok) {
-            const Line la = line_of(p, s.chunks, 2), lb = line_of(p, s.chunks, 3);
-            const int pa = most_parts(la), pb = most_parts(lb);
-            const int base_b = lb.nc ? static_cast<int>((s.chunk[la.nc] >> 10) & 0xfffu) : s.rows;
-            const int blocks = p.H / 128;
-            const size_t width = static_cast<size_t>(la.blocks) * 256;
-            for (int w = ew * static_cast<int>(gridDim.x) + cta; w < p.T * blocks; w += static_cast<int>(gridDim.x) * 8) {
-                const int t = w / blocks, blk = w - t * blocks;
-                const int col = blk * 128 + lane * 4;
-                const size_t at = static_cast<size_t>(t) * p.H + col;
-                uint2 res = make_uint2(0u, 0u);
-                if (p.residual != nullptr) res = *reinterpret_cast<const uint2*>(p.residual + at);
-                float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int j0 = 0; j0 < p.k; j0 += 32) {
-                    // lane j: where assignment j's sums lie (in rows of `width`), of how many parts, its weight
-                    const int j = j0 + lane;
-                    int first = 0, parts = 0;
-                    float wt = 0.f;
-                    const int row = j < p.k ? s.row_of[t * p.k + j] : 0xffff;
-                    if (row != 0xffff) {
-                        wt = __ldg(p.weights + t * p.k + j);
-                        const bool b = row >= base_b;
-                        const Line& ln = b ? lb : la;
-                        // the row's chunk in its line: the last one that starts at or before it
-                        int lo = ln.c0, hi = ln.c0 + ln.nc;
-                        while (hi - lo > 1) {
-                            const int mid = (lo + hi) >> 1;
-                            if (static_cast<int>((s.chunk[mid] >> 10) & 0xfffu) <= row) lo = mid; else hi = mid;
-                        }
-                        const unsigned u0 = static_cast<unsigned>((blk >> 1) * ln.nc + lo - ln.c0) * ln.kbs;
-                        parts = cta_of(u0 + ln.kbs - 1, ln.total) - cta_of(u0, ln.total) + 1;
-                        first = b ? base_b * pa + (row - base_b) * pb : row * pa;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.part_empty[part.stage]);
+                part.next(ML_PARTS);
+                return true;
+            });
+            sum_output<NT>(p, s, (8 + warp - ML_FIN_WARP0) * static_cast<int>(gridDim.x) + cta, ok, abort_flag, lane);
+        } else {
+            // ---------------------------------------------------------------- promotion
+            regs_inc<ML_EPI_REGS>();
+            const int ew = warp - ML_EPI_WARP0;
+            const int q = warp & 3;             // TMEM lane quarter
+            const int h = ew >> 2;              // warpgroup: 8-column groups h, h + 2, ...
+            const int r = q * 32 + lane;        // row of each 128-row tile
+            const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(8 * h);
+            Ring acc, slot, part;
+
+            float a0[NG][8], a1[NG][8];
+            auto clear = [&] {
+#pragma unroll
+                for (int i = 0; i < NG; ++i)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) a0[i][j] = a1[i][j] = 0.f;
+            };
+            // Promotion over a segment: sb0 / sb1 the two tiles' weight scales (by K block), 32 of them a load.
+            auto promote = [&](const Seg& g, const float* sb0, const float* sb1) {
+                float b0n = 0.f, b1n = 0.f;
+                for (int kb = g.kb0; kb < g.kb0 + g.nkb; ++kb) {
+                    const int k32 = (kb - g.kb0) & 31;
+                    if (k32 == 0 && kb + lane < g.kb0 + g.nkb) {
+                        b0n = __ldg(sb0 + kb + lane);
+                        b1n = __ldg(sb1 + kb + lane);
                     }
-                    const int here = min(32, p.k - j0);
-                    // eight assignments' first two parts are loaded together (a unit has more parts only where
-                    // there are few stages in all)
-                    for (int i0 = 0; i0 < here; i0 += 8) {
-                        float4 v[8][2];
+                    bool got = (static_cast<unsigned>(mbar_try_wait(&s.acc_full[acc.stage], acc.phase)) &
+                                static_cast<unsigned>(mbar_try_wait(&s.scale_full[slot.stage], slot.phase))) != 0u;
+                    if (!got)
+                        got = wait_bounded(&s.acc_full[acc.stage], acc.phase, abort_flag, p.status, p.wait_limit_ns) &&
+                              wait_bounded(&s.scale_full[slot.stage], slot.phase, abort_flag, p.status, p.wait_limit_ns);
+                    if (!__all_sync(FULL_MASK, got)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t taddr = lane_addr + static_cast<uint32_t>(acc.stage * 2 * NT);
+                    uint32_t p0[NG][8], p1[NG][8];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int f = __shfl_sync(FULL_MASK, first, (i0 + i) & 31), held = __shfl_sync(FULL_MASK, parts, (i0 + i) & 31);
-                            const int n = i0 + i < here ? held : 0;
-                            const float* src = p.y + static_cast<size_t>(f) * width + col;
-#pragma unroll
-                            for (int c = 0; c < 2; ++c) {
-                                v[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
-                                if (c < n) v[i][c] = __ldcg(reinterpret_cast<const float4*>(src + c * width));
-                            }
+                    for (int i = 0; i < NG; ++i) {
+                        if ((2 * i + h) * 8 < g.n) {
+                            tmem_ld_x8(taddr + 16 * i, p0[i]);
+                            tmem_ld_x8(taddr + NT + 16 * i, p1[i]);
                         }
+                    }
+                    tmem_ld_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s.acc_empty[acc.stage]);
+                    acc.next(NACC);
+                    const float b0 = __shfl_sync(FULL_MASK, b0n, k32), b1 = __shfl_sync(FULL_MASK, b1n, k32);
+                    const float* sx = s.scales[slot.stage];
+                    slot.next(SLOTS);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int f = __shfl_sync(FULL_MASK, first, (i0 + i) & 31), n = __shfl_sync(FULL_MASK, parts, (i0 + i) & 31);
-                            const float u = __shfl_sync(FULL_MASK, wt, (i0 + i) & 31);
-                            if (i0 + i >= here || n == 0) continue;
-                            float4 d = make_float4(v[i][0].x + v[i][1].x, v[i][0].y + v[i][1].y, v[i][0].z + v[i][1].z, v[i][0].w + v[i][1].w);
-                            const float* src = p.y + static_cast<size_t>(f) * width + col;
-                            for (int c = 2; c < n; ++c) {
-                                const float4 e = __ldcg(reinterpret_cast<const float4*>(src + static_cast<size_t>(c) * width));
-                                d.x += e.x; d.y += e.y; d.z += e.z; d.w += e.w;
+                    for (int i = 0; i < NG; ++i) {
+                        if ((2 * i + h) * 8 < g.n) {
+                            const float4 u = *reinterpret_cast<const float4*>(sx + (2 * i + h) * 8);
+                            const float4 w = *reinterpret_cast<const float4*>(sx + (2 * i + h) * 8 + 4);
+                            const float v[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                a0[i][j] = fmaf(__uint_as_float(p0[i][j]), v[j] * b0, a0[i][j]);
+                                a1[i][j] = fmaf(__uint_as_float(p1[i][j]), v[j] * b1, a1[i][j]);
                             }
-                            sum.x = fmaf(u, d.x, sum.x); sum.y = fmaf(u, d.y, sum.y);
-                            sum.z = fmaf(u, d.z, sum.z); sum.w = fmaf(u, d.w, sum.w);
                         }
                     }
                 }
-                sum.x += bf16_lo(res.x); sum.y += bf16_hi(res.x); sum.z += bf16_lo(res.y); sum.w += bf16_hi(res.y);
-                st_global_v2(p.out + at, pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
-            }
+            };
+            // f(column of the chunk, accumulators) for this thread's valid columns
+            auto columns = [&](int n, auto&& f) {
+#pragma unroll
+                for (int i = 0; i < NG; ++i)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if ((2 * i + h) * 8 + j < n) f((2 * i + h) * 8 + j, a0[i][j], a1[i][j]);
+            };
+
+            for_segments<NT>(p, s, nothing, [&](auto tag, int l, const Line& ln, const Seg& g) {
+                clear();
+                if constexpr (decltype(tag)::value == 1) {
+                    const float* sb = p.s13 + (static_cast<size_t>(g.e) * 2 * ln.blocks + g.blk) * ln.kbs;
+                    if (ok) promote(g, sb, sb + static_cast<size_t>(ln.blocks) * ln.kbs);
+                    if (ok) {
+                        const bool got = wait_bounded(&s.part_empty[part.stage], part.phase ^ 1u, abort_flag, p.status, p.wait_limit_ns);
+                        ok = __all_sync(FULL_MASK, got) != 0;
+                    }
+                    float* dst = g.nkb < ln.kbs ? divided_slot(cta, l, static_cast<unsigned>(g.unit) * ln.kbs) : slot_at(cta, 4 + part.stage);
+                    columns(g.n, [&](int col, float& x0, float& x1) {
+                        __stcg(dst + col * 256 + r, x0);
+                        __stcg(dst + col * 256 + 128 + r, x1);
+                    });
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s.part_full[part.stage]);
+                    part.next(ML_PARTS);
+                } else {
+                    const float* sb = p.s2 + (static_cast<size_t>(g.e) * (p.H / 128) + 2 * g.blk) * ln.kbs;
+                    if (ok) promote(g, sb, g.two ? sb + ln.kbs : sb);
+                    // the unit's (part of the) products, by gathered row
+                    const int parts = most_parts(ln);
+                    const int at = g.kb0 == 0 ? 0 : cta - cta_of(static_cast<unsigned>(g.unit) * ln.kbs, ln.total);
+                    const Line first = line_of(p, s.chunks, 2);
+                    const int base = l == 2 ? 0 : static_cast<int>((s.chunk[first.nc] >> 10) & 0xfffu);
+                    const int before = l == 2 ? 0 : base * most_parts(first);
+                    const size_t width = static_cast<size_t>(ln.blocks) * 256;
+                    float* y = p.y + (static_cast<size_t>(before) + (g.off - base) * parts + at) * width + g.blk * 256 + r;
+                    columns(g.n, [&](int col, float& x0, float& x1) {
+                        __stcg(y + static_cast<size_t>(col) * parts * width, x0);
+                        if (g.two) __stcg(y + static_cast<size_t>(col) * parts * width + 128, x1);
+                    });
+                }
+                return true;
+            });
+            line_done(3);
+
+            sum_output<NT>(p, s, (warp - ML_EPI_WARP0) * static_cast<int>(gridDim.x) + cta, ok, abort_flag, lane);
         }
         __syncwarp();
     }
@@ -823,8 +981,8 @@ int64_t y_rows(int T, int k, int E, int H, int I) {
     const int nt = tokens_per_chunk(T), a = T * k;
     const int64_t cap = rows_cap(T, k, E);
     int64_t most = 0;
-    for (int chunks = 1; chunks <= a; ++chunks) {
-        const int ca = (chunks + 1) / 2, cb = chunks - ca;
+    for (int i = 0; i < 2 * a; ++i) {
+        const int chunks = i / 2 + 1, ca = i % 2 ? chunks : (chunks * 5 + 7) / 8, cb = chunks - ca;
         const int64_t pa = parts_bound(ca, H, I), pb = cb ? parts_bound(cb, H, I) : 1;
         const int64_t ra = std::min<int64_t>(cap, static_cast<int64_t>(ca) * nt), rb = std::min<int64_t>(cap, static_cast<int64_t>(cb) * nt);
         const int64_t rows = pb >= pa ? rb * pb + std::min(ra, cap - rb) * pa : ra * pa + std::min(rb, cap - ra) * pb;
@@ -847,7 +1005,7 @@ Layout layout(int T, int k, int E, int H, int I) {
     l.hg = l.sx + up(rows * (H / 128) * 4);
     l.sh = l.hg + up(rows * I);
     l.parts = l.sh + up(rows * (I / 128) * 4);
-    l.y = l.parts + static_cast<int64_t>(ML_MAX_CTAS) * 4 * tokens_per_chunk(T) * 256 * 4;
+    l.y = l.parts + static_cast<int64_t>(ML_MAX_CTAS) * ML_SLOTS * tokens_per_chunk(T) * 256 * 4;
     l.bytes = l.y + y_rows(T, k, E, H, I) * ((H + 255) / 256) * 256 * 4;
     return l;
 }
@@ -880,7 +1038,7 @@ cudaError_t launch_moe(const CUtensorMap& w13, const CUtensorMap& w2, const CUte
             cudaFuncAttributes fa;
             e = cudaFuncGetAttributes(&fa, kern);
             if (e != cudaSuccess) return e;
-            if (fa.numRegs * THREADS != CTRL_REGS * 128 + EPI_REGS * (THREADS - 128)) return cudaErrorInvalidConfiguration;
+            if (fa.numRegs * ML_THREADS != (ML_CTRL_REGS + ML_FIN_REGS) * 128 + ML_EPI_REGS * 256) return cudaErrorInvalidConfiguration;
             ready[dev] = 1;
         }
     }
@@ -889,7 +1047,7 @@ cudaError_t launch_moe(const CUtensorMap& w13, const CUtensorMap& w2, const CUte
     attr[0].id = cudaLaunchAttributeCooperative;
     attr[0].val.cooperative = 1;
     cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
-    cfg.blockDim = dim3(THREADS, 1, 1);
+    cfg.blockDim = dim3(ML_THREADS, 1, 1);
     cfg.dynamicSmemBytes = C::DYN_SMEM;
     cfg.stream = stream;
     cfg.attrs = attr;
