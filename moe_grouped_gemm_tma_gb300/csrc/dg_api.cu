@@ -257,6 +257,36 @@ int choose_split(const Spec (&cands)[NC], Spec* sp, int64_t row_blocks, int n, i
     return best_split;
 }
 
+// Tile width and split-K of the epilogue mode, by the time that its kernels take: waves of a K block's measured
+// time at that width each (64 columns 0.30 us, 128 0.37, 192 0.47: 0.21 us and 1.37 ns a column), 4 us for the
+// launch and the tile's ends, and for a split, which has to fit in one wave, 4 us more and 20 ns a column for
+// the exchange of the partial sums. It named the fastest of 9 to 12 measured choices for every one of twelve
+// shapes (333 x 2112 x 7168: 192 columns, 4 CTAs a tile, 18.5 us, where 64 columns unsplit take 21.6;
+// 150 x 2048 x 1024: 64 unsplit, 7.0, where 2 CTAs a tile take 8.9).
+int plan_epilogue(Spec* sp, int64_t row_blocks, int n, int kbs, int sms) {
+    int split = 1;
+    int64_t best = INT64_MAX;
+    for (const Spec& c : kEpilogueSpecs1) {
+        const int64_t tiles = row_blocks * cdiv(n, c.bn);
+        for (int s = 1; s <= 4; s *= 2) {
+            if (s > 1 && (tiles * s > sms || kbs < 4 * s)) continue;
+            const int64_t waves = s > 1 ? 1 : (tiles + sms - 1) / sms;
+            const int64_t cost = waves * cdiv(kbs, s) * (210000 + 1370 * c.bn) + 4000000 + (s > 1 ? 4000000 + 20000 * c.bn : 0);   // ps
+            if (cost < best) {
+                best = cost;
+                split = s;
+                *sp = c;
+            }
+        }
+    }
+    if (tune(DG_TUNE_BN) >= 0) {
+        *sp = spec_override(kEpilogueSpecs1, *sp);
+        split = 1;
+    }
+    if (const int s = tune(DG_TUNE_SPLIT); s >= 0) split = (s == 2 || s == 4 || s == 8) && kbs >= s ? s : 1;
+    return split;
+}
+
 // CTA-pair (256-row) tiles halve the per-SM B traffic, but with the promotion epilogue as the limit
 // they currently lose to single-CTA tiles on every measured shape (the cross-SM accumulator handoff
 // lengthens the MMA/promotion loop), so they are opt-in: the DG_TUNE_PAIR knob at 2 (only for more
@@ -484,8 +514,7 @@ static dg_status gemm_impl(const uint8_t* A, const float* sfa, const uint8_t* B,
         if (pair) {
             sp = Spec{256, 2};
         } else {
-            sp = spec_override(kEpilogueSpecs1, choose_spec(kEpilogueSpecs1, cdiv(M, BM), N, dev.sms));
-            split = choose_split(kEpilogueSpecs1, &sp, cdiv(M, BM), N, K / 128, dev.sms);
+            split = plan_epilogue(&sp, cdiv(M, BM), N, K / 128, dev.sms);
         }
     } else if (pair) {
         sp = spec_override(kNormalSpecs2, choose_spec(kNormalSpecs2, cdiv(M, 2 * BM), N, dev.sms));
@@ -509,6 +538,11 @@ static dg_status gemm_impl(const uint8_t* A, const float* sfa, const uint8_t* B,
     if (!a_mn && !b_mn && !pair && M <= 128 && tune(DG_TUNE_BN) < 0) {
         const int col_tiles = cdiv(N, 128);
         decode = M <= 64 && K >= 7168 && col_tiles >= 32 && col_tiles <= 64;
+        // With an epilogue the two were measured over M = 1..64, N = 512..24576, K = 128..7168: up to 32 rows and
+        // one wave of column tiles the decode kernel wins (M = 1: 4.0 against 4.5 us at N = 512, K = 128 up to 16
+        // against 31 at 8192 x 7168; M = 20 ties at K <= 512), with more rows from K = 1024 on and up to 32
+        // column tiles, or 64 for a long K (M = 64, N = 7168, K = 2048: 11.9 against 10.5).
+        if (ep) decode = M <= 64 && (M <= 32 ? col_tiles <= dev.sms : K >= 1024 && col_tiles <= (K >= 7168 ? 64 : 32));
         if (const int v = tune(DG_TUNE_SWAP); v >= 0) decode = (v == 1) && (!ep || M <= 64);
         if (decode) pl = ep ? plan_decode<kEpilogue>(1, M, M, N, kbs, dev.sms) : plan_decode<kNormal>(1, M, M, N, kbs, dev.sms);
     }
@@ -574,6 +608,7 @@ static dg_status gemm_impl(const uint8_t* A, const float* sfa, const uint8_t* B,
         set_epilogue(L.params, *ep);
         if (ep->residual && make_tile_output_map(&L.params.tmap_r, const_cast<void*>(ep->residual), M, N) != DG_OK)
             return DG_CUDA_ERROR;
+        if (ep->z && make_tile_output_map(&L.params.tmap_z, ep->z, M, N) != DG_OK) return DG_CUDA_ERROR;
         return launch_spec<kEpilogue>(sp, L) == cudaSuccess ? DG_OK : DG_CUDA_ERROR;
     }
     return launch_spec<kNormal>(sp, L) == cudaSuccess ? DG_OK : DG_CUDA_ERROR;

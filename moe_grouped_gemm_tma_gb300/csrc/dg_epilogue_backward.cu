@@ -4,11 +4,11 @@
 // along M (the B operand of the weight gradient), and the bias gradient, the sum of dZ's rows in FP32.
 //
 // One pass: a CTA owns a 128 x 128 tile, which is one scaling block in either direction, so dZ is computed
-// once, stays in registers, and is quantised twice. A thread holds 8 x 8 values (8 consecutive rows x 8
+// once, stays in registers, and is quantised twice. A thread holds 4 x 8 values (4 consecutive rows x 8
 // consecutive columns): a half warp reads 256 contiguous bytes of a row, a row's largest magnitude is found
-// over 16 lanes by shuffles, a column's over the tile's 16 row groups through shared memory. The transposed
-// codes go through 16 KB of shared memory, eight rows of one column in one 8-byte chunk, chunks XOR-ed by
-// the column group so that neither side conflicts, and leave as 128-byte rows.
+// over 16 lanes by shuffles, a column's over the tile's 16 warps through shared memory. The transposed codes
+// go through 16 KB of shared memory, four rows of one column in a word, words XOR-ed by the column group so
+// that neither side conflicts, and leave as 128-byte rows.
 //
 // The bias gradient is summed in a fixed order whatever the timing: each tile writes its column sums, and
 // the CTA that finishes a column strip last adds the strip's tiles from the first to the last.
@@ -24,7 +24,8 @@
 namespace dg {
 namespace {
 
-constexpr int EB_THREADS = 256;
+constexpr int EB_THREADS = 512;
+constexpr int EB_WARPS = EB_THREADS / 32;
 constexpr int EB_TILE = 128;
 
 struct EbParams {
@@ -43,90 +44,93 @@ struct EbParams {
 
 template <int ACT>
 __global__ void __launch_bounds__(EB_THREADS, 2) epilogue_backward_kernel(const EbParams p) {
-    __shared__ __align__(16) uint8_t s_codes[EB_TILE * EB_TILE];
-    __shared__ __align__(16) uint32_t s_amax[16][EB_TILE];
-    __shared__ __align__(16) float s_sum[8][EB_TILE];
-    __shared__ float2 s_scale[EB_TILE];
+    __shared__ __align__(16) uint32_t s_codes[EB_TILE * EB_TILE / 4];
+    __shared__ __align__(16) float s_amax[EB_WARPS][EB_TILE];
+    __shared__ __align__(16) float s_sum[EB_WARPS][EB_TILE];
+    __shared__ __align__(16) float s_divisor[EB_TILE], s_reciprocal[EB_TILE];   // (divisors negative)
     __shared__ int s_last;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int half = lane >> 4, l16 = lane & 15;
     const int m0 = static_cast<int>(blockIdx.x) * EB_TILE, n0 = static_cast<int>(blockIdx.y) * EB_TILE;
-    const int r0 = warp * 16 + half * 8;               // first of this thread's 8 rows of the tile
+    const int r0 = warp * 8 + half * 4;                // first of this thread's 4 rows of the tile
     const int c0 = l16 * 8;                            // first of its 8 columns
     const size_t base = static_cast<size_t>(m0 + r0) * p.n + n0 + c0;
-    const int valid = p.m - (m0 + r0);                 // rows of the thread's 8 that exist (may be <= 0)
+    const int valid = p.m - (m0 + r0);                 // rows of the thread's 4 that exist (may be <= 0)
 
-    float dz[8][8];
+    float2 dz[4][4];                                   // [row][pair of columns]
     {
-        uint4 d[8], z[8];
+        uint4 d[4], z[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 4; ++i) {
             d[i] = make_uint4(0, 0, 0, 0);
-            if (ACT != DG_ACT_NONE) z[i] = make_uint4(0, 0, 0, 0);
+            z[i] = make_uint4(0, 0, 0, 0);
             if (i < valid) {
                 d[i] = __ldcs(reinterpret_cast<const uint4*>(p.dd + base + static_cast<size_t>(i) * p.n));
                 if (ACT != DG_ACT_NONE) z[i] = __ldcs(reinterpret_cast<const uint4*>(p.z + base + static_cast<size_t>(i) * p.n));
             }
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 4; ++i) {
             const uint32_t dw[4] = {d[i].x, d[i].y, d[i].z, d[i].w};
             const uint32_t zw[4] = {z[i].x, z[i].y, z[i].z, z[i].w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                dz[i][2 * j] = bf16_lo(dw[j]);
-                dz[i][2 * j + 1] = bf16_hi(dw[j]);
-                if (ACT != DG_ACT_NONE) {
-                    dz[i][2 * j] *= act_slope<ACT>(bf16_lo(zw[j]));
-                    dz[i][2 * j + 1] *= act_slope<ACT>(bf16_hi(zw[j]));
-                    // rows past M stay zero (0 * slope(0) is 0)
-                }
+                dz[i][j] = make_float2(bf16_lo(dw[j]), bf16_hi(dw[j]));
+                // (rows past M stay zero: every slope at 0 is finite)
+                if (ACT != DG_ACT_NONE) dz[i][j] = __fmul2_rn(dz[i][j], act_slope2<ACT>(make_float2(bf16_lo(zw[j]), bf16_hi(zw[j]))));
             }
         }
     }
 
-    // ---- the columns' largest magnitudes and sums over this thread's rows, to shared memory
+    // ---- the columns' largest magnitudes and sums over this warp's rows, to shared memory
     if (p.qt != nullptr) {
-        uint32_t a[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            a[j] = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) a[j] = max(a[j], abs_bits(dz[i][j]));
-        }
-        uint4* dst = reinterpret_cast<uint4*>(&s_amax[warp * 2 + half][c0]);
-        dst[0] = make_uint4(a[0], a[1], a[2], a[3]);
-        dst[1] = make_uint4(a[4], a[5], a[6], a[7]);
-    }
-    if (p.dbias != nullptr) {
         float a[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            a[j] = 0.f;
+        for (int j = 0; j < 4; ++j) {
+            a[2 * j] = abs_max(dz[0][j].x, dz[1][j].x, dz[2][j].x);
+            a[2 * j + 1] = abs_max(dz[0][j].y, dz[1][j].y, dz[2][j].y);
+        }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) a[j] += dz[i][j];
-            a[j] += __shfl_xor_sync(0xffffffffu, a[j], 16);
+        for (int j = 0; j < 8; ++j) {
+            a[j] = abs_max(a[j], j & 1 ? dz[3][j >> 1].y : dz[3][j >> 1].x);
+            a[j] = abs_max(a[j], __shfl_xor_sync(0xffffffffu, a[j], 16));
         }
         if (half == 0) {
-            float4* dst = reinterpret_cast<float4*>(&s_sum[warp][c0]);
+            float4* dst = reinterpret_cast<float4*>(&s_amax[warp][c0]);
             dst[0] = make_float4(a[0], a[1], a[2], a[3]);
             dst[1] = make_float4(a[4], a[5], a[6], a[7]);
         }
     }
+    if (p.dbias != nullptr) {
+        float2 a[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            a[j] = __fadd2_rn(__fadd2_rn(dz[0][j], dz[1][j]), __fadd2_rn(dz[2][j], dz[3][j]));
+            a[j].x += __shfl_xor_sync(0xffffffffu, a[j].x, 16);
+            a[j].y += __shfl_xor_sync(0xffffffffu, a[j].y, 16);
+        }
+        if (half == 0) {
+            float4* dst = reinterpret_cast<float4*>(&s_sum[warp][c0]);
+            dst[0] = make_float4(a[0].x, a[0].y, a[1].x, a[1].y);
+            dst[1] = make_float4(a[2].x, a[2].y, a[3].x, a[3].y);
+        }
+    }
     // ---- codes along the rows
     if (p.q != nullptr) {
+        float a[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            uint32_t a = 0;
+        for (int i = 0; i < 4; ++i)
+            a[i] = abs_max(abs_max(dz[i][0].x, dz[i][0].y, dz[i][1].x), abs_max(dz[i][1].y, dz[i][2].x, dz[i][2].y), abs_max(dz[i][3].x, dz[i][3].y));
 #pragma unroll
-            for (int j = 0; j < 8; ++j) a = max(a, abs_bits(dz[i][j]));
+        for (int o = 8; o > 0; o >>= 1)
 #pragma unroll
-            for (int o = 8; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
-            const BlockScale k = block_scale(a);
+            for (int i = 0; i < 4; ++i) a[i] = abs_max(a[i], __shfl_xor_sync(0xffffffffu, a[i], o));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const BlockScale k = block_scale(abs_bits(a[i]));
+            const uint32_t w0 = quantise4(dz[i][0], dz[i][1], k), w1 = quantise4(dz[i][2], dz[i][3], k);
             if (i < valid) {
-                const uint32_t w0 = quantise4(dz[i][0], dz[i][1], dz[i][2], dz[i][3], k);
-                const uint32_t w1 = quantise4(dz[i][4], dz[i][5], dz[i][6], dz[i][7], k);
                 *reinterpret_cast<uint2*>(p.q + base + static_cast<size_t>(i) * p.n) = make_uint2(w0, w1);
                 if (l16 == 0) p.sf[static_cast<size_t>(m0 + r0 + i) * (p.n / 128) + blockIdx.y] = k.s;
             }
@@ -137,47 +141,56 @@ __global__ void __launch_bounds__(EB_THREADS, 2) epilogue_backward_kernel(const 
 
     const int mt = p.m_tiles;                          // scale blocks along the transpose's rows
     if (threadIdx.x < EB_TILE) {
-        const int c = threadIdx.x;
         if (p.qt != nullptr) {
-            uint32_t a = 0;
+            const int c = threadIdx.x;
+            float a = 0.f;
 #pragma unroll
-            for (int g = 0; g < 16; ++g) a = max(a, s_amax[g][c]);
-            const BlockScale k = block_scale(a);
-            s_scale[c] = make_float2(k.d, k.r);
+            for (int g = 0; g < EB_WARPS; ++g) a = abs_max(a, s_amax[g][c]);
+            const BlockScale k = block_scale(abs_bits(a));
+            s_divisor[c] = -k.d;
+            s_reciprocal[c] = k.r;
             p.sft[static_cast<size_t>(n0 + c) * mt + blockIdx.x] = k.s;
         }
-    } else if (p.dbias != nullptr) {
+    } else if (threadIdx.x < 2 * EB_TILE && p.dbias != nullptr) {
         const int c = threadIdx.x - EB_TILE;
         float a = 0.f;
 #pragma unroll
-        for (int w = 0; w < 8; ++w) a += s_sum[w][c];
+        for (int w = 0; w < EB_WARPS; ++w) a += s_sum[w][c];
         __stcg(p.sums + static_cast<size_t>(blockIdx.x) * p.n + n0 + c, a);
-        __threadfence();                               // the strip's last CTA reads it
     }
     __syncthreads();
     if (p.dbias != nullptr && threadIdx.x == 0) {
+        // (releases the sums, which the barrier has ordered before it, to the strip's last CTA)
         __threadfence();
         s_last = atomicAdd(p.done + blockIdx.y, 1u) == static_cast<unsigned>(mt - 1);
     }
 
-    // ---- codes along the columns: chunk (m / 8) of column n at 8-byte slot (m / 8) ^ (n / 8)
+    // ---- codes along the columns: rows 4w .. 4w + 3 of column n in word w ^ 2 (n / 8) of its 32
     if (p.qt != nullptr) {
+        const int word = (warp * 2 + half) ^ (2 * l16);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const BlockScale k{0.f, s_scale[c0 + j].x, s_scale[c0 + j].y};
-            const uint32_t w0 = quantise4(dz[0][j], dz[1][j], dz[2][j], dz[3][j], k);
-            const uint32_t w1 = quantise4(dz[4][j], dz[5][j], dz[6][j], dz[7][j], k);
-            const int slot = (warp * 2 + half) ^ l16;
-            *reinterpret_cast<uint2*>(s_codes + (c0 + j) * EB_TILE + slot * 8) = make_uint2(w0, w1);
+        for (int j = 0; j < 4; j += 2) {
+            const float4 d = *reinterpret_cast<const float4*>(&s_divisor[c0 + 2 * j]);
+            const float4 r = *reinterpret_cast<const float4*>(&s_reciprocal[c0 + 2 * j]);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const float2 nd = x ? make_float2(d.z, d.w) : make_float2(d.x, d.y), rr = x ? make_float2(r.z, r.w) : make_float2(r.x, r.y);
+                float2 v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = quotient2(dz[i][j + x], nd, rr);
+                uint32_t* dst = s_codes + (c0 + 2 * (j + x)) * 32 + word;
+                dst[0] = pack_e4m3x2(v[0].x, v[1].x) | (pack_e4m3x2(v[2].x, v[3].x) << 16);
+                dst[32] = pack_e4m3x2(v[0].y, v[1].y) | (pack_e4m3x2(v[2].y, v[3].y) << 16);
+            }
         }
     }
     __syncthreads();
     if (p.qt != nullptr) {
         const size_t pitch = static_cast<size_t>(mt) * EB_TILE;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int c = i * 16 + warp * 2 + half;
-            const uint2 w = *reinterpret_cast<const uint2*>(s_codes + c * EB_TILE + ((l16 ^ (c >> 3)) * 8));
+        for (int i = 0; i < 4; ++i) {
+            const int c = i * 32 + warp * 2 + half;
+            const uint2 w = *reinterpret_cast<const uint2*>(s_codes + c * 32 + 2 * (l16 ^ (c >> 3)));
             *reinterpret_cast<uint2*>(p.qt + static_cast<size_t>(n0 + c) * pitch + m0 + l16 * 8) = w;
         }
     }

@@ -115,7 +115,7 @@ struct Params {
 
 // What the epilogue mode takes beside that. Only its kernels have these parameters.
 struct EpilogueParams : Params {
-    CUtensorMap tmap_r;            // the residual in the output's boxes (valid when residual is set)
+    CUtensorMap tmap_r, tmap_z;    // the residual and Z in the output's boxes (valid when they are set)
     const float* bias;             // [n], or null
     const __nv_bfloat16* residual; // [rows][n], or null
     __nv_bfloat16* z;              // [rows][n] pre-activation out, or null
@@ -401,72 +401,81 @@ __device__ __forceinline__ void promote_kg_chunk(float (&accum)[COLS], const uin
     }
 }
 
-// The epilogue of one thread's row of a tile: v (the product, COLS columns from column `col`) becomes
-// act(v + bias) + residual in FP32, and the BF16 pre-activation is written on the way. `boxes` is the warp's
-// staging with the residual in 32-column boxes (64 bytes a row, chunk ^ ((row >> 1) & 3)), or null. Lanes of
-// a warp read the same bias words. A lane writes 32 contiguous bytes of Z a store, a whole sector, where the
-// rows are 32-byte aligned (N % 16 == 0), 16 bytes otherwise.
+// The bias of COLS columns from column `col`, which the running sums start from (0 past the last column).
 template <int COLS>
-__device__ __forceinline__ void epilogue_tile(float (&v)[COLS], const EpilogueParams& p, int row, int col, bool row_valid,
-                                              const uint8_t* boxes, int lane) {
-    const bool wide = (p.n & 15) == 0 && (reinterpret_cast<uintptr_t>(p.z) & 31) == 0;
+__device__ __forceinline__ void load_bias(float (&v)[COLS], const float* bias, int col, int n) {
+    if ((reinterpret_cast<uintptr_t>(bias) & 15) == 0) {
 #pragma unroll
-    for (int r = 0; r < COLS / 32; ++r) {
-        float w[32];
-        if (p.bias != nullptr) {
-#pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-                const int c = col + r * 32 + j;
-                // (p.n is a multiple of 8 and the bias only 4-byte aligned)
-                if (c < p.n) {
-                    w[j] = v[r * 32 + j] + __ldg(p.bias + c);
-                    w[j + 1] = v[r * 32 + j + 1] + __ldg(p.bias + c + 1);
-                    w[j + 2] = v[r * 32 + j + 2] + __ldg(p.bias + c + 2);
-                    w[j + 3] = v[r * 32 + j + 3] + __ldg(p.bias + c + 3);
-                } else {
-                    w[j] = w[j + 1] = w[j + 2] = w[j + 3] = 0.f;
-                }
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) w[j] = v[r * 32 + j];
+        for (int j = 0; j < COLS; j += 4) {
+            float4 b = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (col + j < n) b = __ldg(reinterpret_cast<const float4*>(bias + col + j));
+            v[j] = b.x; v[j + 1] = b.y; v[j + 2] = b.z; v[j + 3] = b.w;
         }
-        if (p.z != nullptr && row_valid) {
-            __nv_bfloat16* zrow = p.z + static_cast<size_t>(row) * p.n + col + r * 32;
+    } else {
 #pragma unroll
-            for (int j = 0; j < 32; j += 16) {
-                uint32_t u[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) u[i] = pack_bf16x2(w[j + 2 * i], w[j + 2 * i + 1]);
-                if (wide) {
-                    if (col + r * 32 + j < p.n) st_global_v8(zrow + j, u);
-                } else {
-                    if (col + r * 32 + j < p.n) st_global_v4(zrow + j, u[0], u[1], u[2], u[3]);
-                    if (col + r * 32 + j + 8 < p.n) st_global_v4(zrow + j + 8, u[4], u[5], u[6], u[7]);
-                }
-            }
-        }
-        act_values<32>(p.act, w);
-        if (boxes != nullptr) {
-            // (boxes that lie past the last column were not copied: whatever is there is not stored either)
-            const uint4* mine = reinterpret_cast<const uint4*>(boxes + r * 2048 + lane * 64);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const uint4 u = mine[c ^ ((lane >> 1) & 3)];
-                const uint32_t x[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    w[c * 8 + 2 * i] += bf16_lo(x[i]);
-                    w[c * 8 + 2 * i + 1] += bf16_hi(x[i]);
-                }
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[r * 32 + j] = w[j];
+        for (int j = 0; j < COLS; ++j) v[j] = col + j < n ? __ldg(bias + col + j) : 0.f;
     }
 }
 
-// The same for four columns of a row held by one thread (`at`: their offset in the [rows][n] matrices).
+// The epilogue of one thread's row of a tile: v (the product with its bias, COLS columns from column `col`)
+// becomes act(v) + residual in FP32. `boxes` is the warp's staging, 32-column boxes (64 bytes a row, 16-byte
+// chunk ^ ((row >> 1) & 3)) of its 32 rows from row `y`: with `residual` they hold the residual, and box by
+// box, once its residual is in registers, they take the BF16 pre-activation, whose TMA store runs beside
+// the arithmetic of the rest of the tile. (Written straight from the registers, Z took 1.4 us a tile of 192
+// columns: the SM's stores go at about 20 bytes a cycle.)
+template <int COLS, int ACT>
+__device__ __forceinline__ void epilogue_tile(float (&v)[COLS], const EpilogueParams& p, int y, int col, bool residual,
+                                              uint8_t* boxes, int lane) {
+#pragma unroll
+    for (int r = 0; r < COLS / 32; ++r) {
+        uint4* mine = reinterpret_cast<uint4*>(boxes + r * 2048 + lane * 64);
+        uint4 res[4];
+        if (residual) {
+            // (boxes past the last column were not copied: whatever is there is not stored either)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) res[c] = mine[c ^ ((lane >> 1) & 3)];
+        }
+        if (p.z != nullptr) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int j = r * 32 + c * 8;
+                mine[c ^ ((lane >> 1) & 3)] = make_uint4(pack_bf16x2(v[j], v[j + 1]), pack_bf16x2(v[j + 2], v[j + 3]),
+                                                         pack_bf16x2(v[j + 4], v[j + 5]), pack_bf16x2(v[j + 6], v[j + 7]));
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            // (only boxes that start inside the tensor are stored)
+            if (lane == 0 && y < p.rows && col + r * 32 < p.n) {
+                tma_store_2d(&p.tmap_z, boxes + r * 2048, col + r * 32, y);
+                bulk_commit();
+            }
+        }
+        if (ACT != DG_ACT_NONE) {
+#pragma unroll
+            for (int j = r * 32; j < r * 32 + 32; j += 2) {
+                const float2 a = act_value2<ACT>(make_float2(v[j], v[j + 1]));
+                v[j] = a.x;
+                v[j + 1] = a.y;
+            }
+        }
+        if (residual) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const uint32_t x[4] = {res[c].x, res[c].y, res[c].z, res[c].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int j = r * 32 + c * 8 + 2 * i;
+                    const float2 s = __fadd2_rn(make_float2(v[j], v[j + 1]), make_float2(bf16_lo(x[i]), bf16_hi(x[i])));
+                    v[j] = s.x;
+                    v[j + 1] = s.y;
+                }
+            }
+        }
+    }
+}
+
+// The same for four columns of a row held by one thread (`at`: their offset in the [rows][n] matrices), the
+// bias included.
 __device__ __forceinline__ void epilogue_four(float (&v)[4], const EpilogueParams& p, int col, size_t at) {
     if (p.bias != nullptr) {
 #pragma unroll
@@ -895,27 +904,39 @@ dg_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant
             const int cstart = ti.n0 + h * COLS;   // first output column of this thread
             const int split = (128 * (cstart / 128 + 1) - cstart) / 16;   // chunks before the next block
 
-            // Epilogue mode: the residual's boxes of this warp's part of the tile are copied into the
-            // warp's output staging while the products run, once the previous tile's stores have read it.
+            // Epilogue mode: the residual's boxes of this warp's part of the tile are copied into the warp's
+            // output staging while the products run, from the middle of the tile on: the previous tile's
+            // stores have read the staging by then, and waiting for them at the tile's start stalls it by as
+            // long as a tile's stores take.
             bool residual_on = false;
             if constexpr (MODE == kEpilogue) {
-                const int y = ti.d_row + q * 32;
-                residual_on = p.residual != nullptr && !split_k && y < p.rows && cstart < p.n;
-                rpending = residual_on;
-                if (residual_on && lane == 0) {
-                    bulk_wait_read_n<0>();
-                    const int boxes = min(COLS / 32, (p.n - cstart + 31) / 32);
-                    mbar_arrive_expect_tx(&residual_bar[ew], static_cast<uint32_t>(boxes) * 2048u);
-                    for (int r = 0; r < boxes; ++r)
-                        tma_load_2d(&p.tmap_r, &residual_bar[ew], s_store + ew * C::STORE_WARP_BYTES + r * 2048, cstart + r * 32, y);
-                }
+                residual_on = p.residual != nullptr && !split_k && ti.d_row + q * 32 < p.rows && cstart < p.n;
+                rpending = false;
             }
+            auto load_residual = [&] {
+                if constexpr (MODE == kEpilogue) {
+                    if (residual_on) {
+                        rpending = true;
+                        if (lane == 0) {
+                            bulk_wait_read_n<0>();
+                            const int boxes = min(COLS / 32, (p.n - cstart + 31) / 32);
+                            mbar_arrive_expect_tx(&residual_bar[ew], static_cast<uint32_t>(boxes) * 2048u);
+                            for (int r = 0; r < boxes; ++r)
+                                tma_load_2d(&p.tmap_r, &residual_bar[ew], s_store + ew * C::STORE_WARP_BYTES + r * 2048, cstart + r * 32, ti.d_row + q * 32);
+                        }
+                    }
+                }
+            };
 
             // the k-grouped output is added into D at the tile's end, so every layout starts the tile's
             // sum at zero
             float accum[COLS];
 #pragma unroll
             for (int j = 0; j < COLS; ++j) accum[j] = 0.f;
+            // (epilogue mode: at the bias, loaded while the tile's first block is on its way; split-K tiles and
+            // narrow tiles, whose sums meet elsewhere, add it at the end)
+            if constexpr (MODE == kEpilogue && !C::KPAR)
+                if (p.bias != nullptr && !split_k) load_bias<COLS>(accum, p.bias, cstart, p.n);
 
             if constexpr (C::DIRECT_SCALES) {
                 // sfa of this thread's row and the sfb of its (at most two) 128-column blocks, read one K
@@ -932,6 +953,7 @@ dg_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant
                 constexpr int H1 = C::EPI_ONE ? CHUNKS : (CHUNKS + 1) / 2;
                 constexpr int H2 = CHUNKS - H1;
                 for (int kb = 0; kb < ti.nkb; ++kb) {
+                    if (MODE == kEpilogue && kb == ti.nkb / 2) load_residual();
                     const float sa = sa_n, b0 = b0_n, b1 = b1_n;
                     if (kb + 1 < ti.nkb) {
                         sa_n = __ldg(sfa_row + kb + 1);
@@ -1066,6 +1088,7 @@ dg_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant
                 for (int j = 0; j < BN; ++j) accf[j] = 0.f;
                 const uint32_t row_addr = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
                 for (int kb = 0; kb < ti.nkb; ++kb) {
+                    if (MODE == kEpilogue && kb == ti.nkb / 2) load_residual();
                     if ((kb & 1) == h) {
                         bool got = (static_cast<unsigned>(mbar_try_wait(&tmem_full_bar[acc], acc_phase)) &
                                     static_cast<unsigned>(mbar_try_wait(&scale_full_bar[slot], sphase))) != 0u;
@@ -1167,11 +1190,28 @@ dg_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant
                     rpending = false;
                 }
                 if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
-                // the staging holds the residual as the output's boxes will: this lane's row is its own
-                // 64 bytes of each box
-                const uint8_t* rbuf = s_store + ew * C::STORE_WARP_BYTES;
-                epilogue_tile<COLS>(accum, p, ti.d_row + row_in_tile, cstart, row_in_tile < ti.rows_valid,
-                                    residual_on ? rbuf : nullptr, lane);
+                if (!residual_on && p.z != nullptr) {
+                    // Z goes into the staging next: the previous tile's stores have read it
+                    if (lane == 0) bulk_wait_read_n<0>();
+                    __syncwarp();
+                }
+                uint8_t* boxes = s_store + ew * C::STORE_WARP_BYTES;
+                const int y = ti.d_row + q * 32;
+                if constexpr (C::KPAR) {
+                    if (p.bias != nullptr) {
+                        float bias[COLS];
+                        load_bias<COLS>(bias, p.bias, cstart, p.n);
+#pragma unroll
+                        for (int j = 0; j < COLS; ++j) accum[j] += bias[j];
+                    }
+                }
+                switch (p.act) {
+                    case DG_ACT_RELU: epilogue_tile<COLS, DG_ACT_RELU>(accum, p, y, cstart, residual_on, boxes, lane); break;
+                    case DG_ACT_GELU: epilogue_tile<COLS, DG_ACT_GELU>(accum, p, y, cstart, residual_on, boxes, lane); break;
+                    case DG_ACT_GELU_TANH: epilogue_tile<COLS, DG_ACT_GELU_TANH>(accum, p, y, cstart, residual_on, boxes, lane); break;
+                    case DG_ACT_SILU: epilogue_tile<COLS, DG_ACT_SILU>(accum, p, y, cstart, residual_on, boxes, lane); break;
+                    default: epilogue_tile<COLS, DG_ACT_NONE>(accum, p, y, cstart, residual_on, boxes, lane); break;
+                }
             }
             // ---- store this CTA's rows of the tile
             if constexpr (MODE == kKGrouped) {

@@ -102,14 +102,29 @@ __device__ __forceinline__ DecTile decode_dec(const Params& p, int t, const int*
     return ti;
 }
 
-// Epilogue mode: one element of D (the unsplit tiles hold a column of it per thread).
-__device__ __forceinline__ void epilogue_one(float& x, const EpilogueParams& p, int col, size_t at) {
-    float v[1] = {x};
-    if (p.bias != nullptr) v[0] += __ldg(p.bias + col);
-    if (p.z != nullptr) p.z[at] = __float2bfloat16_rn(v[0]);
-    act_values<1>(p.act, v);
-    if (p.residual != nullptr) v[0] += __bfloat162float(p.residual[at]);
-    x = v[0];
+// Epilogue mode: one column of D per thread (the unsplit tiles), ROWS rows from element `at` on, `valid` of them
+// stored. The residual is loaded for all rows first.
+template <int ROWS>
+__device__ __forceinline__ void epilogue_column(float (&v)[ROWS], const EpilogueParams& p, int col, size_t at, int valid) {
+    float res[ROWS];
+#pragma unroll
+    for (int m = 0; m < ROWS; ++m)
+        res[m] = p.residual != nullptr && m < valid ? __bfloat162float(p.residual[at + static_cast<size_t>(m) * p.n]) : 0.f;
+    if (p.bias != nullptr) {
+        const float b = __ldg(p.bias + col);
+#pragma unroll
+        for (int m = 0; m < ROWS; ++m) v[m] += b;
+    }
+    if (p.z != nullptr) {
+#pragma unroll
+        for (int m = 0; m < ROWS; ++m)
+            if (m < valid) p.z[at + static_cast<size_t>(m) * p.n] = __float2bfloat16_rn(v[m]);
+    }
+    act_values<ROWS>(p.act, v);
+    if (p.residual != nullptr) {
+#pragma unroll
+        for (int m = 0; m < ROWS; ++m) v[m] += res[m];
+    }
 }
 
 template <int MODE, int BMT>
@@ -418,13 +433,12 @@ dg_decode_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_consta
                     if (n < p.n) {
                         __nv_bfloat16* dcol = reinterpret_cast<__nv_bfloat16*>(p.d) + n;
                         const size_t d_row = static_cast<size_t>(ti.a_row);
+                        if constexpr (MODE == kEpilogue)
+                            epilogue_column<HALF>(acc, p, n, (d_row + h * HALF) * p.n + n, ti.rows_valid - h * HALF);
 #pragma unroll
                         for (int m = 0; m < HALF; ++m) {
                             const int rr = h * HALF + m;
-                            if (rr < ti.rows_valid) {
-                                if constexpr (MODE == kEpilogue) epilogue_one(acc[m], p, n, (d_row + rr) * p.n + n);
-                                dcol[(d_row + rr) * p.n] = __float2bfloat16_rn(acc[m]);
-                            }
+                            if (rr < ti.rows_valid) dcol[(d_row + rr) * p.n] = __float2bfloat16_rn(acc[m]);
                         }
                     }
                 }

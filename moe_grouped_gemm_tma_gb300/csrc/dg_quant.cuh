@@ -34,6 +34,12 @@ __device__ __forceinline__ float quotient(float v, float s, float r) {
     return fmaf(fmaf(-q, s, v), r, q);
 }
 
+// The same for two values in packed arithmetic; `nd` are the divisors' negatives.
+__device__ __forceinline__ float2 quotient2(float2 v, float2 nd, float2 r) {
+    const float2 q = __fmul2_rn(v, r);
+    return __ffma2_rn(__ffma2_rn(q, nd, v), r, q);
+}
+
 // The scale of a block, and what its values are divided by. The largest magnitude comes as the bits of |v|:
 // as unsigned integers these order like the magnitudes, with the infinity above every finite value and NaN
 // above that, so integer maxima carry NaN through (fmaxf would drop it). For a scale that is not finite the
@@ -62,17 +68,47 @@ __device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
 }
 
 // Four values of a block to codes, in order from the lowest byte.
+__device__ __forceinline__ uint32_t quantise4(float2 a, float2 b, const BlockScale& k) {
+    const float2 nd = make_float2(-k.d, -k.d), r = make_float2(k.r, k.r);
+    a = quotient2(a, nd, r);
+    b = quotient2(b, nd, r);
+    return pack_e4m3x2(a.x, a.y) | (pack_e4m3x2(b.x, b.y) << 16);
+}
 __device__ __forceinline__ uint32_t quantise4(float a, float b, float c, float d, const BlockScale& k) {
-    return pack_e4m3x2(quotient(a, k.d, k.r), quotient(b, k.d, k.r)) |
-           (pack_e4m3x2(quotient(c, k.d, k.r), quotient(d, k.d, k.r)) << 16);
+    return quantise4(make_float2(a, b), make_float2(c, d), k);
+}
+
+// The largest of two or three magnitudes; NaN wins. (Of two, the result's sign is of no meaning.)
+__device__ __forceinline__ float abs_max(float a, float b) {
+    float d;
+    asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ float abs_max(float a, float b, float c) {
+    float d;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
 }
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// 1 / (1 + exp(-z)) with the fast exponential and reciprocal: both are good to a few ulp of FP32, and
+__device__ __forceinline__ float exp2_approx(float t) {
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+    return e;
+}
+
+__device__ __forceinline__ float reciprocal_approx(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// 1 / (1 + exp(-z)) with the hardware's base-2 exponential and reciprocal, each good to an ulp or two of FP32;
 // every use ends in BF16 or e4m3. Saturates to 0 and 1 without NaN; NaN stays.
-__device__ __forceinline__ float fast_sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+constexpr float LOG2_E = 1.4426950408889634f;
+__device__ __forceinline__ float fast_sigmoid(float z) { return reciprocal_approx(1.f + exp2_approx(-LOG2_E * z)); }
 
 // sqrt(2 / pi) and the cubic coefficient of the tanh form of GELU, z (1 + tanh(y)) / 2 with
 // y = GELU_A (z + GELU_B z^3); (1 + tanh(y)) / 2 = sigmoid(2 y).
@@ -84,25 +120,78 @@ __device__ __forceinline__ float act_value(float z) {
     if (ACT == DG_ACT_RELU) return z < 0.f ? 0.f : z;                     // NaN stays
     if (ACT == DG_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
     if (ACT == DG_ACT_GELU_TANH) return z * fast_sigmoid(2.f * GELU_A * (z + GELU_B * z * z * z));
-    // (the quotient form keeps what the definition gives at the infinities)
-    if (ACT == DG_ACT_SILU) return __fdividef(z, 1.f + __expf(-z));
+    if (ACT == DG_ACT_SILU) return z * fast_sigmoid(z);
     return z;
 }
 
+// The slopes of an activation at two BF16 pre-activations, in packed arithmetic where it has a form for that.
+//
+// SILU: p (1 + z (1 - p)), p = 1 / (1 + exp(-z)). z has eight significant bits, so its product with the upper
+// 16 bits of log2(e) is exact and the rest goes in as a factor: the exponential's error is that of the base-2
+// one alone. It is held under 2^126 to keep that factor from meeting an infinity.
 template <int ACT>
-__device__ __forceinline__ float act_slope(float z) {
-    if (ACT == DG_ACT_RELU) return z > 0.f ? 1.f : 0.f;
-    if (ACT == DG_ACT_GELU)
-        return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * 0.3989422804014327f * __expf(-0.5f * z * z);
-    if (ACT == DG_ACT_GELU_TANH) {
-        const float p = fast_sigmoid(2.f * GELU_A * (z + GELU_B * z * z * z));
-        return p + 2.f * GELU_A * z * p * (1.f - p) * (1.f + 3.f * GELU_B * z * z);
-    }
+__device__ __forceinline__ float2 act_slope2(float2 z) {
+    const float2 one = make_float2(1.f, 1.f), minus = make_float2(-1.f, -1.f);
     if (ACT == DG_ACT_SILU) {
-        const float p = fast_sigmoid(z);
-        return p * (1.f + z * (1.f - p));
+        constexpr float HI = 1.44268798828125f, LO = 7.0526075e-6f * 0.6931471805599453f;   // log2(e), 16 bits; the rest, times ln 2
+        const float2 t = __fmul2_rn(z, make_float2(-HI, -HI));
+        float2 e = make_float2(exp2_approx(fminf(t.x, 126.f)), exp2_approx(fminf(t.y, 126.f)));
+        e = __ffma2_rn(e, __fmul2_rn(z, make_float2(-LO, -LO)), e);
+        const float2 s = __fadd2_rn(e, one);
+        float2 p = make_float2(reciprocal_approx(s.x), reciprocal_approx(s.y));
+        p = __ffma2_rn(__ffma2_rn(__ffma2_rn(e, minus, minus), p, one), p, p);               // Newton: p + (1 - s p) p
+        return __fmul2_rn(p, __ffma2_rn(z, __ffma2_rn(p, minus, one), one));
     }
-    return 1.f;
+    if (ACT == DG_ACT_GELU_TANH) {
+        // p + z p (1 - p) y', with y = 2 a z (1 + b z^2) and p its sigmoid
+        const float2 z2 = __fmul2_rn(z, z);
+        const float2 y = __fmul2_rn(z, __ffma2_rn(z2, make_float2(2.f * GELU_A * GELU_B, 2.f * GELU_A * GELU_B), make_float2(2.f * GELU_A, 2.f * GELU_A)));
+        const float2 dy = __ffma2_rn(z2, make_float2(6.f * GELU_A * GELU_B, 6.f * GELU_A * GELU_B), make_float2(2.f * GELU_A, 2.f * GELU_A));
+        // the rounding of y log2(e), and what log2(e) has beyond FP32, go in as a factor too
+        constexpr float REST = -1.925963e-8f, LN2 = 0.6931471805599453f;       // log2(e) - float(log2(e))
+        const float2 l = make_float2(-LOG2_E, -LOG2_E), t = __fmul2_rn(y, l);
+        float2 e = make_float2(exp2_approx(fminf(t.x, 126.f)), exp2_approx(fminf(t.y, 126.f)));
+        const float2 low = __ffma2_rn(y, make_float2(-REST, -REST), __ffma2_rn(y, l, __fmul2_rn(t, minus)));
+        e = __ffma2_rn(e, __fmul2_rn(low, make_float2(LN2, LN2)), e);
+        const float2 s = __fadd2_rn(e, one);
+        float2 p = make_float2(reciprocal_approx(s.x), reciprocal_approx(s.y));
+        p = __ffma2_rn(__ffma2_rn(__ffma2_rn(e, minus, minus), p, one), p, p);
+        return __ffma2_rn(__fmul2_rn(p, __ffma2_rn(p, minus, one)), __fmul2_rn(z, dy), p);
+    }
+    if (ACT == DG_ACT_GELU)
+        return make_float2(0.5f * (1.f + erff(z.x * 0.70710678118654752f)) + z.x * 0.3989422804014327f * expf(-0.5f * z.x * z.x),
+                           0.5f * (1.f + erff(z.y * 0.70710678118654752f)) + z.y * 0.3989422804014327f * expf(-0.5f * z.y * z.y));
+    if (ACT == DG_ACT_RELU) return make_float2(z.x > 0.f ? 1.f : 0.f, z.y > 0.f ? 1.f : 0.f);
+    return one;
+}
+
+// max(v, floor), NaN staying NaN
+__device__ __forceinline__ float at_least(float v, float floor) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(v), "f"(floor));
+    return d;
+}
+
+// Two products z sigmoid(y) with one reciprocal: with a = 1 + exp(-y0) and b = 1 + exp(-y1), 1 / a = b / (a b).
+// The special-function unit takes eight cycles a warp for each exponential and reciprocal and is what bounds
+// an epilogue of these, so three per pair instead of four count. The exponentials are held under 2^63 (a NaN
+// counts as that) to keep a b finite, so that neither value of the pair can spoil the other; z is held at the
+// value where its sigmoid is 2^-63, below which the product is under 5e-18.
+__device__ __forceinline__ float2 times_sigmoid2(float2 z, float2 y) {
+    const float2 t = __fmul2_rn(y, make_float2(-LOG2_E, -LOG2_E));
+    const float2 a = __fadd2_rn(make_float2(exp2_approx(fminf(t.x, 63.f)), exp2_approx(fminf(t.y, 63.f))), make_float2(1.f, 1.f));
+    const float r = reciprocal_approx(a.x * a.y);
+    return __fmul2_rn(make_float2(at_least(z.x, -43.668f), at_least(z.y, -43.668f)), make_float2(r * a.y, r * a.x));
+}
+
+template <int ACT>
+__device__ __forceinline__ float2 act_value2(float2 z) {
+    if (ACT == DG_ACT_GELU_TANH) {
+        const float2 c = __ffma2_rn(__fmul2_rn(z, z), make_float2(2.f * GELU_A * GELU_B, 2.f * GELU_A * GELU_B), make_float2(2.f * GELU_A, 2.f * GELU_A));
+        return times_sigmoid2(z, __fmul2_rn(z, c));
+    }
+    if (ACT == DG_ACT_SILU) return times_sigmoid2(z, z);
+    return make_float2(act_value<ACT>(z.x), act_value<ACT>(z.y));
 }
 
 // act over an array in registers, with one branch on the (uniform) choice around the whole loop.

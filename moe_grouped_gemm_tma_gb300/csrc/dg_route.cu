@@ -1,14 +1,19 @@
 // The router around the experts' products: top-k selection with its weights (dg_moe_route) and their
 // gradient (dg_moe_route_backward), one warp a row.
 //
-// Selection. Every value becomes an unsigned key that orders like the float (0 = not selectable), and a
-// lane holds VPL consecutive experts of the row, so that lower lanes hold lower experts. k whole-warp
-// maxima over the lanes' best keys give a bound below which no selected value can lie (k lanes hold one
-// at least as large); the few values at or above it -- k and a handful in practice -- are compacted
+// Selection. A lane holds VPL consecutive experts of the row, so that lower lanes hold lower experts. k
+// whole-warp maxima over the lanes' best values give a bound below which no selected value can lie (k lanes
+// hold one at least as large); the few values at or above it -- k and a handful in practice -- are compacted
 // through shared memory, one a lane, and each counts those that precede it (larger, or equal with a lower
-// expert), which is its place in the order. That is about 200 instructions a row of 256 instead of the
-// 400 of k rounds of find-and-remove; more than 32 candidates (many equal values) take those rounds.
-// What bounds it is instruction issue: a row of 256 BF16 logits is 512 bytes.
+// expert), which is its place in the order. More than 32 candidates (many equal values) take k rounds of
+// find-and-remove instead.
+//
+// With a bias the selection values are sums of a sigmoid, and which of two close ones is larger has to be
+// right: they are defined with an accurate exponential and a rounded reciprocal. Only the candidates pay for
+// that: the bound is found with the hardware's approximations, lowered by more than they can be off.
+//
+// What bounds it is instruction issue: a row of 256 BF16 logits is 512 bytes, or 1.5 instructions' time on
+// the whole GPU, and 250 instructions.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -69,16 +74,10 @@ __device__ __forceinline__ void load_row(const T* row, int E, int lane, bool vec
     for (int i = 0; i < VPL; ++i) v[i] = e0 + i < E ? to_f32(row[e0 + i]) : -INFINITY;
 }
 
-// Order-preserving key of a selection value: 0 for what cannot be selected (-inf, NaN). Adding zero makes
-// -0 the same key as +0.
-__device__ __forceinline__ uint32_t order_key(float v) {
-    const uint32_t b = __float_as_uint(v + 0.f);
-    const uint32_t key = (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-    return v > -INFINITY ? key : 0u;
-}
-
-__device__ __forceinline__ float key_value(uint32_t key) {
-    return __uint_as_float((key & 0x80000000u) ? key & 0x7fffffffu : ~key);
+__device__ __forceinline__ float warp_max(float v) {
+    float d;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(d) : "f"(v));
+    return d;
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -87,8 +86,32 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// exact form (IEEE reciprocal of 1 + exp(-l)): the selection with a bias compares these values
+// the accurate form: the selection with a bias compares these values
 __device__ __forceinline__ float sigmoid(float l) { return __frcp_rn(1.f + expf(-l)); }
+
+// How far a sum of the approximate sigmoid and a bias may be from that of the accurate one: 2^-19 of the
+// sigmoid's range covers the exponential (2 ulp and, for arguments whose sigmoid is not tiny, the rounding of
+// its argument) and the reciprocal ten times over; the sums are rounded to 2^-24 of themselves on either side.
+__device__ __forceinline__ float selection_margin(float sum) { return 1.9073486e-6f + 2.4e-7f * fabsf(sum); }
+
+// The VPL biases of a lane's experts (0 past the row's end).
+template <int VPL>
+__device__ __forceinline__ void load_bias(const float* bias, int E, int lane, bool vec, float (&v)[VPL]) {
+    const int e0 = lane * VPL;
+    if constexpr (VPL >= 4) {
+        if (vec) {
+#pragma unroll
+            for (int c = 0; c < VPL / 4; ++c) {
+                float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (e0 < E) u = __ldg(reinterpret_cast<const float4*>(bias + e0) + c);
+                v[4 * c] = u.x; v[4 * c + 1] = u.y; v[4 * c + 2] = u.z; v[4 * c + 3] = u.w;
+            }
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) v[i] = e0 + i < E ? __ldg(bias + e0 + i) : 0.f;
+}
 
 // +inf counts as the largest finite value, so that no score is a quotient of infinities
 __device__ __forceinline__ float finite_top(float l) { return fminf(l, FLT_MAX); }
@@ -97,49 +120,49 @@ template <int VPL, typename T>
 __global__ void __launch_bounds__(32 * ROUTE_WARPS)
 route_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int32_t* __restrict__ ids,
              float* __restrict__ weights, int rows, int E, int k, int sigmoid_scores, int renorm, float scale, int vec) {
-    __shared__ uint2 s_cand[ROUTE_WARPS][32];
+    __shared__ float2 s_cand[ROUTE_WARPS][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int t = static_cast<int>(blockIdx.x) * ROUTE_WARPS + warp;
     if (t >= rows) return;
     const T* row = logits + static_cast<size_t>(t) * E;
-    float l[VPL];
-    load_row<VPL, T>(row, E, lane, vec != 0, l);
-
-    uint32_t key[VPL];
-    uint32_t head = 0;
+    // selection values: the logits, or the approximate sums; -inf where an expert cannot be selected
+    float v[VPL];
+    load_row<VPL, T>(row, E, lane, (vec & 1) != 0, v);
+    if (bias != nullptr) {
+        float b[VPL];
+        load_bias<VPL>(bias, E, lane, (vec & 2) != 0, b);
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        const int e = lane * VPL + i;
-        float pick = finite_top(l[i]);
-        if (!(l[i] > -INFINITY)) pick = -INFINITY;        // fminf drops NaN
-        if (bias != nullptr && e < E && pick > -INFINITY) pick = sigmoid(pick) + __ldg(bias + e);
-        key[i] = order_key(pick);
-        head = max(head, key[i]);
+        for (int i = 0; i < VPL; ++i) v[i] = v[i] > -INFINITY ? fast_sigmoid(v[i]) + b[i] : -INFINITY;
+    } else {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) v[i] = v[i] > -INFINITY ? finite_top(v[i]) : -INFINITY;   // (NaN too)
     }
+    float head = -INFINITY;                            // (fmaxf drops NaN)
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) head = fmaxf(head, v[i]);
 
-    // softmax: the largest logit (with no bias the keys are the logits)
+    // softmax: the largest logit, and the sum where all scores count
     float top = 0.f, total = 1.f;
     if (!sigmoid_scores) {
-        top = key_value(__reduce_max_sync(FULL, head));
+        top = warp_max(head);
         if (!renorm) {
             float sum = 0.f;
 #pragma unroll
-            for (int i = 0; i < VPL; ++i)
-                if (key[i]) sum += __expf(finite_top(l[i]) - top);
+            for (int i = 0; i < VPL; ++i) sum += v[i] > -INFINITY ? __expf(v[i] - top) : 0.f;
             total = warp_sum(sum);
         }
     }
 
-    // the bound: the k-th whole-warp maximum of the lanes' best keys
-    uint32_t h = head, bound = 1;
+    // the bound: the k-th whole-warp maximum of the lanes' best values
+    float h = head, bound = -INFINITY;
     for (int j = 0; j < k; ++j) {
-        bound = __reduce_max_sync(FULL, h);
-        if (h == bound) h = 0;
+        bound = warp_max(h);
+        if (h == bound) h = -INFINITY;
     }
-    bound = max(bound, 1u);
+    if (bias != nullptr && bound < INFINITY) bound -= 2.f * selection_margin(bound);
     uint32_t mask = 0;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) mask |= (key[i] >= bound ? 1u : 0u) << i;
+    for (int i = 0; i < VPL; ++i) mask |= (v[i] >= bound && v[i] > -INFINITY ? 1u : 0u) << i;
     const int mine = __popc(mask);
     int before = mine;
 #pragma unroll
@@ -151,51 +174,69 @@ route_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int32
     before -= mine;
 
     int place = -1, expert = -1;     // this lane's selected expert, and where it comes in the row
-    int picked = min(found, k);
+    float value = -INFINITY;         // its logit
+    const int picked = min(found, k);
     if (found <= 32) {
+        // candidates in expert order, one a lane
         int at = before;
 #pragma unroll
         for (int i = 0; i < VPL; ++i)
-            if (mask >> i & 1u) s_cand[warp][at++] = make_uint2(key[i], static_cast<uint32_t>(lane * VPL + i));
+            if (mask >> i & 1u) s_cand[warp][at++] = make_float2(v[i], __int_as_float(lane * VPL + i));
         __syncwarp();
+        float me = -INFINITY;
         if (lane < found) {
-            const uint2 me = s_cand[warp][lane];
-            int ahead = 0;
-            // candidates lie in expert order, so among equal keys the earlier ones precede
-            for (int c = 0; c < found; ++c) {
-                const uint32_t other = s_cand[warp][c].x;
-                ahead += (other > me.x || (other == me.x && c < lane)) ? 1 : 0;
-            }
-            if (ahead < k) {
-                place = ahead;
-                expert = static_cast<int>(me.y);
-            }
+            const float2 c = s_cand[warp][lane];
+            me = c.x;
+            expert = __float_as_int(c.y);
+            value = finite_top(to_f32(row[expert]));
+            if (bias != nullptr) me = sigmoid(value) + __ldg(bias + expert);
         }
+        // among equal values the lower expert precedes
+        int ahead = 0;
+#pragma unroll 4
+        for (int c = 0; c < found; ++c) {
+            const float other = __shfl_sync(FULL, me, c);
+            ahead += (other > me || (other == me && c < lane)) ? 1 : 0;
+        }
+        if (lane < found && ahead < k) place = ahead;
+        else expert = -1;
     } else {
         // many equal values: k rounds of find-and-remove
+        if (bias != nullptr) {
+#pragma unroll 1
+            for (int i = 0; i < VPL; ++i) {
+                const int e = lane * VPL + i;
+                float exact = -INFINITY;
+                if (e < E) {
+                    const float l = to_f32(row[e]);
+                    if (l > -INFINITY) exact = sigmoid(finite_top(l)) + __ldg(bias + e);
+                }
+#pragma unroll
+                for (int x = 0; x < VPL; ++x)
+                    if (x == i) v[x] = exact;
+            }
+        }
         for (int j = 0; j < k; ++j) {
-            uint32_t best = 0;
+            float best = -INFINITY;
             int bi = 0;
 #pragma unroll
             for (int i = 0; i < VPL; ++i)
-                if (key[i] > best) { best = key[i]; bi = i; }
-            const uint32_t most = __reduce_max_sync(FULL, best);
+                if (v[i] > best) { best = v[i]; bi = i; }
+            const float most = warp_max(best);
             const int owner = __ffs(__ballot_sync(FULL, best == most)) - 1;
             const int e = __shfl_sync(FULL, lane * VPL + bi, owner);
             if (lane == owner) {
 #pragma unroll
                 for (int i = 0; i < VPL; ++i)
-                    if (i == bi) key[i] = 0;
+                    if (i == bi) v[i] = -INFINITY;
             }
             if (lane == j) { place = j; expert = e; }
         }
+        if (place >= 0) value = finite_top(to_f32(row[expert]));
     }
 
     float score = 0.f;
-    if (place >= 0) {
-        const float v = finite_top(to_f32(row[expert]));
-        score = sigmoid_scores ? sigmoid(v) : __expf(v - top);
-    }
+    if (place >= 0) score = sigmoid_scores ? sigmoid(value) : __expf(value - top);
     if (renorm) total = warp_sum(score);
     const float w = total > 0.f ? __fdiv_rn(score, total) : 0.f;
     const size_t out = static_cast<size_t>(t) * k;
@@ -345,7 +386,8 @@ cudaError_t launch_route(const void* logits, const float* bias, int32_t* ids, fl
                          int scoring, int renorm, float scale, cudaStream_t stream) {
     const int grid = cdiv(rows, ROUTE_WARPS);
     route_kernel<VPL, T><<<grid, 32 * ROUTE_WARPS, 0, stream>>>(static_cast<const T*>(logits), bias, ids, weights, rows, E, k,
-                                                               scoring, renorm, scale, vector_rows<VPL, T>(logits, logits, E));
+                                                               scoring, renorm, scale,
+                                                               (vector_rows<VPL, T>(logits, logits, E) ? 1 : 0) | (E % VPL == 0 && aligned(bias, 16) ? 2 : 0));
     return cudaGetLastError();
 }
 
