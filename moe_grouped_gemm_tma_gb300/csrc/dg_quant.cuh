@@ -124,16 +124,31 @@ __device__ __forceinline__ float act_value(float z) {
     return z;
 }
 
+// max(v, floor), NaN staying NaN
+__device__ __forceinline__ float at_least(float v, float floor) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(v), "f"(floor));
+    return d;
+}
+
+// ... and min(v, ceiling)
+__device__ __forceinline__ float at_most(float v, float ceiling) {
+    float d;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(v), "f"(ceiling));
+    return d;
+}
+
 // The slopes of an activation at two BF16 pre-activations, in packed arithmetic where it has a form for that.
 //
 // SILU: p (1 + z (1 - p)), p = 1 / (1 + exp(-z)). z has eight significant bits, so its product with the upper
 // 16 bits of log2(e) is exact and the rest goes in as a factor: the exponential's error is that of the base-2
-// one alone. It is held under 2^126 to keep that factor from meeting an infinity.
+// one alone. It is held under 2^126 to keep everything finite.
 template <int ACT>
 __device__ __forceinline__ float2 act_slope2(float2 z) {
     const float2 one = make_float2(1.f, 1.f), minus = make_float2(-1.f, -1.f);
     if (ACT == DG_ACT_SILU) {
         constexpr float HI = 1.44268798828125f, LO = 7.0526075e-6f * 0.6931471805599453f;   // log2(e), 16 bits; the rest, times ln 2
+        z = make_float2(at_least(z.x, -100.f), at_least(z.y, -100.f));       // (0 to FP32 below)
         const float2 t = __fmul2_rn(z, make_float2(-HI, -HI));
         float2 e = make_float2(exp2_approx(fminf(t.x, 126.f)), exp2_approx(fminf(t.y, 126.f)));
         e = __ffma2_rn(e, __fmul2_rn(z, make_float2(-LO, -LO)), e);
@@ -143,12 +158,13 @@ __device__ __forceinline__ float2 act_slope2(float2 z) {
         return __fmul2_rn(p, __ffma2_rn(z, __ffma2_rn(p, minus, one), one));
     }
     if (ACT == DG_ACT_GELU_TANH) {
-        // p + z p (1 - p) y', with y = 2 a z (1 + b z^2) and p its sigmoid
+        // p + z p (1 - p) y', with y = 2 a z (1 + b z^2) and p its sigmoid; beyond 16 that is 0 or 1 to FP32
+        z = make_float2(at_most(at_least(z.x, -16.f), 16.f), at_most(at_least(z.y, -16.f), 16.f));
         const float2 z2 = __fmul2_rn(z, z);
         const float2 y = __fmul2_rn(z, __ffma2_rn(z2, make_float2(2.f * GELU_A * GELU_B, 2.f * GELU_A * GELU_B), make_float2(2.f * GELU_A, 2.f * GELU_A)));
         const float2 dy = __ffma2_rn(z2, make_float2(6.f * GELU_A * GELU_B, 6.f * GELU_A * GELU_B), make_float2(2.f * GELU_A, 2.f * GELU_A));
         // the rounding of y log2(e), and what log2(e) has beyond FP32, go in as a factor too
-        constexpr float REST = -1.925963e-8f, LN2 = 0.6931471805599453f;       // log2(e) - float(log2(e))
+        constexpr float REST = 1.925963e-8f, LN2 = 0.6931471805599453f;       // log2(e) - float(log2(e))
         const float2 l = make_float2(-LOG2_E, -LOG2_E), t = __fmul2_rn(y, l);
         float2 e = make_float2(exp2_approx(fminf(t.x, 126.f)), exp2_approx(fminf(t.y, 126.f)));
         const float2 low = __ffma2_rn(y, make_float2(-REST, -REST), __ffma2_rn(y, l, __fmul2_rn(t, minus)));
@@ -163,13 +179,6 @@ __device__ __forceinline__ float2 act_slope2(float2 z) {
                            0.5f * (1.f + erff(z.y * 0.70710678118654752f)) + z.y * 0.3989422804014327f * expf(-0.5f * z.y * z.y));
     if (ACT == DG_ACT_RELU) return make_float2(z.x > 0.f ? 1.f : 0.f, z.y > 0.f ? 1.f : 0.f);
     return one;
-}
-
-// max(v, floor), NaN staying NaN
-__device__ __forceinline__ float at_least(float v, float floor) {
-    float d;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(v), "f"(floor));
-    return d;
 }
 
 // Two products z sigmoid(y) with one reciprocal: with a = 1 + exp(-y0) and b = 1 + exp(-y1), 1 / a = b / (a b).

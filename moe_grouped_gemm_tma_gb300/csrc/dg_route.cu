@@ -120,12 +120,16 @@ template <int VPL, typename T>
 __global__ void __launch_bounds__(32 * ROUTE_WARPS)
 route_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int32_t* __restrict__ ids,
              float* __restrict__ weights, int rows, int E, int k, int sigmoid_scores, int renorm, float scale, int vec) {
-    __shared__ float2 s_cand[ROUTE_WARPS][32];
+    __shared__ __align__(16) float s_value[ROUTE_WARPS][32];
+    __shared__ int s_cand[ROUTE_WARPS][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // (One row a warp: persistent warps with the next row and the bias in registers take 61 registers and were
+    // slower at every grid size, 18.8 to 24 us against 14 to 16: the chain of exchanges within a row is hidden by other
+    // warps, which need the registers.)
     const int t = static_cast<int>(blockIdx.x) * ROUTE_WARPS + warp;
     if (t >= rows) return;
     const T* row = logits + static_cast<size_t>(t) * E;
-    // selection values: the logits, or the approximate sums; -inf where an expert cannot be selected
+    // selection values: the logits, or the approximate sums; -inf where an expert cannot be selected (NaN too)
     float v[VPL];
     load_row<VPL, T>(row, E, lane, (vec & 1) != 0, v);
     if (bias != nullptr) {
@@ -135,9 +139,9 @@ route_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int32
         for (int i = 0; i < VPL; ++i) v[i] = v[i] > -INFINITY ? fast_sigmoid(v[i]) + b[i] : -INFINITY;
     } else {
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) v[i] = v[i] > -INFINITY ? finite_top(v[i]) : -INFINITY;   // (NaN too)
+        for (int i = 0; i < VPL; ++i) v[i] = v[i] > -INFINITY ? finite_top(v[i]) : -INFINITY;
     }
-    float head = -INFINITY;                            // (fmaxf drops NaN)
+    float head = -INFINITY;                        // (fmaxf drops NaN)
 #pragma unroll
     for (int i = 0; i < VPL; ++i) head = fmaxf(head, v[i]);
 
@@ -160,9 +164,11 @@ route_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int32
         if (h == bound) h = -INFINITY;
     }
     if (bias != nullptr && bound < INFINITY) bound -= 2.f * selection_margin(bound);
+    bound = fmaxf(bound, -FLT_MAX);                // -inf is never a candidate
     uint32_t mask = 0;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) mask |= (v[i] >= bound && v[i] > -INFINITY ? 1u : 0u) << i;
+    for (int i = 0; i < VPL; ++i)
+        if (v[i] >= bound) mask |= 1u << i;
     const int mine = __popc(mask);
     int before = mine;
 #pragma unroll
@@ -177,26 +183,32 @@ route_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int32
     float value = -INFINITY;         // its logit
     const int picked = min(found, k);
     if (found <= 32) {
-        // candidates in expert order, one a lane
+        // candidates in expert order, one a lane, which reads its logit again (it knows where from only now)
         int at = before;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-            if (mask >> i & 1u) s_cand[warp][at++] = make_float2(v[i], __int_as_float(lane * VPL + i));
+        for (uint32_t m = mask; m != 0; m &= m - 1) s_cand[warp][at++] = lane * VPL + __ffs(m) - 1;
         __syncwarp();
         float me = -INFINITY;
         if (lane < found) {
-            const float2 c = s_cand[warp][lane];
-            me = c.x;
-            expert = __float_as_int(c.y);
+            expert = s_cand[warp][lane];
             value = finite_top(to_f32(row[expert]));
-            if (bias != nullptr) me = sigmoid(value) + __ldg(bias + expert);
+            me = bias != nullptr ? sigmoid(value) + __ldg(bias + expert) : value;
         }
-        // among equal values the lower expert precedes
-        int ahead = 0;
-#pragma unroll 4
-        for (int c = 0; c < found; ++c) {
-            const float other = __shfl_sync(FULL, me, c);
-            ahead += (other > me || (other == me && c < lane)) ? 1 : 0;
+        s_value[warp][lane] = me;
+        __syncwarp();
+        // candidates that are at least as large, four a turn; without equal values the lanes' counts are
+        // 1 .. found, and where they are not, equal ones are counted by their order
+        int ahead = -1;
+        for (int c = 0; c < found; c += 4) {
+            const float4 o = *reinterpret_cast<const float4*>(&s_value[warp][c]);
+            ahead += (o.x >= me ? 1 : 0) + (o.y >= me ? 1 : 0) + (o.z >= me ? 1 : 0) + (o.w >= me ? 1 : 0);
+        }
+        const unsigned counts = __reduce_or_sync(FULL, lane < found ? 1u << ahead : 0u);
+        if (__popc(counts) != found) {
+            ahead = 0;
+            for (int c = 0; c < found; ++c) {
+                const float other = __shfl_sync(FULL, me, c);
+                if (c < lane ? other >= me : other > me) ++ahead;
+            }
         }
         if (lane < found && ahead < k) place = ahead;
         else expert = -1;
@@ -238,7 +250,7 @@ route_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int32
     float score = 0.f;
     if (place >= 0) score = sigmoid_scores ? sigmoid(value) : __expf(value - top);
     if (renorm) total = warp_sum(score);
-    const float w = total > 0.f ? __fdiv_rn(score, total) : 0.f;
+    const float w = total > 0.f ? score * __frcp_rn(total) : 0.f;
     const size_t out = static_cast<size_t>(t) * k;
     if (place >= 0) {
         ids[out + place] = expert;

@@ -300,3 +300,31 @@ def test_training_step_of_a_layer_closes():
     dg.dg_wgrad_fp8_nt(out["qt"].cuda(), out["sft"].cuda(), xt["qt"].cuda(), xt["sft"].cuda(), dW, accumulate=False)
     want = R.row_values(out["qt"], out["sft"]) @ R.row_values(xt["qt"], xt["sft"]).T
     assert np.abs(dW.double().cpu().numpy() - want).max() <= 1e-4 * math.sqrt(np.mean(want ** 2))
+
+
+@pytest.mark.parametrize("act", ["relu", "gelu", "gelu_tanh", "silu"])
+def test_backward_at_large_pre_activations(act):
+    # the slope is 0 or 1 to FP32 there, and finite
+    z = torch.tensor([50.0, 1e2, 1e4, 1e8, 1e15], dtype=torch.bfloat16)
+    Z = torch.cat([z, -z, torch.zeros(118, dtype=torch.bfloat16)]).expand(2, 128).contiguous()
+    dD = torch.ones(2, 128, dtype=torch.bfloat16)
+    got = run_backward(dD, Z, act, ("dbias",))["dbias"]
+    assert (got[:5] == 2).all() and (got[5:10].abs() <= 1e-12).all()
+
+
+@pytest.mark.parametrize("act", ["gelu_tanh", "silu"])
+def test_special_values_do_not_touch_their_neighbours(act):
+    # two columns share a reciprocal: every special value beside every other
+    special = [math.nan, math.inf, -math.inf, 3e38, -3e38, -90.0, 90.0, 0.0, 1.0]
+    pairs = [(a, b) for a in special for b in special]
+    N = 2 * len(pairs) + (-2 * len(pairs)) % 8
+    bias = torch.zeros(N)
+    bias[:2 * len(pairs)] = torch.tensor(pairs).flatten()
+    D = sentinel_bf16(300, N)
+    z8 = torch.zeros(300, 128, dtype=torch.uint8), torch.zeros(N, 128, dtype=torch.uint8)
+    dg.dg_gemm_fp8_nt_epilogue(dev(z8[0]), dev(torch.ones(300, 1)), dev(z8[1]), dev(torch.ones((N + 127) // 128, 1)), D, bias=dev(bias), act=act)
+    got = D[0].double().cpu().numpy()
+    x = bias.double().numpy()
+    finite = np.isfinite(x)
+    np.testing.assert_allclose(got[finite], R.act(x[finite], act), rtol=2.0 ** -8, atol=1e-6)
+    assert np.isnan(got[np.isnan(x)]).all() and (got[x == np.inf] == np.inf).all()
