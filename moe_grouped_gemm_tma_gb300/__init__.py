@@ -321,15 +321,19 @@ def _choice(table, name, what):
     return table[name]
 
 
-def _typed(t, name, dtype, shape):
-    """A contiguous CUDA tensor of this type and shape; None stays None."""
-    if t is None:
-        return None
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    return _dense(t, name)
+def _refuse(**args):
+    """The checks that a call's arguments have not passed, one by one, so that the first that fails says what is
+    wrong: name=(tensor or None, dtypes, shape or None)."""
+    for name, (t, dtypes, shape) in args.items():
+        if t is None:
+            continue
+        if t.dtype not in dtypes:
+            if _torch().uint8 in dtypes and len(dtypes) == 2:
+                _codes(t, name)
+            raise TypeError(f"{name} must be {' or '.join(str(d).replace('torch.', '') for d in dtypes)}, got {t.dtype}")
+        if shape is not None and t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)} (shape mismatch)")
+        _dense(t, name)
 
 
 def _bytes(t, name):
@@ -342,25 +346,35 @@ def _bytes(t, name):
     return _ptr(_dense(t, name)), t.numel()
 
 
+# The five functions below check what the others do, but in one expression: a decode step makes these calls for
+# a few microseconds of GPU work each, and a helper's call per argument adds up to as much. Only arguments that
+# do not pass are looked at one by one.
+def _good(t, dtype, shape):
+    return t is None or (t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous())
+
+
 def dg_gemm_fp8_nt_epilogue(A, sfa, B, sfb, D, bias=None, act="none", residual=None, Z=None, stream=None):
     """D = act(A . B^T + bias) + residual (bf16); A, sfa, B, sfb as dg_gemm_fp8_nt, bias fp32 [N], residual bf16
     [M,N] (may be D), Z bf16 [M,N] receives the pre-activation."""
-    torch = _torch()
-    A, B = _codes(A, "A"), _codes(B, "B")
-    sfa, sfb = _f32(sfa, "sfa"), _f32(sfb, "sfb")
+    torch = _torch_module or _torch()
+    bf16, f32, e4m3 = torch.bfloat16, torch.float32, (torch.float8_e4m3fn, torch.uint8)
     M, K = A.shape
     N = B.shape[0]
-    D = _typed(D, "D", torch.bfloat16, (M, N))
-    if B.shape[1] != K:
-        raise ValueError(f"shape mismatch: A {tuple(A.shape)} B {tuple(B.shape)}")
-    if (sfa.shape, sfb.shape) != scale_shapes(M, N, K):
-        raise ValueError(f"scale shapes {tuple(sfa.shape)}, {tuple(sfb.shape)} != {scale_shapes(M, N, K)}")
-    bias = _typed(bias, "bias", torch.float32, (N,))
-    residual = _typed(residual, "residual", torch.bfloat16, (M, N))
-    Z = _typed(Z, "Z", torch.bfloat16, (M, N))
-    st = load().dg_gemm_fp8_nt_epilogue(_ptr(A), _ptr(sfa), _ptr(B), _ptr(sfb), _ptr(D), _ptr(bias),
-                                        _choice(ACTIVATIONS, act, "act"), _ptr(residual), _ptr(Z), M, N, K, _stream(stream))
-    _check(st, "dg_gemm_fp8_nt_epilogue")
+    MN = (M, N)
+    if not (A.dtype in e4m3 and B.dtype in e4m3 and sfa.dtype is f32 and sfb.dtype is f32 and D.dtype is bf16
+            and B.shape[1] == K and sfa.shape == (M, K // 128) and sfb.shape == ((N + 127) // 128, K // 128) and D.shape == MN
+            and A.is_cuda and A.is_contiguous() and B.is_cuda and B.is_contiguous() and sfa.is_cuda and sfa.is_contiguous()
+            and sfb.is_cuda and sfb.is_contiguous() and D.is_cuda and D.is_contiguous()
+            and (bias is None or _good(bias, f32, (N,))) and (residual is None or _good(residual, bf16, MN))
+            and (Z is None or _good(Z, bf16, MN))):
+        _refuse(A=(A, e4m3, None), B=(B, e4m3, (N, K)), sfa=(sfa, (f32,), (M, K // 128)), sfb=(sfb, (f32,), ((N + 127) // 128, K // 128)),
+                D=(D, (bf16,), MN), bias=(bias, (f32,), (N,)), residual=(residual, (bf16,), MN), Z=(Z, (bf16,), MN))
+    st = (_lib or load()).dg_gemm_fp8_nt_epilogue(
+        A.data_ptr(), sfa.data_ptr(), B.data_ptr(), sfb.data_ptr(), D.data_ptr(), None if bias is None else bias.data_ptr(),
+        _choice(ACTIVATIONS, act, "act"), None if residual is None else residual.data_ptr(), None if Z is None else Z.data_ptr(),
+        M, N, K, _stream(stream))
+    if st:
+        raise DGError(st, "dg_gemm_fp8_nt_epilogue")
     return D
 
 
@@ -375,63 +389,67 @@ def dg_epilogue_backward(dD, Z, q, sf, qt, sft, dbias, workspace=None, act="none
     transpose qt [N,Mp] with scales sft [N,Mp/128] (Mp = M rounded up to 128), and dbias fp32 [N], the sum of
     its rows. q with sf, qt with sft, and dbias may be None; dbias needs a workspace
     (epilogue_backward_workspace). Z is not read for act "none"."""
-    torch = _torch()
+    torch = _torch_module or _torch()
+    bf16, f32, e4m3 = torch.bfloat16, torch.float32, (torch.float8_e4m3fn, torch.uint8)
     M, N = dD.shape
     Mp = (M + 127) // 128 * 128
-    dD = _typed(dD, "dD", torch.bfloat16, (M, N))
-    Z = _typed(Z, "Z", torch.bfloat16, (M, N))
-    for name, t, shape in (("q", q, (M, N)), ("qt", qt, (N, Mp))):
-        if t is not None and _codes(t, name).shape != shape:
-            raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    sf = _typed(sf, "sf", torch.float32, (M, N // 128))
-    sft = _typed(sft, "sft", torch.float32, (N, Mp // 128))
-    dbias = _typed(dbias, "dbias", torch.float32, (N,))
+    MN = (M, N)
+    if not (dD.dtype is bf16 and dD.is_cuda and dD.is_contiguous() and (Z is None or _good(Z, bf16, MN))
+            and (q is None or (q.dtype in e4m3 and q.shape == MN and q.is_cuda and q.is_contiguous()))
+            and (qt is None or (qt.dtype in e4m3 and qt.shape == (N, Mp) and qt.is_cuda and qt.is_contiguous()))
+            and (sf is None or _good(sf, f32, (M, N // 128))) and (sft is None or _good(sft, f32, (N, Mp // 128)))
+            and (dbias is None or _good(dbias, f32, (N,)))):
+        _refuse(dD=(dD, (bf16,), None), Z=(Z, (bf16,), MN), q=(q, e4m3, MN), qt=(qt, e4m3, (N, Mp)), sf=(sf, (f32,), (M, N // 128)),
+                sft=(sft, (f32,), (N, Mp // 128)), dbias=(dbias, (f32,), (N,)))
     ws, size = _bytes(workspace, "workspace")
-    st = load().dg_epilogue_backward(_ptr(dD), _ptr(Z), _choice(ACTIVATIONS, act, "act"), _ptr(q), _ptr(sf), _ptr(qt),
-                                     _ptr(sft), _ptr(dbias), ws, size, M, N, _stream(stream))
-    _check(st, "dg_epilogue_backward")
-
-
-def _logits_type(logits):
-    torch = _torch()
-    if logits.dtype == torch.bfloat16:
-        return 0
-    if logits.dtype == torch.float32:
-        return 1
-    raise TypeError(f"logits must be bfloat16 or float32, got {logits.dtype}")
+    st = (_lib or load()).dg_epilogue_backward(
+        dD.data_ptr(), None if Z is None else Z.data_ptr(), _choice(ACTIVATIONS, act, "act"), None if q is None else q.data_ptr(),
+        None if sf is None else sf.data_ptr(), None if qt is None else qt.data_ptr(), None if sft is None else sft.data_ptr(),
+        None if dbias is None else dbias.data_ptr(), ws, size, M, N, _stream(stream))
+    if st:
+        raise DGError(st, "dg_epilogue_backward")
 
 
 def dg_moe_route(logits, ids, weights, bias=None, scoring="softmax", renormalize=True, scale=1.0, stream=None):
     """The router: ids int32 [T,k] and weights fp32 [T,k] of the k largest selection values of each row of
     logits [T,E] (bf16 or fp32; with a bias fp32 [E], sigmoid scoring only, sigmoid(logit) + bias)."""
-    torch = _torch()
+    torch = _torch_module or _torch()
+    f32, bf16 = torch.float32, torch.bfloat16
     T, E = logits.shape
     k = ids.shape[1]
-    kind = _logits_type(logits)
-    logits = _dense(logits, "logits")
-    ids = _typed(ids, "ids", torch.int32, (T, k))
-    weights = _typed(weights, "weights", torch.float32, (T, k))
-    bias = _typed(bias, "bias", torch.float32, (E,))
-    st = load().dg_moe_route(_ptr(logits), kind, _ptr(bias), _ptr(ids), _ptr(weights), T, E, k,
-                             _choice(SCORES, scoring, "scoring"), 1 if renormalize else 0, float(scale), _stream(stream))
-    _check(st, "dg_moe_route")
+    kind = logits.dtype
+    Tk = (T, k)
+    if not ((kind is f32 or kind is bf16) and logits.is_cuda and logits.is_contiguous() and ids.dtype is torch.int32 and ids.shape == Tk
+            and ids.is_cuda and ids.is_contiguous() and weights.dtype is f32 and weights.shape == Tk and weights.is_cuda
+            and weights.is_contiguous() and (bias is None or _good(bias, f32, (E,)))):
+        _refuse(logits=(logits, (bf16, f32), None), ids=(ids, (torch.int32,), Tk), weights=(weights, (f32,), Tk), bias=(bias, (f32,), (E,)))
+    st = (_lib or load()).dg_moe_route(logits.data_ptr(), 1 if kind is f32 else 0, None if bias is None else bias.data_ptr(), ids.data_ptr(),
+                                       weights.data_ptr(), T, E, k, _choice(SCORES, scoring, "scoring"), 1 if renormalize else 0, scale,
+                                       _stream(stream))
+    if st:
+        raise DGError(st, "dg_moe_route")
     return ids, weights
 
 
 def dg_moe_route_backward(logits, ids, dweights, dlogits, scoring="softmax", renormalize=True, scale=1.0, stream=None):
     """dlogits [T,E] (the logits' type) from dweights fp32 [T,k], for the ids that dg_moe_route gave."""
-    torch = _torch()
+    torch = _torch_module or _torch()
+    f32, bf16 = torch.float32, torch.bfloat16
     T, E = logits.shape
     k = ids.shape[1]
-    kind = _logits_type(logits)
-    logits = _dense(logits, "logits")
-    ids = _typed(ids, "ids", torch.int32, (T, k))
-    dweights = _typed(dweights, "dweights", torch.float32, (T, k))
-    dlogits = _typed(dlogits, "dlogits", logits.dtype, (T, E))
-    st = load().dg_moe_route_backward(_ptr(logits), kind, _ptr(ids), _ptr(dweights), _ptr(dlogits), T, E, k,
-                                      _choice(SCORES, scoring, "scoring"), 1 if renormalize else 0, float(scale),
-                                      _stream(stream))
-    _check(st, "dg_moe_route_backward")
+    kind = logits.dtype
+    Tk = (T, k)
+    if not ((kind is f32 or kind is bf16) and logits.is_cuda and logits.is_contiguous() and ids.dtype is torch.int32 and ids.shape == Tk
+            and ids.is_cuda and ids.is_contiguous() and dweights.dtype is f32 and dweights.shape == Tk and dweights.is_cuda
+            and dweights.is_contiguous() and dlogits.dtype is kind and dlogits.shape == (T, E) and dlogits.is_cuda
+            and dlogits.is_contiguous()):
+        _refuse(logits=(logits, (bf16, f32), None), ids=(ids, (torch.int32,), Tk), dweights=(dweights, (f32,), Tk),
+                dlogits=(dlogits, (kind,), (T, E)))
+    st = (_lib or load()).dg_moe_route_backward(logits.data_ptr(), 1 if kind is f32 else 0, ids.data_ptr(), dweights.data_ptr(),
+                                                dlogits.data_ptr(), T, E, k, _choice(SCORES, scoring, "scoring"),
+                                                1 if renormalize else 0, scale, _stream(stream))
+    if st:
+        raise DGError(st, "dg_moe_route_backward")
     return dlogits
 
 
@@ -449,25 +467,30 @@ def dg_moe_layer(x, ids, weights, W13, s13, W2, s2, out, workspace, act="silu", 
     out[t] = residual[t] + sum_j weights[t,j] W2[e] . Q(act(g) * u), (g; u) = W13[e] . Q(x[t]), e = ids[t,j];
     x, out, residual bf16 [T,H], ids int32 [T,k] (outside [0,E): no expert), weights fp32 [T,k], W13 e4m3
     [E,2I,H] (gate rows, then up rows), W2 e4m3 [E,H,I], each with fp32 scales per 128x128 block."""
-    torch = _torch()
-    T, H = x.shape
+    torch = _torch_module or _torch()
+    bf16, f32, e4m3 = torch.bfloat16, torch.float32, (torch.float8_e4m3fn, torch.uint8)
+    TH = T, H = x.shape
     k = ids.shape[1]
-    W13, W2 = _codes(W13, "W13"), _codes(W2, "W2")
     E, I2, _ = W13.shape
     I = I2 // 2
-    x = _typed(x, "x", torch.bfloat16, (T, H))
-    ids = _typed(ids, "ids", torch.int32, (T, k))
-    weights = _typed(weights, "weights", torch.float32, (T, k))
-    if W13.shape != (E, 2 * I, H) or W2.shape != (E, H, I):
-        raise ValueError(f"shape mismatch: x {tuple(x.shape)} W13 {tuple(W13.shape)} W2 {tuple(W2.shape)}")
-    s13 = _typed(s13, "s13", torch.float32, (E, 2 * I // 128, H // 128))
-    s2 = _typed(s2, "s2", torch.float32, (E, H // 128, I // 128))
-    out = _typed(out, "out", torch.bfloat16, (T, H))
-    residual = _typed(residual, "residual", torch.bfloat16, (T, H))
+    Tk = (T, k)
+    if not (W13.dtype in e4m3 and W2.dtype in e4m3 and x.dtype is bf16 and ids.dtype is torch.int32 and weights.dtype is f32
+            and out.dtype is bf16 and s13.dtype is f32 and s2.dtype is f32
+            and W13.shape == (E, 2 * I, H) and W2.shape == (E, H, I) and s13.shape == (E, I2 // 128, H // 128)
+            and s2.shape == (E, H // 128, I // 128) and ids.shape == Tk and weights.shape == Tk and out.shape == TH
+            and x.is_cuda and x.is_contiguous() and ids.is_cuda and ids.is_contiguous() and weights.is_cuda and weights.is_contiguous()
+            and W13.is_cuda and W13.is_contiguous() and W2.is_cuda and W2.is_contiguous() and s13.is_cuda and s13.is_contiguous()
+            and s2.is_cuda and s2.is_contiguous() and out.is_cuda and out.is_contiguous()
+            and (residual is None or _good(residual, bf16, TH))):
+        _refuse(x=(x, (bf16,), None), ids=(ids, (torch.int32,), Tk), weights=(weights, (f32,), Tk), W13=(W13, e4m3, (E, 2 * I, H)),
+                W2=(W2, e4m3, (E, H, I)), s13=(s13, (f32,), (E, I2 // 128, H // 128)), s2=(s2, (f32,), (E, H // 128, I // 128)),
+                out=(out, (bf16,), TH), residual=(residual, (bf16,), TH))
     ws, size = _bytes(workspace, "workspace")
-    st = load().dg_moe_layer(_ptr(x), _ptr(ids), _ptr(weights), _ptr(W13), _ptr(s13), _ptr(W2), _ptr(s2), _ptr(residual),
-                             _ptr(out), ws, size, T, k, E, H, I, _choice(ACTIVATIONS, act, "act"), _stream(stream))
-    _check(st, "dg_moe_layer")
+    st = (_lib or load()).dg_moe_layer(x.data_ptr(), ids.data_ptr(), weights.data_ptr(), W13.data_ptr(), s13.data_ptr(), W2.data_ptr(),
+                                       s2.data_ptr(), None if residual is None else residual.data_ptr(), out.data_ptr(), ws, size,
+                                       T, k, E, H, I, _choice(ACTIVATIONS, act, "act"), _stream(stream))
+    if st:
+        raise DGError(st, "dg_moe_layer")
     return out
 
 
