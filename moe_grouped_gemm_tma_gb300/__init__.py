@@ -8,7 +8,8 @@ kernels. There is no fallback: when the library or a supported GPU is missing, c
 Operation (DeepGEMM pages, "DeepSeek DeepGEMM" usage example and feature list):
 ``D[m,n] = sum_kb sfa[m,kb] * sfb[n//128,kb] * sum_{k in block kb} A[m,k] B[n,k]`` with e4m3 A/B,
 FP32 1x128 (A) and 128x128 (B) block scales, BF16 output; plus the m-grouped contiguous and masked
-layouts and the k-grouped FP32 weight gradient.
+layouts and the k-grouped FP32 weight gradient. Around them: the router, a whole MoE layer for a few
+tokens, and the GEMM with bias, activation and residual in its epilogue, with its backward pass.
 """
 from __future__ import annotations
 
@@ -22,7 +23,8 @@ __all__ = [
     "dg_m_grouped_contiguous", "dg_m_grouped_masked",
     "dg_k_grouped_wgrad", "dg_wgrad_fp8_nt", "dg_gemm_fp8_nt_epilogue", "dg_epilogue_backward",
     "dg_moe_route", "dg_moe_route_backward", "dg_moe_layer",
-    "epilogue_backward_workspace", "moe_layer_workspace", "ACTIVATIONS", "SCORES", "dg_device_status", "dg_status_string", "scale_shapes", "library_path",
+    "epilogue_backward_workspace", "moe_layer_workspace", "ACTIVATIONS", "SCORES",
+    "dg_device_status", "dg_status_string", "scale_shapes", "library_path",
     "TUNE_KNOBS", "dg_tuning_set", "dg_tuning_get", "dg_tuning_reset", "tuning", "dg_testing_arm_wait_timeout",
 ]
 
