@@ -869,13 +869,13 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap map_w13, const __grid_const
                     if (!__all_sync(FULL_MASK, got)) { ok = false; break; }
                     tc_fence_after();
                     const uint32_t taddr = lane_addr + static_cast<uint32_t>(acc.stage * 2 * NT);
+                    // (columns past the chunk's tokens are loaded too, and not used: a branch between the loads and
+                    // their wait would let the compiler move registers that the loads have yet to write)
                     uint32_t p0[NG][8], p1[NG][8];
 #pragma unroll
                     for (int i = 0; i < NG; ++i) {
-                        if ((2 * i + h) * 8 < g.n) {
-                            tmem_ld_x8(taddr + 16 * i, p0[i]);
-                            tmem_ld_x8(taddr + NT + 16 * i, p1[i]);
-                        }
+                        tmem_ld_x8(taddr + 16 * i, p0[i]);
+                        tmem_ld_x8(taddr + NT + 16 * i, p1[i]);
                     }
                     tmem_ld_wait();
                     tc_fence_before();
