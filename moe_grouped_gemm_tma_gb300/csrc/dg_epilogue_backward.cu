@@ -19,6 +19,7 @@
 
 #include "dg.h"
 #include "dg_host.cuh"
+#include "dg_ptx.cuh"
 #include "dg_quant.cuh"
 
 namespace dg {
@@ -50,6 +51,8 @@ __global__ void __launch_bounds__(EB_THREADS, 2) epilogue_backward_kernel(const 
     __shared__ __align__(16) float s_divisor[EB_TILE], s_reciprocal[EB_TILE];   // (divisors negative)
     __shared__ int s_last;
 
+    grid_dependency_wait();
+    grid_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int half = lane >> 4, l16 = lane & 15;
     const int m0 = static_cast<int>(blockIdx.x) * EB_TILE, n0 = static_cast<int>(blockIdx.y) * EB_TILE;
@@ -207,8 +210,8 @@ __global__ void __launch_bounds__(EB_THREADS, 2) epilogue_backward_kernel(const 
 
 template <int ACT>
 cudaError_t launch_eb(const EbParams& p, cudaStream_t stream) {
-    epilogue_backward_kernel<ACT><<<dim3(static_cast<unsigned>(p.m_tiles), static_cast<unsigned>(p.n / EB_TILE)), EB_THREADS, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_overlapped(epilogue_backward_kernel<ACT>, dim3(static_cast<unsigned>(p.m_tiles), static_cast<unsigned>(p.n / EB_TILE)),
+                             dim3(EB_THREADS), stream, p);
 }
 
 // The counters come first, on their own 128-byte lines' worth of space, then the column sums.

@@ -7,6 +7,7 @@
 #include <cstdint>
 
 #include "dg.h"
+#include "dg_tuning.h"
 
 namespace dg {
 
@@ -34,5 +35,24 @@ dg_status make_operand_map(CUtensorMap* m, const void* base, int64_t rows, int64
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 inline int cdiv(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
+
+// Tuning knobs (dg_tuning.h): the knob's value, or DG_TUNE_AUTO (-1) for the automatic choice.
+int tune(int knob);
+
+// A launch that may begin while the previous grid in the stream ends (the kernel waits for it before its first
+// access to global memory), unless the DG_TUNE_PDL knob is 0.
+template <typename... P, typename... A>
+cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, dim3 block, cudaStream_t stream, A&&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = tune(DG_TUNE_PDL) != 0 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
 
 }  // namespace dg

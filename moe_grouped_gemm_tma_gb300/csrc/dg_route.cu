@@ -21,6 +21,7 @@
 
 #include "dg.h"
 #include "dg_host.cuh"
+#include "dg_ptx.cuh"
 #include "dg_quant.cuh"
 
 namespace dg {
@@ -127,6 +128,8 @@ route_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int32
     // slower at every grid size, 18.8 to 24 us against 14 to 16: the chain of exchanges within a row is hidden by other
     // warps, which need the registers.)
     const int t = static_cast<int>(blockIdx.x) * ROUTE_WARPS + warp;
+    grid_dependency_wait();
+    grid_launch_dependents();
     if (t >= rows) return;
     const T* row = logits + static_cast<size_t>(t) * E;
     // selection values: the logits, or the approximate sums; -inf where an expert cannot be selected (NaN too)
@@ -311,6 +314,8 @@ route_backward_kernel(const T* __restrict__ logits, const int32_t* __restrict__ 
                       T* __restrict__ dlogits, int rows, int E, int k, int sigmoid_scores, int renorm, float scale, int vec) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int t = static_cast<int>(blockIdx.x) * ROUTE_WARPS + warp;
+    grid_dependency_wait();
+    grid_launch_dependents();
     if (t >= rows) return;
     const T* row = logits + static_cast<size_t>(t) * E;
     int e = lane < k ? __ldg(ids + static_cast<size_t>(t) * k + lane) : -1;
@@ -396,21 +401,17 @@ bool vector_rows(const void* a, const void* b, int E) {
 template <int VPL, typename T>
 cudaError_t launch_route(const void* logits, const float* bias, int32_t* ids, float* weights, int rows, int E, int k,
                          int scoring, int renorm, float scale, cudaStream_t stream) {
-    const int grid = cdiv(rows, ROUTE_WARPS);
-    route_kernel<VPL, T><<<grid, 32 * ROUTE_WARPS, 0, stream>>>(static_cast<const T*>(logits), bias, ids, weights, rows, E, k,
-                                                               scoring, renorm, scale,
-                                                               (vector_rows<VPL, T>(logits, logits, E) ? 1 : 0) | (E % VPL == 0 && aligned(bias, 16) ? 2 : 0));
-    return cudaGetLastError();
+    return launch_overlapped(route_kernel<VPL, T>, dim3(cdiv(rows, ROUTE_WARPS)), dim3(32 * ROUTE_WARPS), stream,
+                             static_cast<const T*>(logits), bias, ids, weights, rows, E, k, scoring, renorm, scale,
+                             (vector_rows<VPL, T>(logits, logits, E) ? 1 : 0) | (E % VPL == 0 && aligned(bias, 16) ? 2 : 0));
 }
 
 template <int VPL, typename T>
 cudaError_t launch_route_backward(const void* logits, const int32_t* ids, const float* dweights, void* dlogits, int rows,
                                   int E, int k, int scoring, int renorm, float scale, cudaStream_t stream) {
-    const int grid = cdiv(rows, ROUTE_WARPS);
-    route_backward_kernel<VPL, T><<<grid, 32 * ROUTE_WARPS, 0, stream>>>(
-        static_cast<const T*>(logits), ids, dweights, static_cast<T*>(dlogits), rows, E, k, scoring, renorm, scale,
-        vector_rows<VPL, T>(logits, dlogits, E));
-    return cudaGetLastError();
+    return launch_overlapped(route_backward_kernel<VPL, T>, dim3(cdiv(rows, ROUTE_WARPS)), dim3(32 * ROUTE_WARPS), stream,
+                             static_cast<const T*>(logits), ids, dweights, static_cast<T*>(dlogits), rows, E, k, scoring,
+                             renorm, scale, vector_rows<VPL, T>(logits, dlogits, E) ? 1 : 0);
 }
 
 // Arguments that both directions share. `need` collects what must not be null.
