@@ -308,10 +308,24 @@ cudaError_t launch_spec<kNormal>(Spec sp, const Launch& L) {
     return cudaErrorInvalidValue;
 }
 
+template <int ACT>
+cudaError_t launch_epilogue(Spec sp, const Launch& L) {
+    if (sp.bn == 64) return launch<kEpilogue, 64, 1, ACT>(L);
+    if (sp.bn == 128) return launch<kEpilogue, 128, 1, ACT>(L);
+    if (sp.bn == 192) return launch<kEpilogue, 192, 1, ACT>(L);
+    return cudaErrorInvalidValue;
+}
+
 template <>
 cudaError_t launch_spec<kEpilogue>(Spec sp, const Launch& L) {
-    DG_CASE(kEpilogue, 64, 1) DG_CASE(kEpilogue, 128, 1) DG_CASE(kEpilogue, 192, 1) DG_CASE(kEpilogue, 256, 2)
-    return cudaErrorInvalidValue;
+    switch (L.params.act) {
+        case DG_ACT_NONE: return launch_epilogue<DG_ACT_NONE>(sp, L);
+        case DG_ACT_RELU: return launch_epilogue<DG_ACT_RELU>(sp, L);
+        case DG_ACT_GELU: return launch_epilogue<DG_ACT_GELU>(sp, L);
+        case DG_ACT_GELU_TANH: return launch_epilogue<DG_ACT_GELU_TANH>(sp, L);
+        case DG_ACT_SILU: return launch_epilogue<DG_ACT_SILU>(sp, L);
+        default: return cudaErrorInvalidValue;
+    }
 }
 
 template <>
@@ -499,10 +513,11 @@ static dg_status gemm_impl(const uint8_t* A, const float* sfa, const uint8_t* B,
     // Short K (at most four K blocks) on pair tiles that fill every SM: 256-column CTA pairs, in which
     // each SM stages half of B, so less traffic shares an SM's TMA path with the tile's output stores
     // (in-stream, 4096 x 32768 x 512: 102.3 -> 98.2 us; from K = 1536 on, and for narrower pair tiles,
-    // the single-CTA tiles measured as fast or faster).
-    const bool short_k_pair = !a_mn && !b_mn && tune(DG_TUNE_PAIR) < 0 && tune(DG_TUNE_BN) < 0 && K <= 512 && M > 256 &&
+    // the single-CTA tiles measured as fast or faster). With an epilogue their registers spill: 8192 x 4096 x 512
+    // with residual, bias, silu and Z took 60.9 us on them, 59.4 on 192-column tiles.
+    const bool short_k_pair = !ep && !a_mn && !b_mn && tune(DG_TUNE_PAIR) < 0 && tune(DG_TUNE_BN) < 0 && K <= 512 && M > 256 &&
                               static_cast<int64_t>(cdiv(M, 2 * BM)) * cdiv(N, 256) >= dev.sms;
-    const bool pair = !a_mn && !b_mn && (use_pair(M) || short_k_pair);
+    const bool pair = !ep && !a_mn && !b_mn && (use_pair(M) || short_k_pair);
     Spec sp;
     int split = 1;
     if (b_mn) {
@@ -511,11 +526,7 @@ static dg_status gemm_impl(const uint8_t* A, const float* sfa, const uint8_t* B,
     } else if (short_k_pair) {
         sp = Spec{256, 2};
     } else if (ep) {
-        if (pair) {
-            sp = Spec{256, 2};
-        } else {
-            split = plan_epilogue(&sp, cdiv(M, BM), N, K / 128, dev.sms);
-        }
+        split = plan_epilogue(&sp, cdiv(M, BM), N, K / 128, dev.sms);
     } else if (pair) {
         sp = spec_override(kNormalSpecs2, choose_spec(kNormalSpecs2, cdiv(M, 2 * BM), N, dev.sms));
     } else {

@@ -475,14 +475,16 @@ __device__ __forceinline__ void epilogue_tile(float (&v)[COLS], const EpiloguePa
 }
 
 // The same for four columns of a row held by one thread (`at`: their offset in the [rows][n] matrices), the
-// bias included.
+// bias included (ACT -1: the activation is the parameters').
+template <int ACT = -1>
 __device__ __forceinline__ void epilogue_four(float (&v)[4], const EpilogueParams& p, int col, size_t at) {
     if (p.bias != nullptr) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] += __ldg(p.bias + col + i);
     }
     if (p.z != nullptr) st_global_v2(p.z + at, pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-    act_values<4>(p.act, v);
+    if constexpr (ACT < 0) act_values<4>(p.act, v);
+    else act_pairs<ACT>(v);
     if (p.residual != nullptr) {
         const uint2 u = *reinterpret_cast<const uint2*>(p.residual + at);
         v[0] += bf16_lo(u.x);
@@ -492,7 +494,9 @@ __device__ __forceinline__ void epilogue_four(float (&v)[4], const EpilogueParam
     }
 }
 
-template <int MODE, int BN, int PAIR>
+// (ACT: the epilogue mode's activation. Chosen within the kernel it costs 3 us of 92 at 4096 x 7168 x 2048: the
+// code of the five does not stay in the instruction caches beside the K loop.)
+template <int MODE, int BN, int PAIR, int ACT>
 __global__ void __launch_bounds__(Cfg<MODE, BN, PAIR>::THREADS_C, 1)
 dg_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
                const __grid_constant__ CUtensorMap tmap_d, const __grid_constant__ typename ParamsOf<MODE>::type p) {
@@ -1205,13 +1209,7 @@ dg_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant
                         for (int j = 0; j < COLS; ++j) accum[j] += bias[j];
                     }
                 }
-                switch (p.act) {
-                    case DG_ACT_RELU: epilogue_tile<COLS, DG_ACT_RELU>(accum, p, y, cstart, residual_on, boxes, lane); break;
-                    case DG_ACT_GELU: epilogue_tile<COLS, DG_ACT_GELU>(accum, p, y, cstart, residual_on, boxes, lane); break;
-                    case DG_ACT_GELU_TANH: epilogue_tile<COLS, DG_ACT_GELU_TANH>(accum, p, y, cstart, residual_on, boxes, lane); break;
-                    case DG_ACT_SILU: epilogue_tile<COLS, DG_ACT_SILU>(accum, p, y, cstart, residual_on, boxes, lane); break;
-                    default: epilogue_tile<COLS, DG_ACT_NONE>(accum, p, y, cstart, residual_on, boxes, lane); break;
-                }
+                epilogue_tile<COLS, ACT>(accum, p, y, cstart, residual_on, boxes, lane);
             }
             // ---- store this CTA's rows of the tile
             if constexpr (MODE == kKGrouped) {
@@ -1381,7 +1379,7 @@ dg_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant
                     const size_t at = static_cast<size_t>(ti.d_row + row) * p.n + ti.n0 + c4;
                     __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.d) + at;
                     float v[4] = {sum.x, sum.y, sum.z, sum.w};
-                    if constexpr (MODE == kEpilogue) epilogue_four(v, p, ti.n0 + c4, at);
+                    if constexpr (MODE == kEpilogue) epilogue_four<ACT>(v, p, ti.n0 + c4, at);
                     st_global_v2(dst, pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
                 }
             }

@@ -108,21 +108,13 @@ __device__ __forceinline__ float reciprocal_approx(float v) {
 // 1 / (1 + exp(-z)) with the hardware's base-2 exponential and reciprocal, each good to an ulp or two of FP32;
 // every use ends in BF16 or e4m3. Saturates to 0 and 1 without NaN; NaN stays.
 constexpr float LOG2_E = 1.4426950408889634f;
+constexpr float LOG2_E_REST = 1.925963e-8f;       // log2(e) - float(log2(e))
 __device__ __forceinline__ float fast_sigmoid(float z) { return reciprocal_approx(1.f + exp2_approx(-LOG2_E * z)); }
 
 // sqrt(2 / pi) and the cubic coefficient of the tanh form of GELU, z (1 + tanh(y)) / 2 with
 // y = GELU_A (z + GELU_B z^3); (1 + tanh(y)) / 2 = sigmoid(2 y).
 constexpr float GELU_A = 0.7978845608028654f;
 constexpr float GELU_B = 0.044715f;
-
-template <int ACT>
-__device__ __forceinline__ float act_value(float z) {
-    if (ACT == DG_ACT_RELU) return z < 0.f ? 0.f : z;                     // NaN stays
-    if (ACT == DG_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
-    if (ACT == DG_ACT_GELU_TANH) return z * fast_sigmoid(2.f * GELU_A * (z + GELU_B * z * z * z));
-    if (ACT == DG_ACT_SILU) return z * fast_sigmoid(z);
-    return z;
-}
 
 // max(v, floor), NaN staying NaN
 __device__ __forceinline__ float at_least(float v, float floor) {
@@ -137,6 +129,26 @@ __device__ __forceinline__ float at_most(float v, float ceiling) {
     asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(v), "f"(ceiling));
     return d;
 }
+
+// GELU, z Phi(z), by the normal distribution's upper tail: 1 - Phi(m) = P(t) exp(-m^2 / 2), t = 1 / (1 + 0.35 m),
+// for 0 <= m <= GELU_END; beyond it the tail is 0 to FP32. P was fitted to that quotient for the smallest largest
+// relative error, which is 5.6e-7 in FP32 arithmetic (the form is Hastings' for the error function, whose published
+// coefficients have 1.5e-7 of 1, not of the tail). The two reciprocals of a pair are one.
+constexpr float GELU_END = 14.f;
+__device__ __forceinline__ float2 upper_tail2(float2 m) {
+    const float2 u = __ffma2_rn(m, make_float2(0.35f, 0.35f), make_float2(1.f, 1.f));
+    const float r = reciprocal_approx(u.x * u.y);
+    const float2 t = make_float2(r * u.y, r * u.x);
+    constexpr float P[8] = {-2.7859039619215764e-05f, 0.14027923345565796f, 0.1332964450120926f, 0.15616419911384583f,
+                            -0.017421623691916466f, 0.24108751118183136f, -0.2023855596780777f, 0.04900781065225601f};
+    float2 s = make_float2(P[7], P[7]);
+#pragma unroll
+    for (int i = 6; i >= 0; --i) s = __ffma2_rn(s, t, make_float2(P[i], P[i]));
+    return s;
+}
+
+// below zero g, from zero on 1 - g; NaN stays
+__device__ __forceinline__ float slope_of(float z, float g) { return z < 0.f ? g : (z >= 0.f ? 1.f - g : z); }
 
 // The slopes of an activation at two BF16 pre-activations, in packed arithmetic where it has a form for that.
 //
@@ -164,19 +176,28 @@ __device__ __forceinline__ float2 act_slope2(float2 z) {
         const float2 y = __fmul2_rn(z, __ffma2_rn(z2, make_float2(2.f * GELU_A * GELU_B, 2.f * GELU_A * GELU_B), make_float2(2.f * GELU_A, 2.f * GELU_A)));
         const float2 dy = __ffma2_rn(z2, make_float2(6.f * GELU_A * GELU_B, 6.f * GELU_A * GELU_B), make_float2(2.f * GELU_A, 2.f * GELU_A));
         // the rounding of y log2(e), and what log2(e) has beyond FP32, go in as a factor too
-        constexpr float REST = 1.925963e-8f, LN2 = 0.6931471805599453f;       // log2(e) - float(log2(e))
+        constexpr float LN2 = 0.6931471805599453f;
         const float2 l = make_float2(-LOG2_E, -LOG2_E), t = __fmul2_rn(y, l);
         float2 e = make_float2(exp2_approx(fminf(t.x, 126.f)), exp2_approx(fminf(t.y, 126.f)));
-        const float2 low = __ffma2_rn(y, make_float2(-REST, -REST), __ffma2_rn(y, l, __fmul2_rn(t, minus)));
+        const float2 low = __ffma2_rn(y, make_float2(-LOG2_E_REST, -LOG2_E_REST), __ffma2_rn(y, l, __fmul2_rn(t, minus)));
         e = __ffma2_rn(e, __fmul2_rn(low, make_float2(LN2, LN2)), e);
         const float2 s = __fadd2_rn(e, one);
         float2 p = make_float2(reciprocal_approx(s.x), reciprocal_approx(s.y));
         p = __ffma2_rn(__ffma2_rn(__ffma2_rn(e, minus, minus), p, one), p, p);
         return __ffma2_rn(__fmul2_rn(p, __ffma2_rn(p, minus, one)), __fmul2_rn(z, dy), p);
     }
-    if (ACT == DG_ACT_GELU)
-        return make_float2(0.5f * (1.f + erff(z.x * 0.70710678118654752f)) + z.x * 0.3989422804014327f * expf(-0.5f * z.x * z.x),
-                           0.5f * (1.f + erff(z.y * 0.70710678118654752f)) + z.y * 0.3989422804014327f * expf(-0.5f * z.y * z.y));
+    if (ACT == DG_ACT_GELU) {
+        // Phi(z) + z phi(z): with m = |z| that is g = (P(t) - m / sqrt(2 pi)) exp(-z^2 / 2) below zero, 1 - g above.
+        // z^2 has 16 significant bits; what its product with log2(e) / 2 loses goes in as a factor.
+        const float2 m = make_float2(fminf(fabsf(z.x), GELU_END), fminf(fabsf(z.y), GELU_END));
+        constexpr float L = 0.5f * LOG2_E, LN2 = 0.6931471805599453f;
+        const float2 z2 = __fmul2_rn(m, m), x = __fmul2_rn(z2, make_float2(-L, -L));
+        float2 e = make_float2(exp2_approx(x.x), exp2_approx(x.y));
+        const float2 low = __fadd2_rn(__ffma2_rn(z2, make_float2(-L, -L), __fmul2_rn(x, minus)), __fmul2_rn(z2, make_float2(-0.5f * LOG2_E_REST, -0.5f * LOG2_E_REST)));
+        e = __ffma2_rn(e, __fmul2_rn(low, make_float2(LN2, LN2)), e);
+        const float2 g = __fmul2_rn(e, __ffma2_rn(m, make_float2(-0.3989422804014327f, -0.3989422804014327f), upper_tail2(m)));
+        return make_float2(slope_of(z.x, g.x), slope_of(z.y, g.y));
+    }
     if (ACT == DG_ACT_RELU) return make_float2(z.x > 0.f ? 1.f : 0.f, z.y > 0.f ? 1.f : 0.f);
     return one;
 }
@@ -195,34 +216,40 @@ __device__ __forceinline__ float2 times_sigmoid2(float2 z, float2 y) {
 
 template <int ACT>
 __device__ __forceinline__ float2 act_value2(float2 z) {
+    if (ACT == DG_ACT_RELU) return make_float2(z.x < 0.f ? 0.f : z.x, z.y < 0.f ? 0.f : z.y);     // NaN stays
+    if (ACT == DG_ACT_GELU) {
+        const float2 m = make_float2(fminf(fabsf(z.x), GELU_END), fminf(fabsf(z.y), GELU_END));
+        const float2 x = __fmul2_rn(__fmul2_rn(m, m), make_float2(-0.5f * LOG2_E, -0.5f * LOG2_E));
+        const float2 tail = __fmul2_rn(upper_tail2(m), make_float2(exp2_approx(x.x), exp2_approx(x.y)));
+        return __ffma2_rn(__fmul2_rn(m, make_float2(-1.f, -1.f)), tail, make_float2(at_least(z.x, 0.f), at_least(z.y, 0.f)));
+    }
     if (ACT == DG_ACT_GELU_TANH) {
         const float2 c = __ffma2_rn(__fmul2_rn(z, z), make_float2(2.f * GELU_A * GELU_B, 2.f * GELU_A * GELU_B), make_float2(2.f * GELU_A, 2.f * GELU_A));
         return times_sigmoid2(z, __fmul2_rn(z, c));
     }
     if (ACT == DG_ACT_SILU) return times_sigmoid2(z, z);
-    return make_float2(act_value<ACT>(z.x), act_value<ACT>(z.y));
+    return z;
+}
+
+template <int ACT, int N>
+__device__ __forceinline__ void act_pairs(float (&v)[N]) {
+    static_assert(N % 2 == 0, "pairs");
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+        const float2 a = act_value2<ACT>(make_float2(v[i], v[i + 1]));
+        v[i] = a.x;
+        v[i + 1] = a.y;
+    }
 }
 
 // act over an array in registers, with one branch on the (uniform) choice around the whole loop.
 template <int N>
 __device__ __forceinline__ void act_values(int act, float (&v)[N]) {
     switch (act) {
-        case DG_ACT_RELU:
-#pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = act_value<DG_ACT_RELU>(v[i]);
-            break;
-        case DG_ACT_GELU:
-#pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = act_value<DG_ACT_GELU>(v[i]);
-            break;
-        case DG_ACT_GELU_TANH:
-#pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = act_value<DG_ACT_GELU_TANH>(v[i]);
-            break;
-        case DG_ACT_SILU:
-#pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = act_value<DG_ACT_SILU>(v[i]);
-            break;
+        case DG_ACT_RELU: act_pairs<DG_ACT_RELU>(v); break;
+        case DG_ACT_GELU: act_pairs<DG_ACT_GELU>(v); break;
+        case DG_ACT_GELU_TANH: act_pairs<DG_ACT_GELU_TANH>(v); break;
+        case DG_ACT_SILU: act_pairs<DG_ACT_SILU>(v); break;
         default: break;
     }
 }
