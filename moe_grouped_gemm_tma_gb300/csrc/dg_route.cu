@@ -1,8 +1,9 @@
 // The router around the experts' products: top-k selection with its weights (dg_moe_route) and their
 // gradient (dg_moe_route_backward), one warp a row.
 //
-// Selection. A lane holds VPL consecutive experts of the row, so that lower lanes hold lower experts. k
-// whole-warp maxima over the lanes' best values give a bound below which no selected value can lie (k lanes
+// Selection. A lane holds VPL experts of the row: consecutive ones where the rows can be read in vectors, else
+// every 32nd, so that a load or store of the warp still covers one piece of the row (E = 510, FP32, 25052 rows:
+// the gradient took 52.8 us with consecutive experts and single loads, 13.0 so). k whole-warp maxima over the lanes' best values give a bound below which no selected value can lie (k lanes
 // hold one at least as large); the few values at or above it -- k and a handful in practice -- are compacted
 // through shared memory, one a lane, and each counts those that precede it (larger, or equal with a lower
 // expert), which is its place in the order. More than 32 candidates (many equal values) take k rounds of
@@ -18,6 +19,7 @@
 #include <cuda_runtime.h>
 
 #include <cfloat>
+#include <climits>
 
 #include "dg.h"
 #include "dg_host.cuh"
@@ -33,8 +35,8 @@ constexpr unsigned FULL = 0xffffffffu;
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 
-// The lane's VPL consecutive logits of a row; -inf past the row's end. Vector loads where the rows allow
-// them (`vec`: VPL divides E, and rows and base are aligned to the lane's whole vector).
+// The lane's VPL logits of a row, -inf past the row's end: consecutive ones by vector loads where the rows allow
+// that (`vec`: VPL divides E, and rows and base are aligned to the lane's whole vector), else every 32nd.
 template <int VPL, typename T>
 __device__ __forceinline__ void load_row(const T* row, int E, int lane, bool vec, float (&v)[VPL]) {
     const int e0 = lane * VPL;
@@ -72,7 +74,7 @@ __device__ __forceinline__ void load_row(const T* row, int E, int lane, bool vec
         }
     }
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) v[i] = e0 + i < E ? to_f32(row[e0 + i]) : -INFINITY;
+    for (int i = 0; i < VPL; ++i) v[i] = lane + 32 * i < E ? to_f32(row[lane + 32 * i]) : -INFINITY;
 }
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -95,10 +97,9 @@ __device__ __forceinline__ float sigmoid(float l) { return __frcp_rn(1.f + expf(
 // its argument) and the reciprocal ten times over; the sums are rounded to 2^-24 of themselves on either side.
 __device__ __forceinline__ float selection_margin(float sum) { return 1.9073486e-6f + 2.4e-7f * fabsf(sum); }
 
-// The VPL biases of a lane's experts (0 past the row's end).
+// The VPL biases of a lane's experts e0, e0 + step, ... (0 past the row's end).
 template <int VPL>
-__device__ __forceinline__ void load_bias(const float* bias, int E, int lane, bool vec, float (&v)[VPL]) {
-    const int e0 = lane * VPL;
+__device__ __forceinline__ void load_bias(const float* bias, int E, int e0, int step, bool vec, float (&v)[VPL]) {
     if constexpr (VPL >= 4) {
         if (vec) {
 #pragma unroll
@@ -111,7 +112,7 @@ __device__ __forceinline__ void load_bias(const float* bias, int E, int lane, bo
         }
     }
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) v[i] = e0 + i < E ? __ldg(bias + e0 + i) : 0.f;
+    for (int i = 0; i < VPL; ++i) v[i] = e0 + i * step < E ? __ldg(bias + e0 + i * step) : 0.f;
 }
 
 // +inf counts as the largest finite value, so that no score is a quotient of infinities
@@ -132,12 +133,13 @@ route_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int32
     grid_launch_dependents();
     if (t >= rows) return;
     const T* row = logits + static_cast<size_t>(t) * E;
+    const int e0 = (vec & 1) ? lane * VPL : lane, step = (vec & 1) ? 1 : 32;     // the lane's experts
     // selection values: the logits, or the approximate sums; -inf where an expert cannot be selected (NaN too)
     float v[VPL];
     load_row<VPL, T>(row, E, lane, (vec & 1) != 0, v);
     if (bias != nullptr) {
         float b[VPL];
-        load_bias<VPL>(bias, E, lane, (vec & 2) != 0, b);
+        load_bias<VPL>(bias, E, e0, step, vec == 3, b);
 #pragma unroll
         for (int i = 0; i < VPL; ++i) v[i] = v[i] > -INFINITY ? fast_sigmoid(v[i]) + b[i] : -INFINITY;
     } else {
@@ -186,9 +188,9 @@ route_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int32
     float value = -INFINITY;         // its logit
     const int picked = min(found, k);
     if (found <= 32) {
-        // candidates in expert order, one a lane, which reads its logit again (it knows where from only now)
+        // the candidates one a lane, which reads its logit again (it knows where from only now)
         int at = before;
-        for (uint32_t m = mask; m != 0; m &= m - 1) s_cand[warp][at++] = lane * VPL + __ffs(m) - 1;
+        for (uint32_t m = mask; m != 0; m &= m - 1) s_cand[warp][at++] = e0 + (__ffs(m) - 1) * step;
         __syncwarp();
         float me = -INFINITY;
         if (lane < found) {
@@ -199,7 +201,7 @@ route_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int32
         s_value[warp][lane] = me;
         __syncwarp();
         // candidates that are at least as large, four a turn; without equal values the lanes' counts are
-        // 1 .. found, and where they are not, equal ones are counted by their order
+        // 1 .. found, and where they are not, equal ones are counted by their experts' order
         int ahead = -1;
         for (int c = 0; c < found; c += 4) {
             const float4 o = *reinterpret_cast<const float4*>(&s_value[warp][c]);
@@ -210,7 +212,8 @@ route_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int32
             ahead = 0;
             for (int c = 0; c < found; ++c) {
                 const float other = __shfl_sync(FULL, me, c);
-                if (c < lane ? other >= me : other > me) ++ahead;
+                const int oe = __shfl_sync(FULL, expert, c);
+                if (oe < expert ? other >= me : other > me) ++ahead;
             }
         }
         if (lane < found && ahead < k) place = ahead;
@@ -220,7 +223,7 @@ route_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int32
         if (bias != nullptr) {
 #pragma unroll 1
             for (int i = 0; i < VPL; ++i) {
-                const int e = lane * VPL + i;
+                const int e = e0 + i * step;
                 float exact = -INFINITY;
                 if (e < E) {
                     const float l = to_f32(row[e]);
@@ -238,9 +241,9 @@ route_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int32
             for (int i = 0; i < VPL; ++i)
                 if (v[i] > best) { best = v[i]; bi = i; }
             const float most = warp_max(best);
-            const int owner = __ffs(__ballot_sync(FULL, best == most)) - 1;
-            const int e = __shfl_sync(FULL, lane * VPL + bi, owner);
-            if (lane == owner) {
+            const int own = e0 + bi * step;
+            const int e = __reduce_min_sync(FULL, best == most ? own : INT_MAX);
+            if (own == e) {
 #pragma unroll
                 for (int i = 0; i < VPL; ++i)
                     if (i == bi) v[i] = -INFINITY;
@@ -297,7 +300,7 @@ __device__ __forceinline__ void store_row(T* row, int E, int lane, bool vec, con
     }
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
-        if (e0 + i < E) store_one(row + e0 + i, v[i]);
+        if (lane + 32 * i < E) store_one(row + lane + 32 * i, v[i]);
 }
 
 // The gradient of the row's k weights with respect to its logits. With p the scores of the selected
@@ -395,7 +398,7 @@ template <int VPL, typename T>
 bool vector_rows(const void* a, const void* b, int E) {
     constexpr int BYTES = VPL * static_cast<int>(sizeof(T));
     constexpr int W = BYTES >= 16 ? 16 : BYTES;
-    return E % VPL == 0 && (static_cast<int64_t>(E) * sizeof(T)) % W == 0 && aligned(a, W) && aligned(b, W);
+    return BYTES >= 8 && E % VPL == 0 && (static_cast<int64_t>(E) * sizeof(T)) % W == 0 && aligned(a, W) && aligned(b, W);
 }
 
 template <int VPL, typename T>

@@ -78,6 +78,17 @@ def test_equal_values_take_the_lower_expert():
         check(l.to(torch.bfloat16), k)
 
 
+@pytest.mark.parametrize("E", [48, 256, 301, 510, 1024])
+@pytest.mark.parametrize("levels", [2, 40])
+def test_ties_in_every_layout(E, levels):
+    # few distinct logits; with a bias the sums of equal pairs are equal too
+    g = torch.Generator().manual_seed(E + levels)
+    l = torch.randint(0, levels, (40, E), generator=g).float() / 8
+    check(l, 8)
+    check(l.to(torch.bfloat16), 8, scoring="sigmoid")
+    check(l, 8, torch.full((E,), 0.25), scoring="sigmoid")
+
+
 @pytest.mark.parametrize("half", [False, True])
 def test_masked_experts_and_empty_rows(half):
     l = make(8, 70, 5, half)
