@@ -76,7 +76,7 @@ struct MoeParams {
     float* parts;          // [CTA][ML_SLOTS][NT][256]: sums of phase-1 units and of parts of them
     float* y;              // [gathered row][part][pairs * 256] weighted by nothing yet
     unsigned* barrier;     // grid barrier word
-    unsigned* count;       // [phase-1 line][CTA]: parts written of the unit that the CTA's share ends in
+    unsigned* count;       // [phase-1 line][CTA]: parts of the unit that the CTA's share ends in
     int* status;
     int T, k, E, H, I, rows_cap, act;
     unsigned long long wait_limit_ns;
@@ -129,6 +129,10 @@ __device__ __forceinline__ unsigned atom_add_acq_rel(unsigned* p, unsigned v) {
     return old;
 }
 
+__device__ __forceinline__ void red_add_release(unsigned* p, unsigned v) {
+    asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+
 __device__ __forceinline__ void finishers_barrier() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
 __device__ __forceinline__ void add4(float4& a, const float4& b) { a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w; }
@@ -140,11 +144,26 @@ __device__ __forceinline__ void add4(float4& a, const float4& b) { a.x += b.x; a
 // launch); the wait ends by itself all the same.
 __device__ __forceinline__ bool grid_barrier(unsigned* word, unsigned top, volatile int* abort_flag, int* status, uint64_t limit_ns) {
     const unsigned add = blockIdx.x == 0 ? 0x80000000u - (gridDim.x - 1) : 1u;
-    asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(word), "r"(add) : "memory");
+    red_add_release(word, add);
     const uint64_t t0 = global_timer_ns();
     const uint64_t limit = limit_ns ? limit_ns : WAIT_LIMIT_NS;
     for (int i = 0; i < (1 << 26); ++i) {
         if ((ld_acquire(word) ^ top) & 0x80000000u) return true;
+        if ((i & 63) == 63 && global_timer_ns() - t0 > limit) break;
+    }
+    *abort_flag = 1;
+    record_status(status, STATUS_TIMEOUT);
+    return false;
+}
+
+// A thread's wait until all parts of a unit that its CTAs finish together are there: `arrivals` in the low 16 bits of
+// the count (the high ones count the CTAs that are done with them).
+__device__ __forceinline__ bool wait_parts(const unsigned* count, unsigned arrivals, volatile int* abort_flag, int* status, uint64_t limit_ns) {
+    const uint64_t t0 = global_timer_ns();
+    const uint64_t limit = limit_ns ? limit_ns : WAIT_LIMIT_NS;
+    for (int i = 0; i < (1 << 26); ++i) {
+        if ((ld_acquire(count) & 0xffffu) == arrivals) return true;
+        if (*abort_flag) return false;
         if ((i & 63) == 63 && global_timer_ns() - t0 > limit) break;
     }
     *abort_flag = 1;
@@ -215,6 +234,14 @@ __device__ __forceinline__ int most_parts(const Line& n) {
     if (n.total == 0) return 1;
     const int least = static_cast<int>(static_cast<unsigned>(n.total) / sharers(n.total));
     return (n.kbs - 1 + least - 1) / least + 1;
+}
+
+// Whether the CTAs of a divided phase-1 unit of n columns finish it together: with three parts or more, and more
+// columns than four warps take at once, if the line's shares are shorter than a unit, so that no CTA has more than
+// two segments of it. (55 tokens, 8 experts of 1152 x 128, nine parts and 28 columns a unit: the last CTA alone takes
+// 13 us for them.) The promoting warps count their parts themselves, so that no CTA waits for another's finishers.
+__device__ __forceinline__ bool finished_together(const Line& ln, int n, int parts) {
+    return parts > 2 && n > 4 && ln.total < static_cast<int>(gridDim.x) * ln.kbs;
 }
 
 // What a CTA does of one unit: stages [kb0, kb0 + nkb) of unit `unit`, for one chunk of an expert's tokens.
@@ -732,6 +759,11 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap map_w13, const __grid_const
             regs_dec<ML_FIN_REGS>();
             const int q = warp & 3;
             Ring part;
+            // a CTA is done with a unit that is finished together; the last one leaves the count as the next launch
+            // expects it
+            auto leave = [](unsigned* count, int parts) {
+                if ((atom_add_acq_rel(count, 0x10000u) >> 16) == static_cast<unsigned>(parts - 1)) *count = 0;
+            };
             for_segments<NT>(p, s, [&](int l) {
                 if (l > 0) line_done(l);
                 return l < 2;
@@ -743,16 +775,26 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap map_w13, const __grid_const
                 const unsigned u0 = static_cast<unsigned>(g.unit) * ln.kbs;
                 const bool divided = g.nkb < ln.kbs;
                 const int c_lo = divided ? cta_of(u0, ln.total) : cta, c_hi = divided ? cta_of(u0 + ln.kbs - 1, ln.total) : cta;
+                const int parts = c_hi - c_lo + 1;
+                // A divided unit is finished by the CTA whose part comes last, adding the parts in order, or by all of
+                // them together, each a share of the columns.
+                const bool shared = finished_together(ln, g.n, parts);
+                const int c_first = shared ? 4 * (cta - c_lo) : 0, c_step = shared ? 4 * parts : 4;
+                unsigned* count = p.count + l * ML_MAX_CTAS + c_lo;
                 bool mine = true;
                 if (divided) {
-                    // the unit is finished by the CTA whose part comes last, adding the parts in order
                     finishers_barrier();
                     if (q == 0 && lane == 0) {
                         // (releases what part_full has gathered from this CTA, acquires the others' parts)
-                        unsigned* count = p.count + l * ML_MAX_CTAS + c_lo;
-                        const bool last = atom_add_acq_rel(count, 1u) == static_cast<unsigned>(c_hi - c_lo);
-                        if (last) *count = 0;   // as the next launch expects it
-                        s.last = last ? 1 : 0;
+                        bool here;
+                        if (shared) {
+                            here = c_first < g.n && wait_parts(count, static_cast<unsigned>(EPI_WARPS * parts), abort_flag, p.status, p.wait_limit_ns);
+                            if (!here) leave(count, parts);
+                        } else {
+                            here = atom_add_acq_rel(count, 1u) == static_cast<unsigned>(parts - 1);
+                            if (here) *count = 0;   // as the next launch expects it
+                        }
+                        s.last = here ? 1 : 0;
                     }
                     finishers_barrier();
                     mine = s.last != 0;
@@ -760,7 +802,6 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap map_w13, const __grid_const
                 if (mine) {
                     // A warp takes whole columns (tokens), four rows a lane. Eight pairs of loads are in flight: up
                     // to two parts of four columns, or the first eight parts of one.
-                    const int parts = c_hi - c_lo + 1;
                     const float* mine_at = p.parts + lane * 4;
                     auto part_at = [&](int pt) {    // in floats from there
                         return static_cast<size_t>((divided ? divided_slot(c_lo + pt, l, u0) : slot_at(cta, 4 + part.stage)) - p.parts);
@@ -805,16 +846,18 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap map_w13, const __grid_const
                         }
                     } else {
 #pragma unroll 1
-                        for (int c0 = q; c0 < g.n; c0 += 4) {
+                        for (int c0 = c_first + q; c0 < g.n; c0 += c_step) {
                             float4 gate = make_float4(0.f, 0.f, 0.f, 0.f), upv = gate;
 #pragma unroll 1
                             for (int p0 = 0; p0 < parts; p0 += 8) {
                                 float4 vg[8], vu[8];
+                                const unsigned from = static_cast<unsigned>(part_at(min(p0 + (lane & 7), parts - 1)));
 #pragma unroll
                                 for (int i = 0; i < 8; ++i) {
+                                    const unsigned at = __shfl_sync(FULL_MASK, from, i);
                                     vg[i] = vu[i] = make_float4(0.f, 0.f, 0.f, 0.f);
                                     if (p0 + i < parts) {
-                                        const float* src = mine_at + part_at(p0 + i) + c0 * 256;
+                                        const float* src = mine_at + at + c0 * 256;
                                         vg[i] = __ldcg(reinterpret_cast<const float4*>(src));
                                         vu[i] = __ldcg(reinterpret_cast<const float4*>(src + 128));
                                     }
@@ -827,6 +870,10 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap map_w13, const __grid_const
                             }
                             finish(gate, upv, c0);
                         }
+                    }
+                    if (shared) {
+                        finishers_barrier();
+                        if (q == 0 && lane == 0) leave(count, parts);
                     }
                 }
                 __syncwarp();
@@ -924,7 +971,14 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap map_w13, const __grid_const
                         __stcg(dst + col * 256 + 128 + r, x1);
                     });
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&s.part_full[part.stage]);
+                    if (lane == 0) {
+                        if (g.nkb < ln.kbs) {
+                            const unsigned u0 = static_cast<unsigned>(g.unit) * ln.kbs;
+                            const int c_lo = cta_of(u0, ln.total);
+                            if (finished_together(ln, g.n, cta_of(u0 + ln.kbs - 1, ln.total) - c_lo + 1)) red_add_release(p.count + l * ML_MAX_CTAS + c_lo, 1u);
+                        }
+                        mbar_arrive(&s.part_full[part.stage]);
+                    }
                     part.next(ML_PARTS);
                 } else {
                     const float* sb = p.s2 + (static_cast<size_t>(g.e) * (p.H / 128) + 2 * g.blk) * ln.kbs;
