@@ -132,7 +132,7 @@ def route_backward(logits, ids, dw, scoring, renorm, scale):
     T, E = logits.shape
     out = np.zeros((T, E))
     for t in range(T):
-        l = logits[t]
+        l = np.minimum(logits[t], float(np.finfo(np.float32).max))        # as the forward pass takes +inf
         ok = l > -np.inf
         if not ok.any():
             continue

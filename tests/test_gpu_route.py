@@ -78,6 +78,32 @@ def test_equal_values_take_the_lower_expert():
         check(l.to(torch.bfloat16), k)
 
 
+@pytest.mark.parametrize("T", [4096, 4098])
+@pytest.mark.parametrize("E,k", [(2, 1), (7, 7), (8, 2), (9, 3), (16, 16), (17, 4)])
+def test_few_experts_and_many_rows(T, E, k):
+    logits = make(T, E, T + E, False)
+    logits[::5, : E // 2] = -math.inf
+    logits[3], logits[4] = -math.inf, math.nan
+    logits[5, 0] = math.inf
+    logits[7:40] = torch.round(logits[7:40])                 # ties
+    for scoring in ("softmax", "sigmoid"):
+        for renorm in (False, True):
+            check(logits, k, scoring=scoring, renormalize=renorm, scale=1.5)
+            ids, _ = R.route(logits[:200].double().numpy(), k, scoring, renorm, 1.0)
+            # the whole gradient, with the last row of the forward pass's rows among them
+            every = np.concatenate([ids] * (T // 200 + 1))[:T]
+            src = torch.cat([logits[:200]] * (T // 200 + 1))[:T].contiguous()
+            dw = torch.randn(T, k, generator=torch.Generator().manual_seed(k))
+            out = torch.full((T, E), math.nan, device="cuda")
+            dg.dg_moe_route_backward(src.cuda(), torch.from_numpy(every).int().cuda(), dw.cuda(), out, scoring=scoring,
+                                     renormalize=renorm, scale=1.5)
+            want = R.route_backward(src.double().numpy(), every, dw.double().numpy(), scoring, renorm, 1.5)
+            bound = 1e-5 * 1.5 * np.abs(dw.numpy()).max(1, keepdims=True) * max(1, k)
+            assert (np.abs(out.cpu().double().numpy() - want) <= bound).all()
+    bias = torch.round(torch.randn(E, generator=torch.Generator().manual_seed(4)) * 64) / 64
+    check(torch.round(logits), k, bias, scoring="sigmoid")
+
+
 @pytest.mark.parametrize("E", [48, 256, 301, 510, 1024])
 @pytest.mark.parametrize("levels", [2, 40])
 def test_ties_in_every_layout(E, levels):
