@@ -261,8 +261,8 @@ int choose_split(const Spec (&cands)[NC], Spec* sp, int64_t row_blocks, int n, i
 // time at that width each (64 columns 0.30 us, 128 0.37, 192 0.47: 0.21 us and 1.37 ns a column), 4 us for the
 // launch and the tile's ends, and for a split, which has to fit in one wave, 4 us more and 20 ns a column for
 // the exchange of the partial sums. It named the fastest of 9 to 12 measured choices for every one of twelve
-// shapes (333 x 2112 x 7168: 192 columns, 4 CTAs a tile, 18.5 us, where 64 columns unsplit take 21.6;
-// 150 x 2048 x 1024: 64 unsplit, 7.0, where 2 CTAs a tile take 8.9).
+// shapes (333 x 2112 x 7168: 192 columns, 4 CTAs a tile, 15.5 us, where 64 columns unsplit take 20.9;
+// 150 x 2048 x 1024: 64 unsplit, 7.0, where 2 CTAs a tile take 8.3).
 int plan_epilogue(Spec* sp, int64_t row_blocks, int n, int kbs, int sms) {
     int split = 1;
     int64_t best = INT64_MAX;
@@ -552,7 +552,7 @@ static dg_status gemm_impl(const uint8_t* A, const float* sfa, const uint8_t* B,
         // With an epilogue the two were measured over M = 1..64, N = 512..24576, K = 128..7168: up to 32 rows and
         // one wave of column tiles the decode kernel wins (M = 1: 4.0 against 4.5 us at N = 512, K = 128 up to 16
         // against 31 at 8192 x 7168; M = 20 ties at K <= 512), with more rows from K = 1024 on and up to 32
-        // column tiles, or 64 for a long K (M = 64, N = 7168, K = 2048: 11.9 against 10.5).
+        // column tiles, or 64 for a long K (M = 64, 8192 x 7168: 20.5 against 21.6; 7168 x 2048 ties).
         if (ep) decode = M <= 64 && (M <= 32 ? col_tiles <= dev.sms : K >= 1024 && col_tiles <= (K >= 7168 ? 64 : 32));
         if (const int v = tune(DG_TUNE_SWAP); v >= 0) decode = (v == 1) && (!ep || M <= 64);
         if (decode) pl = ep ? plan_decode<kEpilogue>(1, M, M, N, kbs, dev.sms) : plan_decode<kNormal>(1, M, M, N, kbs, dev.sms);

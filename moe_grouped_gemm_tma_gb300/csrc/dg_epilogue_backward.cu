@@ -13,7 +13,11 @@
 // The bias gradient is summed in a fixed order whatever the timing: each tile writes its column sums, and
 // the CTA that finishes a column strip last adds the strip's tiles from the first to the last.
 //
-// Floor: 4 bytes read and 2 written per element (2 read without an activation).
+// Floor: 4 bytes read and 2 written per element (2 read without an activation), 26.6 us for 4096 x 7168 at the
+// measured copy bandwidth. It takes 45.4 us, 63% of the issue slots and a third of its warps' time at the tile's two
+// barriers: the two scalings need the whole tile's maxima between the loads and the stores, and two CTAs an SM hide
+// only part of that. (A persistent form with the next tile's operands in shared memory by TMA took 54 us, without
+// the exact divisions of the codes it would take 44.5.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -82,7 +82,10 @@ constexpr int STATUS_TIMEOUT = 6;       // DG_DEVICE_TIMEOUT
 enum Mode : int { kNormal = 0, kContiguous = 1, kMasked = 2, kKGrouped = 3, kEpilogue = 4 };
 
 // kEpilogue is the normal layout with bias, activation and residual applied to the tile before it is
-// rounded; everything before that point is the normal layout's.
+// rounded; everything before that point is the normal layout's. 4096 x 7168 x 2048 takes 60 us without, 65 as it,
+// 76 with bias and silu, and 87 with residual and Z too (199 MB, 30 us of HBM): the tile's end is done by the
+// warps that promote, and the tensor cores wait for them. (Four warps of their own for it, taking the FP32 sums
+// through tensor memory, slow the promotion beside them by as much: 90.6 us.)
 __host__ __device__ constexpr bool normal_layout(int mode) { return mode == kNormal || mode == kEpilogue; }
 
 struct Params {

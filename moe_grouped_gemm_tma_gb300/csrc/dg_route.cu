@@ -1,20 +1,21 @@
 // The router around the experts' products: top-k selection with its weights (dg_moe_route) and their
-// gradient (dg_moe_route_backward), one warp a row.
+// gradient (dg_moe_route_backward), one warp a row, or four rows a warp with few experts.
 //
 // Selection. A lane holds VPL experts of the row: consecutive ones where the rows can be read in vectors, else
 // every 32nd, so that a load or store of the warp still covers one piece of the row (E = 510, FP32, 25052 rows:
-// the gradient took 52.8 us with consecutive experts and single loads, 13.0 so). k whole-warp maxima over the lanes' best values give a bound below which no selected value can lie (k lanes
-// hold one at least as large); the few values at or above it -- k and a handful in practice -- are compacted
-// through shared memory, one a lane, and each counts those that precede it (larger, or equal with a lower
-// expert), which is its place in the order. More than 32 candidates (many equal values) take k rounds of
-// find-and-remove instead.
+// the gradient took 52.8 us with consecutive experts and single loads, 13.0 so). k whole-warp maxima over the
+// lanes' best values give a bound below which no selected value can lie (k lanes hold one at least as large); the
+// few values at or above it -- k and a handful in practice -- are compacted through shared memory, one a lane, and
+// each counts those that precede it (larger, or equal with a lower expert), which is its place in the order. More
+// than 32 candidates (many equal values) take k rounds of find-and-remove instead.
 //
 // With a bias the selection values are sums of a sigmoid, and which of two close ones is larger has to be
 // right: they are defined with an accurate exponential and a rounded reciprocal. Only the candidates pay for
 // that: the bound is found with the hardware's approximations, lowered by more than they can be off.
 //
-// What bounds it is instruction issue: a row of 256 BF16 logits is 512 bytes, or 1.5 instructions' time on
-// the whole GPU, and 250 instructions.
+// What bounds it is instruction issue: 32749 rows of 256 BF16 logits are 18.9 MB, 2.8 us of HBM, and 456
+// instructions a row with sigmoid scores, a bias and k = 8, which at 83% of the issue slots take 14.4 us.
+// Few rows are bound by one row's latency (1.7 us in a CUDA graph).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
