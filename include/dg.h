@@ -191,7 +191,8 @@ dg_status dg_gemm_fp8_nt_epilogue(const uint8_t* A, const float* sfa, const uint
  * code = e4m3(v / s), both quotients rounded to FP32. With DG_ACT_NONE this quantises a BF16 matrix in one
  * or both directions. N must be a multiple of 128; M is free. dD, Z, q, qt 16-byte aligned.
  * workspace: device memory of dg_epilogue_backward_workspace(M, N) bytes, 16-byte aligned, needed for dbias
- * (else it may be null), zeroed before its first use; every call leaves it ready for the next one.
+ * (else it may be null), zeroed before its first use; every call leaves it ready for the next one, of any size
+ * that it is large enough for.
  */
 dg_status dg_epilogue_backward(const void* dD, const void* Z, int act, uint8_t* q, float* sf, uint8_t* qt, float* sft,
                                float* dbias, void* workspace, int64_t workspace_bytes, int M, int N,

@@ -10,14 +10,17 @@
 // go through 16 KB of shared memory, four rows of one column in a word, words XOR-ed by the column group so
 // that neither side conflicts, and leave as 128-byte rows.
 //
-// The bias gradient is summed in a fixed order whatever the timing: each tile writes its column sums, and
-// the CTA that finishes a column strip last adds the strip's tiles from the first to the last.
+// The bias gradient is summed in a fixed order whatever the timing: each tile writes its column sums, and these
+// are added up, every fourth tile's in turn, then the four sums: by the CTA that finishes a column strip last, or,
+// where there are more tiles than run at once, by a kernel of its own. Telling which CTA is last costs every
+// tile a fence behind its stores: 44.3 us for 4096 x 7168 with silu and 37.3 without an activation, where the
+// second launch gives 42.0 and 31.1; at 333 x 2048 it gives 5.4 for 5.8 us, less than the launch costs the host.
 //
 // Floor: 4 bytes read and 2 written per element (2 read without an activation), 26.6 us for 4096 x 7168 at the
-// measured copy bandwidth. It takes 45.4 us, 63% of the issue slots and a third of its warps' time at the tile's two
+// measured copy bandwidth. It takes 42 us, two thirds of the issue slots and much of its warps' time at the tile's two
 // barriers: the two scalings need the whole tile's maxima between the loads and the stores, and two CTAs an SM hide
-// only part of that. (A persistent form with the next tile's operands in shared memory by TMA took 54 us, without
-// the exact divisions of the codes it would take 44.5.)
+// only part of that. (A persistent form with the next tile's operands in shared memory by TMA was 7 us
+// slower; without the exact divisions of the codes it would be 1 us faster.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -42,12 +45,13 @@ struct EbParams {
     float* sft;
     float* dbias;
     float* sums;          // [m_tiles][N] column sums of each tile
-    unsigned* done;       // [N / 128] tiles of a strip that have written theirs
+    unsigned* done;       // [N / 128] tiles of a strip that have written theirs; null: a second kernel adds them up
     int m, n, m_tiles;
     int act;
 };
 
-template <int ACT>
+// (STRIPS: the last CTA of a strip adds its tiles' sums)
+template <int ACT, bool STRIPS>
 __global__ void __launch_bounds__(EB_THREADS, 2) epilogue_backward_kernel(const EbParams p) {
     __shared__ __align__(16) uint32_t s_codes[EB_TILE * EB_TILE / 4];
     __shared__ __align__(16) float s_amax[EB_WARPS][EB_TILE];
@@ -163,10 +167,12 @@ __global__ void __launch_bounds__(EB_THREADS, 2) epilogue_backward_kernel(const 
         float a = 0.f;
 #pragma unroll
         for (int w = 0; w < EB_WARPS; ++w) a += s_sum[w][c];
-        __stcg(p.sums + static_cast<size_t>(blockIdx.x) * p.n + n0 + c, a);
+        if (mt == 1) p.dbias[n0 + c] = a;              // the strip's only tile
+        else __stcg(p.sums + static_cast<size_t>(blockIdx.x) * p.n + n0 + c, a);
     }
     __syncthreads();
-    if (p.dbias != nullptr && threadIdx.x == 0) {
+    const bool strip = STRIPS && p.dbias != nullptr && mt > 1;
+    if (strip && threadIdx.x == 0) {
         // (releases the sums, which the barrier has ordered before it, to the strip's last CTA)
         __threadfence();
         s_last = atomicAdd(p.done + blockIdx.y, 1u) == static_cast<unsigned>(mt - 1);
@@ -201,25 +207,50 @@ __global__ void __launch_bounds__(EB_THREADS, 2) epilogue_backward_kernel(const 
             *reinterpret_cast<uint2*>(p.qt + static_cast<size_t>(n0 + c) * pitch + m0 + l16 * 8) = w;
         }
     }
-    if (p.dbias != nullptr && s_last && threadIdx.x < EB_TILE) {
+    if (strip && s_last) {
+        // every fourth tile's sums by each quarter of the threads, then the four in order
         __threadfence();
-        const float* src = p.sums + n0 + threadIdx.x;
+        const int c = threadIdx.x % EB_TILE, part = threadIdx.x / EB_TILE;
+        constexpr int PARTS = EB_THREADS / EB_TILE;
+        const float* src = p.sums + n0 + c;
         float a = 0.f;
 #pragma unroll 8
-        for (int i = 0; i < mt; ++i) a += __ldcg(src + static_cast<size_t>(i) * p.n);
-        p.dbias[n0 + threadIdx.x] = a;
+        for (int i = part; i < mt; i += PARTS) a += __ldcg(src + static_cast<size_t>(i) * p.n);
+        s_sum[part][c] = a;
+        __syncthreads();
+        if (threadIdx.x < EB_TILE) p.dbias[n0 + c] = (s_sum[0][c] + s_sum[1][c]) + (s_sum[2][c] + s_sum[3][c]);
         if (threadIdx.x == 0) p.done[blockIdx.y] = 0;  // the workspace is as the next call expects it
     }
 }
 
-template <int ACT>
-cudaError_t launch_eb(const EbParams& p, cudaStream_t stream) {
-    return launch_overlapped(epilogue_backward_kernel<ACT>, dim3(static_cast<unsigned>(p.m_tiles), static_cast<unsigned>(p.n / EB_TILE)),
-                             dim3(EB_THREADS), stream, p);
+// The bias gradient from the tiles' column sums: 32 columns a CTA, every fourth tile a warp.
+__global__ void __launch_bounds__(128) add_strips_kernel(const float* sums, float* dbias, int n, int m_tiles) {
+    __shared__ float s_part[4][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const float* src = sums + static_cast<int>(blockIdx.x) * 32 + lane;
+    float a = 0.f;
+#pragma unroll 8
+    for (int i = warp; i < m_tiles; i += 4) a += __ldcg(src + static_cast<size_t>(i) * n);
+    s_part[warp][lane] = a;
+    __syncthreads();
+    if (warp == 0) dbias[static_cast<int>(blockIdx.x) * 32 + lane] = (s_part[0][lane] + s_part[1][lane]) + (s_part[2][lane] + s_part[3][lane]);
 }
 
-// The counters come first, on their own 128-byte lines' worth of space, then the column sums.
-int64_t done_bytes(int n) { return (static_cast<int64_t>(cdiv(n, EB_TILE)) * 4 + 255) / 256 * 256; }
+template <int ACT>
+cudaError_t launch_eb(const EbParams& p, cudaStream_t stream) {
+    const dim3 grid(static_cast<unsigned>(p.m_tiles), static_cast<unsigned>(p.n / EB_TILE));
+    const cudaError_t e = p.done != nullptr ? launch_overlapped(epilogue_backward_kernel<ACT, true>, grid, dim3(EB_THREADS), stream, p)
+                                            : launch_overlapped(epilogue_backward_kernel<ACT, false>, grid, dim3(EB_THREADS), stream, p);
+    if (e != cudaSuccess || p.dbias == nullptr || p.m_tiles == 1 || p.done != nullptr) return e;
+    return launch_overlapped(add_strips_kernel, dim3(static_cast<unsigned>(p.n / 32)), dim3(128), stream, static_cast<const float*>(p.sums), p.dbias, p.n, p.m_tiles);
+}
+
+// The workspace: the strips' counters, in the same place whatever the size (no size's sums may lie where another's
+// counters do), then the column sums.
+constexpr int EB_STRIPS = 256;
+constexpr int64_t EB_DONE_BYTES = 4 * EB_STRIPS;
 
 }  // namespace
 }  // namespace dg
@@ -230,7 +261,7 @@ extern "C" {
 
 int64_t dg_epilogue_backward_workspace(int M, int N) {
     if (M <= 0 || N <= 0) return 0;
-    return done_bytes(N) + static_cast<int64_t>(cdiv(M, EB_TILE)) * N * 4;
+    return EB_DONE_BYTES + static_cast<int64_t>(cdiv(M, EB_TILE)) * N * 4;
 }
 
 dg_status dg_epilogue_backward(const void* dD, const void* Z, int act, uint8_t* q, float* sf, uint8_t* qt, float* sft,
@@ -263,11 +294,13 @@ dg_status dg_epilogue_backward(const void* dD, const void* Z, int act, uint8_t* 
     p.qt = qt;
     p.sft = sft;
     p.dbias = dbias;
-    p.done = static_cast<unsigned*>(workspace);
-    p.sums = dbias ? reinterpret_cast<float*>(static_cast<char*>(workspace) + done_bytes(N)) : nullptr;
+    p.sums = dbias ? reinterpret_cast<float*>(static_cast<char*>(workspace) + EB_DONE_BYTES) : nullptr;
     p.m = M;
     p.n = N;
     p.m_tiles = cdiv(M, EB_TILE);
+    const int strips = N / EB_TILE;
+    const bool one_round = static_cast<int64_t>(p.m_tiles) * strips <= 2 * dev.sms && strips <= EB_STRIPS;   // two CTAs fit an SM
+    p.done = one_round ? static_cast<unsigned*>(workspace) : nullptr;
     p.act = act;
     cudaError_t e = cudaErrorInvalidValue;
     switch (act) {

@@ -205,6 +205,16 @@ def test_backward(M, N, act):
     assert (np.abs(out["dbias"].double().numpy() - dz.sum(0)) <= 1e-5 * np.abs(dz).sum(0) + 1e-12).all()
 
 
+def test_backward_workspace_serves_smaller_sizes():
+    # one tile, several of a strip in one round, and more tiles than run at once, in turn on one workspace
+    ws = dg.epilogue_backward_workspace(700, 17024)
+    for M, N in [(300, 128), (256, 17024), (3, 256), (700, 17024), (2500, 2048), (300, 128), (256, 17024)]:
+        dD, Z = backward_inputs(M, N, M + N, "relu")
+        out = run_backward(dD, Z, "relu", ("dbias",), ws)
+        dz = dD.double().numpy() * R.act_slope(Z.double().numpy(), "relu")
+        assert (np.abs(out["dbias"].double().numpy() - dz.sum(0)) <= 1e-5 * np.abs(dz).sum(0) + 1e-12).all(), (M, N)
+
+
 @pytest.mark.parametrize("want", [("q",), ("qt",), ("dbias",), ("q", "dbias"), ("qt", "dbias"), ("q", "qt")])
 def test_backward_parts(want):
     # each output alone is the same, and what is not asked for is not needed
