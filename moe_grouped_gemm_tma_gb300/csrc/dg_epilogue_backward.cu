@@ -133,18 +133,22 @@ __global__ void __launch_bounds__(EB_THREADS, 2) epilogue_backward_kernel(const 
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             a[i] = abs_max(abs_max(dz[i][0].x, dz[i][0].y, dz[i][1].x), abs_max(dz[i][1].y, dz[i][2].x, dz[i][2].y), abs_max(dz[i][3].x, dz[i][3].y));
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) a[i] = abs_max(a[i], __shfl_xor_sync(0xffffffffu, a[i], o));
+        // over the 16 lanes, giving away rows on the way: lane l ends with that of row l / 4, and makes its scale
+        const bool up8 = (l16 & 8) != 0, up4 = (l16 & 4) != 0;
+        const float b0 = abs_max(up8 ? a[2] : a[0], __shfl_xor_sync(0xffffffffu, up8 ? a[0] : a[2], 8));
+        const float b1 = abs_max(up8 ? a[3] : a[1], __shfl_xor_sync(0xffffffffu, up8 ? a[1] : a[3], 8));
+        float most = abs_max(up4 ? b1 : b0, __shfl_xor_sync(0xffffffffu, up4 ? b0 : b1, 4));
+        most = abs_max(most, __shfl_xor_sync(0xffffffffu, most, 2));
+        most = abs_max(most, __shfl_xor_sync(0xffffffffu, most, 1));
+        const BlockScale mine = block_scale(abs_bits(most));
+        if ((l16 & 3) == 0 && (l16 >> 2) < valid) p.sf[static_cast<size_t>(m0 + r0 + (l16 >> 2)) * (p.n / 128) + blockIdx.y] = mine.s;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const BlockScale k = block_scale(abs_bits(a[i]));
+            BlockScale k;
+            k.d = __shfl_sync(0xffffffffu, mine.d, i * 4, 16);
+            k.r = __shfl_sync(0xffffffffu, mine.r, i * 4, 16);
             const uint32_t w0 = quantise4(dz[i][0], dz[i][1], k), w1 = quantise4(dz[i][2], dz[i][3], k);
-            if (i < valid) {
-                *reinterpret_cast<uint2*>(p.q + base + static_cast<size_t>(i) * p.n) = make_uint2(w0, w1);
-                if (l16 == 0) p.sf[static_cast<size_t>(m0 + r0 + i) * (p.n / 128) + blockIdx.y] = k.s;
-            }
+            if (i < valid) *reinterpret_cast<uint2*>(p.q + base + static_cast<size_t>(i) * p.n) = make_uint2(w0, w1);
         }
     }
     if (p.qt == nullptr && p.dbias == nullptr) return;
