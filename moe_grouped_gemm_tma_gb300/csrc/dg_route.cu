@@ -1,5 +1,6 @@
 // The router around the experts' products: top-k selection with its weights (dg_moe_route) and their
-// gradient (dg_moe_route_backward), one warp a row, or four rows a warp with few experts.
+// gradient (dg_moe_route_backward). The general way is a row a warp; up to 32 experts take an expert a lane, and
+// many rows of up to 16 four rows a warp (below).
 //
 // Selection. A lane holds VPL experts of the row: consecutive ones where the rows can be read in vectors, else
 // every 32nd, so that a load or store of the warp still covers one piece of the row (E = 510, FP32, 25052 rows:
@@ -19,6 +20,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cfloat>
 #include <climits>
 
@@ -119,17 +121,13 @@ __device__ __forceinline__ void load_bias(const float* bias, int E, int e0, int 
 // v = the fast sigmoid of v + b; -inf where v is that or NaN.
 template <int VPL>
 __device__ __forceinline__ void approximate_sums(float (&v)[VPL], const float (&b)[VPL]) {
-    if constexpr (VPL == 1) {
-        v[0] = v[0] > -INFINITY ? fast_sigmoid(v[0]) + b[0] : -INFINITY;
-    } else {
 #pragma unroll
-        for (int i = 0; i < VPL; i += 2) {
-            const float2 y = __fmul2_rn(make_float2(v[i], v[i + 1]), make_float2(-LOG2_E, -LOG2_E));
-            const float2 d = __fadd2_rn(make_float2(exp2_approx(y.x), exp2_approx(y.y)), make_float2(1.f, 1.f));
-            const float2 s = __fadd2_rn(make_float2(reciprocal_approx(d.x), reciprocal_approx(d.y)), make_float2(b[i], b[i + 1]));
-            v[i] = v[i] > -INFINITY ? s.x : -INFINITY;
-            v[i + 1] = v[i + 1] > -INFINITY ? s.y : -INFINITY;
-        }
+    for (int i = 0; i < VPL; i += 2) {
+        const float2 y = __fmul2_rn(make_float2(v[i], v[i + 1]), make_float2(-LOG2_E, -LOG2_E));
+        const float2 d = __fadd2_rn(make_float2(exp2_approx(y.x), exp2_approx(y.y)), make_float2(1.f, 1.f));
+        const float2 s = __fadd2_rn(make_float2(reciprocal_approx(d.x), reciprocal_approx(d.y)), make_float2(b[i], b[i + 1]));
+        v[i] = v[i] > -INFINITY ? s.x : -INFINITY;
+        v[i + 1] = v[i + 1] > -INFINITY ? s.y : -INFINITY;
     }
 }
 
@@ -583,6 +581,108 @@ route_few_backward_kernel(const T* __restrict__ logits, const int32_t* __restric
     }
 }
 
+// ---- an expert a lane
+//
+// Up to 32 experts: the k largest by k turns of find-and-remove, the lowest lane that holds the largest value
+// winning, and every lane keeps the turn that it won (32 experts, k = 8: 1.7 us for 64 rows and 8.0 for 32768, where
+// the general way takes 2.0 and 10.0). Warps take several rows, the next one's logits on their way.
+template <typename T>
+__global__ void __launch_bounds__(32 * ROUTE_WARPS, 8)
+route_lane_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int32_t* __restrict__ ids,
+                  float* __restrict__ weights, int rows, int E, int k, int sigmoid_scores, int renorm, float scale) {
+    const int lane = threadIdx.x & 31, stride = static_cast<int>(gridDim.x) * ROUTE_WARPS;
+    int t = static_cast<int>(blockIdx.x) * ROUTE_WARPS + static_cast<int>(threadIdx.x >> 5);
+    grid_dependency_wait();
+    grid_launch_dependents();
+    if (t >= rows) return;
+    const bool mine = lane < E;
+    const float b = bias != nullptr && mine ? __ldg(bias + lane) : 0.f;
+    float next = mine ? to_f32(logits[static_cast<size_t>(t) * E + lane]) : -INFINITY;
+    for (; t < rows; t += stride) {
+        const float l = next > -INFINITY ? finite_top(next) : -INFINITY;        // (NaN cannot be selected either)
+        if (t + stride < rows && mine) next = to_f32(logits[static_cast<size_t>(t + stride) * E + lane]);
+        float score = 0.f, total = 1.f, me = l;
+        if (sigmoid_scores) {
+            if (l > -INFINITY) score = sigmoid(l);
+            if (bias != nullptr && l > -INFINITY) me = score + b;
+        } else {
+            const float top = warp_max(l);
+            if (l > -INFINITY) score = __expf(l - top);
+            if (!renorm) total = warp_sum(score);
+        }
+        int place = -1;
+#pragma unroll 4
+        for (int j = 0; j < k; ++j) {
+            const float most = warp_max(me);
+            if (lane == __ffs(__ballot_sync(FULL, me == most && me > -INFINITY)) - 1) {
+                place = j;
+                me = -INFINITY;
+            }
+        }
+        const int picked = __popc(__ballot_sync(FULL, place >= 0));
+        if (renorm) total = warp_sum(place >= 0 ? score : 0.f);
+        const float w = total > 0.f ? score * __frcp_rn(total) : 0.f;
+        const size_t out = static_cast<size_t>(t) * k;
+        if (place >= 0) {
+            ids[out + place] = lane;
+            weights[out + place] = w * scale;
+        }
+        if (lane >= picked && lane < k) {
+            ids[out + lane] = -1;
+            weights[out + lane] = 0.f;
+        }
+    }
+}
+
+// The gradient by expert, as route_few_backward_kernel's.
+template <typename T>
+__global__ void __launch_bounds__(32 * ROUTE_WARPS, 8)
+route_lane_backward_kernel(const T* __restrict__ logits, const int32_t* __restrict__ ids, const float* __restrict__ dweights,
+                           T* __restrict__ dlogits, int rows, int E, int k, int sigmoid_scores, int renorm, float scale) {
+    const int lane = threadIdx.x & 31, stride = static_cast<int>(gridDim.x) * ROUTE_WARPS;
+    int t = static_cast<int>(blockIdx.x) * ROUTE_WARPS + static_cast<int>(threadIdx.x >> 5);
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const bool quotient = renorm || !sigmoid_scores;
+    for (; t < rows; t += stride) {
+        const float x = lane < E ? to_f32(logits[static_cast<size_t>(t) * E + lane]) : -INFINITY;
+        int e = -1;
+        float dw = 0.f;
+        if (lane < k) {
+            e = __ldg(ids + static_cast<size_t>(t) * k + lane);
+            dw = __ldg(dweights + static_cast<size_t>(t) * k + lane) * scale;
+        }
+        const float l = x > -INFINITY ? finite_top(x) : -INFINITY;
+        float add = 0.f, named = 0.f;
+#pragma unroll 4
+        for (int j = 0; j < k; ++j) {
+            const float od = __shfl_sync(FULL, dw, j);
+            if (__shfl_sync(FULL, e, j) == lane) {
+                add += od;
+                named += 1.f;
+            }
+        }
+        const bool counts = l > -INFINITY && (!renorm || named > 0.f);
+        float p = 0.f, inv = 1.f;
+        if (sigmoid_scores) {
+            if (counts) p = sigmoid(l);
+        } else {
+            const float top = warp_max(counts ? l : -FLT_MAX);
+            if (counts) p = __expf(l - top);
+        }
+        const float times = renorm ? named : 1.f;
+        if (quotient) {
+            const float sum = warp_sum(times * p);
+            inv = sum > 0.f ? __frcp_rn(sum) : 0.f;
+        }
+        float out = p * inv;
+        if (quotient) out *= add - times * warp_sum(out * add);
+        else out *= add;
+        if (sigmoid_scores) out *= 1.f - p;
+        if (lane < E) store_one(dlogits + static_cast<size_t>(t) * E + lane, out);
+    }
+}
+
 template <int VPL, typename T>
 bool vector_rows(const void* a, const void* b, int E) {
     constexpr int BYTES = VPL * static_cast<int>(sizeof(T));
@@ -606,6 +706,29 @@ cudaError_t launch_route_backward(const void* logits, const int32_t* ids, const 
                              renorm, scale, vector_rows<VPL, T>(logits, dlogits, E) ? 1 : 0);
 }
 
+// CTAs for rows that warps take several of: the eight that fit an SM, twice (32768 rows of 32 experts: 8.0 us, with
+// half as many 8.4, with a row a warp 8.5).
+int lane_grid(int rows) {
+    DeviceInfo dev;
+    const int most = device_info(&dev) == DG_OK ? 16 * dev.sms : 1 << 20;
+    return std::min(cdiv(rows, ROUTE_WARPS), most);
+}
+
+template <typename T>
+cudaError_t launch_route_lane(const void* logits, const float* bias, int32_t* ids, float* weights, int rows, int E, int k,
+                              int scoring, int renorm, float scale, cudaStream_t stream) {
+    return launch_overlapped(route_lane_kernel<T>, dim3(lane_grid(rows)), dim3(32 * ROUTE_WARPS), stream,
+                             static_cast<const T*>(logits), bias, ids, weights, rows, E, k, scoring, renorm, scale);
+}
+
+template <typename T>
+cudaError_t launch_route_lane_backward(const void* logits, const int32_t* ids, const float* dweights, void* dlogits, int rows,
+                                       int E, int k, int scoring, int renorm, float scale, cudaStream_t stream) {
+    return launch_overlapped(route_lane_backward_kernel<T>, dim3(lane_grid(rows)), dim3(32 * ROUTE_WARPS), stream,
+                             static_cast<const T*>(logits), ids, dweights, static_cast<T*>(dlogits), rows, E, k, scoring,
+                             renorm, scale);
+}
+
 template <int VPL, typename T>
 cudaError_t launch_route_few(const void* logits, const float* bias, int32_t* ids, float* weights, int rows, int E, int k,
                              int scoring, int renorm, float scale, cudaStream_t stream) {
@@ -621,11 +744,11 @@ cudaError_t launch_route_few_backward(const void* logits, const int32_t* ids, co
                              renorm, scale);
 }
 
-// Four rows a warp for up to 8 experts (softmax, k = 2: 1.84 against 1.95 us for 64 rows, 3.3 against 8.7 for 32768),
-// and for up to 16 from this many rows on (k = 4: 2.13 against 1.94 us for 64, 2.36 against 2.42 for 4096, 4.5
-// against 9.0 for 32768); with more, a row's k turns over eight lanes take longer than a whole warp's (32 experts,
-// k = 8: 4.1 against 3.9 us for 8192; the gradient 10.2 against 8.4 for 32768).
-constexpr int FEW_FROM = 4096;
+// Four rows a warp for up to 16 experts from this many rows on, against an expert a lane (softmax, 8 experts, k = 2:
+// 1.9 against 1.8 us for 4096 rows, 2.0 against 2.6 for 8192, 3.3 against 5.6 for 32768; 16 experts, k = 4: 2.4
+// against 2.0, 2.4 against 2.8, 4.5 against 6.4). With more experts a row's k turns over eight lanes take longer
+// than a whole warp's (32 experts, k = 8: 4.1 against 3.4 us for 8192; the gradient 10.2 against 7.2 for 32768).
+constexpr int FEW_FROM = 6144;
 
 // Arguments that both directions share. `need` collects what must not be null.
 dg_status check_route(int type, int T, int E, int k, int scoring) {
@@ -637,15 +760,16 @@ dg_status check_route(int type, int T, int E, int k, int scoring) {
 }
 
 #define DG_ROUTE_VPL(CALL)                                    \
-    if (E <= 32) return CALL(1);                              \
     if (E <= 64) return CALL(2);                              \
     if (E <= 128) return CALL(4);                             \
     if (E <= 256) return CALL(8);                             \
     if (E <= 512) return CALL(16);                            \
     return CALL(32);
 #define DG_ROUTE_FEW(CALL)                                    \
-    if (E <= GROUP) return CALL(1);                           \
-    if (E <= 2 * GROUP && rows >= FEW_FROM) return CALL(2);
+    if (rows >= FEW_FROM) {                                   \
+        if (E <= GROUP) return CALL(1);                       \
+        if (E <= 2 * GROUP) return CALL(2);                   \
+    }
 
 template <typename T>
 cudaError_t route_any(const void* logits, const float* bias, int32_t* ids, float* weights, int rows, int E, int k,
@@ -653,6 +777,7 @@ cudaError_t route_any(const void* logits, const float* bias, int32_t* ids, float
 #define DG_FEW(V) (launch_route_few<V, T>(logits, bias, ids, weights, rows, E, k, scoring, renorm, scale, stream))
     DG_ROUTE_FEW(DG_FEW)
 #undef DG_FEW
+    if (E <= 32) return launch_route_lane<T>(logits, bias, ids, weights, rows, E, k, scoring, renorm, scale, stream);
 #define DG_CALL(V) (launch_route<V, T>(logits, bias, ids, weights, rows, E, k, scoring, renorm, scale, stream))
     DG_ROUTE_VPL(DG_CALL)
 #undef DG_CALL
@@ -664,6 +789,7 @@ cudaError_t route_backward_any(const void* logits, const int32_t* ids, const flo
 #define DG_FEW(V) (launch_route_few_backward<V, T>(logits, ids, dweights, dlogits, rows, E, k, scoring, renorm, scale, stream))
     DG_ROUTE_FEW(DG_FEW)
 #undef DG_FEW
+    if (E <= 32) return launch_route_lane_backward<T>(logits, ids, dweights, dlogits, rows, E, k, scoring, renorm, scale, stream);
 #define DG_CALL(V) (launch_route_backward<V, T>(logits, ids, dweights, dlogits, rows, E, k, scoring, renorm, scale, stream))
     DG_ROUTE_VPL(DG_CALL)
 #undef DG_CALL
