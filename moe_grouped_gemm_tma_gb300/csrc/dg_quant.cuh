@@ -130,20 +130,20 @@ __device__ __forceinline__ float at_most(float v, float ceiling) {
     return d;
 }
 
-// GELU, z Phi(z), by the normal distribution's upper tail: 1 - Phi(m) = P(t) exp(-m^2 / 2), t = 1 / (1 + 0.35 m),
+// GELU, z Phi(z), by the normal distribution's upper tail: 1 - Phi(m) = P(t) exp(-m^2 / 2), t = 1 / (1 + 0.4 m),
 // for 0 <= m <= GELU_END; beyond it the tail is 0 to FP32. P was fitted to that quotient for the smallest largest
-// relative error, which is 5.6e-7 in FP32 arithmetic (the form is Hastings' for the error function, whose published
+// relative error, which is 3.4e-7 in FP32 arithmetic (the form is Hastings' for the error function, whose published
 // coefficients have 1.5e-7 of 1, not of the tail). The two reciprocals of a pair are one.
 constexpr float GELU_END = 14.f;
 __device__ __forceinline__ float2 upper_tail2(float2 m) {
-    const float2 u = __ffma2_rn(m, make_float2(0.35f, 0.35f), make_float2(1.f, 1.f));
+    const float2 u = __ffma2_rn(m, make_float2(0.4f, 0.4f), make_float2(1.f, 1.f));
     const float r = reciprocal_approx(u.x * u.y);
     const float2 t = make_float2(r * u.y, r * u.x);
-    constexpr float P[8] = {-2.7859039619215764e-05f, 0.14027923345565796f, 0.1332964450120926f, 0.15616419911384583f,
-                            -0.017421623691916466f, 0.24108751118183136f, -0.2023855596780777f, 0.04900781065225601f};
-    float2 s = make_float2(P[7], P[7]);
+    constexpr float P[9] = {-1.1998804438917432e-05f, 0.15990442037582397f, 0.15578454732894897f, 0.15842628479003906f, -0.012412778101861477f,
+                            0.2510190010070801f, -0.37372907996177673f, 0.20062635838985443f, -0.039606764912605286f};
+    float2 s = make_float2(P[8], P[8]);
 #pragma unroll
-    for (int i = 6; i >= 0; --i) s = __ffma2_rn(s, t, make_float2(P[i], P[i]));
+    for (int i = 7; i >= 0; --i) s = __ffma2_rn(s, t, make_float2(P[i], P[i]));
     return s;
 }
 
@@ -152,9 +152,10 @@ __device__ __forceinline__ float slope_of(float z, float g) { return z < 0.f ? g
 
 // The slopes of an activation at two BF16 pre-activations, in packed arithmetic where it has a form for that.
 //
-// SILU: p (1 + z (1 - p)), p = 1 / (1 + exp(-z)). z has eight significant bits, so its product with the upper
-// 16 bits of log2(e) is exact and the rest goes in as a factor: the exponential's error is that of the base-2
-// one alone. It is held under 2^126 to keep everything finite.
+// SILU: p (1 + z (1 - p)) with p = 1 / (1 + e), e = exp(-z), as p^2 (1 + (1 + z) e): 1 - p would cancel where p is
+// near 1. z has eight significant bits, so its product with the upper 16 bits of log2(e) is exact and the rest goes
+// in as a factor: the exponential's error is that of the base-2 one alone. It is held under 2^110 to keep
+// everything finite; the slopes beyond that are under 1e-31.
 template <int ACT>
 __device__ __forceinline__ float2 act_slope2(float2 z) {
     const float2 one = make_float2(1.f, 1.f), minus = make_float2(-1.f, -1.f);
@@ -162,15 +163,14 @@ __device__ __forceinline__ float2 act_slope2(float2 z) {
         constexpr float HI = 1.44268798828125f, LO = 7.0526075e-6f * 0.6931471805599453f;   // log2(e), 16 bits; the rest, times ln 2
         z = make_float2(at_least(z.x, -100.f), at_least(z.y, -100.f));       // (0 to FP32 below)
         const float2 t = __fmul2_rn(z, make_float2(-HI, -HI));
-        float2 e = make_float2(exp2_approx(fminf(t.x, 126.f)), exp2_approx(fminf(t.y, 126.f)));
+        float2 e = make_float2(exp2_approx(fminf(t.x, 110.f)), exp2_approx(fminf(t.y, 110.f)));
         e = __ffma2_rn(e, __fmul2_rn(z, make_float2(-LO, -LO)), e);
         const float2 s = __fadd2_rn(e, one);
-        float2 p = make_float2(reciprocal_approx(s.x), reciprocal_approx(s.y));
-        p = __ffma2_rn(__ffma2_rn(__ffma2_rn(e, minus, minus), p, one), p, p);               // Newton: p + (1 - s p) p
-        return __fmul2_rn(p, __ffma2_rn(z, __ffma2_rn(p, minus, one), one));
+        const float2 p = make_float2(reciprocal_approx(s.x), reciprocal_approx(s.y));
+        return __fmul2_rn(p, __fmul2_rn(p, __ffma2_rn(__fadd2_rn(z, one), e, one)));
     }
     if (ACT == DG_ACT_GELU_TANH) {
-        // p + z p (1 - p) y', with y = 2 a z (1 + b z^2) and p its sigmoid; beyond 16 that is 0 or 1 to FP32
+        // p + z p (1 - p) y', with y = 2 a z (1 + b z^2), p its sigmoid and 1 - p = e p; beyond 16 that is 0 or 1 to FP32
         z = make_float2(at_most(at_least(z.x, -16.f), 16.f), at_most(at_least(z.y, -16.f), 16.f));
         const float2 z2 = __fmul2_rn(z, z);
         const float2 y = __fmul2_rn(z, __ffma2_rn(z2, make_float2(2.f * GELU_A * GELU_B, 2.f * GELU_A * GELU_B), make_float2(2.f * GELU_A, 2.f * GELU_A)));
@@ -182,19 +182,15 @@ __device__ __forceinline__ float2 act_slope2(float2 z) {
         const float2 low = __ffma2_rn(y, make_float2(-LOG2_E_REST, -LOG2_E_REST), __ffma2_rn(y, l, __fmul2_rn(t, minus)));
         e = __ffma2_rn(e, __fmul2_rn(low, make_float2(LN2, LN2)), e);
         const float2 s = __fadd2_rn(e, one);
-        float2 p = make_float2(reciprocal_approx(s.x), reciprocal_approx(s.y));
-        p = __ffma2_rn(__ffma2_rn(__ffma2_rn(e, minus, minus), p, one), p, p);
-        return __ffma2_rn(__fmul2_rn(p, __ffma2_rn(p, minus, one)), __fmul2_rn(z, dy), p);
+        const float2 p = make_float2(reciprocal_approx(s.x), reciprocal_approx(s.y));
+        return __ffma2_rn(__fmul2_rn(p, __fmul2_rn(e, p)), __fmul2_rn(z, dy), p);
     }
     if (ACT == DG_ACT_GELU) {
         // Phi(z) + z phi(z): with m = |z| that is g = (P(t) - m / sqrt(2 pi)) exp(-z^2 / 2) below zero, 1 - g above.
-        // z^2 has 16 significant bits; what its product with log2(e) / 2 loses goes in as a factor.
+        // (z^2 is exact, and the rounding of its product with log2(e) / 2 counts only where g is small.)
         const float2 m = make_float2(fminf(fabsf(z.x), GELU_END), fminf(fabsf(z.y), GELU_END));
-        constexpr float L = 0.5f * LOG2_E, LN2 = 0.6931471805599453f;
-        const float2 z2 = __fmul2_rn(m, m), x = __fmul2_rn(z2, make_float2(-L, -L));
-        float2 e = make_float2(exp2_approx(x.x), exp2_approx(x.y));
-        const float2 low = __fadd2_rn(__ffma2_rn(z2, make_float2(-L, -L), __fmul2_rn(x, minus)), __fmul2_rn(z2, make_float2(-0.5f * LOG2_E_REST, -0.5f * LOG2_E_REST)));
-        e = __ffma2_rn(e, __fmul2_rn(low, make_float2(LN2, LN2)), e);
+        const float2 x = __fmul2_rn(__fmul2_rn(m, m), make_float2(-0.5f * LOG2_E, -0.5f * LOG2_E));
+        const float2 e = make_float2(exp2_approx(x.x), exp2_approx(x.y));
         const float2 g = __fmul2_rn(e, __ffma2_rn(m, make_float2(-0.3989422804014327f, -0.3989422804014327f), upper_tail2(m)));
         return make_float2(slope_of(z.x, g.x), slope_of(z.y, g.y));
     }
