@@ -82,8 +82,8 @@ constexpr int STATUS_TIMEOUT = 6;       // DG_DEVICE_TIMEOUT
 enum Mode : int { kNormal = 0, kContiguous = 1, kMasked = 2, kKGrouped = 3, kEpilogue = 4 };
 
 // kEpilogue is the normal layout with bias, activation and residual applied to the tile before it is
-// rounded; everything before that point is the normal layout's. 4096 x 7168 x 2048 takes 60 us without, 65 as it,
-// 76 with bias and silu, and 87 with residual and Z too (199 MB, 30 us of HBM): the tile's end is done by the
+// rounded; everything before that point is the normal layout's. 4096 x 7168 x 2048 takes 60 us without, 67 as it,
+// 75 with bias and silu, and 87 with residual and Z too (199 MB, 30 us of HBM): the tile's end is done by the
 // warps that promote, and the tensor cores wait for them. (Four warps of their own for it, taking the FP32 sums
 // through tensor memory, slow the promotion beside them by as much: 90.6 us.)
 __host__ __device__ constexpr bool normal_layout(int mode) { return mode == kNormal || mode == kEpilogue; }
@@ -432,7 +432,9 @@ __device__ __forceinline__ void epilogue_tile(float (&v)[COLS], const EpiloguePa
 #pragma unroll
     for (int r = 0; r < COLS / 32; ++r) {
         uint4* mine = reinterpret_cast<uint4*>(boxes + r * 2048 + lane * 64);
-        uint4 res[4];
+        // (without a residual zeros are added: branches around whole registers' worth of the tile cost more, 88.7
+        // against 87.3 us at 4096 x 7168 x 2048 with everything, 65 against 67 with nothing)
+        uint4 res[4] = {};
         if (residual) {
             // (boxes past the last column were not copied: whatever is there is not stored either)
 #pragma unroll
@@ -461,17 +463,15 @@ __device__ __forceinline__ void epilogue_tile(float (&v)[COLS], const EpiloguePa
                 v[j + 1] = a.y;
             }
         }
-        if (residual) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const uint32_t x[4] = {res[c].x, res[c].y, res[c].z, res[c].w};
+        for (int c = 0; c < 4; ++c) {
+            const uint32_t x[4] = {res[c].x, res[c].y, res[c].z, res[c].w};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int j = r * 32 + c * 8 + 2 * i;
-                    const float2 s = __fadd2_rn(make_float2(v[j], v[j + 1]), make_float2(bf16_lo(x[i]), bf16_hi(x[i])));
-                    v[j] = s.x;
-                    v[j + 1] = s.y;
-                }
+            for (int i = 0; i < 4; ++i) {
+                const int j = r * 32 + c * 8 + 2 * i;
+                const float2 s = __fadd2_rn(make_float2(v[j], v[j + 1]), make_float2(bf16_lo(x[i]), bf16_hi(x[i])));
+                v[j] = s.x;
+                v[j + 1] = s.y;
             }
         }
     }
@@ -943,7 +943,7 @@ dg_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant
             // (epilogue mode: at the bias, loaded while the tile's first block is on its way; split-K tiles and
             // narrow tiles, whose sums meet elsewhere, add it at the end)
             if constexpr (MODE == kEpilogue && !C::KPAR)
-                if (p.bias != nullptr && !split_k) load_bias<COLS>(accum, p.bias, cstart, p.n);
+                load_bias<COLS>(accum, p.bias, cstart, p.bias != nullptr && !split_k ? p.n : 0);
 
             if constexpr (C::DIRECT_SCALES) {
                 // sfa of this thread's row and the sfb of its (at most two) 128-column blocks, read one K
