@@ -259,19 +259,19 @@ int choose_split(const Spec (&cands)[NC], Spec* sp, int64_t row_blocks, int n, i
 
 // Tile width and split-K of the epilogue mode, by the time that its kernels take: waves of a K block's measured
 // time at that width each (64 columns 0.30 us, 128 0.37, 192 0.47: 0.21 us and 1.37 ns a column), 4 us for the
-// launch and the tile's ends, and for a split, which has to fit in one wave, 4 us more and 20 ns a column for
-// the exchange of the partial sums. It named the fastest of 9 to 12 measured choices for every one of twelve
-// shapes (333 x 2112 x 7168: 192 columns, 4 CTAs a tile, 15.5 us, where 64 columns unsplit take 20.9;
-// 150 x 2048 x 1024: 64 unsplit, 7.0, where 2 CTAs a tile take 8.3).
+// launch and the tile's ends, and for a split, which has to fit in one wave, 1.6 us more and 10.5 ns a column for
+// the exchange of the partial sums (333 x 2112 x 7168: 192 columns, 4 CTAs a tile, 14.1 us, where 64 columns
+// unsplit take 21.3; 150 x 2048 x 1024: 64 unsplit, 7.0, where 2 CTAs a tile take 7.5). Clusters of four are
+// resident on 144 of 152 SMs at most (64 x 6912 x 2048 over 144 CTAs 9.8 us, 64 x 7104 x 2048 over 148 17.9).
 int plan_epilogue(Spec* sp, int64_t row_blocks, int n, int kbs, int sms) {
     int split = 1;
     int64_t best = INT64_MAX;
     for (const Spec& c : kEpilogueSpecs1) {
         const int64_t tiles = row_blocks * cdiv(n, c.bn);
         for (int s = 1; s <= 4; s *= 2) {
-            if (s > 1 && (tiles * s > sms || kbs < 4 * s)) continue;
+            if (s > 1 && (tiles * s > (s == 4 ? sms * 18 / 19 : sms) || kbs < 4 * s)) continue;
             const int64_t waves = s > 1 ? 1 : (tiles + sms - 1) / sms;
-            const int64_t cost = waves * cdiv(kbs, s) * (210000 + 1370 * c.bn) + 4000000 + (s > 1 ? 4000000 + 20000 * c.bn : 0);   // ps
+            const int64_t cost = waves * cdiv(kbs, s) * (210000 + 1370 * c.bn) + 4000000 + (s > 1 ? 1600000 + 10500 * c.bn : 0);   // ps
             if (cost < best) {
                 best = cost;
                 split = s;
@@ -550,10 +550,10 @@ static dg_status gemm_impl(const uint8_t* A, const float* sfa, const uint8_t* B,
         const int col_tiles = cdiv(N, 128);
         decode = M <= 64 && K >= 7168 && col_tiles >= 32 && col_tiles <= 64;
         // With an epilogue the two were measured over M = 1..64, N = 512..24576, K = 128..7168: up to 32 rows and
-        // one wave of column tiles the decode kernel wins (M = 1: 4.0 against 4.5 us at N = 512, K = 128 up to 16
-        // against 31 at 8192 x 7168; M = 20 ties at K <= 512), with more rows from K = 1024 on and up to 32
-        // column tiles, or 64 for a long K (M = 64, 8192 x 7168: 20.5 against 21.6; 7168 x 2048 ties).
-        if (ep) decode = M <= 64 && (M <= 32 ? col_tiles <= dev.sms : K >= 1024 && col_tiles <= (K >= 7168 ? 64 : 32));
+        // one wave of column tiles the decode kernel wins (M = 1: 3.9 against 4.3 us at N = 512, K = 128 up to 15.5
+        // against 24 at 8192 x 7168; M = 20 ties at K <= 512), with more rows from K = 1024 on and up to 32
+        // column tiles (M = 48, 1024 x 4096: 7.1 against 8.0; M = 64, 4096 x 7168 ties, 8192 x 7168 20.4 against 18.7).
+        if (ep) decode = M <= 64 && (M <= 32 ? col_tiles <= dev.sms : K >= 1024 && col_tiles <= 32);
         if (const int v = tune(DG_TUNE_SWAP); v >= 0) decode = (v == 1) && (!ep || M <= 64);
         if (decode) pl = ep ? plan_decode<kEpilogue>(1, M, M, N, kbs, dev.sms) : plan_decode<kNormal>(1, M, M, N, kbs, dev.sms);
     }

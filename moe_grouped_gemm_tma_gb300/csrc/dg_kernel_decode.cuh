@@ -456,16 +456,22 @@ dg_decode_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_consta
                     const int rows_per = BMT / p.split;
                     const int chunks = rows_per * (C::BNT / 4);
                     const uint32_t part_local = smem_u32(smem);
+                    if constexpr (MODE == kEpilogue) {
+                        finish_split<-1, 1>(p, part_local, static_cast<int>(threadIdx.x) - EPI_WARP0 * 32, chunks, EPI_WARPS * 32, [&](int f) {
+                            const int m = srank * rows_per + f / (C::BNT / 4), n4 = (f % (C::BNT / 4)) * 4;
+                            return SplitItem{static_cast<uint32_t>((m * C::BNT + n4) * 4), ti.n0 + n4, static_cast<size_t>(ti.a_row + m) * p.n + ti.n0 + n4,
+                                             m < ti.rows_valid && ti.n0 + n4 < p.n};
+                        });
+                    } else {
                     for (int f = static_cast<int>(threadIdx.x) - EPI_WARP0 * 32; f < chunks; f += EPI_WARPS * 32) {
                         const int m = srank * rows_per + f / (C::BNT / 4);
                         const int n4 = (f % (C::BNT / 4)) * 4;
                         const float4 sum = cluster_sum_v4(part_local + static_cast<uint32_t>((m * C::BNT + n4) * 4), p.split);
                         if (m < ti.rows_valid && ti.n0 + n4 < p.n) {
                             const size_t at = static_cast<size_t>(ti.a_row + m) * p.n + ti.n0 + n4;
-                            float v[4] = {sum.x, sum.y, sum.z, sum.w};
-                            if constexpr (MODE == kEpilogue) epilogue_four(v, p, ti.n0 + n4, at);
-                            st_global_v2(reinterpret_cast<__nv_bfloat16*>(p.d) + at, pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+                            st_global_v2(reinterpret_cast<__nv_bfloat16*>(p.d) + at, pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
                         }
+                    }
                     }
                 }
                 cluster_sync();
