@@ -269,7 +269,7 @@ int plan_epilogue(Spec* sp, int64_t row_blocks, int n, int kbs, int sms) {
     for (const Spec& c : kEpilogueSpecs1) {
         const int64_t tiles = row_blocks * cdiv(n, c.bn);
         for (int s = 1; s <= 4; s *= 2) {
-            if (s > 1 && (tiles * s > (s == 4 ? sms * 18 / 19 : sms) || kbs < 4 * s)) continue;
+            if (s > 1 && (tiles * s > (s == 4 ? sms * 18 / 19 : sms) || kbs < 2 * s)) continue;
             const int64_t waves = s > 1 ? 1 : (tiles + sms - 1) / sms;
             const int64_t cost = waves * cdiv(kbs, s) * (210000 + 1370 * c.bn) + 4000000 + (s > 1 ? 1600000 + 10500 * c.bn : 0);   // ps
             if (cost < best) {
