@@ -471,7 +471,10 @@ route_few_kernel(const T* __restrict__ logits, const float* __restrict__ bias, i
         }
     }
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) v[i] = bias != nullptr && l[i] > -INFINITY ? sigmoid(l[i]) + __ldg(bias + e0 + i) : l[i];
+    for (int i = 0; i < VPL; ++i) {
+        v[i] = bias != nullptr && l[i] > -INFINITY ? sigmoid(l[i]) + __ldg(bias + e0 + i) : l[i];
+        if (!(v[i] > -INFINITY)) v[i] = -INFINITY;          // a NaN of the bias
+    }
 
     const size_t out = static_cast<size_t>(t) * k;
     for (int j = 0; j < k; ++j) {

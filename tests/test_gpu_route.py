@@ -104,6 +104,14 @@ def test_few_experts_and_many_rows(T, E, k):
     check(torch.round(logits), k, bias, scoring="sigmoid")
 
 
+@pytest.mark.parametrize("T,E", [(8195, 7), (8195, 14), (9, 14), (9, 32), (9, 48), (9, 256), (9, 301)])
+def test_bias_that_is_not_finite(T, E):
+    # a NaN or -inf of the bias takes its expert out of the selection, and no other; +inf puts it first
+    bias = torch.zeros(E)
+    bias[0], bias[3], bias[E - 1], bias[E // 2] = math.nan, -math.inf, math.nan, math.inf
+    check(torch.round(make(T, E, E, False) * 4) / 4, min(E, 6), bias, scoring="sigmoid")
+
+
 @pytest.mark.parametrize("E", [48, 256, 301, 510, 1024])
 @pytest.mark.parametrize("levels", [2, 40])
 def test_ties_in_every_layout(E, levels):
