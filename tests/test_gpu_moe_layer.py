@@ -212,3 +212,15 @@ def test_router_feeds_the_layer():
     c["ids"], c["w"] = ids.cpu(), w.cpu()
     check(c)
     assert (run(c)[4] == 0).all()
+
+
+def test_divided_units_repeat_bit_for_bit():
+    # units in many parts finished by one CTA or by all of them together, in turn on one workspace
+    ws = dg.moe_layer_workspace(64, 8, 16, 1152, 768)
+    cases = [make(55, 4, 8, 1152, 128, seed=1), make(3, 2, 4, 1024, 256, seed=2), make(40, 2, 2, 1152, 640, seed=3), make(20, 3, 16, 384, 128, seed=4)]
+    first = [run(c, ws=ws).clone() for c in cases]
+    for c in cases:
+        check(c, ws=ws)
+    for _ in range(10):
+        for c, f in zip(cases, first):
+            assert torch.equal(run(c, ws=ws), f)
