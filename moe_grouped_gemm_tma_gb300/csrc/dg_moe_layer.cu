@@ -8,7 +8,7 @@
 //
 //   * Split. A stage is 256 weight rows x one 128-wide K block, 32 KB. The stages of a phase (phase 1: W13,
 //     phase 2: W2) form a line, unit after unit, and CTA c of G takes the c-th G-th of it, whatever the
-//     number of met experts: every SM streams the same bytes, to one stage. Parts of a unit that the cuts
+//     number of met experts: every SM streams the same bytes, to one stage (a small layer's: to a few). Parts of a unit that the cuts
 //     divide are summed in the order of the CTAs, so the result does not depend on timing.
 //   * Order. The met experts' chunks are halved, and the lines are: phase 1 of the first half, phase 1 of the
 //     second, phase 2 of the first, phase 2 of the second. The hidden activations of one half are finished
@@ -26,7 +26,7 @@
 //     per gathered row; after the last grid barrier all CTAs sum each token's experts, weighted, in order.
 //
 // Measured (hidden 7168, intermediate 2048): 64 tokens on 16 experts, 705 MB of weights, 147 us where the weights
-// alone are 105; 1 token on 8 experts 63 us of 52.5. What is left: 9 us until the tokens are quantised (the
+// alone are 105; 1 token on 8 experts 62 us of 52.5. What is left: 9 us until the tokens are quantised (the
 // ring fills meanwhile), 3 us for each grid barrier, 7 us for the output of 64 tokens, and HBM at 86% between. A
 // small layer (5 tokens, 8 experts of 1024 x 384) takes 17.5 us for 1.4 of weights: tables 2 us, three grid
 // barriers of 2.2, and two products' and one finisher's latency of 2 each.
@@ -97,7 +97,7 @@ struct MlCfg {
     // The token scales of a stage live until it is promoted: the ring and the accumulators can hold that
     // many stages between the two, so with two more no slot is rewritten before it has been read.
     static constexpr int SLOTS = 6 + NACC + 2;
-    static constexpr int TABLES = 4 * ML_MAX_A + 4 * ML_MAX_A + ML_MAX_ROWS + 4 * 4 * (ML_MAX_CTAS + 1);
+    static constexpr int TABLES = 4 * ML_MAX_A + 4 * ML_MAX_A + ML_MAX_ROWS + 4 * 4 * (ML_MAX_CTAS + 1) + 128;
     static constexpr int STATIC_RESERVE = TABLES + SLOTS * NT * 4 + 768;
     static constexpr int STAGES_FIT = ring_stages(STAGE_BYTES, 0, 0, STATIC_RESERVE);
     static constexpr int STAGES = STAGES_FIT > 6 ? 6 : STAGES_FIT;
@@ -182,6 +182,14 @@ __device__ __forceinline__ uint32_t pack_chunk(int e, int off, int n) {
     return static_cast<uint32_t>(e) | (static_cast<uint32_t>(off) << 10) | (static_cast<uint32_t>(n - 1) << 22);
 }
 
+// The lines: phase 1 of the first half of the chunks, of the second half; phase 2 of the first, of the second.
+struct Line {
+    int c0, nc;            // chunks
+    int kbs, blocks;       // K blocks of a unit; units per chunk
+    int total;             // stages
+    int sharers;           // CTAs that share them
+};
+
 template <int NT>
 struct Shared {
     uint64_t full_w[MlCfg<NT>::STAGES], full_t[MlCfg<NT>::STAGES], empty[MlCfg<NT>::STAGES];   // weights, tokens
@@ -196,25 +204,28 @@ struct Shared {
     uint32_t row_of[ML_MAX_A];                  // gathered row of an assignment (t * k + j) | chunk << 16, or NO_ROW
     uint8_t token[ML_MAX_ROWS];                 // token of a gathered row
     uint32_t share[4][ML_MAX_CTAS + 1];         // first stage of each CTA's share of each line
-};
-
-// The lines: phase 1 of the first half of the chunks, of the second half; phase 2 of the first, of the second.
-struct Line {
-    int c0, nc;            // chunks
-    int kbs, blocks;       // K blocks of a unit; units per chunk
-    int total;             // stages
+    Line line[4];
 };
 
 // Chunks of the first "half", five eighths: the second's phase 1 has to hide the finishing of the first's units,
 // and the first's phase 2, which is half as long per chunk, that of the second's. Where half of phase 1 streams for
-// less than the 8 us that its units take to be finished and seen by all (11 stages a CTA), one half is all: a second one only adds a barrier (5 tokens, 8
-// experts of 1024 x 384: 25 us with halves, 21 without; 1 token, 8 experts of 7168 x 2048: 70 and 76).
+// less than the 8 us that its units take to be finished and seen by all (11 stages a CTA), one half is all: a second
+// one only adds a barrier (5 tokens, 8 experts of 1024 x 384: 25 us with halves, 21 without; 1 token, 8 experts of
+// 7168 x 2048: 70 and 76).
 __device__ __forceinline__ int first_half(const MoeParams& p, int chunks) {
     const int stages = chunks * (p.I / 128) * (p.H / 128);
     return stages >= 22 * static_cast<int>(gridDim.x) ? (chunks * 5 + 7) / 8 : chunks;
 }
 
-__device__ __forceinline__ Line line_of(const MoeParams& p, int chunks, int l) {
+// a / b for 0 <= a < 2^20, 0 < b: half a unit above a is further from the next quotient than the rounding reaches
+__device__ __forceinline__ int small_quotient(int a, int b) { return static_cast<int>((static_cast<float>(a) + 0.5f) * reciprocal_approx(static_cast<float>(b))); }
+
+// A line and the CTAs that share it. Where there are at least as many CTAs as units, a whole number of them takes each
+// unit, so that a CTA has one segment and a unit as few parts as may be, unless that leaves so many CTAs out that the
+// others stream six stages more than an even share (44 tokens, 5 experts of 1536 x 768: 36.5 -> 28.8 us, 64 tokens, 8
+// of 2048 x 1024: 36.9 -> 29.8, one token, 8 of 7168 x 2048: 63.1 -> 62.2). With many rows a phase-2 unit is for two
+// CTAs at most: every part is written and read again, in FP32 (as many as there are: 29.8 us for the first of these).
+__device__ __forceinline__ Line make_line(const MoeParams& p, int chunks, int l) {
     Line n;
     const int half = first_half(p, chunks);
     n.c0 = (l & 1) ? half : 0;
@@ -222,23 +233,29 @@ __device__ __forceinline__ Line line_of(const MoeParams& p, int chunks, int l) {
     n.kbs = (l < 2 ? p.H : p.I) / 128;
     n.blocks = l < 2 ? p.I / 128 : (p.H + 255) / 256;
     n.total = n.nc * n.blocks * n.kbs;
+    n.sharers = min(n.total, static_cast<int>(gridDim.x));
+    const int units = n.nc * n.blocks, ctas = static_cast<int>(gridDim.x);
+    if (units > 0 && units <= ctas) {
+        int m = min(n.kbs, small_quotient(ctas, units));
+        if (l >= 2 && p.T * p.k >= 64) m = min(m, 2);
+        if ((small_quotient(n.kbs + m - 1, m) - 6) * ctas <= n.total) n.sharers = units * m;
+    }
     return n;
 }
 
-// CTAs that share a line (every one of them at least one stage, so that no CTA between two parts of a unit is
-// empty), where a CTA's share starts, and whose share a stage is in. The host keeps total * CTAs in 32 bits.
-__device__ __forceinline__ unsigned sharers(int total) { return min(static_cast<unsigned>(total), gridDim.x); }
-__device__ __forceinline__ unsigned share_start(int total, unsigned cta) {
-    const unsigned n = sharers(total);
-    return cta >= n ? total : static_cast<unsigned>(total) * cta / n;
+// Where a CTA's share of a line starts, and whose share a stage is in. Every sharer has at least one stage, so no CTA
+// between two parts of a unit is empty. The host keeps total * CTAs in 32 bits.
+__device__ __forceinline__ unsigned share_start(const Line& n, unsigned cta) {
+    const unsigned s = static_cast<unsigned>(n.sharers);
+    return cta >= s ? n.total : static_cast<unsigned>(n.total) * cta / s;
 }
-__device__ __forceinline__ int cta_of(unsigned pos, int total) {
-    return static_cast<int>(((pos + 1) * sharers(total) - 1) / static_cast<unsigned>(total));
+__device__ __forceinline__ int cta_of(unsigned pos, const Line& n) {
+    return static_cast<int>(((pos + 1) * static_cast<unsigned>(n.sharers) - 1) / static_cast<unsigned>(n.total));
 }
 // Parts that a unit of the line can have at most.
 __device__ __forceinline__ int most_parts(const Line& n) {
     if (n.total == 0) return 1;
-    const int least = static_cast<int>(static_cast<unsigned>(n.total) / sharers(n.total));
+    const int least = static_cast<int>(static_cast<unsigned>(n.total) / static_cast<unsigned>(n.sharers));
     return (n.kbs - 1 + least - 1) / least + 1;
 }
 
@@ -247,7 +264,7 @@ __device__ __forceinline__ int most_parts(const Line& n) {
 // two segments of it. (55 tokens, 8 experts of 1152 x 128, nine parts and 28 columns a unit: the last CTA alone takes
 // 13 us for them, the layer 33.6 us; together 4, and 23.9.) The promoting warps count their parts themselves, so that no CTA waits for another's finishers.
 __device__ __forceinline__ bool finished_together(const Line& ln, int n, int parts) {
-    return parts > 2 && n > 4 && ln.total < static_cast<int>(gridDim.x) * ln.kbs;
+    return parts > 2 && n > 4 && ln.total < ln.sharers * ln.kbs;
 }
 
 // What a CTA does of one unit: stages [kb0, kb0 + nkb) of unit `unit`, for one chunk of an expert's tokens.
@@ -302,7 +319,7 @@ __device__ __forceinline__ bool for_segments(const MoeParams& p, const Shared<NT
 #pragma unroll 1
     for (int l = 0; l < 2; ++l) {
         if (!enter(l)) return false;
-        const Line ln = line_of(p, s.chunks, l);
+        const Line& ln = s.line[l];
         const int hi = static_cast<int>(s.share[l][cta + 1]);
         for (int pos = static_cast<int>(s.share[l][cta]); pos < hi;) {
             const Seg g = make_seg<1>(p, ln, s.chunk, pos, hi);
@@ -313,7 +330,7 @@ __device__ __forceinline__ bool for_segments(const MoeParams& p, const Shared<NT
 #pragma unroll 1
     for (int l = 2; l < 4; ++l) {
         if (!enter(l)) return false;
-        const Line ln = line_of(p, s.chunks, l);
+        const Line& ln = s.line[l];
         const int hi = static_cast<int>(s.share[l][cta + 1]);
         for (int pos = static_cast<int>(s.share[l][cta]); pos < hi;) {
             const Seg g = make_seg<2>(p, ln, s.chunk, pos, hi);
@@ -388,6 +405,7 @@ __device__ void make_tables(const MoeParams& p, Shared<NT>& s, uint8_t* scratch)
             rows += __shfl_sync(FULL_MASK, r, 31);
             chunks += __shfl_sync(FULL_MASK, c, 31);
         }
+        if (lane < 4) s.line[lane] = make_line(p, chunks, lane);
         if (lane == 0) {
             s.chunks = chunks;
             s.rows = rows;
@@ -410,8 +428,8 @@ __device__ void make_tables(const MoeParams& p, Shared<NT>& s, uint8_t* scratch)
     }
     for (int i = tid; i < 4 * static_cast<int>(gridDim.x + 1); i += ML_THREADS) {
         const int l = i / static_cast<int>(gridDim.x + 1), c = i - l * static_cast<int>(gridDim.x + 1);
-        const Line n = line_of(p, s.chunks, l);
-        s.share[l][c] = n.total ? share_start(n.total, static_cast<unsigned>(c)) : 0u;
+        const Line& n = s.line[l];
+        s.share[l][c] = n.total ? share_start(n, static_cast<unsigned>(c)) : 0u;
     }
 }
 
@@ -422,7 +440,7 @@ __device__ void make_tables(const MoeParams& p, Shared<NT>& s, uint8_t* scratch)
 // longer than for its loads (6 us for one token). The sources are worked out before that barrier.
 template <int NT>
 __device__ __forceinline__ void sum_output(const MoeParams& p, const Shared<NT>& s, int first, bool ok, volatile int* abort_flag, int lane) {
-    const Line la = line_of(p, s.chunks, 2), lb = line_of(p, s.chunks, 3);
+    const Line &la = s.line[2], &lb = s.line[3];
     const int pa = most_parts(la), pb = most_parts(lb);
     const int base_b = lb.nc ? static_cast<int>((s.chunk[la.nc] >> 10) & 0xfffu) : s.rows;
     const size_t width = static_cast<size_t>(la.blocks) * 256;
@@ -446,9 +464,9 @@ __device__ __forceinline__ void sum_output(const MoeParams& p, const Shared<NT>&
                 weight = __ldg(p.weights + t * p.k + j0 + lane);
                 const int row = static_cast<int>(where & 0xffffu), chunk = static_cast<int>(where >> 16);
                 const bool b = chunk >= la.nc;
-                const int nc = b ? lb.nc : la.nc, total = b ? lb.total : la.total;
-                const unsigned u0 = static_cast<unsigned>((blk >> 1) * nc + chunk - (b ? la.nc : 0)) * la.kbs;
-                parts = cta_of(u0 + la.kbs - 1, total) - cta_of(u0, total) + 1;
+                const Line& ln = b ? lb : la;
+                const unsigned u0 = static_cast<unsigned>((blk >> 1) * ln.nc + chunk - (b ? la.nc : 0)) * la.kbs;
+                parts = cta_of(u0 + la.kbs - 1, ln) - cta_of(u0, ln) + 1;
                 at = b ? base_b * pa + (row - base_b) * pb : row * pa;
             }
             const int most = static_cast<int>(__reduce_max_sync(FULL_MASK, static_cast<unsigned>(parts))) * here;
@@ -673,7 +691,7 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap map_w13, const __grid_const
             uint32_t issued = 0, issued_parity = 0;
             const bool ok = for_segments<NT>(p, s, [&](int l) {
                 if (l == 1) return true;
-                if (l == 3 && first_half(p, s.chunks) == s.chunks) return true;
+                if (l == 3 && s.line[1].nc == 0) return true;
                 const bool got = wait_bounded(&s.go[l == 0 ? 0 : l - 1], 0, abort_flag, p.status, p.wait_limit_ns);
                 fence_proxy_async_all();        // what other CTAs wrote before the barrier is read by TMA
                 return __all_sync(FULL_MASK, got) != 0;
@@ -714,7 +732,7 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap map_w13, const __grid_const
                 unsigned top = ld_acquire(p.barrier) & 0x80000000u;
 #pragma unroll 1
                 for (int b = 0; b < ML_BARRIERS; ++b) {
-                    if (b == 2 && first_half(p, s.chunks) == s.chunks) continue;   // no second half
+                    if (b == 2 && s.line[1].nc == 0) continue;   // no second half
                     wait_bounded(&s.done[b], 0, abort_flag, p.status, p.wait_limit_ns);
                     const bool got = grid_barrier(p.barrier, top, abort_flag, p.status, p.wait_limit_ns);
                     top ^= 0x80000000u;
@@ -780,7 +798,7 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap map_w13, const __grid_const
                 }
                 const unsigned u0 = static_cast<unsigned>(g.unit) * ln.kbs;
                 const bool divided = g.nkb < ln.kbs;
-                const int c_lo = divided ? cta_of(u0, ln.total) : cta, c_hi = divided ? cta_of(u0 + ln.kbs - 1, ln.total) : cta;
+                const int c_lo = divided ? cta_of(u0, ln) : cta, c_hi = divided ? cta_of(u0 + ln.kbs - 1, ln) : cta;
                 const int parts = c_hi - c_lo + 1;
                 // A divided unit is finished by the CTA whose part comes last, adding the parts in order, or by all of
                 // them together, each a share of the columns.
@@ -980,8 +998,8 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap map_w13, const __grid_const
                     if (lane == 0) {
                         if (g.nkb < ln.kbs) {
                             const unsigned u0 = static_cast<unsigned>(g.unit) * ln.kbs;
-                            const int c_lo = cta_of(u0, ln.total);
-                            if (finished_together(ln, g.n, cta_of(u0 + ln.kbs - 1, ln.total) - c_lo + 1)) red_add_release(p.count + l * ML_MAX_CTAS + c_lo, 1u);
+                            const int c_lo = cta_of(u0, ln);
+                            if (finished_together(ln, g.n, cta_of(u0 + ln.kbs - 1, ln) - c_lo + 1)) red_add_release(p.count + l * ML_MAX_CTAS + c_lo, 1u);
                         }
                         mbar_arrive(&s.part_full[part.stage]);
                     }
@@ -991,8 +1009,8 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap map_w13, const __grid_const
                     if (ok) promote(g, sb, g.two ? sb + ln.kbs : sb);
                     // the unit's (part of the) products, by gathered row
                     const int parts = most_parts(ln);
-                    const int at = g.kb0 == 0 ? 0 : cta - cta_of(static_cast<unsigned>(g.unit) * ln.kbs, ln.total);
-                    const Line first = line_of(p, s.chunks, 2);
+                    const int at = g.kb0 == 0 ? 0 : cta - cta_of(static_cast<unsigned>(g.unit) * ln.kbs, ln);
+                    const Line& first = s.line[2];
                     const int base = l == 2 ? 0 : static_cast<int>((s.chunk[first.nc] >> 10) & 0xfffu);
                     const int before = l == 2 ? 0 : base * most_parts(first);
                     const size_t width = static_cast<size_t>(ln.blocks) * 256;
