@@ -152,8 +152,8 @@ __device__ __forceinline__ float slope_of(float z, float g) { return z < 0.f ? g
 
 // The slopes of an activation at two BF16 pre-activations, in packed arithmetic where it has a form for that.
 //
-// SILU: p (1 + z (1 - p)) with p = 1 / (1 + e), e = exp(-z), as p^2 (1 + (1 + z) e): 1 - p would cancel where p is
-// near 1. z has eight significant bits, so its product with the upper 16 bits of log2(e) is exact and the rest goes
+// SILU: p (1 + z (1 - p)) with p = 1 / (1 + e), e = exp(-z), and 1 - p = e p, which does not cancel where p is near
+// 1. z has eight significant bits, so its product with the upper 16 bits of log2(e) is exact and the rest goes
 // in as a factor: the exponential's error is that of the base-2 one alone. It is held under 2^110 to keep
 // everything finite; the slopes beyond that are under 1e-31.
 template <int ACT>
@@ -167,7 +167,7 @@ __device__ __forceinline__ float2 act_slope2(float2 z) {
         e = __ffma2_rn(e, __fmul2_rn(z, make_float2(-LO, -LO)), e);
         const float2 s = __fadd2_rn(e, one);
         const float2 p = make_float2(reciprocal_approx(s.x), reciprocal_approx(s.y));
-        return __fmul2_rn(p, __fmul2_rn(p, __ffma2_rn(__fadd2_rn(z, one), e, one)));
+        return __fmul2_rn(p, __ffma2_rn(__fmul2_rn(z, e), p, one));
     }
     if (ACT == DG_ACT_GELU_TANH) {
         // p + z p (1 - p) y', with y = 2 a z (1 + b z^2), p its sigmoid and 1 - p = e p; beyond 16 that is 0 or 1 to FP32
