@@ -93,6 +93,7 @@ __device__ __forceinline__ float abs_max(float a, float b, float c) {
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
+// The hardware's base-2 exponential and reciprocal, good to an ulp or two of FP32.
 __device__ __forceinline__ float exp2_approx(float t) {
     float e;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
@@ -105,11 +106,8 @@ __device__ __forceinline__ float reciprocal_approx(float v) {
     return r;
 }
 
-// 1 / (1 + exp(-z)) with the hardware's base-2 exponential and reciprocal, each good to an ulp or two of FP32;
-// every use ends in BF16 or e4m3. Saturates to 0 and 1 without NaN; NaN stays.
 constexpr float LOG2_E = 1.4426950408889634f;
 constexpr float LOG2_E_REST = 1.925963e-8f;       // log2(e) - float(log2(e))
-__device__ __forceinline__ float fast_sigmoid(float z) { return reciprocal_approx(1.f + exp2_approx(-LOG2_E * z)); }
 
 // sqrt(2 / pi) and the cubic coefficient of the tanh form of GELU, z (1 + tanh(y)) / 2 with
 // y = GELU_A (z + GELU_B z^3); (1 + tanh(y)) / 2 = sigmoid(2 y).
