@@ -56,6 +56,18 @@ void dg_tuning_reset(void);
  */
 dg_status dg_testing_arm_wait_timeout(uint64_t wait_limit_ns);
 
+/*
+ * The same for other waits: what the armed launch leaves out, so that the wait for it runs out. A launch that has
+ * no such step only takes the short limit.
+ */
+enum {
+    DG_FAULT_FIRST_FILL = 1, /* the first pipeline stage (what dg_testing_arm_wait_timeout arms) */
+    DG_FAULT_RESIDUAL = 2    /* dg_gemm_fp8_nt_epilogue: the copies of the residual, in tiles that are not split along K */
+};
+
+/* Arms a fault for the next launch as above. DG_INVALID_ARG for an unknown fault, or a limit of 0 or from 2^60 ns on. */
+dg_status dg_testing_arm_fault(int fault, uint64_t wait_limit_ns);
+
 #ifdef __cplusplus
 }
 #endif

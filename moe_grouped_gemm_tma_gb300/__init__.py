@@ -26,6 +26,7 @@ __all__ = [
     "epilogue_backward_workspace", "moe_layer_workspace", "ACTIVATIONS", "SCORES",
     "dg_device_status", "dg_status_string", "scale_shapes", "library_path",
     "TUNE_KNOBS", "dg_tuning_set", "dg_tuning_get", "dg_tuning_reset", "tuning", "dg_testing_arm_wait_timeout",
+    "FAULTS", "dg_testing_arm_fault",
 ]
 
 _lock = threading.Lock()
@@ -85,6 +86,8 @@ def load(build_if_missing: bool = True):
             L.dg_tuning_reset.restype = None
             L.dg_testing_arm_wait_timeout.argtypes = [ctypes.c_uint64]
             L.dg_testing_arm_wait_timeout.restype = I
+            L.dg_testing_arm_fault.argtypes = [I, ctypes.c_uint64]
+            L.dg_testing_arm_fault.restype = I
             L.dg_status_string.argtypes = [I]
             L.dg_status_string.restype = ctypes.c_char_p
             for f in ("dg_gemm_fp8_nt", "dg_gemm_fp8", "dg_gemm_fp8_nt_ue8m0", "dg_gemm_fp8_nt_ue8m0_packed",
@@ -539,3 +542,13 @@ def dg_testing_arm_wait_timeout(wait_limit_ns: int) -> None:
     """Test hook: the next launch of the main kernel bounds its waits by ``wait_limit_ns`` and leaves its
     first pipeline stage unfilled, so that a wait runs out and the kernel reports DG_DEVICE_TIMEOUT."""
     _check(load().dg_testing_arm_wait_timeout(int(wait_limit_ns)), "dg_testing_arm_wait_timeout")
+
+
+# What an armed launch leaves out (include/dg_tuning.h).
+FAULTS = {"first_fill": 1, "residual": 2}
+
+
+def dg_testing_arm_fault(fault, wait_limit_ns: int) -> None:
+    """Test hook: the next launch bounds its waits by ``wait_limit_ns`` and leaves out what ``fault`` names (a
+    name of FAULTS or its number), so that the wait for it runs out and the kernel reports DG_DEVICE_TIMEOUT."""
+    _check(load().dg_testing_arm_fault(FAULTS[fault] if isinstance(fault, str) else int(fault), int(wait_limit_ns)), "dg_testing_arm_fault")

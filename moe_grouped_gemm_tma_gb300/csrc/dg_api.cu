@@ -28,7 +28,7 @@ namespace {
 // Tuning knobs (dg_tuning.h) and the armed test fault. The environment is read once, at load, and only
 // when DG_TUNING=1.
 std::atomic<int> g_tune[DG_TUNE_COUNT];
-std::atomic<unsigned long long> g_armed_wait_fault{0};
+std::atomic<unsigned long long> g_armed_fault{0};   // wait limit * 8 + fault
 
 struct TuneInit {
     TuneInit() {
@@ -47,9 +47,10 @@ int tune(int knob) {
     return (knob >= 0 && knob < DG_TUNE_COUNT) ? g_tune[knob].load(std::memory_order_relaxed) : DG_TUNE_AUTO;
 }
 
-unsigned long long take_armed_wait_fault() {
-    if (g_armed_wait_fault.load(std::memory_order_relaxed) == 0) return 0;
-    return g_armed_wait_fault.exchange(0);
+ArmedFault take_armed_fault() {
+    if (g_armed_fault.load(std::memory_order_relaxed) == 0) return {0, 0};
+    const unsigned long long armed = g_armed_fault.exchange(0);
+    return {static_cast<int>(armed & 7), armed >> 3};
 }
 
 namespace {
@@ -653,11 +654,13 @@ void dg_tuning_reset(void) {
     for (auto& k : g_tune) k.store(DG_TUNE_AUTO);
 }
 
-dg_status dg_testing_arm_wait_timeout(uint64_t wait_limit_ns) {
-    if (wait_limit_ns == 0) return DG_INVALID_ARG;
-    g_armed_wait_fault.store(static_cast<unsigned long long>(wait_limit_ns));
+dg_status dg_testing_arm_fault(int fault, uint64_t wait_limit_ns) {
+    if (fault < DG_FAULT_FIRST_FILL || fault > DG_FAULT_RESIDUAL || wait_limit_ns == 0 || wait_limit_ns >> 60) return DG_INVALID_ARG;
+    g_armed_fault.store(static_cast<unsigned long long>(wait_limit_ns) << 3 | static_cast<unsigned>(fault));
     return DG_OK;
 }
+
+dg_status dg_testing_arm_wait_timeout(uint64_t wait_limit_ns) { return dg_testing_arm_fault(DG_FAULT_FIRST_FILL, wait_limit_ns); }
 
 dg_status dg_device_status(cudaStream_t stream) {
     DeviceInfo dev;

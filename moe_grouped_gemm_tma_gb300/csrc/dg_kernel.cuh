@@ -56,6 +56,7 @@
 
 #include "dg_ptx.cuh"
 #include "dg_quant.cuh"
+#include "dg_tuning.h"
 
 namespace dg {
 
@@ -111,8 +112,7 @@ struct Params {
     int sf_words;              // block-scaled, packed: int32 words per scale row, ceil(kbs / 4)
     int l2_hint;               // normal layout, long K: A loads evict-last, B loads evict-first in L2
     unsigned long long wait_limit_ns;  // bound of every wait (0 = WAIT_LIMIT_NS); tests shorten it
-    int fault_skip_first_fill;  // test only (0 in every product call): the producer leaves its first
-                                // stage unfilled, so the MMA issuer's wait on it runs out
+    int fault;                 // test only (0 in every product call): DG_FAULT_* (dg_tuning.h), what is left out so that a wait runs out
     int kb_off[MAX_KGROUPS + 1];  // k-grouped: first K block of each expert, kb_off[G] = sumK/128
 };
 
@@ -673,7 +673,7 @@ dg_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant
             uint32_t phase = 0;
             uint32_t issued = 0, issued_parity = 0;   // per-stage bits, for the abort drain
             bool ok = true;
-            bool skip_fill = p.fault_skip_first_fill != 0;   // test only: leave the first stage empty
+            bool skip_fill = p.fault == DG_FAULT_FIRST_FILL;   // test only: leave the first stage empty
             // L2 policies for the long-K normal layout: a band's A row blocks are read again by the next
             // round of tiles, B's column blocks only by tiles in flight at the same time
             const uint64_t pol_a = policy_evict_last(), pol_b = policy_evict_first();
@@ -976,7 +976,7 @@ dg_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant
                 if constexpr (MODE == kEpilogue) {
                     if (residual_on) {
                         rpending = true;
-                        if (lane == 0) {
+                        if (lane == 0 && p.fault != DG_FAULT_RESIDUAL) {
                             bulk_wait_read_n<0>();
                             const int boxes = min(COLS / 32, (p.n - cstart + 31) / 32);
                             mbar_arrive_expect_tx(&residual_bar[ew], static_cast<uint32_t>(boxes) * 2048u);
@@ -1245,8 +1245,11 @@ dg_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant
                 bool got = true;
                 if (residual_on) {
                     got = wait_bounded(&residual_bar[ew], rphase, abort_flag, p.status, p.wait_limit_ns);
-                    rphase ^= 1u;
-                    rpending = false;
+                    // (a copy whose wait gave up is still on its way: it stays pending, in its phase, for the drain below)
+                    if (got) {
+                        rphase ^= 1u;
+                        rpending = false;
+                    }
                 }
                 if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
                 if (!residual_on && p.z != nullptr) {

@@ -41,9 +41,12 @@ int decode_cluster_capacity(int split, int sms);
 // Tuning knobs (dg_tuning.h): the knob's value, or DG_TUNE_AUTO (-1) for the automatic choice.
 int tune(int knob);
 
-// The one-shot wait-limit fault armed by dg_testing_arm_wait_timeout (0 when none is armed); taking it
-// disarms it, so exactly one launch carries it.
-unsigned long long take_armed_wait_fault();
+// The one-shot fault armed by dg_testing_arm_fault (fault 0 when none is armed); taking it disarms it.
+struct ArmedFault {
+    int fault;
+    unsigned long long wait_limit_ns;
+};
+ArmedFault take_armed_fault();
 
 // Programmatic dependent launch is on unless the DG_TUNE_PDL knob is 0.
 inline bool pdl_enabled() { return tune(DG_TUNE_PDL) != 0; }
@@ -135,9 +138,9 @@ cudaError_t launch(const Launch& L) {
         cfg.numAttrs += 1;
     }
     typename ParamsOf<MODE>::type prm = L.params;
-    if (const unsigned long long ns = take_armed_wait_fault()) {
-        prm.wait_limit_ns = ns;
-        prm.fault_skip_first_fill = 1;
+    if (const ArmedFault f = take_armed_fault(); f.fault != 0) {
+        prm.wait_limit_ns = f.wait_limit_ns;
+        prm.fault = f.fault;
     }
     return cudaLaunchKernelEx(&cfg, kern, L.tmap_a, L.tmap_b, L.tmap_d, prm);
 }
