@@ -48,8 +48,8 @@ void dg_tuning_reset(void);
 /*
  * Test hook for the failure path. Arms a one-shot fault for the next call that launches the main
  * block-scaled kernel (the normal GEMM with M > 128 and no split, the m-grouped layouts, the weight
- * gradients): that launch bounds every device wait by wait_limit_ns (> 0) instead of the usual second,
- * and its TMA producer leaves its first pipeline stage unfilled. The MMA issuer's wait on that stage
+ * gradients) or the expert layer: that launch bounds every device wait by wait_limit_ns (> 0) instead
+ * of the usual second, and its TMA producer leaves its first pipeline stage unfilled. The MMA issuer's wait on that stage
  * then runs out: the kernel records DG_DEVICE_TIMEOUT, drains its in-flight copies and MMAs, frees its
  * tensor memory and returns, with its output unspecified. Nothing faults; dg_device_status() reports
  * the timeout. Product calls never arm it. DG_INVALID_ARG when wait_limit_ns is 0.

@@ -85,7 +85,7 @@ struct MoeParams {
     unsigned* count;       // [phase-1 line][CTA]: parts of the unit that the CTA's share ends in
     int* status;
     int T, k, E, H, I, rows_cap, act;
-    unsigned long long wait_limit_ns;
+    unsigned long long wait_limit_ns;   // bound of every wait (0 = WAIT_LIMIT_NS); tests shorten it
 };
 
 template <int NT>
@@ -1187,6 +1187,7 @@ dg_status dg_moe_layer(const void* x, const int32_t* ids, const float* weights, 
     p.I = I;
     p.rows_cap = rows_cap(T, k, E);
     p.act = act;
+    p.wait_limit_ns = take_armed_fault().wait_limit_ns;
     CUtensorMap w13, w2, mx, mh;
     if (make_operand_map(&w13, W13, static_cast<int64_t>(E) * 2 * I, H, 128) != DG_OK ||
         make_operand_map(&w2, W2, static_cast<int64_t>(E) * H, I, 128) != DG_OK ||

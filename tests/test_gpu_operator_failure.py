@@ -14,6 +14,7 @@ import torch
 import moe_grouped_gemm_tma_gb300 as dg
 from moe_grouped_gemm_tma_gb300 import inputs as I
 from tests.gpu_util import bf16_bits, dev, sentinel_bf16
+from tests.test_gpu_moe_layer import make as make_layer, run as run_layer
 
 pytestmark = pytest.mark.gpu
 
@@ -70,6 +71,16 @@ def test_an_epilogue_product_whose_operands_do_not_come(M, split, tune):
     got = [bf16_bits(t) for t in call()]
     assert dg.dg_device_status() == 0
     assert all((a == b).all() for a, b in zip(got, want))
+
+
+def test_an_armed_fault_is_spent_by_the_expert_layer():
+    # not left for a later launch of another kind
+    c = make_layer(3, 2, 4, 256, 128, seed=1)
+    call = epilogue_call(300, 520, 1024)
+    dg.dg_testing_arm_fault("residual", 1_000_000_000)
+    run_layer(c)                                      # (has no residual copy: it runs as usual)
+    call()
+    assert dg.dg_device_status() == 0
 
 
 def test_arming_refuses():
