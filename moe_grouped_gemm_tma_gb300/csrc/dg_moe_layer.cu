@@ -86,6 +86,7 @@ struct MoeParams {
     int* status;
     int T, k, E, H, I, rows_cap, act;
     unsigned long long wait_limit_ns;   // bound of every wait (0 = WAIT_LIMIT_NS); tests shorten it
+    int fault;                          // test only (0 in every product call): DG_FAULT_*, what is left out so that a wait runs out
 };
 
 template <int NT>
@@ -609,6 +610,7 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap map_w13, const __grid_const
             const uint64_t once = policy_evict_first();   // L2 is for the sums and activations
             Ring ring, landed;
             int flying = 0, limit = 1;
+            bool skip_fill = p.fault == DG_FAULT_FIRST_FILL;   // test only: leave the first stage empty
             uint32_t issued = 0, issued_parity = 0;
             bool ok = for_segments<NT>(p, s, nothing, [&](auto tag, int, const Line&, const Seg& g) {
                 const CUtensorMap* map = decltype(tag)::value == 1 ? &map_w13 : &map_w2;
@@ -623,6 +625,11 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap map_w13, const __grid_const
                         ++flying;
                     }
                     if (!__all_sync(FULL_MASK, got)) return false;
+                    if (skip_fill) {
+                        skip_fill = false;
+                        ring.next(STAGES);
+                        continue;
+                    }
                     if (issuer) {
                         uint8_t* dst = smem + ring.stage * ML_W_BYTES;
                         mbar_arrive_expect_tx(&s.full_w[ring.stage], g.two ? ML_W_BYTES : ML_W_BYTES / 2);
@@ -648,11 +655,10 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap map_w13, const __grid_const
             }
         } else if (warp == 1) {
             // ---------------------------------------------------------------- MMA issue
-            Ring ring, acc;
-            int last = -1;
-            uint32_t last_parity = 0;
+            Ring ring, acc, last_ring, last_acc;
+            bool any = false;
             const uint32_t w_base = smem_u32(smem), t_base = smem_u32(smem_t);
-            const bool ok = for_segments<NT>(p, s, nothing, [&](auto, int, const Line&, const Seg& g) {
+            for_segments<NT>(p, s, nothing, [&](auto, int, const Line&, const Seg& g) {
                 const uint32_t idesc = idesc_e4m3_f32(128, (g.n + 15) & ~15);
                 for (int kb = 0; kb < g.nkb; ++kb) {
                     const bool got = wait_bounded(&s.acc_empty[acc.stage], acc.phase ^ 1u, abort_flag, p.status, p.wait_limit_ns) &&
@@ -676,20 +682,28 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap map_w13, const __grid_const
                         mma_commit(&s.empty[ring.stage]);
                         mma_commit(&s.acc_full[acc.stage]);
                     }
-                    last = acc.stage;
-                    last_parity = acc.phase;
+                    any = true;
+                    last_ring = ring;
+                    last_acc = acc;
                     ring.next(STAGES);
                     acc.next(NACC);
                     __syncwarp();
                 }
                 return true;
             });
-            if (!ok && last >= 0 && issuer) drain_wait(&s.acc_full[last], last_parity);
+            // the last MMAs and their arrivals end before the shared and the tensor memory are given up, whichever
+            // warp of the CTA it is that gave up (else they have ended already, or do presently)
+            if (any && issuer) {
+                drain_wait(&s.empty[last_ring.stage], last_ring.phase);
+                drain_wait(&s.acc_full[last_acc.stage], last_acc.phase);
+            }
         } else if (warp == 2) {
             // ---------------------------------------------------------------- tokens
             Ring ring, slot;
-            uint32_t issued = 0, issued_parity = 0;
-            const bool ok = for_segments<NT>(p, s, [&](int l) {
+            uint32_t issued = 0, issued_parity = 0, scaled = 0, scaled_parity = 0;   // stages, scale slots: bits, for the drain
+            static_assert(SLOTS <= 32, "a bit a slot");
+            bool skip_scales = p.fault == DG_FAULT_TOKEN_SCALES;   // test only: leave the first scales out
+            for_segments<NT>(p, s, [&](int l) {
                 if (l == 1) return true;
                 if (l == 3 && s.line[1].nc == 0) return true;
                 const bool got = wait_bounded(&s.go[l == 0 ? 0 : l - 1], 0, abort_flag, p.status, p.wait_limit_ns);
@@ -710,21 +724,28 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap map_w13, const __grid_const
                         for (int b = 0; b < boxes; ++b)
                             tma_load_2d(map, &s.full_t[ring.stage], dst + b * 16 * BK, kb * BK, g.off + b * 16);
                         mbar_arrive_expect_tx(&s.scale_full[slot.stage], scale_bytes);
-                        bulk_load(s.scales[slot.stage], scales + static_cast<size_t>(kb) * p.rows_cap, scale_bytes, &s.scale_full[slot.stage]);
+                        if (!skip_scales)
+                            bulk_load(s.scales[slot.stage], scales + static_cast<size_t>(kb) * p.rows_cap, scale_bytes, &s.scale_full[slot.stage]);
                     }
+                    skip_scales = false;
                     issued |= 1u << ring.stage;
                     issued_parity = (issued_parity & ~(1u << ring.stage)) | (ring.phase << ring.stage);
+                    scaled |= 1u << slot.stage;
+                    scaled_parity = (scaled_parity & ~(1u << slot.stage)) | (slot.phase << slot.stage);
                     ring.next(STAGES);
                     slot.next(SLOTS);
                     __syncwarp();
                 }
                 return true;
             });
-            // (aborting) copies still in flight land before the shared memory is given up; the scales' are older
-            // or as old as a codes' copy waited for here, and as quick
-            if (!ok && issuer) {
+            // copies still in flight, of codes and of scales, land before the shared memory is given up: also where this
+            // warp has issued all of its own and another one gave up. (Without that the consumers have waited for
+            // each, and nothing is waited for here.)
+            if (issuer) {
                 for (int i = 0; i < STAGES; ++i)
                     if (issued & (1u << i)) drain_wait(&s.full_t[i], (issued_parity >> i) & 1u);
+                for (int i = 0; i < SLOTS; ++i)
+                    if (scaled & (1u << i)) drain_wait(&s.scale_full[i], (scaled_parity >> i) & 1u);
             }
         } else if (warp == 3) {
             // ---------------------------------------------------------------- grid barriers
@@ -1187,7 +1208,9 @@ dg_status dg_moe_layer(const void* x, const int32_t* ids, const float* weights, 
     p.I = I;
     p.rows_cap = rows_cap(T, k, E);
     p.act = act;
-    p.wait_limit_ns = take_armed_fault().wait_limit_ns;
+    const ArmedFault armed = take_armed_fault();
+    p.wait_limit_ns = armed.wait_limit_ns;
+    p.fault = armed.fault;
     CUtensorMap w13, w2, mx, mh;
     if (make_operand_map(&w13, W13, static_cast<int64_t>(E) * 2 * I, H, 128) != DG_OK ||
         make_operand_map(&w2, W2, static_cast<int64_t>(E) * H, I, 128) != DG_OK ||

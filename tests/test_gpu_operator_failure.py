@@ -83,6 +83,22 @@ def test_an_armed_fault_is_spent_by_the_expert_layer():
     assert dg.dg_device_status() == 0
 
 
+@pytest.mark.parametrize("fault,least", [("first_fill", 0.0), ("token_scales", DRAIN_S)])
+@pytest.mark.parametrize("T,k,E,H,In", [(5, 2, 8, 1024, 384), (55, 4, 8, 1152, 128), (64, 8, 16, 512, 384)])
+def test_an_expert_layer_that_gives_up(fault, least, T, k, E, H, In):
+    # (the scales that do not come: a few stages a CTA, so the warp that copies them is done before the wait runs out)
+    c = make_layer(T, k, E, H, In, seed=T)
+    ws = dg.moe_layer_workspace(T, k, E, H, In)
+    want = run_layer(c, ws=ws).clone()
+    t = [c[n].cuda() for n in ("x", "ids", "w", "W13", "s13", "W2", "s2")]
+    out = sentinel_bf16(T, H)
+    dg.dg_testing_arm_fault(fault, LIMIT_NS)
+    assert timed_out(lambda: dg.dg_moe_layer(*t, out, ws)) >= least
+    ws.zero_()
+    for _ in range(3):                                # (run_layer looks at the status after each)
+        assert torch.equal(run_layer(c, ws=ws), want)
+
+
 def test_arming_refuses():
     for fault, limit in (("residual", 0), ("residual", 1 << 60), (0, 1000), (99, 1000)):
         with pytest.raises(dg.DGError):
