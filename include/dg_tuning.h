@@ -61,9 +61,10 @@ dg_status dg_testing_arm_wait_timeout(uint64_t wait_limit_ns);
  * no such step only takes the short limit.
  */
 enum {
-    DG_FAULT_FIRST_FILL = 1, /* the first pipeline stage (what dg_testing_arm_wait_timeout arms) */
-    DG_FAULT_RESIDUAL = 2,   /* dg_gemm_fp8_nt_epilogue: the copies of the residual, in tiles that are not split along K */
-    DG_FAULT_TOKEN_SCALES = 3 /* dg_moe_layer: the first copy of token scales in each CTA */
+    DG_FAULT_FIRST_FILL = 1,   /* the first pipeline stage (what dg_testing_arm_wait_timeout arms) */
+    DG_FAULT_RESIDUAL = 2,     /* dg_gemm_fp8_nt_epilogue: the copies of the residual, in tiles that are not split along K */
+    DG_FAULT_TOKEN_SCALES = 3, /* dg_moe_layer: the first copy of token scales in each CTA */
+    DG_FAULT_GRID_BARRIER = 4  /* dg_moe_layer: the last CTA's arrival at the first barrier of all CTAs */
 };
 
 /* Arms a fault for the next launch as above. DG_INVALID_ARG for an unknown fault, or a limit of 0 or from 2^60 ns on. */

@@ -545,7 +545,7 @@ def dg_testing_arm_wait_timeout(wait_limit_ns: int) -> None:
 
 
 # What an armed launch leaves out (include/dg_tuning.h).
-FAULTS = {"first_fill": 1, "residual": 2, "token_scales": 3}
+FAULTS = {"first_fill": 1, "residual": 2, "token_scales": 3, "grid_barrier": 4}
 
 
 def dg_testing_arm_fault(fault, wait_limit_ns: int) -> None:

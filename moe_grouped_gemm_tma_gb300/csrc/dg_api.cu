@@ -655,7 +655,7 @@ void dg_tuning_reset(void) {
 }
 
 dg_status dg_testing_arm_fault(int fault, uint64_t wait_limit_ns) {
-    if (fault < DG_FAULT_FIRST_FILL || fault > DG_FAULT_TOKEN_SCALES || wait_limit_ns == 0 || wait_limit_ns >> 60) return DG_INVALID_ARG;
+    if (fault < DG_FAULT_FIRST_FILL || fault > DG_FAULT_GRID_BARRIER || wait_limit_ns == 0 || wait_limit_ns >> 60) return DG_INVALID_ARG;
     g_armed_fault.store(static_cast<unsigned long long>(wait_limit_ns) << 3 | static_cast<unsigned>(fault));
     return DG_OK;
 }

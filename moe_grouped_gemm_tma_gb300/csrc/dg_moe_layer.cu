@@ -148,10 +148,10 @@ __device__ __forceinline__ void add4(float4& a, const float4& b) { a.x += b.x; a
 // into the top bit, so the bit flips when the last one arrives and the low bits are back at zero: the word
 // needs no reset between barriers or launches. `top` is the top bit before this barrier (it cannot flip before
 // this CTA has arrived), so the arrival itself has nothing to wait for. The CTAs are co-resident (cooperative
-// launch); the wait ends by itself all the same.
-__device__ __forceinline__ bool grid_barrier(unsigned* word, unsigned top, volatile int* abort_flag, int* status, uint64_t limit_ns) {
+// launch); the wait ends by itself all the same. (`arrive` false: it only waits, for the test of that.)
+__device__ __forceinline__ bool grid_barrier(unsigned* word, unsigned top, bool arrive, volatile int* abort_flag, int* status, uint64_t limit_ns) {
     const unsigned add = blockIdx.x == 0 ? 0x80000000u - (gridDim.x - 1) : 1u;
-    red_add_release(word, add);
+    if (arrive) red_add_release(word, add);
     const uint64_t t0 = global_timer_ns();
     const uint64_t limit = limit_ns ? limit_ns : WAIT_LIMIT_NS;
     for (int i = 0; i < (1 << 26); ++i) {
@@ -755,7 +755,8 @@ moe_layer_kernel(const __grid_constant__ CUtensorMap map_w13, const __grid_const
                 for (int b = 0; b < ML_BARRIERS; ++b) {
                     if (b == 2 && s.line[1].nc == 0) continue;   // no second half
                     wait_bounded(&s.done[b], 0, abort_flag, p.status, p.wait_limit_ns);
-                    const bool got = grid_barrier(p.barrier, top, abort_flag, p.status, p.wait_limit_ns);
+                    const bool arrive = p.fault != DG_FAULT_GRID_BARRIER || b > 0 || blockIdx.x != gridDim.x - 1;
+                    const bool got = grid_barrier(p.barrier, top, arrive, abort_flag, p.status, p.wait_limit_ns);
                     top ^= 0x80000000u;
                     fence_proxy_async_all();
                     if (got) mbar_arrive(&s.go[b]);

@@ -83,7 +83,7 @@ def test_an_armed_fault_is_spent_by_the_expert_layer():
     assert dg.dg_device_status() == 0
 
 
-@pytest.mark.parametrize("fault,least", [("first_fill", 0.0), ("token_scales", DRAIN_S)])
+@pytest.mark.parametrize("fault,least", [("first_fill", 0.0), ("token_scales", DRAIN_S), ("grid_barrier", 0.0)])
 @pytest.mark.parametrize("T,k,E,H,In", [(5, 2, 8, 1024, 384), (55, 4, 8, 1152, 128), (64, 8, 16, 512, 384)])
 def test_an_expert_layer_that_gives_up(fault, least, T, k, E, H, In):
     # (the scales that do not come: a few stages a CTA, so the warp that copies them is done before the wait runs out)
