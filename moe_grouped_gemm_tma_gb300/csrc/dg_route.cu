@@ -589,6 +589,11 @@ route_few_backward_kernel(const T* __restrict__ logits, const int32_t* __restric
 // Up to 32 experts: the k largest by k turns of find-and-remove, the lowest lane that holds the largest value
 // winning, and every lane keeps the turn that it won (32 experts, k = 8: 1.7 us for 64 rows and 8.0 for 32768, where
 // the general way takes 2.0 and 10.0). Warps take several rows, the next one's logits on their way.
+
+// Whether a warp that has taken row t has another one, `stride` further on. (t + stride may be past 2^31.)
+__host__ __device__ constexpr bool another_row(int t, int stride, int rows) { return rows - t > stride; }
+static_assert(another_row(0, 8, 9) && !another_row(0, 8, 8) && !another_row(INT_MAX - 8, 32 * 1024, INT_MAX), "next row");
+
 template <typename T>
 __global__ void __launch_bounds__(32 * ROUTE_WARPS, 8)
 route_lane_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int32_t* __restrict__ ids,
@@ -601,9 +606,10 @@ route_lane_kernel(const T* __restrict__ logits, const float* __restrict__ bias, 
     const bool mine = lane < E;
     const float b = bias != nullptr && mine ? __ldg(bias + lane) : 0.f;
     float next = mine ? to_f32(logits[static_cast<size_t>(t) * E + lane]) : -INFINITY;
-    for (; t < rows; t += stride) {
+    for (bool more = true; more; t += more ? stride : 0) {
         const float l = next > -INFINITY ? finite_top(next) : -INFINITY;        // (NaN cannot be selected either)
-        if (t + stride < rows && mine) next = to_f32(logits[static_cast<size_t>(t + stride) * E + lane]);
+        more = another_row(t, stride, rows);
+        if (more && mine) next = to_f32(logits[static_cast<size_t>(t + stride) * E + lane]);
         float score = 0.f, total = 1.f, me = l;
         if (sigmoid_scores) {
             if (l > -INFINITY) score = sigmoid(l);
@@ -646,8 +652,10 @@ route_lane_backward_kernel(const T* __restrict__ logits, const int32_t* __restri
     int t = static_cast<int>(blockIdx.x) * ROUTE_WARPS + static_cast<int>(threadIdx.x >> 5);
     grid_dependency_wait();
     grid_launch_dependents();
+    if (t >= rows) return;
     const bool quotient = renorm || !sigmoid_scores;
-    for (; t < rows; t += stride) {
+    for (bool more = true; more; t += more ? stride : 0) {
+        more = another_row(t, stride, rows);
         const float x = lane < E ? to_f32(logits[static_cast<size_t>(t) * E + lane]) : -INFINITY;
         int e = -1;
         float dw = 0.f;
