@@ -84,3 +84,24 @@ def test_warps_that_take_several_rows(T, E, k, half):
             want = backward(logits.float(), ids, dw, scoring, renorm, 1.5)
             bound = 1e-5 * 1.5 * dw.abs().amax(1, keepdim=True) + (want.abs() * 2.0 ** -8 if half else 0)
             assert ((out.double() - want).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("E", [5, 20, 64, 200, 301, 1024])
+@pytest.mark.parametrize("T", [9, 6150])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_gradient_of_experts_named_more_than_once(E, T, scoring, renorm):
+    # every kernel's way of gathering the slots of an expert; the weights are functions of the slots, each of which
+    # names an expert, so an expert named n times has n weights and counts n times in their sum
+    k = 5
+    g = torch.Generator(device="cuda").manual_seed(E + T)
+    logits = torch.randn(T, E, device="cuda", generator=g) * 2
+    ids = torch.randint(0, E, (T, k), device="cuda", generator=g)
+    ids[:, 3] = ids[:, 0]
+    ids[::2, 4] = ids[::2, 0]
+    ids[::3, 1] = -1
+    dw = torch.randn(T, k, device="cuda", generator=g)
+    out = torch.full_like(logits, math.nan)
+    dg.dg_moe_route_backward(logits, ids.int(), dw, out, scoring=scoring, renormalize=renorm, scale=1.5)
+    want = backward(logits, ids, dw, scoring, renorm, 1.5)
+    assert ((out.double() - want).abs() <= 1e-5 * 1.5 * dw.abs().amax(1, keepdim=True) * k).all()
