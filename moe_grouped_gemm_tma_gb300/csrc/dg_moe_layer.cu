@@ -1076,13 +1076,17 @@ int64_t parts_bound(int nc, int H, int I) {
 }
 
 // Rows of y that any routing of these sizes can need: for every number of chunks, the halves' rows (at most NT a
-// chunk, rows_cap together) times their parts, the half of more parts filled first.
+// chunk, rows_cap together) times their parts, the half of more parts filled first. Every call asks for it, so the
+// search ends at the number of chunks whose smaller half can hold every row: from there on a half has all rows times
+// its parts, and more chunks have no more parts. (All numbers of chunks took 22 us for 64 tokens of 16 experts.)
 int64_t y_rows(int T, int k, int E, int H, int I) {
     const int nt = tokens_per_chunk(T), a = T * k;
     const int64_t cap = rows_cap(T, k, E);
     int64_t most = 0;
-    for (int i = 0; i < 2 * a; ++i) {
+    bool full = false;
+    for (int i = 0; i < 2 * a && !(full && i % 2 == 0); ++i) {
         const int chunks = i / 2 + 1, ca = i % 2 ? chunks : (chunks * 5 + 7) / 8, cb = chunks - ca;
+        full = full || static_cast<int64_t>(cb) * nt >= cap;
         const int64_t pa = parts_bound(ca, H, I), pb = cb ? parts_bound(cb, H, I) : 1;
         const int64_t ra = std::min<int64_t>(cap, static_cast<int64_t>(ca) * nt), rb = std::min<int64_t>(cap, static_cast<int64_t>(cb) * nt);
         const int64_t rows = pb >= pa ? rb * pb + std::min(ra, cap - rb) * pa : ra * pa + std::min(rb, cap - ra) * pb;
