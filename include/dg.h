@@ -191,9 +191,10 @@ dg_status dg_gemm_fp8_nt_epilogue(const uint8_t* A, const float* sfa, const uint
  * code = e4m3(v / s), both quotients rounded to FP32. With DG_ACT_NONE this quantises a BF16 matrix in one
  * or both directions. N must be a multiple of 128; M is free. dD, Z, q, qt 16-byte aligned.
  * workspace: device memory of dg_epilogue_backward_workspace(M, N) bytes, 16-byte aligned, needed for dbias
- * (else it may be null), zeroed before its first use; every call leaves it ready for the next one, of any size
- * that it is large enough for.
+ * (else it may be null), its first DG_EPILOGUE_BACKWARD_ZEROED bytes zero before its first use; every call
+ * leaves it ready for the next one, of any size that it is large enough for.
  */
+enum { DG_EPILOGUE_BACKWARD_ZEROED = 1024 };
 dg_status dg_epilogue_backward(const void* dD, const void* Z, int act, uint8_t* q, float* sf, uint8_t* qt, float* sft,
                                float* dbias, void* workspace, int64_t workspace_bytes, int M, int N,
                                cudaStream_t stream);
@@ -238,10 +239,11 @@ dg_status dg_moe_route_backward(const void* logits, int logits_type, const int32
  * only those of experts that a token meets are read.
  * 1 <= T <= 64 (0: no-op), T * k <= 1024, E <= 1024, H and I multiples of 128.
  * workspace: device memory of dg_moe_layer_workspace(T, k, E, H, I) bytes (-1 for sizes outside these), 256-byte
- * aligned, zeroed before its first use; every call leaves it ready for the next one, of any sizes it is large
- * enough for. After DG_DEVICE_TIMEOUT zero it again. The launch is cooperative: its CTAs, one per SM, run at
+ * aligned, its first DG_MOE_LAYER_ZEROED bytes zero before its first use; every call leaves it ready for the
+ * next one, of any sizes it is large enough for. After DG_DEVICE_TIMEOUT zero those again. The launch is cooperative: its CTAs, one per SM, run at
  * the same time.
  */
+enum { DG_MOE_LAYER_ZEROED = 4096 };
 dg_status dg_moe_layer(const void* x, const int32_t* ids, const float* weights, const uint8_t* W13, const float* s13,
                        const uint8_t* W2, const float* s2, const void* residual, void* out, void* workspace,
                        int64_t workspace_bytes, int T, int k, int E, int H, int I, int act, cudaStream_t stream);

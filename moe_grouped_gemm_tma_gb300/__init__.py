@@ -383,10 +383,20 @@ def dg_gemm_fp8_nt_epilogue(A, sfa, B, sfb, D, bias=None, act="none", residual=N
     return D
 
 
+# What a workspace's first call expects to be zero, from its start (include/dg.h); the rest is written before it is read.
+_EPILOGUE_BACKWARD_ZEROED, _MOE_LAYER_ZEROED = 1024, 4096
+
+
+def _workspace(size, zeroed, device):
+    torch = _torch()
+    ws = torch.empty(size, dtype=torch.uint8, device=device or "cuda")
+    ws[:zeroed].zero_()
+    return ws
+
+
 def epilogue_backward_workspace(M: int, N: int, device=None):
     """A workspace for dg_epilogue_backward with dbias at up to this size, ready for its first call."""
-    torch = _torch()
-    return torch.zeros(load().dg_epilogue_backward_workspace(M, N), dtype=torch.uint8, device=device or "cuda")
+    return _workspace(load().dg_epilogue_backward_workspace(M, N), _EPILOGUE_BACKWARD_ZEROED, device)
 
 
 def dg_epilogue_backward(dD, Z, q, sf, qt, sft, dbias, workspace=None, act="none", stream=None):
@@ -460,11 +470,10 @@ def dg_moe_route_backward(logits, ids, dweights, dlogits, scoring="softmax", ren
 
 def moe_layer_workspace(T: int, k: int, E: int, H: int, I: int, device=None):
     """A workspace for dg_moe_layer at these sizes, ready for its first call."""
-    torch = _torch()
     size = load().dg_moe_layer_workspace(T, k, E, H, I)
     if size < 0:
         raise DGError(2, "dg_moe_layer_workspace")
-    return torch.zeros(size, dtype=torch.uint8, device=device or "cuda")
+    return _workspace(size, _MOE_LAYER_ZEROED, device)
 
 
 def dg_moe_layer(x, ids, weights, W13, s13, W2, s2, out, workspace, act="silu", residual=None, stream=None):

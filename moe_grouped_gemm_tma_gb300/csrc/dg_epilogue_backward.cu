@@ -276,6 +276,7 @@ cudaError_t launch_eb(const EbParams& p, cudaStream_t stream) {
 // counters do), then the column sums.
 constexpr int EB_STRIPS = 256;
 constexpr int64_t EB_DONE_BYTES = 4 * EB_STRIPS;
+static_assert(EB_DONE_BYTES == DG_EPILOGUE_BACKWARD_ZEROED, "the sums need no zeros");
 
 }  // namespace
 }  // namespace dg

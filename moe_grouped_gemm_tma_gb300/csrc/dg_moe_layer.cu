@@ -57,7 +57,7 @@ constexpr int ML_MAX_E = 1024;
 constexpr int ML_MAX_CTAS = 160;               // CTAs (workspace slots) at most; one per SM
 constexpr int ML_MAX_ROWS = ML_MAX_A + 3 * ML_MAX_A;   // gathered rows: every expert's start on a multiple of 4
 constexpr int ML_W_BYTES = 2 * 128 * BK;       // weights of a stage
-constexpr int ML_FIXED = 4096;                 // workspace: barrier word and counters
+constexpr int ML_FIXED = DG_MOE_LAYER_ZEROED;  // workspace: barrier word and counters (all that is read before it is written)
 constexpr int ML_THREADS = 512;
 constexpr int ML_FIN_WARP0 = 4, ML_EPI_WARP0 = 8, ML_WORKERS = 12;
 constexpr int ML_CTRL_REGS = 56, ML_FIN_REGS = 104, ML_EPI_REGS = 176;  // 128 * (56 + 104) + 256 * 176 = 512 * 128

@@ -55,3 +55,16 @@ def test_the_sizes_of_a_large_step_take_no_longer_than_those_of_a_small_one():
         return best
 
     assert shortest(64, 16) < 5 * shortest(1, 1)
+
+
+def test_workspaces_are_zeroed_only_where_a_first_call_reads(monkeypatch):
+    import os
+    import re
+
+    import torch
+    header = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "dg.h")).read()
+    zeroed = {n: int(v) for n, v in re.findall(r"enum \{ (DG_\w+_ZEROED) = (\d+) \};", header)}
+    monkeypatch.setattr(torch, "empty", lambda size, **kw: torch.full((size,), 0xFF, **kw))
+    for ws, n in ((dg.moe_layer_workspace(64, 8, 16, 1024, 512, device="cpu"), zeroed["DG_MOE_LAYER_ZEROED"]),
+                  (dg.epilogue_backward_workspace(700, 512, device="cpu"), zeroed["DG_EPILOGUE_BACKWARD_ZEROED"])):
+        assert ws.numel() > 2 * n and not ws[:n].any() and (ws[n:] == 0xFF).all()
