@@ -47,7 +47,6 @@ struct EbParams {
     float* sums;          // [m_tiles][N] column sums of each tile
     unsigned* done;       // [N / 128] tiles of a strip that have written theirs; null: a second kernel adds them up
     int m, n, m_tiles;
-    int act;
     int ahead;            // tiles between a CTA's own and the one that it asks L2 for; 0: none
 };
 
@@ -330,7 +329,6 @@ dg_status dg_epilogue_backward(const void* dD, const void* Z, int act, uint8_t* 
     // 4096 x 4096 24.0 -> 23.5; 4096 x 2048, 3.4 tiles an SM, 13.9 -> 14.4)
     p.ahead = static_cast<int64_t>(p.m_tiles) * strips >= 6 * dev.sms ? dev.sms * 3 / 2 : 0;
     p.done = one_round ? static_cast<unsigned*>(workspace) : nullptr;
-    p.act = act;
     cudaError_t e = cudaErrorInvalidValue;
     switch (act) {
         case DG_ACT_NONE: e = launch_eb<DG_ACT_NONE>(p, stream); break;

@@ -7,9 +7,11 @@
 // SM whose weight stream stops for nothing but a full ring:
 //
 //   * Split. A stage is 256 weight rows x one 128-wide K block, 32 KB. The stages of a phase (phase 1: W13,
-//     phase 2: W2) form a line, unit after unit, and CTA c of G takes the c-th G-th of it, whatever the
-//     number of met experts: every SM streams the same bytes, to one stage (a small layer's: to a few). Parts of a unit that the cuts
-//     divide are summed in the order of the CTAs, so the result does not depend on timing.
+//     phase 2: W2) form a line, unit after unit. With more units than CTAs, CTA c of G takes the c-th G-th of it, whatever
+//     the number of met experts: every SM streams the same bytes, to one stage. With fewer units each is for a whole number
+//     of CTAs, and the CTAs left over stream nothing, as long as the others' shares stay within six stages of an even one
+//     (make_line). Parts of a unit that the cuts divide are summed in the order of the CTAs, so the result does not depend
+//     on timing.
 //   * Order. The met experts' chunks are halved, and the lines are: phase 1 of the first half, phase 1 of the
 //     second, phase 2 of the first, phase 2 of the second. The hidden activations of one half are finished
 //     (a grid barrier) while the weights of the other half stream.
@@ -55,7 +57,6 @@ constexpr int ML_MAX_T = 64;
 constexpr int ML_MAX_A = 1024;                 // assignments, T * k
 constexpr int ML_MAX_E = 1024;
 constexpr int ML_MAX_CTAS = 160;               // CTAs (workspace slots) at most; one per SM
-constexpr int ML_MAX_ROWS = ML_MAX_A + 3 * ML_MAX_A;   // gathered rows: every expert's start on a multiple of 4
 constexpr int ML_W_BYTES = 2 * 128 * BK;       // weights of a stage
 constexpr int ML_FIXED = DG_MOE_LAYER_ZEROED;  // workspace: barrier word and counters (all that is read before it is written)
 constexpr int ML_THREADS = 512;
@@ -98,7 +99,7 @@ struct MlCfg {
     // The token scales of a stage live until it is promoted: the ring and the accumulators can hold that
     // many stages between the two, so with two more no slot is rewritten before it has been read.
     static constexpr int SLOTS = 6 + NACC + 2;
-    static constexpr int TABLES = 4 * ML_MAX_A + 4 * ML_MAX_A + ML_MAX_ROWS + 4 * 4 * (ML_MAX_CTAS + 1) + 128;
+    static constexpr int TABLES = 4 * ML_MAX_A + 4 * ML_MAX_A + 4 * 4 * (ML_MAX_CTAS + 1) + 128;
     static constexpr int STATIC_RESERVE = TABLES + SLOTS * NT * 4 + 768;
     static constexpr int STAGES_FIT = ring_stages(STAGE_BYTES, 0, 0, STATIC_RESERVE);
     static constexpr int STAGES = STAGES_FIT > 6 ? 6 : STAGES_FIT;
@@ -203,7 +204,6 @@ struct Shared {
     __align__(16) float scales[MlCfg<NT>::SLOTS][NT];
     uint32_t chunk[ML_MAX_A];
     uint32_t row_of[ML_MAX_A];                  // gathered row of an assignment (t * k + j) | chunk << 16, or NO_ROW
-    uint8_t token[ML_MAX_ROWS];                 // token of a gathered row
     uint32_t share[4][ML_MAX_CTAS + 1];         // first stage of each CTA's share of each line
     Line line[4];
 };
@@ -421,9 +421,7 @@ __device__ void make_tables(const MoeParams& p, Shared<NT>& s, uint8_t* scratch)
         uint32_t where = NO_ROW;
         if (e >= 0) {
             const uint32_t n = counts[(a >> 5) * pitch + e] + static_cast<uint32_t>(rank[i]);   // of the expert's rows
-            const uint32_t r = offset[e] + n;
-            where = r | ((first_chunk[e] + n / NT) << 16);
-            s.token[r] = static_cast<uint8_t>(a / p.k);
+            where = (offset[e] + n) | ((first_chunk[e] + n / NT) << 16);
         }
         s.row_of[a] = where;
     }
