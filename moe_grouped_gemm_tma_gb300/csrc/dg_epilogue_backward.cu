@@ -17,7 +17,7 @@
 // second launch gives 42.0 and 31.1; at 333 x 2048 it gives 5.4 for 5.8 us, less than the launch costs the host.
 //
 // Floor: 4 bytes read and 2 written per element (2 read without an activation), 26.6 us for 4096 x 7168 at the
-// measured copy bandwidth. It takes 37.8 us: loads whose latency two CTAs an SM hide only in part, 63% of the issue
+// measured copy bandwidth. It takes 39.1 us: loads whose latency two CTAs an SM hide only in part, 63% of the issue
 // slots, and two barriers a tile, because the two scalings need the whole tile's maxima between the loads and the
 // stores. (A persistent form with the next tile's operands in shared memory by TMA was 7 us slower; without the exact
 // divisions of the codes it would be 1 us faster.)
@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(EB_THREADS, 2) epilogue_backward_kernel(const 
     }
 
     // ---- the tile that is `ahead` further on, into L2: a CTA's loads are what it waits for most. (Not for GELU, which
-    // it makes slower, 45.7 against 47.4 us at 4096 x 7168: its arithmetic needs the registers.)
+    // it made slower, 45.7 against 47.4 us at 4096 x 7168: its arithmetic needs the registers.)
     if (!STRIPS && ACT != DG_ACT_GELU && p.ahead > 0 && (l16 & 7) == 0) {
         const unsigned tile = blockIdx.y * gridDim.x + blockIdx.x + static_cast<unsigned>(p.ahead);
         const unsigned ny = tile / gridDim.x, nx = tile - ny * gridDim.x;
