@@ -172,7 +172,7 @@ route_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int32
         if (!renorm) {
             float sum = 0.f;
 #pragma unroll
-            for (int i = 0; i < VPL; ++i) sum += v[i] > -INFINITY ? __expf(v[i] - top) : 0.f;
+            for (int i = 0; i < VPL; ++i) sum += v[i] > -INFINITY ? expf(v[i] - top) : 0.f;
             total = warp_sum(sum);
         }
     }
@@ -274,7 +274,7 @@ route_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int32
     }
 
     float score = 0.f;
-    if (place >= 0) score = sigmoid_scores ? value : __expf(value - top);
+    if (place >= 0) score = sigmoid_scores ? value : expf(value - top);
     if (renorm) total = warp_sum(score);
     const float w = total > 0.f ? score * __frcp_rn(total) : 0.f;
     const size_t out = static_cast<size_t>(t) * k;
@@ -363,12 +363,12 @@ route_backward_kernel(const T* __restrict__ logits, const int32_t* __restrict__ 
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
-            out[i] = l[i] > -INFINITY ? __expf(l[i] - top) : 0.f;
+            out[i] = l[i] > -INFINITY ? expf(l[i] - top) : 0.f;
             sum += out[i];
         }
         sum = warp_sum(sum);
         const float inv = sum > 0.f ? __frcp_rn(sum) : 0.f;
-        const float p = mine > -INFINITY ? __expf(mine - top) * inv : 0.f;
+        const float p = mine > -INFINITY ? expf(mine - top) * inv : 0.f;
         const float dot = warp_sum(p * dw);
         // duplicates of an expert in one row add up: every lane that names it ends with the same total
         float add = 0.f;
@@ -388,7 +388,7 @@ route_backward_kernel(const T* __restrict__ logits, const int32_t* __restrict__ 
             top = mine;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, o));
-            p = mine > -INFINITY ? __expf(mine - top) : 0.f;
+            p = mine > -INFINITY ? expf(mine - top) : 0.f;
         }
         float g;
         if (renorm) {
@@ -466,7 +466,7 @@ route_few_kernel(const T* __restrict__ logits, const float* __restrict__ bias, i
         top = group_max(top);
         if (!renorm) {
 #pragma unroll
-            for (int i = 0; i < VPL; ++i) sum += l[i] > -INFINITY ? __expf(l[i] - top) : 0.f;
+            for (int i = 0; i < VPL; ++i) sum += l[i] > -INFINITY ? expf(l[i] - top) : 0.f;
             sum = group_sum(sum);
         }
     }
@@ -502,7 +502,7 @@ route_few_kernel(const T* __restrict__ logits, const float* __restrict__ bias, i
         score[m] = 0.f;
         if (m * GROUP + l8 < k) {
             const float x = s_logit[warp][g][m * GROUP + l8];
-            if (x > -INFINITY) score[m] = sigmoid_scores ? sigmoid(x) : __expf(x - top);
+            if (x > -INFINITY) score[m] = sigmoid_scores ? sigmoid(x) : expf(x - top);
         }
     }
     if (renorm) sum = group_sum((score[0] + score[1]) + (score[2] + score[3]));
@@ -562,7 +562,7 @@ route_few_backward_kernel(const T* __restrict__ logits, const int32_t* __restric
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
         const bool counts = l[i] > -INFINITY && (!renorm || named[i] > 0.f);
-        p[i] = !counts ? 0.f : (sigmoid_scores ? sigmoid(l[i]) : __expf(l[i] - top));
+        p[i] = !counts ? 0.f : (sigmoid_scores ? sigmoid(l[i]) : expf(l[i] - top));
         sum = fmaf(renorm ? named[i] : 1.f, p[i], sum);
     }
     const bool quotient = renorm || !sigmoid_scores;
@@ -616,7 +616,7 @@ route_lane_kernel(const T* __restrict__ logits, const float* __restrict__ bias, 
             if (bias != nullptr && l > -INFINITY) me = score + b;
         } else {
             const float top = warp_max(l);
-            if (l > -INFINITY) score = __expf(l - top);
+            if (l > -INFINITY) score = expf(l - top);
             if (!renorm) total = warp_sum(score);
         }
         int place = -1;
@@ -679,7 +679,7 @@ route_lane_backward_kernel(const T* __restrict__ logits, const int32_t* __restri
             if (counts) p = sigmoid(l);
         } else {
             const float top = warp_max(counts ? l : -FLT_MAX);
-            if (counts) p = __expf(l - top);
+            if (counts) p = expf(l - top);
         }
         const float times = renorm ? named : 1.f;
         if (quotient) {
