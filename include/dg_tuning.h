@@ -62,7 +62,7 @@ dg_status dg_testing_arm_wait_timeout(uint64_t wait_limit_ns);
  */
 enum {
     DG_FAULT_FIRST_FILL = 1,   /* the first pipeline stage (what dg_testing_arm_wait_timeout arms) */
-    DG_FAULT_RESIDUAL = 2,     /* dg_gemm_fp8_nt_epilogue: the copies of the residual, in tiles that are not split along K */
+    DG_FAULT_RESIDUAL = 2,     /* dg_gemm_fp8_nt_epilogue: half of the residual, in tiles that are not split along K */
     DG_FAULT_TOKEN_SCALES = 3, /* dg_moe_layer: the first copy of token scales in each CTA */
     DG_FAULT_GRID_BARRIER = 4  /* dg_moe_layer: the last CTA's arrival at the first barrier of all CTAs */
 };

@@ -152,16 +152,25 @@ dg_status make_output_map(CUtensorMap* m, void* base, int64_t rows, int64_t n) {
 
 // Row-major BF16 output [rows, n] written in boxes of 32 rows x 32 columns (64 bytes) with the
 // 64-byte swizzle of the main kernel's whole-tile staging.
-dg_status make_tile_output_map(CUtensorMap* m, void* base, int64_t rows, int64_t n) {
+dg_status make_tile_output_map(CUtensorMap* m, void* base, int64_t rows, int64_t n, uint32_t box_rows = 32) {
     cuuint64_t dims[2] = {static_cast<cuuint64_t>(n), static_cast<cuuint64_t>(rows)};
     cuuint64_t strides[1] = {static_cast<cuuint64_t>(n) * 2};
-    cuuint32_t box[2] = {32u, 32u};
+    cuuint32_t box[2] = {32u, box_rows};
     cuuint32_t es[2] = {1u, 1u};
     CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, es,
                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
                           CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? DG_OK : DG_CUDA_ERROR;
 }
+
+}  // namespace
+
+void halve_residual_copies(EpilogueParams& p) {
+    if (p.residual != nullptr && p.split <= 1)
+        make_tile_output_map(&p.tmap_r, const_cast<__nv_bfloat16*>(p.residual), p.rows, p.n, 16);
+}
+
+namespace {
 
 // Specialisations per layout: (BN, PAIR); each must be instantiated in the matching dg_inst_*.cu.
 struct Spec {

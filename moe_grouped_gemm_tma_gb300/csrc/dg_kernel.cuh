@@ -977,7 +977,7 @@ dg_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant
                 if constexpr (MODE == kEpilogue) {
                     if (residual_on) {
                         rpending = true;
-                        if (lane == 0 && p.fault != DG_FAULT_RESIDUAL) {
+                        if (lane == 0) {
                             bulk_wait_read_n<0>();
                             const int boxes = min(COLS / 32, (p.n - cstart + 31) / 32);
                             mbar_arrive_expect_tx(&residual_bar[ew], static_cast<uint32_t>(boxes) * 2048u);
@@ -1247,10 +1247,8 @@ dg_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant
                 if (residual_on) {
                     got = wait_bounded(&residual_bar[ew], rphase, abort_flag, p.status, p.wait_limit_ns);
                     // (a copy whose wait gave up is still on its way: it stays pending, in its phase, for the drain below)
-                    if (got) {
-                        rphase ^= 1u;
-                        rpending = false;
-                    }
+                    rphase ^= got ? 1u : 0u;
+                    rpending = !got;
                 }
                 if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
                 if (!residual_on && p.z != nullptr) {

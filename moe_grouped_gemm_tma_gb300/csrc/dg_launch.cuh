@@ -48,6 +48,9 @@ struct ArmedFault {
 };
 ArmedFault take_armed_fault();
 
+// Test only: copies of the residual that bring half of the bytes that the kernel waits for.
+void halve_residual_copies(EpilogueParams& p);
+
 // Programmatic dependent launch is on unless the DG_TUNE_PDL knob is 0.
 inline bool pdl_enabled() { return tune(DG_TUNE_PDL) != 0; }
 
@@ -141,6 +144,8 @@ cudaError_t launch(const Launch& L) {
     if (const ArmedFault f = take_armed_fault(); f.fault != 0) {
         prm.wait_limit_ns = f.wait_limit_ns;
         prm.fault = f.fault;
+        if constexpr (MODE == kEpilogue)
+            if (f.fault == DG_FAULT_RESIDUAL) halve_residual_copies(prm);
     }
     return cudaLaunchKernelEx(&cfg, kern, L.tmap_a, L.tmap_b, L.tmap_d, prm);
 }
