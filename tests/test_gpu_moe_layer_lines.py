@@ -111,3 +111,41 @@ def test_cuts_of_the_lines(name):
     for _ in range(5):
         assert torch.equal(run(c, ws=ws), first)
     assert torch.equal(run(c), first)
+
+
+def values64(v):
+    """The 1x128 quantisation's values of float64 [rows, n * 128] on the GPU."""
+    b = v.unflatten(1, (-1, 128))
+    s = (b.abs().amax(2, keepdim=True).clamp_min(float(torch.tensor(1e-4))) / 448).float().double()
+    return ((b / s).float().to(torch.float8_e4m3fn).double() * s).flatten(1)
+
+
+@pytest.mark.parametrize("T,k,E", [(1, 8, 128), (16, 8, 128), (64, 4, 40)])
+def test_serving_sizes(T, k, E):
+    # many experts of a large layer, most of them met by a token or two
+    H, In = 7168, 2048
+    g = torch.Generator(device="cuda").manual_seed(T + E)
+    codes = lambda *s: torch.randint(0x28, 0x48, s, device="cuda", generator=g, dtype=torch.uint8) | (torch.randint(0, 2, s, device="cuda", generator=g, dtype=torch.uint8) << 7)  # noqa: E731
+    scales = lambda K, *s: (torch.rand(*s, device="cuda", generator=g) + 0.5) / (3 * math.sqrt(K))  # noqa: E731
+    W13, s13, W2, s2 = codes(E, 2 * In, H), scales(H, E, 2 * In // 128, H // 128), codes(E, H, In), scales(In, E, H // 128, In // 128)
+    x = torch.randn(T, H, device="cuda", generator=g).to(torch.bfloat16)
+    ids = torch.rand(T, E, device="cuda", generator=g).topk(k, 1)[1].int()
+    w = torch.rand(T, k, device="cuda", generator=g) + 0.1
+    out = torch.full_like(x, math.nan)
+    ws = dg.moe_layer_workspace(T, k, E, H, In)
+    dg.dg_moe_layer(x, ids, w, W13, s13, W2, s2, out, ws, act="silu", residual=x)
+    assert dg.dg_device_status() == 0
+    want, xv = x.double(), values64(x.double())
+    block = lambda q, s: q.view(torch.float8_e4m3fn).double() * s.double().repeat_interleave(128, 0).repeat_interleave(128, 1)  # noqa: E731
+    for e in ids.unique().tolist():
+        t, j = (ids == e).nonzero(as_tuple=True)
+        gate, up = (xv[t] @ block(W13[e], s13[e]).t()).chunk(2, 1)
+        h = values64(gate * torch.sigmoid(gate) * up)
+        want.index_add_(0, t, w[t, j].double().unsqueeze(1) * (h @ block(W2[e], s2[e]).t()))
+    got = out.double()
+    rms = want.square().mean().sqrt()
+    assert ((got - want).abs() <= 1e-2 * want.abs() + 2e-2 * rms).all()
+    assert (got - want).norm() <= 3e-3 * want.norm()
+    again = torch.full_like(x, math.nan)
+    dg.dg_moe_layer(x, ids, w, W13, s13, W2, s2, again, ws, act="silu", residual=x)
+    assert torch.equal(again, out)
