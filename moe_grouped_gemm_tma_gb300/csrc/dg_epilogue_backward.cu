@@ -79,8 +79,8 @@ __global__ void __launch_bounds__(EB_THREADS, 2) epilogue_backward_kernel(const 
             d[i] = make_uint4(0, 0, 0, 0);
             z[i] = make_uint4(0, 0, 0, 0);
             if (i < valid) {
-                d[i] = __ldg(reinterpret_cast<const uint4*>(p.dd + base + static_cast<size_t>(i) * p.n));
-                if (ACT != DG_ACT_NONE) z[i] = __ldg(reinterpret_cast<const uint4*>(p.z + base + static_cast<size_t>(i) * p.n));
+                d[i] = ld_input(reinterpret_cast<const uint4*>(p.dd + base + static_cast<size_t>(i) * p.n));
+                if (ACT != DG_ACT_NONE) z[i] = ld_input(reinterpret_cast<const uint4*>(p.z + base + static_cast<size_t>(i) * p.n));
             }
         }
 #pragma unroll

@@ -276,7 +276,7 @@ __device__ __forceinline__ TileInfo decode_tile(const Params& p, int t, const in
             ti.nkb = ((srank + 1) * p.kbs) / p.split - ti.kb0;
         }
         if (MODE == kContiguous) {
-            const int g = __ldg(p.m_indices + mb * TILE_M);
+            const int g = ld_input(p.m_indices + mb * TILE_M);
             ti.valid = (g >= 0 && g < p.groups);
             ti.g = ti.valid ? g : 0;
             ti.b_row += ti.g * p.n;
@@ -292,7 +292,7 @@ __device__ __forceinline__ TileInfo decode_tile(const Params& p, int t, const in
         const int local = t - s_prefix[g];
         const int mblk = (s_prefix[g + 1] - s_prefix[g]) / p.n_blocks;
         const int mb = local % mblk, nb = local / mblk;
-        const int mm = min(max(__ldg(p.masked_m + g), 0), p.rows);
+        const int mm = min(max(ld_input(p.masked_m + g), 0), p.rows);
         ti.g = g;
         ti.m0 = mb * TILE_M + rank * BM;
         ti.n0 = nb * BN;
@@ -413,12 +413,12 @@ __device__ __forceinline__ void load_bias(float (&v)[COLS], const float* bias, i
 #pragma unroll
         for (int j = 0; j < COLS; j += 4) {
             float4 b = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (col + j < n) b = __ldg(reinterpret_cast<const float4*>(bias + col + j));
+            if (col + j < n) b = ld_input(reinterpret_cast<const float4*>(bias + col + j));
             v[j] = b.x; v[j + 1] = b.y; v[j + 2] = b.z; v[j + 3] = b.w;
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < COLS; ++j) v[j] = col + j < n ? __ldg(bias + col + j) : 0.f;
+        for (int j = 0; j < COLS; ++j) v[j] = col + j < n ? ld_input(bias + col + j) : 0.f;
     }
 }
 
@@ -506,7 +506,7 @@ __device__ __forceinline__ void finish_split(const EpilogueParams& p, uint32_t p
             if (item[u].stored) {
                 if (p.residual != nullptr) res[u] = *reinterpret_cast<const uint2*>(p.residual + item[u].at);
                 if (p.bias != nullptr)
-                    bias[u] = make_float4(__ldg(p.bias + item[u].col), __ldg(p.bias + item[u].col + 1), __ldg(p.bias + item[u].col + 2), __ldg(p.bias + item[u].col + 3));
+                    bias[u] = make_float4(ld_input(p.bias + item[u].col), ld_input(p.bias + item[u].col + 1), ld_input(p.bias + item[u].col + 2), ld_input(p.bias + item[u].col + 3));
             }
         }
         float4 sum[U];
@@ -637,7 +637,7 @@ dg_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant
     if (MODE == kMasked) {
         // per-expert tile counts, then an exclusive prefix sum (one warp)
         for (int g = threadIdx.x; g < p.groups; g += C::THREADS_C) {
-            const int mm = min(max(__ldg(p.masked_m + g), 0), p.rows);
+            const int mm = min(max(ld_input(p.masked_m + g), 0), p.rows);
             s_prefix[g + 1] = ((mm + C::TILE_M - 1) / C::TILE_M) * p.n_blocks;
         }
         __syncthreads();
@@ -1006,7 +1006,7 @@ dg_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant
                 const float* sfa_row = p.sfa + static_cast<size_t>(min(ti.a_row + row_in_tile, a_rows_total - 1)) * p.kbs + ti.kb0;
                 const float* sfb_0 = p.sfb + (static_cast<size_t>(ti.g) * p.sfb_rows + min(cstart / 128, p.sfb_rows - 1)) * p.kbs + ti.kb0;
                 const float* sfb_1 = p.sfb + (static_cast<size_t>(ti.g) * p.sfb_rows + min(cstart / 128 + 1, p.sfb_rows - 1)) * p.kbs + ti.kb0;
-                float sa_n = __ldg(sfa_row), b0_n = __ldg(sfb_0), b1_n = __ldg(sfb_1);
+                float sa_n = ld_input(sfa_row), b0_n = ld_input(sfb_0), b1_n = ld_input(sfb_1);
                 // Each K block's TMEM loads in two halves: the first half is loaded and promoted, then the
                 // second half is loaded and the accumulator released before its FMAs, so the MMA of block
                 // kb + NACC waits for half a block's FMAs instead of three quarters (EPI_ONE tiles load the
@@ -1017,9 +1017,9 @@ dg_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant
                     if (MODE == kEpilogue && kb == ti.nkb / 2) load_residual();
                     const float sa = sa_n, b0 = b0_n, b1 = b1_n;
                     if (kb + 1 < ti.nkb) {
-                        sa_n = __ldg(sfa_row + kb + 1);
-                        b0_n = __ldg(sfb_0 + kb + 1);
-                        b1_n = __ldg(sfb_1 + kb + 1);
+                        sa_n = ld_input(sfa_row + kb + 1);
+                        b0_n = ld_input(sfb_0 + kb + 1);
+                        b1_n = ld_input(sfb_1 + kb + 1);
                     }
                     bool got = mbar_try_wait(&tmem_full_bar[acc], acc_phase);
                     if (!got) got = wait_bounded(&tmem_full_bar[acc], acc_phase, abort_flag, p.status, p.wait_limit_ns);

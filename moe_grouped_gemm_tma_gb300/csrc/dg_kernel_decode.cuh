@@ -77,7 +77,7 @@ __device__ __forceinline__ DecTile decode_dec(const Params& p, int t, const int*
         const int local = t - s_prefix[g];
         const int mblk = (s_prefix[g + 1] - s_prefix[g]) / p.n_blocks;
         const int mb = local % mblk, nb = local / mblk;
-        const int mm = min(max(__ldg(p.masked_m + g), 0), p.rows);
+        const int mm = min(max(ld_input(p.masked_m + g), 0), p.rows);
         ti.g = g;
         ti.m0 = mb * BMT;
         ti.n0 = nb * 128;
@@ -111,7 +111,7 @@ __device__ __forceinline__ void epilogue_column(float (&v)[ROWS], const Epilogue
     for (int m = 0; m < ROWS; ++m)
         res[m] = p.residual != nullptr && m < valid ? __bfloat162float(p.residual[at + static_cast<size_t>(m) * p.n]) : 0.f;
     if (p.bias != nullptr) {
-        const float b = __ldg(p.bias + col);
+        const float b = ld_input(p.bias + col);
 #pragma unroll
         for (int m = 0; m < ROWS; ++m) v[m] += b;
     }
@@ -193,7 +193,7 @@ dg_decode_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_consta
     if (MODE == kMasked) {
         // per-expert tile counts from the device-resident masked_m, then an exclusive prefix sum
         for (int g = threadIdx.x; g < p.groups; g += THREADS) {
-            const int mm = min(max(__ldg(p.masked_m + g), 0), p.rows);
+            const int mm = min(max(ld_input(p.masked_m + g), 0), p.rows);
             s_prefix[g + 1] = ((mm + BMT - 1) / BMT) * p.n_blocks;
         }
         __syncthreads();

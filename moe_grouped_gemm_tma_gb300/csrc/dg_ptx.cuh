@@ -436,6 +436,12 @@ __device__ __forceinline__ void cp_async_wait_all() {
 // memory writes are visible; a no-op when the launch carries no programmatic dependency.
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// An input of a kernel that may have started before the grid that writes it ended: an ordinary load, which the wait above
+// orders. (The read-only path, __ldg or a const __restrict__ argument, is for data that nothing writes from the kernel's
+// start on; the compiler may also move such loads to before the wait.)
+template <typename T>
+__device__ __forceinline__ T ld_input(const T* p) { return *p; }
+
 // Allow the next dependent grid in the stream to be scheduled (its own wait still orders its memory
 // accesses after this grid's completion).
 __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }

@@ -57,10 +57,10 @@ __device__ __forceinline__ void load_row(const T* row, int E, int lane, bool vec
             for (int c = 0; c < BYTES / W; ++c) {
                 uint32_t w[W / 4];
                 if constexpr (W == 16) {
-                    const uint4 u = __ldg(reinterpret_cast<const uint4*>(row + e0) + c);
+                    const uint4 u = ld_input(reinterpret_cast<const uint4*>(row + e0) + c);
                     w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
                 } else {
-                    const uint2 u = __ldg(reinterpret_cast<const uint2*>(row + e0) + c);
+                    const uint2 u = ld_input(reinterpret_cast<const uint2*>(row + e0) + c);
                     w[0] = u.x; w[1] = u.y;
                 }
 #pragma unroll
@@ -108,14 +108,14 @@ __device__ __forceinline__ void load_bias(const float* bias, int E, int e0, int 
 #pragma unroll
             for (int c = 0; c < VPL / 4; ++c) {
                 float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (e0 < E) u = __ldg(reinterpret_cast<const float4*>(bias + e0) + c);
+                if (e0 < E) u = ld_input(reinterpret_cast<const float4*>(bias + e0) + c);
                 v[4 * c] = u.x; v[4 * c + 1] = u.y; v[4 * c + 2] = u.z; v[4 * c + 3] = u.w;
             }
             return;
         }
     }
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) v[i] = e0 + i * step < E ? __ldg(bias + e0 + i * step) : 0.f;
+    for (int i = 0; i < VPL; ++i) v[i] = e0 + i * step < E ? ld_input(bias + e0 + i * step) : 0.f;
 }
 
 // v = the fast sigmoid of v + b; -inf where v is that or NaN.
@@ -136,8 +136,8 @@ __device__ __forceinline__ float finite_top(float l) { return fminf(l, FLT_MAX);
 
 template <int VPL, typename T>
 __global__ void __launch_bounds__(32 * ROUTE_WARPS, VPL <= 8 ? 8 : (VPL == 16 ? 5 : 3))
-route_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int32_t* __restrict__ ids,
-             float* __restrict__ weights, int rows, int E, int k, int sigmoid_scores, int renorm, float scale, int vec) {
+route_kernel(const T* logits, const float* bias, int32_t* ids,
+             float* weights, int rows, int E, int k, int sigmoid_scores, int renorm, float scale, int vec) {
     __shared__ __align__(16) float s_value[ROUTE_WARPS][32];
     __shared__ int s_cand[ROUTE_WARPS][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -213,7 +213,7 @@ route_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int32
             expert = s_cand[warp][lane];
             me = value = finite_top(to_f32(row[expert]));
             if (sigmoid_scores) value = sigmoid(value);
-            if (bias != nullptr) me = value + __ldg(bias + expert);
+            if (bias != nullptr) me = value + ld_input(bias + expert);
         }
         s_value[warp][lane] = me;
         __syncwarp();
@@ -244,7 +244,7 @@ route_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int32
                 float exact = -INFINITY;
                 if (e < E) {
                     const float l = to_f32(row[e]);
-                    if (l > -INFINITY) exact = sigmoid(finite_top(l)) + __ldg(bias + e);
+                    if (l > -INFINITY) exact = sigmoid(finite_top(l)) + ld_input(bias + e);
                 }
 #pragma unroll
                 for (int x = 0; x < VPL; ++x)
@@ -333,17 +333,17 @@ __device__ __forceinline__ void store_row(T* row, int E, int lane, bool vec, con
 // the whole row; every form writes it. Bound by those bytes.
 template <int VPL, typename T>
 __global__ void __launch_bounds__(32 * ROUTE_WARPS)
-route_backward_kernel(const T* __restrict__ logits, const int32_t* __restrict__ ids, const float* __restrict__ dweights,
-                      T* __restrict__ dlogits, int rows, int E, int k, int sigmoid_scores, int renorm, float scale, int vec) {
+route_backward_kernel(const T* logits, const int32_t* ids, const float* dweights,
+                      T* dlogits, int rows, int E, int k, int sigmoid_scores, int renorm, float scale, int vec) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int t = static_cast<int>(blockIdx.x) * ROUTE_WARPS + warp;
     grid_dependency_wait();
     grid_launch_dependents();
     if (t >= rows) return;
     const T* row = logits + static_cast<size_t>(t) * E;
-    int e = lane < k ? __ldg(ids + static_cast<size_t>(t) * k + lane) : -1;
+    int e = lane < k ? ld_input(ids + static_cast<size_t>(t) * k + lane) : -1;
     const bool open = e >= 0 && e < E;
-    const float dw = open ? __ldg(dweights + static_cast<size_t>(t) * k + lane) * scale : 0.f;
+    const float dw = open ? ld_input(dweights + static_cast<size_t>(t) * k + lane) * scale : 0.f;
     float mine = open ? to_f32(row[e]) : -INFINITY;
     if (!(mine > -INFINITY)) mine = -INFINITY;            // NaN is not selectable either
     mine = finite_top(mine);
@@ -446,8 +446,8 @@ __device__ __forceinline__ void load_group(const T* row, int E, int e0, bool the
 
 template <int VPL, typename T>
 __global__ void __launch_bounds__(32 * ROUTE_WARPS)
-route_few_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int32_t* __restrict__ ids,
-                 float* __restrict__ weights, int rows, int E, int k, int sigmoid_scores, int renorm, float scale) {
+route_few_kernel(const T* logits, const float* bias, int32_t* ids,
+                 float* weights, int rows, int E, int k, int sigmoid_scores, int renorm, float scale) {
     __shared__ float s_logit[ROUTE_WARPS][GROUP_ROWS][32];       // of the selected experts, in order
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane / GROUP, l8 = lane % GROUP;
     const int t = (static_cast<int>(blockIdx.x) * ROUTE_WARPS + warp) * GROUP_ROWS + g;
@@ -472,7 +472,7 @@ route_few_kernel(const T* __restrict__ logits, const float* __restrict__ bias, i
     }
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-        v[i] = bias != nullptr && l[i] > -INFINITY ? sigmoid(l[i]) + __ldg(bias + e0 + i) : l[i];
+        v[i] = bias != nullptr && l[i] > -INFINITY ? sigmoid(l[i]) + ld_input(bias + e0 + i) : l[i];
         if (!(v[i] > -INFINITY)) v[i] = -INFINITY;          // a NaN of the bias
     }
 
@@ -518,8 +518,8 @@ route_few_kernel(const T* __restrict__ logits, const float* __restrict__ bias, i
 //   softmax        p (add - dot), dot = sum(p add)      sigmoid   p (1 - p) add
 template <int VPL, typename T>
 __global__ void __launch_bounds__(32 * ROUTE_WARPS)
-route_few_backward_kernel(const T* __restrict__ logits, const int32_t* __restrict__ ids, const float* __restrict__ dweights,
-                          T* __restrict__ dlogits, int rows, int E, int k, int sigmoid_scores, int renorm, float scale) {
+route_few_backward_kernel(const T* logits, const int32_t* ids, const float* dweights,
+                          T* dlogits, int rows, int E, int k, int sigmoid_scores, int renorm, float scale) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane / GROUP, l8 = lane % GROUP;
     const int t = (static_cast<int>(blockIdx.x) * ROUTE_WARPS + warp) * GROUP_ROWS + g;
     grid_dependency_wait();
@@ -535,8 +535,8 @@ route_few_backward_kernel(const T* __restrict__ logits, const int32_t* __restric
         int e = -1;
         float dw = 0.f;
         if (there && j0 + l8 < k) {
-            e = __ldg(ids + static_cast<size_t>(t) * k + j0 + l8);
-            dw = __ldg(dweights + static_cast<size_t>(t) * k + j0 + l8) * scale;
+            e = ld_input(ids + static_cast<size_t>(t) * k + j0 + l8);
+            dw = ld_input(dweights + static_cast<size_t>(t) * k + j0 + l8) * scale;
         }
 #pragma unroll
         for (int j = 0; j < GROUP; ++j) {
@@ -596,15 +596,15 @@ static_assert(another_row(0, 8, 9) && !another_row(0, 8, 8) && !another_row(INT_
 
 template <typename T>
 __global__ void __launch_bounds__(32 * ROUTE_WARPS, 8)
-route_lane_kernel(const T* __restrict__ logits, const float* __restrict__ bias, int32_t* __restrict__ ids,
-                  float* __restrict__ weights, int rows, int E, int k, int sigmoid_scores, int renorm, float scale) {
+route_lane_kernel(const T* logits, const float* bias, int32_t* ids,
+                  float* weights, int rows, int E, int k, int sigmoid_scores, int renorm, float scale) {
     const int lane = threadIdx.x & 31, stride = static_cast<int>(gridDim.x) * ROUTE_WARPS;
     int t = static_cast<int>(blockIdx.x) * ROUTE_WARPS + static_cast<int>(threadIdx.x >> 5);
     grid_dependency_wait();
     grid_launch_dependents();
     if (t >= rows) return;
     const bool mine = lane < E;
-    const float b = bias != nullptr && mine ? __ldg(bias + lane) : 0.f;
+    const float b = bias != nullptr && mine ? ld_input(bias + lane) : 0.f;
     float next = mine ? to_f32(logits[static_cast<size_t>(t) * E + lane]) : -INFINITY;
     for (bool more = true; more; t += more ? stride : 0) {
         const float l = next > -INFINITY ? finite_top(next) : -INFINITY;        // (NaN cannot be selected either)
@@ -646,8 +646,8 @@ route_lane_kernel(const T* __restrict__ logits, const float* __restrict__ bias, 
 // The gradient by expert, as route_few_backward_kernel's.
 template <typename T>
 __global__ void __launch_bounds__(32 * ROUTE_WARPS, 8)
-route_lane_backward_kernel(const T* __restrict__ logits, const int32_t* __restrict__ ids, const float* __restrict__ dweights,
-                           T* __restrict__ dlogits, int rows, int E, int k, int sigmoid_scores, int renorm, float scale) {
+route_lane_backward_kernel(const T* logits, const int32_t* ids, const float* dweights,
+                           T* dlogits, int rows, int E, int k, int sigmoid_scores, int renorm, float scale) {
     const int lane = threadIdx.x & 31, stride = static_cast<int>(gridDim.x) * ROUTE_WARPS;
     int t = static_cast<int>(blockIdx.x) * ROUTE_WARPS + static_cast<int>(threadIdx.x >> 5);
     grid_dependency_wait();
@@ -660,8 +660,8 @@ route_lane_backward_kernel(const T* __restrict__ logits, const int32_t* __restri
         int e = -1;
         float dw = 0.f;
         if (lane < k) {
-            e = __ldg(ids + static_cast<size_t>(t) * k + lane);
-            dw = __ldg(dweights + static_cast<size_t>(t) * k + lane) * scale;
+            e = ld_input(ids + static_cast<size_t>(t) * k + lane);
+            dw = ld_input(dweights + static_cast<size_t>(t) * k + lane) * scale;
         }
         const float l = x > -INFINITY ? finite_top(x) : -INFINITY;
         float add = 0.f, named = 0.f;

@@ -68,3 +68,17 @@ def test_workspaces_are_zeroed_only_where_a_first_call_reads(monkeypatch):
     for ws, n in ((dg.moe_layer_workspace(64, 8, 16, 1024, 512, device="cpu"), zeroed["DG_MOE_LAYER_ZEROED"]),
                   (dg.epilogue_backward_workspace(700, 512, device="cpu"), zeroed["DG_EPILOGUE_BACKWARD_ZEROED"])):
         assert ws.numel() > 2 * n and not ws[:n].any() and (ws[n:] == 0xFF).all()
+
+
+def test_kernels_that_start_early_do_not_read_through_the_read_only_path():
+    # a kernel launched to overlap the previous grid's end may not take data that this grid still writes for constant
+    import os
+    import re
+    csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "moe_grouped_gemm_tma_gb300", "csrc")
+    early = []
+    for f in sorted(os.listdir(csrc)):
+        text = re.sub(r"//[^\n]*", "", open(os.path.join(csrc, f)).read())
+        if re.search(r"\bgrid_dependency_wait\(\);", text):
+            early.append(f)
+            assert not re.search(r"__ldg\(|__restrict__|ld\.global\.nc|__ldcs\(", text), f
+    assert {"dg_kernel.cuh", "dg_kernel_decode.cuh", "dg_kernel_bs.cuh", "dg_route.cu", "dg_epilogue_backward.cu"} <= set(early)
