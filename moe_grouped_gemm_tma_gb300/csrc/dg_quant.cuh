@@ -182,7 +182,7 @@ __device__ __forceinline__ float slope_of(float z, float g) { return z < 0.f ? g
 // good as FP32 operations that round once each make them: over every BF16 pre-activation within 30 the largest error is
 // 1.4e-7 (SILU) and 1.2e-7 (both GELUs), and of 134 M codes 336, 372 and 359 (SILU, GELU_TANH, GELU) differ from the
 // definition in 64 bits, where the definition in FP32 has 318, 623 and 389. Without the Newton steps and with the tail
-// of act_value2 the errors are 1.6e-7 to 2.0e-7, and 4096 x 7168 takes 37.9, 44.4 and 45.7 us for 39.1, 46.4 and 46.8.
+// of act_value2 the errors are 1.6e-7 to 2.0e-7, and 4096 x 7168 takes 37.9, 44.4 and 45.7 us for 39.3, 47.6 and 46.7.
 template <int ACT>
 __device__ __forceinline__ float2 act_slope2(float2 z) {
     const float2 one = make_float2(1.f, 1.f), minus = make_float2(-1.f, -1.f);
