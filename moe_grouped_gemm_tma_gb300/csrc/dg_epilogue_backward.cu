@@ -17,7 +17,7 @@
 // second launch gives 42.0 and 31.1; at 333 x 2048 it gives 5.4 for 5.8 us, less than the launch costs the host.
 //
 // Floor: 4 bytes read and 2 written per element (2 read without an activation), 26.6 us for 4096 x 7168 at the
-// measured copy bandwidth. It takes 39.3 us: 68% of the issue slots, loads whose latency two CTAs an SM hide only
+// measured copy bandwidth. It takes 39.3 us: 67% of the issue slots, loads whose latency two CTAs an SM hide only
 // in part, and two barriers a tile, because the two scalings need the whole tile's maxima between the loads and the
 // stores. (A persistent form with the next tile's operands in shared memory by TMA was 7 us slower; without the exact
 // divisions of the codes it would be 1 us faster.)
