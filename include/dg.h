@@ -158,8 +158,8 @@ dg_status dg_wgrad_fp8_nt(const uint8_t* A, const float* sfa, const uint8_t* B, 
  * GELU_TANH its tanh form, SILU z / (1 + exp(-z)). */
 enum { DG_ACT_NONE = 0, DG_ACT_RELU = 1, DG_ACT_GELU = 2, DG_ACT_GELU_TANH = 3, DG_ACT_SILU = 4 };
 
-/* Element types of the router's logits. */
-enum { DG_TYPE_BF16 = 0, DG_TYPE_F32 = 1 };
+/* Element types: of the router's logits and a norm's weights (BF16, F32), of the rows of dg_moe_gather (BF16, E4M3). */
+enum { DG_TYPE_BF16 = 0, DG_TYPE_F32 = 1, DG_TYPE_E4M3 = 2 };
 
 /* Router scores. */
 enum { DG_SCORE_SOFTMAX = 0, DG_SCORE_SIGMOID = 1 };
@@ -248,6 +248,122 @@ dg_status dg_moe_layer(const void* x, const int32_t* ids, const float* weights, 
                        const uint8_t* W2, const float* s2, const void* residual, void* out, void* workspace,
                        int64_t workspace_bytes, int T, int k, int E, int H, int I, int act, cudaStream_t stream);
 int64_t dg_moe_layer_workspace(int T, int k, int E, int H, int I);
+
+/* ------------------------------------------------- between the grouped products (prefill and training) */
+
+/*
+ * Tokens by expert: the row that each routed slot has in a grouped layout. ids [T, k] int32 as dg_moe_route gives them; an
+ * id outside [0, E) has no row (-1). An expert's rows are in the order of its slots (t, then j), whatever the timing.
+ *   rows    [T, k] int32
+ *   counts, masked_m  [E] int32: the slots of each expert
+ * Contiguous (dg_m_grouped_contiguous): the experts one after the other, each from a multiple of 128 on.
+ *   m_indices [Mt] int32, 16-byte aligned: the expert of each row, -1 where there is none. Mt a multiple of 128, at least
+ *   dg_moe_sort_rows(T, k, E), which every routing fits (DG_UNSUPPORTED_SHAPE otherwise). The rows in use end with the
+ *   last expert's block: a caller that knows the counts may pass later calls that many rows.
+ * Masked (dg_m_grouped_masked): expert e from row e * max_m on. Slots past max_m get no row (-1) and masked_m still counts
+ *   them; the product and dg_glu take no more than max_m.
+ * 1 <= E <= 1024, k <= 32, T * k <= 2^23, E * max_m < 2^31.
+ * workspace: device memory of dg_moe_sort_workspace(T, k, E) bytes, 16-byte aligned, with anything in it; 0 bytes (and null)
+ * up to 4096 slots. dg_moe_sort_rows and dg_moe_sort_workspace return -1 for sizes outside these.
+ */
+dg_status dg_moe_sort_contiguous(const int32_t* ids, int32_t* rows, int32_t* counts, int32_t* m_indices, void* workspace,
+                                 int64_t workspace_bytes, int T, int k, int E, int Mt, cudaStream_t stream);
+dg_status dg_moe_sort_masked(const int32_t* ids, int32_t* rows, int32_t* masked_m, void* workspace, int64_t workspace_bytes,
+                             int T, int k, int E, int max_m, cudaStream_t stream);
+int64_t dg_moe_sort_rows(int T, int k, int E);
+int64_t dg_moe_sort_workspace(int T, int k, int E);
+
+/*
+ * The tokens' rows in a grouped layout: out[rows[t,j]] = x[t] for every slot whose row is in [0, Mt); no two slots may have
+ * the same one.
+ *   x_type DG_TYPE_E4M3   x [T, H], out [Mt, H] codes; sf [T, H/128], out_sf [Mt, H/128]; H a multiple of 128
+ *   x_type DG_TYPE_BF16   x [T, H], out [Mt, H] bf16; sf, out_sf null; H a multiple of 8
+ *   m_indices [Mt] of the contiguous layout, or null. With it the rows without a token in a block of 128 that has some are
+ *   zeros (of scale 1e-4 / 448), so that a weight gradient over the padded segments adds nothing for them. All other rows
+ *   stay as they were. Mt is then a multiple of 128.
+ * x and out 16-byte aligned, k <= 32. Its gradient is dg_moe_combine without weights.
+ */
+dg_status dg_moe_gather(const void* x, const float* sf, int x_type, const int32_t* rows, const int32_t* m_indices, void* out, float* out_sf,
+                        int T, int k, int H, int Mt, cudaStream_t stream);
+
+/*
+ * The way back: out[t] = residual[t] + sum_j weights[t,j] * y[rows[t,j]], over the slots whose row is in [0, Mt).
+ *   y [Mt, H] bf16, weights [T, k] fp32 or null (1), residual [T, H] bf16 or null, may be out; out [T, H] bf16
+ * FP32 sums in the order of j, the residual last, rounded once. H a multiple of 8, k <= 32; y, residual and out 16-byte aligned.
+ */
+dg_status dg_moe_combine(const void* y, const int32_t* rows, const float* weights, const void* residual, void* out, int T, int k,
+                         int H, int Mt, cudaStream_t stream);
+
+/*
+ * Its gradient (the residual's is dout itself):
+ *   dy       [Mt, H] bf16, or null: dy[rows[t,j]] = weights[t,j] * dout[t]; with m_indices zeros as in dg_moe_gather, other
+ *            rows as they were
+ *   dweights [T, k] fp32, or null: the product of y[rows[t,j]] and dout[t], 0 for a slot without a row. Needs y.
+ * weights null: 1. H a multiple of 8, k <= 32; dout, y and dy 16-byte aligned; dy must not overlap y.
+ */
+dg_status dg_moe_combine_backward(const void* dout, const void* y, const int32_t* rows, const float* weights, const int32_t* m_indices, void* dy,
+                                  float* dweights, int T, int k, int H, int Mt, cudaStream_t stream);
+
+/*
+ * Root-mean-square norm with the residual's addition:
+ *   s = bf16(x + residual),   y = s * rsqrt(mean(s^2) + eps) * weight
+ *   x [T, H] bf16, residual [T, H] bf16 or null, weight [H] of weight_type (BF16 or F32)
+ *   sum [T, H] bf16, or null: s, the next residual; may be x or residual
+ *   y   [T, H] bf16, or null; may be x
+ *   q   [T, H] e4m3, sf [T, H/128] fp32, or both null: y quantised (before its rounding to BF16) as in
+ *       dg_epilogue_backward; with pow2 the scale is the power of two above that scale, as the UE8M0 path takes it.
+ *       H a multiple of 128 then.
+ * Sums are FP32. H a multiple of 8 up to 16384, eps >= 0; weight and the matrices 16-byte aligned.
+ */
+dg_status dg_rmsnorm(const void* x, const void* residual, const void* weight, int weight_type, void* sum, void* y, uint8_t* q, float* sf,
+                     int pow2, int T, int H, float eps, cudaStream_t stream);
+
+/*
+ * Its gradient. x is s, what the norm was of (the kept sum); with r = rsqrt(mean(x^2) + eps):
+ *   dx      [T, H] bf16 = r * (weight * dy - x * r^2 * mean(weight * dy * x)) + dsum: of x and of the residual alike; may be
+ *           dy, x or dsum
+ *   dsum    [T, H] bf16, or null: the gradient that reaches the sum by other ways
+ *   dweight [H] fp32, or null: the sum over the rows of dy * x * r, in a fixed order; 0 for T = 0
+ * workspace: device memory of dg_rmsnorm_backward_workspace(T, H) bytes (-1 for sizes outside the range), 16-byte aligned, with
+ * anything in it, needed for dweight.
+ */
+dg_status dg_rmsnorm_backward(const void* dy, const void* x, const void* weight, int weight_type, const void* dsum, void* dx, float* dweight,
+                              void* workspace, int64_t workspace_bytes, int T, int H, float eps, cudaStream_t stream);
+int64_t dg_rmsnorm_backward_workspace(int T, int H);
+
+/*
+ * The gated activation between the two products of an expert (or of a dense layer), quantised for the second:
+ *   h = act(g) * u,   (g; u) = Z's columns [0, I) and [I, 2I)
+ *   Z    [M, 2I] bf16
+ *   q    [M, I] e4m3, sf [M, I/128]: h before any rounding; pow2 as in dg_rmsnorm
+ *   kept [M, 2I] e4m3, kept_sf [M, 2I/128], or both null: Z quantised, what dg_glu_backward takes instead of Z
+ * At most one of (which rows are computed; all others stay as they were):
+ *   m_indices [M] of the contiguous layout: the blocks of 128 rows whose first row has an expert. M a multiple of 128 then.
+ *   masked_m  [G] of the masked layout [G, M/G, 2I]: the first masked_m[g] rows of each group, at most M/G
+ * I a multiple of 128; Z, q and kept 16-byte aligned; no output overlaps Z.
+ */
+dg_status dg_glu(const void* Z, uint8_t* q, float* sf, uint8_t* kept, float* kept_sf, const int32_t* m_indices, const int32_t* masked_m, int G,
+                 int act, int pow2, int M, int I, cudaStream_t stream);
+
+/*
+ * Its backward pass, from Z or from the kept codes (one of them; the other null): dg = dH * u * act'(g), du = dH * act(g).
+ *   dH [M, I] bf16 (not read, and may be null, without q and qt)
+ *   q  [M, 2I] e4m3,   sf  [M, 2I/128]    (dg; du), 1x128 scales along 2I: A of the product that gives the input's gradient
+ *   qt [2I, Mp] e4m3,  sft [2I, Mp/128]   the transpose, 1x128 scales along M, Mp = M rounded up to 128, zeros past M
+ *   ht [I, Mp] e4m3,   hsft [I, Mp/128]   h's transpose, so quantised: an operand of the second product's weight gradient
+ * q with sf, qt with sft, ht with hsft may each be null. The values are those of Z, or of the codes times their scales; every
+ * row is computed. I a multiple of 128, M free; matrices 16-byte aligned.
+ */
+dg_status dg_glu_backward(const void* dH, const void* Z, const uint8_t* kept, const float* kept_sf, int act, uint8_t* q, float* sf, uint8_t* qt,
+                          float* sft, uint8_t* ht, float* hsft, int M, int I, cudaStream_t stream);
+
+/*
+ * The values of 8-bit codes quantised along the other axis: from q [M, N] e4m3 with sf [M, N/128], what a forward product
+ * read, to qt [N, Mp] with sft [N, Mp/128] (Mp = M rounded up to 128, zeros past M), an operand of dg_wgrad_fp8_nt or
+ * dg_k_grouped_wgrad: the 8-bit codes are all that has to be kept of an activation for its weight gradient. The value of a
+ * code is its product with its scale, rounded to FP32. N a multiple of 128, M free; q and qt 16-byte aligned.
+ */
+dg_status dg_transpose_fp8(const uint8_t* q, const float* sf, uint8_t* qt, float* sft, int M, int N, cudaStream_t stream);
 
 /* Human-readable name of a status code (static storage). */
 const char* dg_status_string(dg_status status);

@@ -9,7 +9,9 @@ Operation (DeepGEMM pages, "DeepSeek DeepGEMM" usage example and feature list):
 ``D[m,n] = sum_kb sfa[m,kb] * sfb[n//128,kb] * sum_{k in block kb} A[m,k] B[n,k]`` with e4m3 A/B,
 FP32 1x128 (A) and 128x128 (B) block scales, BF16 output; plus the m-grouped contiguous and masked
 layouts and the k-grouped FP32 weight gradient. Around them: the router, a whole MoE layer for a few
-tokens, and the GEMM with bias, activation and residual in its epilogue, with its backward pass.
+tokens, and the GEMM with bias, activation and residual in its epilogue, with its backward pass. Between the grouped
+products, for prefill and training: tokens sorted by expert and back, the norm before them, the gated activation, and
+activations kept in 8 bits.
 """
 from __future__ import annotations
 
@@ -24,6 +26,9 @@ __all__ = [
     "dg_k_grouped_wgrad", "dg_wgrad_fp8_nt", "dg_gemm_fp8_nt_epilogue", "dg_epilogue_backward",
     "dg_moe_route", "dg_moe_route_backward", "dg_moe_layer",
     "epilogue_backward_workspace", "moe_layer_workspace", "ACTIVATIONS", "SCORES",
+    "dg_moe_sort_contiguous", "dg_moe_sort_masked", "dg_moe_gather", "dg_moe_combine", "dg_moe_combine_backward",
+    "dg_rmsnorm", "dg_rmsnorm_backward", "dg_glu", "dg_glu_backward", "dg_transpose_fp8",
+    "moe_sort_rows", "moe_sort_workspace", "rmsnorm_backward_workspace",
     "dg_device_status", "dg_status_string", "scale_shapes", "library_path",
     "TUNE_KNOBS", "dg_tuning_set", "dg_tuning_get", "dg_tuning_reset", "tuning", "dg_testing_arm_wait_timeout",
     "FAULTS", "dg_testing_arm_fault",
@@ -77,6 +82,19 @@ def load(build_if_missing: bool = True):
             L.dg_epilogue_backward_workspace.argtypes = [I, I]
             L.dg_moe_layer_workspace.argtypes = [I, I, I, I, I]
             L.dg_epilogue_backward_workspace.restype = L.dg_moe_layer_workspace.restype = S
+            L.dg_moe_sort_contiguous.argtypes = [P, P, P, P, P, S, I, I, I, I, P]
+            L.dg_moe_sort_masked.argtypes = [P, P, P, P, S, I, I, I, I, P]
+            L.dg_moe_gather.argtypes = [P, P, I, P, P, P, P, I, I, I, I, P]
+            L.dg_moe_combine.argtypes = [P, P, P, P, P, I, I, I, I, P]
+            L.dg_moe_combine_backward.argtypes = [P, P, P, P, P, P, P, I, I, I, I, P]
+            L.dg_rmsnorm.argtypes = [P, P, P, I, P, P, P, P, I, I, I, F, P]
+            L.dg_rmsnorm_backward.argtypes = [P, P, P, I, P, P, P, P, S, I, I, F, P]
+            L.dg_glu.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, P]
+            L.dg_glu_backward.argtypes = [P, P, P, P, I, P, P, P, P, P, P, I, I, P]
+            L.dg_transpose_fp8.argtypes = [P, P, P, P, I, I, P]
+            L.dg_moe_sort_rows.argtypes = L.dg_moe_sort_workspace.argtypes = [I, I, I]
+            L.dg_rmsnorm_backward_workspace.argtypes = [I, I]
+            L.dg_moe_sort_rows.restype = L.dg_moe_sort_workspace.restype = L.dg_rmsnorm_backward_workspace.restype = S
             L.dg_device_status.argtypes = [P]
             L.dg_tuning_set.argtypes = [I, I]
             L.dg_tuning_set.restype = I
@@ -93,7 +111,9 @@ def load(build_if_missing: bool = True):
             for f in ("dg_gemm_fp8_nt", "dg_gemm_fp8", "dg_gemm_fp8_nt_ue8m0", "dg_gemm_fp8_nt_ue8m0_packed",
                       "dg_m_grouped_contiguous", "dg_m_grouped_masked",
                       "dg_k_grouped_wgrad", "dg_wgrad_fp8_nt", "dg_gemm_fp8_nt_epilogue", "dg_epilogue_backward",
-                      "dg_moe_route", "dg_moe_route_backward", "dg_moe_layer", "dg_device_status"):
+                      "dg_moe_route", "dg_moe_route_backward", "dg_moe_layer", "dg_moe_sort_contiguous",
+                      "dg_moe_sort_masked", "dg_moe_gather", "dg_moe_combine", "dg_moe_combine_backward", "dg_rmsnorm",
+                      "dg_rmsnorm_backward", "dg_glu", "dg_glu_backward", "dg_transpose_fp8", "dg_device_status"):
                 getattr(L, f).restype = I
             _lib = L
     return _lib
@@ -506,6 +526,282 @@ def dg_moe_layer(x, ids, weights, W13, s13, W2, s2, out, workspace, act="silu", 
     if st:
         raise DGError(st, "dg_moe_layer")
     return out
+
+
+# The calls between the grouped products check their arguments in one expression too, and that all of them are on the
+# current device, where the launch goes.
+def _here(stream, device):
+    """The stream's handle; the tensors' device has to be the current one."""
+    c = _torch()._C
+    if device != c._cuda_getDevice():
+        raise ValueError(f"the tensors are on cuda:{device}, the current device is cuda:{c._cuda_getDevice()}")
+    return c._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
+
+
+def _fits(t, dtype, shape, device):
+    return t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous()
+
+
+def _refuse_here(device, **args):
+    _refuse(**args)
+    for name, (t, _, _) in args.items():
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"{name} is on {t.device}, the first argument on cuda:{device}")
+
+
+def moe_sort_rows(T: int, k: int, E: int) -> int:
+    """Rows of the contiguous layout (a multiple of 128) that every routing of T tokens to k of E experts fits."""
+    rows = load().dg_moe_sort_rows(T, k, E)
+    if rows < 0:
+        raise DGError(2, "dg_moe_sort_rows")
+    return rows
+
+
+def moe_sort_workspace(T: int, k: int, E: int, device=None):
+    """A workspace for the sorts of up to T tokens to k of E experts; empty where they need none."""
+    size = load().dg_moe_sort_workspace(T, k, E)
+    if size < 0:
+        raise DGError(2, "dg_moe_sort_workspace")
+    return _workspace(size, 0, device)
+
+
+def dg_moe_sort_contiguous(ids, rows, counts, m_indices, workspace=None, stream=None):
+    """rows int32 [T,k]: where each slot of ids int32 [T,k] goes in the contiguous layout of m_indices int32 [Mt] (written
+    too), -1 for an id outside [0,E); counts int32 [E]: the experts' slots. Mt: moe_sort_rows(T, k, E) or more."""
+    torch = _torch_module or _torch()
+    i32 = torch.int32
+    Tk = T, k = ids.shape
+    E, Mt = counts.shape[0], m_indices.shape[0]
+    dev = ids.get_device()
+    if not (_fits(ids, i32, Tk, dev) and _fits(rows, i32, Tk, dev) and _fits(counts, i32, (E,), dev) and _fits(m_indices, i32, (Mt,), dev) and dev >= 0):
+        _refuse_here(dev, ids=(ids, (i32,), None), rows=(rows, (i32,), Tk), counts=(counts, (i32,), (E,)), m_indices=(m_indices, (i32,), (Mt,)))
+    ws, size = _bytes(workspace, "workspace")
+    st = (_lib or load()).dg_moe_sort_contiguous(ids.data_ptr(), rows.data_ptr(), counts.data_ptr(), m_indices.data_ptr(), ws, size, T, k, E, Mt,
+                                                 _here(stream, dev))
+    if st:
+        raise DGError(st, "dg_moe_sort_contiguous")
+    return rows
+
+
+def dg_moe_sort_masked(ids, rows, masked_m, max_m: int, workspace=None, stream=None):
+    """rows int32 [T,k]: where each slot of ids int32 [T,k] goes in the masked layout of max_m rows an expert, -1 for an id
+    outside [0,E) and past max_m; masked_m int32 [E]: the experts' slots (which may be more than max_m)."""
+    torch = _torch_module or _torch()
+    i32 = torch.int32
+    Tk = T, k = ids.shape
+    E = masked_m.shape[0]
+    dev = ids.get_device()
+    if not (_fits(ids, i32, Tk, dev) and _fits(rows, i32, Tk, dev) and _fits(masked_m, i32, (E,), dev) and dev >= 0):
+        _refuse_here(dev, ids=(ids, (i32,), None), rows=(rows, (i32,), Tk), masked_m=(masked_m, (i32,), (E,)))
+    ws, size = _bytes(workspace, "workspace")
+    st = (_lib or load()).dg_moe_sort_masked(ids.data_ptr(), rows.data_ptr(), masked_m.data_ptr(), ws, size, T, k, E, max_m, _here(stream, dev))
+    if st:
+        raise DGError(st, "dg_moe_sort_masked")
+    return rows
+
+
+def dg_moe_gather(x, sf, rows, out, out_sf=None, m_indices=None, stream=None):
+    """out[rows[t,j]] = x[t]: the tokens' rows in a grouped layout, e4m3 [T,H] with scales sf fp32 [T,H/128] to out [Mt,H] and
+    out_sf [Mt,H/128], or bf16 [T,H] (sf and out_sf None). out may have the masked layout's shape [E,max_m,H] and out_sf
+    its [E,max_m,H/128]. With m_indices int32 [Mt] the rows without a token in a block that has some are zeroed."""
+    torch = _torch_module or _torch()
+    i32, f32, bf16, e4m3 = torch.int32, torch.float32, torch.bfloat16, (torch.float8_e4m3fn, torch.uint8)
+    T, H = x.shape
+    Tk = T, k = rows.shape[0], rows.shape[1]
+    codes = x.dtype is not bf16
+    dev = x.get_device()
+    lead = out.shape[:-1]
+    Mt = lead.numel()
+    if not (x.is_contiguous() and dev >= 0 and x.shape[0] == T and _fits(rows, i32, Tk, dev) and out.shape[-1] == H and out.get_device() == dev
+            and out.is_contiguous() and (m_indices is None or _fits(m_indices, i32, (Mt,), dev))
+            and ((x.dtype in e4m3 and out.dtype in e4m3 and sf is not None and out_sf is not None and _fits(sf, f32, (T, H // 128), dev)
+                  and _fits(out_sf, f32, (*lead, H // 128), dev)) if codes else (out.dtype is bf16 and sf is None and out_sf is None))):
+        if codes and x.dtype not in e4m3:
+            raise TypeError(f"x must be float8_e4m3fn, uint8 or bfloat16, got {x.dtype}")
+        _refuse_here(dev, x=(x, e4m3 if codes else (bf16,), None), rows=(rows, (i32,), (x.shape[0], k)), out=(out, e4m3 if codes else (bf16,), (*lead, H)),
+                     sf=(sf, (f32,), (T, H // 128)), out_sf=(out_sf, (f32,), (*lead, H // 128)), m_indices=(m_indices, (i32,), (Mt,)))
+        raise ValueError("sf and out_sf go with e4m3 rows, and with them only")
+    st = (_lib or load()).dg_moe_gather(x.data_ptr(), None if sf is None else sf.data_ptr(), 2 if codes else 0, rows.data_ptr(),
+                                        None if m_indices is None else m_indices.data_ptr(), out.data_ptr(), None if out_sf is None else out_sf.data_ptr(),
+                                        T, k, H, Mt, _here(stream, dev))
+    if st:
+        raise DGError(st, "dg_moe_gather")
+    return out
+
+
+def dg_moe_combine(y, rows, out, weights=None, residual=None, stream=None):
+    """out[t] = residual[t] + sum_j weights[t,j] y[rows[t,j]]: y bf16 [Mt,H] (or [E,max_m,H]), rows int32 [T,k] (outside [0,Mt):
+    nothing), weights fp32 [T,k] (None: 1), residual and out bf16 [T,H]."""
+    torch = _torch_module or _torch()
+    i32, f32, bf16 = torch.int32, torch.float32, torch.bfloat16
+    Tk = T, k = rows.shape
+    H = y.shape[-1]
+    Mt = y.shape[:-1].numel()
+    TH = (T, H)
+    dev = y.get_device()
+    if not (y.dtype is bf16 and y.is_contiguous() and dev >= 0 and _fits(rows, i32, Tk, dev) and _fits(out, bf16, TH, dev)
+            and (weights is None or _fits(weights, f32, Tk, dev)) and (residual is None or _fits(residual, bf16, TH, dev))):
+        _refuse_here(dev, y=(y, (bf16,), None), rows=(rows, (i32,), None), out=(out, (bf16,), TH), weights=(weights, (f32,), Tk), residual=(residual, (bf16,), TH))
+    st = (_lib or load()).dg_moe_combine(y.data_ptr(), rows.data_ptr(), None if weights is None else weights.data_ptr(),
+                                         None if residual is None else residual.data_ptr(), out.data_ptr(), T, k, H, Mt, _here(stream, dev))
+    if st:
+        raise DGError(st, "dg_moe_combine")
+    return out
+
+
+def dg_moe_combine_backward(dout, rows, dy, weights=None, y=None, dweights=None, m_indices=None, stream=None):
+    """dy[rows[t,j]] = weights[t,j] dout[t] (bf16 [Mt,H], or None) and dweights[t,j] = y[rows[t,j]] . dout[t] (fp32 [T,k], or
+    None; needs y bf16 [Mt,H]). With m_indices int32 [Mt] the rows of dy without a token in a block that has some are zeroed."""
+    torch = _torch_module or _torch()
+    i32, f32, bf16 = torch.int32, torch.float32, torch.bfloat16
+    Tk = T, k = rows.shape
+    H = dout.shape[-1]
+    if y is None and dy is None:
+        raise ValueError("dy, or dweights with y, has to be given")
+    like = y if dy is None else dy
+    lead = like.shape[:-1]
+    Mt = lead.numel()
+    MH = (*lead, H)
+    dev = dout.get_device()
+    if not (_fits(dout, bf16, (T, H), dev) and dev >= 0 and _fits(rows, i32, Tk, dev) and (dy is None or _fits(dy, bf16, MH, dev))
+            and (weights is None or _fits(weights, f32, Tk, dev)) and (y is None or _fits(y, bf16, MH, dev))
+            and (dweights is None or _fits(dweights, f32, Tk, dev)) and (m_indices is None or _fits(m_indices, i32, (Mt,), dev))):
+        _refuse_here(dev, dout=(dout, (bf16,), (T, H)), rows=(rows, (i32,), None), dy=(dy, (bf16,), MH), weights=(weights, (f32,), Tk), y=(y, (bf16,), MH),
+                     dweights=(dweights, (f32,), Tk), m_indices=(m_indices, (i32,), (Mt,)))
+    st = (_lib or load()).dg_moe_combine_backward(
+        dout.data_ptr(), None if y is None else y.data_ptr(), rows.data_ptr(), None if weights is None else weights.data_ptr(),
+        None if m_indices is None else m_indices.data_ptr(), None if dy is None else dy.data_ptr(), None if dweights is None else dweights.data_ptr(),
+        T, k, H, Mt, _here(stream, dev))
+    if st:
+        raise DGError(st, "dg_moe_combine_backward")
+
+
+def dg_rmsnorm(x, weight, y=None, q=None, sf=None, residual=None, sum=None, eps=1e-6, pow2=False, stream=None):
+    """s = bf16(x + residual), y = s rsqrt(mean(s^2) + eps) weight, for x, residual bf16 [T,H] and weight bf16 or fp32 [H]:
+    s to sum (bf16 [T,H]), y to y (bf16 [T,H]) and quantised to q (e4m3 [T,H]) with scales sf (fp32 [T,H/128], powers of
+    two with pow2); each may be None. sum may be x or residual, y may be x."""
+    torch = _torch_module or _torch()
+    f32, bf16, e4m3 = torch.float32, torch.bfloat16, (torch.float8_e4m3fn, torch.uint8)
+    TH = T, H = x.shape
+    dev = x.get_device()
+    kind = weight.dtype
+    if not (x.dtype is bf16 and x.is_contiguous() and dev >= 0 and (kind is f32 or kind is bf16) and _fits(weight, kind, (H,), dev)
+            and (residual is None or _fits(residual, bf16, TH, dev)) and (sum is None or _fits(sum, bf16, TH, dev)) and (y is None or _fits(y, bf16, TH, dev))
+            and (q is None or (q.dtype in e4m3 and q.shape == TH and q.get_device() == dev and q.is_contiguous()))
+            and (sf is None or _fits(sf, f32, (T, H // 128), dev))):
+        _refuse_here(dev, x=(x, (bf16,), None), weight=(weight, (bf16, f32), (H,)), residual=(residual, (bf16,), TH), sum=(sum, (bf16,), TH),
+                     y=(y, (bf16,), TH), q=(q, e4m3, TH), sf=(sf, (f32,), (T, H // 128)))
+    st = (_lib or load()).dg_rmsnorm(x.data_ptr(), None if residual is None else residual.data_ptr(), weight.data_ptr(), 1 if kind is f32 else 0,
+                                     None if sum is None else sum.data_ptr(), None if y is None else y.data_ptr(), None if q is None else q.data_ptr(),
+                                     None if sf is None else sf.data_ptr(), 1 if pow2 else 0, T, H, eps, _here(stream, dev))
+    if st:
+        raise DGError(st, "dg_rmsnorm")
+
+
+def rmsnorm_backward_workspace(T: int, H: int, device=None):
+    """A workspace for dg_rmsnorm_backward with dweight at up to T rows of H."""
+    size = load().dg_rmsnorm_backward_workspace(T, H)
+    if size < 0:
+        raise DGError(2, "dg_rmsnorm_backward_workspace")
+    return _workspace(size, 0, device)
+
+
+def dg_rmsnorm_backward(dy, x, weight, dx, dweight=None, workspace=None, dsum=None, eps=1e-6, stream=None):
+    """The norm's gradient from dy bf16 [T,H] at x bf16 [T,H] (the sum that was normalised): dx bf16 [T,H], of x and of the
+    residual alike, with dsum bf16 [T,H] (or None) added; dweight fp32 [H] (or None) needs a workspace
+    (rmsnorm_backward_workspace). dx may be dy, x or dsum."""
+    torch = _torch_module or _torch()
+    f32, bf16 = torch.float32, torch.bfloat16
+    TH = T, H = x.shape
+    dev = x.get_device()
+    kind = weight.dtype
+    if not (x.dtype is bf16 and x.is_contiguous() and dev >= 0 and (kind is f32 or kind is bf16) and _fits(weight, kind, (H,), dev)
+            and _fits(dy, bf16, TH, dev) and _fits(dx, bf16, TH, dev) and (dweight is None or _fits(dweight, f32, (H,), dev))
+            and (dsum is None or _fits(dsum, bf16, TH, dev))):
+        _refuse_here(dev, x=(x, (bf16,), None), weight=(weight, (bf16, f32), (H,)), dy=(dy, (bf16,), TH), dx=(dx, (bf16,), TH),
+                     dweight=(dweight, (f32,), (H,)), dsum=(dsum, (bf16,), TH))
+    ws, size = _bytes(workspace, "workspace")
+    st = (_lib or load()).dg_rmsnorm_backward(dy.data_ptr(), x.data_ptr(), weight.data_ptr(), 1 if kind is f32 else 0, None if dsum is None else dsum.data_ptr(),
+                                              dx.data_ptr(), None if dweight is None else dweight.data_ptr(), ws, size, T, H, eps, _here(stream, dev))
+    if st:
+        raise DGError(st, "dg_rmsnorm_backward")
+    return dx
+
+
+def dg_glu(Z, q, sf, kept=None, kept_sf=None, m_indices=None, masked_m=None, act="silu", pow2=False, stream=None):
+    """h = act(g) u for (g; u) = the halves of Z's rows, bf16 [M,2I] (or [G,max_m,2I]), as e4m3 codes q [M,I] with scales sf fp32
+    [M,I/128]; kept [M,2I] with kept_sf [M,2I/128] (or None) receive Z quantised, for dg_glu_backward. m_indices int32 [M]
+    (contiguous layout) or masked_m int32 [G] (masked layout) say which rows are computed; the others stay as they were."""
+    torch = _torch_module or _torch()
+    i32, f32, bf16, e4m3 = torch.int32, torch.float32, torch.bfloat16, (torch.float8_e4m3fn, torch.uint8)
+    *lead, I2 = Z.shape
+    I = I2 // 2
+    M = Z.shape[:-1].numel()
+    G = 1 if masked_m is None else masked_m.shape[0]
+    dev = Z.get_device()
+    MI, MI2, sMI, sMI2 = (*lead, I), (*lead, I2), (*lead, I // 128), (*lead, I2 // 128)
+    if not (Z.dtype is bf16 and Z.is_contiguous() and dev >= 0 and I2 % 2 == 0 and q.dtype in e4m3 and q.shape == MI and q.get_device() == dev
+            and q.is_contiguous() and _fits(sf, f32, sMI, dev)
+            and (kept is None or (kept.dtype in e4m3 and kept.shape == MI2 and kept.get_device() == dev and kept.is_contiguous()))
+            and (kept_sf is None or _fits(kept_sf, f32, sMI2, dev)) and (m_indices is None or _fits(m_indices, i32, (M,), dev))
+            and (masked_m is None or (_fits(masked_m, i32, (G,), dev) and (len(lead) != 2 or lead[0] == G)))):
+        _refuse_here(dev, Z=(Z, (bf16,), None), q=(q, e4m3, MI), sf=(sf, (f32,), sMI), kept=(kept, e4m3, MI2), kept_sf=(kept_sf, (f32,), sMI2),
+                     m_indices=(m_indices, (i32,), (M,)), masked_m=(masked_m, (i32,), (lead[0],) if len(lead) == 2 else None))
+        raise ValueError(f"Z must have an even number of columns, got {I2}")
+    st = (_lib or load()).dg_glu(Z.data_ptr(), q.data_ptr(), sf.data_ptr(), None if kept is None else kept.data_ptr(),
+                                 None if kept_sf is None else kept_sf.data_ptr(), None if m_indices is None else m_indices.data_ptr(),
+                                 None if masked_m is None else masked_m.data_ptr(), G, _choice(ACTIVATIONS, act, "act"), 1 if pow2 else 0, M, I, _here(stream, dev))
+    if st:
+        raise DGError(st, "dg_glu")
+    return q
+
+
+def dg_glu_backward(dH, q, sf, qt, sft, ht, hsft, Z=None, kept=None, kept_sf=None, act="silu", stream=None):
+    """The gated activation's backward pass from dH bf16 [M,I] and Z bf16 [M,2I] or the codes that dg_glu kept: (dg; du) as e4m3
+    codes q [M,2I] with scales sf [M,2I/128] and of the transpose qt [2I,Mp] with sft [2I,Mp/128] (Mp = M rounded up to 128),
+    and h's transpose ht [I,Mp] with hsft [I,Mp/128]. Each pair may be None."""
+    torch = _torch_module or _torch()
+    f32, bf16, e4m3 = torch.float32, torch.bfloat16, (torch.float8_e4m3fn, torch.uint8)
+    MI = M, I = dH.shape
+    Mp = (M + 127) // 128 * 128
+    dev = dH.get_device()
+
+    def codes(t, shape):
+        return t is None or (t.dtype in e4m3 and t.shape == shape and t.get_device() == dev and t.is_contiguous())
+
+    def scales(t, shape):
+        return t is None or _fits(t, f32, shape, dev)
+
+    if (Z is None) == (kept is None):
+        raise ValueError("one of Z and kept has to be given")
+    if not (_fits(dH, bf16, MI, dev) and dev >= 0 and (Z is None or _fits(Z, bf16, (M, 2 * I), dev)) and codes(kept, (M, 2 * I)) and scales(kept_sf, (M, 2 * I // 128))
+            and codes(q, (M, 2 * I)) and scales(sf, (M, 2 * I // 128)) and codes(qt, (2 * I, Mp)) and scales(sft, (2 * I, Mp // 128))
+            and codes(ht, (I, Mp)) and scales(hsft, (I, Mp // 128))):
+        _refuse_here(dev, dH=(dH, (bf16,), None), Z=(Z, (bf16,), (M, 2 * I)), kept=(kept, e4m3, (M, 2 * I)), kept_sf=(kept_sf, (f32,), (M, 2 * I // 128)),
+                     q=(q, e4m3, (M, 2 * I)), sf=(sf, (f32,), (M, 2 * I // 128)), qt=(qt, e4m3, (2 * I, Mp)), sft=(sft, (f32,), (2 * I, Mp // 128)),
+                     ht=(ht, e4m3, (I, Mp)), hsft=(hsft, (f32,), (I, Mp // 128)))
+    p = _ptr
+    st = (_lib or load()).dg_glu_backward(dH.data_ptr(), p(Z), p(kept), p(kept_sf), _choice(ACTIVATIONS, act, "act"), p(q), p(sf), p(qt), p(sft), p(ht), p(hsft), M, I,
+                                          _here(stream, dev))
+    if st:
+        raise DGError(st, "dg_glu_backward")
+
+
+def dg_transpose_fp8(q, sf, qt, sft, stream=None):
+    """The values of e4m3 codes q [M,N] with scales sf fp32 [M,N/128], quantised along the other axis: qt [N,Mp] with sft [N,Mp/128]
+    (Mp = M rounded up to 128, zeros past M), an operand of dg_wgrad_fp8_nt and dg_k_grouped_wgrad."""
+    torch = _torch_module or _torch()
+    f32, e4m3 = torch.float32, (torch.float8_e4m3fn, torch.uint8)
+    M, N = q.shape
+    Mp = (M + 127) // 128 * 128
+    dev = q.get_device()
+    if not (q.dtype in e4m3 and q.is_contiguous() and dev >= 0 and _fits(sf, f32, (M, N // 128), dev) and qt.dtype in e4m3 and qt.shape == (N, Mp)
+            and qt.get_device() == dev and qt.is_contiguous() and _fits(sft, f32, (N, Mp // 128), dev)):
+        _refuse_here(dev, q=(q, e4m3, None), sf=(sf, (f32,), (M, N // 128)), qt=(qt, e4m3, (N, Mp)), sft=(sft, (f32,), (N, Mp // 128)))
+    st = (_lib or load()).dg_transpose_fp8(q.data_ptr(), sf.data_ptr(), qt.data_ptr(), sft.data_ptr(), M, N, _here(stream, dev))
+    if st:
+        raise DGError(st, "dg_transpose_fp8")
+    return qt
 
 
 def dg_device_status(stream=None) -> int:

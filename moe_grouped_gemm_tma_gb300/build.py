@@ -17,7 +17,8 @@ LIB = os.path.join(OUT_DIR, "libdg.so")
 
 SOURCES = ["dg_api.cu", "dg_inst_normal.cu", "dg_inst_contiguous.cu", "dg_inst_masked.cu", "dg_inst_kgrouped.cu",
            "dg_inst_bs.cu", "dg_inst_decode.cu", "dg_inst_epilogue_64.cu", "dg_inst_epilogue_128.cu",
-           "dg_inst_epilogue_192.cu", "dg_epilogue_backward.cu", "dg_route.cu", "dg_moe_layer.cu"]
+           "dg_inst_epilogue_192.cu", "dg_epilogue_backward.cu", "dg_route.cu", "dg_moe_layer.cu",
+           "dg_tokens.cu", "dg_rmsnorm.cu", "dg_glu.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -60,6 +60,18 @@ __device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits) {
     return b;
 }
 
+// The same with the power of two above the scale (inputs.quantize_1x128 with pow2: 2^e for s = m 2^e, 1/2 <= m < 1).
+// A finite scale is normal, between 2^-23 and 2^120, so its exponent's bits alone give it and its reciprocal.
+__device__ __forceinline__ BlockScale block_scale_pow2(uint32_t amax_bits) {
+    BlockScale b = block_scale(amax_bits);
+    if (amax_bits < 0x7f800000u) {
+        const uint32_t e = (__float_as_uint(b.s) & 0x7f800000u) + 0x00800000u;
+        b.s = b.d = __uint_as_float(e);
+        b.r = __uint_as_float(0x7f000000u - e);
+    }
+    return b;
+}
+
 // Two values to e4m3 codes, `lo` in the low byte (to nearest even, saturating, NaN kept).
 __device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
     uint16_t d;

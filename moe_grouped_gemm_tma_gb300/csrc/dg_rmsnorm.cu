@@ -1,0 +1,383 @@
+// Root-mean-square norm with the residual's addition (dg_rmsnorm), its output quantised for the FP8 products, and its
+// gradient (dg_rmsnorm_backward).
+//
+//   s = bf16(x + residual),  r = rsqrt(mean(s^2) + eps),  y = s r g
+//   dx = r (g dy - s r^2 mean(g dy s)) + dsum,  dg = sum over rows of dy s r
+//
+// A row is in registers from its load to its stores: up to 1024 values a warp has a row of its own, above that a CTA with
+// up to 32 values a thread. A thread's vectors of 8 values are a whole CTA (warp) apart, so that every load covers
+// consecutive memory, and 16 consecutive lanes hold the 128 values of a scaling block.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "dg.h"
+#include "dg_host.cuh"
+#include "dg_ptx.cuh"
+#include "dg_quant.cuh"
+
+namespace dg {
+namespace {
+
+constexpr unsigned FULL = 0xffffffffu;
+constexpr int NORM_VECTORS = 4;                   // vectors of 8 values a thread at most
+constexpr int NORM_MAX_WARPS = 16;
+constexpr int NORM_MAX_H = NORM_MAX_WARPS * 32 * NORM_VECTORS * 8;
+constexpr int NORM_WARP_H = 32 * NORM_VECTORS * 8;   // rows up to this are a warp's
+constexpr int NORM_ROWS = 4;                      // rows of a CTA then
+
+struct NormParams {
+    const uint4* x;
+    const uint4* residual;
+    const void* weight;
+    uint4* sum;
+    uint4* y;
+    uint2* q;
+    float* sf;
+    int rows, vectors, pow2;
+    float inverse, eps;                           // 1 / H
+};
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
+    return v;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float2 a) {
+    uint32_t d;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(a.y), "f"(a.x));
+    return d;
+}
+
+__device__ __forceinline__ uint4 pack_bf16(const float2 (&a)[4]) {
+    return make_uint4(pack_bf16(a[0]), pack_bf16(a[1]), pack_bf16(a[2]), pack_bf16(a[3]));
+}
+
+__device__ __forceinline__ void unpack_bf16(const uint4& v, float2 (&a)[4]) {
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] = make_float2(bf16_lo(u[i]), bf16_hi(u[i]));
+}
+
+// Eight of the norm's weights.
+template <typename W>
+__device__ __forceinline__ void load_weights(const void* weight, int v, float2 (&g)[4]) {
+    if constexpr (sizeof(W) == 2) {
+        unpack_bf16(ld_input(static_cast<const uint4*>(weight) + v), g);
+    } else {
+        const float4 a = ld_input(static_cast<const float4*>(weight) + 2 * v), b = ld_input(static_cast<const float4*>(weight) + 2 * v + 1);
+        g[0] = make_float2(a.x, a.y);
+        g[1] = make_float2(a.z, a.w);
+        g[2] = make_float2(b.x, b.y);
+        g[3] = make_float2(b.z, b.w);
+    }
+}
+
+// The largest magnitude of a lane's eight values.
+__device__ __forceinline__ float abs_max8(const float2 (&a)[4]) {
+    return abs_max(abs_max(a[0].x, a[0].y, a[1].x), abs_max(a[1].y, a[2].x, a[2].y), abs_max(a[3].x, a[3].y));
+}
+
+// ROW_CTA: a row a CTA, else a row a warp; N vectors a thread.
+template <typename W, bool ROW_CTA, int N>
+__global__ void __launch_bounds__(ROW_CTA ? 32 * NORM_MAX_WARPS : 32 * NORM_ROWS) rmsnorm_kernel(const NormParams p) {
+    __shared__ float s_part[NORM_MAX_WARPS];
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int row = static_cast<int>(ROW_CTA ? blockIdx.x : blockIdx.x * NORM_ROWS + warp);
+    if (!ROW_CTA && row >= p.rows) return;
+    const int first = ROW_CTA ? threadIdx.x : lane, step = ROW_CTA ? blockDim.x : 32;
+    const size_t base = static_cast<size_t>(row) * p.vectors;
+
+    uint4 x[N], r[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int v = first + i * step;
+        x[i] = make_uint4(0, 0, 0, 0);
+        r[i] = make_uint4(0, 0, 0, 0);
+        if (v < p.vectors) {
+            x[i] = ld_input(p.x + base + v);
+            if (p.residual != nullptr) r[i] = ld_input(p.residual + base + v);
+        }
+    }
+    float2 squares = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int v = first + i * step;
+        float2 a[4];
+        unpack_bf16(x[i], a);
+        if (p.residual != nullptr) {
+            float2 b[4];
+            unpack_bf16(r[i], b);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) a[c] = __fadd2_rn(a[c], b[c]);
+            x[i] = pack_bf16(a);                  // the sum as it is kept: the norm is of that
+            unpack_bf16(x[i], a);
+        }
+        if (p.sum != nullptr && v < p.vectors) p.sum[base + v] = x[i];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) squares = __ffma2_rn(a[c], a[c], squares);
+    }
+    float total = warp_sum(squares.x + squares.y);
+    if (ROW_CTA) {
+        if (lane == 0) s_part[warp] = total;
+        __syncthreads();
+        total = 0.f;
+        for (int w = 0; w < step / 32; ++w) total += s_part[w];
+    }
+    const float rs = __frsqrt_rn(fmaf(total, p.inverse, p.eps));
+
+    float2 a[N][4];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int v = first + i * step;
+        float2 g[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) g[c] = make_float2(0.f, 0.f);
+        if (v < p.vectors) load_weights<W>(p.weight, v, g);
+        unpack_bf16(x[i], a[i]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) a[i][c] = __fmul2_rn(__fmul2_rn(a[i][c], make_float2(rs, rs)), g[c]);
+        if (p.y != nullptr && v < p.vectors) p.y[base + v] = pack_bf16(a[i]);
+    }
+    if (p.q == nullptr) return;
+    // (a scaling block's 16 lanes are inside the row, or none of them is)
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int v = first + i * step;
+        float m = v < p.vectors ? abs_max8(a[i]) : 0.f;
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) m = abs_max(m, __shfl_xor_sync(FULL, m, o));
+        const BlockScale k = p.pow2 ? block_scale_pow2(abs_bits(m)) : block_scale(abs_bits(m));
+        if (v < p.vectors) {
+            p.q[base + v] = make_uint2(quantise4(a[i][0], a[i][1], k), quantise4(a[i][2], a[i][3], k));
+            if ((lane & 15) == 0) p.sf[static_cast<size_t>(row) * (p.vectors / 16) + v / 16] = k.s;
+        }
+    }
+}
+
+// ------------------------------------------------------------------------------------ gradient
+struct NormBackwardParams {
+    const uint4* dy;
+    const uint4* x;
+    const void* weight;
+    const uint4* dsum;
+    uint4* dx;
+    float* partial;                               // [groups][H] weight gradients of a group's rows
+    int rows, vectors, groups;
+    float inverse, eps;
+};
+
+// A group (a CTA, or a warp) takes every groups-th row and keeps its columns' weight gradient in registers.
+template <typename W, bool ROW_CTA, int N>
+__global__ void __launch_bounds__(ROW_CTA ? 32 * NORM_MAX_WARPS : 32 * NORM_ROWS) rmsnorm_backward_kernel(const NormBackwardParams p) {
+    __shared__ float2 s_part[2][NORM_MAX_WARPS];
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int group = static_cast<int>(ROW_CTA ? blockIdx.x : blockIdx.x * NORM_ROWS + warp);
+    if (!ROW_CTA && group >= p.groups) return;
+    const int first = ROW_CTA ? threadIdx.x : lane, step = ROW_CTA ? blockDim.x : 32;
+
+    float2 g[N][4], dg[N][4];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) g[i][c] = dg[i][c] = make_float2(0.f, 0.f);
+        if (first + i * step < p.vectors) load_weights<W>(p.weight, first + i * step, g[i]);
+    }
+    int turn = 0;
+    for (int row = group; row < p.rows; row += p.groups, turn ^= 1) {
+        const size_t base = static_cast<size_t>(row) * p.vectors;
+        uint4 x[N], d[N], e[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int v = first + i * step;
+            x[i] = d[i] = e[i] = make_uint4(0, 0, 0, 0);
+            if (v < p.vectors) {
+                x[i] = ld_input(p.x + base + v);
+                d[i] = ld_input(p.dy + base + v);
+                if (p.dsum != nullptr) e[i] = ld_input(p.dsum + base + v);
+            }
+        }
+        float2 squares = make_float2(0.f, 0.f), products = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            float2 a[4], b[4];
+            unpack_bf16(x[i], a);
+            unpack_bf16(d[i], b);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                squares = __ffma2_rn(a[c], a[c], squares);
+                products = __ffma2_rn(__fmul2_rn(b[c], g[i][c]), a[c], products);
+            }
+        }
+        float2 total = make_float2(warp_sum(squares.x + squares.y), warp_sum(products.x + products.y));
+        if (ROW_CTA) {
+            if (lane == 0) s_part[turn][warp] = total;
+            __syncthreads();
+            total = make_float2(0.f, 0.f);
+            for (int w = 0; w < step / 32; ++w) total = __fadd2_rn(total, s_part[turn][w]);
+        }
+        const float rs = __frsqrt_rn(fmaf(total.x, p.inverse, p.eps));
+        const float mean = rs * rs * (total.y * p.inverse);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int v = first + i * step;
+            float2 a[4], b[4], z[4];
+            unpack_bf16(x[i], a);
+            unpack_bf16(d[i], b);
+            unpack_bf16(e[i], z);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                dg[i][c] = __ffma2_rn(__fmul2_rn(b[c], a[c]), make_float2(rs, rs), dg[i][c]);
+                const float2 t = __ffma2_rn(a[c], make_float2(-mean, -mean), __fmul2_rn(b[c], g[i][c]));
+                z[c] = __ffma2_rn(t, make_float2(rs, rs), z[c]);
+            }
+            if (v < p.vectors) p.dx[base + v] = pack_bf16(z);
+        }
+    }
+    if (p.partial == nullptr) return;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int v = first + i * step;
+        if (v < p.vectors) {
+            float4* dst = reinterpret_cast<float4*>(p.partial + (static_cast<size_t>(group) * p.vectors + v) * 8);
+            __stcg(dst, make_float4(dg[i][0].x, dg[i][0].y, dg[i][1].x, dg[i][1].y));
+            __stcg(dst + 1, make_float4(dg[i][2].x, dg[i][2].y, dg[i][3].x, dg[i][3].y));
+        }
+    }
+}
+
+// The weight gradient from the groups' sums: 32 columns a CTA, every ADD_WARPS-th group a warp, then the warps in order.
+constexpr int ADD_WARPS = 16;
+__global__ void __launch_bounds__(32 * ADD_WARPS) add_groups_kernel(const float* partial, float* dweight, int H, int groups) {
+    __shared__ float s_sum[ADD_WARPS][32];
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int c = static_cast<int>(blockIdx.x) * 32 + lane;
+    float a = 0.f;
+    if (c < H) {
+#pragma unroll 8
+        for (int i = warp; i < groups; i += ADD_WARPS) a += __ldcg(partial + static_cast<size_t>(i) * H + c);
+    }
+    s_sum[warp][lane] = a;
+    __syncthreads();
+    if (warp == 0 && c < H) {
+        float sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < ADD_WARPS; ++w) sum += s_sum[w][lane];
+        dweight[c] = sum;
+    }
+}
+
+template <typename W, bool BACKWARD, typename P>
+cudaError_t launch_norm(const P& p, int H, int groups, cudaStream_t stream) {
+    const auto go = [&](auto kernel, bool cta) {
+        const unsigned grid = static_cast<unsigned>(cta ? groups : cdiv(groups, NORM_ROWS));
+        const unsigned block = static_cast<unsigned>(cta ? 32 * cdiv(H, NORM_WARP_H) : 32 * NORM_ROWS);
+        return launch_overlapped(kernel, dim3(grid), dim3(block), stream, p);
+    };
+    if constexpr (BACKWARD) {
+        if (H > NORM_WARP_H) return go(rmsnorm_backward_kernel<W, true, NORM_VECTORS>, true);
+        if (H > 512) return go(rmsnorm_backward_kernel<W, false, 4>, false);
+        if (H > 256) return go(rmsnorm_backward_kernel<W, false, 2>, false);
+        return go(rmsnorm_backward_kernel<W, false, 1>, false);
+    } else {
+        if (H > NORM_WARP_H) return go(rmsnorm_kernel<W, true, NORM_VECTORS>, true);
+        if (H > 512) return go(rmsnorm_kernel<W, false, 4>, false);
+        if (H > 256) return go(rmsnorm_kernel<W, false, 2>, false);
+        return go(rmsnorm_kernel<W, false, 1>, false);
+    }
+}
+
+// Groups of rows of the gradient: what fits the GPU at once, whatever the GPU (so that sums do not depend on it).
+int norm_groups(int T, int H) {
+    const int most = H > NORM_WARP_H ? 304 : 1216;
+    return T < most ? T : most;
+}
+
+dg_status norm_check(int weight_type, int T, int H, float eps) {
+    if (T < 0 || H < 0 || !(eps >= 0.f)) return DG_INVALID_ARG;
+    if (weight_type != DG_TYPE_BF16 && weight_type != DG_TYPE_F32) return DG_INVALID_ARG;
+    if (H % 8 != 0 || H > NORM_MAX_H) return DG_UNSUPPORTED_SHAPE;
+    return DG_OK;
+}
+
+}  // namespace
+}  // namespace dg
+
+using namespace dg;
+
+extern "C" {
+
+dg_status dg_rmsnorm(const void* x, const void* residual, const void* weight, int weight_type, void* sum, void* y, uint8_t* q, float* sf,
+                     int pow2, int T, int H, float eps, cudaStream_t stream) {
+    const dg_status st = norm_check(weight_type, T, H, eps);
+    if (st != DG_OK) return st;
+    if ((q == nullptr) != (sf == nullptr)) return DG_INVALID_ARG;
+    if (q && H % 128 != 0) return DG_UNSUPPORTED_SHAPE;
+    if (T == 0 || H == 0 || (!sum && !y && !q)) return DG_OK;
+    if (!x || !weight) return DG_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(sum, 16) || !aligned(y, 16) || !aligned(q, 16) || !aligned(sf, 4))
+        return DG_MISALIGNED;
+    DeviceInfo dev;
+    const dg_status ds = device_info(&dev);
+    if (ds != DG_OK) return ds;
+    NormParams p;
+    p.x = static_cast<const uint4*>(x);
+    p.residual = static_cast<const uint4*>(residual);
+    p.weight = weight;
+    p.sum = static_cast<uint4*>(sum);
+    p.y = static_cast<uint4*>(y);
+    p.q = reinterpret_cast<uint2*>(q);
+    p.sf = sf;
+    p.rows = T;
+    p.vectors = H / 8;
+    p.pow2 = pow2;
+    p.inverse = 1.f / static_cast<float>(H);
+    p.eps = eps;
+    const cudaError_t e = weight_type == DG_TYPE_F32 ? launch_norm<float, false>(p, H, T, stream) : launch_norm<__nv_bfloat16, false>(p, H, T, stream);
+    return e == cudaSuccess ? DG_OK : DG_CUDA_ERROR;
+}
+
+int64_t dg_rmsnorm_backward_workspace(int T, int H) {
+    if (T < 0 || H < 0 || H % 8 != 0 || H > NORM_MAX_H) return -1;
+    return static_cast<int64_t>(norm_groups(T, H)) * H * 4;
+}
+
+dg_status dg_rmsnorm_backward(const void* dy, const void* x, const void* weight, int weight_type, const void* dsum, void* dx, float* dweight,
+                              void* workspace, int64_t workspace_bytes, int T, int H, float eps, cudaStream_t stream) {
+    const dg_status st = norm_check(weight_type, T, H, eps);
+    if (st != DG_OK) return st;
+    if (H == 0 || (T == 0 && !dweight)) return DG_OK;
+    if (T > 0 && (!dy || !x || !weight || !dx)) return DG_INVALID_ARG;
+    const int64_t need = dweight ? dg_rmsnorm_backward_workspace(T, H) : 0;
+    if (need > 0 && (!workspace || workspace_bytes < need)) return DG_INVALID_ARG;
+    if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(weight, 16) || !aligned(dsum, 16) || !aligned(dx, 16) || !aligned(dweight, 4) || !aligned(workspace, 16))
+        return DG_MISALIGNED;
+    DeviceInfo dev;
+    const dg_status ds = device_info(&dev);
+    if (ds != DG_OK) return ds;
+    if (T == 0) return cudaMemsetAsync(dweight, 0, static_cast<size_t>(H) * 4, stream) == cudaSuccess ? DG_OK : DG_CUDA_ERROR;
+    NormBackwardParams p;
+    p.dy = static_cast<const uint4*>(dy);
+    p.x = static_cast<const uint4*>(x);
+    p.weight = weight;
+    p.dsum = static_cast<const uint4*>(dsum);
+    p.dx = static_cast<uint4*>(dx);
+    p.partial = dweight ? static_cast<float*>(workspace) : nullptr;
+    p.rows = T;
+    p.vectors = H / 8;
+    p.groups = norm_groups(T, H);
+    p.inverse = 1.f / static_cast<float>(H);
+    p.eps = eps;
+    cudaError_t e = weight_type == DG_TYPE_F32 ? launch_norm<float, true>(p, H, p.groups, stream) : launch_norm<__nv_bfloat16, true>(p, H, p.groups, stream);
+    if (e == cudaSuccess && dweight)
+        e = launch_overlapped(add_groups_kernel, dim3(static_cast<unsigned>(cdiv(H, 32))), dim3(32 * ADD_WARPS), stream, static_cast<const float*>(p.partial), dweight, H, p.groups);
+    return e == cudaSuccess ? DG_OK : DG_CUDA_ERROR;
+}
+
+}  // extern "C"

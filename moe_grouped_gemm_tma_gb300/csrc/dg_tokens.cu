@@ -1,0 +1,628 @@
+// Tokens by expert and back, around the grouped products: where every routed slot goes (dg_moe_sort_contiguous,
+// dg_moe_sort_masked), the tokens' rows there (dg_moe_gather), the weighted sum of the experts' rows back to the tokens
+// (dg_moe_combine), and that sum's gradient (dg_moe_combine_backward). The gather's own gradient is the sum without
+// weights.
+//
+// Sort. A counting sort by expert that keeps the slots' order, so that its result does not depend on timing: a warp takes
+// consecutive slots, 32 at a time; match.any gives each lane the others with its expert, whose number below it is its
+// place among the 32, and the lowest of them counts for all. Up to SORT_ONE slots are one CTA's; more are cut into
+// chunks, a CTA each, whose counts a first launch writes and a second adds up: every CTA for itself, because the counts
+// are few (128 chunks x 256 experts are 128 KB out of L2).
+//
+// The rows are moved token by token: a token's row is read once, however many experts it goes to, and every access is a
+// piece of 512 bytes of a row a warp. Rows without a token inside an expert's block of 128 are zeroed by warps of their own.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <climits>
+
+#include "dg.h"
+#include "dg_host.cuh"
+#include "dg_ptx.cuh"
+#include "dg_quant.cuh"
+
+namespace dg {
+namespace {
+
+constexpr unsigned FULL = 0xffffffffu;
+
+// ------------------------------------------------------------------------------------ sort
+constexpr int SORT_THREADS = 512;
+constexpr int SORT_WARPS = SORT_THREADS / 32;
+constexpr int SORT_ONE = 4096;                    // slots that one CTA sorts alone
+constexpr int SORT_CHUNKS = 152;                  // chunks at most
+constexpr int64_t SORT_MAX_SLOTS = 1 << 23;       // (a chunk's counts fit 16 bits: it has 55296 slots then)
+
+struct SortParams {
+    const int32_t* ids;
+    int32_t* rows;
+    int32_t* counts;
+    int32_t* m_indices;   // null: masked layout
+    int32_t* chunk_counts;
+    int slots, experts, blocks, max_m, groups, chunks;
+};
+
+__device__ __forceinline__ unsigned lanes_below() {
+    unsigned m;
+    asm("mov.u32 %0, %%lanemask_lt;" : "=r"(m));
+    return m;
+}
+
+// The expert of a warp's slot in its group g, -1 where there is none.
+__device__ __forceinline__ int slot_expert(const SortParams& p, int slot) {
+    const int id = slot < p.slots ? ld_input(p.ids + slot) : -1;
+    return static_cast<unsigned>(id) < static_cast<unsigned>(p.experts) ? id : -1;
+}
+
+// COUNT: the first of two launches, which writes a chunk's counts; else the slots are placed.
+template <bool COUNT>
+__global__ void __launch_bounds__(SORT_THREADS) sort_kernel(const SortParams p) {
+    __shared__ uint16_t s_warp[SORT_WARPS][MAX_ROUTE_EXPERTS];   // a warp's slots of an expert, then those of the warps before it
+    __shared__ int s_total[MAX_ROUTE_EXPERTS];                   // an expert's slots
+    __shared__ int s_before[MAX_ROUTE_EXPERTS];                  // those of the chunks before this one
+    __shared__ int s_base[MAX_ROUTE_EXPERTS];                    // the expert's first row
+    __shared__ int s_sum[SORT_WARPS];
+
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int E = p.experts, chunk = static_cast<int>(blockIdx.x);
+    for (int i = threadIdx.x; i < E; i += SORT_THREADS) {
+#pragma unroll
+        for (int w = 0; w < SORT_WARPS; ++w) s_warp[w][i] = 0;
+        s_total[i] = 0;
+        s_before[i] = 0;
+    }
+    __syncthreads();
+
+    const int first = (chunk * SORT_WARPS + warp) * p.groups * 32;
+    for (int g = 0; g < p.groups; ++g) {
+        const int e = slot_expert(p, first + g * 32 + lane);
+        const unsigned same = __match_any_sync(FULL, e);
+        if (e >= 0 && (same & lanes_below()) == 0) s_warp[warp][e] += __popc(same);
+        __syncwarp();
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += SORT_THREADS) {
+        int sum = 0;
+#pragma unroll
+        for (int w = 0; w < SORT_WARPS; ++w) {
+            const int c = s_warp[w][e];
+            s_warp[w][e] = static_cast<uint16_t>(sum);
+            sum += c;
+        }
+        if (COUNT) p.chunk_counts[static_cast<size_t>(chunk) * E + e] = sum;
+        else if (p.chunks == 1) s_total[e] = sum;
+    }
+    if (COUNT) return;
+
+    // ---- the other chunks' counts: each part of the threads takes every parts-th chunk
+    if (p.chunks > 1) {
+        const int parts = E < SORT_THREADS ? SORT_THREADS / E : 1;
+        const int part = static_cast<int>(threadIdx.x) / E;
+        if (parts == 1) {
+            for (int e = threadIdx.x; e < E; e += SORT_THREADS) {
+                int total = 0, before = 0;
+#pragma unroll 8
+                for (int c = 0; c < p.chunks; ++c) {
+                    const int n = __ldcg(p.chunk_counts + static_cast<size_t>(c) * E + e);
+                    total += n;
+                    before += c < chunk ? n : 0;
+                }
+                s_total[e] = total;
+                s_before[e] = before;
+            }
+        } else if (part < parts) {
+            const int e = static_cast<int>(threadIdx.x) - part * E;
+            int total = 0, before = 0;
+#pragma unroll 8
+            for (int c = part; c < p.chunks; c += parts) {
+                const int n = __ldcg(p.chunk_counts + static_cast<size_t>(c) * E + e);
+                total += n;
+                before += c < chunk ? n : 0;
+            }
+            atomicAdd(&s_total[e], total);         // (whole numbers: in any order)
+            atomicAdd(&s_before[e], before);
+        }
+    }
+    __syncthreads();
+
+    // ---- the experts' first rows
+    if (p.max_m > 0) {
+        for (int e = threadIdx.x; e < E; e += SORT_THREADS) s_base[e] = e * p.max_m;
+    } else {
+        constexpr int PER = MAX_ROUTE_EXPERTS / SORT_THREADS;
+        int room[PER], sum = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int e = static_cast<int>(threadIdx.x) * PER + i;
+            room[i] = e < E ? (s_total[e] + 127) / 128 * 128 : 0;
+            sum += room[i];
+        }
+        int upto = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(FULL, upto, o);
+            if (lane >= o) upto += v;
+        }
+        if (lane == 31) s_sum[warp] = upto;
+        __syncthreads();
+        int base = upto - sum;
+        for (int w = 0; w < warp; ++w) base += s_sum[w];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int e = static_cast<int>(threadIdx.x) * PER + i;
+            if (e < E) s_base[e] = base;
+            base += room[i];
+        }
+    }
+    __syncthreads();
+
+    // ---- the slots' rows
+    for (int g = 0; g < p.groups; ++g) {
+        const int slot = first + g * 32 + lane;
+        const int e = slot_expert(p, slot);
+        const unsigned same = __match_any_sync(FULL, e);
+        const unsigned below = same & lanes_below();
+        int row = -1;
+        if (e >= 0) {
+            const int place = s_before[e] + s_warp[warp][e] + __popc(below);
+            if (p.max_m == 0 || place < p.max_m) row = s_base[e] + place;
+        }
+        __syncwarp();
+        if (e >= 0 && below == 0) s_warp[warp][e] += __popc(same);
+        __syncwarp();
+        if (slot < p.slots) p.rows[slot] = row;
+    }
+    if (chunk == 0)
+        for (int e = threadIdx.x; e < E; e += SORT_THREADS) p.counts[e] = s_total[e];
+
+    // ---- the expert of every row: a block of 128 rows is one expert's, the last whose first row is not behind it
+    if (p.m_indices != nullptr) {
+        for (int b = chunk * SORT_WARPS + warp; b < p.blocks; b += p.chunks * SORT_WARPS) {
+            int e = 0;
+            for (int lo = 1, hi = E; lo < hi;) {
+                const int mid = (lo + hi) >> 1;
+                if (s_base[mid] <= b * 128) {
+                    e = mid;
+                    lo = mid + 1;
+                } else {
+                    hi = mid;
+                }
+            }
+            const int left = s_total[e] - (b * 128 - s_base[e]) - lane * 4;   // rows from this lane's first on
+            reinterpret_cast<int4*>(p.m_indices)[static_cast<size_t>(b) * 32 + lane] =
+                make_int4(left > 0 ? e : -1, left > 1 ? e : -1, left > 2 ? e : -1, left > 3 ? e : -1);
+        }
+    }
+}
+
+// ------------------------------------------------------------------------------------ rows
+constexpr int MOVE_WARPS = 8;
+constexpr int PAD_ROWS = 8;                       // rows that a warp looks at for zeros
+
+__device__ __forceinline__ int slot_row(const int32_t* rows, size_t at, int Mt) {
+    const int r = ld_input(rows + at);
+    return static_cast<unsigned>(r) < static_cast<unsigned>(Mt) ? r : -1;
+}
+
+// Zeros in the rows without a token of a block that has some: the block's PAD_ROWS rows from `group` on.
+__device__ __forceinline__ void zero_pads(unsigned item, const int32_t* m_indices, uint4* out, float* out_sf, int vectors, int scales, int lane) {
+    const unsigned block = item / (128 / PAD_ROWS), first = item * PAD_ROWS;
+    if (ld_input(m_indices + static_cast<size_t>(block) * 128) < 0) return;
+    const bool pad = lane < PAD_ROWS && ld_input(m_indices + first + lane) < 0;
+    unsigned which = __ballot_sync(FULL, pad);
+    while (which) {
+        const size_t row = first + __ffs(which) - 1;
+        which &= which - 1;
+        for (int v = lane; v < vectors; v += 32) out[row * vectors + v] = make_uint4(0, 0, 0, 0);
+        if (out_sf != nullptr) {
+            const float lowest = block_scale(0).s;
+            for (int b = lane; b < scales; b += 32) out_sf[row * scales + b] = lowest;
+        }
+    }
+}
+
+struct GatherParams {
+    const uint4* x;
+    const float* sf;
+    const int32_t* rows;
+    const int32_t* m_indices;
+    uint4* out;
+    float* out_sf;
+    int k, vectors, scales, Mt, pieces;           // 16-byte vectors, scales and pieces of a row
+    unsigned tokens_items, items;
+};
+
+constexpr int GATHER_VECTORS = 4;                 // a lane's vectors of a piece: 2048 bytes, with 16 scales of codes
+
+__global__ void __launch_bounds__(32 * MOVE_WARPS) gather_kernel(const GatherParams p) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const unsigned item = blockIdx.x * MOVE_WARPS + (threadIdx.x >> 5);
+    if (item >= p.items) return;
+    if (item >= p.tokens_items) {
+        zero_pads(item - p.tokens_items, p.m_indices, p.out, p.out_sf, p.vectors, p.scales, lane);
+        return;
+    }
+    const unsigned t = item / p.pieces, piece = item - t * p.pieces;
+    const int mine = lane < p.k ? slot_row(p.rows, static_cast<size_t>(t) * p.k + lane, p.Mt) : -1;
+    unsigned open = __ballot_sync(FULL, mine >= 0);
+    if (open == 0) return;
+    const int v0 = static_cast<int>(piece) * 32 * GATHER_VECTORS + lane;
+    const uint4* src = p.x + static_cast<size_t>(t) * p.vectors;
+    uint4 v[GATHER_VECTORS];
+#pragma unroll
+    for (int i = 0; i < GATHER_VECTORS; ++i)
+        if (v0 + 32 * i < p.vectors) v[i] = ld_input(src + v0 + 32 * i);
+    const int b = static_cast<int>(piece) * (4 * GATHER_VECTORS) + lane;
+    const bool scaled = p.sf != nullptr && lane < 4 * GATHER_VECTORS && b < p.scales;
+    const float s = scaled ? ld_input(p.sf + static_cast<size_t>(t) * p.scales + b) : 0.f;
+    while (open) {
+        const size_t row = static_cast<size_t>(__shfl_sync(FULL, mine, __ffs(open) - 1));
+        open &= open - 1;
+        uint4* dst = p.out + row * p.vectors;
+#pragma unroll
+        for (int i = 0; i < GATHER_VECTORS; ++i)
+            if (v0 + 32 * i < p.vectors) dst[v0 + 32 * i] = v[i];
+        if (scaled) p.out_sf[row * p.scales + b] = s;
+    }
+}
+
+// ------------------------------------------------------------------------------------ weighted sum
+struct CombineParams {
+    const uint4* y;
+    const int32_t* rows;
+    const float* weights;
+    const uint4* residual;
+    uint4* out;
+    int k, vectors, Mt, pieces;
+    unsigned items;
+};
+
+__device__ __forceinline__ void add_scaled(float2 (&a)[4], const uint4& v, float w) {
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] = __ffma2_rn(make_float2(w, w), make_float2(bf16_lo(u[i]), bf16_hi(u[i])), a[i]);
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+__device__ __forceinline__ uint4 pack_bf16(const float2 (&a)[4]) {
+    return make_uint4(pack_bf16(a[0].x, a[0].y), pack_bf16(a[1].x, a[1].y), pack_bf16(a[2].x, a[2].y), pack_bf16(a[3].x, a[3].y));
+}
+
+// A warp a piece of 512 bytes of a token's row, four experts' rows in flight at a time. FP32 sums, in the slots' order
+// from zero on, the residual last.
+__global__ void __launch_bounds__(32 * MOVE_WARPS) combine_kernel(const CombineParams p) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const unsigned item = blockIdx.x * MOVE_WARPS + (threadIdx.x >> 5);
+    if (item >= p.items) return;
+    const unsigned t = item / p.pieces, piece = item - t * p.pieces;
+    const size_t slot = static_cast<size_t>(t) * p.k + lane;
+    const int mine = lane < p.k ? slot_row(p.rows, slot, p.Mt) : -1;
+    const float weight = mine >= 0 && p.weights != nullptr ? ld_input(p.weights + slot) : 1.f;
+    unsigned open = __ballot_sync(FULL, mine >= 0);
+    const int v = static_cast<int>(piece) * 32 + lane;
+    const bool inside = v < p.vectors;
+    const size_t at = static_cast<size_t>(t) * p.vectors + v;
+    uint4 res = make_uint4(0, 0, 0, 0);
+    if (inside && p.residual != nullptr) res = ld_input(p.residual + at);
+    float2 a[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] = make_float2(0.f, 0.f);
+    while (open) {
+        uint4 y[4];
+        float w[4];
+        const int n = __popc(open);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int j = i < n ? __ffs(open) - 1 : 0;
+            open &= open - 1;
+            const int row = __shfl_sync(FULL, mine, j);
+            w[i] = __shfl_sync(FULL, weight, j);
+            if (i < n && inside) y[i] = ld_input(p.y + static_cast<size_t>(row) * p.vectors + v);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < n && inside) add_scaled(a, y[i], w[i]);
+    }
+    if (!inside) return;
+    if (p.residual != nullptr) add_scaled(a, res, 1.f);
+    p.out[at] = pack_bf16(a);
+}
+
+// ------------------------------------------------------------------------------------ its gradient
+struct CombineBackwardParams {
+    const uint4* dout;
+    const uint4* y;
+    const int32_t* rows;
+    const float* weights;
+    const int32_t* m_indices;
+    uint4* dy;
+    float* dweights;
+    int T, k, vectors, Mt;
+    unsigned token_ctas, pads;
+};
+
+constexpr int CB_WARPS = 4;
+constexpr int CB_VECTORS = 4;                     // a lane's vectors at a time
+
+// WIDE: a CTA a token, else a warp a token. A lane keeps its piece of dout while it goes through the token's experts; the
+// products with their rows are added up over the lanes, and over the warps in order.
+template <bool WIDE>
+__global__ void __launch_bounds__(32 * CB_WARPS) combine_backward_kernel(const CombineBackwardParams p) {
+    __shared__ float s_dot[CB_WARPS][32];
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (blockIdx.x >= p.token_ctas) {
+        const unsigned item = (blockIdx.x - p.token_ctas) * CB_WARPS + warp;
+        if (item < p.pads) zero_pads(item, p.m_indices, p.dy, nullptr, p.vectors, 0, lane);
+        return;
+    }
+    const int t = static_cast<int>(WIDE ? blockIdx.x : blockIdx.x * CB_WARPS + warp);
+    if (!WIDE && t >= p.T) return;
+    const size_t slot = static_cast<size_t>(t) * p.k + lane;
+    const int mine = lane < p.k ? slot_row(p.rows, slot, p.Mt) : -1;
+    const float weight = mine >= 0 && p.weights != nullptr ? ld_input(p.weights + slot) : 1.f;
+    const unsigned open = __ballot_sync(FULL, mine >= 0);
+    const int first = WIDE ? warp * 32 + lane : lane, step = WIDE ? 32 * CB_WARPS : 32;
+    float dot = 0.f;                              // of slot `lane`
+    for (int v0 = first; v0 - lane < p.vectors; v0 += step * CB_VECTORS) {
+        uint4 d[CB_VECTORS];
+#pragma unroll
+        for (int i = 0; i < CB_VECTORS; ++i) {
+            d[i] = make_uint4(0, 0, 0, 0);
+            if (v0 + i * step < p.vectors) d[i] = ld_input(p.dout + static_cast<size_t>(t) * p.vectors + v0 + i * step);
+        }
+        for (unsigned left = open; left; left &= left - 1) {
+            const int j = __ffs(left) - 1;
+            const size_t at = static_cast<size_t>(__shfl_sync(FULL, mine, j)) * p.vectors + v0;
+            const float w = __shfl_sync(FULL, weight, j);
+            if (p.dweights != nullptr) {
+                uint4 y[CB_VECTORS];
+#pragma unroll
+                for (int i = 0; i < CB_VECTORS; ++i) {
+                    y[i] = make_uint4(0, 0, 0, 0);
+                    if (v0 + i * step < p.vectors) y[i] = ld_input(p.y + at + i * step);
+                }
+                float2 a = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < CB_VECTORS; ++i) {
+                    const uint32_t yw[4] = {y[i].x, y[i].y, y[i].z, y[i].w}, dw[4] = {d[i].x, d[i].y, d[i].z, d[i].w};
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        a = __ffma2_rn(make_float2(bf16_lo(yw[c]), bf16_hi(yw[c])), make_float2(bf16_lo(dw[c]), bf16_hi(dw[c])), a);
+                }
+                float sum = a.x + a.y;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
+                if (lane == j) dot += sum;
+            }
+            if (p.dy != nullptr) {
+#pragma unroll
+                for (int i = 0; i < CB_VECTORS; ++i) {
+                    if (v0 + i * step < p.vectors) {
+                        const uint32_t dw[4] = {d[i].x, d[i].y, d[i].z, d[i].w};
+                        uint32_t o[4];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const float2 v = __fmul2_rn(make_float2(w, w), make_float2(bf16_lo(dw[c]), bf16_hi(dw[c])));
+                            o[c] = pack_bf16(v.x, v.y);
+                        }
+                        p.dy[at + i * step] = make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+                }
+            }
+        }
+    }
+    if (p.dweights == nullptr) return;
+    if (!WIDE) {
+        if (lane < p.k) p.dweights[slot] = dot;
+        return;
+    }
+    s_dot[warp][lane] = dot;
+    __syncthreads();
+    if (warp == 0 && lane < p.k) {
+        float sum = s_dot[0][lane];
+#pragma unroll
+        for (int w = 1; w < CB_WARPS; ++w) sum += s_dot[w][lane];
+        p.dweights[slot] = sum;
+    }
+}
+
+// Chunks of the slots and groups of 32 a warp; the chunks' counts are the workspace.
+void sort_plan(int64_t slots, int* groups, int* chunks) {
+    *groups = cdiv(slots, SORT_THREADS);
+    *chunks = 1;
+    if (slots <= SORT_ONE) return;
+    *groups = cdiv(slots, static_cast<int64_t>(SORT_THREADS) * SORT_CHUNKS);
+    *chunks = cdiv(slots, static_cast<int64_t>(SORT_THREADS) * *groups);
+}
+
+dg_status sort_check(const int32_t* ids, int32_t* rows, int32_t* counts, int T, int k, int E) {
+    if (T < 0 || k < 0 || E < 1) return DG_INVALID_ARG;
+    if (k > MAX_ROUTE_K || E > MAX_ROUTE_EXPERTS || static_cast<int64_t>(T) * k > SORT_MAX_SLOTS) return DG_UNSUPPORTED_SHAPE;
+    if (!counts || (static_cast<int64_t>(T) * k > 0 && (!ids || !rows))) return DG_INVALID_ARG;
+    if (!aligned(ids, 4) || !aligned(rows, 4) || !aligned(counts, 4)) return DG_MISALIGNED;
+    return DG_OK;
+}
+
+dg_status sort(const int32_t* ids, int32_t* rows, int32_t* counts, int32_t* m_indices, void* workspace, int64_t workspace_bytes, int T, int k,
+               int E, int Mt, int max_m, cudaStream_t stream) {
+    const int64_t need = dg_moe_sort_workspace(T, k, E);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return DG_INVALID_ARG;
+    if (!aligned(workspace, 16)) return DG_MISALIGNED;
+    DeviceInfo dev;
+    const dg_status st = device_info(&dev);
+    if (st != DG_OK) return st;
+    SortParams p;
+    p.ids = ids;
+    p.rows = rows;
+    p.counts = counts;
+    p.m_indices = Mt > 0 ? m_indices : nullptr;
+    p.chunk_counts = static_cast<int32_t*>(workspace);
+    p.slots = T * k;
+    p.experts = E;
+    p.blocks = Mt / 128;
+    p.max_m = max_m;
+    sort_plan(p.slots, &p.groups, &p.chunks);
+    cudaError_t e = cudaSuccess;
+    if (p.chunks > 1) e = launch_overlapped(sort_kernel<true>, dim3(static_cast<unsigned>(p.chunks)), dim3(SORT_THREADS), stream, p);
+    if (e == cudaSuccess) e = launch_overlapped(sort_kernel<false>, dim3(static_cast<unsigned>(p.chunks)), dim3(SORT_THREADS), stream, p);
+    return e == cudaSuccess ? DG_OK : DG_CUDA_ERROR;
+}
+
+// Common checks of the calls that move rows: sizes, and that items of 32 bits number them.
+dg_status rows_check(const int32_t* rows, int T, int k, int H, int Mt, int granule) {
+    if (T < 0 || k < 0 || H < 0 || Mt < 0) return DG_INVALID_ARG;
+    if (k > MAX_ROUTE_K || H % granule != 0) return DG_UNSUPPORTED_SHAPE;
+    if (static_cast<int64_t>(T) * cdiv(H, 256) + Mt > INT32_MAX) return DG_UNSUPPORTED_SHAPE;
+    if (static_cast<int64_t>(T) * k > 0 && !rows) return DG_INVALID_ARG;
+    return aligned(rows, 4) ? DG_OK : DG_MISALIGNED;
+}
+
+}  // namespace
+}  // namespace dg
+
+using namespace dg;
+
+extern "C" {
+
+int64_t dg_moe_sort_rows(int T, int k, int E) {
+    if (T < 0 || k < 0 || E < 1 || k > MAX_ROUTE_K || E > MAX_ROUTE_EXPERTS) return -1;
+    const int64_t slots = static_cast<int64_t>(T) * k;
+    if (slots > SORT_MAX_SLOTS) return -1;
+    return (slots + 127 * (slots < E ? slots : E)) / 128 * 128;
+}
+
+int64_t dg_moe_sort_workspace(int T, int k, int E) {
+    if (T < 0 || k < 0 || E < 1 || k > MAX_ROUTE_K || E > MAX_ROUTE_EXPERTS) return -1;
+    const int64_t slots = static_cast<int64_t>(T) * k;
+    if (slots > SORT_MAX_SLOTS) return -1;
+    int groups, chunks;
+    sort_plan(slots, &groups, &chunks);
+    return chunks > 1 ? static_cast<int64_t>(SORT_CHUNKS) * E * 4 : 0;
+}
+
+dg_status dg_moe_sort_contiguous(const int32_t* ids, int32_t* rows, int32_t* counts, int32_t* m_indices, void* workspace,
+                                 int64_t workspace_bytes, int T, int k, int E, int Mt, cudaStream_t stream) {
+    const dg_status st = sort_check(ids, rows, counts, T, k, E);
+    if (st != DG_OK) return st;
+    if (Mt < 0) return DG_INVALID_ARG;
+    if (Mt % 128 != 0 || Mt < dg_moe_sort_rows(T, k, E)) return DG_UNSUPPORTED_SHAPE;
+    if (Mt > 0 && !m_indices) return DG_INVALID_ARG;
+    if (!aligned(m_indices, 16)) return DG_MISALIGNED;
+    return sort(ids, rows, counts, m_indices, workspace, workspace_bytes, T, k, E, Mt, 0, stream);
+}
+
+dg_status dg_moe_sort_masked(const int32_t* ids, int32_t* rows, int32_t* masked_m, void* workspace, int64_t workspace_bytes, int T,
+                             int k, int E, int max_m, cudaStream_t stream) {
+    const dg_status st = sort_check(ids, rows, masked_m, T, k, E);
+    if (st != DG_OK) return st;
+    if (max_m < 1) return DG_INVALID_ARG;
+    if (static_cast<int64_t>(E) * max_m > INT32_MAX) return DG_UNSUPPORTED_SHAPE;
+    return sort(ids, rows, masked_m, nullptr, workspace, workspace_bytes, T, k, E, 0, max_m, stream);
+}
+
+dg_status dg_moe_gather(const void* x, const float* sf, int x_type, const int32_t* rows, const int32_t* m_indices, void* out, float* out_sf,
+                        int T, int k, int H, int Mt, cudaStream_t stream) {
+    if (x_type != DG_TYPE_E4M3 && x_type != DG_TYPE_BF16) return DG_INVALID_ARG;
+    const bool codes = x_type == DG_TYPE_E4M3;
+    const dg_status st = rows_check(rows, T, k, H, Mt, codes ? 128 : 8);
+    if (st != DG_OK) return st;
+    if (m_indices && Mt % 128 != 0) return DG_UNSUPPORTED_SHAPE;
+    if (H == 0 || Mt == 0 || (static_cast<int64_t>(T) * k == 0 && !m_indices)) return DG_OK;
+    if (!out || (T > 0 && k > 0 && !x)) return DG_INVALID_ARG;
+    if (codes ? (!out_sf || (T > 0 && k > 0 && !sf)) : (sf || out_sf)) return DG_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(out, 16) || !aligned(sf, 4) || !aligned(out_sf, 4) || !aligned(m_indices, 4)) return DG_MISALIGNED;
+    DeviceInfo dev;
+    const dg_status ds = device_info(&dev);
+    if (ds != DG_OK) return ds;
+    GatherParams p;
+    p.x = static_cast<const uint4*>(x);
+    p.sf = sf;
+    p.rows = rows;
+    p.m_indices = m_indices;
+    p.out = static_cast<uint4*>(out);
+    p.out_sf = out_sf;
+    p.k = k;
+    p.vectors = codes ? H / 16 : H / 8;
+    p.scales = codes ? H / 128 : 0;
+    p.Mt = Mt;
+    p.pieces = cdiv(p.vectors, 32 * GATHER_VECTORS);
+    p.tokens_items = k > 0 ? static_cast<unsigned>(T) * static_cast<unsigned>(p.pieces) : 0u;
+    p.items = p.tokens_items + (m_indices ? static_cast<unsigned>(Mt / PAD_ROWS) : 0u);
+    const cudaError_t e = launch_overlapped(gather_kernel, dim3((p.items + MOVE_WARPS - 1) / MOVE_WARPS), dim3(32 * MOVE_WARPS), stream, p);
+    return e == cudaSuccess ? DG_OK : DG_CUDA_ERROR;
+}
+
+dg_status dg_moe_combine(const void* y, const int32_t* rows, const float* weights, const void* residual, void* out, int T, int k, int H,
+                         int Mt, cudaStream_t stream) {
+    const dg_status st = rows_check(rows, T, k, H, Mt, 8);
+    if (st != DG_OK) return st;
+    if (T == 0 || H == 0) return DG_OK;
+    if (!out || (k > 0 && Mt > 0 && !y)) return DG_INVALID_ARG;
+    if (!aligned(y, 16) || !aligned(residual, 16) || !aligned(out, 16) || !aligned(weights, 4)) return DG_MISALIGNED;
+    DeviceInfo dev;
+    const dg_status ds = device_info(&dev);
+    if (ds != DG_OK) return ds;
+    CombineParams p;
+    p.y = static_cast<const uint4*>(y);
+    p.rows = rows;
+    p.weights = weights;
+    p.residual = static_cast<const uint4*>(residual);
+    p.out = static_cast<uint4*>(out);
+    p.k = k;
+    p.vectors = H / 8;
+    p.Mt = Mt;
+    p.pieces = cdiv(p.vectors, 32);
+    p.items = static_cast<unsigned>(T) * static_cast<unsigned>(p.pieces);
+    const cudaError_t e = launch_overlapped(combine_kernel, dim3((p.items + MOVE_WARPS - 1) / MOVE_WARPS), dim3(32 * MOVE_WARPS), stream, p);
+    return e == cudaSuccess ? DG_OK : DG_CUDA_ERROR;
+}
+
+dg_status dg_moe_combine_backward(const void* dout, const void* y, const int32_t* rows, const float* weights, const int32_t* m_indices, void* dy,
+                                  float* dweights, int T, int k, int H, int Mt, cudaStream_t stream) {
+    const dg_status st = rows_check(rows, T, k, H, Mt, 8);
+    if (st != DG_OK) return st;
+    if (m_indices && Mt % 128 != 0) return DG_UNSUPPORTED_SHAPE;
+    if (!dy && !dweights) return DG_OK;
+    const bool slots = T > 0 && k > 0, pads = dy && m_indices && Mt > 0 && H > 0;
+    if (!slots && !pads) return DG_OK;
+    if (slots && H > 0 && (!dout || (dweights && Mt > 0 && !y))) return DG_INVALID_ARG;
+    if (!aligned(dout, 16) || !aligned(y, 16) || !aligned(dy, 16) || !aligned(dweights, 4) || !aligned(weights, 4) || !aligned(m_indices, 4))
+        return DG_MISALIGNED;
+    DeviceInfo dev;
+    const dg_status ds = device_info(&dev);
+    if (ds != DG_OK) return ds;
+    CombineBackwardParams p;
+    p.dout = static_cast<const uint4*>(dout);
+    p.y = static_cast<const uint4*>(y);
+    p.rows = rows;
+    p.weights = weights;
+    p.m_indices = m_indices;
+    p.dy = static_cast<uint4*>(dy);
+    p.dweights = dweights;
+    p.T = T;
+    p.k = k;
+    p.vectors = H / 8;
+    p.Mt = Mt;
+    const bool wide = H > 32 * CB_VECTORS * 8;
+    p.token_ctas = !slots ? 0u : (wide ? static_cast<unsigned>(T) : static_cast<unsigned>(cdiv(T, CB_WARPS)));
+    p.pads = pads ? static_cast<unsigned>(Mt / PAD_ROWS) : 0u;
+    const dim3 grid(p.token_ctas + (p.pads + CB_WARPS - 1) / CB_WARPS);
+    const cudaError_t e = wide ? launch_overlapped(combine_backward_kernel<true>, grid, dim3(32 * CB_WARPS), stream, p)
+                               : launch_overlapped(combine_backward_kernel<false>, grid, dim3(32 * CB_WARPS), stream, p);
+    return e == cudaSuccess ? DG_OK : DG_CUDA_ERROR;
+}
+
+}  // extern "C"
