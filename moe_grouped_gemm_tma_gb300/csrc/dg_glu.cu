@@ -12,6 +12,8 @@
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include <climits>
+
 #include "dg.h"
 #include "dg_host.cuh"
 #include "dg_ptx.cuh"
@@ -22,6 +24,7 @@ namespace dg {
 namespace {
 
 constexpr unsigned FULL = 0xffffffffu;
+constexpr int64_t TILES_MAX = INT32_MAX / 2;        // (a CTA's next tile is numbered in 32 bits too)
 constexpr int GLU_WARPS = 4;
 constexpr int GLU_ROWS = 8 * GLU_WARPS;           // rows of a CTA
 
@@ -124,14 +127,18 @@ __global__ void __launch_bounds__(32 * GLU_WARPS) glu_kernel(const GluParams p) 
 }
 
 // ------------------------------------------------------------------------------------ backward
-// Eight codes times their scale.
-__device__ __forceinline__ void code_values(uint2 w, float s, float2 (&a)[4]) {
-    const uint32_t u[2] = {w.x, w.y};
+// Four codes times their scale.
+__device__ __forceinline__ void code_values(uint32_t w, float s, float2 (&a)[2]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(u[i >> 1] >> (16 * (i & 1))), __NV_E4M3);
+    for (int i = 0; i < 2; ++i) {
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> (16 * i)), __NV_E4M3);
         a[i] = __fmul2_rn(__half22float2(__half2(h)), make_float2(s, s));
     }
+}
+
+__device__ __forceinline__ void bf16_values(uint2 w, float2 (&a)[2]) {
+    a[0] = make_float2(bf16_lo(w.x), bf16_hi(w.x));
+    a[1] = make_float2(bf16_lo(w.y), bf16_hi(w.y));
 }
 
 struct GluBackwardParams {
@@ -145,54 +152,103 @@ struct GluBackwardParams {
     float* sft;
     uint8_t* ht;
     float* hsft;
-    int m, inner, m_tiles;
+    int m, inner;
+    TileOrder order;
 };
 
-// blockIdx.z: what of the tile this CTA makes: dg, du or h.
+constexpr int GB_ROWS = 4;                        // rows of a warp
+constexpr int GB_THREADS = 32 * TILE / GB_ROWS;
+struct GluBackwardShared {
+    TileColumns<GB_ROWS> dg, du, h;
+};
+
 template <int ACT, bool KEPT>
-__global__ void __launch_bounds__(TILE_THREADS, 2) glu_backward_kernel(const GluBackwardParams p) {
-    __shared__ TileShared s;
+__global__ void __launch_bounds__(GB_THREADS, 1) glu_backward_kernel(const GluBackwardParams p) {
+    extern __shared__ __align__(16) uint8_t s_raw[];
+    GluBackwardShared& s = *reinterpret_cast<GluBackwardShared*>(s_raw);
     grid_dependency_wait();
     grid_launch_dependents();
-    const TileThread me;
-    const int part = static_cast<int>(blockIdx.z);
-    const int m0 = static_cast<int>(blockIdx.x) * TILE, n0 = static_cast<int>(blockIdx.y) * TILE;
-    const int valid = p.m - (m0 + me.row);
-    const size_t row = m0 + me.row, inner = p.inner, blocks = inner / 128;
-
-    float2 v[4][4];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const size_t inner = p.inner, blocks = inner / 128, pitch = static_cast<size_t>(p.order.m_tiles) * TILE;
+    const int tiles = p.order.m_tiles * p.order.n_tiles;
+    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        int tm, tn;
+        p.order.at(tile, &tm, &tn);
+        const int r0 = tm * TILE + warp * GB_ROWS, c0 = tn * TILE + lane * 4, valid = p.m - r0;
+        float2 dg[GB_ROWS][2], du[GB_ROWS][2], h[GB_ROWS][2];
+        {
+            uint2 d[GB_ROWS], g[GB_ROWS], u[GB_ROWS];
+            float scale = 0.f;                    // lanes 0 .. 3: of the rows' g, 4 .. 7: of u
+            if (KEPT && lane < 2 * GB_ROWS && lane % GB_ROWS < valid)
+                scale = ld_input(p.kept_sf + (static_cast<size_t>(r0) + lane % GB_ROWS) * (2 * blocks) + (lane / GB_ROWS) * blocks + tn);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float2 d[4], g[4], u[4];
+            for (int i = 0; i < GB_ROWS; ++i) {
+                d[i] = g[i] = u[i] = make_uint2(0, 0);
+                if (i < valid) {
+                    const size_t row = static_cast<size_t>(r0) + i, at = row * (2 * inner) + c0;
+                    if (p.dh != nullptr) d[i] = ld_input(reinterpret_cast<const uint2*>(p.dh + row * inner + c0));
+                    if (KEPT) {
+                        g[i].x = ld_input(reinterpret_cast<const uint32_t*>(p.kept + at));
+                        u[i].x = ld_input(reinterpret_cast<const uint32_t*>(p.kept + at + inner));
+                    } else {
+                        g[i] = ld_input(reinterpret_cast<const uint2*>(p.z + at));
+                        u[i] = ld_input(reinterpret_cast<const uint2*>(p.z + at + inner));
+                    }
+                }
+            }
+            // (rows past M are 0: so are the activations there, and their slopes are finite)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) d[c] = g[c] = u[c] = make_float2(0.f, 0.f);
-        if (i < valid) {
-            if (part != 2) unpack_bf16(ld_input(reinterpret_cast<const uint4*>(p.dh + (row + i) * inner + n0 + me.column)), d);
-            const size_t at = (row + i) * (2 * inner) + n0 + me.column;
-            if (KEPT) {
-                const float* sf = p.kept_sf + (row + i) * (2 * blocks) + blockIdx.y;
-                code_values(ld_input(reinterpret_cast<const uint2*>(p.kept + at)), ld_input(sf), g);
-                code_values(ld_input(reinterpret_cast<const uint2*>(p.kept + at + inner)), ld_input(sf + blocks), u);
-            } else {
-                unpack_bf16(ld_input(reinterpret_cast<const uint4*>(p.z + at)), g);
-                unpack_bf16(ld_input(reinterpret_cast<const uint4*>(p.z + at + inner)), u);
+            for (int i = 0; i < GB_ROWS; ++i) {
+                float2 dv[2], gv[2], uv[2];
+                bf16_values(d[i], dv);
+                if (KEPT) {
+                    code_values(g[i].x, __shfl_sync(FULL, scale, i), gv);
+                    code_values(u[i].x, __shfl_sync(FULL, scale, GB_ROWS + i), uv);
+                } else {
+                    bf16_values(g[i], gv);
+                    bf16_values(u[i], uv);
+                }
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float2 a, slope;
+                    act_both2<ACT>(gv[c], a, slope);
+                    dg[i][c] = __fmul2_rn(__fmul2_rn(dv[c], uv[c]), slope);
+                    du[i][c] = __fmul2_rn(dv[c], a);
+                    h[i][c] = __fmul2_rn(a, uv[c]);
+                }
             }
         }
-        // (rows past M are 0: so are the activations there, and their slopes are finite)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            if (part == 0) v[i][c] = __fmul2_rn(__fmul2_rn(d[c], u[c]), act_slope2<ACT>(g[c]));
-            else v[i][c] = __fmul2_rn(act_value2<ACT>(g[c]), part == 1 ? d[c] : u[c]);
+        if (p.qt != nullptr) {
+            s.dg.maxima(dg, warp, lane);
+            s.du.maxima(du, warp, lane);
         }
-    }
-    const size_t column = part == 1 ? inner + n0 : n0, pitch = static_cast<size_t>(p.m_tiles) * TILE;
-    if (part != 2) {
-        if (p.q != nullptr)
-            tile_rows(v, p.q + row * (2 * inner) + column + me.column, 2 * inner, p.sf + row * (2 * blocks) + column / 128, 2 * blocks, valid, me.l16);
-        if (p.qt != nullptr)
-            tile_columns(v, s, p.qt + column * pitch + m0, pitch, p.sft + column * p.m_tiles + blockIdx.x, p.m_tiles, me);
-    } else {
-        tile_columns(v, s, p.ht + column * pitch + m0, pitch, p.hsft + column * p.m_tiles + blockIdx.x, p.m_tiles, me);
+        if (p.ht != nullptr) s.h.maxima(h, warp, lane);
+        if (p.q != nullptr) {
+            uint8_t* q = p.q + static_cast<size_t>(r0) * (2 * inner) + c0;
+            float* sf = p.sf + static_cast<size_t>(r0) * (2 * blocks) + tn;
+            tile_rows(dg, q, 2 * inner, sf, 2 * blocks, valid, lane);
+            tile_rows(du, q + inner, 2 * inner, sf + blocks, 2 * blocks, valid, lane);
+        }
+        __syncthreads();
+        const int part = static_cast<int>(threadIdx.x) / TILE, column = static_cast<int>(threadIdx.x) % TILE;
+        if (p.qt != nullptr) {
+            if (part == 0) s.dg.scale(column, p.sft + (static_cast<size_t>(tn) * TILE + column) * p.order.m_tiles + tm);
+            else if (part == 1) s.du.scale(column, p.sft + (inner + static_cast<size_t>(tn) * TILE + column) * p.order.m_tiles + tm);
+        }
+        if (p.ht != nullptr && part == 2) s.h.scale(column, p.hsft + (static_cast<size_t>(tn) * TILE + column) * p.order.m_tiles + tm);
+        __syncthreads();
+        if (p.qt != nullptr) {
+            s.dg.quantise(dg, warp, lane);
+            s.du.quantise(du, warp, lane);
+        }
+        if (p.ht != nullptr) s.h.quantise(h, warp, lane);
+        __syncthreads();
+        const size_t first = static_cast<size_t>(tn) * TILE * pitch + static_cast<size_t>(tm) * TILE;
+        if (p.qt != nullptr) {
+            s.dg.store(p.qt + first, pitch, warp, lane);
+            s.du.store(p.qt + inner * pitch + first, pitch, warp, lane);
+        }
+        if (p.ht != nullptr) s.h.store(p.ht + first, pitch, warp, lane);
     }
 }
 
@@ -201,37 +257,67 @@ struct TransposeParams {
     const float* sf;
     uint8_t* qt;
     float* sft;
-    int m, n, m_tiles;
+    int m, n;
+    TileOrder order;
 };
 
-__global__ void __launch_bounds__(TILE_THREADS, 2) transpose_kernel(const TransposeParams p) {
-    __shared__ TileShared s;
+constexpr int TR_ROWS = 8;
+constexpr int TR_THREADS = 32 * TILE / TR_ROWS;
+
+// A CTA takes every gridDim.x-th tile; the next one's codes are asked for as soon as this one's are in use.
+__global__ void __launch_bounds__(TR_THREADS, 2) transpose_kernel(const TransposeParams p) {
+    __shared__ TileColumns<TR_ROWS> s;
     grid_dependency_wait();
     grid_launch_dependents();
-    const TileThread me;
-    const int m0 = static_cast<int>(blockIdx.x) * TILE, n0 = static_cast<int>(blockIdx.y) * TILE;
-    const int valid = p.m - (m0 + me.row);
-    float2 v[4][4];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int tiles = p.order.m_tiles * p.order.n_tiles;
+    const size_t pitch = static_cast<size_t>(p.order.m_tiles) * TILE;
+    uint32_t codes[TR_ROWS];
+    float scale = 0.f;                            // lanes 0 .. 7: of the warp's rows
+    int tm = 0, tn = 0;
+    const auto load = [&](int tile) {
+        p.order.at(tile, &tm, &tn);
+        const int r0 = tm * TILE + warp * TR_ROWS, valid = p.m - r0;
+        const uint8_t* src = p.q + static_cast<size_t>(r0) * p.n + tn * TILE + lane * 4;
+        scale = lane < TR_ROWS && lane < valid ? ld_input(p.sf + (static_cast<size_t>(r0) + lane) * (p.n / TILE) + tn) : 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const size_t row = m0 + me.row + i;
+        for (int i = 0; i < TR_ROWS; ++i) codes[i] = i < valid ? ld_input(reinterpret_cast<const uint32_t*>(src + static_cast<size_t>(i) * p.n)) : 0u;
+    };
+    if (static_cast<int>(blockIdx.x) < tiles) load(blockIdx.x);
+    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        const size_t column = static_cast<size_t>(tn) * TILE;
+        const int m = tm;
+        float2 v[TR_ROWS][2];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) v[i][c] = make_float2(0.f, 0.f);
-        if (i < valid) code_values(ld_input(reinterpret_cast<const uint2*>(p.q + row * p.n + n0 + me.column)), ld_input(p.sf + row * (p.n / 128) + blockIdx.y), v[i]);
+        for (int i = 0; i < TR_ROWS; ++i) code_values(codes[i], __shfl_sync(FULL, scale, i), v[i]);
+        if (tile + static_cast<int>(gridDim.x) < tiles) load(tile + gridDim.x);
+        s.maxima(v, warp, lane);
+        __syncthreads();
+        if (threadIdx.x < TILE) s.scale(threadIdx.x, p.sft + (column + threadIdx.x) * p.order.m_tiles + m);
+        __syncthreads();
+        s.quantise(v, warp, lane);
+        __syncthreads();
+        s.store(p.qt + column * pitch + static_cast<size_t>(m) * TILE, pitch, warp, lane);
     }
-    const size_t pitch = static_cast<size_t>(p.m_tiles) * TILE;
-    tile_columns(v, s, p.qt + n0 * pitch + m0, pitch, p.sft + static_cast<size_t>(n0) * p.m_tiles + blockIdx.x, p.m_tiles, me);
+}
+
+template <int ACT, bool KEPT>
+cudaError_t launch_backward_as(const GluBackwardParams& p, int sms, cudaStream_t stream) {
+    constexpr int BYTES = sizeof(GluBackwardShared);
+    const cudaError_t e = cudaFuncSetAttribute(glu_backward_kernel<ACT, KEPT>, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES);
+    if (e != cudaSuccess) return e;
+    const int64_t tiles = static_cast<int64_t>(p.order.m_tiles) * p.order.n_tiles;
+    return launch_overlapped_smem(glu_backward_kernel<ACT, KEPT>, dim3(static_cast<unsigned>(tiles < sms ? tiles : sms)), dim3(GB_THREADS), BYTES, stream, p);
 }
 
 template <bool KEPT>
-cudaError_t launch_backward(const GluBackwardParams& p, int act, int parts, cudaStream_t stream) {
-    const dim3 grid(static_cast<unsigned>(p.m_tiles), static_cast<unsigned>(p.inner / TILE), static_cast<unsigned>(parts)), block(TILE_THREADS);
+cudaError_t launch_backward(const GluBackwardParams& p, int act, int sms, cudaStream_t stream) {
     switch (act) {
-        case DG_ACT_RELU: return launch_overlapped(glu_backward_kernel<DG_ACT_RELU, KEPT>, grid, block, stream, p);
-        case DG_ACT_GELU: return launch_overlapped(glu_backward_kernel<DG_ACT_GELU, KEPT>, grid, block, stream, p);
-        case DG_ACT_GELU_TANH: return launch_overlapped(glu_backward_kernel<DG_ACT_GELU_TANH, KEPT>, grid, block, stream, p);
-        case DG_ACT_SILU: return launch_overlapped(glu_backward_kernel<DG_ACT_SILU, KEPT>, grid, block, stream, p);
-        default: return launch_overlapped(glu_backward_kernel<DG_ACT_NONE, KEPT>, grid, block, stream, p);
+        case DG_ACT_RELU: return launch_backward_as<DG_ACT_RELU, KEPT>(p, sms, stream);
+        case DG_ACT_GELU: return launch_backward_as<DG_ACT_GELU, KEPT>(p, sms, stream);
+        case DG_ACT_GELU_TANH: return launch_backward_as<DG_ACT_GELU_TANH, KEPT>(p, sms, stream);
+        case DG_ACT_SILU: return launch_backward_as<DG_ACT_SILU, KEPT>(p, sms, stream);
+        default: return launch_backward_as<DG_ACT_NONE, KEPT>(p, sms, stream);
     }
 }
 
@@ -288,7 +374,7 @@ dg_status dg_glu_backward(const void* dH, const void* Z, const uint8_t* kept, co
     if ((kept == nullptr) != (kept_sf == nullptr) || (Z && kept)) return DG_INVALID_ARG;
     if (I % 128 != 0 || I / 128 > 65535) return DG_UNSUPPORTED_SHAPE;
     if (M == 0 || I == 0 || (!q && !qt && !ht)) return DG_OK;
-    if (M > INT32_MAX - TILE) return DG_UNSUPPORTED_SHAPE;
+    if (M > INT32_MAX - TILE || static_cast<int64_t>(cdiv(M, TILE)) * (I / TILE) > TILES_MAX) return DG_UNSUPPORTED_SHAPE;
     if ((!Z && !kept) || ((q || qt) && !dH)) return DG_INVALID_ARG;
     if (!aligned(dH, 16) || !aligned(Z, 16) || !aligned(kept, 16) || !aligned(q, 16) || !aligned(qt, 16) || !aligned(ht, 16) || !aligned(kept_sf, 4) ||
         !aligned(sf, 4) || !aligned(sft, 4) || !aligned(hsft, 4))
@@ -309,9 +395,9 @@ dg_status dg_glu_backward(const void* dH, const void* Z, const uint8_t* kept, co
     p.hsft = hsft;
     p.m = M;
     p.inner = I;
-    p.m_tiles = cdiv(M, TILE);
-    const int parts = ht ? 3 : 2;
-    const cudaError_t e = kept ? launch_backward<true>(p, act, parts, stream) : launch_backward<false>(p, act, parts, stream);
+    p.order.m_tiles = cdiv(M, TILE);
+    p.order.n_tiles = I / TILE;
+    const cudaError_t e = kept ? launch_backward<true>(p, act, dev.sms, stream) : launch_backward<false>(p, act, dev.sms, stream);
     return e == cudaSuccess ? DG_OK : DG_CUDA_ERROR;
 }
 
@@ -319,14 +405,15 @@ dg_status dg_transpose_fp8(const uint8_t* q, const float* sf, uint8_t* qt, float
     if (M < 0 || N < 0) return DG_INVALID_ARG;
     if (N % 128 != 0 || N / 128 > 65535) return DG_UNSUPPORTED_SHAPE;
     if (M == 0 || N == 0) return DG_OK;
-    if (M > INT32_MAX - TILE) return DG_UNSUPPORTED_SHAPE;
+    if (M > INT32_MAX - TILE || static_cast<int64_t>(cdiv(M, TILE)) * (N / TILE) > TILES_MAX) return DG_UNSUPPORTED_SHAPE;
     if (!q || !sf || !qt || !sft) return DG_INVALID_ARG;
     if (!aligned(q, 16) || !aligned(qt, 16) || !aligned(sf, 4) || !aligned(sft, 4)) return DG_MISALIGNED;
     DeviceInfo dev;
     const dg_status st = device_info(&dev);
     if (st != DG_OK) return st;
-    const TransposeParams p = {q, sf, qt, sft, M, N, cdiv(M, TILE)};
-    const cudaError_t e = launch_overlapped(transpose_kernel, dim3(static_cast<unsigned>(p.m_tiles), static_cast<unsigned>(N / TILE)), dim3(TILE_THREADS), stream, p);
+    const TransposeParams p = {q, sf, qt, sft, M, N, {cdiv(M, TILE), N / TILE}};
+    const int64_t tiles = static_cast<int64_t>(p.order.m_tiles) * p.order.n_tiles;
+    const cudaError_t e = launch_overlapped(transpose_kernel, dim3(static_cast<unsigned>(tiles < 2 * dev.sms ? tiles : 2 * dev.sms)), dim3(TR_THREADS), stream, p);
     return e == cudaSuccess ? DG_OK : DG_CUDA_ERROR;
 }
 

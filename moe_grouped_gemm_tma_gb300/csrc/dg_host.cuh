@@ -42,17 +42,23 @@ int tune(int knob);
 // A launch that may begin while the previous grid in the stream ends (the kernel waits for it before its first
 // access to global memory), unless the DG_TUNE_PDL knob is 0.
 template <typename... P, typename... A>
-cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, dim3 block, cudaStream_t stream, A&&... args) {
+cudaError_t launch_overlapped_smem(void (*kernel)(P...), dim3 grid, dim3 block, size_t dynamic_smem, cudaStream_t stream, A&&... args) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     cfg.gridDim = grid;
     cfg.blockDim = block;
+    cfg.dynamicSmemBytes = dynamic_smem;
     cfg.stream = stream;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = tune(DG_TUNE_PDL) != 0 ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
+template <typename... P, typename... A>
+cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, dim3 block, cudaStream_t stream, A&&... args) {
+    return launch_overlapped_smem(kernel, grid, block, 0, stream, static_cast<A&&>(args)...);
 }
 
 }  // namespace dg

@@ -269,6 +269,28 @@ __device__ __forceinline__ float2 act_value2(float2 z) {
     return z;
 }
 
+// An activation and its slope at two FP32 pre-activations, both to a few roundings of 1 (SILU: of themselves). SILU goes by
+// one sigmoid p: z p and p (1 + z e p), with e = exp(-z) right to a few last places wherever z lies: what the exponent's
+// product is rounded by, and what log2(e) has beyond FP32, go in as a factor.
+template <int ACT>
+__device__ __forceinline__ void act_both2(float2 z, float2& value, float2& slope) {
+    if (ACT == DG_ACT_SILU) {
+        constexpr float LN2 = 0.6931471805599453f;
+        const float2 minus = make_float2(-1.f, -1.f), l = make_float2(-LOG2_E, -LOG2_E);
+        const float2 c = make_float2(at_most(at_least(z.x, -100.f), 100.f), at_most(at_least(z.y, -100.f), 100.f));
+        const float2 t = __fmul2_rn(c, l);
+        float2 e = make_float2(exp2_approx(fminf(t.x, 110.f)), exp2_approx(fminf(t.y, 110.f)));
+        const float2 low = __ffma2_rn(c, make_float2(-LOG2_E_REST, -LOG2_E_REST), __ffma2_rn(c, l, __fmul2_rn(t, minus)));
+        e = __ffma2_rn(e, __fmul2_rn(low, make_float2(LN2, LN2)), e);
+        const float2 p = minus_one_over_one_plus2(e);                    // (negative)
+        value = __fmul2_rn(__fmul2_rn(make_float2(at_least(z.x, -100.f), at_least(z.y, -100.f)), minus), p);
+        slope = __fmul2_rn(p, __ffma2_rn(__fmul2_rn(c, e), p, minus));
+        return;
+    }
+    value = act_value2<ACT>(z);
+    slope = act_slope2<ACT>(z);
+}
+
 template <int ACT, int N>
 __device__ __forceinline__ void act_pairs(float (&v)[N]) {
     static_assert(N % 2 == 0, "pairs");
