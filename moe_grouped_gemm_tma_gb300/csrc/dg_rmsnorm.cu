@@ -169,9 +169,14 @@ struct NormBackwardParams {
     float inverse, eps;
 };
 
-// A group (a CTA, or a warp) takes every groups-th row and keeps its columns' weight gradient in registers.
+// A group (a CTA, or a warp) takes every groups-th row and keeps its columns' weight gradient in registers. The rows come
+// by asynchronous copies into shared memory, STAGES rows ahead, each thread's vectors to places of its own, so that no thread
+// waits for another's copies; the row's two sums cost the only barrier.
+constexpr int NORM_STAGES = 2;
+
 template <typename W, bool ROW_CTA, int N>
-__global__ void __launch_bounds__(ROW_CTA ? 32 * NORM_MAX_WARPS : 32 * NORM_ROWS) rmsnorm_backward_kernel(const NormBackwardParams p) {
+__global__ void __launch_bounds__(ROW_CTA ? 32 * NORM_MAX_WARPS : 32 * NORM_ROWS, ROW_CTA ? (N == 4 ? 1 : 2) : (N == 4 ? 5 : 8)) rmsnorm_backward_kernel(const NormBackwardParams p) {
+    extern __shared__ __align__(16) uint4 s_rows[];   // [stage][x, dy, dsum][N][thread]
     __shared__ float2 s_part[2][NORM_MAX_WARPS];
     grid_dependency_wait();
     grid_launch_dependents();
@@ -179,6 +184,26 @@ __global__ void __launch_bounds__(ROW_CTA ? 32 * NORM_MAX_WARPS : 32 * NORM_ROWS
     const int group = static_cast<int>(ROW_CTA ? blockIdx.x : blockIdx.x * NORM_ROWS + warp);
     if (!ROW_CTA && group >= p.groups) return;
     const int first = ROW_CTA ? threadIdx.x : lane, step = ROW_CTA ? blockDim.x : 32;
+    const int threads = blockDim.x, arrays = p.dsum != nullptr ? 3 : 2;
+    uint4* mine = s_rows + threadIdx.x;
+    const auto place = [&](int stage, int array, int i) { return mine + ((stage * arrays + array) * N + i) * threads; };
+    const auto fetch = [&](int row, int stage) {
+        if (row < p.rows) {
+            const size_t base = static_cast<size_t>(row) * p.vectors;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int v = first + i * step;
+                if (v < p.vectors) {
+                    cp_async_16(place(stage, 0, i), p.x + base + v);
+                    cp_async_16(place(stage, 1, i), p.dy + base + v);
+                    if (arrays == 3) cp_async_16(place(stage, 2, i), p.dsum + base + v);
+                }
+            }
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < NORM_STAGES; ++i) fetch(group + i * p.groups, i);     // (groups * stages is far below 2^31 - rows)
 
     float2 g[N][4], dg[N][4];
 #pragma unroll
@@ -187,26 +212,17 @@ __global__ void __launch_bounds__(ROW_CTA ? 32 * NORM_MAX_WARPS : 32 * NORM_ROWS
         for (int c = 0; c < 4; ++c) g[i][c] = dg[i][c] = make_float2(0.f, 0.f);
         if (first + i * step < p.vectors) load_weights<W>(p.weight, first + i * step, g[i]);
     }
-    int turn = 0;
-    for (int row = group; row < p.rows; row += p.groups, turn ^= 1) {
+    int turn = 0, stage = 0;
+    for (int row = group; row < p.rows; row += p.groups, turn ^= 1, stage = stage + 1 == NORM_STAGES ? 0 : stage + 1) {
         const size_t base = static_cast<size_t>(row) * p.vectors;
-        uint4 x[N], d[N], e[N];
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int v = first + i * step;
-            x[i] = d[i] = e[i] = make_uint4(0, 0, 0, 0);
-            if (v < p.vectors) {
-                x[i] = ld_input(p.x + base + v);
-                d[i] = ld_input(p.dy + base + v);
-                if (p.dsum != nullptr) e[i] = ld_input(p.dsum + base + v);
-            }
-        }
+        cp_async_wait_group<NORM_STAGES - 1>();
         float2 squares = make_float2(0.f, 0.f), products = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
+            if (first + i * step >= p.vectors) break;
             float2 a[4], b[4];
-            unpack_bf16(x[i], a);
-            unpack_bf16(d[i], b);
+            unpack_bf16(*place(stage, 0, i), a);
+            unpack_bf16(*place(stage, 1, i), b);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 squares = __ffma2_rn(a[c], a[c], squares);
@@ -225,18 +241,20 @@ __global__ void __launch_bounds__(ROW_CTA ? 32 * NORM_MAX_WARPS : 32 * NORM_ROWS
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int v = first + i * step;
+            if (v >= p.vectors) break;
             float2 a[4], b[4], z[4];
-            unpack_bf16(x[i], a);
-            unpack_bf16(d[i], b);
-            unpack_bf16(e[i], z);
+            unpack_bf16(*place(stage, 0, i), a);
+            unpack_bf16(*place(stage, 1, i), b);
+            unpack_bf16(arrays == 3 ? *place(stage, 2, i) : make_uint4(0, 0, 0, 0), z);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 dg[i][c] = __ffma2_rn(__fmul2_rn(b[c], a[c]), make_float2(rs, rs), dg[i][c]);
                 const float2 t = __ffma2_rn(a[c], make_float2(-mean, -mean), __fmul2_rn(b[c], g[i][c]));
                 z[c] = __ffma2_rn(t, make_float2(rs, rs), z[c]);
             }
-            if (v < p.vectors) p.dx[base + v] = pack_bf16(z);
+            p.dx[base + v] = pack_bf16(z);
         }
+        fetch(row + NORM_STAGES * p.groups, stage);
     }
     if (p.partial == nullptr) return;
 #pragma unroll
@@ -273,29 +291,41 @@ __global__ void __launch_bounds__(32 * ADD_WARPS) add_groups_kernel(const float*
     }
 }
 
-template <typename W, bool BACKWARD, typename P>
-cudaError_t launch_norm(const P& p, int H, int groups, cudaStream_t stream) {
+template <typename W>
+cudaError_t launch_norm(const NormParams& p, int H, cudaStream_t stream) {
     const auto go = [&](auto kernel, bool cta) {
-        const unsigned grid = static_cast<unsigned>(cta ? groups : cdiv(groups, NORM_ROWS));
+        const unsigned grid = static_cast<unsigned>(cta ? p.rows : cdiv(p.rows, NORM_ROWS));
         const unsigned block = static_cast<unsigned>(cta ? 32 * cdiv(H, NORM_WARP_H) : 32 * NORM_ROWS);
         return launch_overlapped(kernel, dim3(grid), dim3(block), stream, p);
     };
-    if constexpr (BACKWARD) {
-        if (H > NORM_WARP_H) return go(rmsnorm_backward_kernel<W, true, NORM_VECTORS>, true);
-        if (H > 512) return go(rmsnorm_backward_kernel<W, false, 4>, false);
-        if (H > 256) return go(rmsnorm_backward_kernel<W, false, 2>, false);
-        return go(rmsnorm_backward_kernel<W, false, 1>, false);
-    } else {
-        if (H > NORM_WARP_H) return go(rmsnorm_kernel<W, true, NORM_VECTORS>, true);
-        if (H > 512) return go(rmsnorm_kernel<W, false, 4>, false);
-        if (H > 256) return go(rmsnorm_kernel<W, false, 2>, false);
-        return go(rmsnorm_kernel<W, false, 1>, false);
-    }
+    if (H > NORM_WARP_H) return go(rmsnorm_kernel<W, true, NORM_VECTORS>, true);
+    if (H > 512) return go(rmsnorm_kernel<W, false, 4>, false);
+    if (H > 256) return go(rmsnorm_kernel<W, false, 2>, false);
+    return go(rmsnorm_kernel<W, false, 1>, false);
 }
 
-// Groups of rows of the gradient: what fits the GPU at once, whatever the GPU (so that sums do not depend on it).
+template <typename W>
+cudaError_t launch_norm_backward(const NormBackwardParams& p, int H, cudaStream_t stream) {
+    const auto go = [&](auto kernel, bool cta, int vectors) {
+        const unsigned grid = static_cast<unsigned>(cta ? p.groups : cdiv(p.groups, NORM_ROWS));
+        const unsigned block = static_cast<unsigned>(cta ? 32 * cdiv(H, 32 * 8 * vectors) : 32 * NORM_ROWS);
+        const size_t bytes = static_cast<size_t>(NORM_STAGES) * (p.dsum != nullptr ? 3 : 2) * vectors * block * 16;
+        if (bytes > 40 * 1024) {             // (more than every kernel may have without asking, less what is static)
+            const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+            if (e != cudaSuccess) return e;
+        }
+        return launch_overlapped_smem(kernel, dim3(grid), dim3(block), bytes, stream, p);
+    };
+    if (H > NORM_MAX_H / 2) return go(rmsnorm_backward_kernel<W, true, 4>, true, 4);
+    if (H > NORM_WARP_H) return go(rmsnorm_backward_kernel<W, true, 2>, true, 2);
+    if (H > 512) return go(rmsnorm_backward_kernel<W, false, 4>, false, 4);
+    if (H > 256) return go(rmsnorm_backward_kernel<W, false, 2>, false, 2);
+    return go(rmsnorm_backward_kernel<W, false, 1>, false, 1);
+}
+
+// Groups of rows of the gradient: about what fits the GPU at once, by the sizes alone, so that sums do not depend on the GPU.
 int norm_groups(int T, int H) {
-    const int most = H > NORM_WARP_H ? 304 : 1216;
+    const int most = H > 4096 ? 304 : H > 2048 ? 608 : 1216;
     return T < most ? T : most;
 }
 
@@ -339,7 +369,7 @@ dg_status dg_rmsnorm(const void* x, const void* residual, const void* weight, in
     p.pow2 = pow2;
     p.inverse = 1.f / static_cast<float>(H);
     p.eps = eps;
-    const cudaError_t e = weight_type == DG_TYPE_F32 ? launch_norm<float, false>(p, H, T, stream) : launch_norm<__nv_bfloat16, false>(p, H, T, stream);
+    const cudaError_t e = weight_type == DG_TYPE_F32 ? launch_norm<float>(p, H, stream) : launch_norm<__nv_bfloat16>(p, H, stream);
     return e == cudaSuccess ? DG_OK : DG_CUDA_ERROR;
 }
 
@@ -374,7 +404,7 @@ dg_status dg_rmsnorm_backward(const void* dy, const void* x, const void* weight,
     p.groups = norm_groups(T, H);
     p.inverse = 1.f / static_cast<float>(H);
     p.eps = eps;
-    cudaError_t e = weight_type == DG_TYPE_F32 ? launch_norm<float, true>(p, H, p.groups, stream) : launch_norm<__nv_bfloat16, true>(p, H, p.groups, stream);
+    cudaError_t e = weight_type == DG_TYPE_F32 ? launch_norm_backward<float>(p, H, stream) : launch_norm_backward<__nv_bfloat16>(p, H, stream);
     if (e == cudaSuccess && dweight)
         e = launch_overlapped(add_groups_kernel, dim3(static_cast<unsigned>(cdiv(H, 32))), dim3(32 * ADD_WARPS), stream, static_cast<const float*>(p.partial), dweight, H, p.groups);
     return e == cudaSuccess ? DG_OK : DG_CUDA_ERROR;

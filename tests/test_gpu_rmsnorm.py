@@ -127,8 +127,8 @@ def check_backward(dy, s, w, dsum, eps, dx, dw):
     assert ((dx.double() - want).abs() <= 2.0 ** -8 * want.abs() + 4 * REL * mag + 2.0 ** -133).all()
     if dw is not None:
         # a product, r's chain, and the sum: up to T / groups rows, groups / 16, 16 warps
-        T = s.shape[0]
-        groups = min(T, 304 if s.shape[1] > 1024 else 1216)
+        T, H = s.shape
+        groups = dg.load().dg_rmsnorm_backward_workspace(T, H) // (4 * H)
         chain = 24 + 3 + -(-T // groups) + -(-groups // 16) + 16
         assert ((dw.double() - want_dw).abs() <= chain * 2.0 ** -24 * (d * sd * r).abs().sum(0)).all()
 
