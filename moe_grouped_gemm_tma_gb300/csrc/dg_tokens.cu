@@ -206,20 +206,14 @@ __device__ __forceinline__ int slot_row(const int32_t* rows, size_t at, int Mt) 
     return static_cast<unsigned>(r) < static_cast<unsigned>(Mt) ? r : -1;
 }
 
-// Zeros in the rows without a token of a block that has some: the block's PAD_ROWS rows from `group` on.
-__device__ __forceinline__ void zero_pads(unsigned item, const int32_t* m_indices, uint4* out, float* out_sf, int vectors, int scales, int lane) {
+// Zeros in the rows without a token of a block that has some: the item's PAD_ROWS rows.
+__device__ __forceinline__ void zero_pads(unsigned item, const int32_t* m_indices, uint4* out, int vectors, int lane) {
     const unsigned block = item / (128 / PAD_ROWS), first = item * PAD_ROWS;
     if (ld_input(m_indices + static_cast<size_t>(block) * 128) < 0) return;
     const bool pad = lane < PAD_ROWS && ld_input(m_indices + first + lane) < 0;
-    unsigned which = __ballot_sync(FULL, pad);
-    while (which) {
+    for (unsigned which = __ballot_sync(FULL, pad); which; which &= which - 1) {
         const size_t row = first + __ffs(which) - 1;
-        which &= which - 1;
         for (int v = lane; v < vectors; v += 32) out[row * vectors + v] = make_uint4(0, 0, 0, 0);
-        if (out_sf != nullptr) {
-            const float lowest = block_scale(0).s;
-            for (int b = lane; b < scales; b += 32) out_sf[row * scales + b] = lowest;
-        }
     }
 }
 
@@ -234,40 +228,65 @@ struct GatherParams {
     unsigned tokens_items, items;
 };
 
-constexpr int GATHER_VECTORS = 4;                 // a lane's vectors of a piece: 2048 bytes, with 16 scales of codes
+// A warp has a piece of a token's row in shared memory, from where lane j has it copied to the row of slot j: the copies
+// are what the kernel is about, and each is one instruction, whatever its length.
+constexpr int GATHER_VECTORS = 256;               // a piece: 4096 bytes, with 32 scales of codes
 
 __global__ void __launch_bounds__(32 * MOVE_WARPS) gather_kernel(const GatherParams p) {
+    __shared__ __align__(128) uint4 s_piece[MOVE_WARPS][GATHER_VECTORS];
     grid_dependency_wait();
     grid_launch_dependents();
-    const int lane = threadIdx.x & 31;
-    const unsigned item = blockIdx.x * MOVE_WARPS + (threadIdx.x >> 5);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const unsigned item = blockIdx.x * MOVE_WARPS + warp;
     if (item >= p.items) return;
+    uint4* piece = s_piece[warp];
     if (item >= p.tokens_items) {
-        zero_pads(item - p.tokens_items, p.m_indices, p.out, p.out_sf, p.vectors, p.scales, lane);
+        // the rows without a token of 8 rows of a block that has some
+        const unsigned first = (item - p.tokens_items) * PAD_ROWS;
+        if (ld_input(p.m_indices + first / 128 * 128) < 0) return;
+        const unsigned pads = __ballot_sync(FULL, lane < PAD_ROWS && ld_input(p.m_indices + first + lane % PAD_ROWS) < 0);
+        if (pads == 0) return;
+#pragma unroll
+        for (int i = 0; i < GATHER_VECTORS / 32; ++i) piece[i * 32 + lane] = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+        for (int i = lane; i < PAD_ROWS * p.pieces; i += 32) {
+            const int at = i / PAD_ROWS * GATHER_VECTORS, left = p.vectors - at;
+            if (pads >> (i % PAD_ROWS) & 1)
+                bulk_store(p.out + static_cast<size_t>(first + i % PAD_ROWS) * p.vectors + at, piece, 16u * static_cast<uint32_t>(left < GATHER_VECTORS ? left : GATHER_VECTORS));
+        }
+        bulk_commit();
+        if (p.out_sf != nullptr) {
+            const float lowest = block_scale(0).s;
+            for (unsigned which = pads; which; which &= which - 1)
+                for (int b = lane; b < p.scales; b += 32) p.out_sf[static_cast<size_t>(first + __ffs(which) - 1) * p.scales + b] = lowest;
+        }
+        bulk_wait_read();
         return;
     }
-    const unsigned t = item / p.pieces, piece = item - t * p.pieces;
+    const unsigned t = item / p.pieces;
+    const int at = static_cast<int>(item - t * p.pieces) * GATHER_VECTORS;
+    const int here = p.vectors - at < GATHER_VECTORS ? p.vectors - at : GATHER_VECTORS;
     const int mine = lane < p.k ? slot_row(p.rows, static_cast<size_t>(t) * p.k + lane, p.Mt) : -1;
-    unsigned open = __ballot_sync(FULL, mine >= 0);
-    if (open == 0) return;
-    const int v0 = static_cast<int>(piece) * 32 * GATHER_VECTORS + lane;
-    const uint4* src = p.x + static_cast<size_t>(t) * p.vectors;
-    uint4 v[GATHER_VECTORS];
+    const uint4* src = p.x + static_cast<size_t>(t) * p.vectors + at;
 #pragma unroll
-    for (int i = 0; i < GATHER_VECTORS; ++i)
-        if (v0 + 32 * i < p.vectors) v[i] = ld_input(src + v0 + 32 * i);
-    const int b = static_cast<int>(piece) * (4 * GATHER_VECTORS) + lane;
-    const bool scaled = p.sf != nullptr && lane < 4 * GATHER_VECTORS && b < p.scales;
+    for (int i = 0; i < GATHER_VECTORS / 32; ++i)
+        if (i * 32 + lane < here) cp_async_16(piece + i * 32 + lane, src + i * 32 + lane);
+    const int b = at / 8 + lane;                  // (a scale for each 8 vectors)
+    const bool scaled = p.sf != nullptr && b < p.scales;
     const float s = scaled ? ld_input(p.sf + static_cast<size_t>(t) * p.scales + b) : 0.f;
-    while (open) {
-        const size_t row = static_cast<size_t>(__shfl_sync(FULL, mine, __ffs(open) - 1));
-        open &= open - 1;
-        uint4* dst = p.out + row * p.vectors;
-#pragma unroll
-        for (int i = 0; i < GATHER_VECTORS; ++i)
-            if (v0 + 32 * i < p.vectors) dst[v0 + 32 * i] = v[i];
-        if (scaled) p.out_sf[row * p.scales + b] = s;
-    }
+    const unsigned open = __ballot_sync(FULL, mine >= 0);
+    cp_async_wait_all();
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (mine >= 0) bulk_store(p.out + static_cast<size_t>(mine) * p.vectors + at, piece, 16u * static_cast<uint32_t>(here));
+    bulk_commit();
+    if (p.sf != nullptr)
+        for (unsigned left = open; left; left &= left - 1) {
+            const size_t row = static_cast<size_t>(__shfl_sync(FULL, mine, __ffs(left) - 1));
+            if (scaled) p.out_sf[row * p.scales + b] = s;
+        }
+    bulk_wait_read();
 }
 
 // ------------------------------------------------------------------------------------ weighted sum
@@ -299,7 +318,7 @@ __device__ __forceinline__ uint4 pack_bf16(const float2 (&a)[4]) {
 
 // A warp a piece of 512 bytes of a token's row, four experts' rows in flight at a time. FP32 sums, in the slots' order
 // from zero on, the residual last.
-__global__ void __launch_bounds__(32 * MOVE_WARPS) combine_kernel(const CombineParams p) {
+__global__ void __launch_bounds__(32 * MOVE_WARPS, 6) combine_kernel(const CombineParams p) {
     grid_dependency_wait();
     grid_launch_dependents();
     const int lane = threadIdx.x & 31;
@@ -318,7 +337,7 @@ __global__ void __launch_bounds__(32 * MOVE_WARPS) combine_kernel(const CombineP
     float2 a[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) a[i] = make_float2(0.f, 0.f);
-    while (open) {
+    for (; open != 0;) {
         uint4 y[4];
         float w[4];
         const int n = __popc(open);
@@ -365,7 +384,7 @@ __global__ void __launch_bounds__(32 * CB_WARPS) combine_backward_kernel(const C
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (blockIdx.x >= p.token_ctas) {
         const unsigned item = (blockIdx.x - p.token_ctas) * CB_WARPS + warp;
-        if (item < p.pads) zero_pads(item, p.m_indices, p.dy, nullptr, p.vectors, 0, lane);
+        if (item < p.pads) zero_pads(item, p.m_indices, p.dy, p.vectors, lane);
         return;
     }
     const int t = static_cast<int>(WIDE ? blockIdx.x : blockIdx.x * CB_WARPS + warp);
@@ -558,7 +577,7 @@ dg_status dg_moe_gather(const void* x, const float* sf, int x_type, const int32_
     p.vectors = codes ? H / 16 : H / 8;
     p.scales = codes ? H / 128 : 0;
     p.Mt = Mt;
-    p.pieces = cdiv(p.vectors, 32 * GATHER_VECTORS);
+    p.pieces = cdiv(p.vectors, GATHER_VECTORS);
     p.tokens_items = k > 0 ? static_cast<unsigned>(T) * static_cast<unsigned>(p.pieces) : 0u;
     p.items = p.tokens_items + (m_indices ? static_cast<unsigned>(Mt / PAD_ROWS) : 0u);
     const cudaError_t e = launch_overlapped(gather_kernel, dim3((p.items + MOVE_WARPS - 1) / MOVE_WARPS), dim3(32 * MOVE_WARPS), stream, p);
