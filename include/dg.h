@@ -264,7 +264,7 @@ int64_t dg_moe_layer_workspace(int T, int k, int E, int H, int I);
  *   them; the product and dg_glu take no more than max_m.
  * 1 <= E <= 1024, k <= 32, T * k <= 2^23, E * max_m < 2^31.
  * workspace: device memory of dg_moe_sort_workspace(T, k, E) bytes, 16-byte aligned, with anything in it; 0 bytes (and null)
- * up to 4096 slots. dg_moe_sort_rows and dg_moe_sort_workspace return -1 for sizes outside these.
+ * up to 16384 slots. dg_moe_sort_rows and dg_moe_sort_workspace return -1 for sizes outside these.
  */
 dg_status dg_moe_sort_contiguous(const int32_t* ids, int32_t* rows, int32_t* counts, int32_t* m_indices, void* workspace,
                                  int64_t workspace_bytes, int T, int k, int E, int Mt, cudaStream_t stream);

@@ -4,10 +4,9 @@
 // weights.
 //
 // Sort. A counting sort by expert that keeps the slots' order, so that its result does not depend on timing: a warp takes
-// consecutive slots, 32 at a time; match.any gives each lane the others with its expert, whose number below it is its
-// place among the 32, and the lowest of them counts for all. Up to SORT_ONE slots are one CTA's; more are cut into
-// chunks, a CTA each, whose counts a first launch writes and a second adds up: every CTA for itself, because the counts
-// are few (128 chunks x 256 experts are 128 KB out of L2).
+// consecutive slots, 32 at a time; ballots over the bits of the expert give each lane the others with its own, whose number
+// below it is its place among the 32. Up to SORT_ALONE slots are sorted by one launch, whose CTAs each count all slots and
+// place 512 of them; more are cut into chunks, whose counts a first launch writes, a second adds up and a third uses.
 //
 // The rows are moved token by token: a token's row is read once, however many experts it goes to, and every access is a
 // piece of 512 bytes of a row a warp. Rows without a token inside an expert's block of 128 are zeroed by warps of their own.
@@ -29,17 +28,18 @@ constexpr unsigned FULL = 0xffffffffu;
 // ------------------------------------------------------------------------------------ sort
 constexpr int SORT_THREADS = 512;
 constexpr int SORT_WARPS = SORT_THREADS / 32;
-constexpr int SORT_ONE = 4096;                    // slots that one CTA sorts alone
-constexpr int SORT_CHUNKS = 152;                  // chunks at most
-constexpr int64_t SORT_MAX_SLOTS = 1 << 23;       // (a chunk's counts fit 16 bits: it has 55296 slots then)
+constexpr int SORT_ALONE = 16384;                 // slots that one launch sorts
+constexpr int SORT_CHUNKS = 608;                  // chunks at most: four CTAs an SM
+constexpr int64_t SORT_MAX_SLOTS = 1 << 23;       // (a chunk's counts fit 16 bits: it has 13824 slots then)
 
 struct SortParams {
     const int32_t* ids;
     int32_t* rows;
     int32_t* counts;
     int32_t* m_indices;   // null: masked layout
+    int32_t* totals;      // [E], then, by expert, the chunks' counts, which become those of the chunks before
     int32_t* chunk_counts;
-    int slots, experts, blocks, max_m, groups, chunks;
+    int slots, experts, bits, blocks, max_m, groups, chunks;
 };
 
 __device__ __forceinline__ unsigned lanes_below() {
@@ -48,17 +48,31 @@ __device__ __forceinline__ unsigned lanes_below() {
     return m;
 }
 
-// The expert of a warp's slot in its group g, -1 where there is none.
+// A slot's expert, `experts` where there is none.
 __device__ __forceinline__ int slot_expert(const SortParams& p, int slot) {
     const int id = slot < p.slots ? ld_input(p.ids + slot) : -1;
-    return static_cast<unsigned>(id) < static_cast<unsigned>(p.experts) ? id : -1;
+    return static_cast<unsigned>(id) < static_cast<unsigned>(p.experts) ? id : p.experts;
 }
 
-// COUNT: the first of two launches, which writes a chunk's counts; else the slots are placed.
-template <bool COUNT>
+// The lanes that have the same e, of `bits` bits. (match.any goes through the values one by one: a group of 32 slots took
+// 1 us.)
+__device__ __forceinline__ unsigned same_lanes(int e, int bits) {
+    unsigned same = FULL;
+    for (int i = 0; i < bits; ++i) {
+        const unsigned ones = __ballot_sync(FULL, e >> i & 1);
+        same &= e >> i & 1 ? ones : ~ones;
+    }
+    return same;
+}
+
+// ALONE: the only launch; each CTA counts all slots, and places its own chunk. COUNT: the first of three launches, which
+// writes the chunks' counts; PLACE: the last, when they have been added up.
+enum SortStep { SORT_STEP_ALONE, SORT_STEP_COUNT, SORT_STEP_PLACE };
+
+template <SortStep STEP>
 __global__ void __launch_bounds__(SORT_THREADS) sort_kernel(const SortParams p) {
-    __shared__ uint16_t s_warp[SORT_WARPS][MAX_ROUTE_EXPERTS];   // a warp's slots of an expert, then those of the warps before it
-    __shared__ int s_total[MAX_ROUTE_EXPERTS];                   // an expert's slots
+    __shared__ uint32_t s_warp[SORT_WARPS][MAX_ROUTE_EXPERTS / 2];   // 16 bits each: a warp's slots of an expert, then those of the warps before it
+    __shared__ int s_total[MAX_ROUTE_EXPERTS + 1];               // an expert's slots
     __shared__ int s_before[MAX_ROUTE_EXPERTS];                  // those of the chunks before this one
     __shared__ int s_base[MAX_ROUTE_EXPERTS];                    // the expert's first row
     __shared__ int s_sum[SORT_WARPS];
@@ -67,62 +81,61 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_kernel(const SortParams p) 
     grid_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int E = p.experts, chunk = static_cast<int>(blockIdx.x);
-    for (int i = threadIdx.x; i < E; i += SORT_THREADS) {
+    const int first = (chunk * SORT_WARPS + warp) * p.groups * 32 + lane;
+    for (int i = threadIdx.x; i < (E + 1) / 2; i += SORT_THREADS) {
 #pragma unroll
         for (int w = 0; w < SORT_WARPS; ++w) s_warp[w][i] = 0;
-        s_total[i] = 0;
-        s_before[i] = 0;
     }
+    if (STEP == SORT_STEP_ALONE)
+        for (int i = threadIdx.x; i <= E; i += SORT_THREADS) s_total[i] = 0;
     __syncthreads();
 
-    const int first = (chunk * SORT_WARPS + warp) * p.groups * 32;
-    for (int g = 0; g < p.groups; ++g) {
-        const int e = slot_expert(p, first + g * 32 + lane);
-        const unsigned same = __match_any_sync(FULL, e);
-        if (e >= 0 && (same & lanes_below()) == 0) s_warp[warp][e] += __popc(same);
-        __syncwarp();
+    // ---- counts (whole numbers: in any order)
+    if (STEP == SORT_STEP_ALONE) {
+        // a total in the lower 16 bits, what of it lies before this chunk in the upper ones
+        const int start = chunk * SORT_THREADS;
+#pragma unroll 4
+        for (int slot = threadIdx.x; slot < p.slots; slot += SORT_THREADS) {
+            const int e = slot_expert(p, slot);
+            atomicAdd(&s_total[e], slot < start ? 0x10001 : 1);
+            if (slot == first && e < E) atomicAdd(&s_warp[warp][e >> 1], 1u << (16 * (e & 1)));
+        }
+    } else {
+#pragma unroll 4
+        for (int g = 0; g < p.groups; ++g) {
+            const int e = slot_expert(p, first + g * 32);
+            if (e < E) atomicAdd(&s_warp[warp][e >> 1], 1u << (16 * (e & 1)));
+        }
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < E; e += SORT_THREADS) {
-        int sum = 0;
+    if (STEP == SORT_STEP_ALONE) {
+        for (int e = threadIdx.x; e < E; e += SORT_THREADS) {
+            const int both = s_total[e];
+            s_total[e] = both & 0xffff;
+            s_before[e] = both >> 16;
+        }
+    }
+    // ---- over the warps, two experts a thread
+    for (int i = threadIdx.x; i < (E + 1) / 2; i += SORT_THREADS) {
+        uint32_t sum = 0;
 #pragma unroll
         for (int w = 0; w < SORT_WARPS; ++w) {
-            const int c = s_warp[w][e];
-            s_warp[w][e] = static_cast<uint16_t>(sum);
+            const uint32_t c = s_warp[w][i];
+            s_warp[w][i] = sum;
             sum += c;
         }
-        if (COUNT) p.chunk_counts[static_cast<size_t>(chunk) * E + e] = sum;
-        else if (p.chunks == 1) s_total[e] = sum;
+        if (STEP == SORT_STEP_COUNT) {
+            int32_t* dst = p.chunk_counts + 2 * i * p.chunks + chunk;
+            dst[0] = static_cast<int>(sum & 0xffff);
+            if (2 * i + 1 < E) dst[p.chunks] = static_cast<int>(sum >> 16);
+        }
     }
-    if (COUNT) return;
+    if (STEP == SORT_STEP_COUNT) return;
 
-    // ---- the other chunks' counts: each part of the threads takes every parts-th chunk
-    if (p.chunks > 1) {
-        const int parts = E < SORT_THREADS ? SORT_THREADS / E : 1;
-        const int part = static_cast<int>(threadIdx.x) / E;
-        if (parts == 1) {
-            for (int e = threadIdx.x; e < E; e += SORT_THREADS) {
-                int total = 0, before = 0;
-#pragma unroll 8
-                for (int c = 0; c < p.chunks; ++c) {
-                    const int n = __ldcg(p.chunk_counts + static_cast<size_t>(c) * E + e);
-                    total += n;
-                    before += c < chunk ? n : 0;
-                }
-                s_total[e] = total;
-                s_before[e] = before;
-            }
-        } else if (part < parts) {
-            const int e = static_cast<int>(threadIdx.x) - part * E;
-            int total = 0, before = 0;
-#pragma unroll 8
-            for (int c = part; c < p.chunks; c += parts) {
-                const int n = __ldcg(p.chunk_counts + static_cast<size_t>(c) * E + e);
-                total += n;
-                before += c < chunk ? n : 0;
-            }
-            atomicAdd(&s_total[e], total);         // (whole numbers: in any order)
-            atomicAdd(&s_before[e], before);
+    if (STEP == SORT_STEP_PLACE) {
+        for (int e = threadIdx.x; e < E; e += SORT_THREADS) {
+            s_total[e] = __ldcg(p.totals + e);
+            s_before[e] = __ldcg(p.chunk_counts + e * p.chunks + chunk);
         }
     }
     __syncthreads();
@@ -159,27 +172,30 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_kernel(const SortParams p) 
     __syncthreads();
 
     // ---- the slots' rows
-    for (int g = 0; g < p.groups; ++g) {
-        const int slot = first + g * 32 + lane;
-        const int e = slot_expert(p, slot);
-        const unsigned same = __match_any_sync(FULL, e);
-        const unsigned below = same & lanes_below();
-        int row = -1;
-        if (e >= 0) {
-            const int place = s_before[e] + s_warp[warp][e] + __popc(below);
-            if (p.max_m == 0 || place < p.max_m) row = s_base[e] + place;
+    if (chunk < p.chunks) {
+        for (int g = 0; g < p.groups; ++g) {
+            const int slot = first + g * 32;
+            const int e = slot_expert(p, slot);
+            const unsigned same = same_lanes(e, p.bits), below = same & lanes_below();
+            int row = -1;
+            if (e < E) {
+                const int place = s_before[e] + static_cast<int>(s_warp[warp][e >> 1] >> (16 * (e & 1)) & 0xffff) + __popc(below);
+                if (p.max_m == 0 || place < p.max_m) row = s_base[e] + place;
+            }
+            if (p.groups > 1) {
+                __syncwarp();
+                if (e < E && below == 0) atomicAdd(&s_warp[warp][e >> 1], static_cast<uint32_t>(__popc(same)) << (16 * (e & 1)));
+                __syncwarp();
+            }
+            if (slot < p.slots) p.rows[slot] = row;
         }
-        __syncwarp();
-        if (e >= 0 && below == 0) s_warp[warp][e] += __popc(same);
-        __syncwarp();
-        if (slot < p.slots) p.rows[slot] = row;
     }
     if (chunk == 0)
         for (int e = threadIdx.x; e < E; e += SORT_THREADS) p.counts[e] = s_total[e];
 
     // ---- the expert of every row: a block of 128 rows is one expert's, the last whose first row is not behind it
     if (p.m_indices != nullptr) {
-        for (int b = chunk * SORT_WARPS + warp; b < p.blocks; b += p.chunks * SORT_WARPS) {
+        for (int b = chunk * SORT_WARPS + warp; b < p.blocks; b += static_cast<int>(gridDim.x) * SORT_WARPS) {
             int e = 0;
             for (int lo = 1, hi = E; lo < hi;) {
                 const int mid = (lo + hi) >> 1;
@@ -194,6 +210,34 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_kernel(const SortParams p) 
             reinterpret_cast<int4*>(p.m_indices)[static_cast<size_t>(b) * 32 + lane] =
                 make_int4(left > 0 ? e : -1, left > 1 ? e : -1, left > 2 ? e : -1, left > 3 ? e : -1);
         }
+    }
+}
+
+// The chunks' counts of an expert added up, a warp an expert.
+__global__ void __launch_bounds__(SORT_THREADS) sort_scan_kernel(int32_t* totals, int32_t* chunk_counts, int experts, int chunks) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int lane = threadIdx.x & 31, e = static_cast<int>(blockIdx.x) * SORT_WARPS + (threadIdx.x >> 5);
+    if (e >= experts) return;
+    constexpr int PER = SORT_CHUNKS / 32;
+    int32_t* mine = chunk_counts + e * chunks + lane * PER;   // the lane's chunks are consecutive
+    int n[PER], sum = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) n[i] = lane * PER + i < chunks ? __ldcg(mine + i) : 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) sum += n[i];
+    int upto = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(FULL, upto, o);
+        if (lane >= o) upto += v;
+    }
+    if (lane == 31) totals[e] = upto;
+    int before = upto - sum;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        if (lane * PER + i < chunks) mine[i] = before;
+        before += n[i];
     }
 }
 
@@ -458,12 +502,10 @@ __global__ void __launch_bounds__(32 * CB_WARPS) combine_backward_kernel(const C
     }
 }
 
-// Chunks of the slots and groups of 32 a warp; the chunks' counts are the workspace.
+// Chunks of the slots and groups of 32 a warp; several launches' worth of chunks have their counts in the workspace.
 void sort_plan(int64_t slots, int* groups, int* chunks) {
-    *groups = cdiv(slots, SORT_THREADS);
-    *chunks = 1;
-    if (slots <= SORT_ONE) return;
-    *groups = cdiv(slots, static_cast<int64_t>(SORT_THREADS) * SORT_CHUNKS);
+    *groups = 1;
+    if (slots > SORT_ALONE) *groups = cdiv(slots, static_cast<int64_t>(SORT_THREADS) * SORT_CHUNKS);
     *chunks = cdiv(slots, static_cast<int64_t>(SORT_THREADS) * *groups);
 }
 
@@ -488,15 +530,28 @@ dg_status sort(const int32_t* ids, int32_t* rows, int32_t* counts, int32_t* m_in
     p.rows = rows;
     p.counts = counts;
     p.m_indices = Mt > 0 ? m_indices : nullptr;
-    p.chunk_counts = static_cast<int32_t*>(workspace);
+    p.totals = static_cast<int32_t*>(workspace);
+    p.chunk_counts = p.totals + E;
     p.slots = T * k;
     p.experts = E;
     p.blocks = Mt / 128;
     p.max_m = max_m;
     sort_plan(p.slots, &p.groups, &p.chunks);
+    for (p.bits = 0; E >> p.bits != 0;) ++p.bits;         // of 0 .. E
     cudaError_t e = cudaSuccess;
-    if (p.chunks > 1) e = launch_overlapped(sort_kernel<true>, dim3(static_cast<unsigned>(p.chunks)), dim3(SORT_THREADS), stream, p);
-    if (e == cudaSuccess) e = launch_overlapped(sort_kernel<false>, dim3(static_cast<unsigned>(p.chunks)), dim3(SORT_THREADS), stream, p);
+    const dim3 block(SORT_THREADS);
+    if (p.slots <= SORT_ALONE) {
+        // (CTAs without slots help to write m_indices, four blocks of rows a warp)
+        const int most = p.m_indices != nullptr ? cdiv(p.blocks, 4 * SORT_WARPS) : 1;
+        const int ctas = p.chunks > most ? p.chunks : most < SORT_CHUNKS ? most : SORT_CHUNKS;
+        e = launch_overlapped(sort_kernel<SORT_STEP_ALONE>, dim3(static_cast<unsigned>(ctas)), block, stream, p);
+    } else {
+        const dim3 grid(static_cast<unsigned>(p.chunks));
+        e = launch_overlapped(sort_kernel<SORT_STEP_COUNT>, grid, block, stream, p);
+        if (e == cudaSuccess)
+            e = launch_overlapped(sort_scan_kernel, dim3(static_cast<unsigned>(cdiv(E, SORT_WARPS))), block, stream, p.totals, p.chunk_counts, E, p.chunks);
+        if (e == cudaSuccess) e = launch_overlapped(sort_kernel<SORT_STEP_PLACE>, grid, block, stream, p);
+    }
     return e == cudaSuccess ? DG_OK : DG_CUDA_ERROR;
 }
 
@@ -527,9 +582,10 @@ int64_t dg_moe_sort_workspace(int T, int k, int E) {
     if (T < 0 || k < 0 || E < 1 || k > MAX_ROUTE_K || E > MAX_ROUTE_EXPERTS) return -1;
     const int64_t slots = static_cast<int64_t>(T) * k;
     if (slots > SORT_MAX_SLOTS) return -1;
-    int groups, chunks;
-    sort_plan(slots, &groups, &chunks);
-    return chunks > 1 ? static_cast<int64_t>(SORT_CHUNKS) * E * 4 : 0;
+    if (slots <= SORT_ALONE) return 0;
+    // (the most chunks that any number of slots up to this has: a workspace is for smaller calls too)
+    const int64_t chunks = cdiv(slots, SORT_THREADS) < SORT_CHUNKS ? cdiv(slots, SORT_THREADS) : SORT_CHUNKS;
+    return (chunks + 1) * E * 4;
 }
 
 dg_status dg_moe_sort_contiguous(const int32_t* ids, int32_t* rows, int32_t* counts, int32_t* m_indices, void* workspace,

@@ -34,7 +34,7 @@ def test_sort_refusals():
     for name in ("ids", "rows", "counts"):
         assert call(**{name: ODD2}) == MISALIGNED, name
     assert call(m=ODD8) == MISALIGNED and call(ws=ODD8) == MISALIGNED
-    assert call(T=4096, ws=None, Mt=1 << 14) == INVALID and call(T=4096, size=16, Mt=1 << 14) == INVALID
+    assert call(T=8193, ws=None, Mt=1 << 15) == INVALID and call(T=8193, size=16, Mt=1 << 15) == INVALID
     base = dict(ids=OK, rows=OK, counts=OK, ws=OK, size=1 << 30, T=4, k=2, E=4, max_m=16)
     call = calls(L.dg_moe_sort_masked, base)
     assert call(T=-1) == INVALID and call(k=-1) == INVALID and call(E=0) == INVALID and call(max_m=0) == INVALID and call(max_m=-1) == INVALID
@@ -53,9 +53,11 @@ def test_sort_sizes():
         met = min(E, T * k)
         spare = T * k - met
         assert rows == 128 * (met + spare // 128), (T, k, E)
-    assert L.dg_moe_sort_workspace(4096, 1, 8) == 0 and L.dg_moe_sort_workspace(4097, 1, 8) == 152 * 8 * 4
+    assert L.dg_moe_sort_workspace(16384, 1, 8) == 0 and L.dg_moe_sort_workspace(1 << 20, 8, 8) == (608 + 1) * 8 * 4 and L.dg_moe_sort_workspace(16385, 1, 8) == (33 + 1) * 8 * 4
     for bad in ((-1, 1, 1), (1, -1, 1), (1, 1, 0), (1, 33, 64), (1, 1, 1025), (1 << 22, 8, 64)):
         assert L.dg_moe_sort_rows(*bad) == -1 and L.dg_moe_sort_workspace(*bad) == -1
+    sizes = [L.dg_moe_sort_workspace(n, 1, 64) for n in range(16000, 1 << 20, 497)]
+    assert sizes == sorted(sizes)                  # one for many tokens serves fewer
     with pytest.raises(dg.DGError):
         dg.moe_sort_rows(1, 33, 64)
     with pytest.raises(dg.DGError):

@@ -39,7 +39,7 @@ def sort_contiguous(ids, E, extra=0, ws=None):
     return rows, counts, m_indices
 
 
-SIZES = [(1, 1, 1), (1, 8, 64), (5, 2, 8), (33, 6, 3), (127, 1, 2), (128, 4, 256), (511, 8, 256), (512, 8, 1024), (513, 8, 7), (1000, 32, 40), (8189, 8, 256),
+SIZES = [(1, 1, 1), (1, 8, 64), (5, 2, 8), (33, 6, 3), (127, 1, 2), (128, 4, 256), (511, 8, 256), (512, 8, 1024), (513, 8, 7), (1000, 32, 40), (512, 32, 256), (2049, 8, 64), (8189, 8, 256),
          (2500, 3, 1000), (20000, 4, 600)]
 
 
@@ -92,12 +92,12 @@ def test_sort_of_nothing():
 
 
 def test_sort_refuses_too_few_rows_and_no_workspace():
-    ids = make_ids(600, 8, 16, "spread")
+    ids = make_ids(2100, 8, 16, "spread")
     out = lambda n: torch.empty(n, dtype=torch.int32, device=DEV)  # noqa: E731
     with pytest.raises(dg.DGError, match="UNSUPPORTED"):
-        dg.dg_moe_sort_contiguous(ids, torch.empty_like(ids), out(16), out(dg.moe_sort_rows(600, 8, 16) - 128), dg.moe_sort_workspace(600, 8, 16))
+        dg.dg_moe_sort_contiguous(ids, torch.empty_like(ids), out(16), out(dg.moe_sort_rows(2100, 8, 16) - 128), dg.moe_sort_workspace(2100, 8, 16))
     with pytest.raises(dg.DGError, match="INVALID"):
-        dg.dg_moe_sort_contiguous(ids, torch.empty_like(ids), out(16), out(dg.moe_sort_rows(600, 8, 16)))
+        dg.dg_moe_sort_contiguous(ids, torch.empty_like(ids), out(16), out(dg.moe_sort_rows(2100, 8, 16)))
 
 
 # ---------------------------------------------------------------- rows
