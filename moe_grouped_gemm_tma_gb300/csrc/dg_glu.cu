@@ -24,7 +24,7 @@ namespace dg {
 namespace {
 
 constexpr unsigned FULL = 0xffffffffu;
-constexpr int64_t TILES_MAX = INT32_MAX / 2;        // (a CTA's next tile is numbered in 32 bits too)
+constexpr int64_t TILES_MAX = INT32_MAX / 2;        // (tiles are numbered in 32 bits)
 constexpr int GLU_WARPS = 4;
 constexpr int GLU_ROWS = 8 * GLU_WARPS;           // rows of a CTA
 
@@ -153,7 +153,7 @@ struct GluBackwardParams {
     uint8_t* ht;
     float* hsft;
     int m, inner;
-    TileOrder order;
+    int m_tiles, n_tiles;
 };
 
 constexpr int GB_ROWS = 4;                        // rows of a warp
@@ -169,11 +169,9 @@ __global__ void __launch_bounds__(GB_THREADS, 1) glu_backward_kernel(const GluBa
     grid_dependency_wait();
     grid_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const size_t inner = p.inner, blocks = inner / 128, pitch = static_cast<size_t>(p.order.m_tiles) * TILE;
-    const int tiles = p.order.m_tiles * p.order.n_tiles;
-    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-        int tm, tn;
-        p.order.at(tile, &tm, &tn);
+    const size_t inner = p.inner, blocks = inner / 128, pitch = static_cast<size_t>(p.m_tiles) * TILE;
+    for (TileWalk walk(p.m_tiles, p.n_tiles); walk.more(); walk.next()) {
+        const int tm = walk.m, tn = walk.n;
         const int r0 = tm * TILE + warp * GB_ROWS, c0 = tn * TILE + lane * 4, valid = p.m - r0;
         float2 dg[GB_ROWS][2], du[GB_ROWS][2], h[GB_ROWS][2];
         {
@@ -232,10 +230,10 @@ __global__ void __launch_bounds__(GB_THREADS, 1) glu_backward_kernel(const GluBa
         __syncthreads();
         const int part = static_cast<int>(threadIdx.x) / TILE, column = static_cast<int>(threadIdx.x) % TILE;
         if (p.qt != nullptr) {
-            if (part == 0) s.dg.scale(column, p.sft + (static_cast<size_t>(tn) * TILE + column) * p.order.m_tiles + tm);
-            else if (part == 1) s.du.scale(column, p.sft + (inner + static_cast<size_t>(tn) * TILE + column) * p.order.m_tiles + tm);
+            if (part == 0) s.dg.scale(column, p.sft + (static_cast<size_t>(tn) * TILE + column) * p.m_tiles + tm);
+            else if (part == 1) s.du.scale(column, p.sft + (inner + static_cast<size_t>(tn) * TILE + column) * p.m_tiles + tm);
         }
-        if (p.ht != nullptr && part == 2) s.h.scale(column, p.hsft + (static_cast<size_t>(tn) * TILE + column) * p.order.m_tiles + tm);
+        if (p.ht != nullptr && part == 2) s.h.scale(column, p.hsft + (static_cast<size_t>(tn) * TILE + column) * p.m_tiles + tm);
         __syncthreads();
         if (p.qt != nullptr) {
             s.dg.quantise(dg, warp, lane);
@@ -258,7 +256,7 @@ struct TransposeParams {
     uint8_t* qt;
     float* sft;
     int m, n;
-    TileOrder order;
+    int m_tiles, n_tiles;
 };
 
 constexpr int TR_ROWS = 8;
@@ -270,30 +268,38 @@ __global__ void __launch_bounds__(TR_THREADS, 2) transpose_kernel(const Transpos
     grid_dependency_wait();
     grid_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int tiles = p.order.m_tiles * p.order.n_tiles;
-    const size_t pitch = static_cast<size_t>(p.order.m_tiles) * TILE;
+    const size_t pitch = static_cast<size_t>(p.m_tiles) * TILE;
     uint32_t codes[TR_ROWS];
     float scale = 0.f;                            // lanes 0 .. 7: of the warp's rows
-    int tm = 0, tn = 0;
-    const auto load = [&](int tile) {
-        p.order.at(tile, &tm, &tn);
-        const int r0 = tm * TILE + warp * TR_ROWS, valid = p.m - r0;
-        const uint8_t* src = p.q + static_cast<size_t>(r0) * p.n + tn * TILE + lane * 4;
-        scale = lane < TR_ROWS && lane < valid ? ld_input(p.sf + (static_cast<size_t>(r0) + lane) * (p.n / TILE) + tn) : 0.f;
+    const size_t n = p.n, blocks = n / TILE;
+    TileWalk walk(p.m_tiles, p.n_tiles);
+    const auto load = [&]() {
+        const int r0 = walk.m * TILE + warp * TR_ROWS, valid = p.m - r0;
+        const uint8_t* src = p.q + r0 * n + walk.n * TILE + lane * 4;
+        const float* sf = p.sf + (r0 + lane) * blocks + walk.n;
+        if (valid >= TR_ROWS) {
+            if (lane < TR_ROWS) scale = ld_input(sf);
 #pragma unroll
-        for (int i = 0; i < TR_ROWS; ++i) codes[i] = i < valid ? ld_input(reinterpret_cast<const uint32_t*>(src + static_cast<size_t>(i) * p.n)) : 0u;
+            for (int i = 0; i < TR_ROWS; ++i, src += n) codes[i] = ld_input(reinterpret_cast<const uint32_t*>(src));
+        } else {
+            scale = lane < valid ? ld_input(sf) : 0.f;
+#pragma unroll
+            for (int i = 0; i < TR_ROWS; ++i, src += n) codes[i] = i < valid ? ld_input(reinterpret_cast<const uint32_t*>(src)) : 0u;
+        }
     };
-    if (static_cast<int>(blockIdx.x) < tiles) load(blockIdx.x);
-    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-        const size_t column = static_cast<size_t>(tn) * TILE;
-        const int m = tm;
+    if (walk.more()) load();
+    for (bool more = walk.more(); more;) {
+        const size_t column = static_cast<size_t>(walk.n) * TILE;
+        const int m = walk.m;
         float2 v[TR_ROWS][2];
 #pragma unroll
         for (int i = 0; i < TR_ROWS; ++i) code_values(codes[i], __shfl_sync(FULL, scale, i), v[i]);
-        if (tile + static_cast<int>(gridDim.x) < tiles) load(tile + gridDim.x);
+        walk.next();
+        more = walk.more();
+        if (more) load();
         s.maxima(v, warp, lane);
         __syncthreads();
-        if (threadIdx.x < TILE) s.scale(threadIdx.x, p.sft + (column + threadIdx.x) * p.order.m_tiles + m);
+        if (threadIdx.x < TILE) s.scale(threadIdx.x, p.sft + (column + threadIdx.x) * p.m_tiles + m);
         __syncthreads();
         s.quantise(v, warp, lane);
         __syncthreads();
@@ -306,7 +312,7 @@ cudaError_t launch_backward_as(const GluBackwardParams& p, int sms, cudaStream_t
     constexpr int BYTES = sizeof(GluBackwardShared);
     const cudaError_t e = cudaFuncSetAttribute(glu_backward_kernel<ACT, KEPT>, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES);
     if (e != cudaSuccess) return e;
-    const int64_t tiles = static_cast<int64_t>(p.order.m_tiles) * p.order.n_tiles;
+    const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
     return launch_overlapped_smem(glu_backward_kernel<ACT, KEPT>, dim3(static_cast<unsigned>(tiles < sms ? tiles : sms)), dim3(GB_THREADS), BYTES, stream, p);
 }
 
@@ -395,8 +401,8 @@ dg_status dg_glu_backward(const void* dH, const void* Z, const uint8_t* kept, co
     p.hsft = hsft;
     p.m = M;
     p.inner = I;
-    p.order.m_tiles = cdiv(M, TILE);
-    p.order.n_tiles = I / TILE;
+    p.m_tiles = cdiv(M, TILE);
+    p.n_tiles = I / TILE;
     const cudaError_t e = kept ? launch_backward<true>(p, act, dev.sms, stream) : launch_backward<false>(p, act, dev.sms, stream);
     return e == cudaSuccess ? DG_OK : DG_CUDA_ERROR;
 }
@@ -411,8 +417,8 @@ dg_status dg_transpose_fp8(const uint8_t* q, const float* sf, uint8_t* qt, float
     DeviceInfo dev;
     const dg_status st = device_info(&dev);
     if (st != DG_OK) return st;
-    const TransposeParams p = {q, sf, qt, sft, M, N, {cdiv(M, TILE), N / TILE}};
-    const int64_t tiles = static_cast<int64_t>(p.order.m_tiles) * p.order.n_tiles;
+    const TransposeParams p = {q, sf, qt, sft, M, N, cdiv(M, TILE), N / TILE};
+    const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
     const cudaError_t e = launch_overlapped(transpose_kernel, dim3(static_cast<unsigned>(tiles < 2 * dev.sms ? tiles : 2 * dev.sms)), dim3(TR_THREADS), stream, p);
     return e == cudaSuccess ? DG_OK : DG_CUDA_ERROR;
 }
