@@ -141,6 +141,8 @@ __device__ __forceinline__ void bf16_values(uint2 w, float2 (&a)[2]) {
     a[1] = make_float2(bf16_lo(w.y), bf16_hi(w.y));
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 struct GluBackwardParams {
     const __nv_bfloat16* dh;
     const __nv_bfloat16* z;
@@ -159,7 +161,7 @@ struct GluBackwardParams {
 constexpr int GB_ROWS = 4;                        // rows of a warp
 constexpr int GB_THREADS = 32 * TILE / GB_ROWS;
 struct GluBackwardShared {
-    TileColumns<GB_ROWS> dg, du, h;
+    TileColumns<GB_ROWS, false> dg, du, h;
 };
 
 template <int ACT, bool KEPT>
@@ -216,6 +218,22 @@ __global__ void __launch_bounds__(GB_THREADS, 1) glu_backward_kernel(const GluBa
                 }
             }
         }
+        // ---- the next tile's rows, into L2
+        TileWalk ahead = walk;
+        ahead.next();
+        if (ahead.more() && threadIdx.x < TILE * (KEPT ? 4 : 6)) {
+            const int row = ahead.m * TILE + static_cast<int>(threadIdx.x) % TILE, which = static_cast<int>(threadIdx.x) / TILE;
+            if (row < p.m) {
+                const size_t at = row * (2 * inner) + ahead.n * TILE;
+                if (which < 2) {
+                    if (p.dh != nullptr) prefetch_l2(p.dh + row * inner + ahead.n * TILE + which * 64);
+                } else if (KEPT) {
+                    prefetch_l2(p.kept + at + (which - 2) * inner);
+                } else {
+                    prefetch_l2(p.z + at + (which >> 1 == 2 ? inner : 0) + (which & 1) * 64);
+                }
+            }
+        }
         if (p.qt != nullptr) {
             s.dg.maxima(dg, warp, lane);
             s.du.maxima(du, warp, lane);
@@ -224,8 +242,7 @@ __global__ void __launch_bounds__(GB_THREADS, 1) glu_backward_kernel(const GluBa
         if (p.q != nullptr) {
             uint8_t* q = p.q + static_cast<size_t>(r0) * (2 * inner) + c0;
             float* sf = p.sf + static_cast<size_t>(r0) * (2 * blocks) + tn;
-            tile_rows(dg, q, 2 * inner, sf, 2 * blocks, valid, lane);
-            tile_rows(du, q + inner, 2 * inner, sf + blocks, 2 * blocks, valid, lane);
+            tile_rows2(dg, du, q, q + inner, 2 * inner, sf, sf + blocks, 2 * blocks, valid, lane);
         }
         __syncthreads();
         const int part = static_cast<int>(threadIdx.x) / TILE, column = static_cast<int>(threadIdx.x) % TILE;
@@ -264,7 +281,7 @@ constexpr int TR_THREADS = 32 * TILE / TR_ROWS;
 
 // A CTA takes every gridDim.x-th tile; the next one's codes are asked for as soon as this one's are in use.
 __global__ void __launch_bounds__(TR_THREADS, 2) transpose_kernel(const TransposeParams p) {
-    __shared__ TileColumns<TR_ROWS> s;
+    __shared__ TileColumns<TR_ROWS, true> s;
     grid_dependency_wait();
     grid_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;

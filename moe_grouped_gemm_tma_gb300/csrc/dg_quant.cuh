@@ -79,6 +79,15 @@ __device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
     return d;
 }
 
+// Four products to codes, in order from the lowest byte: values times the reciprocal of their scale, which is within an ulp
+// or so of the quotient. For values that have several roundings of their own, which move as many of them across a midpoint.
+__device__ __forceinline__ uint32_t quantise4_by(float2 a, float2 b, float r) {
+    const float2 rr = make_float2(r, r);
+    a = __fmul2_rn(a, rr);
+    b = __fmul2_rn(b, rr);
+    return pack_e4m3x2(a.x, a.y) | (pack_e4m3x2(b.x, b.y) << 16);
+}
+
 // Four values of a block to codes, in order from the lowest byte.
 __device__ __forceinline__ uint32_t quantise4(float2 a, float2 b, const BlockScale& k) {
     const float2 nd = make_float2(-k.d, -k.d), r = make_float2(k.r, k.r);
@@ -271,20 +280,23 @@ __device__ __forceinline__ float2 act_value2(float2 z) {
 
 // An activation and its slope at two FP32 pre-activations, both to a few roundings of 1 (SILU: of themselves). SILU goes by
 // one sigmoid p: z p and p (1 + z e p), with e = exp(-z) right to a few last places wherever z lies: what the exponent's
-// product is rounded by, and what log2(e) has beyond FP32, go in as a factor.
+// product is rounded by, and what log2(e) has beyond FP32, go in as a factor. Beyond 87 p is 0 or 1 to FP32. (Signs are
+// chosen so that no negation is an instruction.)
 template <int ACT>
 __device__ __forceinline__ void act_both2(float2 z, float2& value, float2& slope) {
     if (ACT == DG_ACT_SILU) {
         constexpr float LN2 = 0.6931471805599453f;
-        const float2 minus = make_float2(-1.f, -1.f), l = make_float2(-LOG2_E, -LOG2_E);
-        const float2 c = make_float2(at_most(at_least(z.x, -100.f), 100.f), at_most(at_least(z.y, -100.f), 100.f));
-        const float2 t = __fmul2_rn(c, l);
-        float2 e = make_float2(exp2_approx(fminf(t.x, 110.f)), exp2_approx(fminf(t.y, 110.f)));
-        const float2 low = __ffma2_rn(c, make_float2(-LOG2_E_REST, -LOG2_E_REST), __ffma2_rn(c, l, __fmul2_rn(t, minus)));
-        e = __ffma2_rn(e, __fmul2_rn(low, make_float2(LN2, LN2)), e);
+        const float2 one = make_float2(1.f, 1.f), minus = make_float2(-1.f, -1.f);
+        const float2 m = make_float2(at_most(-z.x, 87.f), at_most(-z.y, 87.f));      // -z, and held above as well
+        const float2 c = make_float2(at_least(m.x, -87.f), at_least(m.y, -87.f));
+        const float2 t = __fmul2_rn(c, make_float2(LOG2_E, LOG2_E));
+        float2 e = make_float2(exp2_approx(t.x), exp2_approx(t.y));
+        float2 low = __fmul2_rn(__ffma2_rn(c, make_float2(-LOG2_E, -LOG2_E), t), make_float2(-LN2, -LN2));
+        low = __ffma2_rn(c, make_float2(LOG2_E_REST * LN2, LOG2_E_REST * LN2), low);
+        e = __ffma2_rn(e, low, e);
         const float2 p = minus_one_over_one_plus2(e);                    // (negative)
-        value = __fmul2_rn(__fmul2_rn(make_float2(at_least(z.x, -100.f), at_least(z.y, -100.f)), minus), p);
-        slope = __fmul2_rn(p, __ffma2_rn(__fmul2_rn(c, e), p, minus));
+        value = __fmul2_rn(m, p);
+        slope = __fmul2_rn(__fmul2_rn(p, minus), __ffma2_rn(__fmul2_rn(c, e), p, one));
         return;
     }
     value = act_value2<ACT>(z);

@@ -19,32 +19,37 @@ __device__ __forceinline__ float warp_abs_max(float v) {
     return d;
 }
 
-// Codes along the rows: q points at the lane's first value, rows `pitch` apart, sf at the warp's first row's scale, `scales`
-// apart; `valid` of the R rows exist. Lane l makes the scale of row l / (32 / R) and hands round what it divides by.
+// Codes along the rows of two tiles' values at once: q points at the lane's first value of each, rows `pitch` apart, sf at the
+// warp's first row's scale, `scales` apart; `valid` of the R rows exist. Lane l makes the scale of row l / (16 / R) of the first
+// tile, or, from lane 16 on, of the second, and hands round its reciprocal.
 template <int R>
-__device__ __forceinline__ void tile_rows(const float2 (&v)[R][2], uint8_t* q, size_t pitch, float* sf, size_t scales, int valid, int lane) {
-    constexpr int SHARE = 32 / R;
+__device__ __forceinline__ void tile_rows2(const float2 (&v)[R][2], const float2 (&u)[R][2], uint8_t* qv, uint8_t* qu, size_t pitch, float* sfv, float* sfu,
+                                           size_t scales, int valid, int lane) {
+    constexpr int SHARE = 16 / R;
     float most = 0.f;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
         const float a = warp_abs_max(abs_max(abs_max(v[i][0].x, v[i][0].y, v[i][1].x), v[i][1].y));
-        most = lane / SHARE == i ? a : most;
+        const float b = warp_abs_max(abs_max(abs_max(u[i][0].x, u[i][0].y, u[i][1].x), u[i][1].y));
+        most = lane / SHARE == i ? a : (lane / SHARE == R + i ? b : most);
     }
     const BlockScale mine = block_scale(abs_bits(most));
-    if (lane % SHARE == 0 && lane / SHARE < valid) sf[static_cast<size_t>(lane / SHARE) * scales] = mine.s;
+    const int row = lane / SHARE & (R - 1);
+    if (lane % SHARE == 0 && row < valid) (lane < 16 ? sfv : sfu)[row * scales] = mine.s;
 #pragma unroll
-    for (int i = 0; i < R; ++i, q += pitch) {
-        BlockScale k;
-        k.d = __shfl_sync(0xffffffffu, mine.d, i * SHARE);
-        k.r = __shfl_sync(0xffffffffu, mine.r, i * SHARE);
-        const uint32_t w = quantise4(v[i][0], v[i][1], k);
-        if (i < valid) *reinterpret_cast<uint32_t*>(q) = w;
+    for (int i = 0; i < R; ++i, qv += pitch, qu += pitch) {
+        const float rv = __shfl_sync(0xffffffffu, mine.r, i * SHARE), ru = __shfl_sync(0xffffffffu, mine.r, 16 + i * SHARE);
+        const uint32_t a = quantise4_by(v[i][0], v[i][1], rv), b = quantise4_by(u[i][0], u[i][1], ru);
+        if (i < valid) {
+            *reinterpret_cast<uint32_t*>(qv) = a;
+            *reinterpret_cast<uint32_t*>(qu) = b;
+        }
     }
 }
 
 // Codes along the columns, in three steps with a barrier of the CTA behind each: every warp's maxima, the columns' scales,
-// the codes, which then leave as the rows of the transpose.
-template <int R>
+// the codes, which then leave as the rows of the transpose. EXACT: by the rounded quotient, else by the reciprocal.
+template <int R, bool EXACT>
 struct TileColumns {
     static constexpr int WARPS = TILE / R;
     __align__(16) float amax[WARPS][TILE];
@@ -91,7 +96,7 @@ struct TileColumns {
             for (int i = 0; i < R; i += 4) {
                 float2 w[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) w[j] = quotient2(v[i + j][x], nd, rr);
+                for (int j = 0; j < 4; ++j) w[j] = EXACT ? quotient2(v[i + j][x], nd, rr) : __fmul2_rn(v[i + j][x], rr);
                 lo[i / 4] = pack_e4m3x2(w[0].x, w[1].x) | (pack_e4m3x2(w[2].x, w[3].x) << 16);
                 hi[i / 4] = pack_e4m3x2(w[0].y, w[1].y) | (pack_e4m3x2(w[2].y, w[3].y) << 16);
             }
