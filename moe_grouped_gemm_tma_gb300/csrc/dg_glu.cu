@@ -181,19 +181,26 @@ __global__ void __launch_bounds__(GB_THREADS, 1) glu_backward_kernel(const GluBa
             float scale = 0.f;                    // lanes 0 .. 3: of the rows' g, 4 .. 7: of u
             if (KEPT && lane < 2 * GB_ROWS && lane % GB_ROWS < valid)
                 scale = ld_input(p.kept_sf + (static_cast<size_t>(r0) + lane % GB_ROWS) * (2 * blocks) + (lane / GB_ROWS) * blocks + tn);
+            const size_t first = static_cast<size_t>(r0) * inner, at = 2 * first + c0;
+            const auto load = [&](int i) {
+                d[i] = make_uint2(0, 0);
+                if (p.dh != nullptr) d[i] = ld_input(reinterpret_cast<const uint2*>(p.dh + first + c0 + i * inner));
+                if (KEPT) {
+                    g[i] = make_uint2(ld_input(reinterpret_cast<const uint32_t*>(p.kept + at + 2 * i * inner)), 0);
+                    u[i] = make_uint2(ld_input(reinterpret_cast<const uint32_t*>(p.kept + at + (2 * i + 1) * inner)), 0);
+                } else {
+                    g[i] = ld_input(reinterpret_cast<const uint2*>(p.z + at + 2 * i * inner));
+                    u[i] = ld_input(reinterpret_cast<const uint2*>(p.z + at + (2 * i + 1) * inner));
+                }
+            };
+            if (valid >= GB_ROWS) {
 #pragma unroll
-            for (int i = 0; i < GB_ROWS; ++i) {
-                d[i] = g[i] = u[i] = make_uint2(0, 0);
-                if (i < valid) {
-                    const size_t row = static_cast<size_t>(r0) + i, at = row * (2 * inner) + c0;
-                    if (p.dh != nullptr) d[i] = ld_input(reinterpret_cast<const uint2*>(p.dh + row * inner + c0));
-                    if (KEPT) {
-                        g[i].x = ld_input(reinterpret_cast<const uint32_t*>(p.kept + at));
-                        u[i].x = ld_input(reinterpret_cast<const uint32_t*>(p.kept + at + inner));
-                    } else {
-                        g[i] = ld_input(reinterpret_cast<const uint2*>(p.z + at));
-                        u[i] = ld_input(reinterpret_cast<const uint2*>(p.z + at + inner));
-                    }
+                for (int i = 0; i < GB_ROWS; ++i) load(i);
+            } else {
+#pragma unroll
+                for (int i = 0; i < GB_ROWS; ++i) {
+                    d[i] = g[i] = u[i] = make_uint2(0, 0);
+                    if (i < valid) load(i);
                 }
             }
             // (rows past M are 0: so are the activations there, and their slopes are finite)

@@ -296,7 +296,36 @@ __device__ __forceinline__ void act_both2(float2 z, float2& value, float2& slope
         e = __ffma2_rn(e, low, e);
         const float2 p = minus_one_over_one_plus2(e);                    // (negative)
         value = __fmul2_rn(m, p);
-        slope = __fmul2_rn(__fmul2_rn(p, minus), __ffma2_rn(__fmul2_rn(c, e), p, one));
+        slope = __fmul2_rn(__fmul2_rn(p, minus), __ffma2_rn(__fmul2_rn(e, p), c, one));       // (e p is within 1)
+        return;
+    }
+    if (ACT == DG_ACT_GELU_TANH) {
+        // (as act_slope2, whose sigmoid gives the value too)
+        constexpr float LN2 = 0.6931471805599453f, A2 = 2.f * GELU_A, A2B = 2.f * GELU_A * GELU_B;
+        const float2 one = make_float2(1.f, 1.f), minus = make_float2(-1.f, -1.f);
+        const float2 m = make_float2(at_most(-z.x, 16.f), at_most(-z.y, 16.f));      // -z, and held above as well
+        const float2 c = make_float2(at_least(m.x, -16.f), at_least(m.y, -16.f));
+        const float2 c2 = __fmul2_rn(c, c);
+        const float2 y = __fmul2_rn(c, __ffma2_rn(c2, make_float2(A2B, A2B), make_float2(A2, A2)));     // -y
+        const float2 dy = __ffma2_rn(c2, make_float2(3.f * A2B, 3.f * A2B), make_float2(A2, A2));
+        float2 t = __fmul2_rn(y, make_float2(LOG2_E, LOG2_E));
+        float2 low = __fmul2_rn(__ffma2_rn(y, make_float2(-LOG2_E, -LOG2_E), t), make_float2(-LN2, -LN2));
+        low = __ffma2_rn(y, make_float2(LOG2_E_REST * LN2, LOG2_E_REST * LN2), low);
+        float2 e = make_float2(exp2_approx(fminf(t.x, 126.f)), exp2_approx(fminf(t.y, 126.f)));
+        e = __ffma2_rn(e, low, e);
+        const float2 p = minus_one_over_one_plus2(e);                    // (negative)
+        value = __fmul2_rn(m, p);
+        slope = __fmul2_rn(__fmul2_rn(p, minus), __ffma2_rn(__fmul2_rn(__fmul2_rn(e, p), c), dy, one));
+        return;
+    }
+    if (ACT == DG_ACT_GELU) {
+        const float2 m = make_float2(fminf(fabsf(z.x), GELU_END), fminf(fabsf(z.y), GELU_END));
+        const float2 x = __fmul2_rn(__fmul2_rn(m, m), make_float2(-0.5f * LOG2_E, -0.5f * LOG2_E));
+        const float2 e = make_float2(exp2_approx(x.x), exp2_approx(x.y)), tail = upper_tail_slope2(m);
+        const float2 f = __fmul2_rn(e, tail);
+        const float2 g = __fmul2_rn(e, __ffma2_rn(m, make_float2(-0.3989422804014327f, -0.3989422804014327f), tail));
+        value = __fmul2_rn(make_float2(at_least(z.x, -GELU_END), at_least(z.y, -GELU_END)), make_float2(slope_of(z.x, f.x), slope_of(z.y, f.y)));
+        slope = make_float2(slope_of(z.x, g.x), slope_of(z.y, g.y));
         return;
     }
     value = act_value2<ACT>(z);

@@ -26,13 +26,19 @@ template <int R>
 __device__ __forceinline__ void tile_rows2(const float2 (&v)[R][2], const float2 (&u)[R][2], uint8_t* qv, uint8_t* qu, size_t pitch, float* sfv, float* sfu,
                                            size_t scales, int valid, int lane) {
     constexpr int SHARE = 16 / R;
-    float most = 0.f;
+    float a[2 * R];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-        const float a = warp_abs_max(abs_max(abs_max(v[i][0].x, v[i][0].y, v[i][1].x), v[i][1].y));
-        const float b = warp_abs_max(abs_max(abs_max(u[i][0].x, u[i][0].y, u[i][1].x), u[i][1].y));
-        most = lane / SHARE == i ? a : (lane / SHARE == R + i ? b : most);
+        a[i] = warp_abs_max(abs_max(abs_max(v[i][0].x, v[i][0].y, v[i][1].x), v[i][1].y));
+        a[R + i] = warp_abs_max(abs_max(abs_max(u[i][0].x, u[i][0].y, u[i][1].x), u[i][1].y));
     }
+#pragma unroll
+    for (int half = R; half >= 1; half /= 2) {        // a[lane / SHARE], by the bits of the lane
+        const bool up = (lane & half * SHARE) != 0;
+#pragma unroll
+        for (int i = 0; i < half; ++i) a[i] = up ? a[half + i] : a[i];
+    }
+    const float most = a[0];
     const BlockScale mine = block_scale(abs_bits(most));
     const int row = lane / SHARE & (R - 1);
     if (lane % SHARE == 0 && row < valid) (lane < 16 ? sfv : sfu)[row * scales] = mine.s;

@@ -190,6 +190,29 @@ def test_backward_over_the_whole_range():
         check_backward(dH, Z[:, :128].double(), Z[:, 128:].double(), act, out, 0.0)
 
 
+@pytest.mark.parametrize("act", ACTS)
+def test_very_large_gates(act):
+    # beyond where any exponential of them is finite: the activation is the gate or nothing, its slope 1 or 0
+    big = torch.tensor([60.0, 86.0, 87.0, 88.0, 90.0, 100.0, 126.0, 150.0, 1000.0, 65536.0, 2.0 ** 60, 2.0 ** 100, 2.0 ** 126], device=DEV)
+    g = torch.cat((big, -big)).repeat(5)[:128].bfloat16()
+    Z = torch.ones(3, 256, dtype=torch.bfloat16, device=DEV)
+    Z[1, :128] = g.abs().neg()
+    Z[0, :128], Z[2, :128] = g.abs(), 0.5
+    Z[:, 128:] = 2.0 ** -30
+    out = alloc(3, 128, True)
+    dg.dg_glu(Z, *out, act=act)
+    back = run_backward(torch.ones(3, 128, dtype=torch.bfloat16, device=DEV), Z=Z, act=act)
+    gd, u = Z.double().split(128, 1)
+    value = torch.where(gd > 1, gd, B.act(gd.clamp(-80, 1), act) if act != "none" else gd)
+    slope = torch.where(gd > 1, 1.0, B.slope(gd.clamp(-80, 1), act) if act != "none" else 1.0)
+    err = lambda v: v.abs() * 2.0 ** -17 + 1e-17  # noqa: E731
+    B.check_codes(out[0], out[1], value * u, err(value * u), what="h")
+    dz = torch.cat((u * slope, value), 1)
+    B.check_codes(*back["q"], dz, err(dz), what="rows")
+    B.check_codes(*back["qt"], B.columns(dz), B.columns(err(dz)), what="columns")
+    B.check_codes(*back["ht"], B.columns(value * u), B.columns(err(value * u)), what="h")
+
+
 def test_backward_nan_stays_in_its_blocks():
     M, I = 256, 256
     Z, dH = make_z(M, I), torch.randn(M, I, device=DEV, generator=gen(1)).bfloat16()
