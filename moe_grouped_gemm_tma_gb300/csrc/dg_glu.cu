@@ -141,13 +141,12 @@ __device__ __forceinline__ void bf16_values(uint2 w, float2 (&a)[2]) {
     a[1] = make_float2(bf16_lo(w.y), bf16_hi(w.y));
 }
 
-__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
-
 struct GluBackwardParams {
     const __nv_bfloat16* dh;
     const __nv_bfloat16* z;
     const uint8_t* kept;
     const float* kept_sf;
+    const void* any;      // an address to name where nothing is read
     uint8_t* q;
     float* sf;
     uint8_t* qt;
@@ -160,85 +159,81 @@ struct GluBackwardParams {
 
 constexpr int GB_ROWS = 4;                        // rows of a warp
 constexpr int GB_THREADS = 32 * TILE / GB_ROWS;
+template <bool KEPT>
 struct GluBackwardShared {
     TileColumns<GB_ROWS, false> dg, du, h;
+    __align__(16) uint2 dh[TILE][32];             // the tile's inputs, as they are in global memory
+    __align__(16) uint32_t g[TILE][KEPT ? 32 : 64], u[TILE][KEPT ? 32 : 64];
+    __align__(16) float scale[2][TILE];           // of g's and u's codes
 };
 
+// A CTA makes all three outputs of a tile, so that what they share is computed once: 48 values a thread, which is what the
+// registers hold with one CTA an SM. Its barriers are hidden by nothing else, therefore: the next tile's inputs come while
+// this one's are in use, and the rows' codes are made while some warps make the columns' scales.
 template <int ACT, bool KEPT>
 __global__ void __launch_bounds__(GB_THREADS, 1) glu_backward_kernel(const GluBackwardParams p) {
     extern __shared__ __align__(16) uint8_t s_raw[];
-    GluBackwardShared& s = *reinterpret_cast<GluBackwardShared*>(s_raw);
+    GluBackwardShared<KEPT>& s = *reinterpret_cast<GluBackwardShared<KEPT>*>(s_raw);
     grid_dependency_wait();
     grid_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const size_t inner = p.inner, blocks = inner / 128, pitch = static_cast<size_t>(p.m_tiles) * TILE;
-    for (TileWalk walk(p.m_tiles, p.n_tiles); walk.more(); walk.next()) {
+    // (rows past M are zeros: so are the activations there, and their slopes are finite)
+    const auto fetch = [&](const TileWalk& at) {
+        const int t = threadIdx.x, m0 = at.m * TILE, n0 = at.n * TILE;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = i * 64 + t / 16;
+            const size_t row = m0 + r;
+            const bool there = m0 + r < p.m;
+            cp_async_16_or_zero(&s.dh[r][t % 16 * 2], there && p.dh != nullptr ? p.dh + row * inner + n0 + t % 16 * 8 : p.any, there && p.dh != nullptr);
+            if (!KEPT) {
+                const __nv_bfloat16* src = there ? p.z + row * (2 * inner) + n0 + t % 16 * 8 : static_cast<const __nv_bfloat16*>(p.any);
+                cp_async_16_or_zero(&s.g[r][t % 16 * 4], src, there);
+                cp_async_16_or_zero(&s.u[r][t % 16 * 4], there ? src + inner : src, there);
+            }
+        }
+        if (KEPT) {
+            const int r = t / 8;
+            const size_t row = m0 + r;
+            const bool there = m0 + r < p.m;
+            const uint8_t* src = there ? p.kept + row * (2 * inner) + n0 + t % 8 * 16 : static_cast<const uint8_t*>(p.any);
+            cp_async_16_or_zero(&s.g[r][t % 8 * 4], src, there);
+            cp_async_16_or_zero(&s.u[r][t % 8 * 4], there ? src + inner : src, there);
+            if (t < 2 * TILE) {
+                const int which = t / TILE, rs = t % TILE;
+                if (m0 + rs < p.m) cp_async_4(&s.scale[which][rs], p.kept_sf + static_cast<size_t>(m0 + rs) * (2 * blocks) + which * blocks + at.n);
+                else s.scale[which][rs] = 0.f;
+            }
+        }
+    };
+    TileWalk walk(p.m_tiles, p.n_tiles);
+    if (walk.more()) fetch(walk);
+    cp_async_wait_all();
+    __syncthreads();
+    for (bool more = walk.more(); more;) {
         const int tm = walk.m, tn = walk.n;
         const int r0 = tm * TILE + warp * GB_ROWS, c0 = tn * TILE + lane * 4, valid = p.m - r0;
         float2 dg[GB_ROWS][2], du[GB_ROWS][2], h[GB_ROWS][2];
-        {
-            uint2 d[GB_ROWS], g[GB_ROWS], u[GB_ROWS];
-            float scale = 0.f;                    // lanes 0 .. 3: of the rows' g, 4 .. 7: of u
-            if (KEPT && lane < 2 * GB_ROWS && lane % GB_ROWS < valid)
-                scale = ld_input(p.kept_sf + (static_cast<size_t>(r0) + lane % GB_ROWS) * (2 * blocks) + (lane / GB_ROWS) * blocks + tn);
-            const size_t first = static_cast<size_t>(r0) * inner, at = 2 * first + c0;
-            const auto load = [&](int i) {
-                d[i] = make_uint2(0, 0);
-                if (p.dh != nullptr) d[i] = ld_input(reinterpret_cast<const uint2*>(p.dh + first + c0 + i * inner));
-                if (KEPT) {
-                    g[i] = make_uint2(ld_input(reinterpret_cast<const uint32_t*>(p.kept + at + 2 * i * inner)), 0);
-                    u[i] = make_uint2(ld_input(reinterpret_cast<const uint32_t*>(p.kept + at + (2 * i + 1) * inner)), 0);
-                } else {
-                    g[i] = ld_input(reinterpret_cast<const uint2*>(p.z + at + 2 * i * inner));
-                    u[i] = ld_input(reinterpret_cast<const uint2*>(p.z + at + (2 * i + 1) * inner));
-                }
-            };
-            if (valid >= GB_ROWS) {
 #pragma unroll
-                for (int i = 0; i < GB_ROWS; ++i) load(i);
+        for (int i = 0; i < GB_ROWS; ++i) {
+            const int r = warp * GB_ROWS + i;
+            float2 dv[2], gv[2], uv[2];
+            bf16_values(s.dh[r][lane], dv);
+            if (KEPT) {
+                code_values(s.g[r][lane], s.scale[0][r], gv);
+                code_values(s.u[r][lane], s.scale[1][r], uv);
             } else {
-#pragma unroll
-                for (int i = 0; i < GB_ROWS; ++i) {
-                    d[i] = g[i] = u[i] = make_uint2(0, 0);
-                    if (i < valid) load(i);
-                }
+                bf16_values(*reinterpret_cast<const uint2*>(&s.g[r][lane * 2]), gv);
+                bf16_values(*reinterpret_cast<const uint2*>(&s.u[r][lane * 2]), uv);
             }
-            // (rows past M are 0: so are the activations there, and their slopes are finite)
 #pragma unroll
-            for (int i = 0; i < GB_ROWS; ++i) {
-                float2 dv[2], gv[2], uv[2];
-                bf16_values(d[i], dv);
-                if (KEPT) {
-                    code_values(g[i].x, __shfl_sync(FULL, scale, i), gv);
-                    code_values(u[i].x, __shfl_sync(FULL, scale, GB_ROWS + i), uv);
-                } else {
-                    bf16_values(g[i], gv);
-                    bf16_values(u[i], uv);
-                }
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    float2 a, slope;
-                    act_both2<ACT>(gv[c], a, slope);
-                    dg[i][c] = __fmul2_rn(__fmul2_rn(dv[c], uv[c]), slope);
-                    du[i][c] = __fmul2_rn(dv[c], a);
-                    h[i][c] = __fmul2_rn(a, uv[c]);
-                }
-            }
-        }
-        // ---- the next tile's rows, into L2
-        TileWalk ahead = walk;
-        ahead.next();
-        if (ahead.more() && threadIdx.x < TILE * (KEPT ? 4 : 6)) {
-            const int row = ahead.m * TILE + static_cast<int>(threadIdx.x) % TILE, which = static_cast<int>(threadIdx.x) / TILE;
-            if (row < p.m) {
-                const size_t at = row * (2 * inner) + ahead.n * TILE;
-                if (which < 2) {
-                    if (p.dh != nullptr) prefetch_l2(p.dh + row * inner + ahead.n * TILE + which * 64);
-                } else if (KEPT) {
-                    prefetch_l2(p.kept + at + (which - 2) * inner);
-                } else {
-                    prefetch_l2(p.z + at + (which >> 1 == 2 ? inner : 0) + (which & 1) * 64);
-                }
+            for (int c = 0; c < 2; ++c) {
+                float2 a, slope;
+                act_both2<ACT>(gv[c], a, slope);
+                dg[i][c] = __fmul2_rn(__fmul2_rn(dv[c], uv[c]), slope);
+                du[i][c] = __fmul2_rn(dv[c], a);
+                h[i][c] = __fmul2_rn(a, uv[c]);
             }
         }
         if (p.qt != nullptr) {
@@ -246,24 +241,28 @@ __global__ void __launch_bounds__(GB_THREADS, 1) glu_backward_kernel(const GluBa
             s.du.maxima(du, warp, lane);
         }
         if (p.ht != nullptr) s.h.maxima(h, warp, lane);
-        if (p.q != nullptr) {
-            uint8_t* q = p.q + static_cast<size_t>(r0) * (2 * inner) + c0;
-            float* sf = p.sf + static_cast<size_t>(r0) * (2 * blocks) + tn;
-            tile_rows2(dg, du, q, q + inner, 2 * inner, sf, sf + blocks, 2 * blocks, valid, lane);
-        }
         __syncthreads();
+        walk.next();
+        more = walk.more();
+        if (more) fetch(walk);
         const int part = static_cast<int>(threadIdx.x) / TILE, column = static_cast<int>(threadIdx.x) % TILE;
         if (p.qt != nullptr) {
             if (part == 0) s.dg.scale(column, p.sft + (static_cast<size_t>(tn) * TILE + column) * p.m_tiles + tm);
             else if (part == 1) s.du.scale(column, p.sft + (inner + static_cast<size_t>(tn) * TILE + column) * p.m_tiles + tm);
         }
         if (p.ht != nullptr && part == 2) s.h.scale(column, p.hsft + (static_cast<size_t>(tn) * TILE + column) * p.m_tiles + tm);
+        if (p.q != nullptr) {
+            uint8_t* q = p.q + static_cast<size_t>(r0) * (2 * inner) + c0;
+            float* sf = p.sf + static_cast<size_t>(r0) * (2 * blocks) + tn;
+            tile_rows2(dg, du, q, q + inner, 2 * inner, sf, sf + blocks, 2 * blocks, valid, lane);
+        }
         __syncthreads();
         if (p.qt != nullptr) {
             s.dg.quantise(dg, warp, lane);
             s.du.quantise(du, warp, lane);
         }
         if (p.ht != nullptr) s.h.quantise(h, warp, lane);
+        cp_async_wait_all();
         __syncthreads();
         const size_t first = static_cast<size_t>(tn) * TILE * pitch + static_cast<size_t>(tm) * TILE;
         if (p.qt != nullptr) {
@@ -333,7 +332,7 @@ __global__ void __launch_bounds__(TR_THREADS, 2) transpose_kernel(const Transpos
 
 template <int ACT, bool KEPT>
 cudaError_t launch_backward_as(const GluBackwardParams& p, int sms, cudaStream_t stream) {
-    constexpr int BYTES = sizeof(GluBackwardShared);
+    constexpr int BYTES = sizeof(GluBackwardShared<KEPT>);
     const cudaError_t e = cudaFuncSetAttribute(glu_backward_kernel<ACT, KEPT>, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES);
     if (e != cudaSuccess) return e;
     const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
@@ -417,6 +416,7 @@ dg_status dg_glu_backward(const void* dH, const void* Z, const uint8_t* kept, co
     p.z = static_cast<const __nv_bfloat16*>(Z);
     p.kept = kept;
     p.kept_sf = kept_sf;
+    p.any = kept ? static_cast<const void*>(kept) : Z;
     p.q = q;
     p.sf = sf;
     p.qt = qt;
