@@ -360,9 +360,14 @@ __device__ __forceinline__ uint4 pack_bf16(const float2 (&a)[4]) {
     return make_uint4(pack_bf16(a[0].x, a[0].y), pack_bf16(a[1].x, a[1].y), pack_bf16(a[2].x, a[2].y), pack_bf16(a[3].x, a[3].y));
 }
 
-// A warp a piece of 512 bytes of a token's row, four experts' rows in flight at a time. FP32 sums, in the slots' order
-// from zero on, the residual last.
-__global__ void __launch_bounds__(32 * MOVE_WARPS, 6) combine_kernel(const CombineParams p) {
+// A warp a piece of 1024 bytes of a token's row, two experts' rows in flight at a time. FP32 sums, in the slots' order from
+// zero on, the residual last. What bounds it is memory: 4099 tokens of 7168, a quarter of 8 slots each, 39.1 us (6.0 TB/s), all
+// slots 86.8 us (6.8). Pieces of 512 bytes with 2 or 4 rows take 42.2 and 50.3 us, 1024 with 4 rows 42.3, 2048 with 2 42.7: the
+// registers of more loads cost more warps than the loads bring.
+constexpr int COMBINE_VECTORS = 2, COMBINE_ROWS = 2;
+
+__global__ void __launch_bounds__(32 * MOVE_WARPS) combine_kernel(const CombineParams p) {
+    constexpr int VECTORS = COMBINE_VECTORS, BATCH = COMBINE_ROWS;
     grid_dependency_wait();
     grid_launch_dependents();
     const int lane = threadIdx.x & 31;
@@ -371,35 +376,45 @@ __global__ void __launch_bounds__(32 * MOVE_WARPS, 6) combine_kernel(const Combi
     const unsigned t = item / p.pieces, piece = item - t * p.pieces;
     const size_t slot = static_cast<size_t>(t) * p.k + lane;
     const int mine = lane < p.k ? slot_row(p.rows, slot, p.Mt) : -1;
-    const float weight = mine >= 0 && p.weights != nullptr ? ld_input(p.weights + slot) : 1.f;
+    const float weight = lane < p.k && p.weights != nullptr ? ld_input(p.weights + slot) : 1.f;
     unsigned open = __ballot_sync(FULL, mine >= 0);
-    const int v = static_cast<int>(piece) * 32 + lane;
-    const bool inside = v < p.vectors;
+    const int v = static_cast<int>(piece) * 32 * VECTORS + lane;
     const size_t at = static_cast<size_t>(t) * p.vectors + v;
-    uint4 res = make_uint4(0, 0, 0, 0);
-    if (inside && p.residual != nullptr) res = ld_input(p.residual + at);
-    float2 a[4];
+    uint4 res[VECTORS];
+    float2 a[VECTORS][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) a[i] = make_float2(0.f, 0.f);
+    for (int u = 0; u < VECTORS; ++u) {
+        res[u] = make_uint4(0, 0, 0, 0);
+        if (p.residual != nullptr && v + 32 * u < p.vectors) res[u] = ld_input(p.residual + at + 32 * u);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[u][i] = make_float2(0.f, 0.f);
+    }
     for (; open != 0;) {
-        uint4 y[4];
-        float w[4];
+        uint4 y[BATCH][VECTORS];
+        float w[BATCH];
         const int n = __popc(open);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < BATCH; ++i) {
             const int j = i < n ? __ffs(open) - 1 : 0;
             open &= open - 1;
             const int row = __shfl_sync(FULL, mine, j);
             w[i] = __shfl_sync(FULL, weight, j);
-            if (i < n && inside) y[i] = ld_input(p.y + static_cast<size_t>(row) * p.vectors + v);
+#pragma unroll
+            for (int u = 0; u < VECTORS; ++u)
+                if (i < n && v + 32 * u < p.vectors) y[i][u] = ld_input(p.y + static_cast<size_t>(row) * p.vectors + v + 32 * u);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i < n && inside) add_scaled(a, y[i], w[i]);
+        for (int i = 0; i < BATCH; ++i)
+#pragma unroll
+            for (int u = 0; u < VECTORS; ++u)
+                if (i < n && v + 32 * u < p.vectors) add_scaled(a[u], y[i][u], w[i]);
     }
-    if (!inside) return;
-    if (p.residual != nullptr) add_scaled(a, res, 1.f);
-    p.out[at] = pack_bf16(a);
+#pragma unroll
+    for (int u = 0; u < VECTORS; ++u) {
+        if (v + 32 * u >= p.vectors) break;
+        if (p.residual != nullptr) add_scaled(a[u], res[u], 1.f);
+        p.out[at + 32 * u] = pack_bf16(a[u]);
+    }
 }
 
 // ------------------------------------------------------------------------------------ its gradient
@@ -415,29 +430,31 @@ struct CombineBackwardParams {
     unsigned token_ctas, pads;
 };
 
-constexpr int CB_WARPS = 4;
+constexpr int CB_NARROW = 4;                      // tokens of a CTA, a warp each
+constexpr int CB_WARPS = 8;                       // warps of a token at most
 constexpr int CB_VECTORS = 4;                     // a lane's vectors at a time
 
-// WIDE: a CTA a token, else a warp a token. A lane keeps its piece of dout while it goes through the token's experts; the
-// products with their rows are added up over the lanes, and over the warps in order.
+// WIDE: a CTA a token; else a warp a token. A lane keeps its piece of dout while it goes through the token's experts; the
+// products with their rows are added up over the lanes, and over the warps in order. What bounds it is memory, half of it
+// written: 4096 tokens of 8 x 7168 take 172.6 us, 6.1 TB/s.
 template <bool WIDE>
-__global__ void __launch_bounds__(32 * CB_WARPS) combine_backward_kernel(const CombineBackwardParams p) {
+__global__ void __launch_bounds__(32 * (WIDE ? CB_WARPS : CB_NARROW)) combine_backward_kernel(const CombineBackwardParams p) {
     __shared__ float s_dot[CB_WARPS][32];
     grid_dependency_wait();
     grid_launch_dependents();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x / 32;
     if (blockIdx.x >= p.token_ctas) {
-        const unsigned item = (blockIdx.x - p.token_ctas) * CB_WARPS + warp;
+        const unsigned item = (blockIdx.x - p.token_ctas) * warps + warp;
         if (item < p.pads) zero_pads(item, p.m_indices, p.dy, p.vectors, lane);
         return;
     }
-    const int t = static_cast<int>(WIDE ? blockIdx.x : blockIdx.x * CB_WARPS + warp);
+    const int t = static_cast<int>(WIDE ? blockIdx.x : blockIdx.x * CB_NARROW + warp);
     if (!WIDE && t >= p.T) return;
     const size_t slot = static_cast<size_t>(t) * p.k + lane;
     const int mine = lane < p.k ? slot_row(p.rows, slot, p.Mt) : -1;
-    const float weight = mine >= 0 && p.weights != nullptr ? ld_input(p.weights + slot) : 1.f;
+    const float weight = lane < p.k && p.weights != nullptr ? ld_input(p.weights + slot) : 1.f;
     const unsigned open = __ballot_sync(FULL, mine >= 0);
-    const int first = WIDE ? warp * 32 + lane : lane, step = WIDE ? 32 * CB_WARPS : 32;
+    const int first = WIDE ? warp * 32 + lane : lane, step = WIDE ? static_cast<int>(blockDim.x) : 32;
     float dot = 0.f;                              // of slot `lane`
     for (int v0 = first; v0 - lane < p.vectors; v0 += step * CB_VECTORS) {
         uint4 d[CB_VECTORS];
@@ -449,28 +466,14 @@ __global__ void __launch_bounds__(32 * CB_WARPS) combine_backward_kernel(const C
         for (unsigned left = open; left; left &= left - 1) {
             const int j = __ffs(left) - 1;
             const size_t at = static_cast<size_t>(__shfl_sync(FULL, mine, j)) * p.vectors + v0;
-            const float w = __shfl_sync(FULL, weight, j);
-            if (p.dweights != nullptr) {
-                uint4 y[CB_VECTORS];
+            uint4 y[CB_VECTORS];
 #pragma unroll
-                for (int i = 0; i < CB_VECTORS; ++i) {
-                    y[i] = make_uint4(0, 0, 0, 0);
-                    if (v0 + i * step < p.vectors) y[i] = ld_input(p.y + at + i * step);
-                }
-                float2 a = make_float2(0.f, 0.f);
-#pragma unroll
-                for (int i = 0; i < CB_VECTORS; ++i) {
-                    const uint32_t yw[4] = {y[i].x, y[i].y, y[i].z, y[i].w}, dw[4] = {d[i].x, d[i].y, d[i].z, d[i].w};
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        a = __ffma2_rn(make_float2(bf16_lo(yw[c]), bf16_hi(yw[c])), make_float2(bf16_lo(dw[c]), bf16_hi(dw[c])), a);
-                }
-                float sum = a.x + a.y;
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
-                if (lane == j) dot += sum;
+            for (int i = 0; i < CB_VECTORS; ++i) {
+                y[i] = make_uint4(0, 0, 0, 0);
+                if (p.dweights != nullptr && v0 + i * step < p.vectors) y[i] = ld_input(p.y + at + i * step);
             }
             if (p.dy != nullptr) {
+                const float w = __shfl_sync(FULL, weight, j);
 #pragma unroll
                 for (int i = 0; i < CB_VECTORS; ++i) {
                     if (v0 + i * step < p.vectors) {
@@ -485,6 +488,20 @@ __global__ void __launch_bounds__(32 * CB_WARPS) combine_backward_kernel(const C
                     }
                 }
             }
+            if (p.dweights != nullptr) {
+                float2 a = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < CB_VECTORS; ++i) {
+                    const uint32_t yw[4] = {y[i].x, y[i].y, y[i].z, y[i].w}, dw[4] = {d[i].x, d[i].y, d[i].z, d[i].w};
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        a = __ffma2_rn(make_float2(bf16_lo(yw[c]), bf16_hi(yw[c])), make_float2(bf16_lo(dw[c]), bf16_hi(dw[c])), a);
+                }
+                float sum = a.x + a.y;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
+                if (lane == j) dot += sum;
+            }
         }
     }
     if (p.dweights == nullptr) return;
@@ -496,8 +513,7 @@ __global__ void __launch_bounds__(32 * CB_WARPS) combine_backward_kernel(const C
     __syncthreads();
     if (warp == 0 && lane < p.k) {
         float sum = s_dot[0][lane];
-#pragma unroll
-        for (int w = 1; w < CB_WARPS; ++w) sum += s_dot[w][lane];
+        for (int w = 1; w < warps; ++w) sum += s_dot[w][lane];
         p.dweights[slot] = sum;
     }
 }
@@ -659,7 +675,7 @@ dg_status dg_moe_combine(const void* y, const int32_t* rows, const float* weight
     p.k = k;
     p.vectors = H / 8;
     p.Mt = Mt;
-    p.pieces = cdiv(p.vectors, 32);
+    p.pieces = cdiv(p.vectors, 32 * COMBINE_VECTORS);
     p.items = static_cast<unsigned>(T) * static_cast<unsigned>(p.pieces);
     const cudaError_t e = launch_overlapped(combine_kernel, dim3((p.items + MOVE_WARPS - 1) / MOVE_WARPS), dim3(32 * MOVE_WARPS), stream, p);
     return e == cudaSuccess ? DG_OK : DG_CUDA_ERROR;
@@ -691,12 +707,16 @@ dg_status dg_moe_combine_backward(const void* dout, const void* y, const int32_t
     p.k = k;
     p.vectors = H / 8;
     p.Mt = Mt;
+    // Two warps a token where there are many (4096 tokens of 8 x 7168: 172.6 us, with 1, 4 and 7 warps 178.8, 178.6 and 181.6; of
+    // 8192 tokens of 2 x 7168 113.7, with 4 and 7 122 and 129), as many as have a piece where there are few (16 tokens: 39 us with
+    // two, 29 with four). The order of the sums goes by the sizes alone.
     const bool wide = H > 32 * CB_VECTORS * 8;
-    p.token_ctas = !slots ? 0u : (wide ? static_cast<unsigned>(T) : static_cast<unsigned>(cdiv(T, CB_WARPS)));
+    const int most = T >= 1024 ? 2 : CB_WARPS, pieces = cdiv(p.vectors, 32 * CB_VECTORS);
+    const int warps = !wide ? CB_NARROW : pieces < most ? pieces : most;
+    p.token_ctas = !slots ? 0u : (wide ? static_cast<unsigned>(T) : static_cast<unsigned>(cdiv(T, CB_NARROW)));
     p.pads = pads ? static_cast<unsigned>(Mt / PAD_ROWS) : 0u;
-    const dim3 grid(p.token_ctas + (p.pads + CB_WARPS - 1) / CB_WARPS);
-    const cudaError_t e = wide ? launch_overlapped(combine_backward_kernel<true>, grid, dim3(32 * CB_WARPS), stream, p)
-                               : launch_overlapped(combine_backward_kernel<false>, grid, dim3(32 * CB_WARPS), stream, p);
+    const dim3 grid(p.token_ctas + static_cast<unsigned>(cdiv(p.pads, warps))), block(32u * static_cast<unsigned>(warps));
+    const cudaError_t e = launch_overlapped(wide ? combine_backward_kernel<true> : combine_backward_kernel<false>, grid, block, stream, p);
     return e == cudaSuccess ? DG_OK : DG_CUDA_ERROR;
 }
 

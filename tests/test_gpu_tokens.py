@@ -223,7 +223,7 @@ def test_infinities_and_nan_stay_in_their_tokens():
 
 
 @pytest.mark.parametrize("weighted", [False, True])
-@pytest.mark.parametrize("T,k,E,H", SUMS + [(40, 3, 4, 1024), (40, 3, 4, 4096), (9, 8, 8, 9000)])
+@pytest.mark.parametrize("T,k,E,H", SUMS + [(40, 3, 4, 1024), (40, 3, 4, 4096), (9, 8, 8, 9000), (1100, 3, 4, 2600)])
 def test_combine_backward(T, k, E, H, weighted):
     ids = make_ids(T, k, E, "outside" if T > 20 else "spread")
     rows, counts, m_indices = sort_contiguous(ids, E, extra=128)
@@ -247,8 +247,8 @@ def test_combine_backward(T, k, E, H, weighted):
         want[r] = dout[t].double() * (1.0 if w is None else w[t, j, None].double())
     # a product in FP32, rounded to BF16
     assert ((dy.double() - want).abs() <= (2.0 ** -8 + 2.0 ** -22) * want.abs() + 2.0 ** -133).all()
-    # 16 products a lane and its 2 halves for each 4096 values, 5 exchanges, 4 warps: one rounding each
-    chain = 17 * (H // 1024 + 1) + 5 + 4
+    # 16 products, 2 halves, 5 exchanges and the running sum for each piece of 1024 values a warp, 8 warps: a rounding each
+    chain = (16 + 1 + 5 + 1) * (H // 1024 + 1) + 8
     assert ((dw.double() - want_dw).abs() <= chain * 2.0 ** -24 * mag).all()
     # one without the other, and the same bits
     only, alone = torch.full_like(dy, 3.0), torch.empty_like(dw)
