@@ -266,10 +266,10 @@ __global__ void __launch_bounds__(GB_THREADS, 1) glu_backward_kernel(const GluBa
         __syncthreads();
         const size_t first = static_cast<size_t>(tn) * TILE * pitch + static_cast<size_t>(tm) * TILE;
         if (p.qt != nullptr) {
-            s.dg.store(p.qt + first, pitch, warp, lane);
-            s.du.store(p.qt + inner * pitch + first, pitch, warp, lane);
+            s.dg.store(p.qt + first, pitch);
+            s.du.store(p.qt + inner * pitch + first, pitch);
         }
-        if (p.ht != nullptr) s.h.store(p.ht + first, pitch, warp, lane);
+        if (p.ht != nullptr) s.h.store(p.ht + first, pitch);
     }
 }
 
@@ -282,51 +282,58 @@ struct TransposeParams {
     int m_tiles, n_tiles;
 };
 
-constexpr int TR_ROWS = 8;
-constexpr int TR_THREADS = 32 * TILE / TR_ROWS;
+// Tiles of 128 rows and 64 columns, four CTAs an SM: its three barriers a tile leave a CTA's warps waiting together, which more
+// and smaller CTAs fill (128 columns and two CTAs took 106.8 us for 32768 x 7168). A CTA takes every gridDim.x-th tile; the next
+// one's codes are asked for as soon as this one's are in use.
+constexpr int TR_ROWS = 8;                        // rows of a half warp
+constexpr int TR_COLUMNS = 64;
+constexpr int TR_CTAS = 4;
+using TransposeTile = TileColumns<TR_ROWS, true, TR_COLUMNS>;
 
-// A CTA takes every gridDim.x-th tile; the next one's codes are asked for as soon as this one's are in use.
-__global__ void __launch_bounds__(TR_THREADS, 2) transpose_kernel(const TransposeParams p) {
-    __shared__ TileColumns<TR_ROWS, true> s;
+__global__ void __launch_bounds__(TransposeTile::THREADS, TR_CTAS) transpose_kernel(const TransposeParams p) {
+    __shared__ TransposeTile s;
     grid_dependency_wait();
     grid_launch_dependents();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const size_t pitch = static_cast<size_t>(p.m_tiles) * TILE;
+    const int group = static_cast<int>(threadIdx.x) / 16, l16 = static_cast<int>(threadIdx.x) % 16;
+    const int64_t n = p.n, blocks = n / TILE, pitch = static_cast<int64_t>(p.m_tiles) * TILE;
     uint32_t codes[TR_ROWS];
-    float scale = 0.f;                            // lanes 0 .. 7: of the warp's rows
-    const size_t n = p.n, blocks = n / TILE;
+    float scale = 0.f;                            // the first 8 lanes of each half: of its rows
     TileWalk walk(p.m_tiles, p.n_tiles);
+    const uint8_t* q = p.q + group * TR_ROWS * n + l16 * 4;
+    const float* sf = p.sf + (group * TR_ROWS + l16) * blocks;
+    TileOffset from(walk, TILE * n, TR_COLUMNS), to(walk, TILE, TR_COLUMNS * pitch), scales(walk, 1, static_cast<int64_t>(TR_COLUMNS) * p.m_tiles);
     const auto load = [&]() {
-        const int r0 = walk.m * TILE + warp * TR_ROWS, valid = p.m - r0;
-        const uint8_t* src = p.q + r0 * n + walk.n * TILE + lane * 4;
-        const float* sf = p.sf + (r0 + lane) * blocks + walk.n;
+        const int valid = p.m - walk.m * TILE - group * TR_ROWS;
+        const uint8_t* src = q + from.at;
+        const float* ssf = sf + (walk.m * TILE * blocks + walk.n * TR_COLUMNS / TILE);
         if (valid >= TR_ROWS) {
-            if (lane < TR_ROWS) scale = ld_input(sf);
+            if (l16 < TR_ROWS) scale = ld_input(ssf);
 #pragma unroll
             for (int i = 0; i < TR_ROWS; ++i, src += n) codes[i] = ld_input(reinterpret_cast<const uint32_t*>(src));
         } else {
-            scale = lane < valid ? ld_input(sf) : 0.f;
+            scale = l16 < TR_ROWS && l16 < valid ? ld_input(ssf) : 0.f;
 #pragma unroll
             for (int i = 0; i < TR_ROWS; ++i, src += n) codes[i] = i < valid ? ld_input(reinterpret_cast<const uint32_t*>(src)) : 0u;
         }
     };
     if (walk.more()) load();
     for (bool more = walk.more(); more;) {
-        const size_t column = static_cast<size_t>(walk.n) * TILE;
-        const int m = walk.m;
         float2 v[TR_ROWS][2];
 #pragma unroll
-        for (int i = 0; i < TR_ROWS; ++i) code_values(codes[i], __shfl_sync(FULL, scale, i), v[i]);
-        walk.next();
+        for (int i = 0; i < TR_ROWS; ++i) code_values(codes[i], __shfl_sync(FULL, scale, i, 16), v[i]);
+        const bool wrapped = walk.next();
+        from.next(wrapped);
         more = walk.more();
         if (more) load();
-        s.maxima(v, warp, lane);
+        s.maxima(v, group, l16);
         __syncthreads();
-        if (threadIdx.x < TILE) s.scale(threadIdx.x, p.sft + (column + threadIdx.x) * p.m_tiles + m);
+        if (threadIdx.x < TR_COLUMNS) s.scale(threadIdx.x, p.sft + scales.at + static_cast<int>(threadIdx.x) * p.m_tiles);
+        scales.next(wrapped);
         __syncthreads();
-        s.quantise(v, warp, lane);
+        s.quantise(v, group, l16);
         __syncthreads();
-        s.store(p.qt + column * pitch + static_cast<size_t>(m) * TILE, pitch, warp, lane);
+        s.store(p.qt + to.at, pitch);
+        to.next(wrapped);
     }
 }
 
@@ -441,9 +448,9 @@ dg_status dg_transpose_fp8(const uint8_t* q, const float* sf, uint8_t* qt, float
     DeviceInfo dev;
     const dg_status st = device_info(&dev);
     if (st != DG_OK) return st;
-    const TransposeParams p = {q, sf, qt, sft, M, N, cdiv(M, TILE), N / TILE};
-    const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
-    const cudaError_t e = launch_overlapped(transpose_kernel, dim3(static_cast<unsigned>(tiles < 2 * dev.sms ? tiles : 2 * dev.sms)), dim3(TR_THREADS), stream, p);
+    const TransposeParams p = {q, sf, qt, sft, M, N, cdiv(M, TILE), N / TR_COLUMNS};
+    const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles, most = static_cast<int64_t>(TR_CTAS) * dev.sms;
+    const cudaError_t e = launch_overlapped(transpose_kernel, dim3(static_cast<unsigned>(tiles < most ? tiles : most)), dim3(TransposeTile::THREADS), stream, p);
     return e == cudaSuccess ? DG_OK : DG_CUDA_ERROR;
 }
 

@@ -53,17 +53,20 @@ __device__ __forceinline__ void tile_rows2(const float2 (&v)[R][2], const float2
     }
 }
 
-// Codes along the columns, in three steps with a barrier of the CTA behind each: every warp's maxima, the columns' scales,
-// the codes, which then leave as the rows of the transpose. EXACT: by the rounded quotient, else by the reciprocal.
-template <int R, bool EXACT>
+// Codes along the columns of a tile of 128 rows and COLUMNS columns, in three steps with a barrier of the CTA behind each: the
+// largest magnitudes of every group of R rows, the columns' scales, the codes, which then leave as the rows of the transpose.
+// A group of R rows is COLUMNS / 4 lanes', a warp's or half a warp's; `lane` is the one of these. EXACT: by the rounded quotient,
+// else by the reciprocal.
+template <int R, bool EXACT, int COLUMNS = TILE>
 struct TileColumns {
-    static constexpr int WARPS = TILE / R;
-    __align__(16) float amax[WARPS][TILE];
-    __align__(16) float divisor[TILE];            // negative
-    __align__(16) float reciprocal[TILE];
-    __align__(16) uint32_t codes[TILE * TILE / 4];
+    static constexpr int GROUPS = TILE / R;
+    static constexpr int THREADS = GROUPS * COLUMNS / 4;
+    __align__(16) float amax[GROUPS][COLUMNS];
+    __align__(16) float reciprocal[COLUMNS];
+    __align__(16) float rest[COLUMNS];            // of the reciprocal
+    __align__(16) uint32_t codes[TILE * COLUMNS / 4];
 
-    __device__ __forceinline__ void maxima(const float2 (&v)[R][2], int warp, int lane) {
+    __device__ __forceinline__ void maxima(const float2 (&v)[R][2], int group, int lane) {
         float a[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -73,36 +76,37 @@ struct TileColumns {
             for (int i = 3; i + 1 < R; i += 2) a[c] = abs_max(a[c], at(i), at(i + 1));
             if (R % 2 == 0) a[c] = abs_max(a[c], at(R - 1));
         }
-        *reinterpret_cast<float4*>(&amax[warp][lane * 4]) = make_float4(a[0], a[1], a[2], a[3]);
+        *reinterpret_cast<float4*>(&amax[group][lane * 4]) = make_float4(a[0], a[1], a[2], a[3]);
     }
 
-    // by 128 threads, one a column; sft: the column's scale
+    // by one thread a column; sft: the column's scale
     __device__ __forceinline__ void scale(int c, float* sft) {
         float a[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int w = 0; w < WARPS; w += 8)
+        for (int w = 0; w < GROUPS; w += 8)
 #pragma unroll
             for (int j = 0; j < 4; ++j) a[j] = abs_max(a[j], amax[w + j][c], amax[w + j + 4][c]);
         const BlockScale k = block_scale(abs_bits(abs_max(abs_max(a[0], a[1], a[2]), a[3])));
-        divisor[c] = -k.d;
         reciprocal[c] = k.r;
+        if (EXACT) rest[c] = reciprocal_rest(k.d, k.r);
         *sft = k.s;
     }
 
-    // Rows 4w .. 4w + 3 of column c are word w of its 32, at w ^ (R / 4) ((c / 4) % WARPS): neither these stores nor the loads
-    // below meet in a bank.
-    __device__ __forceinline__ void quantise(const float2 (&v)[R][2], int warp, int lane) {
-        const float4 d = *reinterpret_cast<const float4*>(&divisor[lane * 4]), r = *reinterpret_cast<const float4*>(&reciprocal[lane * 4]);
-        const int slot = warp ^ (lane & (WARPS - 1));
+    // Rows 4w .. 4w + 3 of column c are word w of its 32. A group's words are at group ^ (c / 4 % GROUPS): neither these stores nor
+    // the loads below meet in a bank.
+    __device__ __forceinline__ void quantise(const float2 (&v)[R][2], int group, int lane) {
+        const float4 r = *reinterpret_cast<const float4*>(&reciprocal[lane * 4]);
+        const float4 d = EXACT ? *reinterpret_cast<const float4*>(&rest[lane * 4]) : r;
+        const int slot = group ^ (lane & (GROUPS - 1));
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            const float2 nd = x ? make_float2(d.z, d.w) : make_float2(d.x, d.y), rr = x ? make_float2(r.z, r.w) : make_float2(r.x, r.y);
+            const float2 rest2 = x ? make_float2(d.z, d.w) : make_float2(d.x, d.y), rr = x ? make_float2(r.z, r.w) : make_float2(r.x, r.y);
             uint32_t lo[R / 4], hi[R / 4];
 #pragma unroll
             for (int i = 0; i < R; i += 4) {
                 float2 w[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) w[j] = EXACT ? quotient2(v[i + j][x], nd, rr) : __fmul2_rn(v[i + j][x], rr);
+                for (int j = 0; j < 4; ++j) w[j] = EXACT ? quotient2_by(v[i + j][x], rr, rest2) : __fmul2_rn(v[i + j][x], rr);
                 lo[i / 4] = pack_e4m3x2(w[0].x, w[1].x) | (pack_e4m3x2(w[2].x, w[3].x) << 16);
                 hi[i / 4] = pack_e4m3x2(w[0].y, w[1].y) | (pack_e4m3x2(w[2].y, w[3].y) << 16);
             }
@@ -117,21 +121,17 @@ struct TileColumns {
         }
     }
 
-    // 128 bytes a column, R = 8: 16 lanes, R = 4: the warp; qt points at the tile's first column's codes, columns `pitch` apart.
-    __device__ __forceinline__ void store(uint8_t* qt, size_t pitch, int warp, int lane) const {
-        if constexpr (R == 8) {
-            const int l16 = lane & 15, c0 = warp * 2 + (lane >> 4);
-            uint8_t* dst = qt + static_cast<size_t>(c0) * pitch + l16 * 8;
-            const uint32_t* src = codes + c0 * 32;
+    // 128 bytes a column by GROUPS lanes; qt points at the tile's first column's codes, columns `pitch` apart.
+    __device__ __forceinline__ void store(uint8_t* qt, size_t pitch) const {
+        constexpr int PASS = THREADS / GROUPS;    // columns at a time
+        const int l = static_cast<int>(threadIdx.x) % GROUPS, c0 = static_cast<int>(threadIdx.x) / GROUPS;
+        uint8_t* dst = qt + static_cast<size_t>(c0) * pitch + l * R;
+        const uint32_t* src = codes + c0 * 32;
 #pragma unroll
-            for (int i = 0; i < 4; ++i, dst += 32 * pitch)        // ((c >> 2) & 15 = c0 >> 2 ^ 8 (i & 1) for c = c0 + 32 i)
-                *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(src + i * 1024 + 2 * (l16 ^ (c0 >> 2) ^ (8 * (i & 1))));
-        } else {
-            uint8_t* dst = qt + static_cast<size_t>(warp) * pitch + lane * 4;
-            const uint32_t* src = codes + warp * 32;
-#pragma unroll
-            for (int i = 0; i < 4; ++i, dst += 32 * pitch)        // (c >> 2 = warp >> 2 ^ 8 i for c = warp + 32 i)
-                *reinterpret_cast<uint32_t*>(dst) = src[i * 1024 + (lane ^ (warp >> 2) ^ (8 * i))];
+        for (int i = 0; i < COLUMNS / PASS; ++i, dst += PASS * pitch) {
+            const int at = i * PASS * 32 + (l ^ (c0 >> 2) ^ (i * (PASS / 4) & (GROUPS - 1))) * (R / 4);      // (c0 >> 2 is below PASS / 4)
+            if constexpr (R == 8) *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(src + at);
+            else *reinterpret_cast<uint32_t*>(dst) = src[at];
         }
     }
 };
@@ -147,14 +147,23 @@ struct TileWalk {
         step_n = static_cast<int>(gridDim.x) - step_m * n_tiles;
     }
     __device__ __forceinline__ bool more() const { return m < m_tiles; }
-    __device__ __forceinline__ void next() {
+    // To the next tile; whether it is past the end of a row of tiles.
+    __device__ __forceinline__ bool next() {
         m += step_m;
         n += step_n;
-        if (n >= n_tiles) {
-            n -= n_tiles;
-            ++m;
-        }
+        if (n < n_tiles) return false;
+        n -= n_tiles;
+        ++m;
+        return true;
     }
+};
+
+// A place in an array that moves with the tiles: by `of_m` a row of tiles and `of_n` a column of them.
+struct TileOffset {
+    int64_t at, step, wrap;
+    __device__ __forceinline__ TileOffset(const TileWalk& w, int64_t of_m, int64_t of_n)
+        : at(w.m * of_m + w.n * of_n), step(w.step_m * of_m + w.step_n * of_n), wrap(of_m - w.n_tiles * of_n) {}
+    __device__ __forceinline__ void next(bool wrapped) { at += wrapped ? step + wrap : step; }
 };
 
 }  // namespace dg
