@@ -26,7 +26,8 @@ namespace {
 constexpr unsigned FULL = 0xffffffffu;
 constexpr int64_t TILES_MAX = INT32_MAX / 2;        // (tiles are numbered in 32 bits)
 constexpr int GLU_WARPS = 4;
-constexpr int GLU_ROWS = 8 * GLU_WARPS;           // rows of a CTA
+constexpr int GLU_LANE_ROWS = 4;                  // rows of a half warp
+__host__ __device__ constexpr int glu_ctas(bool keep) { return keep ? 4 : 5; }    // of an SM: what the registers hold
 
 struct GluParams {
     const __nv_bfloat16* z;
@@ -39,16 +40,6 @@ struct GluParams {
     int m, inner, max_m, pow2;
 };
 
-// Four lines' largest magnitudes over 16 lanes, giving away lines on the way: lane l ends with that of line l / 4.
-__device__ __forceinline__ float four_maxima(const float (&a)[4], int l16) {
-    const bool up8 = (l16 & 8) != 0, up4 = (l16 & 4) != 0;
-    const float b0 = abs_max(up8 ? a[2] : a[0], __shfl_xor_sync(FULL, up8 ? a[0] : a[2], 8));
-    const float b1 = abs_max(up8 ? a[3] : a[1], __shfl_xor_sync(FULL, up8 ? a[1] : a[3], 8));
-    float most = abs_max(up4 ? b1 : b0, __shfl_xor_sync(FULL, up4 ? b0 : b1, 4));
-    most = abs_max(most, __shfl_xor_sync(FULL, most, 2));
-    return abs_max(most, __shfl_xor_sync(FULL, most, 1));
-}
-
 __device__ __forceinline__ float abs_max8(const float2 (&a)[4]) {
     return abs_max(abs_max(a[0].x, a[0].y, a[1].x), abs_max(a[1].y, a[2].x, a[2].y), abs_max(a[3].x, a[3].y));
 }
@@ -59,71 +50,151 @@ __device__ __forceinline__ void unpack_bf16(const uint4& v, float2 (&a)[4]) {
     for (int i = 0; i < 4; ++i) a[i] = make_float2(bf16_lo(u[i]), bf16_hi(u[i]));
 }
 
-// Codes of 4 rows of a block of 128 and their scales; `rows` has a bit for each row that is written.
-__device__ __forceinline__ void quantise_rows(const float2 (&v)[4][4], uint8_t* q, size_t pitch, float* sf, size_t scales, bool pow2, unsigned rows,
-                                              int l16) {
-    const float a[4] = {abs_max8(v[0]), abs_max8(v[1]), abs_max8(v[2]), abs_max8(v[3])};
-    const uint32_t most = abs_bits(four_maxima(a, l16));
-    const BlockScale mine = pow2 ? block_scale_pow2(most) : block_scale(most);
-    if ((l16 & 3) == 0 && (rows >> (l16 >> 2) & 1)) sf[static_cast<size_t>(l16 >> 2) * scales] = mine.s;
+// The largest magnitudes of N lines (a power of two up to 16), each spread over 16 lanes, giving away lines on the way: lane l
+// ends with that of line l / (16 / N).
+template <int N>
+__device__ __forceinline__ float line_maxima(float (&a)[N], int l16) {
+    int step = 8;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        BlockScale k;
-        k.d = __shfl_sync(FULL, mine.d, i * 4, 16);
-        k.r = __shfl_sync(FULL, mine.r, i * 4, 16);
-        const uint2 w = make_uint2(quantise4(v[i][0], v[i][1], k), quantise4(v[i][2], v[i][3], k));
-        if (rows >> i & 1) *reinterpret_cast<uint2*>(q + static_cast<size_t>(i) * pitch) = w;
+    for (int n = N; n > 1; n /= 2, step /= 2) {
+        const bool up = (l16 & step) != 0;
+#pragma unroll
+        for (int i = 0; i < n / 2; ++i) {
+            const float give = up ? a[i] : a[n / 2 + i], keep = up ? a[n / 2 + i] : a[i];
+            a[i] = abs_max(keep, __shfl_xor_sync(FULL, give, step));
+        }
     }
+    float most = a[0];
+#pragma unroll
+    for (; step > 0; step /= 2) most = abs_max(most, __shfl_xor_sync(FULL, most, step));
+    return most;
 }
 
-template <int ACT>
-__global__ void __launch_bounds__(32 * GLU_WARPS) glu_kernel(const GluParams p) {
+// Codes of a lane's 8 values of a line whose scale lane `from` has: exact quotients for values that are exact, for others by
+// the reciprocal.
+template <bool EXACT>
+__device__ __forceinline__ uint2 line_codes(const float2 (&v)[4], const BlockScale& mine, float rest, int from) {
+    const float r = __shfl_sync(FULL, mine.r, from, 16);
+    if (!EXACT) return make_uint2(quantise4_by(v[0], v[1], r), quantise4_by(v[2], v[3], r));
+    const float l = __shfl_sync(FULL, rest, from, 16);
+    const float2 rr = make_float2(r, r), ll = make_float2(l, l);
+    float2 c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = quotient2_by(v[i], rr, ll);
+    return make_uint2(pack_e4m3x2(c[0].x, c[0].y) | (pack_e4m3x2(c[1].x, c[1].y) << 16), pack_e4m3x2(c[2].x, c[2].y) | (pack_e4m3x2(c[3].x, c[3].y) << 16));
+}
+
+// A half warp has the 128 values of a scaling block of 4 rows, a lane 8 columns of each, in both halves of Z. The largest
+// magnitudes of all its lines (h's, with KEEP g's and u's) are found together, and each line's scale is made by one lane. A warp
+// takes piece after piece, and the next one's values come by asynchronous copies into places that only their lane reads: with
+// loads into registers 36.8 k rows of 2 x 2048 took 94.4 us (two rows a lane, 8 CTAs an SM) with codes kept and 58.9 without, so
+// they take 81.6 and 55.5, the memory's time (6.5 and 6.8 TB/s).
+template <int ACT, bool KEEP>
+__global__ void __launch_bounds__(32 * GLU_WARPS, glu_ctas(KEEP)) glu_kernel(const GluParams p) {
+    constexpr int R = GLU_LANE_ROWS, LINES = KEEP ? 4 * R : R, SHARE = 16 / LINES;
+    constexpr unsigned ALL = (1u << R) - 1;
+    __shared__ __align__(16) uint4 s_z[2][2 * R][32 * GLU_WARPS];     // [stage][row of g, row of u][thread]
     grid_dependency_wait();
     grid_launch_dependents();
     const int warp = threadIdx.x >> 5, l16 = threadIdx.x & 15, half = (threadIdx.x >> 4) & 1;
-    const int r0 = static_cast<int>(blockIdx.x) * GLU_ROWS + warp * 8 + half * 4;
-    const int c0 = static_cast<int>(blockIdx.y) * 128 + l16 * 8;
-    unsigned rows = 0;
-    if (p.m_indices != nullptr) {
-        // (4 rows are of one block of 128, which is computed if its first row has an expert)
-        if (r0 < p.m && ld_input(p.m_indices + r0 / 128 * 128) >= 0) rows = 15;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (r0 + i < p.m && (p.masked_m == nullptr || (r0 + i) % p.max_m < ld_input(p.masked_m + (r0 + i) / p.max_m))) rows |= 1u << i;
-    }
-    if (__all_sync(FULL, rows == 0)) return;
+    const size_t inner = p.inner, blocks = inner / 128;
+    TileWalk walk((p.m + 2 * R - 1) / (2 * R), p.inner / 128, static_cast<int>(blockIdx.x) * GLU_WARPS + warp, static_cast<int>(gridDim.x) * GLU_WARPS);
 
-    const size_t base = static_cast<size_t>(r0) * (2 * p.inner) + c0;
-    uint4 gw[4], uw[4];
+    // Asks for the next piece that has rows to compute: their mask, 0 where there is no such piece.
+    unsigned rows = 0;
+    int r0 = 0, block = 0;
+    const auto fetch = [&](int stage) {
+        for (rows = 0; walk.more(); walk.next()) {
+            r0 = (walk.outer * 2 + half) * R;
+            block = walk.inner;
+            if (p.m_indices != nullptr) {
+                // (the rows are of one block of 128, which is computed if its first row has an expert)
+                if (r0 < p.m && ld_input(p.m_indices + r0 / 128 * 128) >= 0) rows = ALL;
+            } else if (p.masked_m != nullptr) {
+                int g = r0 / p.max_m, at = r0 - g * p.max_m;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        gw[i] = uw[i] = make_uint4(0, 0, 0, 0);
-        if (rows >> i & 1) {
-            gw[i] = ld_input(reinterpret_cast<const uint4*>(p.z + base + static_cast<size_t>(i) * (2 * p.inner)));
-            uw[i] = ld_input(reinterpret_cast<const uint4*>(p.z + base + static_cast<size_t>(i) * (2 * p.inner) + p.inner));
+                for (int i = 0; i < R; ++i) {
+                    if (r0 + i < p.m && at < ld_input(p.masked_m + g)) rows |= 1u << i;
+                    if (++at == p.max_m) {
+                        at = 0;
+                        ++g;
+                    }
+                }
+            } else {
+                const int left = p.m - r0;
+                rows = left >= R ? ALL : left > 0 ? (1u << left) - 1 : 0;
+            }
+            if (__any_sync(FULL, rows != 0)) {
+                walk.next();
+                break;
+            }
+        }
+        const __nv_bfloat16* src = p.z + static_cast<size_t>(r0) * (2 * inner) + block * 128 + l16 * 8;
+#pragma unroll
+        for (int i = 0; i < R; ++i, src += 2 * inner) {
+            if (rows >> i & 1) {
+                cp_async_16(&s_z[stage][i][threadIdx.x], src);
+                cp_async_16(&s_z[stage][R + i][threadIdx.x], src + inner);
+            } else {
+                s_z[stage][i][threadIdx.x] = s_z[stage][R + i][threadIdx.x] = make_uint4(0, 0, 0, 0);
+            }
+        }
+        cp_async_commit();
+        return __any_sync(FULL, rows != 0);
+    };
+    int stage = 0;
+    for (bool more = fetch(0); more; stage ^= 1) {
+        const unsigned mask = rows;
+        const int row0 = r0, column = block;
+        more = fetch(stage ^ 1);
+        cp_async_wait_group<1>();
+        float2 h[R][4];
+        float most[LINES];
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            float2 g[4], u[4];
+            unpack_bf16(s_z[stage][i][threadIdx.x], g);
+            unpack_bf16(s_z[stage][R + i][threadIdx.x], u);
+            if (KEEP) {
+                most[R + i] = abs_max8(g);
+                most[2 * R + i] = abs_max8(u);
+                most[3 * R + i] = 0.f;
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c) h[i][c] = __fmul2_rn(act_value2<ACT>(g[c]), u[c]);
+            most[i] = abs_max8(h[i]);
+        }
+        const uint32_t bits = abs_bits(line_maxima(most, l16));
+        const int line = l16 / SHARE, row = line & (R - 1), which = line / R;
+        const BlockScale mine = p.pow2 && which == 0 ? block_scale_pow2(bits) : block_scale(bits);
+        const float rest = KEEP ? reciprocal_rest(mine.d, mine.r) : 0.f;
+        if (l16 % SHARE == 0 && (mask >> row & 1)) {
+            const size_t at = static_cast<size_t>(row0 + row) * blocks;
+            if (which == 0) p.sf[at + column] = mine.s;
+            if (KEEP && (which == 1 || which == 2)) p.kept_sf[2 * at + (which - 1) * blocks + column] = mine.s;
+        }
+        uint8_t* q = p.q + static_cast<size_t>(row0) * inner + column * 128 + l16 * 8;
+        uint8_t* kept = KEEP ? p.kept + static_cast<size_t>(row0) * (2 * inner) + column * 128 + l16 * 8 : nullptr;
+#pragma unroll
+        for (int i = 0; i < R; ++i, q += inner) {
+            const uint2 w = line_codes<false>(h[i], mine, rest, i * SHARE);
+            if (mask >> i & 1) *reinterpret_cast<uint2*>(q) = w;
+        }
+        if (KEEP) {
+#pragma unroll
+            for (int i = 0; i < R; ++i, kept += 2 * inner) {
+                float2 v[4];
+                unpack_bf16(s_z[stage][i][threadIdx.x], v);
+                const uint2 gq = line_codes<true>(v, mine, rest, (R + i) * SHARE);
+                unpack_bf16(s_z[stage][R + i][threadIdx.x], v);
+                const uint2 uq = line_codes<true>(v, mine, rest, (2 * R + i) * SHARE);
+                if (mask >> i & 1) {
+                    *reinterpret_cast<uint2*>(kept) = gq;
+                    *reinterpret_cast<uint2*>(kept + inner) = uq;
+                }
+            }
         }
     }
-    const size_t blocks = p.inner / 128;
-    float2 v[4][4];
-    if (p.kept != nullptr) {
-        float* sf = p.kept_sf + static_cast<size_t>(r0) * (2 * blocks) + blockIdx.y;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) unpack_bf16(gw[i], v[i]);
-        quantise_rows(v, p.kept + base, 2 * static_cast<size_t>(p.inner), sf, 2 * blocks, false, rows, l16);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) unpack_bf16(uw[i], v[i]);
-        quantise_rows(v, p.kept + base + p.inner, 2 * static_cast<size_t>(p.inner), sf + blocks, 2 * blocks, false, rows, l16);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float2 g[4], u[4];
-        unpack_bf16(gw[i], g);
-        unpack_bf16(uw[i], u);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) v[i][c] = __fmul2_rn(act_value2<ACT>(g[c]), u[c]);
-    }
-    quantise_rows(v, p.q + static_cast<size_t>(r0) * p.inner + c0, p.inner, p.sf + static_cast<size_t>(r0) * blocks + blockIdx.y, blocks, p.pow2 != 0, rows, l16);
 }
 
 // ------------------------------------------------------------------------------------ backward
@@ -180,7 +251,7 @@ __global__ void __launch_bounds__(GB_THREADS, 1) glu_backward_kernel(const GluBa
     const size_t inner = p.inner, blocks = inner / 128, pitch = static_cast<size_t>(p.m_tiles) * TILE;
     // (rows past M are zeros: so are the activations there, and their slopes are finite)
     const auto fetch = [&](const TileWalk& at) {
-        const int t = threadIdx.x, m0 = at.m * TILE, n0 = at.n * TILE;
+        const int t = threadIdx.x, m0 = at.outer * TILE, n0 = at.inner * TILE;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int r = i * 64 + t / 16;
@@ -202,7 +273,7 @@ __global__ void __launch_bounds__(GB_THREADS, 1) glu_backward_kernel(const GluBa
             cp_async_16_or_zero(&s.u[r][t % 8 * 4], there ? src + inner : src, there);
             if (t < 2 * TILE) {
                 const int which = t / TILE, rs = t % TILE;
-                if (m0 + rs < p.m) cp_async_4(&s.scale[which][rs], p.kept_sf + static_cast<size_t>(m0 + rs) * (2 * blocks) + which * blocks + at.n);
+                if (m0 + rs < p.m) cp_async_4(&s.scale[which][rs], p.kept_sf + static_cast<size_t>(m0 + rs) * (2 * blocks) + which * blocks + at.inner);
                 else s.scale[which][rs] = 0.f;
             }
         }
@@ -212,7 +283,7 @@ __global__ void __launch_bounds__(GB_THREADS, 1) glu_backward_kernel(const GluBa
     cp_async_wait_all();
     __syncthreads();
     for (bool more = walk.more(); more;) {
-        const int tm = walk.m, tn = walk.n;
+        const int tm = walk.outer, tn = walk.inner;
         const int r0 = tm * TILE + warp * GB_ROWS, c0 = tn * TILE + lane * 4, valid = p.m - r0;
         float2 dg[GB_ROWS][2], du[GB_ROWS][2], h[GB_ROWS][2];
 #pragma unroll
@@ -303,9 +374,9 @@ __global__ void __launch_bounds__(TransposeTile::THREADS, TR_CTAS) transpose_ker
     const float* sf = p.sf + (group * TR_ROWS + l16) * blocks;
     TileOffset from(walk, TILE * n, TR_COLUMNS), to(walk, TILE, TR_COLUMNS * pitch), scales(walk, 1, static_cast<int64_t>(TR_COLUMNS) * p.m_tiles);
     const auto load = [&]() {
-        const int valid = p.m - walk.m * TILE - group * TR_ROWS;
+        const int valid = p.m - walk.outer * TILE - group * TR_ROWS;
         const uint8_t* src = q + from.at;
-        const float* ssf = sf + (walk.m * TILE * blocks + walk.n * TR_COLUMNS / TILE);
+        const float* ssf = sf + (walk.outer * TILE * blocks + walk.inner * TR_COLUMNS / TILE);
         if (valid >= TR_ROWS) {
             if (l16 < TR_ROWS) scale = ld_input(ssf);
 #pragma unroll
@@ -334,6 +405,19 @@ __global__ void __launch_bounds__(TransposeTile::THREADS, TR_CTAS) transpose_ker
         __syncthreads();
         s.store(p.qt + to.at, pitch);
         to.next(wrapped);
+    }
+}
+
+template <bool KEEP>
+cudaError_t launch_glu(const GluParams& p, int act, int sms, cudaStream_t stream) {
+    const int64_t pieces = static_cast<int64_t>(cdiv(p.m, 2 * GLU_LANE_ROWS)) * (p.inner / 128), ctas = (pieces + GLU_WARPS - 1) / GLU_WARPS;
+    const dim3 grid(static_cast<unsigned>(ctas < glu_ctas(KEEP) * sms ? ctas : glu_ctas(KEEP) * sms)), block(32 * GLU_WARPS);
+    switch (act) {
+        case DG_ACT_RELU: return launch_overlapped(glu_kernel<DG_ACT_RELU, KEEP>, grid, block, stream, p);
+        case DG_ACT_GELU: return launch_overlapped(glu_kernel<DG_ACT_GELU, KEEP>, grid, block, stream, p);
+        case DG_ACT_GELU_TANH: return launch_overlapped(glu_kernel<DG_ACT_GELU_TANH, KEEP>, grid, block, stream, p);
+        case DG_ACT_SILU: return launch_overlapped(glu_kernel<DG_ACT_SILU, KEEP>, grid, block, stream, p);
+        default: return launch_overlapped(glu_kernel<DG_ACT_NONE, KEEP>, grid, block, stream, p);
     }
 }
 
@@ -372,7 +456,7 @@ dg_status dg_glu(const void* Z, uint8_t* q, float* sf, uint8_t* kept, float* kep
     if (m_indices && M % 128 != 0) return DG_UNSUPPORTED_SHAPE;
     if (masked_m && (G < 1 || M % G != 0)) return DG_INVALID_ARG;
     if (M == 0 || I == 0) return DG_OK;
-    if (M > INT32_MAX - GLU_ROWS) return DG_UNSUPPORTED_SHAPE;
+    if (M > INT32_MAX - TILE || static_cast<int64_t>(cdiv(M, 2 * GLU_LANE_ROWS)) * (I / 128) > TILES_MAX) return DG_UNSUPPORTED_SHAPE;
     if (!Z || !q || !sf) return DG_INVALID_ARG;
     if (!aligned(Z, 16) || !aligned(q, 16) || !aligned(kept, 16) || !aligned(sf, 4) || !aligned(kept_sf, 4) || !aligned(m_indices, 4) || !aligned(masked_m, 4))
         return DG_MISALIGNED;
@@ -391,15 +475,7 @@ dg_status dg_glu(const void* Z, uint8_t* q, float* sf, uint8_t* kept, float* kep
     p.inner = I;
     p.max_m = masked_m ? M / G : M;
     p.pow2 = pow2;
-    const dim3 grid(static_cast<unsigned>(cdiv(M, GLU_ROWS)), static_cast<unsigned>(I / 128)), block(32 * GLU_WARPS);
-    cudaError_t e = cudaErrorInvalidValue;
-    switch (act) {
-        case DG_ACT_NONE: e = launch_overlapped(glu_kernel<DG_ACT_NONE>, grid, block, stream, p); break;
-        case DG_ACT_RELU: e = launch_overlapped(glu_kernel<DG_ACT_RELU>, grid, block, stream, p); break;
-        case DG_ACT_GELU: e = launch_overlapped(glu_kernel<DG_ACT_GELU>, grid, block, stream, p); break;
-        case DG_ACT_GELU_TANH: e = launch_overlapped(glu_kernel<DG_ACT_GELU_TANH>, grid, block, stream, p); break;
-        case DG_ACT_SILU: e = launch_overlapped(glu_kernel<DG_ACT_SILU>, grid, block, stream, p); break;
-    }
+    const cudaError_t e = kept ? launch_glu<true>(p, act, dev.sms, stream) : launch_glu<false>(p, act, dev.sms, stream);
     return e == cudaSuccess ? DG_OK : DG_CUDA_ERROR;
 }
 

@@ -136,33 +136,34 @@ struct TileColumns {
     }
 };
 
-// The tiles that a CTA takes: every gridDim.x-th, along the rows of tiles first, so that what runs at the same time reads whole
-// rows. The steps are worked out once: a division for each tile would be a tenth of its instructions.
+// The tiles that a CTA (or a warp) takes: every gridDim.x-th, the inner index first. The steps are worked out once: a division for each tile
+// would be a tenth of its instructions.
 struct TileWalk {
-    int m, n, step_m, step_n, m_tiles, n_tiles;
-    __device__ __forceinline__ TileWalk(int m_tiles, int n_tiles) : m_tiles(m_tiles), n_tiles(n_tiles) {
-        m = static_cast<int>(blockIdx.x) / n_tiles;
-        n = static_cast<int>(blockIdx.x) - m * n_tiles;
-        step_m = static_cast<int>(gridDim.x) / n_tiles;
-        step_n = static_cast<int>(gridDim.x) - step_m * n_tiles;
+    int outer, inner, step_outer, step_inner, outers, inners;
+    __device__ __forceinline__ TileWalk(int outers, int inners, int first, int every) : outers(outers), inners(inners) {
+        outer = first / inners;
+        inner = first - outer * inners;
+        step_outer = every / inners;
+        step_inner = every - step_outer * inners;
     }
-    __device__ __forceinline__ bool more() const { return m < m_tiles; }
-    // To the next tile; whether it is past the end of a row of tiles.
+    __device__ __forceinline__ TileWalk(int outers, int inners) : TileWalk(outers, inners, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x)) {}
+    __device__ __forceinline__ bool more() const { return outer < outers; }
+    // To the next tile; whether the inner index has begun again.
     __device__ __forceinline__ bool next() {
-        m += step_m;
-        n += step_n;
-        if (n < n_tiles) return false;
-        n -= n_tiles;
-        ++m;
+        outer += step_outer;
+        inner += step_inner;
+        if (inner < inners) return false;
+        inner -= inners;
+        ++outer;
         return true;
     }
 };
 
-// A place in an array that moves with the tiles: by `of_m` a row of tiles and `of_n` a column of them.
+// A place in an array that moves with the tiles, by so much for each step of the outer and the inner index.
 struct TileOffset {
     int64_t at, step, wrap;
-    __device__ __forceinline__ TileOffset(const TileWalk& w, int64_t of_m, int64_t of_n)
-        : at(w.m * of_m + w.n * of_n), step(w.step_m * of_m + w.step_n * of_n), wrap(of_m - w.n_tiles * of_n) {}
+    __device__ __forceinline__ TileOffset(const TileWalk& w, int64_t of_outer, int64_t of_inner)
+        : at(w.outer * of_outer + w.inner * of_inner), step(w.step_outer * of_outer + w.step_inner * of_inner), wrap(of_outer - w.inners * of_inner) {}
     __device__ __forceinline__ void next(bool wrapped) { at += wrapped ? step + wrap : step; }
 };
 
