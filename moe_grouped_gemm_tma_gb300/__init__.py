@@ -529,15 +529,7 @@ def dg_moe_layer(x, ids, weights, W13, s13, W2, s2, out, workspace, act="silu", 
 
 
 # The calls between the grouped products check their arguments in one expression too, and that all of them are on the
-# current device, where the launch goes.
-def _here(stream, device):
-    """The stream's handle; the tensors' device has to be the current one."""
-    c = _torch()._C
-    if device != c._cuda_getDevice():
-        raise ValueError(f"the tensors are on cuda:{device}, the current device is cuda:{c._cuda_getDevice()}")
-    return c._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
-
-
+# current device, where the launch goes: _refuse_here says what is wrong.
 def _fits(t, dtype, shape, device):
     return t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous()
 
@@ -547,6 +539,18 @@ def _refuse_here(device, **args):
     for name, (t, _, _) in args.items():
         if t is not None and t.get_device() != device:
             raise ValueError(f"{name} is on {t.device}, the first argument on cuda:{device}")
+
+
+def _workspace_here(t, device):
+    """A workspace's address and size."""
+    ws, size = _bytes(t, "workspace")
+    if size and t.get_device() != device:
+        raise ValueError(f"workspace is on {t.device}, the first argument on cuda:{device}")
+    return ws, size
+
+
+def _refuse_device(device):
+    raise ValueError(f"the tensors are on cuda:{device}, the current device is cuda:{_torch()._C._cuda_getDevice()}")
 
 
 def moe_sort_rows(T: int, k: int, E: int) -> int:
@@ -573,11 +577,15 @@ def dg_moe_sort_contiguous(ids, rows, counts, m_indices, workspace=None, stream=
     Tk = T, k = ids.shape
     E, Mt = counts.shape[0], m_indices.shape[0]
     dev = ids.get_device()
-    if not (_fits(ids, i32, Tk, dev) and _fits(rows, i32, Tk, dev) and _fits(counts, i32, (E,), dev) and _fits(m_indices, i32, (Mt,), dev) and dev >= 0):
+    if not (ids.dtype is i32 and ids.is_contiguous() and dev >= 0 and rows.dtype is i32 and rows.shape == Tk and rows.get_device() == dev
+            and rows.is_contiguous() and counts.dtype is i32 and counts.shape == (E,) and counts.get_device() == dev and counts.is_contiguous()
+            and m_indices.dtype is i32 and m_indices.shape == (Mt,) and m_indices.get_device() == dev and m_indices.is_contiguous()
+            and torch._C._cuda_getDevice() == dev):
         _refuse_here(dev, ids=(ids, (i32,), None), rows=(rows, (i32,), Tk), counts=(counts, (i32,), (E,)), m_indices=(m_indices, (i32,), (Mt,)))
-    ws, size = _bytes(workspace, "workspace")
+        _refuse_device(dev)
+    ws, size = _workspace_here(workspace, dev)
     st = (_lib or load()).dg_moe_sort_contiguous(ids.data_ptr(), rows.data_ptr(), counts.data_ptr(), m_indices.data_ptr(), ws, size, T, k, E, Mt,
-                                                 _here(stream, dev))
+                                                 torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
     if st:
         raise DGError(st, "dg_moe_sort_contiguous")
     return rows
@@ -591,10 +599,14 @@ def dg_moe_sort_masked(ids, rows, masked_m, max_m: int, workspace=None, stream=N
     Tk = T, k = ids.shape
     E = masked_m.shape[0]
     dev = ids.get_device()
-    if not (_fits(ids, i32, Tk, dev) and _fits(rows, i32, Tk, dev) and _fits(masked_m, i32, (E,), dev) and dev >= 0):
+    if not (ids.dtype is i32 and ids.is_contiguous() and dev >= 0 and rows.dtype is i32 and rows.shape == Tk and rows.get_device() == dev
+            and rows.is_contiguous() and masked_m.dtype is i32 and masked_m.shape == (E,) and masked_m.get_device() == dev and masked_m.is_contiguous()
+            and torch._C._cuda_getDevice() == dev):
         _refuse_here(dev, ids=(ids, (i32,), None), rows=(rows, (i32,), Tk), masked_m=(masked_m, (i32,), (E,)))
-    ws, size = _bytes(workspace, "workspace")
-    st = (_lib or load()).dg_moe_sort_masked(ids.data_ptr(), rows.data_ptr(), masked_m.data_ptr(), ws, size, T, k, E, max_m, _here(stream, dev))
+        _refuse_device(dev)
+    ws, size = _workspace_here(workspace, dev)
+    st = (_lib or load()).dg_moe_sort_masked(ids.data_ptr(), rows.data_ptr(), masked_m.data_ptr(), ws, size, T, k, E, int(max_m),
+                                             torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
     if st:
         raise DGError(st, "dg_moe_sort_masked")
     return rows
@@ -612,18 +624,22 @@ def dg_moe_gather(x, sf, rows, out, out_sf=None, m_indices=None, stream=None):
     dev = x.get_device()
     lead = out.shape[:-1]
     Mt = lead.numel()
-    if not (x.is_contiguous() and dev >= 0 and x.shape[0] == T and _fits(rows, i32, Tk, dev) and out.shape[-1] == H and out.get_device() == dev
-            and out.is_contiguous() and (m_indices is None or _fits(m_indices, i32, (Mt,), dev))
-            and ((x.dtype in e4m3 and out.dtype in e4m3 and sf is not None and out_sf is not None and _fits(sf, f32, (T, H // 128), dev)
-                  and _fits(out_sf, f32, (*lead, H // 128), dev)) if codes else (out.dtype is bf16 and sf is None and out_sf is None))):
+    if not (x.is_contiguous() and dev >= 0 and x.shape[0] == T and rows.dtype is i32 and rows.get_device() == dev and rows.is_contiguous()
+            and out.shape[-1] == H and out.get_device() == dev and out.is_contiguous() and (m_indices is None or _fits(m_indices, i32, (Mt,), dev))
+            and ((x.dtype in e4m3 and out.dtype in e4m3 and sf is not None and out_sf is not None and sf.dtype is f32 and sf.shape == (T, H // 128)
+                  and sf.get_device() == dev and sf.is_contiguous() and out_sf.dtype is f32 and out_sf.shape == (*lead, H // 128)
+                  and out_sf.get_device() == dev and out_sf.is_contiguous()) if codes else (out.dtype is bf16 and sf is None and out_sf is None))
+            and torch._C._cuda_getDevice() == dev):
         if codes and x.dtype not in e4m3:
             raise TypeError(f"x must be float8_e4m3fn, uint8 or bfloat16, got {x.dtype}")
         _refuse_here(dev, x=(x, e4m3 if codes else (bf16,), None), rows=(rows, (i32,), (x.shape[0], k)), out=(out, e4m3 if codes else (bf16,), (*lead, H)),
                      sf=(sf, (f32,), (T, H // 128)), out_sf=(out_sf, (f32,), (*lead, H // 128)), m_indices=(m_indices, (i32,), (Mt,)))
-        raise ValueError("sf and out_sf go with e4m3 rows, and with them only")
+        if codes == (sf is None) or codes == (out_sf is None):
+            raise ValueError("sf and out_sf go with e4m3 rows, and with them only")
+        _refuse_device(dev)
     st = (_lib or load()).dg_moe_gather(x.data_ptr(), None if sf is None else sf.data_ptr(), 2 if codes else 0, rows.data_ptr(),
                                         None if m_indices is None else m_indices.data_ptr(), out.data_ptr(), None if out_sf is None else out_sf.data_ptr(),
-                                        T, k, H, Mt, _here(stream, dev))
+                                        T, k, H, Mt, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
     if st:
         raise DGError(st, "dg_moe_gather")
     return out
@@ -639,11 +655,14 @@ def dg_moe_combine(y, rows, out, weights=None, residual=None, stream=None):
     Mt = y.shape[:-1].numel()
     TH = (T, H)
     dev = y.get_device()
-    if not (y.dtype is bf16 and y.is_contiguous() and dev >= 0 and _fits(rows, i32, Tk, dev) and _fits(out, bf16, TH, dev)
-            and (weights is None or _fits(weights, f32, Tk, dev)) and (residual is None or _fits(residual, bf16, TH, dev))):
+    if not (y.dtype is bf16 and y.is_contiguous() and dev >= 0 and rows.dtype is i32 and rows.get_device() == dev and rows.is_contiguous()
+            and out.dtype is bf16 and out.shape == TH and out.get_device() == dev and out.is_contiguous()
+            and (weights is None or _fits(weights, f32, Tk, dev)) and (residual is None or _fits(residual, bf16, TH, dev))
+            and torch._C._cuda_getDevice() == dev):
         _refuse_here(dev, y=(y, (bf16,), None), rows=(rows, (i32,), None), out=(out, (bf16,), TH), weights=(weights, (f32,), Tk), residual=(residual, (bf16,), TH))
+        _refuse_device(dev)
     st = (_lib or load()).dg_moe_combine(y.data_ptr(), rows.data_ptr(), None if weights is None else weights.data_ptr(),
-                                         None if residual is None else residual.data_ptr(), out.data_ptr(), T, k, H, Mt, _here(stream, dev))
+                                         None if residual is None else residual.data_ptr(), out.data_ptr(), T, k, H, Mt, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
     if st:
         raise DGError(st, "dg_moe_combine")
     return out
@@ -665,13 +684,15 @@ def dg_moe_combine_backward(dout, rows, dy, weights=None, y=None, dweights=None,
     dev = dout.get_device()
     if not (_fits(dout, bf16, (T, H), dev) and dev >= 0 and _fits(rows, i32, Tk, dev) and (dy is None or _fits(dy, bf16, MH, dev))
             and (weights is None or _fits(weights, f32, Tk, dev)) and (y is None or _fits(y, bf16, MH, dev))
-            and (dweights is None or _fits(dweights, f32, Tk, dev)) and (m_indices is None or _fits(m_indices, i32, (Mt,), dev))):
+            and (dweights is None or _fits(dweights, f32, Tk, dev)) and (m_indices is None or _fits(m_indices, i32, (Mt,), dev))
+            and torch._C._cuda_getDevice() == dev):
         _refuse_here(dev, dout=(dout, (bf16,), (T, H)), rows=(rows, (i32,), None), dy=(dy, (bf16,), MH), weights=(weights, (f32,), Tk), y=(y, (bf16,), MH),
                      dweights=(dweights, (f32,), Tk), m_indices=(m_indices, (i32,), (Mt,)))
+        _refuse_device(dev)
     st = (_lib or load()).dg_moe_combine_backward(
         dout.data_ptr(), None if y is None else y.data_ptr(), rows.data_ptr(), None if weights is None else weights.data_ptr(),
         None if m_indices is None else m_indices.data_ptr(), None if dy is None else dy.data_ptr(), None if dweights is None else dweights.data_ptr(),
-        T, k, H, Mt, _here(stream, dev))
+        T, k, H, Mt, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
     if st:
         raise DGError(st, "dg_moe_combine_backward")
 
@@ -685,15 +706,20 @@ def dg_rmsnorm(x, weight, y=None, q=None, sf=None, residual=None, sum=None, eps=
     TH = T, H = x.shape
     dev = x.get_device()
     kind = weight.dtype
-    if not (x.dtype is bf16 and x.is_contiguous() and dev >= 0 and (kind is f32 or kind is bf16) and _fits(weight, kind, (H,), dev)
-            and (residual is None or _fits(residual, bf16, TH, dev)) and (sum is None or _fits(sum, bf16, TH, dev)) and (y is None or _fits(y, bf16, TH, dev))
+    if not (x.dtype is bf16 and x.is_contiguous() and dev >= 0 and (kind is f32 or kind is bf16) and weight.shape == (H,) and weight.get_device() == dev
+            and weight.is_contiguous()
+            and (residual is None or (residual.dtype is bf16 and residual.shape == TH and residual.get_device() == dev and residual.is_contiguous()))
+            and (sum is None or (sum.dtype is bf16 and sum.shape == TH and sum.get_device() == dev and sum.is_contiguous()))
+            and (y is None or (y.dtype is bf16 and y.shape == TH and y.get_device() == dev and y.is_contiguous()))
             and (q is None or (q.dtype in e4m3 and q.shape == TH and q.get_device() == dev and q.is_contiguous()))
-            and (sf is None or _fits(sf, f32, (T, H // 128), dev))):
+            and (sf is None or (sf.dtype is f32 and sf.shape == (T, H // 128) and sf.get_device() == dev and sf.is_contiguous()))
+            and torch._C._cuda_getDevice() == dev):
         _refuse_here(dev, x=(x, (bf16,), None), weight=(weight, (bf16, f32), (H,)), residual=(residual, (bf16,), TH), sum=(sum, (bf16,), TH),
                      y=(y, (bf16,), TH), q=(q, e4m3, TH), sf=(sf, (f32,), (T, H // 128)))
+        _refuse_device(dev)
     st = (_lib or load()).dg_rmsnorm(x.data_ptr(), None if residual is None else residual.data_ptr(), weight.data_ptr(), 1 if kind is f32 else 0,
                                      None if sum is None else sum.data_ptr(), None if y is None else y.data_ptr(), None if q is None else q.data_ptr(),
-                                     None if sf is None else sf.data_ptr(), 1 if pow2 else 0, T, H, eps, _here(stream, dev))
+                                     None if sf is None else sf.data_ptr(), 1 if pow2 else 0, T, H, eps, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
     if st:
         raise DGError(st, "dg_rmsnorm")
 
@@ -717,12 +743,13 @@ def dg_rmsnorm_backward(dy, x, weight, dx, dweight=None, workspace=None, dsum=No
     kind = weight.dtype
     if not (x.dtype is bf16 and x.is_contiguous() and dev >= 0 and (kind is f32 or kind is bf16) and _fits(weight, kind, (H,), dev)
             and _fits(dy, bf16, TH, dev) and _fits(dx, bf16, TH, dev) and (dweight is None or _fits(dweight, f32, (H,), dev))
-            and (dsum is None or _fits(dsum, bf16, TH, dev))):
+            and (dsum is None or _fits(dsum, bf16, TH, dev)) and torch._C._cuda_getDevice() == dev):
         _refuse_here(dev, x=(x, (bf16,), None), weight=(weight, (bf16, f32), (H,)), dy=(dy, (bf16,), TH), dx=(dx, (bf16,), TH),
                      dweight=(dweight, (f32,), (H,)), dsum=(dsum, (bf16,), TH))
-    ws, size = _bytes(workspace, "workspace")
+        _refuse_device(dev)
+    ws, size = _workspace_here(workspace, dev)
     st = (_lib or load()).dg_rmsnorm_backward(dy.data_ptr(), x.data_ptr(), weight.data_ptr(), 1 if kind is f32 else 0, None if dsum is None else dsum.data_ptr(),
-                                              dx.data_ptr(), None if dweight is None else dweight.data_ptr(), ws, size, T, H, eps, _here(stream, dev))
+                                              dx.data_ptr(), None if dweight is None else dweight.data_ptr(), ws, size, T, H, eps, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
     if st:
         raise DGError(st, "dg_rmsnorm_backward")
     return dx
@@ -741,16 +768,19 @@ def dg_glu(Z, q, sf, kept=None, kept_sf=None, m_indices=None, masked_m=None, act
     dev = Z.get_device()
     MI, MI2, sMI, sMI2 = (*lead, I), (*lead, I2), (*lead, I // 128), (*lead, I2 // 128)
     if not (Z.dtype is bf16 and Z.is_contiguous() and dev >= 0 and I2 % 2 == 0 and q.dtype in e4m3 and q.shape == MI and q.get_device() == dev
-            and q.is_contiguous() and _fits(sf, f32, sMI, dev)
+            and q.is_contiguous() and sf.dtype is f32 and sf.shape == sMI and sf.get_device() == dev and sf.is_contiguous()
             and (kept is None or (kept.dtype in e4m3 and kept.shape == MI2 and kept.get_device() == dev and kept.is_contiguous()))
             and (kept_sf is None or _fits(kept_sf, f32, sMI2, dev)) and (m_indices is None or _fits(m_indices, i32, (M,), dev))
-            and (masked_m is None or (_fits(masked_m, i32, (G,), dev) and (len(lead) != 2 or lead[0] == G)))):
+            and (masked_m is None or (_fits(masked_m, i32, (G,), dev) and (len(lead) != 2 or lead[0] == G)))
+            and torch._C._cuda_getDevice() == dev):
         _refuse_here(dev, Z=(Z, (bf16,), None), q=(q, e4m3, MI), sf=(sf, (f32,), sMI), kept=(kept, e4m3, MI2), kept_sf=(kept_sf, (f32,), sMI2),
                      m_indices=(m_indices, (i32,), (M,)), masked_m=(masked_m, (i32,), (lead[0],) if len(lead) == 2 else None))
-        raise ValueError(f"Z must have an even number of columns, got {I2}")
+        if I2 % 2:
+            raise ValueError(f"Z must have an even number of columns, got {I2}")
+        _refuse_device(dev)
     st = (_lib or load()).dg_glu(Z.data_ptr(), q.data_ptr(), sf.data_ptr(), None if kept is None else kept.data_ptr(),
                                  None if kept_sf is None else kept_sf.data_ptr(), None if m_indices is None else m_indices.data_ptr(),
-                                 None if masked_m is None else masked_m.data_ptr(), G, _choice(ACTIVATIONS, act, "act"), 1 if pow2 else 0, M, I, _here(stream, dev))
+                                 None if masked_m is None else masked_m.data_ptr(), G, _choice(ACTIVATIONS, act, "act"), 1 if pow2 else 0, M, I, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
     if st:
         raise DGError(st, "dg_glu")
     return q
@@ -776,13 +806,14 @@ def dg_glu_backward(dH, q, sf, qt, sft, ht, hsft, Z=None, kept=None, kept_sf=Non
         raise ValueError("one of Z and kept has to be given")
     if not (_fits(dH, bf16, MI, dev) and dev >= 0 and (Z is None or _fits(Z, bf16, (M, 2 * I), dev)) and codes(kept, (M, 2 * I)) and scales(kept_sf, (M, 2 * I // 128))
             and codes(q, (M, 2 * I)) and scales(sf, (M, 2 * I // 128)) and codes(qt, (2 * I, Mp)) and scales(sft, (2 * I, Mp // 128))
-            and codes(ht, (I, Mp)) and scales(hsft, (I, Mp // 128))):
+            and codes(ht, (I, Mp)) and scales(hsft, (I, Mp // 128)) and torch._C._cuda_getDevice() == dev):
         _refuse_here(dev, dH=(dH, (bf16,), None), Z=(Z, (bf16,), (M, 2 * I)), kept=(kept, e4m3, (M, 2 * I)), kept_sf=(kept_sf, (f32,), (M, 2 * I // 128)),
                      q=(q, e4m3, (M, 2 * I)), sf=(sf, (f32,), (M, 2 * I // 128)), qt=(qt, e4m3, (2 * I, Mp)), sft=(sft, (f32,), (2 * I, Mp // 128)),
                      ht=(ht, e4m3, (I, Mp)), hsft=(hsft, (f32,), (I, Mp // 128)))
+        _refuse_device(dev)
     p = _ptr
     st = (_lib or load()).dg_glu_backward(dH.data_ptr(), p(Z), p(kept), p(kept_sf), _choice(ACTIVATIONS, act, "act"), p(q), p(sf), p(qt), p(sft), p(ht), p(hsft), M, I,
-                                          _here(stream, dev))
+                                          torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
     if st:
         raise DGError(st, "dg_glu_backward")
 
@@ -795,10 +826,13 @@ def dg_transpose_fp8(q, sf, qt, sft, stream=None):
     M, N = q.shape
     Mp = (M + 127) // 128 * 128
     dev = q.get_device()
-    if not (q.dtype in e4m3 and q.is_contiguous() and dev >= 0 and _fits(sf, f32, (M, N // 128), dev) and qt.dtype in e4m3 and qt.shape == (N, Mp)
-            and qt.get_device() == dev and qt.is_contiguous() and _fits(sft, f32, (N, Mp // 128), dev)):
+    if not (q.dtype in e4m3 and q.is_contiguous() and dev >= 0 and sf.dtype is f32 and sf.shape == (M, N // 128) and sf.get_device() == dev
+            and sf.is_contiguous() and qt.dtype in e4m3 and qt.shape == (N, Mp) and qt.get_device() == dev and qt.is_contiguous()
+            and sft.dtype is f32 and sft.shape == (N, Mp // 128) and sft.get_device() == dev and sft.is_contiguous()
+            and torch._C._cuda_getDevice() == dev):
         _refuse_here(dev, q=(q, e4m3, None), sf=(sf, (f32,), (M, N // 128)), qt=(qt, e4m3, (N, Mp)), sft=(sft, (f32,), (N, Mp // 128)))
-    st = (_lib or load()).dg_transpose_fp8(q.data_ptr(), sf.data_ptr(), qt.data_ptr(), sft.data_ptr(), M, N, _here(stream, dev))
+        _refuse_device(dev)
+    st = (_lib or load()).dg_transpose_fp8(q.data_ptr(), sf.data_ptr(), qt.data_ptr(), sft.data_ptr(), M, N, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
     if st:
         raise DGError(st, "dg_transpose_fp8")
     return qt
