@@ -262,7 +262,7 @@ int64_t dg_moe_layer_workspace(int T, int k, int E, int H, int I);
  *   last expert's block: a caller that knows the counts may pass later calls that many rows.
  * Masked (dg_m_grouped_masked): expert e from row e * max_m on. Slots past max_m get no row (-1) and masked_m still counts
  *   them; the product and dg_glu take no more than max_m.
- * 1 <= E <= 1024, k <= 32, T * k <= 2^23, E * max_m < 2^31.
+ * 1 <= E <= 1024, k <= 32, T * k <= 2^23, E * max_m < 2^31. No output overlaps ids.
  * workspace: device memory of dg_moe_sort_workspace(T, k, E) bytes, 16-byte aligned, with anything in it; 0 bytes (and null)
  * up to 16384 slots. dg_moe_sort_rows and dg_moe_sort_workspace return -1 for sizes outside these.
  */
@@ -281,7 +281,8 @@ int64_t dg_moe_sort_workspace(int T, int k, int E);
  *   m_indices [Mt] of the contiguous layout, or null. With it the rows without a token in a block of 128 that has some are
  *   zeros (of scale 1e-4 / 448), so that a weight gradient over the padded segments adds nothing for them. All other rows
  *   stay as they were. Mt is then a multiple of 128.
- * x and out 16-byte aligned, k <= 32. Its gradient is dg_moe_combine without weights.
+ * x and out 16-byte aligned and apart, k <= 32, about T * H / 256 + Mt < 2^31 (as in the next two calls). Its gradient is
+ * dg_moe_combine without weights.
  */
 dg_status dg_moe_gather(const void* x, const float* sf, int x_type, const int32_t* rows, const int32_t* m_indices, void* out, float* out_sf,
                         int T, int k, int H, int Mt, cudaStream_t stream);
@@ -289,7 +290,8 @@ dg_status dg_moe_gather(const void* x, const float* sf, int x_type, const int32_
 /*
  * The way back: out[t] = residual[t] + sum_j weights[t,j] * y[rows[t,j]], over the slots whose row is in [0, Mt).
  *   y [Mt, H] bf16, weights [T, k] fp32 or null (1), residual [T, H] bf16 or null, may be out; out [T, H] bf16
- * FP32 sums in the order of j, the residual last, rounded once. H a multiple of 8, k <= 32; y, residual and out 16-byte aligned.
+ * FP32 sums in the order of j, the residual last, rounded once. H a multiple of 8, k <= 32; y, residual and out 16-byte aligned;
+ * out must not overlap y.
  */
 dg_status dg_moe_combine(const void* y, const int32_t* rows, const float* weights, const void* residual, void* out, int T, int k,
                          int H, int Mt, cudaStream_t stream);
@@ -299,7 +301,7 @@ dg_status dg_moe_combine(const void* y, const int32_t* rows, const float* weight
  *   dy       [Mt, H] bf16, or null: dy[rows[t,j]] = weights[t,j] * dout[t]; with m_indices zeros as in dg_moe_gather, other
  *            rows as they were
  *   dweights [T, k] fp32, or null: the product of y[rows[t,j]] and dout[t], 0 for a slot without a row. Needs y.
- * weights null: 1. H a multiple of 8, k <= 32; dout, y and dy 16-byte aligned; dy must not overlap y.
+ * weights null: 1. H a multiple of 8, k <= 32; dout, y and dy 16-byte aligned; dy must not overlap y or dout.
  */
 dg_status dg_moe_combine_backward(const void* dout, const void* y, const int32_t* rows, const float* weights, const int32_t* m_indices, void* dy,
                                   float* dweights, int T, int k, int H, int Mt, cudaStream_t stream);
@@ -313,7 +315,8 @@ dg_status dg_moe_combine_backward(const void* dout, const void* y, const int32_t
  *   q   [T, H] e4m3, sf [T, H/128] fp32, or both null: y quantised (before its rounding to BF16) as in
  *       dg_epilogue_backward; with pow2 the scale is the power of two above that scale, as the UE8M0 path takes it.
  *       H a multiple of 128 then.
- * Sums are FP32. H a multiple of 8 up to 16384, eps >= 0; weight and the matrices 16-byte aligned.
+ * Sums are FP32 (a row whose squares pass their range, from about 1e19 on, comes out as zeros). H a multiple of 8 up to 16384,
+ * eps >= 0; weight and the matrices 16-byte aligned.
  */
 dg_status dg_rmsnorm(const void* x, const void* residual, const void* weight, int weight_type, void* sum, void* y, uint8_t* q, float* sf,
                      int pow2, int T, int H, float eps, cudaStream_t stream);
@@ -335,8 +338,10 @@ int64_t dg_rmsnorm_backward_workspace(int T, int H);
  * The gated activation between the two products of an expert (or of a dense layer), quantised for the second:
  *   h = act(g) * u,   (g; u) = Z's columns [0, I) and [I, 2I)
  *   Z    [M, 2I] bf16
- *   q    [M, I] e4m3, sf [M, I/128]: h before any rounding; pow2 as in dg_rmsnorm
- *   kept [M, 2I] e4m3, kept_sf [M, 2I/128], or both null: Z quantised, what dg_glu_backward takes instead of Z
+ *   q    [M, I] e4m3, sf [M, I/128]: h in FP32, quantised as in dg_epilogue_backward, but that a code may be that of a
+ *        quotient a last place of FP32 away; pow2 as in dg_rmsnorm
+ *   kept [M, 2I] e4m3, kept_sf [M, 2I/128], or both null: Z quantised as in dg_epilogue_backward, what dg_glu_backward takes
+ *        instead of Z
  * At most one of (which rows are computed; all others stay as they were):
  *   m_indices [M] of the contiguous layout: the blocks of 128 rows whose first row has an expert. M a multiple of 128 then.
  *   masked_m  [G] of the masked layout [G, M/G, 2I]: the first masked_m[g] rows of each group, at most M/G
@@ -351,8 +356,8 @@ dg_status dg_glu(const void* Z, uint8_t* q, float* sf, uint8_t* kept, float* kep
  *   q  [M, 2I] e4m3,   sf  [M, 2I/128]    (dg; du), 1x128 scales along 2I: A of the product that gives the input's gradient
  *   qt [2I, Mp] e4m3,  sft [2I, Mp/128]   the transpose, 1x128 scales along M, Mp = M rounded up to 128, zeros past M
  *   ht [I, Mp] e4m3,   hsft [I, Mp/128]   h's transpose, so quantised: an operand of the second product's weight gradient
- * q with sf, qt with sft, ht with hsft may each be null. The values are those of Z, or of the codes times their scales; every
- * row is computed. I a multiple of 128, M free; matrices 16-byte aligned.
+ * q with sf, qt with sft, ht with hsft may each be null. The values are those of Z, or of the codes times their scales in FP32,
+ * the codes are made as dg_glu's; every row is computed. I a multiple of 128, M free; matrices 16-byte aligned.
  */
 dg_status dg_glu_backward(const void* dH, const void* Z, const uint8_t* kept, const float* kept_sf, int act, uint8_t* q, float* sf, uint8_t* qt,
                           float* sft, uint8_t* ht, float* hsft, int M, int I, cudaStream_t stream);
@@ -361,7 +366,8 @@ dg_status dg_glu_backward(const void* dH, const void* Z, const uint8_t* kept, co
  * The values of 8-bit codes quantised along the other axis: from q [M, N] e4m3 with sf [M, N/128], what a forward product
  * read, to qt [N, Mp] with sft [N, Mp/128] (Mp = M rounded up to 128, zeros past M), an operand of dg_wgrad_fp8_nt or
  * dg_k_grouped_wgrad: the 8-bit codes are all that has to be kept of an activation for its weight gradient. The value of a
- * code is its product with its scale, rounded to FP32. N a multiple of 128, M free; q and qt 16-byte aligned.
+ * code is its product with its scale, rounded to FP32, and quantised as in dg_epilogue_backward. N a multiple of 128, M free;
+ * q and qt 16-byte aligned and apart.
  */
 dg_status dg_transpose_fp8(const uint8_t* q, const float* sf, uint8_t* qt, float* sft, int M, int N, cudaStream_t stream);
 

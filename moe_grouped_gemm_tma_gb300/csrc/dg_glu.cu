@@ -88,7 +88,7 @@ __device__ __forceinline__ uint2 line_codes(const float2 (&v)[4], const BlockSca
 // magnitudes of all its lines (h's, with KEEP g's and u's) are found together, and each line's scale is made by one lane. A warp
 // takes piece after piece, and the next one's values come by asynchronous copies into places that only their lane reads: with
 // loads into registers 36.8 k rows of 2 x 2048 took 94.4 us (two rows a lane, 8 CTAs an SM) with codes kept and 58.9 without, so
-// they take 81.6 and 55.5, the memory's time (6.5 and 6.8 TB/s).
+// they take 86.1 (6.2 TB/s) and 56.7 (6.7).
 template <int ACT, bool KEEP>
 __global__ void __launch_bounds__(32 * GLU_WARPS, glu_ctas(KEEP)) glu_kernel(const GluParams p) {
     constexpr int R = GLU_LANE_ROWS, LINES = KEEP ? 4 * R : R, SHARE = 16 / LINES;
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(32 * GLU_WARPS, glu_ctas(KEEP)) glu_kernel(con
                 most[3 * R + i] = 0.f;
             }
 #pragma unroll
-            for (int c = 0; c < 4; ++c) h[i][c] = __fmul2_rn(act_value2<ACT>(g[c]), u[c]);
+            for (int c = 0; c < 4; ++c) h[i][c] = __fmul2_rn(act_fine2<ACT>(g[c]), u[c]);
             most[i] = abs_max8(h[i]);
         }
         const uint32_t bits = abs_bits(line_maxima(most, l16));
@@ -424,7 +424,7 @@ cudaError_t launch_glu(const GluParams& p, int act, int sms, cudaStream_t stream
 template <int ACT, bool KEPT>
 cudaError_t launch_backward_as(const GluBackwardParams& p, int sms, cudaStream_t stream) {
     constexpr int BYTES = sizeof(GluBackwardShared<KEPT>);
-    const cudaError_t e = cudaFuncSetAttribute(glu_backward_kernel<ACT, KEPT>, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES);
+    const cudaError_t e = allow_smem<glu_backward_kernel<ACT, KEPT>>(BYTES);
     if (e != cudaSuccess) return e;
     const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
     return launch_overlapped_smem(glu_backward_kernel<ACT, KEPT>, dim3(static_cast<unsigned>(tiles < sms ? tiles : sms)), dim3(GB_THREADS), BYTES, stream, p);

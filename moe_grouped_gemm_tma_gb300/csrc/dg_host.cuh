@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "dg.h"
@@ -54,6 +55,21 @@ cudaError_t launch_overlapped_smem(void (*kernel)(P...), dim3 grid, dim3 block, 
     cfg.attrs = attr;
     cfg.numAttrs = tune(DG_TUNE_PDL) != 0 ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
+// Lets a kernel have `bytes` of dynamic shared memory on the current device (asked for once per kernel and device; `bytes`
+// is the most that it is ever launched with).
+template <auto KERNEL>
+cudaError_t allow_smem(int bytes) {
+    static std::atomic<bool> done[kMaxDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    if (done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done[dev].store(true, std::memory_order_relaxed);
+    return e;
 }
 
 template <typename... P, typename... A>

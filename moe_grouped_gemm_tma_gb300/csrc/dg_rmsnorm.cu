@@ -10,6 +10,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <climits>
+
 #include "dg.h"
 #include "dg_host.cuh"
 #include "dg_ptx.cuh"
@@ -23,6 +25,7 @@ constexpr int NORM_VECTORS = 4;                   // vectors of 8 values a threa
 constexpr int NORM_MAX_WARPS = 16;
 constexpr int NORM_MAX_H = NORM_MAX_WARPS * 32 * NORM_VECTORS * 8;
 constexpr int NORM_WARP_H = 32 * NORM_VECTORS * 8;   // rows up to this are a warp's
+constexpr int NORM_MAX_T = INT32_MAX - 65536;     // (rows are numbered in 32 bits, a few thousand past the last too)
 constexpr int NORM_ROWS = 4;                      // rows of a CTA then
 
 struct NormParams {
@@ -304,23 +307,24 @@ cudaError_t launch_norm(const NormParams& p, int H, cudaStream_t stream) {
     return go(rmsnorm_kernel<W, false, 1>, false);
 }
 
+template <typename W, bool ROW_CTA, int N>
+cudaError_t launch_norm_backward_as(const NormBackwardParams& p, int H, cudaStream_t stream) {
+    constexpr auto kernel = rmsnorm_backward_kernel<W, ROW_CTA, N>;
+    constexpr int STAGE = 3 * N * 16 * (ROW_CTA ? 32 * NORM_MAX_WARPS : 32 * NORM_ROWS);      // of the largest CTA
+    const unsigned grid = static_cast<unsigned>(ROW_CTA ? p.groups : cdiv(p.groups, NORM_ROWS));
+    const unsigned block = static_cast<unsigned>(ROW_CTA ? 32 * cdiv(H, 32 * 8 * N) : 32 * NORM_ROWS);
+    const cudaError_t e = allow_smem<kernel>(NORM_STAGES * STAGE);
+    if (e != cudaSuccess) return e;
+    return launch_overlapped_smem(kernel, dim3(grid), dim3(block), static_cast<size_t>(NORM_STAGES) * (p.dsum != nullptr ? 3 : 2) * N * block * 16, stream, p);
+}
+
 template <typename W>
 cudaError_t launch_norm_backward(const NormBackwardParams& p, int H, cudaStream_t stream) {
-    const auto go = [&](auto kernel, bool cta, int vectors) {
-        const unsigned grid = static_cast<unsigned>(cta ? p.groups : cdiv(p.groups, NORM_ROWS));
-        const unsigned block = static_cast<unsigned>(cta ? 32 * cdiv(H, 32 * 8 * vectors) : 32 * NORM_ROWS);
-        const size_t bytes = static_cast<size_t>(NORM_STAGES) * (p.dsum != nullptr ? 3 : 2) * vectors * block * 16;
-        if (bytes > 40 * 1024) {             // (more than every kernel may have without asking, less what is static)
-            const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
-            if (e != cudaSuccess) return e;
-        }
-        return launch_overlapped_smem(kernel, dim3(grid), dim3(block), bytes, stream, p);
-    };
-    if (H > NORM_MAX_H / 2) return go(rmsnorm_backward_kernel<W, true, 4>, true, 4);
-    if (H > NORM_WARP_H) return go(rmsnorm_backward_kernel<W, true, 2>, true, 2);
-    if (H > 512) return go(rmsnorm_backward_kernel<W, false, 4>, false, 4);
-    if (H > 256) return go(rmsnorm_backward_kernel<W, false, 2>, false, 2);
-    return go(rmsnorm_backward_kernel<W, false, 1>, false, 1);
+    if (H > NORM_MAX_H / 2) return launch_norm_backward_as<W, true, 4>(p, H, stream);
+    if (H > NORM_WARP_H) return launch_norm_backward_as<W, true, 2>(p, H, stream);
+    if (H > 512) return launch_norm_backward_as<W, false, 4>(p, H, stream);
+    if (H > 256) return launch_norm_backward_as<W, false, 2>(p, H, stream);
+    return launch_norm_backward_as<W, false, 1>(p, H, stream);
 }
 
 // Groups of rows of the gradient: about what fits the GPU at once, by the sizes alone, so that sums do not depend on the GPU.
@@ -332,7 +336,7 @@ int norm_groups(int T, int H) {
 dg_status norm_check(int weight_type, int T, int H, float eps) {
     if (T < 0 || H < 0 || !(eps >= 0.f)) return DG_INVALID_ARG;
     if (weight_type != DG_TYPE_BF16 && weight_type != DG_TYPE_F32) return DG_INVALID_ARG;
-    if (H % 8 != 0 || H > NORM_MAX_H) return DG_UNSUPPORTED_SHAPE;
+    if (H % 8 != 0 || H > NORM_MAX_H || T > NORM_MAX_T) return DG_UNSUPPORTED_SHAPE;
     return DG_OK;
 }
 
@@ -374,7 +378,7 @@ dg_status dg_rmsnorm(const void* x, const void* residual, const void* weight, in
 }
 
 int64_t dg_rmsnorm_backward_workspace(int T, int H) {
-    if (T < 0 || H < 0 || H % 8 != 0 || H > NORM_MAX_H) return -1;
+    if (T < 0 || H < 0 || H % 8 != 0 || H > NORM_MAX_H || T > NORM_MAX_T) return -1;
     return static_cast<int64_t>(norm_groups(T, H)) * H * 4;
 }
 

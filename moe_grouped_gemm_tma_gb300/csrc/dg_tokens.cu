@@ -571,11 +571,11 @@ dg_status sort(const int32_t* ids, int32_t* rows, int32_t* counts, int32_t* m_in
     return e == cudaSuccess ? DG_OK : DG_CUDA_ERROR;
 }
 
-// Common checks of the calls that move rows: sizes, and that items of 32 bits number them.
+// Common checks of the calls that move rows: sizes, and that 32 bits number the warps' pieces, a few past the last too.
 dg_status rows_check(const int32_t* rows, int T, int k, int H, int Mt, int granule) {
     if (T < 0 || k < 0 || H < 0 || Mt < 0) return DG_INVALID_ARG;
     if (k > MAX_ROUTE_K || H % granule != 0) return DG_UNSUPPORTED_SHAPE;
-    if (static_cast<int64_t>(T) * cdiv(H, 256) + Mt > INT32_MAX) return DG_UNSUPPORTED_SHAPE;
+    if (static_cast<int64_t>(T) * (1 + H / 256) + Mt > INT32_MAX - 65536) return DG_UNSUPPORTED_SHAPE;
     if (static_cast<int64_t>(T) * k > 0 && !rows) return DG_INVALID_ARG;
     return aligned(rows, 4) ? DG_OK : DG_MISALIGNED;
 }

@@ -73,7 +73,7 @@ def test_gather_refusals():
     for name in ("T", "k", "H", "Mt"):
         assert call(**{name: -1}) == INVALID, name
     assert call(k=33) == SHAPE and call(H=200) == SHAPE and call(H=204, **bf16) == SHAPE and call(Mt=200) == SHAPE
-    assert call(T=1 << 30, H=1 << 16) == SHAPE
+    assert call(T=1 << 30, H=1 << 16) == SHAPE and call(T=2 ** 31 - 1, H=128) == SHAPE and call(Mt=2 ** 31 - 128) == SHAPE
     for name in ("x", "sf", "rows", "out", "osf"):
         assert call(**{name: None}) == INVALID, name
     assert call(type=0) == INVALID and call(type=0, sf=None) == INVALID          # scales go with codes
@@ -89,7 +89,7 @@ def test_combine_refusals():
     call = calls(dg.load().dg_moe_combine, base)
     for name in ("T", "k", "H", "Mt"):
         assert call(**{name: -1}) == INVALID, name
-    assert call(k=33) == SHAPE and call(H=100) == SHAPE
+    assert call(k=33) == SHAPE and call(H=100) == SHAPE and call(T=2 ** 31 - 1, H=8) == SHAPE
     for name in ("y", "rows", "out"):
         assert call(**{name: None}) == INVALID, name
     for name in ("y", "res", "out"):
@@ -101,7 +101,7 @@ def test_combine_refusals():
     call = calls(dg.load().dg_moe_combine_backward, base)
     for name in ("T", "k", "H", "Mt"):
         assert call(**{name: -1}) == INVALID, name
-    assert call(k=33) == SHAPE and call(H=100) == SHAPE and call(Mt=200) == SHAPE
+    assert call(k=33) == SHAPE and call(H=100) == SHAPE and call(Mt=200) == SHAPE and call(T=2 ** 31 - 1, H=8) == SHAPE
     for name in ("dout", "y", "rows"):
         assert call(**{name: None}) == INVALID, name
     for name in ("dout", "y", "dy"):
@@ -118,7 +118,7 @@ def test_rmsnorm_refusals():
     assert call(T=-1) == INVALID and call(H=-8) == INVALID and call(type=2) == INVALID and call(type=-1) == INVALID
     assert call(eps=-1.0) == INVALID and call(eps=float("nan")) == INVALID
     assert call(q=None) == INVALID and call(sf=None) == INVALID
-    assert call(H=100) == SHAPE and call(H=16392) == SHAPE and call(H=200) == SHAPE
+    assert call(H=100) == SHAPE and call(H=16392) == SHAPE and call(H=200) == SHAPE and call(T=2 ** 31 - 1) == SHAPE
     assert call(x=None) == INVALID and call(w=None) == INVALID
     for name in ("x", "res", "w", "sum", "y", "q"):
         assert call(**{name: ODD8}) == MISALIGNED, name
@@ -127,7 +127,7 @@ def test_rmsnorm_refusals():
     base = dict(dy=OK, x=OK, w=OK, type=1, dsum=OK, dx=OK, dw=OK, ws=OK, size=1 << 30, T=4, H=256, eps=1e-6)
     call = calls(L.dg_rmsnorm_backward, base)
     assert call(T=-1) == INVALID and call(H=-8) == INVALID and call(type=2) == INVALID and call(eps=-1.0) == INVALID
-    assert call(H=100) == SHAPE and call(H=16392) == SHAPE
+    assert call(H=100) == SHAPE and call(H=16392) == SHAPE and call(T=2 ** 31 - 1) == SHAPE
     for name in ("dy", "x", "w", "dx"):
         assert call(**{name: None}) == INVALID, name
     assert call(ws=None) == INVALID and call(size=4 * 256 * 4 - 1) == INVALID
@@ -147,7 +147,7 @@ def test_glu_refusals():
     call = calls(L.dg_glu, base)
     assert call(M=-1) == INVALID and call(I=-1) == INVALID and call(G=-1) == INVALID and call(act=5) == INVALID and call(act=-1) == INVALID
     assert call(kept=None) == INVALID and call(ksf=None) == INVALID and call(mi=OK, mm=OK) == INVALID
-    assert call(I=200) == SHAPE and call(mi=OK, M=200) == SHAPE
+    assert call(I=200) == SHAPE and call(mi=OK, M=200) == SHAPE and call(M=2 ** 31 - 1) == SHAPE and call(M=2 ** 30, I=1 << 20) == SHAPE
     assert call(mm=OK, G=0) == INVALID and call(mm=OK, G=3) == INVALID
     for name in ("Z", "q", "sf"):
         assert call(**{name: None}) == INVALID, name
@@ -161,7 +161,7 @@ def test_glu_refusals():
     for name in ("sf", "q", "sft", "qt", "hsft", "ht", "dH", "Z"):
         assert call(**{name: None}) == INVALID, name
     assert call(kept=OK) == INVALID and call(kept=OK, ksf=OK) == INVALID and call(ksf=OK) == INVALID      # one of Z and the codes
-    assert call(I=200) == SHAPE
+    assert call(I=200) == SHAPE and call(M=2 ** 31 - 1) == SHAPE and call(M=2 ** 30, I=1 << 22) == SHAPE
     for name in ("dH", "Z", "q", "qt", "ht"):
         assert call(**{name: ODD8}) == MISALIGNED, name
     assert call(Z=None, kept=ODD8, ksf=OK) == MISALIGNED and call(Z=None, kept=OK, ksf=ODD2) == MISALIGNED
@@ -173,6 +173,7 @@ def test_glu_refusals():
 def test_transpose_refusals():
     call = calls(dg.load().dg_transpose_fp8, dict(q=OK, sf=OK, qt=OK, sft=OK, M=256, N=256))
     assert call(M=-1) == INVALID and call(N=-1) == INVALID and call(N=200) == SHAPE
+    assert call(M=2 ** 31 - 1) == SHAPE and call(M=2 ** 30, N=1 << 22) == SHAPE
     for name in ("q", "sf", "qt", "sft"):
         assert call(**{name: None}) == INVALID, name
     assert call(q=ODD8) == MISALIGNED and call(qt=ODD8) == MISALIGNED and call(sf=ODD2) == MISALIGNED and call(sft=ODD2) == MISALIGNED
