@@ -228,7 +228,7 @@ struct GluBackwardParams {
     int m_tiles, n_tiles;
 };
 
-constexpr int GB_ROWS = 4;                        // rows of a warp
+constexpr int GB_ROWS = 8;                        // rows of a warp
 constexpr int GB_THREADS = 32 * TILE / GB_ROWS;
 template <bool KEPT>
 struct GluBackwardShared {
@@ -253,8 +253,8 @@ __global__ void __launch_bounds__(GB_THREADS, 1) glu_backward_kernel(const GluBa
     const auto fetch = [&](const TileWalk& at) {
         const int t = threadIdx.x, m0 = at.outer * TILE, n0 = at.inner * TILE;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = i * 64 + t / 16;
+        for (int i = 0; i < TILE * 16 / GB_THREADS; ++i) {
+            const int r = i * (GB_THREADS / 16) + t / 16;
             const size_t row = m0 + r;
             const bool there = m0 + r < p.m;
             cp_async_16_or_zero(&s.dh[r][t % 16 * 2], there && p.dh != nullptr ? p.dh + row * inner + n0 + t % 16 * 8 : p.any, there && p.dh != nullptr);
@@ -265,12 +265,15 @@ __global__ void __launch_bounds__(GB_THREADS, 1) glu_backward_kernel(const GluBa
             }
         }
         if (KEPT) {
-            const int r = t / 8;
-            const size_t row = m0 + r;
-            const bool there = m0 + r < p.m;
-            const uint8_t* src = there ? p.kept + row * (2 * inner) + n0 + t % 8 * 16 : static_cast<const uint8_t*>(p.any);
-            cp_async_16_or_zero(&s.g[r][t % 8 * 4], src, there);
-            cp_async_16_or_zero(&s.u[r][t % 8 * 4], there ? src + inner : src, there);
+#pragma unroll
+            for (int i = 0; i < TILE * 8 / GB_THREADS; ++i) {
+                const int r = i * (GB_THREADS / 8) + t / 8;
+                const size_t row = m0 + r;
+                const bool there = m0 + r < p.m;
+                const uint8_t* src = there ? p.kept + row * (2 * inner) + n0 + t % 8 * 16 : static_cast<const uint8_t*>(p.any);
+                cp_async_16_or_zero(&s.g[r][t % 8 * 4], src, there);
+                cp_async_16_or_zero(&s.u[r][t % 8 * 4], there ? src + inner : src, there);
+            }
             if (t < 2 * TILE) {
                 const int which = t / TILE, rs = t % TILE;
                 if (m0 + rs < p.m) cp_async_4(&s.scale[which][rs], p.kept_sf + static_cast<size_t>(m0 + rs) * (2 * blocks) + which * blocks + at.inner);
@@ -354,8 +357,10 @@ struct TransposeParams {
 };
 
 // Tiles of 128 rows and 64 columns, four CTAs an SM: its three barriers a tile leave a CTA's warps waiting together, which more
-// and smaller CTAs fill (128 columns and two CTAs took 106.8 us for 32768 x 7168). A CTA takes every gridDim.x-th tile; the next
-// one's codes are asked for as soon as this one's are in use.
+// and smaller CTAs fill (32768 x 7168: 99.3 us, with 128 columns and two CTAs 102.5, with 32 and eight 117.6). A CTA takes every
+// gridDim.x-th tile; the next one's codes are asked for as soon as this one's are in use (two tiles ahead into shared memory
+// was no faster: 98.3, and slower at 4096 x 7168). What bounds it is instruction issue between the barriers: 300 instructions a
+// warp for 32 x 32 codes, a fifth of them their way to FP32, at 56% of the slots. The copies alone, in the same pieces, take 82 us.
 constexpr int TR_ROWS = 8;                        // rows of a half warp
 constexpr int TR_COLUMNS = 64;
 constexpr int TR_CTAS = 4;

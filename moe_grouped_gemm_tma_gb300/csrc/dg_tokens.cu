@@ -436,7 +436,7 @@ constexpr int CB_VECTORS = 4;                     // a lane's vectors at a time
 
 // WIDE: a CTA a token; else a warp a token. A lane keeps its piece of dout while it goes through the token's experts; the
 // products with their rows are added up over the lanes, and over the warps in order. What bounds it is memory, half of it
-// written: 4096 tokens of 8 x 7168 take 172.6 us, 6.1 TB/s.
+// written: 4096 tokens of 8 x 7168 take 168 us, 6.3 TB/s.
 template <bool WIDE>
 __global__ void __launch_bounds__(32 * (WIDE ? CB_WARPS : CB_NARROW)) combine_backward_kernel(const CombineBackwardParams p) {
     __shared__ float s_dot[CB_WARPS][32];
@@ -707,11 +707,11 @@ dg_status dg_moe_combine_backward(const void* dout, const void* y, const int32_t
     p.k = k;
     p.vectors = H / 8;
     p.Mt = Mt;
-    // Two warps a token where there are many (4096 tokens of 8 x 7168: 172.6 us, with 1, 4 and 7 warps 178.8, 178.6 and 181.6; of
-    // 8192 tokens of 2 x 7168 113.7, with 4 and 7 122 and 129), as many as have a piece where there are few (16 tokens: 39 us with
-    // two, 29 with four). The order of the sums goes by the sizes alone.
+    // Few tokens get as many warps each as they have pieces for, up to eight (256 tokens of 8 x 7168: 37.7 us, with four 39.9, with two
+    // 46.0); many get four, or two where a token has few experts, whose sums' end weighs more (4096 of 8: 168 us, with eight and two
+    // 181 and 176; 8192 of 2: 107 with two, 116 with four, 129 with eight). The order of the sums goes by the sizes alone.
     const bool wide = H > 32 * CB_VECTORS * 8;
-    const int most = T >= 1024 ? 2 : CB_WARPS, pieces = cdiv(p.vectors, 32 * CB_VECTORS);
+    const int most = T < 512 ? CB_WARPS : k > 4 ? 4 : 2, pieces = cdiv(p.vectors, 32 * CB_VECTORS);
     const int warps = !wide ? CB_NARROW : pieces < most ? pieces : most;
     p.token_ctas = !slots ? 0u : (wide ? static_cast<unsigned>(T) : static_cast<unsigned>(cdiv(T, CB_NARROW)));
     p.pads = pads ? static_cast<unsigned>(Mt / PAD_ROWS) : 0u;
