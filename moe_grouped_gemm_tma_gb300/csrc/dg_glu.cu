@@ -6,7 +6,8 @@
 //   dg = dh u act'(g),  du = dh act(g): Q(dg; du) along rows and along columns, Q(h) along columns
 //
 // Forward: a half warp has the 128 values of a scaling block of 4 rows, 8 columns a lane, and both halves of Z's rows there.
-// Backward and transposition: tiles of 128 x 128 (dg_tile.cuh).
+// Backward and transposition: tiles of 128 rows (dg_tile.cuh). All three are memory's by their bytes; the backward pass and the
+// transposition are held up by instructions and barriers.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -238,9 +239,14 @@ struct GluBackwardShared {
     __align__(16) float scale[2][TILE];           // of g's and u's codes
 };
 
-// A CTA makes all three outputs of a tile, so that what they share is computed once: 48 values a thread, which is what the
-// registers hold with one CTA an SM. Its barriers are hidden by nothing else, therefore: the next tile's inputs come while
-// this one's are in use, and the rows' codes are made while some warps make the columns' scales.
+// A CTA makes all three outputs of a tile, so that what they share is computed once: 96 values a thread, which is what the
+// registers hold with one CTA of 512 threads an SM. Its barriers are hidden by nothing else, therefore: the next tile's
+// inputs come while this one's are in use, and the rows' codes are made while some warps make the columns' scales.
+//
+// Floor: 9.25 bytes an element of dH from codes, 45.6 us for 16384 x 2048. It takes 78.5 us (SILU; GELU 87.6, its tanh form 81.6;
+// from BF16 79.2): 47 instructions an element at 52% of the issue slots. A CTA for each of the three outputs took 153 us, 1024
+// threads with 4 rows a lane 84.1, inputs by loads into registers 85.0 and without a prefetch 115; codes by rounded quotients
+// and the slopes and values by forms of their own cost 28 us more than by the reciprocal and one sigmoid.
 template <int ACT, bool KEPT>
 __global__ void __launch_bounds__(GB_THREADS, 1) glu_backward_kernel(const GluBackwardParams p) {
     extern __shared__ __align__(16) uint8_t s_raw[];
@@ -356,38 +362,41 @@ struct TransposeParams {
     int m_tiles, n_tiles;
 };
 
-// Tiles of 128 rows and 64 columns, four CTAs an SM: its three barriers a tile leave a CTA's warps waiting together, which more
-// and smaller CTAs fill (32768 x 7168: 99.3 us, with 128 columns and two CTAs 102.5, with 32 and eight 117.6). A CTA takes every
-// gridDim.x-th tile; the next one's codes are asked for as soon as this one's are in use (two tiles ahead into shared memory
-// was no faster: 98.3, and slower at 4096 x 7168). What bounds it is instruction issue between the barriers: 300 instructions a
-// warp for 32 x 32 codes, a fifth of them their way to FP32, at 56% of the slots. The copies alone, in the same pieces, take 82 us.
-constexpr int TR_ROWS = 8;                        // rows of a half warp
+// Tiles of 128 rows and 64 columns, 16 rows a lane, four CTAs of 128 threads an SM: three barriers a tile leave a CTA's warps
+// waiting together, which more and smaller CTAs fill, and what a lane does once a tile is spread over more codes. 32768 x 7168
+// takes 93.2 us (5.2 TB/s); with 128 columns and two CTAs 95.3, with 8 rows a lane 99.3 (128 columns 102.5, 32 columns 117.6). A CTA
+// takes every gridDim.x-th tile; the next one's codes are asked for as soon as this one's are in use (two tiles ahead into
+// shared memory was no faster). What bounds it is instruction issue between the barriers, a fifth of it the codes' way to
+// FP32, and the pieces: copies of as many bytes in the same pieces take 82 us.
+constexpr int TR_ROWS = 16;                       // rows of a half warp
 constexpr int TR_COLUMNS = 64;
 constexpr int TR_CTAS = 4;
 using TransposeTile = TileColumns<TR_ROWS, true, TR_COLUMNS>;
+static_assert(TR_ROWS <= TR_COLUMNS / 4, "a lane loads the scale of one of its group's rows");
 
 __global__ void __launch_bounds__(TransposeTile::THREADS, TR_CTAS) transpose_kernel(const TransposeParams p) {
     __shared__ TransposeTile s;
     grid_dependency_wait();
     grid_launch_dependents();
-    const int group = static_cast<int>(threadIdx.x) / 16, l16 = static_cast<int>(threadIdx.x) % 16;
+    constexpr int LANES = TR_COLUMNS / 4;         // of a group of rows
+    const int group = static_cast<int>(threadIdx.x) / LANES, lane = static_cast<int>(threadIdx.x) % LANES;
     const int64_t n = p.n, blocks = n / TILE, pitch = static_cast<int64_t>(p.m_tiles) * TILE;
     uint32_t codes[TR_ROWS];
-    float scale = 0.f;                            // the first 8 lanes of each half: of its rows
+    float scale = 0.f;                            // of the group's row `lane`
     TileWalk walk(p.m_tiles, p.n_tiles);
-    const uint8_t* q = p.q + group * TR_ROWS * n + l16 * 4;
-    const float* sf = p.sf + (group * TR_ROWS + l16) * blocks;
+    const uint8_t* q = p.q + group * TR_ROWS * n + lane * 4;
+    const float* sf = p.sf + (group * TR_ROWS + lane) * blocks;
     TileOffset from(walk, TILE * n, TR_COLUMNS), to(walk, TILE, TR_COLUMNS * pitch), scales(walk, 1, static_cast<int64_t>(TR_COLUMNS) * p.m_tiles);
     const auto load = [&]() {
         const int valid = p.m - walk.outer * TILE - group * TR_ROWS;
         const uint8_t* src = q + from.at;
         const float* ssf = sf + (walk.outer * TILE * blocks + walk.inner * TR_COLUMNS / TILE);
         if (valid >= TR_ROWS) {
-            if (l16 < TR_ROWS) scale = ld_input(ssf);
+            if (lane < TR_ROWS) scale = ld_input(ssf);
 #pragma unroll
             for (int i = 0; i < TR_ROWS; ++i, src += n) codes[i] = ld_input(reinterpret_cast<const uint32_t*>(src));
         } else {
-            scale = l16 < TR_ROWS && l16 < valid ? ld_input(ssf) : 0.f;
+            scale = lane < TR_ROWS && lane < valid ? ld_input(ssf) : 0.f;
 #pragma unroll
             for (int i = 0; i < TR_ROWS; ++i, src += n) codes[i] = i < valid ? ld_input(reinterpret_cast<const uint32_t*>(src)) : 0u;
         }
@@ -396,17 +405,17 @@ __global__ void __launch_bounds__(TransposeTile::THREADS, TR_CTAS) transpose_ker
     for (bool more = walk.more(); more;) {
         float2 v[TR_ROWS][2];
 #pragma unroll
-        for (int i = 0; i < TR_ROWS; ++i) code_values(codes[i], __shfl_sync(FULL, scale, i, 16), v[i]);
+        for (int i = 0; i < TR_ROWS; ++i) code_values(codes[i], __shfl_sync(FULL, scale, i, LANES), v[i]);
         const bool wrapped = walk.next();
         from.next(wrapped);
         more = walk.more();
         if (more) load();
-        s.maxima(v, group, l16);
+        s.maxima(v, group, lane);
         __syncthreads();
         if (threadIdx.x < TR_COLUMNS) s.scale(threadIdx.x, p.sft + scales.at + static_cast<int>(threadIdx.x) * p.m_tiles);
         scales.next(wrapped);
         __syncthreads();
-        s.quantise(v, group, l16);
+        s.quantise(v, group, lane);
         __syncthreads();
         s.store(p.qt + to.at, pitch);
         to.next(wrapped);

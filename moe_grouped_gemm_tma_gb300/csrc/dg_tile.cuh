@@ -111,7 +111,10 @@ struct TileColumns {
                 hi[i / 4] = pack_e4m3x2(w[0].y, w[1].y) | (pack_e4m3x2(w[2].y, w[3].y) << 16);
             }
             uint32_t* dst = codes + (lane * 4 + 2 * x) * 32 + slot * (R / 4);
-            if constexpr (R == 8) {
+            if constexpr (R == 16) {
+                *reinterpret_cast<uint4*>(dst) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                *reinterpret_cast<uint4*>(dst + 32) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            } else if constexpr (R == 8) {
                 *reinterpret_cast<uint2*>(dst) = make_uint2(lo[0], lo[1]);
                 *reinterpret_cast<uint2*>(dst + 32) = make_uint2(hi[0], hi[1]);
             } else {
@@ -130,7 +133,8 @@ struct TileColumns {
 #pragma unroll
         for (int i = 0; i < COLUMNS / PASS; ++i, dst += PASS * pitch) {
             const int at = i * PASS * 32 + (l ^ (c0 >> 2) ^ (i * (PASS / 4) & (GROUPS - 1))) * (R / 4);      // (c0 >> 2 is below PASS / 4)
-            if constexpr (R == 8) *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(src + at);
+            if constexpr (R == 16) *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(src + at);
+            else if constexpr (R == 8) *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(src + at);
             else *reinterpret_cast<uint32_t*>(dst) = src[at];
         }
     }

@@ -6,10 +6,11 @@
 // Sort. A counting sort by expert that keeps the slots' order, so that its result does not depend on timing: a warp takes
 // consecutive slots, 32 at a time; ballots over the bits of the expert give each lane the others with its own, whose number
 // below it is its place among the 32. Up to SORT_ALONE slots are sorted by one launch, whose CTAs each count all slots and
-// place 512 of them; more are cut into chunks, whose counts a first launch writes, a second adds up and a third uses.
+// place 512 of them; more are cut into chunks, whose counts a first launch writes, a second adds up and a third uses. It is
+// bound by the latency of its steps: 512 slots of 256 experts take 4.3 us in a CUDA graph, 65512 7.2, 262144 17.
 //
-// The rows are moved token by token: a token's row is read once, however many experts it goes to, and every access is a
-// piece of 512 bytes of a row a warp. Rows without a token inside an expert's block of 128 are zeroed by warps of their own.
+// The rows are moved token by token: a token's row is read once, however many experts it goes to. Rows without a token inside an
+// expert's block of 128 are zeroed by warps of their own.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -273,7 +274,9 @@ struct GatherParams {
 };
 
 // A warp has a piece of a token's row in shared memory, from where lane j has it copied to the row of slot j: the copies
-// are what the kernel is about, and each is one instruction, whatever its length.
+// are what the kernel is about, and each is one instruction, whatever its length. What bounds it is memory, nearly all written:
+// 8189 tokens of 7168 codes to 8 experts each, with the zeros, take 107.8 us (6.2 TB/s; a memset of the 702 MB that they lie in takes 173),
+// by 16-byte stores of the lanes 112.
 constexpr int GATHER_VECTORS = 256;               // a piece: 4096 bytes, with 32 scales of codes
 
 __global__ void __launch_bounds__(32 * MOVE_WARPS) gather_kernel(const GatherParams p) {
