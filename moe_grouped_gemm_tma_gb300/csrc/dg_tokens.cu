@@ -550,7 +550,7 @@ dg_status sort(const int32_t* ids, int32_t* rows, int32_t* counts, int32_t* m_in
     p.counts = counts;
     p.m_indices = Mt > 0 ? m_indices : nullptr;
     p.totals = static_cast<int32_t*>(workspace);
-    p.chunk_counts = p.totals + E;
+    p.chunk_counts = need > 0 ? p.totals + E : nullptr;
     p.slots = T * k;
     p.experts = E;
     p.blocks = Mt / 128;
