@@ -30,6 +30,7 @@ constexpr int NORM_MAX_H = NORM_MAX_WARPS * 32 * NORM_VECTORS * 8;
 constexpr int NORM_WARP_H = 32 * NORM_VECTORS * 8;   // rows up to this are a warp's
 constexpr int NORM_MAX_T = INT32_MAX - 65536;     // (rows are numbered in 32 bits, a few thousand past the last too)
 constexpr int NORM_ROWS = 4;                      // rows of a CTA then
+constexpr int NORM_BACK_ROWS = 8;                 // ... and of the gradient's
 
 struct NormParams {
     const uint4* x;
@@ -170,25 +171,25 @@ struct NormBackwardParams {
     const void* weight;
     const uint4* dsum;
     uint4* dx;
-    float* partial;                               // [groups][H] weight gradients of a group's rows
-    int rows, vectors, groups;
+    float* partial;                               // [ctas][H] weight gradients of a CTA's rows
+    int rows, vectors, ctas;
     float inverse, eps;
 };
 
-// A group (a CTA, or a warp) takes every groups-th row and keeps its columns' weight gradient in registers. The rows come
+// A group (a CTA, or a warp of 8 in a CTA) takes every groups-th row and keeps its columns' weight gradient in registers. The rows come
 // by asynchronous copies into shared memory, NORM_STAGES rows ahead, each thread's vectors to places of its own, so that no
 // thread waits for another's copies; the row's two sums cost the only barrier. (By loads into registers, 8192 x 7168 took 118 us.)
 constexpr int NORM_STAGES = 2;
 
 template <typename W, bool ROW_CTA, int N>
-__global__ void __launch_bounds__(ROW_CTA ? 32 * NORM_MAX_WARPS : 32 * NORM_ROWS, ROW_CTA ? (N == 4 ? 1 : 2) : (N == 4 ? 5 : 8)) rmsnorm_backward_kernel(const NormBackwardParams p) {
+__global__ void __launch_bounds__(ROW_CTA ? 32 * NORM_MAX_WARPS : 32 * NORM_BACK_ROWS, ROW_CTA ? (N == 4 ? 1 : 2) : (N == 4 ? 2 : 4)) rmsnorm_backward_kernel(const NormBackwardParams p) {
     extern __shared__ __align__(16) uint4 s_rows[];   // [stage][x, dy, dsum][N][thread]
     __shared__ float2 s_part[2][NORM_MAX_WARPS];
     grid_dependency_wait();
     grid_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int group = static_cast<int>(ROW_CTA ? blockIdx.x : blockIdx.x * NORM_ROWS + warp);
-    if (!ROW_CTA && group >= p.groups) return;
+    const int group = static_cast<int>(ROW_CTA ? blockIdx.x : blockIdx.x * NORM_BACK_ROWS + warp);
+    const int groups = static_cast<int>(ROW_CTA ? gridDim.x : gridDim.x * NORM_BACK_ROWS);
     const int first = ROW_CTA ? threadIdx.x : lane, step = ROW_CTA ? blockDim.x : 32;
     const int threads = blockDim.x, arrays = p.dsum != nullptr ? 3 : 2;
     uint4* mine = s_rows + threadIdx.x;
@@ -209,7 +210,7 @@ __global__ void __launch_bounds__(ROW_CTA ? 32 * NORM_MAX_WARPS : 32 * NORM_ROWS
         cp_async_commit();
     };
 #pragma unroll
-    for (int i = 0; i < NORM_STAGES; ++i) fetch(group + i * p.groups, i);     // (groups * stages is far below 2^31 - rows)
+    for (int i = 0; i < NORM_STAGES; ++i) fetch(group + i * groups, i);
 
     float2 g[N][4], dg[N][4];
 #pragma unroll
@@ -219,7 +220,7 @@ __global__ void __launch_bounds__(ROW_CTA ? 32 * NORM_MAX_WARPS : 32 * NORM_ROWS
         if (first + i * step < p.vectors) load_weights<W>(p.weight, first + i * step, g[i]);
     }
     int turn = 0, stage = 0;
-    for (int row = group; row < p.rows; row += p.groups, turn ^= 1, stage = stage + 1 == NORM_STAGES ? 0 : stage + 1) {
+    for (int row = group; row < p.rows; row += groups, turn ^= 1, stage = stage + 1 == NORM_STAGES ? 0 : stage + 1) {
         const size_t base = static_cast<size_t>(row) * p.vectors;
         cp_async_wait_group<NORM_STAGES - 1>();
         float2 squares = make_float2(0.f, 0.f), products = make_float2(0.f, 0.f);
@@ -260,16 +261,40 @@ __global__ void __launch_bounds__(ROW_CTA ? 32 * NORM_MAX_WARPS : 32 * NORM_ROWS
             }
             p.dx[base + v] = pack_bf16(z);
         }
-        fetch(row + NORM_STAGES * p.groups, stage);
+        fetch(row + NORM_STAGES * groups, stage);
     }
     if (p.partial == nullptr) return;
+    if (!ROW_CTA) {
+        // the warps' sums, in order, by way of the rows' places
+        cp_async_wait_all();
+        __syncthreads();
+        float4* s_sums = reinterpret_cast<float4*>(s_rows);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int v = first + i * step;
-        if (v < p.vectors) {
-            float4* dst = reinterpret_cast<float4*>(p.partial + (static_cast<size_t>(group) * p.vectors + v) * 8);
-            __stcg(dst, make_float4(dg[i][0].x, dg[i][0].y, dg[i][1].x, dg[i][1].y));
-            __stcg(dst + 1, make_float4(dg[i][2].x, dg[i][2].y, dg[i][3].x, dg[i][3].y));
+        for (int i = 0; i < N; ++i) {
+            if (first + i * step >= p.vectors) break;
+            float4* dst = s_sums + (warp * p.vectors + first + i * step) * 2;
+            dst[0] = make_float4(dg[i][0].x, dg[i][0].y, dg[i][1].x, dg[i][1].y);
+            dst[1] = make_float4(dg[i][2].x, dg[i][2].y, dg[i][3].x, dg[i][3].y);
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < 2 * p.vectors; i += threads) {
+            float4 a = s_sums[i];
+#pragma unroll
+            for (int w = 1; w < NORM_BACK_ROWS; ++w) {
+                const float4 b = s_sums[w * 2 * p.vectors + i];
+                a = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+            }
+            __stcg(reinterpret_cast<float4*>(p.partial) + static_cast<size_t>(blockIdx.x) * 2 * p.vectors + i, a);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int v = first + i * step;
+            if (v < p.vectors) {
+                float4* dst = reinterpret_cast<float4*>(p.partial + (static_cast<size_t>(group) * p.vectors + v) * 8);
+                __stcg(dst, make_float4(dg[i][0].x, dg[i][0].y, dg[i][1].x, dg[i][1].y));
+                __stcg(dst + 1, make_float4(dg[i][2].x, dg[i][2].y, dg[i][3].x, dg[i][3].y));
+            }
         }
     }
 }
@@ -313,9 +338,9 @@ cudaError_t launch_norm(const NormParams& p, int H, cudaStream_t stream) {
 template <typename W, bool ROW_CTA, int N>
 cudaError_t launch_norm_backward_as(const NormBackwardParams& p, int H, cudaStream_t stream) {
     constexpr auto kernel = rmsnorm_backward_kernel<W, ROW_CTA, N>;
-    constexpr int STAGE = 3 * N * 16 * (ROW_CTA ? 32 * NORM_MAX_WARPS : 32 * NORM_ROWS);      // of the largest CTA
-    const unsigned grid = static_cast<unsigned>(ROW_CTA ? p.groups : cdiv(p.groups, NORM_ROWS));
-    const unsigned block = static_cast<unsigned>(ROW_CTA ? 32 * cdiv(H, 32 * 8 * N) : 32 * NORM_ROWS);
+    constexpr int STAGE = 3 * N * 16 * (ROW_CTA ? 32 * NORM_MAX_WARPS : 32 * NORM_BACK_ROWS);      // of the largest CTA
+    const unsigned grid = static_cast<unsigned>(p.ctas);
+    const unsigned block = static_cast<unsigned>(ROW_CTA ? 32 * cdiv(H, 32 * 8 * N) : 32 * NORM_BACK_ROWS);
     const cudaError_t e = allow_smem<kernel>(NORM_STAGES * STAGE);
     if (e != cudaSuccess) return e;
     return launch_overlapped_smem(kernel, dim3(grid), dim3(block), static_cast<size_t>(NORM_STAGES) * (p.dsum != nullptr ? 3 : 2) * N * block * 16, stream, p);
@@ -330,10 +355,16 @@ cudaError_t launch_norm_backward(const NormBackwardParams& p, int H, cudaStream_
     return launch_norm_backward_as<W, false, 1>(p, H, stream);
 }
 
-// Groups of rows of the gradient: about what fits the GPU at once, by the sizes alone, so that sums do not depend on the GPU.
-int norm_groups(int T, int H) {
-    const int most = H > 4096 ? 304 : H > 2048 ? 608 : 1216;
-    return T < most ? T : most;
+// CTAs of the gradient: about what fits the GPU at once, but rather one an SM than fewer than 8 rows for a CTA (4 for a warp),
+// whose sums would be as many as its rows (900 x 3792: 9.4 us, with a row or two for each of 608 CTAs 15.2). By the sizes alone, so that
+// sums do not depend on the GPU.
+int norm_ctas(int T, int H) {
+    const bool warp_rows = H <= NORM_WARP_H;
+    const int most = warp_rows ? 304 : H <= 4096 ? 608 : H <= NORM_MAX_H / 2 ? 304 : 152;
+    const int one = warp_rows ? cdiv(T, NORM_BACK_ROWS) : T;      // a row a warp, or a CTA
+    const int few = warp_rows ? cdiv(T, 4 * NORM_BACK_ROWS) : cdiv(T, 8);
+    const int least = one < 152 ? one : 152;
+    return few > most ? most : few > least ? few : least;
 }
 
 dg_status norm_check(int weight_type, int T, int H, float eps) {
@@ -382,7 +413,7 @@ dg_status dg_rmsnorm(const void* x, const void* residual, const void* weight, in
 
 int64_t dg_rmsnorm_backward_workspace(int T, int H) {
     if (T < 0 || H < 0 || H % 8 != 0 || H > NORM_MAX_H || T > NORM_MAX_T) return -1;
-    return static_cast<int64_t>(norm_groups(T, H)) * H * 4;
+    return static_cast<int64_t>(norm_ctas(T, H)) * H * 4;
 }
 
 dg_status dg_rmsnorm_backward(const void* dy, const void* x, const void* weight, int weight_type, const void* dsum, void* dx, float* dweight,
@@ -408,12 +439,12 @@ dg_status dg_rmsnorm_backward(const void* dy, const void* x, const void* weight,
     p.partial = dweight ? static_cast<float*>(workspace) : nullptr;
     p.rows = T;
     p.vectors = H / 8;
-    p.groups = norm_groups(T, H);
+    p.ctas = norm_ctas(T, H);
     p.inverse = 1.f / static_cast<float>(H);
     p.eps = eps;
     cudaError_t e = weight_type == DG_TYPE_F32 ? launch_norm_backward<float>(p, H, stream) : launch_norm_backward<__nv_bfloat16>(p, H, stream);
     if (e == cudaSuccess && dweight)
-        e = launch_overlapped(add_groups_kernel, dim3(static_cast<unsigned>(cdiv(H, 32))), dim3(32 * ADD_WARPS), stream, static_cast<const float*>(p.partial), dweight, H, p.groups);
+        e = launch_overlapped(add_groups_kernel, dim3(static_cast<unsigned>(cdiv(H, 32))), dim3(32 * ADD_WARPS), stream, static_cast<const float*>(p.partial), dweight, H, p.ctas);
     return e == cudaSuccess ? DG_OK : DG_CUDA_ERROR;
 }
 

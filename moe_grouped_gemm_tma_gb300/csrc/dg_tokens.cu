@@ -243,23 +243,24 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_scan_kernel(int32_t* totals
 }
 
 // ------------------------------------------------------------------------------------ rows
-constexpr int MOVE_WARPS = 8;
-constexpr int PAD_ROWS = 8;                       // rows that a warp looks at for zeros
+constexpr int MOVE_WARPS = 8;                     // of a CTA of the weighted sum
+constexpr int GATHER_WARPS = 2;                   // ... and of the gather, which the copies out of an SM limit where there are few
+
+// Rows that a warp looks at for zeros, a power of two: fewer the longer they are. (With 8 for every length and 8 warps a CTA, 45
+// tokens of 6528 codes to 5 of 6 experts took 11.5 us with their sort instead of 4.9, 8189 of 7168 to 8 of 256 115.6 instead of 105.2;
+// with 2 for every length 8189 of 1024 took 38.8 instead of 24.2.)
+int pad_rows(int64_t row_bytes) { return row_bytes <= 2048 ? 8 : row_bytes <= 4096 ? 4 : 2; }
 
 __device__ __forceinline__ int slot_row(const int32_t* rows, size_t at, int Mt) {
     const int r = ld_input(rows + at);
     return static_cast<unsigned>(r) < static_cast<unsigned>(Mt) ? r : -1;
 }
 
-// Zeros in the rows without a token of a block that has some: the item's PAD_ROWS rows.
-__device__ __forceinline__ void zero_pads(unsigned item, const int32_t* m_indices, uint4* out, int vectors, int lane) {
-    const unsigned block = item / (128 / PAD_ROWS), first = item * PAD_ROWS;
-    if (ld_input(m_indices + static_cast<size_t>(block) * 128) < 0) return;
-    const bool pad = lane < PAD_ROWS && ld_input(m_indices + first + lane) < 0;
-    for (unsigned which = __ballot_sync(FULL, pad); which; which &= which - 1) {
-        const size_t row = first + __ffs(which) - 1;
-        for (int v = lane; v < vectors; v += 32) out[row * vectors + v] = make_uint4(0, 0, 0, 0);
-    }
+// The rows without a token of a block that has some, as bits, of the item's `rows`.
+__device__ __forceinline__ unsigned pads_of(unsigned item, int rows, const int32_t* m_indices, int lane) {
+    const unsigned first = item * rows;
+    if (ld_input(m_indices + first / 128 * 128) < 0) return 0;
+    return __ballot_sync(FULL, lane < rows && ld_input(m_indices + first + (lane & (rows - 1))) < 0);
 }
 
 struct GatherParams {
@@ -269,38 +270,33 @@ struct GatherParams {
     const int32_t* m_indices;
     uint4* out;
     float* out_sf;
-    int k, vectors, scales, Mt, pieces;           // 16-byte vectors, scales and pieces of a row
+    int k, vectors, scales, Mt, pieces, pad_rows; // 16-byte vectors, scales and pieces of a row
     unsigned tokens_items, items;
 };
 
 // A warp has a piece of a token's row in shared memory, from where lane j has it copied to the row of slot j: the copies
 // are what the kernel is about, and each is one instruction, whatever its length. What bounds it is memory, nearly all written:
-// 8189 tokens of 7168 codes to 8 experts each, with the zeros, take 107.8 us (6.2 TB/s; a memset of the 702 MB that they lie in takes 173),
-// by 16-byte stores of the lanes 112.
+// 8189 tokens of 7168 codes to 8 experts each, with the zeros, take 98 us without their sort (6.8 TB/s; a memset of the 702 MB that they lie in takes 173).
 constexpr int GATHER_VECTORS = 256;               // a piece: 4096 bytes, with 32 scales of codes
 
-__global__ void __launch_bounds__(32 * MOVE_WARPS) gather_kernel(const GatherParams p) {
-    __shared__ __align__(128) uint4 s_piece[MOVE_WARPS][GATHER_VECTORS];
+__global__ void __launch_bounds__(32 * GATHER_WARPS) gather_kernel(const GatherParams p) {
+    __shared__ __align__(128) uint4 s_piece[GATHER_WARPS][GATHER_VECTORS];
     grid_dependency_wait();
     grid_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const unsigned item = blockIdx.x * MOVE_WARPS + warp;
+    const unsigned item = blockIdx.x * GATHER_WARPS + warp;
     if (item >= p.items) return;
     uint4* piece = s_piece[warp];
     if (item >= p.tokens_items) {
-        // the rows without a token of 8 rows of a block that has some
-        const unsigned first = (item - p.tokens_items) * PAD_ROWS;
-        if (ld_input(p.m_indices + first / 128 * 128) < 0) return;
-        const unsigned pads = __ballot_sync(FULL, lane < PAD_ROWS && ld_input(p.m_indices + first + lane % PAD_ROWS) < 0);
+        const unsigned first = (item - p.tokens_items) * p.pad_rows, pads = pads_of(item - p.tokens_items, p.pad_rows, p.m_indices, lane);
         if (pads == 0) return;
 #pragma unroll
         for (int i = 0; i < GATHER_VECTORS / 32; ++i) piece[i * 32 + lane] = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
         __syncwarp();
-        for (int i = lane; i < PAD_ROWS * p.pieces; i += 32) {
-            const int at = i / PAD_ROWS * GATHER_VECTORS, left = p.vectors - at;
-            if (pads >> (i % PAD_ROWS) & 1)
-                bulk_store(p.out + static_cast<size_t>(first + i % PAD_ROWS) * p.vectors + at, piece, 16u * static_cast<uint32_t>(left < GATHER_VECTORS ? left : GATHER_VECTORS));
+        for (int i = lane; i < p.pad_rows * p.pieces; i += 32) {
+            const int r = i & (p.pad_rows - 1), at = i / p.pad_rows * GATHER_VECTORS, left = p.vectors - at;
+            if (pads >> r & 1) bulk_store(p.out + static_cast<size_t>(first + r) * p.vectors + at, piece, 16u * static_cast<uint32_t>(left < GATHER_VECTORS ? left : GATHER_VECTORS));
         }
         bulk_commit();
         if (p.out_sf != nullptr) {
@@ -429,7 +425,7 @@ struct CombineBackwardParams {
     const int32_t* m_indices;
     uint4* dy;
     float* dweights;
-    int T, k, vectors, Mt;
+    int T, k, vectors, Mt, pad_rows;
     unsigned token_ctas, pads;
 };
 
@@ -448,7 +444,11 @@ __global__ void __launch_bounds__(32 * (WIDE ? CB_WARPS : CB_NARROW)) combine_ba
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x / 32;
     if (blockIdx.x >= p.token_ctas) {
         const unsigned item = (blockIdx.x - p.token_ctas) * warps + warp;
-        if (item < p.pads) zero_pads(item, p.m_indices, p.dy, p.vectors, lane);
+        if (item >= p.pads) return;
+        for (unsigned which = pads_of(item, p.pad_rows, p.m_indices, lane); which; which &= which - 1) {
+            uint4* row = p.dy + (static_cast<size_t>(item) * p.pad_rows + __ffs(which) - 1) * p.vectors;
+            for (int v = lane; v < p.vectors; v += 32) row[v] = make_uint4(0, 0, 0, 0);
+        }
         return;
     }
     const int t = static_cast<int>(WIDE ? blockIdx.x : blockIdx.x * CB_NARROW + warp);
@@ -654,8 +654,9 @@ dg_status dg_moe_gather(const void* x, const float* sf, int x_type, const int32_
     p.Mt = Mt;
     p.pieces = cdiv(p.vectors, GATHER_VECTORS);
     p.tokens_items = k > 0 ? static_cast<unsigned>(T) * static_cast<unsigned>(p.pieces) : 0u;
-    p.items = p.tokens_items + (m_indices ? static_cast<unsigned>(Mt / PAD_ROWS) : 0u);
-    const cudaError_t e = launch_overlapped(gather_kernel, dim3((p.items + MOVE_WARPS - 1) / MOVE_WARPS), dim3(32 * MOVE_WARPS), stream, p);
+    p.pad_rows = pad_rows(16 * static_cast<int64_t>(p.vectors));
+    p.items = p.tokens_items + (m_indices ? static_cast<unsigned>(Mt / p.pad_rows) : 0u);
+    const cudaError_t e = launch_overlapped(gather_kernel, dim3((p.items + GATHER_WARPS - 1) / GATHER_WARPS), dim3(32 * GATHER_WARPS), stream, p);
     return e == cudaSuccess ? DG_OK : DG_CUDA_ERROR;
 }
 
@@ -717,7 +718,8 @@ dg_status dg_moe_combine_backward(const void* dout, const void* y, const int32_t
     const int most = T < 512 ? CB_WARPS : k > 4 ? 4 : 2, pieces = cdiv(p.vectors, 32 * CB_VECTORS);
     const int warps = !wide ? CB_NARROW : pieces < most ? pieces : most;
     p.token_ctas = !slots ? 0u : (wide ? static_cast<unsigned>(T) : static_cast<unsigned>(cdiv(T, CB_NARROW)));
-    p.pads = pads ? static_cast<unsigned>(Mt / PAD_ROWS) : 0u;
+    p.pad_rows = pad_rows(16 * static_cast<int64_t>(p.vectors));
+    p.pads = pads ? static_cast<unsigned>(Mt / p.pad_rows) : 0u;
     const dim3 grid(p.token_ctas + static_cast<unsigned>(cdiv(p.pads, warps))), block(32u * static_cast<unsigned>(warps));
     const cudaError_t e = launch_overlapped(wide ? combine_backward_kernel<true> : combine_backward_kernel<false>, grid, block, stream, p);
     return e == cudaSuccess ? DG_OK : DG_CUDA_ERROR;

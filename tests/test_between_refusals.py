@@ -130,13 +130,16 @@ def test_rmsnorm_refusals():
     assert call(H=100) == SHAPE and call(H=16392) == SHAPE and call(T=2 ** 31 - 1) == SHAPE
     for name in ("dy", "x", "w", "dx"):
         assert call(**{name: None}) == INVALID, name
-    assert call(ws=None) == INVALID and call(size=4 * 256 * 4 - 1) == INVALID
+    assert call(ws=None) == INVALID and call(size=256 * 4 - 1) == INVALID and call(T=9, size=2 * 256 * 4 - 1) == INVALID
     for name in ("dy", "x", "w", "dsum", "dx", "ws"):
         assert call(**{name: ODD8}) == MISALIGNED, name
     assert call(dw=ODD2) == MISALIGNED
     assert call(H=0) == 0 and call(T=0, dw=None) == 0
-    assert L.dg_rmsnorm_backward_workspace(4, 256) == 4 * 256 * 4 and L.dg_rmsnorm_backward_workspace(1, 100) == -1
+    assert L.dg_rmsnorm_backward_workspace(4, 256) == 256 * 4 and L.dg_rmsnorm_backward_workspace(4, 2048) == 4 * 2048 * 4 and L.dg_rmsnorm_backward_workspace(1, 100) == -1
     assert L.dg_rmsnorm_backward_workspace(1 << 20, 7168) == 304 * 7168 * 4 and L.dg_rmsnorm_backward_workspace(1, 16392) == -1
+    for H in (8, 1024, 1032, 2048, 4096, 7168, 16384):
+        sizes = [L.dg_rmsnorm_backward_workspace(T, H) for T in range(0, 9000)]
+        assert sizes == sorted(sizes)              # one for many rows serves fewer
     with pytest.raises(dg.DGError):
         dg.rmsnorm_backward_workspace(1, 100)
 

@@ -126,15 +126,15 @@ def check_backward(dy, s, w, dsum, eps, dx, dw):
     mag = r * (d * wd).abs() + sd.abs() * r ** 3 * (d * wd * sd).abs().mean(1, keepdim=True) + (0 if dsum is None else dsum.double().abs())
     assert ((dx.double() - want).abs() <= 2.0 ** -8 * want.abs() + 4 * REL * mag + 2.0 ** -133).all()
     if dw is not None:
-        # a product, r's chain, and the sum: up to T / groups rows, groups / 16, 16 warps
+        # a product, r's chain, and the sum: a CTA's rows (up to 8 warps'), ctas / 16, 16 warps
         T, H = s.shape
-        groups = dg.load().dg_rmsnorm_backward_workspace(T, H) // (4 * H)
-        chain = 24 + 3 + -(-T // groups) + -(-groups // 16) + 16
+        ctas = dg.load().dg_rmsnorm_backward_workspace(T, H) // (4 * H)
+        chain = 24 + 3 + -(-T // ctas) + 8 + -(-ctas // 16) + 16
         assert ((dw.double() - want_dw).abs() <= chain * 2.0 ** -24 * (d * sd * r).abs().sum(0)).all()
 
 
 @pytest.mark.parametrize("half", [False, True])
-@pytest.mark.parametrize("T,H", [(1, 8), (1, 7168), (3, 256), (70, 384), (1300, 512), (33, 1024), (700, 1152), (330, 2048), (1, 16384), (610, 7168), (2, 1000), (5, 5000), (2500, 136)])
+@pytest.mark.parametrize("T,H", [(1, 8), (1, 7168), (3, 256), (70, 384), (1300, 512), (33, 1024), (700, 1152), (330, 2048), (1, 16384), (610, 7168), (2, 1000), (5, 5000), (2500, 136), (5000, 1000), (9, 2048), (1250, 3000), (200, 12000)])
 def test_backward(T, H, half):
     s, dsum, w = make(T, H, half)
     dy = torch.randn(T, H, device=DEV, generator=gen(9)).bfloat16()
