@@ -5,7 +5,7 @@
 //   dx = r (g dy - s r^2 mean(g dy s)) + dsum,  dg = sum over rows of dy s r
 //
 // What bounds them is memory: 16381 x 7168 with residual, sum and both outputs takes 153 us (6.9 TB/s), its gradient at 8192 x 7168
-// 75.6 (6.2 TB/s, the second launch for the weight gradient included); one row of 7168 takes 3.0 us in a CUDA graph.
+// 74.1 (6.3 TB/s, the second launch for the weight gradient included); one row of 7168 takes 3.0 us in a CUDA graph.
 //
 // A row is in registers from its load to its stores: up to 1024 values a warp has a row of its own, above that a CTA with
 // up to 32 values a thread. A thread's vectors of 8 values are a whole CTA (warp) apart, so that every load covers

@@ -435,7 +435,7 @@ constexpr int CB_VECTORS = 4;                     // a lane's vectors at a time
 
 // WIDE: a CTA a token; else a warp a token. A lane keeps its piece of dout while it goes through the token's experts; the
 // products with their rows are added up over the lanes, and over the warps in order. What bounds it is memory, half of it
-// written: 4096 tokens of 8 x 7168 take 168 us, 6.3 TB/s.
+// written: 4096 tokens of 8 x 7168 take 164 us, 6.4 TB/s.
 template <bool WIDE>
 __global__ void __launch_bounds__(32 * (WIDE ? CB_WARPS : CB_NARROW)) combine_backward_kernel(const CombineBackwardParams p) {
     __shared__ float s_dot[CB_WARPS][32];
@@ -711,11 +711,10 @@ dg_status dg_moe_combine_backward(const void* dout, const void* y, const int32_t
     p.k = k;
     p.vectors = H / 8;
     p.Mt = Mt;
-    // Few tokens get as many warps each as they have pieces for, up to eight (256 tokens of 8 x 7168: 37.7 us, with four 39.9, with two
-    // 46.0); many get four, or two where a token has few experts, whose sums' end weighs more (4096 of 8: 168 us, with eight and two
-    // 181 and 176; 8192 of 2: 107 with two, 116 with four, 129 with eight). The order of the sums goes by the sizes alone.
+    // Few tokens get as many warps each as they have pieces for, up to eight (256 tokens of 8 x 7168: 27.5 us, with four 31.8, with two
+    // 43.1), many get four (4096: 163.7 us, with eight 170.4, with two 171.3). The order of the sums goes by the sizes alone.
     const bool wide = H > 32 * CB_VECTORS * 8;
-    const int most = T < 512 ? CB_WARPS : k > 4 ? 4 : 2, pieces = cdiv(p.vectors, 32 * CB_VECTORS);
+    const int most = T < 2048 ? CB_WARPS : 4, pieces = cdiv(p.vectors, 32 * CB_VECTORS);
     const int warps = !wide ? CB_NARROW : pieces < most ? pieces : most;
     p.token_ctas = !slots ? 0u : (wide ? static_cast<unsigned>(T) : static_cast<unsigned>(cdiv(T, CB_NARROW)));
     p.pad_rows = pad_rows(16 * static_cast<int64_t>(p.vectors));

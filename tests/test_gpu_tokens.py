@@ -223,7 +223,7 @@ def test_infinities_and_nan_stay_in_their_tokens():
 
 
 @pytest.mark.parametrize("weighted", [False, True])
-@pytest.mark.parametrize("T,k,E,H", SUMS + [(40, 3, 4, 1024), (40, 3, 4, 4096), (9, 8, 8, 9000), (1100, 3, 4, 2600)])
+@pytest.mark.parametrize("T,k,E,H", SUMS + [(40, 3, 4, 1024), (40, 3, 4, 4096), (9, 8, 8, 9000), (1100, 3, 4, 2600), (2100, 3, 4, 5000)])
 def test_combine_backward(T, k, E, H, weighted):
     ids = make_ids(T, k, E, "outside" if T > 20 else "spread")
     rows, counts, m_indices = sort_contiguous(ids, E, extra=128)
