@@ -244,7 +244,7 @@ struct GluBackwardShared {
 // inputs come while this one's are in use, and the rows' codes are made while some warps make the columns' scales.
 //
 // Floor: 9.25 bytes an element of dH from codes, 45.6 us for 16384 x 2048. It takes 78.5 us (SILU; GELU 87.6, its tanh form 81.6;
-// from BF16 79.2): 47 instructions an element at 52% of the issue slots. A CTA for each of the three outputs took 153 us, 1024
+// from BF16 79.2): 46 instructions an element at 52% of the issue slots. A CTA for each of the three outputs took 153 us, 1024
 // threads with 4 rows a lane 84.1, inputs by loads into registers 85.0 and without a prefetch 115; codes by rounded quotients
 // and the slopes and values by forms of their own cost 28 us more than by the reciprocal and one sigmoid.
 template <int ACT, bool KEPT>
