@@ -244,9 +244,10 @@ struct GluBackwardShared {
 // inputs come while this one's are in use, and the rows' codes are made while some warps make the columns' scales.
 //
 // Floor: 9.25 bytes an element of dH from codes, 45.6 us for 16384 x 2048. It takes 78.5 us (SILU; GELU 87.6, its tanh form 81.6;
-// from BF16 79.2): 46 instructions an element at 52% of the issue slots. A CTA for each of the three outputs took 153 us, 1024
-// threads with 4 rows a lane 84.1, inputs by loads into registers 85.0 and without a prefetch 115; codes by rounded quotients
-// and the slopes and values by forms of their own cost 28 us more than by the reciprocal and one sigmoid.
+// from BF16 79.2): 46 instructions an element at 52% of the issue slots. A CTA for each of the three outputs took 153 us; all
+// three in one with 1024 threads and 4 rows a lane 115.7, then 87.3 with codes by the reciprocal, one sigmoid for value and slope
+// and the next inputs asked into L2, and 84.1 with them copied to shared memory. Two CTAs an SM with half a tile's columns each,
+// a pair of them exchanging the rows' maxima, took 83.7.
 template <int ACT, bool KEPT>
 __global__ void __launch_bounds__(GB_THREADS, 1) glu_backward_kernel(const GluBackwardParams p) {
     extern __shared__ __align__(16) uint8_t s_raw[];

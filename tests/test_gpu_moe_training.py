@@ -49,7 +49,7 @@ def test_every_step_of_a_training_step(T, H, I, E, k, act):
     # forward
     n = B.rmsnorm(x, block.norm, float(torch.tensor(1e-6)))
     assert ((s["y"].double() - n).abs() <= (2.0 ** -8 + 2.0 ** -18) * n.abs() + 2.0 ** -133).all()
-    want = B.sort(s["ids"].tolist(), E, len(mi) + 128 * 4096)
+    want = B.sort(s["ids"].tolist(), E, dg.moe_sort_rows(T, k, E))
     assert s["rows"].tolist() == want[0] and s["counts"].tolist() == want[1] and mi.tolist() == want[2][: len(mi)]
     row = s["rows"][s["rows"] >= 0].long()
     token = (s["rows"] >= 0).nonzero()[:, 0]
