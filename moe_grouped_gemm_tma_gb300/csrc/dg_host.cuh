@@ -57,6 +57,11 @@ cudaError_t launch_overlapped_smem(void (*kernel)(P...), dim3 grid, dim3 block, 
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
 }
 
+template <typename... P, typename... A>
+cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, dim3 block, cudaStream_t stream, A&&... args) {
+    return launch_overlapped_smem(kernel, grid, block, 0, stream, static_cast<A&&>(args)...);
+}
+
 // Lets a kernel have `bytes` of dynamic shared memory on the current device (asked for once per kernel and device; `bytes`
 // is the most that it is ever launched with).
 template <auto KERNEL>
@@ -70,11 +75,6 @@ cudaError_t allow_smem(int bytes) {
     e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e == cudaSuccess) done[dev].store(true, std::memory_order_relaxed);
     return e;
-}
-
-template <typename... P, typename... A>
-cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, dim3 block, cudaStream_t stream, A&&... args) {
-    return launch_overlapped_smem(kernel, grid, block, 0, stream, static_cast<A&&>(args)...);
 }
 
 }  // namespace dg

@@ -1,6 +1,7 @@
-// A 128 x 128 tile of FP32 values in registers, quantised along its rows and along its columns: one scaling block in either
-// direction. A warp has R whole rows and a lane 4 columns of each, v[row][pair of columns]: a row's largest magnitude is one
-// reduction of the warp, and a column's needs no exchange inside a warp, only one over the 128 / R warps through shared memory.
+// A tile of FP32 values in registers, 128 rows of 128 columns (a scaling block in either direction) or fewer, quantised along its
+// columns and, with 128 of them, along its rows. A warp (or half of one) has R whole rows and a lane 4 columns of each, v[row][pair
+// of columns]: a row's largest magnitude is one reduction of the warp, and a column's needs no exchange inside a warp, only
+// one over the 128 / R groups of rows through shared memory.
 #pragma once
 
 #include <cstdint>
@@ -59,6 +60,7 @@ __device__ __forceinline__ void tile_rows2(const float2 (&v)[R][2], const float2
 // else by the reciprocal.
 template <int R, bool EXACT, int COLUMNS = TILE>
 struct TileColumns {
+    static_assert(R == 8 || R == 16, "two or four words of codes a lane and column");
     static constexpr int GROUPS = TILE / R;
     static constexpr int THREADS = GROUPS * COLUMNS / 4;
     __align__(16) float amax[GROUPS][COLUMNS];
@@ -74,7 +76,7 @@ struct TileColumns {
             a[c] = abs_max(at(0), at(1), at(2));
 #pragma unroll
             for (int i = 3; i + 1 < R; i += 2) a[c] = abs_max(a[c], at(i), at(i + 1));
-            if (R % 2 == 0) a[c] = abs_max(a[c], at(R - 1));
+            a[c] = abs_max(a[c], at(R - 1));
         }
         *reinterpret_cast<float4*>(&amax[group][lane * 4]) = make_float4(a[0], a[1], a[2], a[3]);
     }
@@ -114,12 +116,9 @@ struct TileColumns {
             if constexpr (R == 16) {
                 *reinterpret_cast<uint4*>(dst) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 *reinterpret_cast<uint4*>(dst + 32) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            } else if constexpr (R == 8) {
+            } else {
                 *reinterpret_cast<uint2*>(dst) = make_uint2(lo[0], lo[1]);
                 *reinterpret_cast<uint2*>(dst + 32) = make_uint2(hi[0], hi[1]);
-            } else {
-                dst[0] = lo[0];
-                dst[32] = hi[0];
             }
         }
     }
@@ -134,8 +133,7 @@ struct TileColumns {
         for (int i = 0; i < COLUMNS / PASS; ++i, dst += PASS * pitch) {
             const int at = i * PASS * 32 + (l ^ (c0 >> 2) ^ (i * (PASS / 4) & (GROUPS - 1))) * (R / 4);      // (c0 >> 2 is below PASS / 4)
             if constexpr (R == 16) *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(src + at);
-            else if constexpr (R == 8) *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(src + at);
-            else *reinterpret_cast<uint32_t*>(dst) = src[at];
+            else *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(src + at);
         }
     }
 };
