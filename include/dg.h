@@ -338,8 +338,7 @@ int64_t dg_rmsnorm_backward_workspace(int T, int H);
  * The gated activation between the two products of an expert (or of a dense layer), quantised for the second:
  *   h = act(g) * u,   (g; u) = Z's columns [0, I) and [I, 2I)
  *   Z    [M, 2I] bf16
- *   q    [M, I] e4m3, sf [M, I/128]: h in FP32, quantised as in dg_epilogue_backward, but that a code may be that of a
- *        quotient a last place of FP32 away; pow2 as in dg_rmsnorm
+ *   q    [M, I] e4m3, sf [M, I/128]: h in FP32, quantised as in dg_epilogue_backward; pow2 as in dg_rmsnorm
  *   kept [M, 2I] e4m3, kept_sf [M, 2I/128], or both null: Z quantised as in dg_epilogue_backward, what dg_glu_backward takes
  *        instead of Z
  * At most one of (which rows are computed; all others stay as they were):
@@ -357,7 +356,7 @@ dg_status dg_glu(const void* Z, uint8_t* q, float* sf, uint8_t* kept, float* kep
  *   qt [2I, Mp] e4m3,  sft [2I, Mp/128]   the transpose, 1x128 scales along M, Mp = M rounded up to 128, zeros past M
  *   ht [I, Mp] e4m3,   hsft [I, Mp/128]   h's transpose, so quantised: an operand of the second product's weight gradient
  * q with sf, qt with sft, ht with hsft may each be null. The values are those of Z, or of the codes times their scales in FP32,
- * the codes are made as dg_glu's; every row is computed. I a multiple of 128, M free; matrices 16-byte aligned.
+ * quantised as in dg_epilogue_backward; every row is computed. I a multiple of 128, M free; matrices 16-byte aligned.
  */
 dg_status dg_glu_backward(const void* dH, const void* Z, const uint8_t* kept, const float* kept_sf, int act, uint8_t* q, float* sf, uint8_t* qt,
                           float* sft, uint8_t* ht, float* hsft, int M, int I, cudaStream_t stream);

@@ -71,18 +71,10 @@ __device__ __forceinline__ float line_maxima(float (&a)[N], int l16) {
     return most;
 }
 
-// Codes of a lane's 8 values of a line whose scale lane `from` has: exact quotients for values that are exact, for others by
-// the reciprocal.
-template <bool EXACT>
+// Codes of a lane's 8 values of a line whose scale lane `from` has.
 __device__ __forceinline__ uint2 line_codes(const float2 (&v)[4], const BlockScale& mine, float rest, int from) {
-    const float r = __shfl_sync(FULL, mine.r, from, 16);
-    if (!EXACT) return make_uint2(quantise4_by(v[0], v[1], r), quantise4_by(v[2], v[3], r));
-    const float l = __shfl_sync(FULL, rest, from, 16);
-    const float2 rr = make_float2(r, r), ll = make_float2(l, l);
-    float2 c[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = quotient2_by(v[i], rr, ll);
-    return make_uint2(pack_e4m3x2(c[0].x, c[0].y) | (pack_e4m3x2(c[1].x, c[1].y) << 16), pack_e4m3x2(c[2].x, c[2].y) | (pack_e4m3x2(c[3].x, c[3].y) << 16));
+    const float r = __shfl_sync(FULL, mine.r, from, 16), l = __shfl_sync(FULL, rest, from, 16);
+    return make_uint2(quantise4_by(v[0], v[1], r, l), quantise4_by(v[2], v[3], r, l));
 }
 
 // A half warp has the 128 values of a scaling block of 4 rows, a lane 8 columns of each, in both halves of Z. The largest
@@ -168,7 +160,7 @@ __global__ void __launch_bounds__(32 * GLU_WARPS, glu_ctas(KEEP)) glu_kernel(con
         const uint32_t bits = abs_bits(line_maxima(most, l16));
         const int line = l16 / SHARE, row = line & (R - 1), which = line / R;
         const BlockScale mine = p.pow2 && which == 0 ? block_scale_pow2(bits) : block_scale(bits);
-        const float rest = KEEP ? reciprocal_rest(mine.d, mine.r) : 0.f;
+        const float rest = reciprocal_rest(mine.d, mine.r);
         if (l16 % SHARE == 0 && (mask >> row & 1)) {
             const size_t at = static_cast<size_t>(row0 + row) * blocks;
             if (which == 0) p.sf[at + column] = mine.s;
@@ -178,7 +170,7 @@ __global__ void __launch_bounds__(32 * GLU_WARPS, glu_ctas(KEEP)) glu_kernel(con
         uint8_t* kept = KEEP ? p.kept + static_cast<size_t>(row0) * (2 * inner) + column * 128 + l16 * 8 : nullptr;
 #pragma unroll
         for (int i = 0; i < R; ++i, q += inner) {
-            const uint2 w = line_codes<false>(h[i], mine, rest, i * SHARE);
+            const uint2 w = line_codes(h[i], mine, rest, i * SHARE);
             if (mask >> i & 1) *reinterpret_cast<uint2*>(q) = w;
         }
         if (KEEP) {
@@ -186,9 +178,9 @@ __global__ void __launch_bounds__(32 * GLU_WARPS, glu_ctas(KEEP)) glu_kernel(con
             for (int i = 0; i < R; ++i, kept += 2 * inner) {
                 float2 v[4];
                 unpack_bf16(s_z[stage][i][threadIdx.x], v);
-                const uint2 gq = line_codes<true>(v, mine, rest, (R + i) * SHARE);
+                const uint2 gq = line_codes(v, mine, rest, (R + i) * SHARE);
                 unpack_bf16(s_z[stage][R + i][threadIdx.x], v);
-                const uint2 uq = line_codes<true>(v, mine, rest, (2 * R + i) * SHARE);
+                const uint2 uq = line_codes(v, mine, rest, (2 * R + i) * SHARE);
                 if (mask >> i & 1) {
                     *reinterpret_cast<uint2*>(kept) = gq;
                     *reinterpret_cast<uint2*>(kept + inner) = uq;
@@ -233,7 +225,7 @@ constexpr int GB_ROWS = 8;                        // rows of a warp
 constexpr int GB_THREADS = 32 * TILE / GB_ROWS;
 template <bool KEPT>
 struct GluBackwardShared {
-    TileColumns<GB_ROWS, false> dg, du, h;
+    TileColumns<GB_ROWS> dg, du, h;
     __align__(16) uint2 dh[TILE][32];             // the tile's inputs, as they are in global memory
     __align__(16) uint32_t g[TILE][KEPT ? 32 : 64], u[TILE][KEPT ? 32 : 64];
     __align__(16) float scale[2][TILE];           // of g's and u's codes
@@ -372,7 +364,7 @@ struct TransposeParams {
 constexpr int TR_ROWS = 16;                       // rows of a half warp
 constexpr int TR_COLUMNS = 64;
 constexpr int TR_CTAS = 4;
-using TransposeTile = TileColumns<TR_ROWS, true, TR_COLUMNS>;
+using TransposeTile = TileColumns<TR_ROWS, TR_COLUMNS>;
 static_assert(TR_ROWS <= TR_COLUMNS / 4, "a lane loads the scale of one of its group's rows");
 
 __global__ void __launch_bounds__(TransposeTile::THREADS, TR_CTAS) transpose_kernel(const TransposeParams p) {

@@ -85,12 +85,11 @@ __device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
     return d;
 }
 
-// Four products to codes, in order from the lowest byte: values times the reciprocal of their scale, which is within an ulp
-// or so of the quotient. For values that have several roundings of their own, which move as many of them across a midpoint.
-__device__ __forceinline__ uint32_t quantise4_by(float2 a, float2 b, float r) {
-    const float2 rr = make_float2(r, r);
-    a = __fmul2_rn(a, rr);
-    b = __fmul2_rn(b, rr);
+// Four values to codes, in order from the lowest byte, by the reciprocal of their scale and its rest.
+__device__ __forceinline__ uint32_t quantise4_by(float2 a, float2 b, float r, float rest) {
+    const float2 rr = make_float2(r, r), ll = make_float2(rest, rest);
+    a = quotient2_by(a, rr, ll);
+    b = quotient2_by(b, rr, ll);
     return pack_e4m3x2(a.x, a.y) | (pack_e4m3x2(b.x, b.y) << 16);
 }
 

@@ -22,7 +22,7 @@ __device__ __forceinline__ float warp_abs_max(float v) {
 
 // Codes along the rows of two tiles' values at once: q points at the lane's first value of each, rows `pitch` apart, sf at the
 // warp's first row's scale, `scales` apart; `valid` of the R rows exist. Lane l makes the scale of row l / (16 / R) of the first
-// tile, or, from lane 16 on, of the second, and hands round its reciprocal.
+// tile, or, from lane 16 on, of the second, and hands round its reciprocal and the reciprocal's rest.
 template <int R>
 __device__ __forceinline__ void tile_rows2(const float2 (&v)[R][2], const float2 (&u)[R][2], uint8_t* qv, uint8_t* qu, size_t pitch, float* sfv, float* sfu,
                                            size_t scales, int valid, int lane) {
@@ -41,12 +41,14 @@ __device__ __forceinline__ void tile_rows2(const float2 (&v)[R][2], const float2
     }
     const float most = a[0];
     const BlockScale mine = block_scale(abs_bits(most));
+    const float rest = reciprocal_rest(mine.d, mine.r);
     const int row = lane / SHARE & (R - 1);
     if (lane % SHARE == 0 && row < valid) (lane < 16 ? sfv : sfu)[row * scales] = mine.s;
 #pragma unroll
     for (int i = 0; i < R; ++i, qv += pitch, qu += pitch) {
         const float rv = __shfl_sync(0xffffffffu, mine.r, i * SHARE), ru = __shfl_sync(0xffffffffu, mine.r, 16 + i * SHARE);
-        const uint32_t a = quantise4_by(v[i][0], v[i][1], rv), b = quantise4_by(u[i][0], u[i][1], ru);
+        const float lv = __shfl_sync(0xffffffffu, rest, i * SHARE), lu = __shfl_sync(0xffffffffu, rest, 16 + i * SHARE);
+        const uint32_t a = quantise4_by(v[i][0], v[i][1], rv, lv), b = quantise4_by(u[i][0], u[i][1], ru, lu);
         if (i < valid) {
             *reinterpret_cast<uint32_t*>(qv) = a;
             *reinterpret_cast<uint32_t*>(qu) = b;
@@ -56,9 +58,8 @@ __device__ __forceinline__ void tile_rows2(const float2 (&v)[R][2], const float2
 
 // Codes along the columns of a tile of 128 rows and COLUMNS columns, in three steps with a barrier of the CTA behind each: the
 // largest magnitudes of every group of R rows, the columns' scales, the codes, which then leave as the rows of the transpose.
-// A group of R rows is COLUMNS / 4 lanes', a warp's or half a warp's; `lane` is the one of these. EXACT: by the rounded quotient,
-// else by the reciprocal.
-template <int R, bool EXACT, int COLUMNS = TILE>
+// A group of R rows is COLUMNS / 4 lanes', a warp's or half a warp's; `lane` is the one of these.
+template <int R, int COLUMNS = TILE>
 struct TileColumns {
     static_assert(R == 8 || R == 16, "two or four words of codes a lane and column");
     static constexpr int GROUPS = TILE / R;
@@ -90,7 +91,7 @@ struct TileColumns {
             for (int j = 0; j < 4; ++j) a[j] = abs_max(a[j], amax[w + j][c], amax[w + j + 4][c]);
         const BlockScale k = block_scale(abs_bits(abs_max(abs_max(a[0], a[1], a[2]), a[3])));
         reciprocal[c] = k.r;
-        if (EXACT) rest[c] = reciprocal_rest(k.d, k.r);
+        rest[c] = reciprocal_rest(k.d, k.r);
         *sft = k.s;
     }
 
@@ -98,7 +99,7 @@ struct TileColumns {
     // the loads below meet in a bank.
     __device__ __forceinline__ void quantise(const float2 (&v)[R][2], int group, int lane) {
         const float4 r = *reinterpret_cast<const float4*>(&reciprocal[lane * 4]);
-        const float4 d = EXACT ? *reinterpret_cast<const float4*>(&rest[lane * 4]) : r;
+        const float4 d = *reinterpret_cast<const float4*>(&rest[lane * 4]);
         const int slot = group ^ (lane & (GROUPS - 1));
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
@@ -108,7 +109,7 @@ struct TileColumns {
             for (int i = 0; i < R; i += 4) {
                 float2 w[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) w[j] = EXACT ? quotient2_by(v[i + j][x], rr, rest2) : __fmul2_rn(v[i + j][x], rr);
+                for (int j = 0; j < 4; ++j) w[j] = quotient2_by(v[i + j][x], rr, rest2);
                 lo[i / 4] = pack_e4m3x2(w[0].x, w[1].x) | (pack_e4m3x2(w[2].x, w[3].x) << 16);
                 hi[i / 4] = pack_e4m3x2(w[0].y, w[1].y) | (pack_e4m3x2(w[2].y, w[3].y) << 16);
             }
