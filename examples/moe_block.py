@@ -73,6 +73,7 @@ class Block:
             self.decode(x)
         torch.cuda.current_stream().wait_stream(side)
         g = torch.cuda.CUDAGraph()
+        g.block = self                    # whose weights it reads: they live as long as it does
         with torch.cuda.graph(g):
             out = self.decode(x)
         return x, out, g
@@ -145,18 +146,24 @@ class Experts:
         self.router = torch.randn(E, H, generator=g, device=device) / H ** 0.5
         self.master13 = torch.randn(E, 2 * I, H, generator=g, device=device) / H ** 0.5
         self.master2 = torch.randn(E, H, I, generator=g, device=device) / I ** 0.5
+        self.weights = None
         self.update()
 
     def update(self):
-        """The products' weights from the master weights. (A 128x128 block's codes and scale are its transpose's too, which
-        the backward pass multiplies by.)"""
+        """The products' weights from the master weights, in the same memory each time, where captured passes read them. (A 128x128
+        block's codes and scale are its transpose's too, which the backward pass multiplies by.)"""
         def codes(w):
             e, n, k = w.shape
             q, s = quantize_128x128(w.reshape(e * n, k))
             q, s = q.view(e, n, k), s.view(e, n // 128, k // 128)
-            return q, s, q.transpose(1, 2).contiguous(), s.transpose(1, 2).contiguous()
-        self.W13, self.s13, self.W13t, self.s13t = codes(self.master13)
-        self.W2, self.s2, self.W2t, self.s2t = codes(self.master2)
+            return [q, s, q.transpose(1, 2).contiguous(), s.transpose(1, 2).contiguous()]
+        made = codes(self.master13) + codes(self.master2)
+        if self.weights is None:
+            self.weights = made
+            self.W13, self.s13, self.W13t, self.s13t, self.W2, self.s2, self.W2t, self.s2t = made
+        else:
+            for old, new in zip(self.weights, made):
+                old.copy_(new)
 
     def forward(self, x, rows_at_most=None):
         """The block's output for x, bf16 [T,H]. rows_at_most: rows of the grouped layout, known from the counts (None: as many as
@@ -188,7 +195,7 @@ class Experts:
         return dg.dg_moe_combine(s["Y"], s["rows"], out, weights=s["weights"], residual=x)
 
     def graph(self, T):
-        """(x, out, graph): the captured forward pass of T tokens."""
+        """(x, out, graph): the captured forward pass of T tokens. Its replays read the block's weights as they are then."""
         x = torch.zeros(T, self.H, dtype=torch.bfloat16, device=self.norm.device)
         side = torch.cuda.Stream()
         side.wait_stream(torch.cuda.current_stream())
@@ -196,6 +203,7 @@ class Experts:
             self.forward(x)
         torch.cuda.current_stream().wait_stream(side)
         g = torch.cuda.CUDAGraph()
+        g.block = self                    # whose weights it reads: they live as long as it does
         with torch.cuda.graph(g):
             out = self.forward(x)
         return x, out, g
