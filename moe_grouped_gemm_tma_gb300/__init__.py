@@ -619,12 +619,12 @@ def dg_moe_gather(x, sf, rows, out, out_sf=None, m_indices=None, stream=None):
     torch = _torch_module or _torch()
     i32, f32, bf16, e4m3 = torch.int32, torch.float32, torch.bfloat16, (torch.float8_e4m3fn, torch.uint8)
     T, H = x.shape
-    Tk = T, k = rows.shape[0], rows.shape[1]
+    _, k = rows.shape
     codes = x.dtype is not bf16
     dev = x.get_device()
     lead = out.shape[:-1]
     Mt = lead.numel()
-    if not (x.is_contiguous() and dev >= 0 and x.shape[0] == T and rows.dtype is i32 and rows.get_device() == dev and rows.is_contiguous()
+    if not (x.is_contiguous() and dev >= 0 and rows.dtype is i32 and rows.shape[0] == T and rows.get_device() == dev and rows.is_contiguous()
             and out.shape[-1] == H and out.get_device() == dev and out.is_contiguous() and (m_indices is None or _fits(m_indices, i32, (Mt,), dev))
             and ((x.dtype in e4m3 and out.dtype in e4m3 and sf is not None and out_sf is not None and sf.dtype is f32 and sf.shape == (T, H // 128)
                   and sf.get_device() == dev and sf.is_contiguous() and out_sf.dtype is f32 and out_sf.shape == (*lead, H // 128)
@@ -632,7 +632,7 @@ def dg_moe_gather(x, sf, rows, out, out_sf=None, m_indices=None, stream=None):
             and torch._C._cuda_getDevice() == dev):
         if codes and x.dtype not in e4m3:
             raise TypeError(f"x must be float8_e4m3fn, uint8 or bfloat16, got {x.dtype}")
-        _refuse_here(dev, x=(x, e4m3 if codes else (bf16,), None), rows=(rows, (i32,), (x.shape[0], k)), out=(out, e4m3 if codes else (bf16,), (*lead, H)),
+        _refuse_here(dev, x=(x, e4m3 if codes else (bf16,), None), rows=(rows, (i32,), (T, k)), out=(out, e4m3 if codes else (bf16,), (*lead, H)),
                      sf=(sf, (f32,), (T, H // 128)), out_sf=(out_sf, (f32,), (*lead, H // 128)), m_indices=(m_indices, (i32,), (Mt,)))
         if codes == (sf is None) or codes == (out_sf is None):
             raise ValueError("sf and out_sf go with e4m3 rows, and with them only")
