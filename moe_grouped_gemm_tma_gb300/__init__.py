@@ -789,12 +789,21 @@ def dg_glu(Z, q, sf, kept=None, kept_sf=None, m_indices=None, masked_m=None, act
 def dg_glu_backward(dH, q, sf, qt, sft, ht, hsft, Z=None, kept=None, kept_sf=None, act="silu", stream=None):
     """The gated activation's backward pass from dH bf16 [M,I] and Z bf16 [M,2I] or the codes that dg_glu kept: (dg; du) as e4m3
     codes q [M,2I] with scales sf [M,2I/128] and of the transpose qt [2I,Mp] with sft [2I,Mp/128] (Mp = M rounded up to 128),
-    and h's transpose ht [I,Mp] with hsft [I,Mp/128]. Each pair may be None."""
+    and h's transpose ht [I,Mp] with hsft [I,Mp/128]. Each pair may be None, and dH where q and qt are."""
     torch = _torch_module or _torch()
     f32, bf16, e4m3 = torch.float32, torch.bfloat16, (torch.float8_e4m3fn, torch.uint8)
-    MI = M, I = dH.shape
+    if (Z is None) == (kept is None):
+        raise ValueError("one of Z and kept has to be given")
+    if dH is None:
+        if q is not None or qt is not None:
+            raise ValueError("q and qt need dH")
+        M, I2 = (kept if Z is None else Z).shape
+        I = I2 // 2
+        dev = (kept if Z is None else Z).get_device()
+    else:
+        M, I = dH.shape
+        dev = dH.get_device()
     Mp = (M + 127) // 128 * 128
-    dev = dH.get_device()
 
     def codes(t, shape):
         return t is None or (t.dtype in e4m3 and t.shape == shape and t.get_device() == dev and t.is_contiguous())
@@ -802,9 +811,7 @@ def dg_glu_backward(dH, q, sf, qt, sft, ht, hsft, Z=None, kept=None, kept_sf=Non
     def scales(t, shape):
         return t is None or _fits(t, f32, shape, dev)
 
-    if (Z is None) == (kept is None):
-        raise ValueError("one of Z and kept has to be given")
-    if not (_fits(dH, bf16, MI, dev) and dev >= 0 and (Z is None or _fits(Z, bf16, (M, 2 * I), dev)) and codes(kept, (M, 2 * I)) and scales(kept_sf, (M, 2 * I // 128))
+    if not ((dH is None or _fits(dH, bf16, (M, I), dev)) and dev >= 0 and (Z is None or _fits(Z, bf16, (M, 2 * I), dev)) and codes(kept, (M, 2 * I)) and scales(kept_sf, (M, 2 * I // 128))
             and codes(q, (M, 2 * I)) and scales(sf, (M, 2 * I // 128)) and codes(qt, (2 * I, Mp)) and scales(sft, (2 * I, Mp // 128))
             and codes(ht, (I, Mp)) and scales(hsft, (I, Mp // 128)) and torch._C._cuda_getDevice() == dev):
         _refuse_here(dev, dH=(dH, (bf16,), None), Z=(Z, (bf16,), (M, 2 * I)), kept=(kept, e4m3, (M, 2 * I)), kept_sf=(kept_sf, (f32,), (M, 2 * I // 128)),
@@ -812,7 +819,7 @@ def dg_glu_backward(dH, q, sf, qt, sft, ht, hsft, Z=None, kept=None, kept_sf=Non
                      ht=(ht, e4m3, (I, Mp)), hsft=(hsft, (f32,), (I, Mp // 128)))
         _refuse_device(dev)
     p = _ptr
-    st = (_lib or load()).dg_glu_backward(dH.data_ptr(), p(Z), p(kept), p(kept_sf), _choice(ACTIVATIONS, act, "act"), p(q), p(sf), p(qt), p(sft), p(ht), p(hsft), M, I,
+    st = (_lib or load()).dg_glu_backward(p(dH), p(Z), p(kept), p(kept_sf), _choice(ACTIVATIONS, act, "act"), p(q), p(sf), p(qt), p(sft), p(ht), p(hsft), M, I,
                                           torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
     if st:
         raise DGError(st, "dg_glu_backward")

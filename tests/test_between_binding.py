@@ -15,3 +15,33 @@ def test_gather_wants_rows_of_two_axes_and_as_many_as_tokens(shape):
         dg.dg_moe_gather(c(4, 128, dtype=b), None, c(*shape, dtype=i), c(16, 128, dtype=b))
     with pytest.raises(ValueError):
         dg.dg_moe_gather(c(4, 128, dtype=u), c(4, 1), c(*shape, dtype=i), c(16, 128, dtype=u), c(16, 1))
+
+
+def test_glu_backward_without_dh_refuses_what_needs_it():
+    for out in ({"q": c(2, 256, dtype=u), "sf": c(2, 2)}, {"qt": c(256, 128, dtype=u), "sft": c(256, 1)}):
+        args = [out.get(n) for n in ("q", "sf", "qt", "sft", "ht", "hsft")]
+        with pytest.raises(ValueError, match="need dH"):
+            dg.dg_glu_backward(None, *args, Z=c(2, 256, dtype=b))
+    with pytest.raises(ValueError, match="one of Z and kept"):
+        dg.dg_glu_backward(None, *[None] * 4, c(128, 128, dtype=u), c(128, 1))
+    with pytest.raises(ValueError, match="ht must have shape"):
+        dg.dg_glu_backward(None, *[None] * 4, c(64, 128, dtype=u), c(128, 1), Z=c(2, 256, dtype=b))
+    with pytest.raises(ValueError, match="Z must have shape"):
+        dg.dg_glu_backward(None, *[None] * 4, c(128, 128, dtype=u), c(128, 1), Z=c(2, 257, dtype=b))
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        dg.dg_glu_backward(None, *[None] * 4, c(128, 128, dtype=u), c(128, 1), Z=torch.empty(2, 256, dtype=b))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kept", [False, True])
+def test_glu_backward_without_dh_gives_the_transposed_activation(kept):
+    from tests.test_gpu_glu import alloc, make_z, run_backward
+    M, I = 200, 256
+    Z = make_z(M, I)
+    q, sf, codes, ksf = alloc(M, I, True)
+    dg.dg_glu(Z, q, sf, codes, ksf)
+    given = {"kept": codes, "kept_sf": ksf} if kept else {"Z": Z}
+    want = run_backward(torch.ones(M, I, dtype=b, device="cuda"), **({"kept": codes, "ksf": ksf} if kept else {"Z": Z}))["ht"]
+    ht, hsft = torch.zeros_like(want[0]), torch.zeros_like(want[1])
+    dg.dg_glu_backward(None, None, None, None, None, ht, hsft, **given)
+    assert torch.equal(ht, want[0]) and torch.equal(hsft, want[1])
