@@ -549,13 +549,19 @@ def _workspace_here(t, device):
     return ws, size
 
 
+def _refuse_sizes(where):
+    """The C calls take 32-bit sizes, which ctypes would cut larger ones to (a caller's check: sizes or-ed together, shifted by
+    31, are 0)."""
+    raise DGError(2, where)
+
+
 def _refuse_device(device):
     raise ValueError(f"the tensors are on cuda:{device}, the current device is cuda:{_torch()._C._cuda_getDevice()}")
 
 
 def moe_sort_rows(T: int, k: int, E: int) -> int:
     """Rows of the contiguous layout (a multiple of 128) that every routing of T tokens to k of E experts fits."""
-    rows = load().dg_moe_sort_rows(T, k, E)
+    rows = -1 if (T | k | E) >> 31 else load().dg_moe_sort_rows(T, k, E)
     if rows < 0:
         raise DGError(2, "dg_moe_sort_rows")
     return rows
@@ -563,7 +569,7 @@ def moe_sort_rows(T: int, k: int, E: int) -> int:
 
 def moe_sort_workspace(T: int, k: int, E: int, device=None):
     """A workspace for the sorts of up to T tokens to k of E experts; empty where they need none."""
-    size = load().dg_moe_sort_workspace(T, k, E)
+    size = -1 if (T | k | E) >> 31 else load().dg_moe_sort_workspace(T, k, E)
     if size < 0:
         raise DGError(2, "dg_moe_sort_workspace")
     return _workspace(size, 0, device)
@@ -576,6 +582,8 @@ def dg_moe_sort_contiguous(ids, rows, counts, m_indices, workspace=None, stream=
     i32 = torch.int32
     Tk = T, k = ids.shape
     E, Mt = counts.shape[0], m_indices.shape[0]
+    if (T | k | E | Mt) >> 31:
+        _refuse_sizes("dg_moe_sort_contiguous")
     dev = ids.get_device()
     if not (ids.dtype is i32 and ids.is_contiguous() and dev >= 0 and rows.dtype is i32 and rows.shape == Tk and rows.get_device() == dev
             and rows.is_contiguous() and counts.dtype is i32 and counts.shape == (E,) and counts.get_device() == dev and counts.is_contiguous()
@@ -597,7 +605,9 @@ def dg_moe_sort_masked(ids, rows, masked_m, max_m: int, workspace=None, stream=N
     torch = _torch_module or _torch()
     i32 = torch.int32
     Tk = T, k = ids.shape
-    E = masked_m.shape[0]
+    E, max_m = masked_m.shape[0], int(max_m)
+    if (T | k | E) >> 31 or max_m >> 31 not in (0, -1):
+        _refuse_sizes("dg_moe_sort_masked")
     dev = ids.get_device()
     if not (ids.dtype is i32 and ids.is_contiguous() and dev >= 0 and rows.dtype is i32 and rows.shape == Tk and rows.get_device() == dev
             and rows.is_contiguous() and masked_m.dtype is i32 and masked_m.shape == (E,) and masked_m.get_device() == dev and masked_m.is_contiguous()
@@ -605,7 +615,7 @@ def dg_moe_sort_masked(ids, rows, masked_m, max_m: int, workspace=None, stream=N
         _refuse_here(dev, ids=(ids, (i32,), None), rows=(rows, (i32,), Tk), masked_m=(masked_m, (i32,), (E,)))
         _refuse_device(dev)
     ws, size = _workspace_here(workspace, dev)
-    st = (_lib or load()).dg_moe_sort_masked(ids.data_ptr(), rows.data_ptr(), masked_m.data_ptr(), ws, size, T, k, E, int(max_m),
+    st = (_lib or load()).dg_moe_sort_masked(ids.data_ptr(), rows.data_ptr(), masked_m.data_ptr(), ws, size, T, k, E, max_m,
                                              torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
     if st:
         raise DGError(st, "dg_moe_sort_masked")
@@ -624,6 +634,8 @@ def dg_moe_gather(x, sf, rows, out, out_sf=None, m_indices=None, stream=None):
     dev = x.get_device()
     lead = out.shape[:-1]
     Mt = lead.numel()
+    if (T | k | H | Mt) >> 31:
+        _refuse_sizes("dg_moe_gather")
     if not (x.is_contiguous() and dev >= 0 and rows.dtype is i32 and rows.shape[0] == T and rows.get_device() == dev and rows.is_contiguous()
             and out.shape[-1] == H and out.get_device() == dev and out.is_contiguous() and (m_indices is None or _fits(m_indices, i32, (Mt,), dev))
             and ((x.dtype in e4m3 and out.dtype in e4m3 and sf is not None and out_sf is not None and sf.dtype is f32 and sf.shape == (T, H // 128)
@@ -653,6 +665,8 @@ def dg_moe_combine(y, rows, out, weights=None, residual=None, stream=None):
     Tk = T, k = rows.shape
     H = y.shape[-1]
     Mt = y.shape[:-1].numel()
+    if (T | k | H | Mt) >> 31:
+        _refuse_sizes("dg_moe_combine")
     TH = (T, H)
     dev = y.get_device()
     if not (y.dtype is bf16 and y.is_contiguous() and dev >= 0 and rows.dtype is i32 and rows.get_device() == dev and rows.is_contiguous()
@@ -680,6 +694,8 @@ def dg_moe_combine_backward(dout, rows, dy, weights=None, y=None, dweights=None,
     like = y if dy is None else dy
     lead = like.shape[:-1]
     Mt = lead.numel()
+    if (T | k | H | Mt) >> 31:
+        _refuse_sizes("dg_moe_combine_backward")
     MH = (*lead, H)
     dev = dout.get_device()
     if not (_fits(dout, bf16, (T, H), dev) and dev >= 0 and _fits(rows, i32, Tk, dev) and (dy is None or _fits(dy, bf16, MH, dev))
@@ -704,6 +720,8 @@ def dg_rmsnorm(x, weight, y=None, q=None, sf=None, residual=None, sum=None, eps=
     torch = _torch_module or _torch()
     f32, bf16, e4m3 = torch.float32, torch.bfloat16, (torch.float8_e4m3fn, torch.uint8)
     TH = T, H = x.shape
+    if (T | H) >> 31:
+        _refuse_sizes("dg_rmsnorm")
     dev = x.get_device()
     kind = weight.dtype
     if not (x.dtype is bf16 and x.is_contiguous() and dev >= 0 and (kind is f32 or kind is bf16) and weight.shape == (H,) and weight.get_device() == dev
@@ -726,7 +744,7 @@ def dg_rmsnorm(x, weight, y=None, q=None, sf=None, residual=None, sum=None, eps=
 
 def rmsnorm_backward_workspace(T: int, H: int, device=None):
     """A workspace for dg_rmsnorm_backward with dweight at up to T rows of H."""
-    size = load().dg_rmsnorm_backward_workspace(T, H)
+    size = -1 if (T | H) >> 31 else load().dg_rmsnorm_backward_workspace(T, H)
     if size < 0:
         raise DGError(2, "dg_rmsnorm_backward_workspace")
     return _workspace(size, 0, device)
@@ -739,6 +757,8 @@ def dg_rmsnorm_backward(dy, x, weight, dx, dweight=None, workspace=None, dsum=No
     torch = _torch_module or _torch()
     f32, bf16 = torch.float32, torch.bfloat16
     TH = T, H = x.shape
+    if (T | H) >> 31:
+        _refuse_sizes("dg_rmsnorm_backward")
     dev = x.get_device()
     kind = weight.dtype
     if not (x.dtype is bf16 and x.is_contiguous() and dev >= 0 and (kind is f32 or kind is bf16) and _fits(weight, kind, (H,), dev)
@@ -765,6 +785,8 @@ def dg_glu(Z, q, sf, kept=None, kept_sf=None, m_indices=None, masked_m=None, act
     I = I2 // 2
     M = Z.shape[:-1].numel()
     G = 1 if masked_m is None else masked_m.shape[0]
+    if (M | I2 | G) >> 31:
+        _refuse_sizes("dg_glu")
     dev = Z.get_device()
     MI, MI2, sMI, sMI2 = (*lead, I), (*lead, I2), (*lead, I // 128), (*lead, I2 // 128)
     if not (Z.dtype is bf16 and Z.is_contiguous() and dev >= 0 and I2 % 2 == 0 and q.dtype in e4m3 and q.shape == MI and q.get_device() == dev
@@ -803,6 +825,8 @@ def dg_glu_backward(dH, q, sf, qt, sft, ht, hsft, Z=None, kept=None, kept_sf=Non
     else:
         M, I = dH.shape
         dev = dH.get_device()
+    if (M | I) >> 31:
+        _refuse_sizes("dg_glu_backward")
     Mp = (M + 127) // 128 * 128
 
     def codes(t, shape):
@@ -831,6 +855,8 @@ def dg_transpose_fp8(q, sf, qt, sft, stream=None):
     torch = _torch_module or _torch()
     f32, e4m3 = torch.float32, (torch.float8_e4m3fn, torch.uint8)
     M, N = q.shape
+    if (M | N) >> 31:
+        _refuse_sizes("dg_transpose_fp8")
     Mp = (M + 127) // 128 * 128
     dev = q.get_device()
     if not (q.dtype in e4m3 and q.is_contiguous() and dev >= 0 and sf.dtype is f32 and sf.shape == (M, N // 128) and sf.get_device() == dev

@@ -3,7 +3,7 @@ import pytest
 import torch
 
 import moe_grouped_gemm_tma_gb300 as dg
-from tests.test_between_refusals import c
+from tests.test_between_refusals import _Cuda, c
 
 b, i, u = torch.bfloat16, torch.int32, torch.uint8
 
@@ -45,3 +45,45 @@ def test_glu_backward_without_dh_gives_the_transposed_activation(kept):
     ht, hsft = torch.zeros_like(want[0]), torch.zeros_like(want[1])
     dg.dg_glu_backward(None, None, None, None, None, ht, hsft, **given)
     assert torch.equal(ht, want[0]) and torch.equal(hsft, want[1])
+
+
+BIG = 2 ** 32 + 4                                 # 4, cut to 32 bits
+
+
+def m(*shape, dtype=torch.float32):
+    return _Cuda(torch.empty(*shape, dtype=dtype, device="meta"))
+
+
+@pytest.mark.parametrize("big", [BIG, 2 ** 31, 2 ** 33 + 1])
+def test_sizes_beyond_32_bits_are_refused(big):
+    with pytest.raises(dg.DGError):
+        dg.moe_sort_rows(big, 1, 8)
+    with pytest.raises(dg.DGError):
+        dg.moe_sort_rows(4, 1, big)
+    with pytest.raises(dg.DGError):
+        dg.moe_sort_workspace(4, big, 8)
+    with pytest.raises(dg.DGError):
+        dg.rmsnorm_backward_workspace(big, 8)
+    calls = [
+        lambda: dg.dg_moe_sort_contiguous(m(big, 1, dtype=i), m(big, 1, dtype=i), m(8, dtype=i), m(1024, dtype=i)),
+        lambda: dg.dg_moe_sort_contiguous(m(4, 1, dtype=i), m(4, 1, dtype=i), m(big, dtype=i), m(1024, dtype=i)),
+        lambda: dg.dg_moe_sort_masked(m(4, 1, dtype=i), m(4, 1, dtype=i), m(big, dtype=i), 8),
+        lambda: dg.dg_moe_sort_masked(m(4, 1, dtype=i), m(4, 1, dtype=i), m(8, dtype=i), big),
+        lambda: dg.dg_moe_sort_masked(m(4, 1, dtype=i), m(4, 1, dtype=i), m(8, dtype=i), 8 - 2 ** 32),
+        lambda: dg.dg_moe_gather(m(big, 8, dtype=b), None, m(big, 0, dtype=i), m(16, 8, dtype=b)),
+        lambda: dg.dg_moe_gather(m(4, 8, dtype=b), None, m(4, 2, dtype=i), m(big, 8, dtype=b)),
+        lambda: dg.dg_moe_combine(m(big, 8, dtype=b), m(4, 1, dtype=i), m(4, 8, dtype=b)),
+        lambda: dg.dg_moe_combine(m(16, 8, dtype=b), m(big, 1, dtype=i), m(big, 8, dtype=b)),
+        lambda: dg.dg_moe_combine_backward(m(big, 8, dtype=b), m(big, 1, dtype=i), m(16, 8, dtype=b)),
+        lambda: dg.dg_moe_combine_backward(m(4, 8, dtype=b), m(4, 1, dtype=i), m(big, 8, dtype=b)),
+        lambda: dg.dg_rmsnorm(m(big, 8, dtype=b), m(8), y=m(big, 8, dtype=b)),
+        lambda: dg.dg_rmsnorm_backward(m(big, 8, dtype=b), m(big, 8, dtype=b), m(8), m(big, 8, dtype=b)),
+        lambda: dg.dg_glu(m(big, 256, dtype=b), m(big, 128, dtype=u), m(big, 1)),
+        lambda: dg.dg_glu(m(8, 256, dtype=b), m(8, 128, dtype=u), m(8, 1), masked_m=m(big, dtype=i)),
+        lambda: dg.dg_glu_backward(m(big, 128, dtype=b), *[None] * 6, Z=m(big, 256, dtype=b)),
+        lambda: dg.dg_transpose_fp8(m(big, 128, dtype=u), m(big, 1), m(128, big, dtype=u), m(128, big // 128)),
+    ]
+    for n, call in enumerate(calls):
+        with pytest.raises(dg.DGError):
+            call()
+            pytest.fail(f"call {n}")
