@@ -338,7 +338,8 @@ int64_t dg_rmsnorm_backward_workspace(int T, int H);
  * The gated activation between the two products of an expert (or of a dense layer), quantised for the second:
  *   h = act(g) * u,   (g; u) = Z's columns [0, I) and [I, 2I)
  *   Z    [M, 2I] bf16
- *   q    [M, I] e4m3, sf [M, I/128]: h in FP32, quantised as in dg_epilogue_backward; pow2 as in dg_rmsnorm
+ *   q    [M, I] e4m3, sf [M, I/128]: h in FP32, quantised as in dg_epilogue_backward; pow2 as in dg_rmsnorm. An
+ *        activation of less than 2^-119 in magnitude may count as 0, here and in dg_glu_backward
  *   kept [M, 2I] e4m3, kept_sf [M, 2I/128], or both null: Z quantised as in dg_epilogue_backward, what dg_glu_backward takes
  *        instead of Z
  * At most one of (which rows are computed; all others stay as they were):

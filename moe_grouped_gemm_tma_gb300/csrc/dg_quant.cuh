@@ -283,17 +283,18 @@ __device__ __forceinline__ float2 act_value2(float2 z) {
     return z;
 }
 
-// An activation and its slope at two FP32 pre-activations, both to a few roundings of 1 (SILU: of themselves). SILU goes by
-// one sigmoid p: z p and p (1 + z e p), with e = exp(-z) right to a few last places wherever z lies: what the exponent's
-// product is rounded by, and what log2(e) has beyond FP32, go in as a factor. Beyond 87 p is 0 or 1 to FP32. (Signs are
-// chosen so that no negation is an instruction.)
+// An activation and its slope at two FP32 pre-activations, the slope to a few roundings of 1. The value of SILU and GELU_TANH
+// is right to a few roundings of itself (GELU_TANH: and those of y, which its exponential makes |y| times as large), GELU's
+// to a few of z. SILU goes by one sigmoid p: z p and p (1 + z e p), with e = exp(-z) right to a few last places wherever z lies:
+// what the exponent's product is rounded by, and what log2(e) has beyond FP32, go in as a factor. A sigmoid below 2^-126 is
+// 0: the exponential is held where its reciprocal is one. (Signs are chosen so that no negation is an instruction.)
 template <int ACT>
 __device__ __forceinline__ void act_both2(float2 z, float2& value, float2& slope) {
     if (ACT == DG_ACT_SILU) {
         constexpr float LN2 = 0.6931471805599453f;
         const float2 one = make_float2(1.f, 1.f), minus = make_float2(-1.f, -1.f);
-        const float2 m = make_float2(at_most(-z.x, 87.f), at_most(-z.y, 87.f));      // -z, and held above as well
-        const float2 c = make_float2(at_least(m.x, -87.f), at_least(m.y, -87.f));
+        const float2 m = make_float2(at_most(-z.x, 88.f), at_most(-z.y, 88.f));      // -z, and held above as well
+        const float2 c = make_float2(at_least(m.x, -88.f), at_least(m.y, -88.f));
         const float2 t = __fmul2_rn(c, make_float2(LOG2_E, LOG2_E));
         float2 e = make_float2(exp2_approx(t.x), exp2_approx(t.y));
         float2 low = __fmul2_rn(__ffma2_rn(c, make_float2(-LOG2_E, -LOG2_E), t), make_float2(-LN2, -LN2));
@@ -316,7 +317,7 @@ __device__ __forceinline__ void act_both2(float2 z, float2& value, float2& slope
         float2 t = __fmul2_rn(y, make_float2(LOG2_E, LOG2_E));
         float2 low = __fmul2_rn(__ffma2_rn(y, make_float2(-LOG2_E, -LOG2_E), t), make_float2(-LN2, -LN2));
         low = __ffma2_rn(y, make_float2(LOG2_E_REST * LN2, LOG2_E_REST * LN2), low);
-        float2 e = make_float2(exp2_approx(fminf(t.x, 126.f)), exp2_approx(fminf(t.y, 126.f)));
+        float2 e = make_float2(exp2_approx(fminf(t.x, 127.f)), exp2_approx(fminf(t.y, 127.f)));
         e = __ffma2_rn(e, low, e);
         const float2 p = minus_one_over_one_plus2(e);                    // (negative)
         value = __fmul2_rn(m, p);
@@ -337,17 +338,28 @@ __device__ __forceinline__ void act_both2(float2 z, float2& value, float2& slope
     slope = act_slope2<ACT>(z);
 }
 
-// An activation at two BF16 pre-activations, as good as FP32 operations that round once each make it. SILU: z has eight
-// significant bits, so its product with the upper 16 bits of log2(e) is exact and the rest goes in as a factor.
+// An activation at two BF16 pre-activations, which may be multiplied by anything: one that vanishes comes out as 0, where
+// act_value2 holds a sigmoid at 2^-63. SILU is as good as FP32 operations that round once each make it: z has eight significant
+// bits, so its product with the upper 16 bits of log2(e) is exact and the rest goes in as a factor. GELU_TANH has log2(e) in
+// its polynomial's coefficients: three roundings of y, which the exponential makes |y| times as large. GELU is act_value2's: within
+// 1e-6 of itself, and what z^2 / 2 is off, by two roundings.
 template <int ACT>
 __device__ __forceinline__ float2 act_fine2(float2 z) {
     if (ACT == DG_ACT_SILU) {
         constexpr float HI = 1.44268798828125f, LO = 7.0526075e-6f * 0.6931471805599453f;   // log2(e), 16 bits; the rest, times ln 2
-        const float2 m = make_float2(at_most(-z.x, 87.f), at_most(-z.y, 87.f));      // -z, and held above as well
-        const float2 c = make_float2(at_least(m.x, -87.f), at_least(m.y, -87.f)), t = __fmul2_rn(c, make_float2(HI, HI));
+        const float2 m = make_float2(at_most(-z.x, 88.f), at_most(-z.y, 88.f));      // -z, and held above as well
+        const float2 c = make_float2(at_least(m.x, -88.f), at_least(m.y, -88.f)), t = __fmul2_rn(c, make_float2(HI, HI));
         float2 e = make_float2(exp2_approx(t.x), exp2_approx(t.y));
         e = __ffma2_rn(e, __fmul2_rn(c, make_float2(LO, LO)), e);
         return __fmul2_rn(m, minus_one_over_one_plus2(e));
+    }
+    if (ACT == DG_ACT_GELU_TANH) {
+        constexpr float A = -2.f * GELU_A * LOG2_E, B = -2.f * GELU_A * GELU_B * LOG2_E;
+        z = make_float2(at_least(z.x, -16.f), at_least(z.y, -16.f));         // (its sigmoid is 0 there)
+        const float2 t = __fmul2_rn(z, __ffma2_rn(__fmul2_rn(z, z), make_float2(B, B), make_float2(A, A)));
+        const float2 e = make_float2(exp2_approx(fminf(t.x, 127.f)), exp2_approx(fminf(t.y, 127.f)));
+        const float2 a = __fadd2_rn(e, make_float2(1.f, 1.f));
+        return __fmul2_rn(z, make_float2(reciprocal_approx(a.x), reciprocal_approx(a.y)));
     }
     return act_value2<ACT>(z);
 }
