@@ -315,7 +315,8 @@ dg_status dg_moe_combine_backward(const void* dout, const void* y, const int32_t
  *   q   [T, H] e4m3, sf [T, H/128] fp32, or both null: y quantised (before its rounding to BF16) as in
  *       dg_epilogue_backward; with pow2 the scale is the power of two above that scale, as the UE8M0 path takes it.
  *       H a multiple of 128 then.
- * Sums are FP32 (a row whose squares pass their range, from about 1e19 on, comes out as zeros). H a multiple of 8 up to 16384,
+ * Sums are FP32 (a row whose squares pass their range, from about 1e19 on, comes out as zeros; squares below 2^-149, of values under
+ * 3.7e-23, are lost, which counts only where eps is as small). H a multiple of 8 up to 16384,
  * eps >= 0; weight and the matrices 16-byte aligned.
  */
 dg_status dg_rmsnorm(const void* x, const void* residual, const void* weight, int weight_type, void* sum, void* y, uint8_t* q, float* sf,

@@ -80,8 +80,10 @@ __device__ __forceinline__ uint2 line_codes(const float2 (&v)[4], const BlockSca
 // A half warp has the 128 values of a scaling block of 4 rows, a lane 8 columns of each, in both halves of Z. The largest
 // magnitudes of all its lines (h's, with KEEP g's and u's) are found together, and each line's scale is made by one lane. A warp
 // takes piece after piece, and the next one's values come by asynchronous copies into places that only their lane reads: with
-// loads into registers 36.8 k rows of 2 x 2048 took 94.4 us (two rows a lane, 8 CTAs an SM) with codes kept and 58.9 without, so
-// they take 86.1 (6.2 TB/s) and 56.7 (6.7).
+// loads into registers 36.8 k rows of 2 x 2048 took 94.4 us (two rows a lane, 8 CTAs an SM) with codes kept and 58.9 without; so
+// they take 86.6 (6.2 TB/s) and 56.6 (6.7), of which h's codes by the rounded quotient, where the reciprocal alone would move some
+// twenty in a million by a step, are 1.9 and 0.7. With masked_m the walk goes over the room of all experts: 32 experts of 16 rows each
+// take 4.4 us with max_m = 64 and 29 with 4096.
 template <int ACT, bool KEEP>
 __global__ void __launch_bounds__(32 * GLU_WARPS, glu_ctas(KEEP)) glu_kernel(const GluParams p) {
     constexpr int R = GLU_LANE_ROWS, LINES = KEEP ? 4 * R : R, SHARE = 16 / LINES;
@@ -235,11 +237,13 @@ struct GluBackwardShared {
 // registers hold with one CTA of 512 threads an SM. Its barriers are hidden by nothing else, therefore: the next tile's
 // inputs come while this one's are in use, and the rows' codes are made while some warps make the columns' scales.
 //
-// Floor: 9.25 bytes an element of dH from codes, 45.6 us for 16384 x 2048. It takes 78.5 us (SILU; GELU 87.6, its tanh form 81.6;
-// from BF16 79.2): 46 instructions an element at 52% of the issue slots. A CTA for each of the three outputs took 153 us; all
-// three in one with 1024 threads and 4 rows a lane 115.7, then 87.3 with codes by the reciprocal, one sigmoid for value and slope
-// and the next inputs asked into L2, and 84.1 with them copied to shared memory. Two CTAs an SM with half a tile's columns each,
-// a pair of them exchanging the rows' maxima, took 83.7.
+// Floor: 9.25 bytes an element of dH from codes, 45.6 us for 16384 x 2048. It takes 82.3 us (SILU; GELU 91.1, its tanh form 85.3;
+// from BF16 80.7), with codes by the reciprocal alone, some twenty in a million off by a step, 77.7. What bounds it is latency:
+// 49 instructions an element at 53% of the issue slots, with the FP32 pipe 40% busy, the integer one 41% and DRAM 28%;
+// four warps a scheduler that wait together at three barriers a tile leave the rest empty.
+// With codes by the reciprocal a CTA for each of the three outputs took 153 us; all three in one with 1024 threads and 4 rows
+// a lane 87.3 (one sigmoid for value and slope, the next inputs asked into L2), 84.1 with them copied to shared memory, 77.7 with 512
+// threads; two CTAs an SM with half a tile's columns each, a pair of them exchanging the rows' maxima, took 83.7.
 template <int ACT, bool KEPT>
 __global__ void __launch_bounds__(GB_THREADS, 1) glu_backward_kernel(const GluBackwardParams p) {
     extern __shared__ __align__(16) uint8_t s_raw[];

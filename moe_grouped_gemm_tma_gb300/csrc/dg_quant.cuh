@@ -40,9 +40,10 @@ __device__ __forceinline__ float2 quotient2(float2 v, float2 nd, float2 r) {
     return __ffma2_rn(__ffma2_rn(q, nd, v), r, q);
 }
 
-// 1 / s = r + reciprocal_rest(s, r) to 47 bits, for a nonzero s; and by the two v / s: the sum's one rounding is that of the quotient but
-// for quotients within 2^-47 of themselves of a number halfway between two FP32 numbers (quotients of 24-bit numbers are on
-// neither). An instruction a pair less than quotient2, where many values have one scale.
+// 1 / s = r + reciprocal_rest(s, r) to 47 bits, for a nonzero s up to 2^101 (above that the rest loses bits below 2^-149: 31
+// are left at 2^120); and by the two v / s: the sum's one rounding is that of the quotient but for quotients within 2^-47 of
+// themselves of a number halfway between two FP32 numbers (quotients of 24-bit numbers are on neither). An instruction a pair less
+// than quotient2, where many values have one scale.
 __device__ __forceinline__ float reciprocal_rest(float s, float r) { return fmaf(-s, r, 1.f) * r; }
 __device__ __forceinline__ float2 quotient2_by(float2 v, float2 r, float2 rest) { return __ffma2_rn(v, r, __fmul2_rn(v, rest)); }
 

@@ -711,8 +711,13 @@ dg_status dg_moe_combine_backward(const void* dout, const void* y, const int32_t
     p.k = k;
     p.vectors = H / 8;
     p.Mt = Mt;
-    // Few tokens get as many warps each as they have pieces for, up to eight (256 tokens of 8 x 7168: 27.5 us, with four 31.8, with two
-    // 43.1), many get four (4096: 163.7 us, with eight 170.4, with two 171.3). The order of the sums goes by the sizes alone.
+    // Few tokens get as many warps each as they have pieces for, up to eight, many get four. Rows of 7168, us with 8, 4 and 2 warps:
+    //   tokens of 8    16: 19.1, 26.3, 38.0    256: 27.6, 32.0, 43.2    1024: 53.6, 57.9, 56.2    1536: 72.5, 70.1, 73.8    2048: 92.6, 92.7, 103.2
+    //                  4096: 170.5, 163.9, 171.4    8192: 324.4, 312.4, 313.8
+    //   tokens of 2    16: 11.2, 11.3, 14.6    256: 21.4, 21.3, 24.1    1024: 30.8, 28.8, 29.6    2048: 42.3, 38.1, 40.5
+    //                  4096: 66.1, 60.4, 60.5    8192: 114.8, 106.2, 102.2
+    // (Four would be best from somewhere between 1024 and 1536 tokens of 8 on, and from 256 of 2; with rows of 2048 all take the
+    // same.) By the sizes alone, and so is the order of the sums.
     const bool wide = H > 32 * CB_VECTORS * 8;
     const int most = T < 2048 ? CB_WARPS : 4, pieces = cdiv(p.vectors, 32 * CB_VECTORS);
     const int warps = !wide ? CB_NARROW : pieces < most ? pieces : most;
